@@ -310,6 +310,41 @@ int moe_router_bwd(const void *x, const void *w_router, const float *d_logits, i
                    int accumulate_dx, void *dx, void *dw_router, void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * RMS norms before and after the block, fused with the block's gate and the scaled residual. With
+ * rms(v) = 1 / sqrt(mean(v^2) + eps), per token (rows of x, y, out, n: [T, d] in dtype):
+ *   moe_norm_fwd            n   = x rms(x) w
+ *   moe_norm_residual_fwd   out = res_scale x + gate * (y rms(y) w_post)
+ *                           n   = out rms(out) w_next       (the next block's norm; w_next, n may be NULL)
+ * w, w_post, w_next [d] and gate are in dtype; gate_kind says what gate is: none (NULL; 1), one value
+ * per channel [d], or one per token and channel [T, d]. Sums and statistics are fp32; n is formed from
+ * the unrounded out.
+ * Backward: for dout [T, d], the gradient that reaches out through the stream (NULL: zero, allowed only
+ * with dn), and dn [T, d], the gradient of n (given exactly when w_next is),
+ *   moe_norm_bwd            dx = dx_in + (norm backward of dn at x)  (dx_in NULL: zero; dx may be dx_in), dw [d]
+ *   moe_norm_residual_bwd   G = dout + (norm backward of dn at out);  dx = res_scale G,
+ *                           dy = norm backward of G * gate at y, dw_post [d], d_gate ([d] or [T, d], as gate;
+ *                           unused without a gate), dw_next [d]
+ * Statistics are formed again from x, y and the stored out, so the forward saves nothing else. Weight
+ * gradients are summed in fp32 in a fixed order (deterministic), rounded once, and overwritten.
+ * Requires 1 <= d <= MOE_NORM_MAX_D, eps > 0, T >= 0 (T = 0: the weight gradients are zeros).
+ * ws: moe_norm_bwd_workspace_size(T, d, dtype) bytes, 256-byte aligned, any content. Except dx == dx_in,
+ * outputs may not overlap inputs.
+ */
+#define MOE_NORM_MAX_D 8192
+enum moe_gate_kind { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
+int moe_norm_fwd(const void *x, const void *w, int T, int d, int dtype, float eps, void *n, moe_stream_t stream);
+int moe_norm_residual_fwd(const void *y, const void *x, const void *w_post, const void *gate, int gate_kind,
+                          const void *w_next, int T, int d, int dtype, float res_scale, float eps, void *out, void *n,
+                          moe_stream_t stream);
+size_t moe_norm_bwd_workspace_size(int T, int d, int dtype);
+int moe_norm_bwd(const void *dn, const void *x, const void *w, const void *dx_in, int T, int d, int dtype, float eps,
+                 void *dx, void *dw, void *ws, size_t ws_bytes, moe_stream_t stream);
+int moe_norm_residual_bwd(const void *dout, const void *dn, const void *out, const void *y, const void *w_post,
+                          const void *gate, int gate_kind, const void *w_next, int T, int d, int dtype,
+                          float res_scale, float eps, void *dx, void *dy, void *dw_post, void *d_gate, void *dw_next,
+                          void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Synchronises `stream`, then returns the device status word at the start of a workspace used by
  * moe_count_index, moe_grouped_ffn_* or moe_router_*: MOE_OK or a negative moe_status. Not for
  * the hot path.

@@ -2,10 +2,12 @@
 router weights), per-expert token counting and index generation, token permutation, grouped SwiGLU
 GEMM on tcgen05 tensor cores, and the weighted combine, forward and backward, behind the C ABI in
 include/moe.h. MoELayer holds one layer's buffers and call order (and can record a pass as a CUDA
-graph); HostPipeline runs passes from pinned host memory with the copies overlapped."""
+graph); HostPipeline runs passes from pinned host memory with the copies overlapped. Around the layer:
+BlockNorms (the norms before and after it, with the gate and the residual)."""
 from . import _lib
 from ._lib import MoeError
+from .block import BlockNorms
 from .layer import MoELayer
 from .pipeline import HostPipeline
 
-__all__ = ["MoELayer", "HostPipeline", "MoeError", "_lib"]
+__all__ = ["MoELayer", "HostPipeline", "BlockNorms", "MoeError", "_lib"]

@@ -19,6 +19,8 @@ MOE_F32, MOE_BF16 = 0, 1
 GROUP_ROWS = 128
 MAX_EXPERTS = 256
 MAX_TOPK = 16
+NORM_MAX_D = 8192
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED", -3: "MOE_ERR_CUDA",
           -4: "MOE_ERR_DEVICE_TIMEOUT", -5: "MOE_ERR_BAD_INDEX", -6: "MOE_ERR_CHECK_FAILED"}
 
@@ -26,6 +28,7 @@ _lock = threading.Lock()
 _lib = None
 
 _P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_F, _D = ctypes.c_float, ctypes.c_double
 _SIGS = {
     "moe_route_topk": (_I, [_P, _I, _I, _I, _P, _P, _P]),
     "moe_grouped_rows_max": (_I64, [_I, _I, _I]),
@@ -50,6 +53,12 @@ _SIGS = {
     "moe_router_workspace_size": (_SZ, [_I, _I, _I, _I]),
     "moe_router_fwd": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
     "moe_router_bwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "moe_norm_fwd": (_I, [_P, _P, _I, _I, _I, _F, _P, _P]),
+    "moe_norm_residual_fwd": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _F, _F, _P, _P, _P]),
+    "moe_norm_bwd_workspace_size": (_SZ, [_I, _I, _I]),
+    "moe_norm_bwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "moe_norm_residual_bwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _P, _SZ,
+                                   _P]),
     "moe_read_status": (_I, [_P, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_version": (_I, []),
@@ -101,6 +110,19 @@ def _p(t):
 def _s(stream):
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _want(name, t, dtype, shape):
+    """A tensor argument that a kernel reads as contiguous memory of this type and shape."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} is needed, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+
+
+def _bytes_at_least(name, t, n):
+    if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: a contiguous uint8 tensor of at least {n} bytes is needed, got {t.dtype} "
+                         f"{tuple(t.shape)}")
 
 
 def _ok(fn, rc):
@@ -250,6 +272,87 @@ def moe_router_bwd(x, w_router, d_logits, dx, dw_router, ws, accumulate_dx=False
     _ok("moe_router_bwd", lib().moe_router_bwd(
         _p(x), _p(w_router), _p(d_logits), T, d, E, dtype_code(x.dtype), int(bool(accumulate_dx)), _p(dx),
         _p(dw_router), _p(ws), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def _gate_kind(gate, T, d, dtype):
+    if gate is None:
+        return GATE_NONE
+    if gate.dim() == 1:
+        _want("gate", gate, dtype, (d,))
+        return GATE_CHANNEL
+    _want("gate", gate, dtype, (T, d))
+    return GATE_TOKEN
+
+
+def moe_norm_fwd(x, w, n, eps=1e-6, stream=None):
+    """n = x rms(x) w, x [T, d]."""
+    T, d = x.shape
+    dt = x.dtype
+    _want("x", x, dt, (T, d))
+    _want("w", w, dt, (d,))
+    _want("n", n, dt, (T, d))
+    _ok("moe_norm_fwd", lib().moe_norm_fwd(_p(x), _p(w), T, d, dtype_code(dt), eps, _p(n), _s(stream)))
+
+
+def moe_norm_residual_fwd(y, x, w_post, gate, w_next, out, n, res_scale=1.0, eps=1e-6, stream=None):
+    """out = res_scale x + gate * (y rms(y) w_post); n = out rms(out) w_next. gate: None, [d] or [T, d];
+    w_next and n may be None (no next norm)."""
+    T, d = x.shape
+    dt = x.dtype
+    _want("x", x, dt, (T, d))
+    _want("y", y, dt, (T, d))
+    _want("out", out, dt, (T, d))
+    _want("w_post", w_post, dt, (d,))
+    if (w_next is None) != (n is None):
+        raise ValueError("w_next and n are given together")
+    if n is not None:
+        _want("w_next", w_next, dt, (d,))
+        _want("n", n, dt, (T, d))
+    kind = _gate_kind(gate, T, d, dt)
+    _ok("moe_norm_residual_fwd", lib().moe_norm_residual_fwd(
+        _p(y), _p(x), _p(w_post), _p(gate), kind, _p(w_next), T, d, dtype_code(dt), res_scale, eps, _p(out), _p(n),
+        _s(stream)))
+
+
+def moe_norm_bwd_workspace_size(T, d, dtype):
+    return int(lib().moe_norm_bwd_workspace_size(T, d, dtype))
+
+
+def moe_norm_bwd(dn, x, w, dx_in, dx, dw, ws, eps=1e-6, stream=None):
+    """Backward of moe_norm_fwd; dx_in (may be None, may be dx) is added to dx."""
+    T, d = x.shape
+    dt = x.dtype
+    for name, t in (("x", x), ("dn", dn), ("dx", dx)) + ((("dx_in", dx_in),) if dx_in is not None else ()):
+        _want(name, t, dt, (T, d))
+    _want("w", w, dt, (d,))
+    _want("dw", dw, dt, (d,))
+    _ok("moe_norm_bwd", lib().moe_norm_bwd(_p(dn), _p(x), _p(w), _p(dx_in), T, d, dtype_code(dt), eps, _p(dx), _p(dw),
+                                           _p(ws), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_norm_residual_bwd(dout, dn, out, y, w_post, gate, w_next, dx, dy, dw_post, d_gate, dw_next, ws, res_scale=1.0,
+                          eps=1e-6, stream=None):
+    """Backward of moe_norm_residual_fwd. dout may be None (zero) when dn is given; dn, out, w_next and dw_next
+    belong to the next norm and may be None together; d_gate is None without a gate."""
+    T, d = y.shape
+    dt = y.dtype
+    for name, t in (("y", y), ("dx", dx), ("dy", dy)) + ((("dout", dout),) if dout is not None else ()):
+        _want(name, t, dt, (T, d))
+    _want("w_post", w_post, dt, (d,))
+    _want("dw_post", dw_post, dt, (d,))
+    if w_next is not None:
+        for name, t in (("dn", dn), ("out", out)):
+            _want(name, t, dt, (T, d))
+        _want("w_next", w_next, dt, (d,))
+        _want("dw_next", dw_next, dt, (d,))
+    elif dn is not None or dout is None:
+        raise ValueError("dn needs w_next, and without them dout is needed")
+    kind = _gate_kind(gate, T, d, dt)
+    if kind != GATE_NONE:
+        _want("d_gate", d_gate, dt, gate.shape)
+    _ok("moe_norm_residual_bwd", lib().moe_norm_residual_bwd(
+        _p(dout), _p(dn), _p(out), _p(y), _p(w_post), _p(gate), kind, _p(w_next), T, d, dtype_code(dt), res_scale, eps,
+        _p(dx), _p(dy), _p(dw_post), _p(d_gate), _p(dw_next), _p(ws), ws.numel() * ws.element_size(), _s(stream)))
 
 
 def moe_read_status(ws, stream=None):
