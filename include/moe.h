@@ -345,6 +345,53 @@ int moe_norm_residual_bwd(const void *dout, const void *dn, const void *out, con
                           void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * One AdamW step over any number of tensors, one launch per kind of tensor (parameter type, master copy,
+ * state type). With t the step count after this step and c = grad_scale, per value
+ *   m = beta1 m + (1 - beta1) c g,  v = beta2 v + (1 - beta2) (c g)^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * computed in fp32 and written in place.
+ *   dtype   of p and g: MOE_F32 or MOE_BF16
+ *   master  fp32 copy of a bf16 parameter, updated in its place (p is then its value rounded to nearest), or NULL
+ *   state   MOE_ADAMW_F32: m, v fp32 [n].
+ *           MOE_ADAMW_F8: m holds e4m3 codes of m / m_scale, v holds e4m3 codes of sqrt(v) / v_scale, one fp32
+ *           scale (the block's largest magnitude / 448) per MOE_ADAMW_BLOCK consecutive values; m_scale, v_scale
+ *           have ceil(n / MOE_ADAMW_BLOCK) entries. A block whose largest magnitude is below 1e-30 is held as zeros.
+ * Values kept in few bits only (the e4m3 states, a bf16 parameter without a master) are rounded with a dither
+ * that depends on the place in the tensor and on t: down after adding u / 2^b of a rounding step, where u is
+ * the top b bits of (place * 2654435769 + t * 1640531535 + shift) mod 2^32 (b = 20 and shift 0 for m, shift
+ * 0x55555555 for v; b = 16 and shift 0xaaaaaaaa for p). Rounding to nearest would lose steps smaller than half
+ * a rounding step; this keeps them on average, and repeats exactly.
+ * Pointers need the alignment of their elements; 16 bytes (8 for e4m3 states) is faster. Tensors may not overlap.
+ *
+ * moe_adamw_plan checks the tensors and lists their chunks in host memory (moe_adamw_plan_size bytes, 8-byte
+ * aligned); copy it as it is to device memory (16-byte aligned) and pass both to every step. The plan holds the tensors'
+ * addresses: make a new one when a tensor moves. `state` is device memory: the step count (advanced by the
+ * call; a captured call counts on when it is replayed), lr and grad_scale, which the caller may change between steps,
+ * and a counter that must be 0 before the first call.
+ */
+#define MOE_ADAMW_BLOCK 256
+enum moe_adamw_state_kind { MOE_ADAMW_F32 = 0, MOE_ADAMW_F8 = 1 };
+typedef struct moe_adamw_tensor {
+  void *p;
+  float *master;
+  const void *g;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  int64_t n;
+  float weight_decay;
+  int32_t dtype, state, reserved;
+} moe_adamw_tensor;
+typedef struct moe_adamw_state {
+  int64_t step;
+  float lr, grad_scale;
+  uint32_t arrived, reserved;
+} moe_adamw_state;
+size_t moe_adamw_plan_size(const moe_adamw_tensor *tensors, int count);
+int moe_adamw_plan(const moe_adamw_tensor *tensors, int count, void *plan, size_t plan_bytes);
+int moe_adamw_step(const void *plan_host, const void *plan_device, double beta1, double beta2, float eps,
+                   moe_adamw_state *state, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Synchronises `stream`, then returns the device status word at the start of a workspace used by
  * moe_count_index, moe_grouped_ffn_* or moe_router_*: MOE_OK or a negative moe_status. Not for
  * the hot path.

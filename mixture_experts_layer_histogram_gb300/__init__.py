@@ -3,11 +3,13 @@ router weights), per-expert token counting and index generation, token permutati
 GEMM on tcgen05 tensor cores, and the weighted combine, forward and backward, behind the C ABI in
 include/moe.h. MoELayer holds one layer's buffers and call order (and can record a pass as a CUDA
 graph); HostPipeline runs passes from pinned host memory with the copies overlapped. Around the layer:
-BlockNorms (the norms before and after it, with the gate and the residual)."""
+BlockNorms (the norms before and after it, with the gate and the residual) and AdamW (one step over
+many tensors, states in fp32 or 8 bits)."""
 from . import _lib
 from ._lib import MoeError
 from .block import BlockNorms
 from .layer import MoELayer
+from .optim import AdamW
 from .pipeline import HostPipeline
 
-__all__ = ["MoELayer", "HostPipeline", "BlockNorms", "MoeError", "_lib"]
+__all__ = ["MoELayer", "HostPipeline", "BlockNorms", "AdamW", "MoeError", "_lib"]

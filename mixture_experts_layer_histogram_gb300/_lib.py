@@ -21,6 +21,8 @@ MAX_EXPERTS = 256
 MAX_TOPK = 16
 NORM_MAX_D = 8192
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
+ADAMW_F32, ADAMW_F8 = 0, 1
+ADAMW_BLOCK = 256
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED", -3: "MOE_ERR_CUDA",
           -4: "MOE_ERR_DEVICE_TIMEOUT", -5: "MOE_ERR_BAD_INDEX", -6: "MOE_ERR_CHECK_FAILED"}
 
@@ -29,6 +31,15 @@ _lib = None
 
 _P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 _F, _D = ctypes.c_float, ctypes.c_double
+
+
+class AdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor"""
+    _fields_ = [("p", _P), ("master", _P), ("g", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P),
+                ("n", _I64), ("weight_decay", _F), ("dtype", ctypes.c_int32), ("state", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 _SIGS = {
     "moe_route_topk": (_I, [_P, _I, _I, _I, _P, _P, _P]),
     "moe_grouped_rows_max": (_I64, [_I, _I, _I]),
@@ -59,6 +70,9 @@ _SIGS = {
     "moe_norm_bwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
     "moe_norm_residual_bwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _P, _SZ,
                                    _P]),
+    "moe_adamw_plan_size": (_SZ, [_P, _I]),
+    "moe_adamw_plan": (_I, [_P, _I, _P, _SZ]),
+    "moe_adamw_step": (_I, [_P, _P, _D, _D, _F, _P, _P]),
     "moe_read_status": (_I, [_P, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_version": (_I, []),
@@ -353,6 +367,21 @@ def moe_norm_residual_bwd(dout, dn, out, y, w_post, gate, w_next, dx, dy, dw_pos
     _ok("moe_norm_residual_bwd", lib().moe_norm_residual_bwd(
         _p(dout), _p(dn), _p(out), _p(y), _p(w_post), _p(gate), kind, _p(w_next), T, d, dtype_code(dt), res_scale, eps,
         _p(dx), _p(dy), _p(dw_post), _p(d_gate), _p(dw_next), _p(ws), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_adamw_plan(tensors):
+    """The plan of a list of AdamWTensor: a uint8 host tensor, to be copied to the device as it is."""
+    arr = (AdamWTensor * max(1, len(tensors)))(*tensors)
+    size = int(lib().moe_adamw_plan_size(arr, len(tensors)))
+    plan = torch.empty((size + 7) // 8, dtype=torch.int64).view(torch.uint8)
+    _ok("moe_adamw_plan", lib().moe_adamw_plan(arr, len(tensors), ctypes.c_void_p(plan.data_ptr()), plan.numel()))
+    return plan
+
+
+def moe_adamw_step(plan_host, plan_device, beta1, beta2, eps, state, stream=None):
+    """state: 24 bytes of device memory laid out as moe_adamw_state."""
+    _ok("moe_adamw_step", lib().moe_adamw_step(ctypes.c_void_p(plan_host.data_ptr()), _p(plan_device), beta1, beta2,
+                                               eps, _p(state), _s(stream)))
 
 
 def moe_read_status(ws, stream=None):

@@ -45,3 +45,38 @@ def test_norm_refusals(L):
                NULL) == -1
     assert res(FAKE, NULL, NULL, FAKE, FAKE, FAKE, 1, NULL, 4, 64, 0, 1.0, 1e-6, FAKE, FAKE, FAKE, NULL, NULL, FAKE, ws,
                NULL) == -1
+
+
+def test_adamw_plans(L):
+    from mixture_experts_layer_histogram_gb300 import _lib
+    T = _lib.AdamWTensor
+
+    def plan(**kw):
+        a = T(**{**dict(p=4096, g=4096, m=4096, v=4096, n=10, dtype=0, state=0), **kw})
+        size = L.moe_adamw_plan_size(ctypes.byref(a), 1)
+        buf = (ctypes.c_int64 * (size // 8 + 1))()
+        return L.moe_adamw_plan(ctypes.byref(a), 1, buf, size)
+
+    assert plan() == 0
+    assert plan(n=0, p=None, g=None, m=None, v=None) == 0
+    assert plan(n=-1) == -1
+    assert plan(p=None) == -1 and plan(g=None) == -1 and plan(m=None) == -1 and plan(v=None) == -1
+    assert plan(p=4098) == -1 and plan(p=4098, g=4098, dtype=1) == 0
+    assert plan(dtype=2) == -1 and plan(state=2) == -1
+    assert plan(weight_decay=-0.1) == -1 and plan(weight_decay=float("nan")) == -1
+    assert plan(master=4096) == -1 and plan(master=4096, dtype=1) == 0
+    assert plan(state=1) == -1                                  # 8-bit states without scales
+    assert plan(state=1, m_scale=4096, v_scale=4096) == 0
+    with pytest.raises(_lib.MoeError):
+        _lib._ok("moe_adamw_plan", L.moe_adamw_plan(None, 1, FAKE, 64))
+    # a chunk of 4096 values is 8 bytes of the plan
+    sizes = [L.moe_adamw_plan_size(ctypes.byref(T(n=n)), 1) for n in (0, 1, 4096, 4097, 1 << 30)]
+    assert [s - sizes[0] for s in sizes] == [0, 8, 8, 16, 8 << 18]
+    host = _lib.moe_adamw_plan([T(p=4096, g=4096, m=4096, v=4096, n=10)])
+    ptr = ctypes.c_void_p(host.data_ptr())
+    for args in ((NULL, FAKE, .9, .99, 1e-8, FAKE), (ptr, NULL, .9, .99, 1e-8, FAKE), (ptr, FAKE, 1.0, .99, 1e-8, FAKE),
+                 (ptr, FAKE, .9, -.1, 1e-8, FAKE), (ptr, FAKE, .9, .99, 0.0, FAKE), (ptr, FAKE, .9, .99, 1e-8, NULL),
+                 (ptr, ctypes.c_void_p((1 << 20) + 8), .9, .99, 1e-8, FAKE)):
+        assert L.moe_adamw_step(*args, NULL) == -1
+    host[0] = 0                                                 # no plan
+    assert L.moe_adamw_step(ptr, FAKE, .9, .99, 1e-8, FAKE, NULL) == -1
