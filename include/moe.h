@@ -392,6 +392,45 @@ int moe_adamw_step(const void *plan_host, const void *plan_device, double beta1,
                    moe_adamw_state *state, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * MXFP4 (OCP Microscaling Formats 1.0): blocks of 32 values along K share one E8M0 scale; codes are E2M1.
+ *   codes   [R, K/2] bytes, two per byte, the even column in the low half
+ *   scales  moe_fp4_scale_bytes(R, K) bytes: row r, block kb (= column / 32) at byte
+ *           ((r / 128) * ceil(K / 128) + kb / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + kb % 4,
+ *           the order in which the tensor cores take them; places past R or K hold 0
+ * A block's scale is 2^(floor(log2 max|x|) - 2), not below 2^-127 (byte b stands for 2^(b - 127)); codes are
+ * x / scale rounded to nearest even, saturating at 6. A block that holds an infinity or a NaN gets the NaN scale
+ * (255) and zero codes, and stands for NaNs. K must be a multiple of 32 (MOE_ERR_UNSUPPORTED otherwise).
+ */
+size_t moe_fp4_scale_bytes(int64_t R, int K);
+int moe_fp4_quantize(const void *x, int dtype, int64_t R, int K, void *codes, void *scales, moe_stream_t stream);
+int moe_fp4_dequantize(const void *codes, const void *scales, int64_t R, int K, int dtype, void *x,
+                       moe_stream_t stream);
+
+/*
+ * moe_permute with MXFP4 output: x [T, d] is quantised once per token and written to the token's grouped rows,
+ * codes [rows_max, d/2] and scales [moe_fp4_scale_bytes(rows_max, d)]; padding rows of every expert are zeros,
+ * rows from tile_offsets[E] * MOE_GROUP_ROWS on are not touched. Requires d % 128 == 0.
+ */
+int moe_permute_fp4(const void *x, int dtype, int T, int d, int k, int E, const int32_t *row_of_slot,
+                    const int32_t *counts, const int32_t *tile_offsets, int64_t rows_max, void *codes, void *scales,
+                    moe_stream_t stream);
+
+/*
+ * Grouped expert FFN, forward, with MXFP4 tokens and weights (inference):
+ *   x_codes, x_scales     from moe_permute_fp4
+ *   wgu_codes, wgu_scales moe_fp4_quantize of w_gate_up viewed as [E * 2f, d]
+ *   wd_codes, wd_scales   moe_fp4_quantize of w_down viewed as [E * d, f]
+ *   h_codes, h_scales     scratch and output: MXFP4 of h = silu(x Wg^T) * (x Wu^T) [rows_max, f]
+ *   y_perm                [rows_max, d] bf16: h Wd^T over the values that h_codes stand for
+ * Products run on the block-scaled tensor cores with fp32 accumulation; h is quantised from fp32. Requires
+ * d % 256 == 0 and f % 256 == 0. Padding rows come out as zeros. ws: as for moe_grouped_ffn_fwd with MOE_BF16.
+ */
+int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales, const void *wgu_codes, const void *wgu_scales,
+                            const void *wd_codes, const void *wd_scales, const int32_t *tile_offsets,
+                            const int32_t *offsets, int E, int d, int f, int64_t rows_max, void *h_codes,
+                            void *h_scales, void *y_perm, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Synchronises `stream`, then returns the device status word at the start of a workspace used by
  * moe_count_index, moe_grouped_ffn_* or moe_router_*: MOE_OK or a negative moe_status. Not for
  * the hot path.

@@ -3,13 +3,15 @@ router weights), per-expert token counting and index generation, token permutati
 GEMM on tcgen05 tensor cores, and the weighted combine, forward and backward, behind the C ABI in
 include/moe.h. MoELayer holds one layer's buffers and call order (and can record a pass as a CUDA
 graph); HostPipeline runs passes from pinned host memory with the copies overlapped. Around the layer:
-BlockNorms (the norms before and after it, with the gate and the residual) and AdamW (one step over
-many tensors, states in fp32 or 8 bits)."""
+BlockNorms (the norms before and after it, with the gate and the residual), AdamW (one step over many
+tensors, states in fp32 or 8 bits), and MoELayerFp4 / Fp4Weights (serving with MXFP4 experts)."""
 from . import _lib
 from ._lib import MoeError
 from .block import BlockNorms
+from .fp4 import Fp4Weights, MoELayerFp4, fp4_dequantize, fp4_quantize
 from .layer import MoELayer
 from .optim import AdamW
 from .pipeline import HostPipeline
 
-__all__ = ["MoELayer", "HostPipeline", "BlockNorms", "AdamW", "MoeError", "_lib"]
+__all__ = ["MoELayer", "HostPipeline", "BlockNorms", "AdamW", "MoELayerFp4", "Fp4Weights", "fp4_quantize",
+           "fp4_dequantize", "MoeError", "_lib"]

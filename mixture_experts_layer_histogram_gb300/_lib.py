@@ -73,6 +73,11 @@ _SIGS = {
     "moe_adamw_plan_size": (_SZ, [_P, _I]),
     "moe_adamw_plan": (_I, [_P, _I, _P, _SZ]),
     "moe_adamw_step": (_I, [_P, _P, _D, _D, _F, _P, _P]),
+    "moe_fp4_scale_bytes": (_SZ, [_I64, _I]),
+    "moe_fp4_quantize": (_I, [_P, _I, _I64, _I, _P, _P, _P]),
+    "moe_fp4_dequantize": (_I, [_P, _P, _I64, _I, _I, _P, _P]),
+    "moe_permute_fp4": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _I64, _P, _P, _P]),
+    "moe_grouped_ffn_fwd_fp4": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I64, _P, _P, _P, _P, _SZ, _P]),
     "moe_read_status": (_I, [_P, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_version": (_I, []),
@@ -382,6 +387,63 @@ def moe_adamw_step(plan_host, plan_device, beta1, beta2, eps, state, stream=None
     """state: 24 bytes of device memory laid out as moe_adamw_state."""
     _ok("moe_adamw_step", lib().moe_adamw_step(ctypes.c_void_p(plan_host.data_ptr()), _p(plan_device), beta1, beta2,
                                                eps, _p(state), _s(stream)))
+
+
+def moe_fp4_scale_bytes(R, K):
+    return int(lib().moe_fp4_scale_bytes(R, K))
+
+
+def _rows(x):
+    """A tensor [..., K] as its number of rows and K."""
+    return (x.numel() // x.shape[-1] if x.shape[-1] else 0), x.shape[-1]
+
+
+def moe_fp4_quantize(x, codes, scales, stream=None):
+    """x [..., K] (rows in order) -> codes [..., K/2] uint8, scales [moe_fp4_scale_bytes(rows, K)] uint8."""
+    R, K = _rows(x)
+    _want("x", x, x.dtype, x.shape)
+    _want("codes", codes, torch.uint8, x.shape[:-1] + (K // 2,))
+    _bytes_at_least("scales", scales, moe_fp4_scale_bytes(R, K))
+    _ok("moe_fp4_quantize", lib().moe_fp4_quantize(_p(x), dtype_code(x.dtype), R, K, _p(codes), _p(scales), _s(stream)))
+
+
+def moe_fp4_dequantize(codes, scales, x, stream=None):
+    """The values that codes and scales stand for, into x [..., K]."""
+    R, K = _rows(x)
+    _want("x", x, x.dtype, x.shape)
+    _want("codes", codes, torch.uint8, x.shape[:-1] + (K // 2,))
+    _bytes_at_least("scales", scales, moe_fp4_scale_bytes(R, K))
+    _ok("moe_fp4_dequantize", lib().moe_fp4_dequantize(_p(codes), _p(scales), R, K, dtype_code(x.dtype), _p(x),
+                                                       _s(stream)))
+
+
+def moe_permute_fp4(x, k, E, row_of_slot, counts, tile_offsets, codes, scales, stream=None):
+    """moe_permute with MXFP4 output: codes [rows_max, d/2], scales [moe_fp4_scale_bytes(rows_max, d)]."""
+    T, d = x.shape
+    _want("x", x, x.dtype, (T, d))
+    _want("codes", codes, torch.uint8, (codes.shape[0], d // 2))
+    _bytes_at_least("scales", scales, moe_fp4_scale_bytes(codes.shape[0], d))
+    _ok("moe_permute_fp4", lib().moe_permute_fp4(_p(x), dtype_code(x.dtype), T, d, k, E, _p(row_of_slot), _p(counts),
+                                                 _p(tile_offsets), codes.shape[0], _p(codes), _p(scales), _s(stream)))
+
+
+def moe_grouped_ffn_fwd_fp4(x_codes, x_scales, wgu_codes, wgu_scales, wd_codes, wd_scales, tile_offsets, offsets,
+                            h_codes, h_scales, y_perm, ws, stream=None):
+    """wgu_codes [E, 2f, d/2], wd_codes [E, d, f/2]; h_codes [rows_max, f/2] and h_scales are scratch."""
+    E, d, f2 = wd_codes.shape
+    R, f = x_codes.shape[0], 2 * f2
+    _want("x_codes", x_codes, torch.uint8, (R, d // 2))
+    _want("wgu_codes", wgu_codes, torch.uint8, (E, 2 * f, d // 2))
+    _want("wd_codes", wd_codes, torch.uint8, (E, d, f // 2))
+    _want("h_codes", h_codes, torch.uint8, (R, f // 2))
+    _want("y_perm", y_perm, torch.bfloat16, (R, d))
+    for name, t, rows, cols in (("x_scales", x_scales, R, d), ("h_scales", h_scales, R, f),
+                                ("wgu_scales", wgu_scales, E * 2 * f, d), ("wd_scales", wd_scales, E * d, f)):
+        _bytes_at_least(name, t, -(-rows // 128) * -(-cols // 128) * 512)
+    _ok("moe_grouped_ffn_fwd_fp4", lib().moe_grouped_ffn_fwd_fp4(
+        _p(x_codes), _p(x_scales), _p(wgu_codes), _p(wgu_scales), _p(wd_codes), _p(wd_scales), _p(tile_offsets),
+        _p(offsets), E, d, f, R, _p(h_codes), _p(h_scales), _p(y_perm), _p(ws), ws.numel() * ws.element_size(),
+        _s(stream)))
 
 
 def moe_read_status(ws, stream=None):

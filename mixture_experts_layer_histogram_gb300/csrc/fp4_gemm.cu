@@ -1,0 +1,468 @@
+// Grouped expert FFN on MXFP4 operands: block-scaled tensor cores (sm_103a, tcgen05.mma kind::mxf4),
+// forward only.
+//
+//   GATEUP  [a | b] = xq Wgu[e]^T, h = silu(a) b, written as MXFP4 (codes and scales)
+//   DOWN    y = hq Wd[e]^T, written as bf16
+//
+// One CTA computes 128 grouped rows (the MMA's M, one TMEM lane each) by 256 weight rows (N). For GATEUP
+// the 256 are 128 gate rows and the same features' 128 up rows, so a thread of the epilogue holds a and
+// b of one token for 128 features: it forms h, takes the largest magnitude of each 32 features in its own
+// registers, and writes 16 bytes of codes and one scale byte per block, with no exchange between threads.
+//
+// Per 256 values of K (one ring stage: 16 KB of tokens, 32 KB of weights, 3 KB of scales): six tcgen05.cp
+// bring the scales into TMEM, four per 128 rows and 128 values as the MMA wants them (the scale layout in
+// memory is the one the copy reads), and four MMAs of K = 64 follow, each naming its pair of scale bytes
+// in its instruction descriptor.
+//
+// TMEM has 512 columns and two 256-column accumulators would leave none for scales. The two accumulators
+// overlap in 48 columns instead ([0, 256) and [208, 464), scales in [464, 512)): the epilogue reads the
+// shared columns first and then lets the next tile's MMAs start.
+//
+// Warp roles: warp 0 producer (TMA), warp 1 TMEM allocation and MMA issue, warps 2..9 epilogue (two warps
+// per 32-lane TMEM quarter). The grid is persistent, at most one CTA per SM; every wait is bounded (0.2 s),
+// on timeout the kernel records MOE_ERR_DEVICE_TIMEOUT in the workspace status word and leaves.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "fp4.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+
+namespace moe {
+namespace tc {
+namespace fp4g {
+
+enum Kind { GATEUP = 0, DOWN = 1 };
+
+constexpr int MT = 128;                       // grouped rows per tile
+constexpr int NT = 256;                       // weight rows per tile
+constexpr int KS = 256;                       // values of K per ring stage (128 bytes of codes: the swizzle span)
+constexpr int STAGES = 4;
+constexpr int A_BYTES = MT * 128, B_BYTES = NT * 128;
+constexpr int SF_BYTES = (KS / 128) * 512;    // scales of 128 rows per stage
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 3 * SF_BYTES;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int BUF_BYTES = 2048;               // DOWN: one 32 x 32 block of y per epilogue warp
+constexpr int EPI_BYTES = EPI_WARPS * BUF_BYTES;
+constexpr int NBARS = 2 * STAGES + 3;
+constexpr int MAX_E = MOE_MAX_EXPERTS;
+constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 8 * NBARS + 16 + (MAX_E + 1) * 4;
+static_assert(SMEM <= 232448, "MXFP4 GEMM shared memory exceeds 227 KB");
+static_assert(STAGE_BYTES % 1024 == 0, "ring stages keep the swizzle atoms' 1024-byte alignment");
+
+constexpr uint32_t ACC1 = 208;                // first column of the second accumulator
+constexpr uint32_t SF_COL = 464;              // scales: two sets of 8 (tokens) + 16 (weights) columns
+constexpr uint32_t SF_SET = 24;
+
+struct Params {
+  const int32_t *tile_offsets, *offsets;
+  WsHeader *hdr;
+  int E;
+  int n_ft;               // feature tiles per expert
+  int num_kb;             // ring stages per tile
+  int w_rows_e;           // weight rows per expert
+  int w_second;           // rows from a tile's first 128 weight rows to its second (GATEUP: f, DOWN: 128)
+  int w_step;             // weight rows from one feature tile to the next
+  const uint8_t *a_scales, *w_scales;
+  uint8_t *h, *h_scales;  // GATEUP
+  int f;
+  int64_t rows_max;
+};
+
+struct Tile {
+  int e, ft, start, valid;   // expert, feature tile, first grouped row, routed rows (1..128)
+};
+
+// One CTA's tiles in order: first, first + step, ...; tile = token tile gt * n_ft + feature tile.
+struct Walker {
+  int tile, step, num;
+  int e;
+  __device__ __forceinline__ Walker(int first, int step_, int n) : tile(first), step(step_), num(n), e(0) {}
+  __device__ __forceinline__ bool next(Tile &t, const Params &p, const int *ttoff) {
+    if (tile >= num) return false;
+    const int gt = tile / p.n_ft;
+    t.ft = tile - gt * p.n_ft;
+    while (e + 1 < p.E && ttoff[e + 1] <= gt) ++e;
+    const int i = gt - ttoff[e];
+    const int c = p.offsets[e + 1] - p.offsets[e];
+    t.e = e;
+    t.start = (p.tile_offsets[e] + i) * MT;
+    t.valid = min(MT, c - i * MT);
+    tile += step;
+    return true;
+  }
+};
+
+// Instruction descriptor, kind::mxf4: A and B E2M1, scales E8M0, M = 128, N = 256, both K-major; sf = the
+// first of the two scale bytes (0 or 2) of each operand.
+__device__ __forceinline__ uint32_t idesc(uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NT >> 3) << 17) | (1u << 23) | ((uint32_t)(MT >> 4) << 24) |
+         (sf << 29);
+}
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate));
+}
+// 512 bytes of scales (32 rows of 16 bytes) to four TMEM columns, repeated in each 32-lane quarter.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc));
+}
+// Shared-memory descriptor without swizzle: core matrices of 8 rows x 16 bytes, 128 bytes apart.
+__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(const CUtensorMap *map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+
+// tmA, tmA32: the token codes in boxes of 128 and of 32 rows; tmB: the weight codes, 128 rows; tmC: y (DOWN).
+template <int K>
+__global__ void __launch_bounds__(THREADS, 1)
+    fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+               const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmC, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *epi_smem = smem + STAGES * STAGE_BYTES;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + EPI_BYTES);
+  // bars: full[STAGES], empty[STAGES], tfull, tdrain (the shared columns have been read), mma_done
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + NBARS);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+  int *ttoff = reinterpret_cast<int *>(tmem_holder + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  const uint32_t tfull_bar = bar0 + 8u * (2 * STAGES), tdrain_bar = tfull_bar + 8u, mma_done_bar = tfull_bar + 16u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(tfull_bar, 1);
+    mbar_init(tdrain_bar, EPI_WARPS);
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {   // ttoff = exclusive scan of the token tiles per expert, ceil(rows / 128)
+    int c[8], sum = 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int e = lane * 8 + q;
+      c[q] = e < p.E ? (p.offsets[e + 1] - p.offsets[e] + MT - 1) / MT : 0;
+      sum += c[q];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    int run = incl - sum;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int e = lane * 8 + q;
+      if (e < p.E) ttoff[e] = run;
+      run += c[q];
+    }
+    if (lane == 31) ttoff[p.E] = incl;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const int num_tiles = ttoff[p.E] * p.n_ft;
+  const int64_t kt = (int64_t)p.num_kb * (KS / 128);   // 512-byte scale tiles along K
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ producer
+    int stage = 0, fills = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    Walker walk(blockIdx.x, gridDim.x, num_tiles);
+    for (Tile t; ok && walk.next(t, p, ttoff);) {
+      // rows past the routed ones are not loaded when the tile is at most half full: their products land
+      // in TMEM lanes that the epilogue replaces with zeros
+      const int boxes = t.valid > MT / 2 ? 4 : (t.valid + 31) / 32;
+      const int w0 = t.e * p.w_rows_e + t.ft * p.w_step, w1 = w0 + p.w_second;
+      const uint8_t *sa = p.a_scales + (int64_t)(t.start / MT) * kt * 512;
+      const uint8_t *s0 = p.w_scales + (int64_t)(w0 / 128) * kt * 512, *s1 = p.w_scales + (int64_t)(w1 / 128) * kt * 512;
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 41)) { ok = false; break; }
+        if (elect_one()) {
+          const uint32_t sA = sbase + stage * STAGE_BYTES, sB = sA + A_BYTES, sS = sB + B_BYTES, fb = full_bar(stage);
+          mbar_expect_tx(fb, (uint32_t)boxes * (A_BYTES / 4) + B_BYTES + 3 * SF_BYTES);
+          tma_load_2d(sB, &tmB, kb * 128, w0, fb);
+          tma_load_2d(sB + B_BYTES / 2, &tmB, kb * 128, w1, fb);
+          if (boxes == 4) {
+            tma_load_2d(sA, &tmA, kb * 128, t.start, fb);
+          } else {
+            for (int b = 0; b < boxes; ++b) tma_load_2d(sA + b * (A_BYTES / 4), &tmA32, kb * 128, t.start + 32 * b, fb);
+          }
+          bulk_load(sS, sa + (int64_t)kb * SF_BYTES, SF_BYTES, fb);
+          bulk_load(sS + SF_BYTES, s0 + (int64_t)kb * SF_BYTES, SF_BYTES, fb);
+          bulk_load(sS + 2 * SF_BYTES, s1 + (int64_t)kb * SF_BYTES, SF_BYTES, fb);
+        }
+        __syncwarp();
+        ++fills;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (*abort_flag) {   // leave no copy in flight: wait (bounded) for the last fill of every stage
+      const uint64_t t0 = global_ns();
+      for (int i = 1; i <= STAGES && i <= fills; ++i) {
+        const int f = fills - i;   // fill number f went to stage f % STAGES in ring round f / STAGES
+        while (!mbar_try_wait(full_bar(f % STAGES), (uint32_t)(f / STAGES) & 1u) && global_ns() - t0 < kWaitLimitNs) {}
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    int stage = 0, n = 0, set = 0;
+    uint32_t phase = 0;
+    bool issued = false, ok = true;
+    const uint64_t desc_a0 = sdesc(sbase, 16, 1024), desc_b0 = sdesc(sbase + A_BYTES, 16, 1024);
+    const uint64_t desc_s0 = sf_desc(sbase + A_BYTES + B_BYTES);
+    Walker walk(blockIdx.x, gridDim.x, num_tiles);
+    for (Tile t; ok && walk.next(t, p, ttoff); ++n) {
+      if (n > 0 && !mbar_wait(tdrain_bar, (uint32_t)(n - 1) & 1u, abort_flag, p.hdr, 42)) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + ((n & 1) ? ACC1 : 0u);
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!mbar_wait(full_bar(stage), phase, abort_flag, p.hdr, 43)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t so = (uint32_t)(stage * STAGE_BYTES) >> 4;
+          const uint32_t sfa = tmem_base + SF_COL + (uint32_t)set * SF_SET, sfb = sfa + 8;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {   // 128 values of K each
+            copy_scales(sfa + 4 * h, desc_s0 + so + (uint32_t)((h * 512) >> 4));
+            copy_scales(sfb + 8 * h, desc_s0 + so + (uint32_t)((SF_BYTES + h * 512) >> 4));
+            copy_scales(sfb + 8 * h + 4, desc_s0 + so + (uint32_t)((2 * SF_BYTES + h * 512) >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+              const uint32_t koff = (uint32_t)((2 * h + kk) * 32) >> 4;
+              mma_mxf4(d, desc_a0 + so + koff, desc_b0 + so + koff, idesc(2u * kk), sfa + 4 * h, sfb + 8 * h,
+                       (kb | h | kk) != 0 ? 1u : 0u);
+            }
+          }
+          mma_commit(empty_bar(stage));
+        }
+        __syncwarp();
+        issued = true;
+        set ^= 1;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) break;
+      if (elect_one()) mma_commit(tfull_bar);
+      __syncwarp();
+    }
+    if (issued) {   // every MMA is done before TMEM is freed
+      if (elect_one()) mma_commit(mma_done_bar);
+      __syncwarp();
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(mma_done_bar, 0) && global_ns() - t0 < kWaitLimitNs) {}
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, hh = (warp - 2) >> 2;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t buf = smem_u32(epi_smem) + (uint32_t)(warp - 2) * BUF_BYTES;
+    int n = 0;
+    Walker walk(blockIdx.x, gridDim.x, num_tiles);
+    for (Tile t; walk.next(t, p, ttoff); ++n) {
+      if (!mbar_wait(tfull_bar, (uint32_t)n & 1u, abort_flag, p.hdr, 44)) break;
+      tc_fence_after();
+      const bool second = n & 1;
+      const uint32_t tacc = tmem_base + lane_off + (second ? ACC1 : 0u);
+      const int r_in = quarter * 32 + lane;                 // row within the tile
+      const bool real = r_in < t.valid;
+      // the columns shared with the other accumulator come first: the last 48 of the first
+      // accumulator, the first 48 of the second
+      if (K == GATEUP) {
+        const int64_t row = (int64_t)t.start + r_in;
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int b = second ? 2 * i + hh : 3 - 2 * i - hh;   // block of 32 features
+          uint32_t ra[32], rb[32];
+          tmem_ld32(tacc + 32u * b, ra);
+          tmem_ld32(tacc + 128u + 32u * b, rb);
+          tmem_ld_wait();
+          if (i == 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tdrain_bar);
+          }
+          float hv[32];
+          uint32_t amax = 0;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float a = __uint_as_float(ra[c]);
+            hv[c] = a * sigmoidf_(a) * __uint_as_float(rb[c]);
+            amax = max(amax, __float_as_uint(hv[c]) & 0x7fffffffu);
+          }
+          const uint32_t byte = real ? fp4::scale_byte(amax) : 0u;
+          const float inv = real ? fp4::inv_scale(byte) : 0.0f;
+          uint32_t q[4];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) hv[c] = inv == 0.0f ? 0.0f : hv[c] * inv;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) q[c] = fp4::pack_e2m1x8(hv + 8 * c);
+          if (row < p.rows_max) {
+            *reinterpret_cast<uint4 *>(p.h + row * (p.f / 2) + t.ft * 64 + 16 * b) = make_uint4(q[0], q[1], q[2], q[3]);
+            p.h_scales[fp4::scale_word(row, t.ft, p.f / 128) + b] = (uint8_t)byte;
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int c8 = second ? 2 * i + hh : 7 - 2 * i - hh;   // block of 32 columns
+          uint32_t r[32];
+          tmem_ld32(tacc + 32u * c8, r);
+          tmem_ld_wait();
+          if (i == 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tdrain_bar);
+          }
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = real ? pack_bf16x2(__uint_as_float(r[8 * q + 2 * j]), __uint_as_float(r[8 * q + 2 * j + 1])) : 0u;
+            const uint32_t addr = buf + (uint32_t)lane * 64 + ((uint32_t)(q ^ ((lane >> 1) & 3)) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            bulk_store(&tmC, t.ft * NT + 32 * c8, t.start + quarter * 32, buf);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        }
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
+  }
+}
+
+// 2D codes [rows, bytes per row], boxes of 128 bytes x box_rows rows, 128-byte swizzle.
+static bool codes_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {row_bytes, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int K>
+static int launch(const CUtensorMap &a, const CUtensorMap &a32, const CUtensorMap &b, const CUtensorMap &c,
+                  const Params &p, cudaStream_t s) {
+  MOE_TRY_CUDA(cudaFuncSetAttribute(fp4_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
+  int64_t grid = sm_count();
+  const int64_t most = p.rows_max / MT * p.n_ft;   // tiles there can be
+  if (most < grid) grid = most;
+  fp4_kernel<K><<<(int)grid, THREADS, SMEM, s>>>(a, a32, b, c, p);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
+}  // namespace fp4g
+}  // namespace tc
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales, const void *wgu_codes,
+                                       const void *wgu_scales, const void *wd_codes, const void *wd_scales,
+                                       const int32_t *tile_offsets, const int32_t *offsets, int E, int d, int f,
+                                       int64_t rows_max, void *h_codes, void *h_scales, void *y_perm, void *ws,
+                                       size_t ws_bytes, moe_stream_t stream) {
+  using namespace tc::fp4g;
+  if (E < 1 || E > MOE_MAX_EXPERTS || d < 1 || f < 1 || rows_max < 0 || rows_max % MOE_GROUP_ROWS)
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) ||
+      ws_bytes < moe_grouped_ffn_workspace_size(E, d, f, rows_max, MOE_BF16, 0))
+    return MOE_ERR_INVALID_ARG;
+  if (d % 256 || f % 256 || rows_max >= ((int64_t)1 << 31) || (int64_t)E * 2 * f >= ((int64_t)1 << 31) ||
+      (int64_t)E * d >= ((int64_t)1 << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if (rows_max == 0) return MOE_OK;
+  const void *ptrs[] = {x_codes, x_scales, wgu_codes, wgu_scales, wd_codes, wd_scales, h_codes, h_scales, y_perm};
+  for (const void *q : ptrs)
+    if (!q || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (!tile_offsets || !offsets) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  CUtensorMap a, a32, b, c;
+  Params p{};
+  p.tile_offsets = tile_offsets;
+  p.offsets = offsets;
+  p.hdr = static_cast<WsHeader *>(ws);
+  p.E = E;
+  p.rows_max = rows_max;
+  p.f = f;
+
+  if (!codes_map(&a, x_codes, rows_max, d / 2, MT) || !codes_map(&a32, x_codes, rows_max, d / 2, 32) ||
+      !codes_map(&b, wgu_codes, (uint64_t)E * 2 * f, d / 2, 128))
+    return MOE_ERR_CUDA;
+  p.n_ft = f / 128;
+  p.num_kb = d / KS;
+  p.w_rows_e = 2 * f;
+  p.w_second = f;
+  p.w_step = 128;
+  p.a_scales = (const uint8_t *)x_scales;
+  p.w_scales = (const uint8_t *)wgu_scales;
+  p.h = (uint8_t *)h_codes;
+  p.h_scales = (uint8_t *)h_scales;
+  int rc = launch<GATEUP>(a, a32, b, b, p, s);   // tmC is not used
+  if (rc) return rc;
+
+  if (!codes_map(&a, h_codes, rows_max, f / 2, MT) || !codes_map(&a32, h_codes, rows_max, f / 2, 32) ||
+      !codes_map(&b, wd_codes, (uint64_t)E * d, f / 2, 128) || !tc::make_store_map(&c, y_perm, rows_max, d))
+    return MOE_ERR_CUDA;
+  p.n_ft = d / NT;
+  p.num_kb = f / KS;
+  p.w_rows_e = d;
+  p.w_second = 128;
+  p.w_step = NT;
+  p.a_scales = (const uint8_t *)h_scales;
+  p.w_scales = (const uint8_t *)wd_scales;
+  return launch<DOWN>(a, a32, b, c, p, s);
+}

@@ -80,3 +80,26 @@ def test_adamw_plans(L):
         assert L.moe_adamw_step(*args, NULL) == -1
     host[0] = 0                                                 # no plan
     assert L.moe_adamw_step(ptr, FAKE, .9, .99, 1e-8, FAKE, NULL) == -1
+
+
+def test_fp4_refusals(L):
+    assert L.moe_fp4_scale_bytes(129, 160) == 2 * 2 * 512 and L.moe_fp4_scale_bytes(0, 32) == 0
+    assert L.moe_fp4_quantize(FAKE, 1, 4, 48, FAKE, FAKE, NULL) == -2
+    assert L.moe_fp4_quantize(FAKE, 2, 4, 64, FAKE, FAKE, NULL) == -1
+    assert L.moe_fp4_quantize(FAKE, 1, -1, 64, FAKE, FAKE, NULL) == -1
+    assert L.moe_fp4_quantize(ODD, 1, 4, 64, FAKE, FAKE, NULL) == -1
+    assert L.moe_fp4_quantize(NULL, 1, 0, 64, NULL, NULL, NULL) == 0
+    assert L.moe_fp4_dequantize(FAKE, NULL, 4, 64, 1, FAKE, NULL) == -1
+    assert L.moe_fp4_dequantize(FAKE, FAKE, 4, 63, 1, FAKE, NULL) == -2
+    rm = L.moe_grouped_rows_max(64, 2, 8)
+    assert L.moe_permute_fp4(FAKE, 1, 64, 96, 2, 8, FAKE, FAKE, FAKE, rm, FAKE, FAKE, NULL) == -2
+    assert L.moe_permute_fp4(FAKE, 1, 64, 128, 2, 8, FAKE, FAKE, FAKE, rm - 128, FAKE, FAKE, NULL) == -1
+    assert L.moe_permute_fp4(FAKE, 1, 64, 128, 17, 8, FAKE, FAKE, FAKE, rm, FAKE, FAKE, NULL) == -1
+    ws = L.moe_grouped_ffn_workspace_size(8, 256, 256, rm, 1, 0)
+
+    def ffn(E=8, d=256, f=256, rows=rm, y=FAKE, w=FAKE, n=ws):
+        return L.moe_grouped_ffn_fwd_fp4(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, E, d, f, rows, FAKE, FAKE, y, w, n,
+                                         NULL)
+    assert ffn(d=128) == -2 and ffn(f=384) == -2 and ffn(E=0) == -1 and ffn(E=300) == -1
+    assert ffn(rows=rm + 1) == -1 and ffn(y=NULL) == -1 and ffn(w=NULL) == -1 and ffn(n=8) == -1 and ffn(w=ODD) == -1
+    assert ffn(rows=0) == 0
