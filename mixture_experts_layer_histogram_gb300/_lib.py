@@ -93,6 +93,8 @@ class MoeError(RuntimeError):
 def lib():
     """Load libmoe.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -123,12 +125,19 @@ def _p(t):
         return None
     if not t.is_cuda:
         raise ValueError("libmoe takes CUDA tensors only")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+# The current stream's handle without building a Stream object (0.1 us instead of 3 us per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _s(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _want(name, t, dtype, shape):
@@ -136,6 +145,10 @@ def _want(name, t, dtype, shape):
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} is needed, got {t.dtype} "
                          f"{tuple(t.shape)} with strides {t.stride()}")
+
+
+def _scale_bytes(rows, cols):
+    return -(-rows // 128) * -(-cols // 128) * 512
 
 
 def _bytes_at_least(name, t, n):
@@ -395,36 +408,43 @@ def moe_fp4_scale_bytes(R, K):
 
 def _rows(x):
     """A tensor [..., K] as its number of rows and K."""
-    return (x.numel() // x.shape[-1] if x.shape[-1] else 0), x.shape[-1]
+    K = x.shape[-1]
+    return (x.numel() // K if K else 0), K
 
 
 def moe_fp4_quantize(x, codes, scales, stream=None):
     """x [..., K] (rows in order) -> codes [..., K/2] uint8, scales [moe_fp4_scale_bytes(rows, K)] uint8."""
+    shape = x.shape
     R, K = _rows(x)
-    _want("x", x, x.dtype, x.shape)
-    _want("codes", codes, torch.uint8, x.shape[:-1] + (K // 2,))
-    _bytes_at_least("scales", scales, moe_fp4_scale_bytes(R, K))
-    _ok("moe_fp4_quantize", lib().moe_fp4_quantize(_p(x), dtype_code(x.dtype), R, K, _p(codes), _p(scales), _s(stream)))
+    dt = x.dtype
+    _want("x", x, dt, shape)
+    _want("codes", codes, torch.uint8, shape[:-1] + (K // 2,))
+    _bytes_at_least("scales", scales, _scale_bytes(R, K))
+    _ok("moe_fp4_quantize", lib().moe_fp4_quantize(_p(x), dtype_code(dt), R, K, _p(codes), _p(scales), _s(stream)))
 
 
 def moe_fp4_dequantize(codes, scales, x, stream=None):
     """The values that codes and scales stand for, into x [..., K]."""
+    shape = x.shape
     R, K = _rows(x)
-    _want("x", x, x.dtype, x.shape)
-    _want("codes", codes, torch.uint8, x.shape[:-1] + (K // 2,))
-    _bytes_at_least("scales", scales, moe_fp4_scale_bytes(R, K))
-    _ok("moe_fp4_dequantize", lib().moe_fp4_dequantize(_p(codes), _p(scales), R, K, dtype_code(x.dtype), _p(x),
+    dt = x.dtype
+    _want("x", x, dt, shape)
+    _want("codes", codes, torch.uint8, shape[:-1] + (K // 2,))
+    _bytes_at_least("scales", scales, _scale_bytes(R, K))
+    _ok("moe_fp4_dequantize", lib().moe_fp4_dequantize(_p(codes), _p(scales), R, K, dtype_code(dt), _p(x),
                                                        _s(stream)))
 
 
 def moe_permute_fp4(x, k, E, row_of_slot, counts, tile_offsets, codes, scales, stream=None):
     """moe_permute with MXFP4 output: codes [rows_max, d/2], scales [moe_fp4_scale_bytes(rows_max, d)]."""
     T, d = x.shape
-    _want("x", x, x.dtype, (T, d))
-    _want("codes", codes, torch.uint8, (codes.shape[0], d // 2))
-    _bytes_at_least("scales", scales, moe_fp4_scale_bytes(codes.shape[0], d))
-    _ok("moe_permute_fp4", lib().moe_permute_fp4(_p(x), dtype_code(x.dtype), T, d, k, E, _p(row_of_slot), _p(counts),
-                                                 _p(tile_offsets), codes.shape[0], _p(codes), _p(scales), _s(stream)))
+    R = codes.shape[0]
+    dt = x.dtype
+    _want("x", x, dt, (T, d))
+    _want("codes", codes, torch.uint8, (R, d // 2))
+    _bytes_at_least("scales", scales, _scale_bytes(R, d))
+    _ok("moe_permute_fp4", lib().moe_permute_fp4(_p(x), dtype_code(dt), T, d, k, E, _p(row_of_slot), _p(counts),
+                                                 _p(tile_offsets), R, _p(codes), _p(scales), _s(stream)))
 
 
 def moe_grouped_ffn_fwd_fp4(x_codes, x_scales, wgu_codes, wgu_scales, wd_codes, wd_scales, tile_offsets, offsets,
@@ -437,9 +457,10 @@ def moe_grouped_ffn_fwd_fp4(x_codes, x_scales, wgu_codes, wgu_scales, wd_codes, 
     _want("wd_codes", wd_codes, torch.uint8, (E, d, f // 2))
     _want("h_codes", h_codes, torch.uint8, (R, f // 2))
     _want("y_perm", y_perm, torch.bfloat16, (R, d))
-    for name, t, rows, cols in (("x_scales", x_scales, R, d), ("h_scales", h_scales, R, f),
-                                ("wgu_scales", wgu_scales, E * 2 * f, d), ("wd_scales", wd_scales, E * d, f)):
-        _bytes_at_least(name, t, -(-rows // 128) * -(-cols // 128) * 512)
+    _bytes_at_least("x_scales", x_scales, _scale_bytes(R, d))
+    _bytes_at_least("h_scales", h_scales, _scale_bytes(R, f))
+    _bytes_at_least("wgu_scales", wgu_scales, _scale_bytes(E * 2 * f, d))
+    _bytes_at_least("wd_scales", wd_scales, _scale_bytes(E * d, f))
     _ok("moe_grouped_ffn_fwd_fp4", lib().moe_grouped_ffn_fwd_fp4(
         _p(x_codes), _p(x_scales), _p(wgu_codes), _p(wgu_scales), _p(wd_codes), _p(wd_scales), _p(tile_offsets),
         _p(offsets), E, d, f, R, _p(h_codes), _p(h_scales), _p(y_perm), _p(ws), ws.numel() * ws.element_size(),
