@@ -64,16 +64,33 @@ struct Hyper {
 
 __device__ __forceinline__ uint32_t weyl(uint32_t i, uint32_t t) { return i * 2654435769u + t * 1640531535u; }
 
-// y (|y| <= 448) to e4m3 codes, rounded down on the grid of its binade after adding u20 / 2^20 of a step.
-__device__ __forceinline__ float dither_e4m3(float y, uint32_t u20) {
-  const float a = fabsf(y);
-  const float normal = __uint_as_float((__float_as_uint(a) + u20) & 0xfff00000u);
-  const float small = (float)((__float2int_rz(a * 536870912.0f) + (int)u20) >> 20) * 0.001953125f;   // steps of 2^-9
-  const float r = a < 0.015625f ? small : normal;
-  return y != y ? y : copysignf(fminf(r, 448.0f), y);
+// e4m3 codes of y (|y| <= 448 but for rounding), rounded down in magnitude after adding u / 2^20 of a step, where
+// u = h >> 12. z = y 2^-120 moves e4m3's exponents onto the lowest ones of fp32, subnormals onto subnormals, so
+// its bits from the 20th on are the code and adding u below them is the dither; four bits higher, the code is
+// the top byte (at most 0x7e, 448: a block's largest value may lie an ulp above it).
+__device__ __forceinline__ uint32_t dither_top(float z, uint32_t h) {
+  return min(((h >> 12) + __float_as_uint(z)) << 4, 0x7effffffu);
 }
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {   // exact here: the values lie on the grid
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t dither_top_signed(float z, uint32_t h) {
+  return dither_top(z, h) | (__float_as_uint(z) & 0x80000000u);   // the shift has dropped z's sign
+}
+// The same for any y: a NaN or an infinity becomes e4m3 NaN.
+__device__ __forceinline__ uint32_t dither_top_any(float y, uint32_t h) {
+  return fabsf(y) <= 500.0f ? dither_top_signed(y * 0x1p-120f, h) : 0x7f000000u;
+}
+// The top bytes of four words
+__device__ __forceinline__ uint32_t top_bytes(const uint32_t *x) {
+  return __byte_perm(__byte_perm(x[0], x[1], 0x0073), __byte_perm(x[2], x[3], 0x0073), 0x5410);
+}
+__device__ __forceinline__ float sqrt_approx(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 __device__ __forceinline__ void unpack_e4m3x8(const uint2 &q, float *v) {
   const uint32_t w[2] = {q.x, q.y};
@@ -92,162 +109,299 @@ __device__ __forceinline__ uint32_t dither_bf16_bits(float p, uint32_t u16) {
   return (b + u16) & 0xffff0000u;
 }
 
-__device__ __forceinline__ void load8(const float *p, float *v) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// Loads of values that are read once: they pass by the L1, which keeps the plan's entries.
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint2 ld_once2(const void *p) {
+  uint2 r;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
 }
 __device__ __forceinline__ void store8(float *p, const float *v) {
   reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *v) {
-  unpack_bf16x8(*reinterpret_cast<const uint4 *>(p), v);
 }
 template <typename T> __device__ __forceinline__ float load1(const T *p) {
   if constexpr (sizeof(T) == 4) return *p;
   else return __bfloat162float(*p);
 }
 
-template <int K>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const Tensor *__restrict__ tensors,
-                                                         const Chunk *__restrict__ chunks, int64_t nchunks,
-                                                         const Hyper hy, moe_adamw_state *st, int bump) {
+// Blocks per SM (they set the grid and the registers). fp32 states are bound by HBM, which a few blocks with
+// wide rows of loads fill best; 8-bit states by instructions, which more warps issue better. Measured on
+// one layer's 403M values (bf16): fp32 states with a master 1851 us at 2 blocks, 1922 at 3, 1956 at 4; 8-bit
+// states 934 us at 5 blocks, 1004 at 4, 1030 at 6, 1082 at 3.
+constexpr int per_sm(int k) { return k >= F32_F8 ? 5 : 2; }
+
+// The step's constants.
+struct Coef {
+  float lr, gs, lr1, inv_root2;
+  uint32_t t32;
+};
+
+// One thread's eight values of a tensor as they lie in memory (the aligned, complete case).
+template <int K> struct Raw8 {
+  static constexpr bool kF8 = K >= F32_F8, kF32 = K == F32_F32 || K == F32_F8;
+  static constexpr bool kMaster = K == BF16_MASTER_F32 || K == BF16_MASTER_F8;
+  uint4 g[kF32 ? 2 : 1], p[kF32 || kMaster ? 2 : 1], m[kF8 ? 1 : 2], v[kF8 ? 1 : 2];
+  float ms, vs;
+  __device__ __forceinline__ void load(const Tensor &t, int64_t i0) {
+    const int64_t es = kF32 ? 4 : 2;
+    const uint8_t *gp = (const uint8_t *)t.g + i0 * es;
+    g[0] = ld_once(gp);
+    if (kF32) g[kF32 ? 1 : 0] = ld_once(gp + 16);
+    const uint8_t *pp = kMaster ? (const uint8_t *)(t.master + i0) : (const uint8_t *)t.p + i0 * es;
+    p[0] = ld_once(pp);
+    if (kF32 || kMaster) p[kF32 || kMaster ? 1 : 0] = ld_once(pp + 16);
+    if (kF8) {
+      const uint2 a = ld_once2((const uint8_t *)t.m + i0), b = ld_once2((const uint8_t *)t.v + i0);
+      m[0] = make_uint4(a.x, a.y, 0, 0);
+      v[0] = make_uint4(b.x, b.y, 0, 0);
+      ms = t.m_scale[i0 / kBlockQ];
+      vs = t.v_scale[i0 / kBlockQ];
+    } else {
+      const float *mp = (const float *)t.m + i0, *vp = (const float *)t.v + i0;
+      m[0] = ld_once(mp);
+      m[kF8 ? 0 : 1] = ld_once(mp + 4);
+      v[0] = ld_once(vp);
+      v[kF8 ? 0 : 1] = ld_once(vp + 4);
+    }
+  }
+};
+__device__ __forceinline__ void unpack_f32x8(const uint4 &a, const uint4 &b, float *v) {
+  v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+  v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+}
+
+// Eight values of a tensor, the thread's own from i0 on. FULL: all eight are inside it, vector access is aligned and
+// `raw` holds them; otherwise the `live` ones inside are read one by one. All lanes of a warp take part (8-bit
+// states: its 256 values are one block).
+template <int K, bool FULL>
+__device__ __forceinline__ void update8(const Tensor &t, const Raw8<K> &raw, int64_t i0, int live, const Hyper &hy,
+                                        const Coef &co, float decay) {
   constexpr bool kF8 = K >= F32_F8;
   constexpr bool kMaster = K == BF16_MASTER_F32 || K == BF16_MASTER_F8;
   constexpr bool kF32 = K == F32_F32 || K == F32_F8;
   using T = typename std::conditional<kF32, float, __nv_bfloat16>::type;
+  const T *gp = (const T *)t.g + i0;
+  T *pp = (T *)t.p + i0;
+  float *master = t.master + (kMaster ? i0 : 0);
+  float *mf = (float *)t.m + (kF8 ? 0 : i0), *vf = (float *)t.v + (kF8 ? 0 : i0);
+  uint8_t *m8 = (uint8_t *)t.m + (kF8 ? i0 : 0), *v8 = (uint8_t *)t.v + (kF8 ? i0 : 0);
+  const int64_t qb = i0 / kBlockQ;
+  float g[kVec], p[kVec], m[kVec], v[kVec];
+  float ms = 0.0f, vs = 0.0f;
+  if (FULL) {
+    if (kF32) unpack_f32x8(raw.g[0], raw.g[kF32 ? 1 : 0], g);
+    else unpack_bf16x8(raw.g[0], g);
+    if (kF32 || kMaster) unpack_f32x8(raw.p[0], raw.p[kF32 || kMaster ? 1 : 0], p);
+    else unpack_bf16x8(raw.p[0], p);
+    if (kF8) {
+      unpack_e4m3x8(make_uint2(raw.m[0].x, raw.m[0].y), m);
+      unpack_e4m3x8(make_uint2(raw.v[0].x, raw.v[0].y), v);
+      ms = raw.ms;
+      vs = raw.vs;
+    } else {
+      unpack_f32x8(raw.m[0], raw.m[kF8 ? 0 : 1], m);
+      unpack_f32x8(raw.v[0], raw.v[kF8 ? 0 : 1], v);
+    }
+  } else {
+    if (kF8) {
+      ms = t.m_scale[qb];
+      vs = t.v_scale[qb];
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      g[j] = p[j] = m[j] = v[j] = 0.0f;
+      if (j >= live) continue;
+      g[j] = load1(gp + j);
+      p[j] = kMaster ? master[j] : load1(pp + j);
+      m[j] = kF8 ? (float)((const __nv_fp8_e4m3 *)m8)[j] : mf[j];
+      v[j] = kF8 ? (float)((const __nv_fp8_e4m3 *)v8)[j] : vf[j];
+    }
+  }
+  const uint32_t h0 = weyl((uint32_t)i0, co.t32);
+  float sum = 0.0f;   // of the parameters: NaN where one of them is
+  bool odd = false;
+  if constexpr (!kF8) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const float gj = g[j] * co.gs;
+      m[j] = fmaf(hy.beta1, m[j], hy.omb1 * gj);
+      v[j] = fmaf(hy.beta2, v[j], hy.omb2 * gj * gj);
+      // approximate root and reciprocal: off by a few 2^-24, on a term that is a small part of p
+      p[j] = fmaf(p[j], decay, co.lr1 * m[j] * rcp_approx(fmaf(sqrt_approx(v[j]), co.inv_root2, hy.eps)));
+      sum += p[j];
+    }
+    odd = sum != sum;
+    if (FULL) {
+      store8(mf, m);
+      store8(vf, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        if (j >= live) continue;
+        mf[j] = m[j];
+        vf[j] = v[j];
+      }
+    }
+  } else {
+    // m and v are rounded at each operation (no fused multiply-add), and the largest root is the root of the
+    // largest v, rounded to nearest: the scales then follow from the formulas alone, bit for bit, and a
+    // block's largest value gets the code it should. The other roots may be approximate.
+    const float kg = hy.omb1 * co.gs, kg2 = hy.omb2 * (co.gs * co.gs);
+    float mx = 0.0f, vx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      m[j] = __fadd_rn(__fmul_rn(hy.beta1, __fmul_rn(m[j], ms)), __fmul_rn(kg, g[j]));
+      const float a = __fmul_rn(v[j], vs);
+      v[j] = __fadd_rn(__fmul_rn(hy.beta2, __fmul_rn(a, a)), __fmul_rn(kg2, __fmul_rn(g[j], g[j])));
+      mx = fmaxf(mx, fabsf(m[j]));
+      vx = fmaxf(vx, v[j]);
+    }
+    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));   // of numbers >= 0, as integers
+    float vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vx)));
+    vx = sqrtf(vtop);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      v[j] = v[j] == vtop ? vx : sqrt_approx(v[j]);
+      p[j] = fmaf(p[j], decay, co.lr1 * m[j] * rcp_approx(fmaf(v[j], co.inv_root2, hy.eps)));
+      sum += p[j];
+    }
+    // A NaN in m or v shows in p and so in the sum; infinities show in the maxima. Such blocks, and those whose
+    // scaling would leave fp32's normal range, take the general form.
+    odd = __any_sync(0xffffffffu, sum != sum) || !(fmaxf(mx, vx) < 16384.0f);
+    uint32_t mc[kVec], vc[kVec];
+    if (odd) {   // a non-finite value counts for nothing in the scale and is held as NaN
+      constexpr float kMax = 3.402823466e38f;
+      mx = vx = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        if (fabsf(m[j]) <= kMax) mx = fmaxf(mx, fabsf(m[j]));
+        if (v[j] <= kMax) vx = fmaxf(vx, v[j]);
+      }
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+      vx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vx)));
+    }
+    // below 1e-30 a block is held as zeros
+    const bool mk = mx >= 1e-30f, vk = vx >= 1e-30f;
+    const float mi = mk ? __frcp_rn(mx) * 448.0f : 0.0f, vi = vk ? __frcp_rn(vx) * 448.0f : 0.0f;
+    if (!odd) {
+      const float mz = mi * 0x1p-120f, vz = vi * 0x1p-120f;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const uint32_t h = h0 + (uint32_t)j * 2654435769u;
+        mc[j] = dither_top_signed(m[j] * mz, h);
+        vc[j] = dither_top(v[j] * vz, h + 0x55555555u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const uint32_t h = h0 + (uint32_t)j * 2654435769u;
+        mc[j] = dither_top_any(m[j] * mi, h);
+        vc[j] = dither_top_any(v[j] * vi, h + 0x55555555u);
+      }
+    }
+    if ((threadIdx.x & 31) == 0) {
+      t.m_scale[qb] = mk ? mx * (1.0f / 448.0f) : 0.0f;
+      t.v_scale[qb] = vk ? vx * (1.0f / 448.0f) : 0.0f;
+    }
+    if (FULL) {
+      *reinterpret_cast<uint2 *>(m8) = make_uint2(top_bytes(mc), top_bytes(mc + 4));
+      *reinterpret_cast<uint2 *>(v8) = make_uint2(top_bytes(vc), top_bytes(vc + 4));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        if (j >= live) continue;
+        m8[j] = (uint8_t)(mc[j] >> 24);
+        v8[j] = (uint8_t)(vc[j] >> 24);
+      }
+    }
+  }
+  if constexpr (kF32) {
+    if (FULL) {
+      store8(pp, p);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (j < live) pp[j] = p[j];
+    }
+  } else {
+    uint32_t pb[kVec / 2];   // two bf16 each
+    if (kMaster) {
+#pragma unroll
+      for (int j = 0; j < kVec / 2; ++j) pb[j] = pack_bf16x2(p[2 * j], p[2 * j + 1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; j += 2) {
+        uint32_t b[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          b[q] = ((h0 + 0xaaaaaaaau + (uint32_t)(j + q) * 2654435769u) >> 16) + __float_as_uint(p[j + q]);
+          if (odd && p[j + q] != p[j + q]) b[q] = 0x7fff0000u;   // the sum can wrap on the bits of a NaN
+        }
+        pb[j / 2] = __byte_perm(b[0], b[1], 0x7632);
+      }
+    }
+    if (FULL) {
+      *reinterpret_cast<uint4 *>(pp) = make_uint4(pb[0], pb[1], pb[2], pb[3]);
+      if (kMaster) store8(master, p);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        if (j >= live) continue;
+        pp[j] = __ushort_as_bfloat16((unsigned short)(pb[j / 2] >> (16 * (j & 1))));
+        if (kMaster) master[j] = p[j];
+      }
+    }
+  }
+}
+
+template <int K>
+__global__ void __launch_bounds__(kThreads, per_sm(K)) adamw_kernel(const Tensor *__restrict__ tensors,
+                                                                    const Chunk *__restrict__ chunks, int64_t nchunks,
+                                                                    const Hyper hy, moe_adamw_state *st, int bump) {
+  constexpr int kPasses = kChunk / (kThreads * kVec);
+  constexpr bool kF8 = K >= F32_F8;
   const int lane = threadIdx.x & 31;
   const int64_t step = st->step + 1;
-  const float lr = st->lr, gs = st->grad_scale;
+  Coef co;
+  co.lr = st->lr;
+  co.gs = st->grad_scale;
   const float bc1 = -expm1f((float)step * hy.log_beta1), bc2 = -expm1f((float)step * hy.log_beta2);
-  const float lr1 = lr / bc1, inv_root2 = 1.0f / sqrtf(bc2);
-  const uint32_t t32 = (uint32_t)step;
+  co.lr1 = -co.lr / bc1;
+  co.inv_root2 = 1.0f / sqrtf(bc2);
+  co.t32 = (uint32_t)step;
 
+  Chunk ahead = blockIdx.x < nchunks ? chunks[blockIdx.x] : Chunk{0, 0};
   for (int64_t ci = blockIdx.x; ci < nchunks; ci += gridDim.x) {
-    const Chunk ch = chunks[ci];
+    const Chunk ch = ahead;
+    if (ci + gridDim.x < nchunks) ahead = chunks[ci + gridDim.x];
     const Tensor t = tensors[ch.tensor];
-    const float decay = 1.0f - lr * t.weight_decay;
-    const T *gp = (const T *)t.g;
-    T *pp = (T *)t.p;
-#pragma unroll
-    for (int pass = 0; pass < kChunk / (kThreads * kVec); ++pass) {
-      const int64_t i0 = (int64_t)ch.index * kChunk + pass * (kThreads * kVec) + threadIdx.x * kVec;
-      if (i0 - lane * kVec >= t.n) continue;              // the whole warp lies past the end
-      const int64_t left = t.n - i0;
-      const int live = left >= kVec ? kVec : (left > 0 ? (int)left : 0);
-      const bool vec = live == kVec && t.aligned;
-      float g[kVec], p[kVec], m[kVec], v[kVec];
-      float ms = 0.0f, vs = 0.0f;
-      const int64_t qb = i0 / kBlockQ;
-      if (kF8) {
-        ms = t.m_scale[qb];
-        vs = t.v_scale[qb];
+    const float decay = 1.0f - co.lr * t.weight_decay;
+    const int64_t first = (int64_t)ch.index * kChunk + threadIdx.x * kVec;
+    Raw8<K> raw;
+    if (t.aligned && (int64_t)(ch.index + 1) * kChunk <= t.n) {
+#pragma unroll 1
+      for (int pass = 0; pass < kPasses; ++pass) {
+        raw.load(t, first + pass * (kThreads * kVec));
+        update8<K, true>(t, raw, first + pass * (kThreads * kVec), kVec, hy, co, decay);
       }
-      if (vec) {
-        load8(gp + i0, g);
-        if (kMaster) load8(t.master + i0, p);
-        else load8(pp + i0, p);
-        if (kF8) {
-          unpack_e4m3x8(*reinterpret_cast<const uint2 *>((const uint8_t *)t.m + i0), m);
-          unpack_e4m3x8(*reinterpret_cast<const uint2 *>((const uint8_t *)t.v + i0), v);
+    } else {
+#pragma unroll 1
+      for (int pass = 0; pass < kPasses; ++pass) {
+        const int64_t i0 = first + pass * (kThreads * kVec);
+        const int64_t left = t.n - i0, warp_left = left + lane * kVec;
+        if (warp_left <= 0) break;
+        // 8-bit states: the warp's 256 values are updated together
+        if (t.aligned && (kF8 ? warp_left >= 32 * kVec : left >= kVec)) {
+          raw.load(t, i0);
+          update8<K, true>(t, raw, i0, kVec, hy, co, decay);
         } else {
-          load8((const float *)t.m + i0, m);
-          load8((const float *)t.v + i0, v);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          g[j] = p[j] = m[j] = v[j] = 0.0f;
-          if (j >= live) continue;
-          g[j] = load1(gp + i0 + j);
-          p[j] = kMaster ? t.master[i0 + j] : load1(pp + i0 + j);
-          if (kF8) {
-            m[j] = (float)((const __nv_fp8_e4m3 *)t.m)[i0 + j];
-            v[j] = (float)((const __nv_fp8_e4m3 *)t.v)[i0 + j];
-          } else {
-            m[j] = ((const float *)t.m)[i0 + j];
-            v[j] = ((const float *)t.v)[i0 + j];
-          }
-        }
-      }
-      float mx = 0.0f, vx = 0.0f;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float gj = g[j] * gs;
-        if (kF8) {
-          m[j] *= ms;
-          v[j] *= vs;
-          v[j] *= v[j];
-        }
-        m[j] = hy.beta1 * m[j] + hy.omb1 * gj;
-        v[j] = hy.beta2 * v[j] + hy.omb2 * (gj * gj);
-        const float root = sqrtf(v[j]);
-        p[j] = p[j] * decay - lr1 * m[j] / (root * inv_root2 + hy.eps);
-        if (kF8) {
-          v[j] = root;
-          mx = fmaxf(mx, fabsf(m[j]));
-          vx = fmaxf(vx, root);
-        }
-      }
-      float mi = 0.0f, vi = 0.0f;
-      if (kF8) {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-          vx = fmaxf(vx, __shfl_xor_sync(0xffffffffu, vx, off));
-        }
-        mi = mx >= 1e-30f ? 448.0f / mx : 0.0f;   // below it the block is held as zeros
-        vi = vx >= 1e-30f ? 448.0f / vx : 0.0f;
-        if (lane == 0) {
-          t.m_scale[qb] = mx >= 1e-30f ? mx / 448.0f : 0.0f;
-          t.v_scale[qb] = vx >= 1e-30f ? vx / 448.0f : 0.0f;
-        }
-      }
-      uint32_t pb[kVec];
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const uint32_t h = weyl((uint32_t)i0 + j, t32);
-        if (kF8) {
-          m[j] = dither_e4m3(m[j] * mi, h >> 12);
-          v[j] = dither_e4m3(v[j] * vi, (h + 0x55555555u) >> 12);
-        }
-        if (!kF32 && !kMaster) pb[j] = dither_bf16_bits(p[j], (h + 0xaaaaaaaau) >> 16);
-        if (kMaster) pb[j] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(p[j])) << 16;
-      }
-      if (vec) {
-        if constexpr (kF32) {
-          store8((float *)t.p + i0, p);
-        } else {
-          *reinterpret_cast<uint4 *>(pp + i0) =
-              make_uint4((pb[0] >> 16) | pb[1], (pb[2] >> 16) | pb[3], (pb[4] >> 16) | pb[5], (pb[6] >> 16) | pb[7]);
-          if (kMaster) store8(t.master + i0, p);
-        }
-        if (kF8) {
-          *reinterpret_cast<uint2 *>((uint8_t *)t.m + i0) =
-              make_uint2(e4m3x2(m[0], m[1]) | e4m3x2(m[2], m[3]) << 16, e4m3x2(m[4], m[5]) | e4m3x2(m[6], m[7]) << 16);
-          *reinterpret_cast<uint2 *>((uint8_t *)t.v + i0) =
-              make_uint2(e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16, e4m3x2(v[4], v[5]) | e4m3x2(v[6], v[7]) << 16);
-        } else {
-          store8((float *)t.m + i0, m);
-          store8((float *)t.v + i0, v);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          if (j >= live) continue;
-          if constexpr (kF32) {
-            ((float *)t.p)[i0 + j] = p[j];
-          } else {
-            pp[i0 + j] = __ushort_as_bfloat16((unsigned short)(pb[j] >> 16));
-            if (kMaster) t.master[i0 + j] = p[j];
-          }
-          if (kF8) {
-            ((uint8_t *)t.m)[i0 + j] = (uint8_t)e4m3x2(m[j], 0.0f);
-            ((uint8_t *)t.v)[i0 + j] = (uint8_t)e4m3x2(v[j], 0.0f);
-          } else {
-            ((float *)t.m)[i0 + j] = m[j];
-            ((float *)t.v)[i0 + j] = v[j];
-          }
+          update8<K, false>(t, raw, i0, left >= kVec ? kVec : (left > 0 ? (int)left : 0), hy, co, decay);
         }
       }
     }
@@ -286,9 +440,7 @@ static int check(const moe_adamw_tensor &t) {
 template <int K>
 static int launch(const uint8_t *dev, const Header *h, int64_t first, int64_t n, const Hyper &hy, moe_adamw_state *st,
                   bool bump, cudaStream_t s) {
-  int per_sm = 0;
-  MOE_TRY_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, adamw_kernel<K>, kThreads, 0));
-  int64_t grid = (int64_t)sm_count() * per_sm;
+  int64_t grid = (int64_t)sm_count() * per_sm(K);
   if (grid > n) grid = n;
   if (grid < 1) grid = 1;
   adamw_kernel<K><<<(int)grid, kThreads, 0, s>>>((const Tensor *)(dev + sizeof(Header)),
