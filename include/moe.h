@@ -399,7 +399,7 @@ int moe_adamw_step(const void *plan_host, const void *plan_device, double beta1,
  *           the order in which the tensor cores take them; places past R or K hold 0
  * A block's scale is 2^(floor(log2 max|x|) - 2), not below 2^-127 (byte b stands for 2^(b - 127)); codes are
  * x / scale rounded to nearest even, saturating at 6. A block that holds an infinity or a NaN gets the NaN scale
- * (255) and zero codes, and stands for NaNs. K must be a multiple of 32 (MOE_ERR_UNSUPPORTED otherwise).
+ * (255) and zero codes, and stands for NaNs. K must be a multiple of 32, at most 2^26 (MOE_ERR_UNSUPPORTED otherwise).
  */
 size_t moe_fp4_scale_bytes(int64_t R, int K);
 int moe_fp4_quantize(const void *x, int dtype, int64_t R, int K, void *codes, void *scales, moe_stream_t stream);
