@@ -4,24 +4,41 @@
 //   GATEUP  [a | b] = xq Wgu[e]^T, h = silu(a) b, written as MXFP4 (codes and scales)
 //   DOWN    y = hq Wd[e]^T, written as bf16
 //
-// One CTA computes 128 grouped rows (the MMA's M, one TMEM lane each) by 256 weight rows (N). For GATEUP
-// the 256 are 128 gate rows and the same features' 128 up rows, so a thread of the epilogue holds a and
-// b of one token for 128 features: it forms h, takes the largest magnitude of each 32 features in its own
-// registers, and writes 16 bytes of codes and one scale byte per block, with no exchange between threads.
+// A pair of CTAs computes 256 grouped rows (the MMA's M: 128 per CTA, one TMEM lane each) by 256 weight
+// rows (N), each CTA loading its own rows and half of the weights (cta_group::2). A single CTA with 128 x 256
+// tiles reads 51 KB from L2 for every 512 cycles of tensor work, more than an SM takes in; the pair needs 35 KB
+// per CTA. For GATEUP the 256 are 128 gate rows (one CTA's half) and the same features' 128 up rows (the
+// other's), so a thread of the epilogue holds a and b of one token for 128 features: it forms h, takes the
+// largest magnitude of each 32 features in its own registers, and writes 16 bytes of codes and one scale byte per
+// block, with no exchange between threads.
 //
-// Per 256 values of K (one ring stage: 16 KB of tokens, 32 KB of weights, 3 KB of scales): six tcgen05.cp
-// bring the scales into TMEM, four per 128 rows and 128 values as the MMA wants them (the scale layout in
-// memory is the one the copy reads), and four MMAs of K = 64 follow, each naming its pair of scale bytes
-// in its instruction descriptor.
+// Per 256 values of K (one ring stage per CTA: 16 KB of tokens, 16 KB of weights, 3 KB of scales): six
+// tcgen05.cp bring the scales into TMEM, four columns per 128 rows and 128 values as the MMA wants them (the
+// scale layout in memory is the one the copy reads; each CTA holds its own rows' scales and all 256 weight
+// rows'), and four MMAs of K = 64 follow, each naming its pair of scale bytes in its instruction descriptor.
 //
 // TMEM has 512 columns and two 256-column accumulators would leave none for scales. The two accumulators
 // overlap in 48 columns instead ([0, 256) and [208, 464), scales in [464, 512)): the epilogue reads the
 // shared columns first and then lets the next tile's MMAs start.
 //
-// Warp roles: warp 0 producer (TMA), warp 1 TMEM allocation and MMA issue, warps 2..9 epilogue (two warps
-// per 32-lane TMEM quarter). The grid is persistent, at most one CTA per SM; every wait is bounded (0.2 s),
-// on timeout the kernel records MOE_ERR_DEVICE_TIMEOUT in the workspace status word and leaves.
+// An expert with at most 128 rows left uses the first CTA's lanes only: the second CTA still brings its half
+// of the weights, which at such sizes are the traffic. Rows past the routed ones are not loaded where a box of
+// 32 rows can be spared; their lanes hold products of stale codes, which the epilogue replaces with zeros.
+//
+// Both kernels are launched as programmatic dependents, GATEUP of the permutation and DOWN of GATEUP (and the
+// combine after DOWN is one, too): a CTA sets up
+// and its producer brings the first tile's weights and their scales while the kernel before still runs, then
+// waits for that kernel before it touches the tokens or writes anything. The routing (offsets) and the weights
+// are older than the kernel before: of the kernels that let a successor start early, moe_permute_fp4's starts
+// after all that precedes it has ended, and GATEUP and DOWN end after what precedes them.
+//
+// Warp roles in both CTAs: warp 0 producer (TMA), warp 1 TMEM allocation and, in the leader, MMA issue,
+// warps 2..9 epilogue (two warps per 32-lane TMEM quarter). The grid is persistent, at most one CTA per SM; every
+// wait is bounded (0.2 s), on timeout the kernel records MOE_ERR_DEVICE_TIMEOUT in the workspace status word and
+// leaves.
 #include <cuda.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "fp4.cuh"
@@ -34,21 +51,28 @@ namespace fp4g {
 
 enum Kind { GATEUP = 0, DOWN = 1 };
 
-constexpr int MT = 128;                       // grouped rows per tile
-constexpr int NT = 256;                       // weight rows per tile
+constexpr int MT = 256;                       // grouped rows per tile, MC of them per CTA
+constexpr int MC = 128;
+constexpr int NT = 256;                       // weight rows per tile, half of them loaded by each CTA
 constexpr int KS = 256;                       // values of K per ring stage (128 bytes of codes: the swizzle span)
-constexpr int STAGES = 4;
-constexpr int A_BYTES = MT * 128, B_BYTES = NT * 128;
+constexpr int A_BYTES = MC * 128, B_BYTES = NT / 2 * 128;
 constexpr int SF_BYTES = (KS / 128) * 512;    // scales of 128 rows per stage
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 3 * SF_BYTES;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int BUF_BYTES = 2048;               // DOWN: one 32 x 32 block of y per epilogue warp
-constexpr int EPI_BYTES = EPI_WARPS * BUF_BYTES;
-constexpr int NBARS = 2 * STAGES + 3;
 constexpr int MAX_E = MOE_MAX_EXPERTS;
-constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 8 * NBARS + 16 + (MAX_E + 1) * 4;
-static_assert(SMEM <= 232448, "MXFP4 GEMM shared memory exceeds 227 KB");
+
+// GATEUP writes codes straight from registers and gives all shared memory to the ring. DOWN's tile of y (64 KB per
+// CTA) is staged whole, so the accumulator drains at once and the stores run behind the next tile's MMAs.
+template <int K> struct Cfg {
+  static constexpr int STAGES = K == GATEUP ? 6 : 4;
+  static constexpr int BUF_BYTES = 4096;                     // 32 rows x 64 columns of y, 128-byte swizzle
+  static constexpr int NBUF = K == GATEUP ? 0 : 2;           // per epilogue warp
+  static constexpr int EPI_BYTES = EPI_WARPS * NBUF * BUF_BYTES;
+  static constexpr int NBARS = 2 * STAGES + 3;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 8 * NBARS + 16 + (MAX_E + 1) * 4;
+  static_assert(SMEM <= 232448, "MXFP4 GEMM shared memory exceeds 227 KB");
+};
 static_assert(STAGE_BYTES % 1024 == 0, "ring stages keep the swizzle atoms' 1024-byte alignment");
 
 constexpr uint32_t ACC1 = 208;                // first column of the second accumulator
@@ -64,17 +88,16 @@ struct Params {
   int w_rows_e;           // weight rows per expert
   int w_second;           // rows from a tile's first 128 weight rows to its second (GATEUP: f, DOWN: 128)
   int w_step;             // weight rows from one feature tile to the next
-  const uint8_t *a_scales, *w_scales;
   uint8_t *h, *h_scales;  // GATEUP
   int f;
   int64_t rows_max;
 };
 
 struct Tile {
-  int e, ft, start, valid;   // expert, feature tile, first grouped row, routed rows (1..128)
+  int e, ft, start, valid;   // expert, feature tile, first grouped row, routed rows (1..256)
 };
 
-// One CTA's tiles in order: first, first + step, ...; tile = token tile gt * n_ft + feature tile.
+// One pair's tiles in order: first, first + step, ...; tile = token tile gt * n_ft + feature tile.
 struct Walker {
   int tile, step, num;
   int e;
@@ -87,14 +110,14 @@ struct Walker {
     const int i = gt - ttoff[e];
     const int c = p.offsets[e + 1] - p.offsets[e];
     t.e = e;
-    t.start = (p.tile_offsets[e] + i) * MT;
+    t.start = p.tile_offsets[e] * MC + i * MT;
     t.valid = min(MT, c - i * MT);
     tile += step;
     return true;
   }
 };
 
-// Instruction descriptor, kind::mxf4: A and B E2M1, scales E8M0, M = 128, N = 256, both K-major; sf = the
+// Instruction descriptor, kind::mxf4: A and B E2M1, scales E8M0, M = 256 (the pair), N = 256, both K-major; sf = the
 // first of the two scale bytes (0 or 2) of each operand.
 __device__ __forceinline__ uint32_t idesc(uint32_t sf) {
   return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NT >> 3) << 17) | (1u << 23) | ((uint32_t)(MT >> 4) << 24) |
@@ -105,60 +128,64 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t ad, uint64_t bd, u
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "l"(ad), "l"(bd), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate));
 }
-// 512 bytes of scales (32 rows of 16 bytes) to four TMEM columns, repeated in each 32-lane quarter.
+// 512 bytes of scales (32 rows of 16 bytes) to four TMEM columns, repeated in each 32-lane quarter; each CTA of
+// the pair from its own shared memory to its own TMEM.
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc));
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc));
 }
 // Shared-memory descriptor without swizzle: core matrices of 8 rows x 16 bytes, 128 bytes apart.
 __device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// Arrival (without release) on a barrier that may lie in the peer CTA. Announces that TMEM columns have been read:
+// tcgen05.wait::ld has completed the reads and no memory is handed over. A releasing arrival would first
+// wait for the warp's earlier global stores: 1300 to 3500 cycles in every tile here, with the tensor cores idle.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ void bulk_store(const CUtensorMap *map, int x, int y, uint32_t src) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(src)
-               : "memory");
-}
-
-// tmA, tmA32: the token codes in boxes of 128 and of 32 rows; tmB: the weight codes, 128 rows; tmC: y (DOWN).
+// tmA, tmA32: the token codes in boxes of 128 and of 32 rows; tmB: the weight codes, 128 rows; tmSA, tmSB: the
+// scales, one stage of 128 rows per box; tmC: y (DOWN), blocks of 32 rows x 64 columns.
 template <int K>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
-               const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmC, const Params p) {
+               const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmSA,
+               const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmC, const Params p) {
+  using C = Cfg<K>;
+  constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *epi_smem = smem + STAGES * STAGE_BYTES;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + EPI_BYTES);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + C::EPI_BYTES);
   // bars: full[STAGES], empty[STAGES], tfull, tdrain (the shared columns have been read), mma_done
-  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + NBARS);
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + C::NBARS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
   int *ttoff = reinterpret_cast<int *>(tmem_holder + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const bool leader = rank == 0;
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = smem_u32(bars);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };              // the leader's counts both CTAs' bytes
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   const uint32_t tfull_bar = bar0 + 8u * (2 * STAGES), tdrain_bar = tfull_bar + 8u, mma_done_bar = tfull_bar + 16u;
 
+  start_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(tfull_bar, 1);
-    mbar_init(tdrain_bar, EPI_WARPS);
+    mbar_init(tdrain_bar, 2 * EPI_WARPS);
     mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmSB)) : "memory");
   }
   if (warp == 0) {   // ttoff = exclusive scan of the token tiles per expert, ceil(rows / 128)
     int c[8], sum = 0;
@@ -184,73 +211,95 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 31) ttoff[p.E] = incl;
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                  "r"(512u)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();   // both CTAs: barriers initialised, ttoff written, TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const int num_tiles = ttoff[p.E] * p.n_ft;
-  const int64_t kt = (int64_t)p.num_kb * (KS / 128);   // 512-byte scale tiles along K
+  const int cluster_id = blockIdx.x >> 1, num_clusters = gridDim.x >> 1;
+  // routed rows of a tile among a CTA's 128, and the 32-row boxes that hold them (4: one box of 128)
+  auto rows_of = [](const Tile &t, int r) { return min(MC, max(0, t.valid - MC * r)); };
+  auto boxes_of = [](int rows) { return rows > MC / 2 ? 4 : (rows + 31) / 32; };
 
   if (warp == 0) {
-    // ------------------------------------------------------------------ producer
-    int stage = 0, fills = 0;
+    // ------------------------------------------------------------------ producer (both CTAs)
+    int stage = 0, fills = 0, early = 0;
     uint32_t phase = 0;
-    bool ok = true;
-    Walker walk(blockIdx.x, gridDim.x, num_tiles);
-    for (Tile t; ok && walk.next(t, p, ttoff);) {
-      // rows past the routed ones are not loaded when the tile is at most half full: their products land
-      // in TMEM lanes that the epilogue replaces with zeros
-      const int boxes = t.valid > MT / 2 ? 4 : (t.valid + 31) / 32;
+    bool ok = true, waited = false;
+    // one stage's weights and scales; the tokens and theirs
+    auto load_weights = [&](const Tile &t, int kb, int st) {
+      const uint32_t sB = sbase + st * STAGE_BYTES + A_BYTES, sS = sB + B_BYTES, fb = mapa_shared(full_bar(st), 0);
       const int w0 = t.e * p.w_rows_e + t.ft * p.w_step, w1 = w0 + p.w_second;
-      const uint8_t *sa = p.a_scales + (int64_t)(t.start / MT) * kt * 512;
-      const uint8_t *s0 = p.w_scales + (int64_t)(w0 / 128) * kt * 512, *s1 = p.w_scales + (int64_t)(w1 / 128) * kt * 512;
+      if (leader) {
+        const int b0 = boxes_of(rows_of(t, 0)), b1 = boxes_of(rows_of(t, 1));
+        mbar_expect_tx(full_bar(st), (uint32_t)(b0 + b1) * (A_BYTES / 4) + 2u * B_BYTES + (b1 ? 6u : 5u) * SF_BYTES);
+      }
+      tma_load_2d_pair(sB, &tmB, kb * 128, leader ? w0 : w1, fb);
+      tma_load_2d_pair(sS + SF_BYTES, &tmSB, kb * (SF_BYTES / 4), w0 / 128, fb);
+      tma_load_2d_pair(sS + 2 * SF_BYTES, &tmSB, kb * (SF_BYTES / 4), w1 / 128, fb);
+    };
+    auto load_tokens = [&](const Tile &t, int kb, int st) {
+      const uint32_t sA = sbase + st * STAGE_BYTES, fb = mapa_shared(full_bar(st), 0);
+      const int arow = t.start + MC * rank, boxes = boxes_of(rows_of(t, rank));
+      if (boxes == 4) {
+        tma_load_2d_pair(sA, &tmA, kb * 128, arow, fb);
+      } else {
+        for (int b = 0; b < boxes; ++b) tma_load_2d_pair(sA + b * (A_BYTES / 4), &tmA32, kb * 128, arow + 32 * b, fb);
+      }
+      if (boxes) tma_load_2d_pair(sA + A_BYTES + B_BYTES, &tmSA, kb * (SF_BYTES / 4), arow / 128, fb);
+    };
+    Walker walk(cluster_id, num_clusters, num_tiles);
+    for (Tile t; ok && walk.next(t, p, ttoff);) {
+      if (!waited) {   // the first tile: its stages' weights first, then wait for the kernel before
+        early = min(p.num_kb, STAGES);
+        if (elect_one())
+          for (int kb = 0; kb < early; ++kb) load_weights(t, kb, kb);
+        __syncwarp();
+        wait_previous();
+        waited = true;
+      }
       for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 41)) { ok = false; break; }
+        if (!mbar_spin_cluster(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 41)) { ok = false; break; }
         if (elect_one()) {
-          const uint32_t sA = sbase + stage * STAGE_BYTES, sB = sA + A_BYTES, sS = sB + B_BYTES, fb = full_bar(stage);
-          mbar_expect_tx(fb, (uint32_t)boxes * (A_BYTES / 4) + B_BYTES + 3 * SF_BYTES);
-          tma_load_2d(sB, &tmB, kb * 128, w0, fb);
-          tma_load_2d(sB + B_BYTES / 2, &tmB, kb * 128, w1, fb);
-          if (boxes == 4) {
-            tma_load_2d(sA, &tmA, kb * 128, t.start, fb);
-          } else {
-            for (int b = 0; b < boxes; ++b) tma_load_2d(sA + b * (A_BYTES / 4), &tmA32, kb * 128, t.start + 32 * b, fb);
-          }
-          bulk_load(sS, sa + (int64_t)kb * SF_BYTES, SF_BYTES, fb);
-          bulk_load(sS + SF_BYTES, s0 + (int64_t)kb * SF_BYTES, SF_BYTES, fb);
-          bulk_load(sS + 2 * SF_BYTES, s1 + (int64_t)kb * SF_BYTES, SF_BYTES, fb);
+          if (fills >= early) load_weights(t, kb, stage);
+          load_tokens(t, kb, stage);
         }
         __syncwarp();
         ++fills;
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
     }
-    if (*abort_flag) {   // leave no copy in flight: wait (bounded) for the last fill of every stage
+    if (!waited) wait_previous();
+    if (leader && *abort_flag) {
+      // leave no copy in flight: wait (bounded) for the last fill of every stage; the peer, whose bytes arrive on
+      // the same barriers, stays until the cluster meets below
       const uint64_t t0 = global_ns();
+      fills = max(fills, early);   // stages whose weights were asked for early never complete if they were not reached
       for (int i = 1; i <= STAGES && i <= fills; ++i) {
         const int f = fills - i;   // fill number f went to stage f % STAGES in ring round f / STAGES
         while (!mbar_try_wait(full_bar(f % STAGES), (uint32_t)(f / STAGES) & 1u) && global_ns() - t0 < kWaitLimitNs) {}
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
+  } else if (warp == 1 && leader) {
+    // ------------------------------------------------------------------ MMA issuer (leader only)
+    wait_previous();
     int stage = 0, n = 0, set = 0;
     uint32_t phase = 0;
     bool issued = false, ok = true;
     const uint64_t desc_a0 = sdesc(sbase, 16, 1024), desc_b0 = sdesc(sbase + A_BYTES, 16, 1024);
     const uint64_t desc_s0 = sf_desc(sbase + A_BYTES + B_BYTES);
-    Walker walk(blockIdx.x, gridDim.x, num_tiles);
+    Walker walk(cluster_id, num_clusters, num_tiles);
     for (Tile t; ok && walk.next(t, p, ttoff); ++n) {
-      if (n > 0 && !mbar_wait(tdrain_bar, (uint32_t)(n - 1) & 1u, abort_flag, p.hdr, 42)) break;
+      if (n > 0 && !mbar_spin_cluster(tdrain_bar, (uint32_t)(n - 1) & 1u, abort_flag, p.hdr, 42)) break;
       tc_fence_after();
       const uint32_t d = tmem_base + ((n & 1) ? ACC1 : 0u);
       for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (!mbar_wait(full_bar(stage), phase, abort_flag, p.hdr, 43)) { ok = false; break; }
+        if (!mbar_spin_cluster(full_bar(stage), phase, abort_flag, p.hdr, 43)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
           const uint32_t so = (uint32_t)(stage * STAGE_BYTES) >> 4;
@@ -267,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                        (kb | h | kk) != 0 ? 1u : 0u);
             }
           }
-          mma_commit(empty_bar(stage));
+          mma_commit_pair(empty_bar(stage), 0x3);   // frees the stage in both CTAs
         }
         __syncwarp();
         issued = true;
@@ -275,33 +324,39 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
       if (!ok) break;
-      if (elect_one()) mma_commit(tfull_bar);
+      if (elect_one()) mma_commit_pair(tfull_bar, 0x3);
       __syncwarp();
     }
     if (issued) {   // every MMA is done before TMEM is freed
-      if (elect_one()) mma_commit(mma_done_bar);
+      if (elect_one()) mma_commit_pair(mma_done_bar, 0x1);
       __syncwarp();
       const uint64_t t0 = global_ns();
       while (!mbar_try_wait(mma_done_bar, 0) && global_ns() - t0 < kWaitLimitNs) {}
     }
-  } else {
+  } else if (warp >= 2) {
     // ------------------------------------------------------------------ epilogue
+    wait_previous();
     const int quarter = warp & 3, hh = (warp - 2) >> 2;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t buf = smem_u32(epi_smem) + (uint32_t)(warp - 2) * BUF_BYTES;
+    const uint32_t buf = smem_u32(epi_smem) + (uint32_t)(warp - 2) * (C::NBUF * C::BUF_BYTES);
     int n = 0;
-    Walker walk(blockIdx.x, gridDim.x, num_tiles);
+    Walker walk(cluster_id, num_clusters, num_tiles);
     for (Tile t; walk.next(t, p, ttoff); ++n) {
-      if (!mbar_wait(tfull_bar, (uint32_t)n & 1u, abort_flag, p.hdr, 44)) break;
+      if (!mbar_spin_cluster(tfull_bar, (uint32_t)n & 1u, abort_flag, p.hdr, 44)) break;
       tc_fence_after();
       const bool second = n & 1;
       const uint32_t tacc = tmem_base + lane_off + (second ? ACC1 : 0u);
-      const int r_in = quarter * 32 + lane;                 // row within the tile
-      const bool real = r_in < t.valid;
+      const int r_in = quarter * 32 + lane;                 // row among this CTA's 128
+      const int valid = rows_of(t, rank), row0 = t.start + MC * rank;
+      if (valid == 0) {   // the second CTA of a tile of at most 128 rows: nothing to write, not even padding
+        if (lane == 0) arrive_relaxed(mapa_shared(tdrain_bar, 0));
+        continue;
+      }
+      const bool real = r_in < valid;
       // the columns shared with the other accumulator come first: the last 48 of the first
       // accumulator, the first 48 of the second
       if (K == GATEUP) {
-        const int64_t row = (int64_t)t.start + r_in;
+        const int64_t row = (int64_t)row0 + r_in;
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int b = second ? 2 * i + hh : 3 - 2 * i - hh;   // block of 32 features
@@ -312,23 +367,26 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (i == 0) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tdrain_bar);
+            if (lane == 0) arrive_relaxed(mapa_shared(tdrain_bar, 0));
           }
-          float hv[32];
-          uint32_t amax = 0;
+          float hv[32], top = 0.0f;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float a = __uint_as_float(ra[c]);
-            hv[c] = a * sigmoidf_(a) * __uint_as_float(rb[c]);
-            amax = max(amax, __float_as_uint(hv[c]) & 0x7fffffffu);
+          for (int c = 0; c < 32; c += 2) {
+            const float a0 = __uint_as_float(ra[c]), a1 = __uint_as_float(ra[c + 1]);
+            hv[c] = a0 * __uint_as_float(rb[c]) * sigmoidf_(a0);
+            hv[c + 1] = a1 * __uint_as_float(rb[c + 1]) * sigmoidf_(a1);
+            // largest magnitude; a NaN stays
+            asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(top) : "f"(hv[c]), "f"(hv[c + 1]), "f"(top));
           }
-          const uint32_t byte = real ? fp4::scale_byte(amax) : 0u;
-          const float inv = real ? fp4::inv_scale(byte) : 0.0f;
+          uint32_t byte = fp4::scale_byte(__float_as_uint(top) & 0x7fffffffu);
+          const float inv = fp4::inv_scale(byte);
           uint32_t q[4];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) hv[c] = inv == 0.0f ? 0.0f : hv[c] * inv;
+          for (int c = 0; c < 32; ++c) hv[c] *= inv;
 #pragma unroll
           for (int c = 0; c < 4; ++c) q[c] = fp4::pack_e2m1x8(hv + 8 * c);
+          if (!real || byte == 255u) q[0] = q[1] = q[2] = q[3] = 0u;
+          if (!real) byte = 0u;
           if (row < p.rows_max) {
             *reinterpret_cast<uint4 *>(p.h + row * (p.f / 2) + t.ft * 64 + 16 * b) = make_uint4(q[0], q[1], q[2], q[3]);
             p.h_scales[fp4::scale_word(row, t.ft, p.f / 128) + b] = (uint8_t)byte;
@@ -336,46 +394,52 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       } else {
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const int c8 = second ? 2 * i + hh : 7 - 2 * i - hh;   // block of 32 columns
-          uint32_t r[32];
-          tmem_ld32(tacc + 32u * c8, r);
+        for (int i = 0; i < 2; ++i) {
+          const int c4 = second ? 2 * i + hh : 3 - 2 * i - hh;   // block of 64 columns
+          uint32_t r[64];
+          tmem_ld32(tacc + 64u * c4, *reinterpret_cast<uint32_t(*)[32]>(r));
+          tmem_ld32(tacc + 64u * c4 + 32u, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
           tmem_ld_wait();
           if (i == 0) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tdrain_bar);
+            if (lane == 0) arrive_relaxed(mapa_shared(tdrain_bar, 0));
           }
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          const uint32_t block = buf + (uint32_t)i * C::BUF_BYTES;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the block's last store has read it
           __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 8; ++q) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               w[j] = real ? pack_bf16x2(__uint_as_float(r[8 * q + 2 * j]), __uint_as_float(r[8 * q + 2 * j + 1])) : 0u;
-            const uint32_t addr = buf + (uint32_t)lane * 64 + ((uint32_t)(q ^ ((lane >> 1) & 3)) << 4);
+            const uint32_t addr = block + (uint32_t)lane * 128 + ((uint32_t)(q ^ (lane & 7)) << 4);
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                          : "memory");
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            bulk_store(&tmC, t.ft * NT + 32 * c8, t.start + quarter * 32, buf);
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                             reinterpret_cast<uint64_t>(&tmC)),
+                         "r"(t.ft * NT + 64 * c4), "r"(row0 + quarter * 32), "r"(block)
+                         : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         }
       }
     }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (K == DOWN && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
   }
 
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();   // no CTA leaves while its peer may still signal its barriers or use its TMEM
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
   }
 }
 
@@ -392,15 +456,45 @@ static bool codes_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scales of [rows, K] (rows, K multiples of 128) as 32-bit words [rows / 128, K]: a box is the 1024 bytes of one stage.
+static bool scales_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t k) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {k, rows / 128};
+  cuuint64_t strides[1] = {k * 4};
+  cuuint32_t box[2] = {SF_BYTES / 4, 1};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+  CUtensorMap a, a32, b, sa, sb, c;
+};
+
+// The kernel's dynamic shared memory limit, raised once per device (the call costs a host microsecond).
+template <int K> static bool smem_allowed() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return true;
+  if (cudaFuncSetAttribute(fp4_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<K>::SMEM) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  if (dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  return true;
+}
+
 template <int K>
-static int launch(const CUtensorMap &a, const CUtensorMap &a32, const CUtensorMap &b, const CUtensorMap &c,
-                  const Params &p, cudaStream_t s) {
-  MOE_TRY_CUDA(cudaFuncSetAttribute(fp4_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
-  int64_t grid = sm_count();
-  const int64_t most = p.rows_max / MT * p.n_ft;   // tiles there can be
-  if (most < grid) grid = most;
-  fp4_kernel<K><<<(int)grid, THREADS, SMEM, s>>>(a, a32, b, c, p);
-  MOE_CHECK_LAUNCH();
+static int launch(const Maps &m, const Params &p, cudaStream_t s) {
+  if (!smem_allowed<K>()) return MOE_ERR_CUDA;
+  int64_t clusters = sm_count() / 2;
+  const int64_t most = p.rows_max / MC * p.n_ft;   // tiles there can be
+  if (most < clusters) clusters = most;
+  MOE_TRY_CUDA(launch_after(fp4_kernel<K>, dim3((unsigned)(2 * clusters)), dim3(THREADS), Cfg<K>::SMEM, s, m.a, m.a32,
+                            m.b, m.sa, m.sb, m.c, p));
   return MOE_OK;
 }
 
@@ -430,7 +524,7 @@ extern "C" int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales
     if (!q || !aligned16(q)) return MOE_ERR_INVALID_ARG;
   if (!tile_offsets || !offsets) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
-  CUtensorMap a, a32, b, c;
+  Maps m{};
   Params p{};
   p.tile_offsets = tile_offsets;
   p.offsets = offsets;
@@ -439,30 +533,29 @@ extern "C" int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales
   p.rows_max = rows_max;
   p.f = f;
 
-  if (!codes_map(&a, x_codes, rows_max, d / 2, MT) || !codes_map(&a32, x_codes, rows_max, d / 2, 32) ||
-      !codes_map(&b, wgu_codes, (uint64_t)E * 2 * f, d / 2, 128))
+  if (!codes_map(&m.a, x_codes, rows_max, d / 2, MC) || !codes_map(&m.a32, x_codes, rows_max, d / 2, 32) ||
+      !codes_map(&m.b, wgu_codes, (uint64_t)E * 2 * f, d / 2, 128) || !scales_map(&m.sa, x_scales, rows_max, d) ||
+      !scales_map(&m.sb, wgu_scales, (uint64_t)E * 2 * f, d))
     return MOE_ERR_CUDA;
+  m.c = m.b;   // not used
   p.n_ft = f / 128;
   p.num_kb = d / KS;
   p.w_rows_e = 2 * f;
   p.w_second = f;
   p.w_step = 128;
-  p.a_scales = (const uint8_t *)x_scales;
-  p.w_scales = (const uint8_t *)wgu_scales;
   p.h = (uint8_t *)h_codes;
   p.h_scales = (uint8_t *)h_scales;
-  int rc = launch<GATEUP>(a, a32, b, b, p, s);   // tmC is not used
+  int rc = launch<GATEUP>(m, p, s);
   if (rc) return rc;
 
-  if (!codes_map(&a, h_codes, rows_max, f / 2, MT) || !codes_map(&a32, h_codes, rows_max, f / 2, 32) ||
-      !codes_map(&b, wd_codes, (uint64_t)E * d, f / 2, 128) || !tc::make_store_map(&c, y_perm, rows_max, d))
+  if (!codes_map(&m.a, h_codes, rows_max, f / 2, MC) || !codes_map(&m.a32, h_codes, rows_max, f / 2, 32) ||
+      !codes_map(&m.b, wd_codes, (uint64_t)E * d, f / 2, 128) || !scales_map(&m.sa, h_scales, rows_max, f) ||
+      !scales_map(&m.sb, wd_scales, (uint64_t)E * d, f) || !tc::make_map(&m.c, y_perm, rows_max, d, 32))
     return MOE_ERR_CUDA;
   p.n_ft = d / NT;
   p.num_kb = f / KS;
   p.w_rows_e = d;
   p.w_second = 128;
   p.w_step = NT;
-  p.a_scales = (const uint8_t *)h_scales;
-  p.w_scales = (const uint8_t *)wd_scales;
-  return launch<DOWN>(a, a32, b, c, p, s);
+  return launch<DOWN>(m, p, s);
 }

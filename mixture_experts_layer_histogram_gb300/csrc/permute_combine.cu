@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const uint4 *__res
                                                               const int32_t *__restrict__ row_of_slot, int64_t Tn,
                                                               int64_t row_vecs, int k, int64_t rows_max,
                                                               uint4 *__restrict__ out) {
+  wait_previous();
   constexpr int N = Elem<T>::N;
   const int lane = threadIdx.x & 31;
   const int64_t nw = (int64_t)gridDim.x * (kRowThreads / 32);
@@ -267,7 +268,9 @@ extern "C" int moe_combine_fwd(const void *y_perm, const float *topk_w, const in
   cudaStream_t s = (cudaStream_t)stream;
   const uint4 *y = (const uint4 *)y_perm;
   uint4 *o = (uint4 *)out;
-#define MOE_COMBINE(TYPE, W, KM) combine_kernel<TYPE, W, KM><<<nb, kRowThreads, 0, s>>>(y, topk_w, row_of_slot, T, rv, k, rows_max, o)
+#define MOE_COMBINE(TYPE, W, KM)                                                                                   \
+  MOE_TRY_CUDA(launch_after(combine_kernel<TYPE, W, KM>, dim3(nb), dim3(kRowThreads), 0, s, y, topk_w, row_of_slot, \
+                            (int64_t)T, rv, k, rows_max, o))
 #define MOE_COMBINE_K(TYPE, W)                     \
   do {                                             \
     if (k <= 2) MOE_COMBINE(TYPE, W, 2);           \
