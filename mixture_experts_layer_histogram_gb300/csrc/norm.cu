@@ -11,8 +11,18 @@
 // and one reduction of six sums serves the whole row (its rounding error is of the order of the one
 // that the subtraction in G makes).
 //
-// One thread block per row, the row in registers (read once, written once); HBM-bound. The weight
-// gradients are summed over a block's rows in registers, written as one fp32 partial row per block and
+// HBM-bound: a thread block works on one row at a time, every row is read once and written once. Rows come
+// through a ring of up to three stages in shared memory, filled by cp.async: the copies of the next rows are in
+// flight while a row is reduced, whatever the registers hold. Where a row is a multiple of 16 bytes each
+// thread copies and reads its own vectors, so no barrier stands between copy and use. Other rows are copied as the
+// 16-byte windows that cover them (aligned, whole sectors) and read one element per lane after a barrier.
+// Measured (bf16, channel gate, next norm): forward at T = 8192, d = 2048 25.1 us (134 MB, 5.4 TB/s), backward at
+// T = 16384, d = 4096 132 us (805 MB, 6.1 TB/s); fp32 rows of 1537 with a token gate, T = 8192, 81 us (403 MB, 5.0 TB/s).
+// Before: rows in registers without the ring and one fp32 per instruction took 34 and 288 us, the ring alone 31 and
+// 278 us; the instructions were the bound, which pairs of fp32, shared addresses formed once per row and weights
+// kept in registers took off.
+//
+// The weight gradients are summed over a block's rows in registers, written as one fp32 partial row per block and
 // added up by a second kernel in a fixed order, so they do not depend on timing. With a gate per
 // channel, dw_post and d_gate are both multiples of A = sum_t G y r, so one accumulator serves both.
 #include "common.cuh"
@@ -21,74 +31,250 @@ namespace moe {
 namespace norm {
 
 constexpr int kMaxThreads = 512;
-constexpr int kSums = 8;   // floats per warp in the reduction buffer
+constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kStages = 3;                    // at most; fewer where long rows leave no room
+constexpr size_t kRingMost = 200 * 1024;
 
-// VEC elements of type T as they lie in memory: a 16-byte vector, or one element for rows whose
-// length is no multiple of 16 bytes.
-template <typename T, int VEC> struct Pack;
-template <> struct Pack<float, 4> {
+// Arithmetic on one lane of values: two fp32 at a time (f32x2 instructions) for rows of 16-byte vectors, one fp32,
+// or one fp64. At bf16 the instructions, not HBM, bound these kernels when each value takes its own.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+template <typename S> __device__ __forceinline__ S mul(S a, S b) { return a * b; }
+template <typename S> __device__ __forceinline__ S add(S a, S b) { return a + b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ double fma(double a, double b, double c) { return ::fma(a, b, c); }
+template <typename L> __device__ __forceinline__ L splat(float v);
+template <> __device__ __forceinline__ F2 splat<F2>(float v) { return pair(v, v); }
+template <> __device__ __forceinline__ float splat<float>(float v) { return v; }
+template <> __device__ __forceinline__ double splat<double>(float v) { return v; }
+__device__ __forceinline__ F2 all(float v, F2) { return pair(v, v); }
+__device__ __forceinline__ float all(float v, float) { return v; }
+__device__ __forceinline__ double all(double v, double) { return v; }
+__device__ __forceinline__ float total(F2 a) {
+  float x, y;
+  split(a, x, y);
+  return x + y;
+}
+__device__ __forceinline__ float total(float a) { return a; }
+__device__ __forceinline__ double total(double a) { return a; }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 q;
-  __device__ __forceinline__ void load(const float *p) { q = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ void load_once(const float *p) { q = ld_stream(reinterpret_cast<const uint4 *>(p)); }
-  __device__ __forceinline__ void unpack(float *v) const {
-    v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y); v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(a) : "memory");
+  return q;
+}
+
+// How VEC elements of type T are held: N lanes of type L.
+template <typename T, int VEC, typename S> struct Lanes;
+template <> struct Lanes<__nv_bfloat16, 8, float> {
+  typedef F2 L;
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void load(const void *p, L *v) {
+    unpack(*reinterpret_cast<const uint4 *>(p), v);
   }
-  static __device__ __forceinline__ void store(float *p, const float *v) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  static __device__ __forceinline__ void load_shared(uint32_t a, L *v) { unpack(lds128(a), v); }
+  static __device__ __forceinline__ void unpack(const uint4 &q, L *v) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const L *v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x, y;
+      split(v[i], x, y);
+      w[i] = pack_bf16x2(x, y);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
-template <> struct Pack<__nv_bfloat16, 8> {
-  uint4 q;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { q = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ void load_once(const __nv_bfloat16 *p) { q = ld_stream(reinterpret_cast<const uint4 *>(p)); }
-  __device__ __forceinline__ void unpack(float *v) const { unpack_bf16x8(q, v); }
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) {
-    *reinterpret_cast<uint4 *>(p) = pack_bf16x8(v);
+template <> struct Lanes<float, 4, float> {
+  typedef F2 L;
+  static constexpr int N = 2;
+  static __device__ __forceinline__ void load(const void *p, L *v) {
+    const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(p);
+    v[0].v = q.x;
+    v[1].v = q.y;
+  }
+  static __device__ __forceinline__ void load_shared(uint32_t a, L *v) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0].v), "=l"(v[1].v) : "r"(a) : "memory");
+  }
+  static __device__ __forceinline__ void store(float *p, const L *v) {
+    *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(v[0].v, v[1].v);
   }
 };
-template <> struct Pack<float, 1> {
-  float q;
-  __device__ __forceinline__ void load(const float *p) { q = *p; }
-  __device__ __forceinline__ void load_once(const float *p) { q = *p; }
-  __device__ __forceinline__ void unpack(float *v) const { v[0] = q; }
-  static __device__ __forceinline__ void store(float *p, const float *v) { *p = v[0]; }
+template <typename S> struct Lanes<float, 1, S> {
+  typedef S L;
+  static constexpr int N = 1;
+  static __device__ __forceinline__ void load(const void *p, L *v) { v[0] = *reinterpret_cast<const float *>(p); }
+  static __device__ __forceinline__ void load_shared(uint32_t a, L *v) {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a) : "memory");
+    v[0] = f;
+  }
+  static __device__ __forceinline__ void store(float *p, const L *v) { *p = (float)v[0]; }
 };
-template <> struct Pack<__nv_bfloat16, 1> {
-  __nv_bfloat16 q;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { q = *p; }
-  __device__ __forceinline__ void load_once(const __nv_bfloat16 *p) { q = *p; }
-  __device__ __forceinline__ void unpack(float *v) const { v[0] = __bfloat162float(q); }
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) { *p = __float2bfloat16_rn(v[0]); }
+template <typename S> struct Lanes<__nv_bfloat16, 1, S> {
+  typedef S L;
+  static constexpr int N = 1;
+  static __device__ __forceinline__ void load(const void *p, L *v) {
+    v[0] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p));
+  }
+  static __device__ __forceinline__ void load_shared(uint32_t a, L *v) {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+    v[0] = __uint_as_float((uint32_t)h << 16);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const L *v) { *p = __float2bfloat16_rn((float)v[0]); }
 };
 
-// Sums of N values over the block, the same on every thread. `buf` alternates between two halves, so
-// one barrier per reduction is enough: a half is written again only after the next reduction's barrier.
-template <int N, typename S>
-__device__ __forceinline__ void block_sum(S (&v)[N], float *buf, int &half) {
+// Geometry of the ring of rows. A stage holds the row buffers of the kernel's tensors, `row_bytes` each. VEC > 1: the
+// vector v of a row lies at 16 v of its buffer, where the thread that uses it has copied it to. VEC == 1: the buffer
+// holds the 16-byte windows that cover the row, whose first element is then `shift` elements into the first.
+struct Geometry {
+  uint32_t row_bytes, stage_bytes;
+  int stages;
+};
+// One thread's view of it. ITER: vectors (elements) per thread, blockDim apart.
+template <typename T, int VEC, int ITER> struct Ring {
+  uint32_t mine;           // shared address of this thread's first vector (VEC == 1: of the ring)
+  uint32_t row_bytes, stage_bytes, step;
+  int stages, d, nvec;
+  int64_t all;             // bytes of one tensor
+
+  __device__ __forceinline__ Ring(const uint8_t *smem, const Geometry &g, int64_t rows, int d_)
+      : row_bytes(g.row_bytes), stage_bytes(g.stage_bytes), stages(g.stages), d(d_), nvec(d_ / VEC) {
+    mine = (uint32_t)__cvta_generic_to_shared(smem) + (VEC > 1 ? 16u * threadIdx.x : 0u);
+    step = VEC > 1 ? 16u * blockDim.x : (uint32_t)sizeof(T) * blockDim.x;
+    all = rows * d * (int64_t)sizeof(T);
+  }
+  // Whether this thread's i-th vector exists
+  __device__ __forceinline__ bool has(int i) const { return (int)(threadIdx.x + i * blockDim.x) < nvec; }
+  // Byte offset of `row` in a tensor, with the thread's first vector where threads copy their own
+  __device__ __forceinline__ int64_t offset(int64_t row) const {
+    return row * d * (int64_t)sizeof(T) + (VEC > 1 ? 16u * threadIdx.x : 0u);
+  }
+  // Copy (asynchronously) the row at `off` (offset()) of one tensor into buffer `slot` of `stage`.
+  __device__ __forceinline__ void fetch(const void *base, int64_t off, int stage, int slot) const {
+    const uint32_t dst = mine + (uint32_t)stage * stage_bytes + (uint32_t)slot * row_bytes;
+    const uint8_t *src = (const uint8_t *)base + off;
+    if (VEC > 1) {
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        if (has(i))
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * step), "l"(src + i * step) : "memory");
+      }
+    } else {
+      const int lead = (int)(off & 15), bytes = lead + d * (int)sizeof(T);
+      const int64_t left = all - (off - lead);            // up to the tensor's end
+      for (int c = 16 * threadIdx.x; c < bytes; c += 16 * blockDim.x) {
+        const int n = left - c < 16 ? (int)(left - c) : 16;   // nothing past the tensor is read
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + c), "l"(src - lead + c), "r"(n) : "memory");
+      }
+    }
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // The oldest row's copies have landed (and are visible to all threads that read them); with three stages the
+  // next row's may be in flight.
+  __device__ __forceinline__ void wait() const {
+    if (stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (VEC == 1) __syncthreads();
+  }
+  // Shared address of this thread's first vector (element) of the row at `off` in `stage`; buffers are row_bytes
+  // apart, the thread's vectors `step`.
+  __device__ __forceinline__ uint32_t at(int stage, int64_t off) const {
+    return mine + (uint32_t)stage * stage_bytes +
+           (VEC > 1 ? 0u : ((uint32_t)(off & 15) + (uint32_t)sizeof(T) * threadIdx.x));
+  }
+  // The stage whose row was the last one before `stage`'s: free once every thread has left that row.
+  __device__ __forceinline__ int freed(int stage) const { return stage >= 1 ? stage - 1 : stages - 1; }
+};
+
+// Sums over the block, the same on every thread. `buf` alternates between two halves, so one barrier per
+// reduction is enough: a half is written again only after the next reduction's barrier.
+struct SumBuf {
+  float v[2][8][kMaxWarps];
+};
+__device__ __forceinline__ void clear(SumBuf &buf) {   // the places of warps that the block does not have stay 0
+  for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps; i += blockDim.x) (&buf.v[0][0][0])[i] = 0.0f;
+  __syncthreads();
+}
+__device__ __forceinline__ float block_sum(float v, SumBuf &buf, int &half) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if (blockDim.x == 32) return v;
+  float *b = buf.v[half][0];
+  half ^= 1;
+  if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMaxWarps / 4; ++i) {
+    if (i * 128 >= (int)blockDim.x) break;
+    const float4 q = reinterpret_cast<const float4 *>(b)[i];
+    v += (q.x + q.y) + (q.z + q.w);
+  }
+  return v;
+}
+// Six sums. In the warp, each exchange halves the values a lane carries (9 exchanges, not 30): lane 4 i ends with value i.
+__device__ __forceinline__ void block_sum6(float (&s)[6], SumBuf &buf, int &half) {
+  const int lane = threadIdx.x & 31;
+  float v[8] = {s[0], s[1], s[2], s[3], s[4], s[5], 0.0f, 0.0f};
+#pragma unroll
+  for (int n = 4, off = 16; n >= 1; n >>= 1, off >>= 1) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+    }
+  }
+  float r = v[0];
+  r += __shfl_xor_sync(0xffffffffu, r, 2);
+  r += __shfl_xor_sync(0xffffffffu, r, 1);
+  if (blockDim.x > 32) {
+    float(*b)[kMaxWarps] = buf.v[half];
+    half ^= 1;
+    if ((lane & 3) == 0) b[lane >> 2][threadIdx.x >> 5] = r;
+    __syncthreads();
+    const float4 q = *reinterpret_cast<const float4 *>(&b[lane >> 2][4 * (lane & 3)]);
+    r = (q.x + q.y) + (q.z + q.w);
+    r += __shfl_xor_sync(0xffffffffu, r, 1);
+    r += __shfl_xor_sync(0xffffffffu, r, 2);
+  }
+#pragma unroll
+  for (int i = 0; i < 6; ++i) s[i] = __shfl_sync(0xffffffffu, r, 4 * i);
+}
+__device__ __forceinline__ void block_sum6(double (&s)[6], SumBuf &, int &) {   // rows of at most 32 values: one warp
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+    for (int i = 0; i < 6; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
   }
-  const int nw = blockDim.x >> 5;
-  if (nw == 1) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float *b = buf + half * (kMaxThreads / 32) * kSums;
-  half ^= 1;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) b[warp * kSums + i] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < nw ? b[lane * kSums + i] : 0.0f;
-#pragma unroll
-  for (int off = kMaxThreads / 64; off > 0; off >>= 1) {   // nw <= 16: lanes 0..15 hold the warps' sums
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
 }
 
 struct FwdParams {
@@ -99,89 +285,129 @@ struct FwdParams {
   float res_scale, eps;
 };
 
-// BLOCK: the residual form (out from y, x); without it x itself is normed. NEXT: n is written.
+// BLOCK: the residual form (out from y, x); without it x itself is normed. NEXT: n is written. With few vectors
+// per thread the weights stay in registers from row to row.
 template <typename T, int VEC, int ITER, bool BLOCK, bool NEXT>
-__global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const FwdParams p) {
-  using P = Pack<T, VEC>;
-  __shared__ float buf[2 * (kMaxThreads / 32) * kSums];
+__global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) norm_fwd_kernel(const FwdParams p, const Geometry geom) {
+  using V = Lanes<T, VEC, float>;
+  using L = typename V::L;
+  constexpr int N = V::N;
+  constexpr bool kHold = ITER * VEC <= 16 && ITER <= 4;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ SumBuf sums;
+  const Ring<T, VEC, ITER> ring(dyn, geom, p.T, p.d);
   int half = 0;
-  const int nvec = p.d / VEC;
   const float inv_d = 1.0f / (float)p.d;
+  const bool token = BLOCK && p.gate_kind == MOE_GATE_TOKEN, channel = BLOCK && p.gate_kind == MOE_GATE_CHANNEL;
+  clear(sums);
+  auto fetch = [&](int64_t row, int stage) {   // x, y, gate
+    if (row < p.T) {
+      const int64_t off = ring.offset(row);
+      ring.fetch(p.x, off, stage, 0);
+      if (BLOCK) ring.fetch(p.y, off, stage, 1);
+      if (token) ring.fetch(p.gate, off, stage, 2);
+    }
+    ring.commit();
+  };
+  for (int s = 0; s < ring.stages - 1; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  // w_post (times the channel gate) and w_next of vector v
+  auto weights = [&](int v, L *wg, L *wn) {
+    if (BLOCK) {
+      V::load((const T *)p.w_post + (int64_t)v * VEC, wg);
+      if (channel) {
+        L g[N];
+        V::load((const T *)p.gate + (int64_t)v * VEC, g);
+#pragma unroll
+        for (int c = 0; c < N; ++c) wg[c] = mul(wg[c], g[c]);
+      }
+    }
+    if (NEXT) V::load((const T *)p.w_next + (int64_t)v * VEC, wn);
+  };
+  L hold_g[kHold ? ITER : 1][N], hold_n[kHold ? ITER : 1][N];
+  if (kHold) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i)
+      if (ring.has(i)) weights(threadIdx.x + i * blockDim.x, hold_g[kHold ? i : 0], hold_n[kHold ? i : 0]);
+  }
+  const L scale = splat<L>(p.res_scale);
+  int stage = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-    const int64_t base = row * p.d;
-    P px[ITER], py[ITER];
+    if (ring.stages == 1) {
+      if (VEC == 1) __syncthreads();   // every thread has left the row before
+      fetch(row, 0);
+    }
+    ring.wait();
+    const int64_t off = ring.offset(row);
+    const uint32_t here = ring.at(stage, off);
+    auto place = [&](void *out, int i) {   // of this thread's i-th vector in an output
+      return reinterpret_cast<T *>((uint8_t *)out + off + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step);
+    };
+    L o[ITER][N];
+    float r = 0.0f;
+    if (BLOCK) {
+      L s = splat<L>(0.0f);
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        if (!ring.has(i)) continue;
+        V::load_shared(here + ring.row_bytes + i * ring.step, o[i]);
+#pragma unroll
+        for (int c = 0; c < N; ++c) s = fma(o[i][c], o[i][c], s);
+      }
+      r = rsqrtf(block_sum(total(s), sums, half) * inv_d + p.eps);
+    }
+    L s = splat<L>(0.0f), rr = splat<L>(r);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
+      if (!ring.has(i)) continue;
       const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nvec) continue;
-      px[i].load_once((const T *)p.x + base + (int64_t)v * VEC);
-      if (BLOCK) py[i].load_once((const T *)p.y + base + (int64_t)v * VEC);
-    }
-    float o[ITER][VEC];
-    if (BLOCK) {
-      float s[1] = {0.0f};
+      L x[N];
+      V::load_shared(here + i * ring.step, x);
+      if (BLOCK) {
+        L(&wg)[N] = hold_g[kHold ? i : 0];
+        if (!kHold) weights(v, wg, hold_n[0]);
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v >= nvec) continue;
-        float t[VEC];
-        py[i].unpack(t);
+        for (int c = 0; c < N; ++c) o[i][c] = mul(mul(o[i][c], rr), wg[c]);
+        if (token) {
+          L g[N];
+          V::load_shared(here + 2 * ring.row_bytes + i * ring.step, g);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) s[0] = fmaf(t[c], t[c], s[0]);
-      }
-      block_sum(s, buf, half);
-      const float r = 1.0f / sqrtf(s[0] * inv_d + p.eps);
-#pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v >= nvec) continue;
-        float ty[VEC], tx[VEC], tw[VEC], tg[VEC];
-        P pw, pg;
-        pw.load((const T *)p.w_post + (int64_t)v * VEC);
-        pw.unpack(tw);
-        if (p.gate_kind != MOE_GATE_NONE) {
-          pg.load((const T *)p.gate + (p.gate_kind == MOE_GATE_TOKEN ? base : 0) + (int64_t)v * VEC);
-          pg.unpack(tg);
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) tw[c] *= tg[c];
+          for (int c = 0; c < N; ++c) o[i][c] = mul(o[i][c], g[c]);
         }
-        py[i].unpack(ty);
-        px[i].unpack(tx);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) o[i][c] = fmaf(p.res_scale, tx[c], ty[c] * r * tw[c]);
-        P::store((T *)p.out + base + (int64_t)v * VEC, o[i]);
+        for (int c = 0; c < N; ++c) o[i][c] = fma(scale, x[c], o[i][c]);
+        V::store(place(p.out, i), o[i]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < N; ++c) o[i][c] = x[c];
       }
-    } else {
+      if (NEXT) {
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        if ((int)(threadIdx.x + i * blockDim.x) < nvec) px[i].unpack(o[i]);
+        for (int c = 0; c < N; ++c) s = fma(o[i][c], o[i][c], s);
       }
     }
+    // the row is in registers: its stage's successor may be overwritten (windows: the barrier of wait() has
+    // passed, so every thread has left that row)
+    if (ring.stages > 1) fetch(row + (int64_t)(ring.stages - 1) * gridDim.x, ring.freed(stage));
     if (NEXT) {   // from the unrounded stream: n is rounded once
-      float s[1] = {0.0f};
+      rr = splat<L>(rsqrtf(block_sum(total(s), sums, half) * inv_d + p.eps));
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
-        if ((int)(threadIdx.x + i * blockDim.x) >= nvec) continue;
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) s[0] = fmaf(o[i][c], o[i][c], s[0]);
-      }
-      block_sum(s, buf, half);
-      const float r = 1.0f / sqrtf(s[0] * inv_d + p.eps);
-#pragma unroll
-      for (int i = 0; i < ITER; ++i) {
+        if (!ring.has(i)) continue;
         const int v = threadIdx.x + i * blockDim.x;
-        if (v >= nvec) continue;
-        float tw[VEC], t[VEC];
-        P pw;
-        pw.load((const T *)p.w_next + (int64_t)v * VEC);
-        pw.unpack(tw);
+        L(&wn)[N] = hold_n[kHold ? i : 0];
+        if (!kHold) V::load((const T *)p.w_next + (int64_t)v * VEC, wn);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) t[c] = o[i][c] * r * tw[c];
-        P::store((T *)p.n + base + (int64_t)v * VEC, t);
+        for (int c = 0; c < N; ++c) o[i][c] = mul(mul(o[i][c], rr), wn[c]);
+        V::store(place(p.n, i), o[i]);
       }
     }
+    if (++stage == ring.stages) stage = 0;
   }
 }
+
+// Blocks of kMaxThreads that the backward's registers leave room for: the accumulators and weights of a 16-byte
+// vector per thread take over 64, four single elements do not.
+constexpr int bwd_per_sm(int vec, int iter) { return vec == 1 && iter <= 4 ? 2 : 1; }
 
 struct BwdParams {
   const void *dout, *dn, *out, *y, *w_post, *gate, *w_next;   // dout may be null (zero)
@@ -192,140 +418,205 @@ struct BwdParams {
   float res_scale, eps;
 };
 
+template <int N> __device__ __forceinline__ void put_part(float *p, const F2 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) *reinterpret_cast<ulonglong2 *>(p + 2 * i) = make_ulonglong2(v[i].v, v[i + 1].v);
+}
+__device__ __forceinline__ void put_part(float *p, const float (&v)[1]) { *p = v[0]; }
+__device__ __forceinline__ void put_part(float *p, const double (&v)[1]) { *p = (float)v[0]; }
+__device__ __forceinline__ float inv_root(float v) { return rsqrtf(v); }
+__device__ __forceinline__ double inv_root(double v) { return 1.0 / sqrt(v); }
+
 // BLOCK: the residual form; without it the backward of one norm (out = its input, w_next its weights).
 // S: the type of the sums and of the differences u - v r^2 mean(u v). In a row of few values the two terms
 // can all but cancel (in a row of one value what is left is u eps r^2), so rows of at most 32 values are
 // computed in 64 bits; a warp holds such a row at one value per lane.
 template <typename T, int VEC, int ITER, bool BLOCK, bool NEXT, typename S>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdParams p) {
-  using P = Pack<T, VEC>;
-  __shared__ float buf[2 * (kMaxThreads / 32) * kSums];
+__global__ void __launch_bounds__(kMaxThreads, bwd_per_sm(VEC, ITER)) norm_bwd_kernel(const BwdParams p, const Geometry geom) {
+  using V = Lanes<T, VEC, S>;
+  using L = typename V::L;
+  constexpr int N = V::N;
+  constexpr bool kHold = ITER * VEC <= 16 && ITER <= 4;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ SumBuf sums;
+  const Ring<T, VEC, ITER> ring(dyn, geom, p.T, p.d);
   int half = 0;
-  const int nvec = p.d / VEC;
   const S inv_d = S(1) / (S)p.d;
-  float acc_n[ITER][VEC], acc_p[ITER][VEC];
+  const bool has_d = p.dout != nullptr;
+  const bool token = BLOCK && p.gate_kind == MOE_GATE_TOKEN, channel = BLOCK && p.gate_kind == MOE_GATE_CHANNEL;
+  // buffers of a stage: dn, out, y, then dout and gate where they are
+  constexpr int kDn = 0, kOut = NEXT ? 1 : 0, kY = NEXT ? 2 : 0, kFixed = (NEXT ? 2 : 0) + (BLOCK ? 1 : 0);
+  const int at_d = kFixed, at_g = kFixed + (has_d ? 1 : 0);
+  clear(sums);
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.T) {
+      const int64_t off = ring.offset(row);
+      if (NEXT) {
+        ring.fetch(p.dn, off, stage, kDn);
+        ring.fetch(p.out, off, stage, kOut);
+      }
+      if (BLOCK) ring.fetch(p.y, off, stage, kY);
+      if (has_d) ring.fetch(p.dout, off, stage, at_d);
+      if (token) ring.fetch(p.gate, off, stage, at_g);
+    }
+    ring.commit();
+  };
+  L acc_n[ITER][N], acc_p[ITER][N];
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) acc_n[i][c] = acc_p[i][c] = 0.0f;
+    for (int c = 0; c < N; ++c) acc_n[i][c] = acc_p[i][c] = splat<L>(0.0f);
   }
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-    const int64_t base = row * p.d;
-    P pd[ITER], pn[ITER], po[ITER], py[ITER], pg[ITER];
+  for (int s = 0; s < ring.stages - 1; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  // w_post (times the channel gate) and w_next of vector v
+  auto weights = [&](int v, L *wg, L *wn) {
+    if (BLOCK) {
+      V::load((const T *)p.w_post + (int64_t)v * VEC, wg);
+      if (channel) {
+        L g[N];
+        V::load((const T *)p.gate + (int64_t)v * VEC, g);
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nvec) continue;
-      const int64_t at = base + (int64_t)v * VEC;
-      if (p.dout) pd[i].load_once((const T *)p.dout + at);
-      if (NEXT) {
-        pn[i].load_once((const T *)p.dn + at);
-        po[i].load_once((const T *)p.out + at);
-      }
-      if (BLOCK) {
-        py[i].load_once((const T *)p.y + at);
-        if (p.gate_kind == MOE_GATE_TOKEN) pg[i].load_once((const T *)p.gate + at);
-        else if (p.gate_kind == MOE_GATE_CHANNEL) pg[i].load((const T *)p.gate + (int64_t)v * VEC);
+        for (int c = 0; c < N; ++c) wg[c] = mul(wg[c], g[c]);
       }
     }
+    if (NEXT) V::load((const T *)p.w_next + (int64_t)v * VEC, wn);
+  };
+  L hold_g[kHold ? ITER : 1][N], hold_n[kHold ? ITER : 1][N];
+  if (kHold) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i)
+      if (ring.has(i)) weights(threadIdx.x + i * blockDim.x, hold_g[kHold ? i : 0], hold_n[kHold ? i : 0]);
+  }
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    if (ring.stages == 1) {
+      if (VEC == 1) __syncthreads();   // every thread has left the row before
+      fetch(row, 0);
+    }
+    ring.wait();
+    // every thread has left the row before (its own vectors: the thread itself; windows: the barrier in wait())
+    if (ring.stages > 1) fetch(row + (int64_t)(ring.stages - 1) * gridDim.x, ring.freed(stage));
+    const int64_t off = ring.offset(row);
+    const uint32_t here = ring.at(stage, off);
+    auto place = [&](void *out, int i) {   // of this thread's i-th vector in an output
+      return reinterpret_cast<T *>((uint8_t *)out + off + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step);
+    };
     // out^2, out w_next dn | y^2, q dout, q w_next dn, q out
-    S s[6] = {0, 0, 0, 0, 0, 0};
+    L t[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) t[i] = splat<L>(0.0f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
+      if (!ring.has(i)) continue;
       const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nvec) continue;
-      float td[VEC], tn[VEC], to[VEC], ty[VEC], tw[VEC], tg[VEC];
-      S u[VEC];
-      P pw;
+      L(&wg)[N] = hold_g[kHold ? i : 0], (&wn)[N] = hold_n[kHold ? i : 0];
+      if (!kHold) weights(v, wg, wn);
+      L u[N], o[N], q[N];
       if (NEXT) {
-        pw.load((const T *)p.w_next + (int64_t)v * VEC);
-        pw.unpack(tw);
-        pn[i].unpack(tn);
-        po[i].unpack(to);
+        V::load_shared(here + kDn * ring.row_bytes + i * ring.step, u);
+        V::load_shared(here + kOut * ring.row_bytes + i * ring.step, o);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          u[c] = (S)tn[c] * tw[c];
-          s[0] += (S)to[c] * to[c];
-          s[1] += to[c] * u[c];
+        for (int c = 0; c < N; ++c) {
+          u[c] = mul(u[c], wn[c]);
+          t[0] = fma(o[c], o[c], t[0]);
+          t[1] = fma(o[c], u[c], t[1]);
         }
       }
       if (BLOCK) {
-        py[i].unpack(ty);
-        pw.load((const T *)p.w_post + (int64_t)v * VEC);
-        pw.unpack(tw);
-        if (p.gate_kind != MOE_GATE_NONE) pg[i].unpack(tg);
-        if (p.dout) pd[i].unpack(td);
+        V::load_shared(here + kY * ring.row_bytes + i * ring.step, q);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          s[2] += (S)ty[c] * ty[c];
-          const S q = (S)ty[c] * tw[c] * (p.gate_kind != MOE_GATE_NONE ? tg[c] : 1.0f);
-          if (p.dout) s[3] += q * td[c];
-          if (NEXT) {
-            s[4] += q * u[c];
-            s[5] += q * to[c];
+        for (int c = 0; c < N; ++c) {
+          t[2] = fma(q[c], q[c], t[2]);
+          q[c] = mul(q[c], wg[c]);
+        }
+        if (token) {
+          L g[N];
+          V::load_shared(here + at_g * ring.row_bytes + i * ring.step, g);
+#pragma unroll
+          for (int c = 0; c < N; ++c) q[c] = mul(q[c], g[c]);
+        }
+        if (has_d) {
+          L d[N];
+          V::load_shared(here + at_d * ring.row_bytes + i * ring.step, d);
+#pragma unroll
+          for (int c = 0; c < N; ++c) t[3] = fma(q[c], d[c], t[3]);
+        }
+        if (NEXT) {
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            t[4] = fma(q[c], u[c], t[4]);
+            t[5] = fma(q[c], o[c], t[5]);
           }
         }
       }
     }
-    block_sum(s, buf, half);
-    const S rn = NEXT ? S(1) / sqrt(s[0] * inv_d + p.eps) : S(0);
+    S s[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) s[i] = total(t[i]);
+    block_sum6(s, sums, half);
+    const S rn = NEXT ? inv_root(s[0] * inv_d + p.eps) : S(0);
     const S cn = rn * rn * (s[1] * inv_d);                   // r^2 mean(out u)
-    const S ry = BLOCK ? S(1) / sqrt(s[2] * inv_d + p.eps) : S(0);
+    const S ry = BLOCK ? inv_root(s[2] * inv_d + p.eps) : S(0);
     const S uy = s[3] + rn * (s[4] - cn * s[5]);             // sum u y
     const S cy = ry * ry * (uy * inv_d);
+    const L Rn = all(rn, L()), Cn = all(-cn, L()), Ry = all(ry, L()), Cy = all(-cy, L()), scale = splat<L>(p.res_scale);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
+      if (!ring.has(i)) continue;
       const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nvec) continue;
-      const int64_t at = base + (int64_t)v * VEC;
-      float tn[VEC], to[VEC], ty[VEC], tw[VEC], tg[VEC], t[VEC];
-      S G[VEC];
-      P pw;
-      if (p.dout) pd[i].unpack(t);
+      L(&wg)[N] = hold_g[kHold ? i : 0], (&wn)[N] = hold_n[kHold ? i : 0];
+      if (!kHold) weights(v, wg, wn);
+      L G[N], a[N], b[N];
+      if (has_d) {
+        V::load_shared(here + at_d * ring.row_bytes + i * ring.step, G);
+      } else {
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) G[c] = p.dout ? (S)t[c] : S(0);
+        for (int c = 0; c < N; ++c) G[c] = splat<L>(0.0f);
+      }
       if (NEXT) {
-        pw.load((const T *)p.w_next + (int64_t)v * VEC);
-        pw.unpack(tw);
-        pn[i].unpack(tn);
-        po[i].unpack(to);
+        V::load_shared(here + kDn * ring.row_bytes + i * ring.step, a);
+        V::load_shared(here + kOut * ring.row_bytes + i * ring.step, b);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          G[c] += rn * ((S)tn[c] * tw[c] - to[c] * cn);
-          acc_n[i][c] = fmaf(tn[c] * (float)rn, to[c], acc_n[i][c]);
+        for (int c = 0; c < N; ++c) {
+          G[c] = fma(fma(b[c], Cn, mul(a[c], wn[c])), Rn, G[c]);
+          acc_n[i][c] = fma(mul(a[c], Rn), b[c], acc_n[i][c]);
         }
       }
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) t[c] = (float)(BLOCK ? p.res_scale * G[c] : G[c]);
-      P::store((T *)p.dx + at, t);
+      for (int c = 0; c < N; ++c) a[c] = BLOCK ? mul(G[c], scale) : G[c];
+      V::store(place(p.dx, i), a);
       if (BLOCK) {
-        py[i].unpack(ty);
-        pw.load((const T *)p.w_post + (int64_t)v * VEC);
-        pw.unpack(tw);
-        if (p.gate_kind != MOE_GATE_NONE) pg[i].unpack(tg);
+        V::load_shared(here + kY * ring.row_bytes + i * ring.step, a);
+        if (token) {   // d_gate = G y r w_post; then wg is per token
+          V::load_shared(here + at_g * ring.row_bytes + i * ring.step, b);
+          L dg[N];
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          const float g = p.gate_kind != MOE_GATE_NONE ? tg[c] : 1.0f;
-          const float Gy = (float)(G[c] * ty[c] * ry);
-          acc_p[i][c] = p.gate_kind == MOE_GATE_TOKEN ? fmaf(g, Gy, acc_p[i][c]) : acc_p[i][c] + Gy;
-          t[c] = (float)(ry * ((S)g * tw[c] * G[c] - ty[c] * cy));
-          tg[c] = Gy * tw[c];
+          for (int c = 0; c < N; ++c) {
+            const L Gy = mul(mul(a[c], Ry), G[c]);
+            acc_p[i][c] = fma(b[c], Gy, acc_p[i][c]);
+            dg[c] = mul(Gy, wg[c]);
+            G[c] = mul(G[c], b[c]);
+          }
+          V::store(place(p.d_gate, i), dg);
+        } else {
+#pragma unroll
+          for (int c = 0; c < N; ++c) acc_p[i][c] = fma(mul(a[c], Ry), G[c], acc_p[i][c]);
         }
-        P::store((T *)p.dy + at, t);
-        if (p.gate_kind == MOE_GATE_TOKEN) P::store((T *)p.d_gate + at, tg);
+#pragma unroll
+        for (int c = 0; c < N; ++c) a[c] = mul(fma(a[c], Cy, mul(wg[c], G[c])), Ry);
+        V::store(place(p.dy, i), a);
       }
     }
+    if (++stage == ring.stages) stage = 0;
   }
+  start_next();   // the kernel that adds up the partial rows
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
+    if (!ring.has(i)) continue;
     const int v = threadIdx.x + i * blockDim.x;
-    if (v >= nvec) continue;
     float *dst = p.part + (int64_t)blockIdx.x * p.d + (int64_t)v * VEC;
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) {
-      if (NEXT) dst[c] = acc_n[i][c];
-      if (BLOCK) dst[(int64_t)gridDim.x * p.d + c] = acc_p[i][c];
-    }
+    if (NEXT) put_part(dst, acc_n[i]);
+    if (BLOCK) put_part(dst + (int64_t)gridDim.x * p.d, acc_p[i]);
   }
 }
 
@@ -334,6 +625,7 @@ template <typename T>
 __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *part, int blocks, int d, int gate_kind,
                                                             const T *w_post, const T *gate, T *dw_next, T *dw_post,
                                                             T *d_gate) {
+  wait_previous();
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
@@ -365,57 +657,86 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *part, i
   }
 }
 
-// Vectors per row, per thread and threads per block for one row length: 16-byte vectors where a row is
-// a multiple of 16 bytes, else single elements.
+// Geometry of one row length: 16-byte vectors where a row is a multiple of 16 bytes, else single elements; values per
+// thread (iter vectors) and threads per block; the ring's row buffers.
 struct Shape {
   int vec, iter, threads;
+  uint32_t row_bytes;
 };
 static Shape shape_of(int d, int dtype) {
-  const int full = dtype == MOE_BF16 ? 8 : 4;
+  const int es = dtype == MOE_BF16 ? 2 : 4, full = 16 / es;
   Shape s;
   s.vec = d % full == 0 ? full : 1;
   const int nvec = d / s.vec;
   s.iter = s.vec > 1 ? 1 : 4;
   while (s.iter * kMaxThreads < nvec) s.iter *= s.vec > 1 ? 2 : 4;
-  const int per = (nvec + s.iter - 1) / s.iter;
-  s.threads = (per + 31) / 32 * 32;
+  s.threads = ((nvec + s.iter - 1) / s.iter + 31) / 32 * 32;
+  s.row_bytes = s.vec > 1 ? (uint32_t)d * es : ((uint32_t)d * es + 15) / 16 * 16 + 16;   // windows may start 15 bytes early
   return s;
 }
+static int stages_of(const Shape &s, int tensors) {
+  int n = kStages;
+  while (n > 1 && (size_t)n * tensors * s.row_bytes > kRingMost) --n;
+  return n;   // one stage of five fp32 rows of MOE_NORM_MAX_D is 164 KB
+}
+static size_t ring_bytes(const Shape &s, int tensors) { return (size_t)stages_of(s, tensors) * tensors * s.row_bytes; }
 
-// Blocks of the backward: each leaves a partial row, so there are no more than keep the GPU busy.
-static int bwd_blocks(int64_t T, const Shape &s) {
-  int64_t b = 152 * (s.threads >= 512 ? 2 : 1024 / s.threads);
+// Blocks that an SM holds at once, by threads (the kernels' launch bounds) and by shared memory.
+static int per_sm(const Shape &s, int tensors, int threads_max) {
+  int n = threads_max / s.threads;
+  const int by_smem = (int)((size_t)220 * 1024 / (ring_bytes(s, tensors) + 2048));
+  if (n > by_smem) n = by_smem;
+  return n < 1 ? 1 : (n > 16 ? 16 : n);
+}
+
+// Blocks of the backward on rows of `tensors` inputs: each leaves a partial row, so there are no more than the GPU
+// holds at once. (More inputs, fewer blocks.)
+static int bwd_blocks(int64_t T, const Shape &s, int tensors) {
+  int64_t b = 152 * per_sm(s, tensors, bwd_per_sm(s.vec, s.iter) * kMaxThreads);
   if (b > T) b = T;
   return b < 1 ? 1 : (int)b;
 }
 
+template <typename Params>
+static int launch(void (*kernel)(Params, Geometry), const Params &p, const Shape &sh, int tensors, int grid, cudaStream_t s) {
+  const size_t smem = ring_bytes(sh, tensors);
+  const Geometry ring{sh.row_bytes, tensors * sh.row_bytes, stages_of(sh, tensors)};
+  if (smem > 40 * 1024)   // with the sums' buffer past the 48 KB that every kernel may have
+    MOE_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  kernel<<<grid, sh.threads, smem, s>>>(p, ring);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
 template <typename T, int VEC, int ITER>
-static void launch_fwd(const FwdParams &p, bool block, bool next, int grid, int threads, cudaStream_t s) {
-  if (!block) norm_fwd_kernel<T, VEC, ITER, false, true><<<grid, threads, 0, s>>>(p);
-  else if (next) norm_fwd_kernel<T, VEC, ITER, true, true><<<grid, threads, 0, s>>>(p);
-  else norm_fwd_kernel<T, VEC, ITER, true, false><<<grid, threads, 0, s>>>(p);
+static int launch_fwd(const FwdParams &p, bool block, bool next, const Shape &sh, cudaStream_t s) {
+  const int tensors = block ? (p.gate_kind == MOE_GATE_TOKEN ? 3 : 2) : 1;
+  int64_t grid = (int64_t)sm_count() * per_sm(sh, tensors, sh.iter == 1 ? 2 * kMaxThreads : kMaxThreads);
+  if (grid > p.T) grid = p.T;
+  if (!block) return launch(norm_fwd_kernel<T, VEC, ITER, false, true>, p, sh, tensors, (int)grid, s);
+  if (next) return launch(norm_fwd_kernel<T, VEC, ITER, true, true>, p, sh, tensors, (int)grid, s);
+  return launch(norm_fwd_kernel<T, VEC, ITER, true, false>, p, sh, tensors, (int)grid, s);
 }
 template <typename T, int VEC, int ITER, typename S = float>
-static void launch_bwd(const BwdParams &p, bool block, bool next, int grid, int threads, cudaStream_t s) {
-  if (!block) norm_bwd_kernel<T, VEC, ITER, false, true, S><<<grid, threads, 0, s>>>(p);
-  else if (next) norm_bwd_kernel<T, VEC, ITER, true, true, S><<<grid, threads, 0, s>>>(p);
-  else norm_bwd_kernel<T, VEC, ITER, true, false, S><<<grid, threads, 0, s>>>(p);
+static int launch_bwd(const BwdParams &p, bool block, bool next, const Shape &sh, int tensors, int grid, cudaStream_t s) {
+  if (!block) return launch(norm_bwd_kernel<T, VEC, ITER, false, true, S>, p, sh, tensors, grid, s);
+  if (next) return launch(norm_bwd_kernel<T, VEC, ITER, true, true, S>, p, sh, tensors, grid, s);
+  return launch(norm_bwd_kernel<T, VEC, ITER, true, false, S>, p, sh, tensors, grid, s);
 }
 
-#define MOE_NORM_DISPATCH(FN, ...)                                        \
-  do {                                                                    \
-    if (dtype == MOE_BF16) {                                              \
-      if (sh.vec == 8 && sh.iter == 1) FN<__nv_bfloat16, 8, 1>(__VA_ARGS__); \
-      else if (sh.vec == 8) FN<__nv_bfloat16, 8, 2>(__VA_ARGS__);         \
-      else if (sh.iter == 4) FN<__nv_bfloat16, 1, 4>(__VA_ARGS__);        \
-      else FN<__nv_bfloat16, 1, 16>(__VA_ARGS__);                         \
-    } else {                                                              \
-      if (sh.vec == 4 && sh.iter == 1) FN<float, 4, 1>(__VA_ARGS__);      \
-      else if (sh.vec == 4 && sh.iter == 2) FN<float, 4, 2>(__VA_ARGS__); \
-      else if (sh.vec == 4) FN<float, 4, 4>(__VA_ARGS__);                 \
-      else if (sh.iter == 4) FN<float, 1, 4>(__VA_ARGS__);                \
-      else FN<float, 1, 16>(__VA_ARGS__);                                 \
-    }                                                                     \
+#define MOE_NORM_DISPATCH(FN, ...)                                                   \
+  do {                                                                               \
+    if (dtype == MOE_BF16) {                                                         \
+      if (sh.vec == 8 && sh.iter == 1) rc = FN<__nv_bfloat16, 8, 1>(__VA_ARGS__);    \
+      else if (sh.vec == 8) rc = FN<__nv_bfloat16, 8, 2>(__VA_ARGS__);               \
+      else if (sh.iter == 4) rc = FN<__nv_bfloat16, 1, 4>(__VA_ARGS__);              \
+      else rc = FN<__nv_bfloat16, 1, 16>(__VA_ARGS__);                               \
+    } else {                                                                         \
+      if (sh.vec == 4 && sh.iter == 1) rc = FN<float, 4, 1>(__VA_ARGS__);            \
+      else if (sh.vec == 4 && sh.iter == 2) rc = FN<float, 4, 2>(__VA_ARGS__);       \
+      else if (sh.vec == 4) rc = FN<float, 4, 4>(__VA_ARGS__);                       \
+      else if (sh.iter == 4) rc = FN<float, 1, 4>(__VA_ARGS__);                      \
+      else rc = FN<float, 1, 16>(__VA_ARGS__);                                       \
+    }                                                                                \
   } while (0)
 
 static int check_shape(int T, int d, int dtype, float eps) {
@@ -427,38 +748,41 @@ static bool bad(const void *p) { return !p || !aligned16(p); }
 
 static int run_fwd(const FwdParams &p, int dtype, bool block, bool next, cudaStream_t s) {
   const Shape sh = shape_of(p.d, dtype);
-  int64_t grid = (int64_t)sm_count() * (2048 / sh.threads < 32 ? 2048 / sh.threads : 32);
-  if (grid > p.T) grid = p.T;
-  MOE_NORM_DISPATCH(launch_fwd, p, block, next, (int)grid, sh.threads, s);
-  MOE_CHECK_LAUNCH();
-  return MOE_OK;
+  int rc = MOE_OK;
+  MOE_NORM_DISPATCH(launch_fwd, p, block, next, sh, s);
+  return rc;
 }
 
 static int run_bwd(BwdParams p, int dtype, bool block, bool next, void *dw_next, void *dw_post, void *d_gate, void *ws,
                    size_t ws_bytes, cudaStream_t s) {
   const Shape sh = shape_of(p.d, dtype);
-  const int grid = bwd_blocks(p.T, sh);
+  const int tensors = (next ? 2 : 0) + (block ? 1 : 0) + (p.dout ? 1 : 0) + (block && p.gate_kind == MOE_GATE_TOKEN ? 1 : 0);
+  const int grid = bwd_blocks(p.T, sh, tensors);
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < moe_norm_bwd_workspace_size((int)p.T, p.d, dtype))
     return MOE_ERR_INVALID_ARG;
   p.part = static_cast<float *>(ws);
-  if (p.d <= 32) {
-    if (dtype == MOE_BF16) launch_bwd<__nv_bfloat16, 1, 1, double>(p, block, next, grid, sh.threads, s);
-    else launch_bwd<float, 1, 1, double>(p, block, next, grid, sh.threads, s);
+  int rc = MOE_OK;
+  if (p.d <= 32) {   // one element per lane, in 64 bits
+    Shape one = sh;
+    one.vec = one.iter = 1;
+    one.threads = 32;
+    one.row_bytes = ((uint32_t)p.d * (uint32_t)dtype_size(dtype) + 15) / 16 * 16 + 16;
+    if (dtype == MOE_BF16) rc = launch_bwd<__nv_bfloat16, 1, 1, double>(p, block, next, one, tensors, grid, s);
+    else rc = launch_bwd<float, 1, 1, double>(p, block, next, one, tensors, grid, s);
   } else {
-    MOE_NORM_DISPATCH(launch_bwd, p, block, next, grid, sh.threads, s);
+    MOE_NORM_DISPATCH(launch_bwd, p, block, next, sh, tensors, grid, s);
   }
-  MOE_CHECK_LAUNCH();
+  if (rc) return rc;
   const dim3 g((p.d + 31) / 32, block ? 2 : 1);
   if (dtype == MOE_BF16) {
     using B = __nv_bfloat16;
-    norm_bwd_sum_kernel<B><<<g, 1024, 0, s>>>(p.part, grid, p.d, p.gate_kind, (const B *)p.w_post, (const B *)p.gate,
-                                              (B *)dw_next, (B *)dw_post, (B *)d_gate);
+    MOE_TRY_CUDA(launch_after(norm_bwd_sum_kernel<B>, g, dim3(1024), 0, s, p.part, grid, p.d, p.gate_kind,
+                              (const B *)p.w_post, (const B *)p.gate, (B *)dw_next, (B *)dw_post, (B *)d_gate));
   } else {
-    norm_bwd_sum_kernel<float><<<g, 1024, 0, s>>>(p.part, grid, p.d, p.gate_kind, (const float *)p.w_post,
-                                                  (const float *)p.gate, (float *)dw_next, (float *)dw_post,
-                                                  (float *)d_gate);
+    MOE_TRY_CUDA(launch_after(norm_bwd_sum_kernel<float>, g, dim3(1024), 0, s, p.part, grid, p.d, p.gate_kind,
+                              (const float *)p.w_post, (const float *)p.gate, (float *)dw_next, (float *)dw_post,
+                              (float *)d_gate));
   }
-  MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
 
@@ -470,7 +794,7 @@ using namespace moe::norm;
 
 extern "C" size_t moe_norm_bwd_workspace_size(int T, int d, int dtype) {
   if (T < 0 || d < 1) return 0;
-  return (size_t)2 * bwd_blocks(T, shape_of(d, dtype)) * d * sizeof(float) + 256;
+  return (size_t)2 * bwd_blocks(T, shape_of(d, dtype), 2) * d * sizeof(float) + 256;
 }
 
 extern "C" int moe_norm_fwd(const void *x, const void *w, int T, int d, int dtype, float eps, void *n,
