@@ -147,14 +147,25 @@ def _want(name, t, dtype, shape):
                          f"{tuple(t.shape)} with strides {t.stride()}")
 
 
+def _ptr(name, t, dtype, shape):
+    """The address of a tensor argument that _want accepts."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _want(name, t, dtype, shape)
+    if not t.is_cuda:
+        raise ValueError("libmoe takes CUDA tensors only")
+    return t.data_ptr()
+
+
 def _scale_bytes(rows, cols):
     return -(-rows // 128) * -(-cols // 128) * 512
 
 
 def _bytes_at_least(name, t, n):
+    """The address of a tensor of at least n bytes."""
     if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{name}: a contiguous uint8 tensor of at least {n} bytes is needed, got {t.dtype} "
                          f"{tuple(t.shape)}")
+    return _p(t)
 
 
 def _ok(fn, rc):
@@ -414,25 +425,20 @@ def _rows(x):
 
 def moe_fp4_quantize(x, codes, scales, stream=None):
     """x [..., K] (rows in order) -> codes [..., K/2] uint8, scales [moe_fp4_scale_bytes(rows, K)] uint8."""
-    shape = x.shape
+    shape, dt = x.shape, x.dtype
     R, K = _rows(x)
-    dt = x.dtype
-    _want("x", x, dt, shape)
-    _want("codes", codes, torch.uint8, shape[:-1] + (K // 2,))
-    _bytes_at_least("scales", scales, _scale_bytes(R, K))
-    _ok("moe_fp4_quantize", lib().moe_fp4_quantize(_p(x), dtype_code(dt), R, K, _p(codes), _p(scales), _s(stream)))
+    _ok("moe_fp4_quantize", lib().moe_fp4_quantize(
+        _ptr("x", x, dt, shape), dtype_code(dt), R, K, _ptr("codes", codes, torch.uint8, shape[:-1] + (K // 2,)),
+        _bytes_at_least("scales", scales, _scale_bytes(R, K)), _s(stream)))
 
 
 def moe_fp4_dequantize(codes, scales, x, stream=None):
     """The values that codes and scales stand for, into x [..., K]."""
-    shape = x.shape
+    shape, dt = x.shape, x.dtype
     R, K = _rows(x)
-    dt = x.dtype
-    _want("x", x, dt, shape)
-    _want("codes", codes, torch.uint8, shape[:-1] + (K // 2,))
-    _bytes_at_least("scales", scales, _scale_bytes(R, K))
-    _ok("moe_fp4_dequantize", lib().moe_fp4_dequantize(_p(codes), _p(scales), R, K, dtype_code(dt), _p(x),
-                                                       _s(stream)))
+    _ok("moe_fp4_dequantize", lib().moe_fp4_dequantize(
+        _ptr("codes", codes, torch.uint8, shape[:-1] + (K // 2,)),
+        _bytes_at_least("scales", scales, _scale_bytes(R, K)), R, K, dtype_code(dt), _ptr("x", x, dt, shape), _s(stream)))
 
 
 def moe_permute_fp4(x, k, E, row_of_slot, counts, tile_offsets, codes, scales, stream=None):
@@ -440,31 +446,25 @@ def moe_permute_fp4(x, k, E, row_of_slot, counts, tile_offsets, codes, scales, s
     T, d = x.shape
     R = codes.shape[0]
     dt = x.dtype
-    _want("x", x, dt, (T, d))
-    _want("codes", codes, torch.uint8, (R, d // 2))
-    _bytes_at_least("scales", scales, _scale_bytes(R, d))
-    _ok("moe_permute_fp4", lib().moe_permute_fp4(_p(x), dtype_code(dt), T, d, k, E, _p(row_of_slot), _p(counts),
-                                                 _p(tile_offsets), R, _p(codes), _p(scales), _s(stream)))
+    _ok("moe_permute_fp4", lib().moe_permute_fp4(
+        _ptr("x", x, dt, (T, d)), dtype_code(dt), T, d, k, E, _p(row_of_slot), _p(counts), _p(tile_offsets), R,
+        _ptr("codes", codes, torch.uint8, (R, d // 2)), _bytes_at_least("scales", scales, _scale_bytes(R, d)),
+        _s(stream)))
 
 
 def moe_grouped_ffn_fwd_fp4(x_codes, x_scales, wgu_codes, wgu_scales, wd_codes, wd_scales, tile_offsets, offsets,
                             h_codes, h_scales, y_perm, ws, stream=None):
     """wgu_codes [E, 2f, d/2], wd_codes [E, d, f/2]; h_codes [rows_max, f/2] and h_scales are scratch."""
     E, d, f2 = wd_codes.shape
-    R, f = x_codes.shape[0], 2 * f2
-    _want("x_codes", x_codes, torch.uint8, (R, d // 2))
-    _want("wgu_codes", wgu_codes, torch.uint8, (E, 2 * f, d // 2))
-    _want("wd_codes", wd_codes, torch.uint8, (E, d, f // 2))
-    _want("h_codes", h_codes, torch.uint8, (R, f // 2))
-    _want("y_perm", y_perm, torch.bfloat16, (R, d))
-    _bytes_at_least("x_scales", x_scales, _scale_bytes(R, d))
-    _bytes_at_least("h_scales", h_scales, _scale_bytes(R, f))
-    _bytes_at_least("wgu_scales", wgu_scales, _scale_bytes(E * 2 * f, d))
-    _bytes_at_least("wd_scales", wd_scales, _scale_bytes(E * d, f))
+    R, f, u8 = x_codes.shape[0], 2 * f2, torch.uint8
     _ok("moe_grouped_ffn_fwd_fp4", lib().moe_grouped_ffn_fwd_fp4(
-        _p(x_codes), _p(x_scales), _p(wgu_codes), _p(wgu_scales), _p(wd_codes), _p(wd_scales), _p(tile_offsets),
-        _p(offsets), E, d, f, R, _p(h_codes), _p(h_scales), _p(y_perm), _p(ws), ws.numel() * ws.element_size(),
-        _s(stream)))
+        _ptr("x_codes", x_codes, u8, (R, d // 2)), _bytes_at_least("x_scales", x_scales, _scale_bytes(R, d)),
+        _ptr("wgu_codes", wgu_codes, u8, (E, 2 * f, d // 2)),
+        _bytes_at_least("wgu_scales", wgu_scales, _scale_bytes(E * 2 * f, d)),
+        _ptr("wd_codes", wd_codes, u8, (E, d, f2)), _bytes_at_least("wd_scales", wd_scales, _scale_bytes(E * d, f)),
+        _p(tile_offsets), _p(offsets), E, d, f, R, _ptr("h_codes", h_codes, u8, (R, f2)),
+        _bytes_at_least("h_scales", h_scales, _scale_bytes(R, f)), _ptr("y_perm", y_perm, torch.bfloat16, (R, d)),
+        _p(ws), ws.numel() * ws.element_size(), _s(stream)))
 
 
 def moe_read_status(ws, stream=None):

@@ -33,6 +33,9 @@ class BlockNorms:
         act = dict(dtype=dtype, device=self.device)
         self.n = torch.empty((T, d), **act)
         self.out = torch.empty((T, d), **act)
+        self._kind = {None: L.GATE_NONE, "channel": L.GATE_CHANNEL, "token": L.GATE_TOKEN}[gate]
+        self._code = L.dtype_code(dtype)
+        self._out_ptr, self._n_ptr = self.out.data_ptr(), self.n.data_ptr() if next_norm else None
         self.backward_enabled = backward
         if backward:
             self.dx = torch.empty((T, d), **act)
@@ -56,10 +59,18 @@ class BlockNorms:
 
     def post(self, y, x, w_post, gate=None, w_next=None, stream=None):
         """(out, n): the stream after the block and the next block's input (None without a next norm)."""
-        self._check_gate(gate)
-        n = self.n if self.next_norm else None
-        L.moe_norm_residual_fwd(y, x, w_post, gate, w_next, self.out, n, self.res_scale, self.eps, stream)
-        return self.out, n
+        T, d, dt = self.T, self.d, self.dtype
+        if (w_next is not None) != self.next_norm:
+            raise ValueError("w_next is needed with a next norm, and only there")
+        if self._kind or gate is not None:
+            self._check_gate(gate)
+            gate = L._ptr("gate", gate, dt, (d,) if self._kind == L.GATE_CHANNEL else (T, d))
+        ptr = L._ptr
+        L._ok("moe_norm_residual_fwd", L.lib().moe_norm_residual_fwd(
+            ptr("y", y, dt, (T, d)), ptr("x", x, dt, (T, d)), ptr("w_post", w_post, dt, (d,)), gate, self._kind,
+            ptr("w_next", w_next, dt, (d,)) if self.next_norm else None, T, d, self._code, self.res_scale, self.eps,
+            self._out_ptr, self._n_ptr, L._s(stream)))
+        return self.out, (self.n if self.next_norm else None)
 
     def post_backward(self, dout, dn, out, y, w_post, gate=None, w_next=None, stream=None):
         """Gradients of post: dout reaches out through the stream, dn through the next norm. Returns dx, dy, dw_post,

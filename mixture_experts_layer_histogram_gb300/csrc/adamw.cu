@@ -130,11 +130,13 @@ template <typename T> __device__ __forceinline__ float load1(const T *p) {
   else return __bfloat162float(*p);
 }
 
-// Blocks per SM (they set the grid and the registers). fp32 states are bound by HBM, which a few blocks with
+// Blocks per SM (they set the registers, and the grid of plans that fill the GPU). fp32 states are bound by HBM, which a few blocks with
 // wide rows of loads fill best; 8-bit states by instructions, which more warps issue better. Measured on
 // one layer's 403M values (bf16): fp32 states with a master 1851 us at 2 blocks, 1922 at 3, 1956 at 4; 8-bit
 // states 934 us at 5 blocks, 1004 at 4, 1030 at 6, 1082 at 3.
 constexpr int per_sm(int k) { return k >= F32_F8 ? 5 : 2; }
+// Blocks per SM that the registers allow: a plan with at most that many chunks runs one chunk per block.
+constexpr int per_sm_most(int k) { return k >= F32_F8 ? 5 : 3; }
 
 // The step's constants.
 struct Coef {
@@ -361,7 +363,7 @@ __device__ __forceinline__ void update8(const Tensor &t, const Raw8<K> &raw, int
 }
 
 template <int K>
-__global__ void __launch_bounds__(kThreads, per_sm(K)) adamw_kernel(const Tensor *__restrict__ tensors,
+__global__ void __launch_bounds__(kThreads, per_sm_most(K)) adamw_kernel(const Tensor *__restrict__ tensors,
                                                                     const Chunk *__restrict__ chunks, int64_t nchunks,
                                                                     const Hyper hy, moe_adamw_state *st, int bump) {
   constexpr int kPasses = kChunk / (kThreads * kVec);
@@ -371,6 +373,13 @@ __global__ void __launch_bounds__(kThreads, per_sm(K)) adamw_kernel(const Tensor
   Coef co;
   co.lr = st->lr;
   co.gs = st->grad_scale;
+  // Every thread of a block has read the state when the block arrives, so the block that arrives last may advance
+  // it at once. (Arriving at the kernel's end put a fence and an atomic behind the last stores.)
+  __syncthreads();
+  if (bump && threadIdx.x == 0 && atomicAdd(&st->arrived, 1u) == gridDim.x - 1) {
+    st->arrived = 0;
+    st->step = step;
+  }
   const float bc1 = -expm1f((float)step * hy.log_beta1), bc2 = -expm1f((float)step * hy.log_beta2);
   co.lr1 = -co.lr / bc1;
   co.inv_root2 = 1.0f / sqrtf(bc2);
@@ -406,15 +415,6 @@ __global__ void __launch_bounds__(kThreads, per_sm(K)) adamw_kernel(const Tensor
       }
     }
   }
-  // every thread of a block has read the step count when the block arrives; the last block advances it
-  __syncthreads();
-  if (bump && threadIdx.x == 0) {
-    __threadfence();
-    if (atomicAdd(&st->arrived, 1u) == gridDim.x - 1) {
-      st->arrived = 0;
-      st->step = step;
-    }
-  }
 }
 
 static int kind_of(const moe_adamw_tensor &t) {
@@ -440,7 +440,8 @@ static int check(const moe_adamw_tensor &t) {
 template <int K>
 static int launch(const uint8_t *dev, const Header *h, int64_t first, int64_t n, const Hyper &hy, moe_adamw_state *st,
                   bool bump, cudaStream_t s) {
-  int64_t grid = (int64_t)sm_count() * per_sm(K);
+  const int sms = sm_count();
+  int64_t grid = n <= (int64_t)sms * per_sm_most(K) ? n : (int64_t)sms * per_sm(K);
   if (grid > n) grid = n;
   if (grid < 1) grid = 1;
   adamw_kernel<K><<<(int)grid, kThreads, 0, s>>>((const Tensor *)(dev + sizeof(Header)),
