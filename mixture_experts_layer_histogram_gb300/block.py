@@ -31,7 +31,8 @@ class BlockNorms:
         self.res_scale, self.eps, self.next_norm = res_scale, eps, next_norm
         self.device = torch.device(device)
         act = dict(dtype=dtype, device=self.device)
-        self.n = torch.empty((T, d), **act)
+        self.n_first = torch.empty((T, d), **act)      # pre's output: the block may read it again in its backward
+        self.n = torch.empty((T, d), **act) if next_norm else None
         self.out = torch.empty((T, d), **act)
         self._kind = {None: L.GATE_NONE, "channel": L.GATE_CHANNEL, "token": L.GATE_TOKEN}[gate]
         self._code = L.dtype_code(dtype)
@@ -54,8 +55,8 @@ class BlockNorms:
 
     def pre(self, x, w, stream=None):
         """n [T, d] = x rms(x) w."""
-        L.moe_norm_fwd(x, w, self.n, self.eps, stream)
-        return self.n
+        L.moe_norm_fwd(x, w, self.n_first, self.eps, stream)
+        return self.n_first
 
     def post(self, y, x, w_post, gate=None, w_next=None, stream=None):
         """(out, n): the stream after the block and the next block's input (None without a next norm)."""
@@ -70,7 +71,7 @@ class BlockNorms:
             ptr("y", y, dt, (T, d)), ptr("x", x, dt, (T, d)), ptr("w_post", w_post, dt, (d,)), gate, self._kind,
             ptr("w_next", w_next, dt, (d,)) if self.next_norm else None, T, d, self._code, self.res_scale, self.eps,
             self._out_ptr, self._n_ptr, L._s(stream)))
-        return self.out, (self.n if self.next_norm else None)
+        return self.out, self.n
 
     def post_backward(self, dout, dn, out, y, w_post, gate=None, w_next=None, stream=None):
         """Gradients of post: dout reaches out through the stream, dn through the next norm. Returns dx, dy, dw_post,

@@ -204,6 +204,30 @@ def test_repeats_bit_for_bit_on_another_stream_and_in_a_graph():
     assert torch.equal(layer.out, first) and layer.status() == (0, 0)
 
 
+def test_non_finite_tokens_and_weights():
+    """A token with a NaN or an infinity gives NaN rows of its own only; a weight, the features that it enters."""
+    T, d, E, k, f = 40, 512, 4, 2, 256
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(T, d, generator=g).bfloat16()
+    x[3, 100], x[17, 5] = float("nan"), float("inf")
+    wgu = (torch.randn(E, 2 * f, d, generator=g) * 0.05).bfloat16()
+    wd = (torch.randn(E, d, f, generator=g) * 0.05).bfloat16()
+    layer = MoELayerFp4(T, d, E, k, f)
+    logits = routed(T, E, k, 4).cuda()
+    out = layer.forward(x.cuda(), logits, Fp4Weights.quantize(wgu.cuda(), wd.cuda())).float().cpu()
+    bad = torch.zeros(T, dtype=torch.bool)
+    bad[[3, 17]] = True
+    assert torch.isnan(out[bad]).all() and torch.isfinite(out[~bad]).all()
+    wd[1, 7, 3] = float("nan")                              # output feature 7 of expert 1
+    x = torch.randn(T, d, generator=g).bfloat16().cuda()
+    out = layer.forward(x, logits, Fp4Weights.quantize(wgu.cuda(), wd.cuda())).float().cpu()
+    hit = (layer.topk_idx.cpu() == 1).any(1)
+    assert torch.isnan(out[hit, 7]).all() and torch.isfinite(out[~hit]).all()
+    rest = torch.ones(d, dtype=torch.bool)
+    rest[7] = False
+    assert torch.isfinite(out[:, rest]).all() and layer.status() == (0, 0)
+
+
 def test_no_tokens():
     layer = MoELayerFp4(0, 256, 4, 2, 256)
     W = Fp4Weights.quantize(torch.randn(4, 512, 256, device="cuda"), torch.randn(4, 256, 256, device="cuda"))

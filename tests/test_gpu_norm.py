@@ -172,6 +172,17 @@ def test_non_finite_rows_stay_in_their_row():
     assert torch.isfinite(out[4].float()).sum().item() == 2047
 
 
+def test_pre_output_outlives_post():
+    """A block's backward may read its input again (a router's weight gradient does): post writes the next block's input
+    elsewhere."""
+    s = make(20, 256, torch.bfloat16, None)
+    nm = BlockNorms(20, 256, torch.bfloat16, res_scale=A, eps=EPS)
+    n0 = nm.pre(s["x"], s["w"])
+    keep = n0.clone()
+    _, n1 = nm.post(s["y"], s["x"], s["w"], w_next=s["wn"])
+    assert torch.equal(n0, keep) and n1.data_ptr() != n0.data_ptr()
+
+
 def test_no_tokens():
     d = 128
     nm = BlockNorms(0, d, torch.bfloat16, gate="channel", eps=EPS)
