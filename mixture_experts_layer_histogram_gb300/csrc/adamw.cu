@@ -3,8 +3,8 @@
 //   m' = b1 m + (1 - b1) c g,   v' = b2 v + (1 - b2) (c g)^2,   c = grad_scale
 //   p' = p (1 - lr wd) - lr (m' / (1 - b1^t)) / (sqrt(v' / (1 - b2^t)) + eps)
 //
-// HBM-bound: every value is read and written once. The tensors are cut into chunks of 4096 values; a
-// plan made on the host lists them, so a launch covers any number of tensors of any size and a block
+// HBM-bound: every value is read and written once. The tensors are cut into chunks of 4096 (8-bit states: 8192)
+// values; a plan made on the host lists them, so a launch covers any number of tensors of any size and a block
 // finds its tensor with two dependent loads. The bias corrections come from the step count in device
 // memory, which the launch's last block advances: a captured step counts on when it is replayed.
 //
@@ -25,12 +25,12 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace moe {
 namespace adamw {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 4096;      // values per chunk: two passes of 8 values per thread
 constexpr int kVec = 8;
 constexpr int kBlockQ = MOE_ADAMW_BLOCK;
 static_assert(kBlockQ == 32 * kVec, "a warp owns one block of an 8-bit state");
@@ -38,8 +38,12 @@ static_assert(kBlockQ == 32 * kVec, "a warp owns one block of an 8-bit state");
 // Kinds of tensors: parameter and gradient type, fp32 master copy, state.
 enum Kind { F32_F32 = 0, BF16_F32, BF16_MASTER_F32, F32_F8, BF16_F8, BF16_MASTER_F8, KINDS };
 
+// Values per chunk. fp32 states: two passes of 8 values per thread, one after the other. 8-bit states carry a
+// third of the bytes per value, so four passes' loads are issued before any of them is used.
+constexpr int chunk_of(int kind) { return kind >= F32_F8 ? 8192 : 4096; }
+
 struct Chunk {
-  int32_t tensor, index;          // values [index * kChunk, ...) of the tensor
+  int32_t tensor, index;          // values [index * chunk, ...) of the tensor
 };
 struct Tensor {                   // device form of moe_adamw_tensor
   void *p;
@@ -66,21 +70,30 @@ __device__ __forceinline__ uint32_t weyl(uint32_t i, uint32_t t) { return i * 26
 
 // e4m3 codes of y (|y| <= 448 but for rounding), rounded down in magnitude after adding u / 2^20 of a step, where
 // u = h >> 12. z = y 2^-120 moves e4m3's exponents onto the lowest ones of fp32, subnormals onto subnormals, so
-// its bits from the 20th on are the code and adding u below them is the dither; four bits higher, the code is
-// the top byte (at most 0x7e, 448: a block's largest value may lie an ulp above it).
-__device__ __forceinline__ uint32_t dither_top(float z, uint32_t h) {
-  return min(((h >> 12) + __float_as_uint(z)) << 4, 0x7effffffu);
+// its bits 20..26 are the code, adding u below them is the dither, and bit 31 is the sign.
+__device__ __forceinline__ uint32_t dither(float z, uint32_t h) { return (h >> 12) + __float_as_uint(z); }
+// Four codes from four such words, two at a time in 16-bit halves; at most 0x7e (448): a block's largest value may lie
+// an ulp above it.
+template <bool SIGNED> __device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t ab = __byte_perm(a, b, 0x7632), cd = __byte_perm(c, d, 0x7632);
+  uint32_t p = __vminu2((ab << 4) & (SIGNED ? 0x7fff7fffu : 0xffffffffu), 0x7eff7effu);   // codes in bytes 1 and 3
+  uint32_t q = __vminu2((cd << 4) & (SIGNED ? 0x7fff7fffu : 0xffffffffu), 0x7eff7effu);
+  if (SIGNED) {
+    p |= ab & 0x80008000u;
+    q |= cd & 0x80008000u;
+  }
+  return __byte_perm(p, q, 0x7531);
 }
-__device__ __forceinline__ uint32_t dither_top_signed(float z, uint32_t h) {
-  return dither_top(z, h) | (__float_as_uint(z) & 0x80000000u);   // the shift has dropped z's sign
+// One code, of any y: a NaN or an infinity becomes e4m3 NaN.
+__device__ __forceinline__ uint32_t code_any(float y, uint32_t h) {
+  if (!(fabsf(y) <= 500.0f)) return 0x7fu;
+  const uint32_t x = dither(y * 0x1p-120f, h);
+  return min(x >> 20 & 0x7fu, 0x7eu) | (x >> 24 & 0x80u);
 }
-// The same for any y: a NaN or an infinity becomes e4m3 NaN.
-__device__ __forceinline__ uint32_t dither_top_any(float y, uint32_t h) {
-  return fabsf(y) <= 500.0f ? dither_top_signed(y * 0x1p-120f, h) : 0x7f000000u;
-}
-// The top bytes of four words
-__device__ __forceinline__ uint32_t top_bytes(const uint32_t *x) {
-  return __byte_perm(__byte_perm(x[0], x[1], 0x0073), __byte_perm(x[2], x[3], 0x0073), 0x5410);
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ float sqrt_approx(float v) {
   float r;
@@ -130,13 +143,14 @@ template <typename T> __device__ __forceinline__ float load1(const T *p) {
   else return __bfloat162float(*p);
 }
 
-// Blocks per SM (they set the registers, and the grid of plans that fill the GPU). fp32 states are bound by HBM, which a few blocks with
-// wide rows of loads fill best; 8-bit states by instructions, which more warps issue better. Measured on
-// one layer's 403M values (bf16): fp32 states with a master 1851 us at 2 blocks, 1922 at 3, 1956 at 4; 8-bit
-// states 934 us at 5 blocks, 1004 at 4, 1030 at 6, 1082 at 3.
-constexpr int per_sm(int k) { return k >= F32_F8 ? 5 : 2; }
+// Blocks per SM (they set the registers, and the grid of plans that fill the GPU). Measured on one layer's 403M
+// values (bf16): fp32 states with a master 1851 us at 2 blocks, 1922 at 3, 1956 at 4. 8-bit states, (values per
+// chunk, passes loaded ahead, blocks): (8192, 4, 2) 755 us, (8192, 4, 3) 795, (6144, 3, 3) 765, (4096, 2, 3) 800,
+// (4096, 1, 5) 903, (4096, 1, 3) 1063; one fp32 per instruction instead of two: (4096, 1, 5) 934. Sums that are
+// not paired (see update8) cost (8192, 4, 2) 18 us: 773.
+constexpr int per_sm(int) { return 2; }
 // Blocks per SM that the registers allow: a plan with at most that many chunks runs one chunk per block.
-constexpr int per_sm_most(int k) { return k >= F32_F8 ? 5 : 3; }
+constexpr int per_sm_most(int kind) { return kind >= F32_F8 ? 2 : 3; }
 
 // The step's constants.
 struct Coef {
@@ -254,29 +268,50 @@ __device__ __forceinline__ void update8(const Tensor &t, const Raw8<K> &raw, int
     // m and v are rounded at each operation (no fused multiply-add), and the largest root is the root of the
     // largest v, rounded to nearest: the scales then follow from the formulas alone, bit for bit, and a
     // block's largest value gets the code it should. The other roots may be approximate.
-    const float kg = hy.omb1 * co.gs, kg2 = hy.omb2 * (co.gs * co.gs);
+    const F2 b1 = pair(hy.beta1, hy.beta1), b2 = pair(hy.beta2, hy.beta2), ms2 = pair(ms, ms), vs2 = pair(vs, vs);
+    const float kg1 = hy.omb1 * co.gs, kg2 = hy.omb2 * (co.gs * co.gs);
+    const F2 c1 = pair(kg1, kg1), c2 = pair(kg2, kg2);
+    F2 m2[kVec / 2];
     float mx = 0.0f, vx = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      m[j] = __fadd_rn(__fmul_rn(hy.beta1, __fmul_rn(m[j], ms)), __fmul_rn(kg, g[j]));
-      const float a = __fmul_rn(v[j], vs);
-      v[j] = __fadd_rn(__fmul_rn(hy.beta2, __fmul_rn(a, a)), __fmul_rn(kg2, __fmul_rn(g[j], g[j])));
-      mx = fmaxf(mx, fabsf(m[j]));
-      vx = fmaxf(vx, v[j]);
+    for (int j = 0; j < kVec / 2; ++j) {
+      const F2 gg = pair(g[2 * j], g[2 * j + 1]);
+      // the sums one value at a time: the assembler fuses a paired product and sum
+      float x, y, x1, y1;
+      split(mul(b1, mul(pair(m[2 * j], m[2 * j + 1]), ms2)), x, y);
+      split(mul(c1, gg), x1, y1);
+      m[2 * j] = __fadd_rn(x, x1);
+      m[2 * j + 1] = __fadd_rn(y, y1);
+      const F2 a = mul(pair(v[2 * j], v[2 * j + 1]), vs2);
+      split(mul(b2, mul(a, a)), x, y);
+      split(mul(c2, mul(gg, gg)), x1, y1);
+      v[2 * j] = __fadd_rn(x, x1);
+      v[2 * j + 1] = __fadd_rn(y, y1);
+      m2[j] = pair(m[2 * j], m[2 * j + 1]);
+      mx = max_abs3(m[2 * j], m[2 * j + 1], mx);
+      vx = max_abs3(v[2 * j], v[2 * j + 1], vx);
     }
     mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));   // of numbers >= 0, as integers
-    float vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vx)));
+    const float vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vx)));
     vx = sqrtf(vtop);
+    const F2 ir = pair(co.inv_root2, co.inv_root2), eps = pair(hy.eps, hy.eps), l1 = pair(co.lr1, co.lr1), dc = pair(decay, decay);
+    F2 sum2 = pair(0.0f, 0.0f);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      v[j] = v[j] == vtop ? vx : sqrt_approx(v[j]);
-      p[j] = fmaf(p[j], decay, co.lr1 * m[j] * rcp_approx(fmaf(v[j], co.inv_root2, hy.eps)));
-      sum += p[j];
+    for (int j = 0; j < kVec / 2; ++j) {
+      v[2 * j] = v[2 * j] == vtop ? vx : sqrt_approx(v[2 * j]);
+      v[2 * j + 1] = v[2 * j + 1] == vtop ? vx : sqrt_approx(v[2 * j + 1]);
+      float d0, d1;
+      split(fma(pair(v[2 * j], v[2 * j + 1]), ir, eps), d0, d1);
+      const F2 pp = fma(pair(p[2 * j], p[2 * j + 1]), dc, mul(mul(l1, m2[j]), pair(rcp_approx(d0), rcp_approx(d1))));
+      sum2 = add(sum2, pp);
+      split(pp, p[2 * j], p[2 * j + 1]);
     }
+    float s0, s1;
+    split(sum2, s0, s1);
+    sum = s0 + s1;
     // A NaN in m or v shows in p and so in the sum; infinities show in the maxima. Such blocks, and those whose
     // scaling would leave fp32's normal range, take the general form.
     odd = __any_sync(0xffffffffu, sum != sum) || !(fmaxf(mx, vx) < 16384.0f);
-    uint32_t mc[kVec], vc[kVec];
     if (odd) {   // a non-finite value counts for nothing in the scale and is held as NaN
       constexpr float kMax = 3.402823466e38f;
       mx = vx = 0.0f;
@@ -291,20 +326,37 @@ __device__ __forceinline__ void update8(const Tensor &t, const Raw8<K> &raw, int
     // below 1e-30 a block is held as zeros
     const bool mk = mx >= 1e-30f, vk = vx >= 1e-30f;
     const float mi = mk ? __frcp_rn(mx) * 448.0f : 0.0f, vi = vk ? __frcp_rn(vx) * 448.0f : 0.0f;
+    uint32_t mc[2], vc[2];   // four codes each
     if (!odd) {
       const float mz = mi * 0x1p-120f, vz = vi * 0x1p-120f;
+      const F2 mz2 = pair(mz, mz), vz2 = pair(vz, vz);
+      uint32_t mw[kVec], vw[kVec];
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const uint32_t h = h0 + (uint32_t)j * 2654435769u;
-        mc[j] = dither_top_signed(m[j] * mz, h);
-        vc[j] = dither_top(v[j] * vz, h + 0x55555555u);
+      for (int j = 0; j < kVec; j += 2) {
+        const uint32_t h = h0 + (uint32_t)j * 2654435769u, h1 = h0 + (uint32_t)(j + 1) * 2654435769u;
+        float x, y;
+        split(mul(m2[j / 2], mz2), x, y);
+        mw[j] = dither(x, h);
+        mw[j + 1] = dither(y, h1);
+        split(mul(pair(v[j], v[j + 1]), vz2), x, y);
+        vw[j] = dither(x, h + 0x55555555u);
+        vw[j + 1] = dither(y, h1 + 0x55555555u);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        mc[j] = codes4<true>(mw[4 * j], mw[4 * j + 1], mw[4 * j + 2], mw[4 * j + 3]);
+        vc[j] = codes4<false>(vw[4 * j], vw[4 * j + 1], vw[4 * j + 2], vw[4 * j + 3]);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const uint32_t h = h0 + (uint32_t)j * 2654435769u;
-        mc[j] = dither_top_any(m[j] * mi, h);
-        vc[j] = dither_top_any(v[j] * vi, h + 0x55555555u);
+      for (int j = 0; j < 2; ++j) {
+        mc[j] = vc[j] = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t h = h0 + (uint32_t)(4 * j + q) * 2654435769u;
+          mc[j] |= code_any(m[4 * j + q] * mi, h) << (8 * q);
+          vc[j] |= code_any(v[4 * j + q] * vi, h + 0x55555555u) << (8 * q);
+        }
       }
     }
     if ((threadIdx.x & 31) == 0) {
@@ -312,14 +364,14 @@ __device__ __forceinline__ void update8(const Tensor &t, const Raw8<K> &raw, int
       t.v_scale[qb] = vk ? vx * (1.0f / 448.0f) : 0.0f;
     }
     if (FULL) {
-      *reinterpret_cast<uint2 *>(m8) = make_uint2(top_bytes(mc), top_bytes(mc + 4));
-      *reinterpret_cast<uint2 *>(v8) = make_uint2(top_bytes(vc), top_bytes(vc + 4));
+      *reinterpret_cast<uint2 *>(m8) = make_uint2(mc[0], mc[1]);
+      *reinterpret_cast<uint2 *>(v8) = make_uint2(vc[0], vc[1]);
     } else {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         if (j >= live) continue;
-        m8[j] = (uint8_t)(mc[j] >> 24);
-        v8[j] = (uint8_t)(vc[j] >> 24);
+        m8[j] = (uint8_t)(mc[j / 4] >> (8 * (j & 3)));
+        v8[j] = (uint8_t)(vc[j / 4] >> (8 * (j & 3)));
       }
     }
   }
@@ -366,8 +418,8 @@ template <int K>
 __global__ void __launch_bounds__(kThreads, per_sm_most(K)) adamw_kernel(const Tensor *__restrict__ tensors,
                                                                     const Chunk *__restrict__ chunks, int64_t nchunks,
                                                                     const Hyper hy, moe_adamw_state *st, int bump) {
-  constexpr int kPasses = kChunk / (kThreads * kVec);
   constexpr bool kF8 = K >= F32_F8;
+  constexpr int kChunk = chunk_of(K), kPasses = kChunk / (kThreads * kVec);
   const int lane = threadIdx.x & 31;
   const int64_t step = st->step + 1;
   Coef co;
@@ -394,10 +446,15 @@ __global__ void __launch_bounds__(kThreads, per_sm_most(K)) adamw_kernel(const T
     const int64_t first = (int64_t)ch.index * kChunk + threadIdx.x * kVec;
     Raw8<K> raw;
     if (t.aligned && (int64_t)(ch.index + 1) * kChunk <= t.n) {
+      constexpr int kAhead = kF8 ? kPasses : 1;   // passes whose loads are in flight together
 #pragma unroll 1
-      for (int pass = 0; pass < kPasses; ++pass) {
-        raw.load(t, first + pass * (kThreads * kVec));
-        update8<K, true>(t, raw, first + pass * (kThreads * kVec), kVec, hy, co, decay);
+      for (int pass = 0; pass < kPasses; pass += kAhead) {
+        Raw8<K> r[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) r[a].load(t, first + (pass + a) * (kThreads * kVec));
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+          update8<K, true>(t, r[a], first + (pass + a) * (kThreads * kVec), kVec, hy, co, decay);
       }
     } else {
 #pragma unroll 1
@@ -422,6 +479,11 @@ static int kind_of(const moe_adamw_tensor &t) {
   return base + (t.state == MOE_ADAMW_F8 ? 3 : 0);
 }
 
+static int64_t chunks_of(const moe_adamw_tensor &t) {
+  const int c = chunk_of(kind_of(t));
+  return t.n > 0 ? (t.n + c - 1) / c : 0;
+}
+
 static int check(const moe_adamw_tensor &t) {
   if (t.n < 0 || (t.dtype != MOE_F32 && t.dtype != MOE_BF16) || (t.state != MOE_ADAMW_F32 && t.state != MOE_ADAMW_F8))
     return MOE_ERR_INVALID_ARG;
@@ -433,7 +495,7 @@ static int check(const moe_adamw_tensor &t) {
   if (!is(t.p, es) || !is(t.g, es) || !is(t.m, ss) || !is(t.v, ss) || (t.master && !is(t.master, 4)))
     return MOE_ERR_INVALID_ARG;
   if (t.state == MOE_ADAMW_F8 && (!is(t.m_scale, 4) || !is(t.v_scale, 4))) return MOE_ERR_INVALID_ARG;
-  if ((t.n + kChunk - 1) / kChunk >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  if (chunks_of(t) >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -459,8 +521,7 @@ using namespace moe::adamw;
 extern "C" size_t moe_adamw_plan_size(const moe_adamw_tensor *tensors, int count) {
   if (count < 0 || (count > 0 && !tensors)) return 0;
   size_t chunks = 0;
-  for (int i = 0; i < count; ++i)
-    if (tensors[i].n > 0) chunks += (size_t)((tensors[i].n + kChunk - 1) / kChunk);
+  for (int i = 0; i < count; ++i) chunks += (size_t)chunks_of(tensors[i]);
   return sizeof(Header) + (size_t)count * sizeof(Tensor) + chunks * sizeof(Chunk);
 }
 
@@ -491,7 +552,7 @@ extern "C" int moe_adamw_plan(const moe_adamw_tensor *tensors, int count, void *
   for (int k = 0; k < KINDS; ++k) {
     for (int i = 0; i < count; ++i) {
       if (kind_of(tensors[i]) != k) continue;
-      const int64_t n = (tensors[i].n + kChunk - 1) / kChunk;
+      const int64_t n = chunks_of(tensors[i]);
       for (int64_t j = 0; j < n; ++j) *c++ = Chunk{i, (int32_t)j};
       h->chunks[k] += n;
     }

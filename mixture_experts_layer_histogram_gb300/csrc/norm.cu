@@ -26,6 +26,7 @@
 // added up by a second kernel in a fixed order, so they do not depend on timing. With a gate per
 // channel, dw_post and d_gate are both multiples of A = sum_t G y r, so one accumulator serves both.
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace moe {
 namespace norm {
@@ -37,30 +38,9 @@ constexpr size_t kRingMost = 200 * 1024;
 
 // Arithmetic on one lane of values: two fp32 at a time (f32x2 instructions) for rows of 16-byte vectors, one fp32,
 // or one fp64. At bf16 the instructions, not HBM, bound these kernels when each value takes its own.
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 pair(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void split(F2 a, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 add(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
+using moe::add;
+using moe::fma;
+using moe::mul;
 template <typename S> __device__ __forceinline__ S mul(S a, S b) { return a * b; }
 template <typename S> __device__ __forceinline__ S add(S a, S b) { return a + b; }
 __device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
