@@ -112,12 +112,15 @@ def exported_symbols():
     return list(_SIGS)
 
 
+_U8 = torch.uint8
+_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
 def dtype_code(t: torch.dtype) -> int:
-    if t == torch.float32:
-        return MOE_F32
-    if t == torch.bfloat16:
-        return MOE_BF16
-    raise TypeError(f"unsupported dtype {t}")
+    code = _CODES.get(t)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t}")
+    return code
 
 
 def _p(t):
@@ -130,13 +133,14 @@ def _p(t):
 
 # The current stream's handle without building a Stream object (0.1 us instead of 3 us per call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _s(stream):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -149,11 +153,10 @@ def _want(name, t, dtype, shape):
 
 def _ptr(name, t, dtype, shape):
     """The address of a tensor argument that _want accepts."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        _want(name, t, dtype, shape)
-    if not t.is_cuda:
-        raise ValueError("libmoe takes CUDA tensors only")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
+    _want(name, t, dtype, shape)
+    return _p(t)
 
 
 def _scale_bytes(rows, cols):
@@ -162,6 +165,8 @@ def _scale_bytes(rows, cols):
 
 def _bytes_at_least(name, t, n):
     """The address of a tensor of at least n bytes."""
+    if t.dtype is _U8 and t.numel() >= n and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
     if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{name}: a contiguous uint8 tensor of at least {n} bytes is needed, got {t.dtype} "
                          f"{tuple(t.shape)}")
@@ -417,27 +422,30 @@ def moe_fp4_scale_bytes(R, K):
     return int(lib().moe_fp4_scale_bytes(R, K))
 
 
-def _rows(x):
-    """A tensor [..., K] as its number of rows and K."""
-    K = x.shape[-1]
-    return (x.numel() // K if K else 0), K
+def _rows(shape):
+    """A shape [..., K] as its number of rows and K."""
+    K = shape[-1]
+    R = 1
+    for n in shape[:-1]:
+        R *= n
+    return R, K
 
 
 def moe_fp4_quantize(x, codes, scales, stream=None):
     """x [..., K] (rows in order) -> codes [..., K/2] uint8, scales [moe_fp4_scale_bytes(rows, K)] uint8."""
     shape, dt = x.shape, x.dtype
-    R, K = _rows(x)
+    R, K = _rows(shape)
     _ok("moe_fp4_quantize", lib().moe_fp4_quantize(
-        _ptr("x", x, dt, shape), dtype_code(dt), R, K, _ptr("codes", codes, torch.uint8, shape[:-1] + (K // 2,)),
+        _ptr("x", x, dt, shape), dtype_code(dt), R, K, _ptr("codes", codes, torch.uint8, (*shape[:-1], K // 2)),
         _bytes_at_least("scales", scales, _scale_bytes(R, K)), _s(stream)))
 
 
 def moe_fp4_dequantize(codes, scales, x, stream=None):
     """The values that codes and scales stand for, into x [..., K]."""
     shape, dt = x.shape, x.dtype
-    R, K = _rows(x)
+    R, K = _rows(shape)
     _ok("moe_fp4_dequantize", lib().moe_fp4_dequantize(
-        _ptr("codes", codes, torch.uint8, shape[:-1] + (K // 2,)),
+        _ptr("codes", codes, torch.uint8, (*shape[:-1], K // 2)),
         _bytes_at_least("scales", scales, _scale_bytes(R, K)), R, K, dtype_code(dt), _ptr("x", x, dt, shape), _s(stream)))
 
 
@@ -456,7 +464,7 @@ def moe_grouped_ffn_fwd_fp4(x_codes, x_scales, wgu_codes, wgu_scales, wd_codes, 
                             h_codes, h_scales, y_perm, ws, stream=None):
     """wgu_codes [E, 2f, d/2], wd_codes [E, d, f/2]; h_codes [rows_max, f/2] and h_scales are scratch."""
     E, d, f2 = wd_codes.shape
-    R, f, u8 = x_codes.shape[0], 2 * f2, torch.uint8
+    R, f, u8 = x_codes.shape[0], 2 * f2, _U8
     _ok("moe_grouped_ffn_fwd_fp4", lib().moe_grouped_ffn_fwd_fp4(
         _ptr("x_codes", x_codes, u8, (R, d // 2)), _bytes_at_least("x_scales", x_scales, _scale_bytes(R, d)),
         _ptr("wgu_codes", wgu_codes, u8, (E, 2 * f, d // 2)),

@@ -16,7 +16,7 @@ from . import _lib as L
 
 def fp4_quantize(x, stream=None):
     """MXFP4 codes [..., K/2] and scales of x [..., K]."""
-    R, K = L._rows(x)
+    R, K = L._rows(x.shape)
     codes = torch.empty(x.shape[:-1] + (K // 2,), dtype=torch.uint8, device=x.device)
     scales = torch.empty(L.moe_fp4_scale_bytes(R, K), dtype=torch.uint8, device=x.device)
     L.moe_fp4_quantize(x, codes, scales, stream)
