@@ -36,32 +36,19 @@
 // warps 2..9 epilogue (two warps per 32-lane TMEM quarter). The grid is persistent, at most one CTA per SM; every
 // wait is bounded (0.2 s), on timeout the kernel records MOE_ERR_DEVICE_TIMEOUT in the workspace status word and
 // leaves.
-#include <cuda.h>
-
 #include <atomic>
 
-#include "common.cuh"
-#include "fp4.cuh"
-#include "tc_ptx.cuh"
-#include "tma_host.cuh"
+#include "fp4_gemm.cuh"
 
 namespace moe {
 namespace tc {
 namespace fp4g {
 
-enum Kind { GATEUP = 0, DOWN = 1 };
-
 constexpr int MT = 256;                       // grouped rows per tile, MC of them per CTA
 constexpr int MC = 128;
 constexpr int NT = 256;                       // weight rows per tile, half of them loaded by each CTA
-constexpr int KS = 256;                       // values of K per ring stage (128 bytes of codes: the swizzle span)
 constexpr int A_BYTES = MC * 128, B_BYTES = NT / 2 * 128;
-constexpr int SF_BYTES = (KS / 128) * 512;    // scales of 128 rows per stage
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 3 * SF_BYTES;
-constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int MAX_E = MOE_MAX_EXPERTS;
-
 // GATEUP writes codes straight from registers and gives all shared memory to the ring. DOWN stages its tile of y (64 KB
 // per CTA) in 32 KB, one block of 32 x 64 per epilogue warp, and has five stages left; with 64 KB and four stages the
 // whole FFN took 246 instead of 244 us at 8192 tokens, with plain 16-byte stores 250.
@@ -79,20 +66,6 @@ static_assert(STAGE_BYTES % 1024 == 0, "ring stages keep the swizzle atoms' 1024
 constexpr uint32_t ACC1 = 208;                // first column of the second accumulator
 constexpr uint32_t SF_COL = 464;              // scales: two sets of 8 (tokens) + 16 (weights) columns
 constexpr uint32_t SF_SET = 24;
-
-struct Params {
-  const int32_t *tile_offsets, *offsets;
-  WsHeader *hdr;
-  int E;
-  int n_ft;               // feature tiles per expert
-  int num_kb;             // ring stages per tile
-  int w_rows_e;           // weight rows per expert
-  int w_second;           // rows from a tile's first 128 weight rows to its second (GATEUP: f, DOWN: 128)
-  int w_step;             // weight rows from one feature tile to the next
-  uint8_t *h, *h_scales;  // GATEUP
-  int f;
-  int64_t rows_max;
-};
 
 struct Tile {
   int e, ft, start, valid;   // expert, feature tile, first grouped row, routed rows (1..256)
@@ -118,29 +91,6 @@ struct Walker {
   }
 };
 
-// Instruction descriptor, kind::mxf4: A and B E2M1, scales E8M0, M = 256 (the pair), N = 256, both K-major; sf = the
-// first of the two scale bytes (0 or 2) of each operand.
-__device__ __forceinline__ uint32_t idesc(uint32_t sf) {
-  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NT >> 3) << 17) | (1u << 23) | ((uint32_t)(MT >> 4) << 24) |
-         (sf << 29);
-}
-__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t sfa, uint32_t sfb,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(ad), "l"(bd), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate));
-}
-// 512 bytes of scales (32 rows of 16 bytes) to four TMEM columns, repeated in each 32-lane quarter; each CTA of
-// the pair from its own shared memory to its own TMEM.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc));
-}
-// Shared-memory descriptor without swizzle: core matrices of 8 rows x 16 bytes, 128 bytes apart.
-__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
-}
 // Arrival (without release) on a barrier that may lie in the peer CTA. Announces that TMEM columns have been read:
 // tcgen05.wait::ld has completed the reads and no memory is handed over. A releasing arrival would first
 // wait for the warp's earlier global stores: 1300 to 3500 cycles in every tile here, with the tensor cores idle.
@@ -188,29 +138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmSB)) : "memory");
   }
-  if (warp == 0) {   // ttoff = exclusive scan of the token tiles per expert, ceil(rows / 128)
-    int c[8], sum = 0;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int e = lane * 8 + q;
-      c[q] = e < p.E ? (p.offsets[e + 1] - p.offsets[e] + MT - 1) / MT : 0;
-      sum += c[q];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += v;
-    }
-    int run = incl - sum;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int e = lane * 8 + q;
-      if (e < p.E) ttoff[e] = run;
-      run += c[q];
-    }
-    if (lane == 31) ttoff[p.E] = incl;
-  }
+  if (warp == 0) scan_tiles(p, MT, lane, ttoff);
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                  "r"(512u)
@@ -307,13 +235,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const uint32_t sfa = tmem_base + SF_COL + (uint32_t)set * SF_SET, sfb = sfa + 8;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {   // 128 values of K each
-            copy_scales(sfa + 4 * h, desc_s0 + so + (uint32_t)((h * 512) >> 4));
-            copy_scales(sfb + 8 * h, desc_s0 + so + (uint32_t)((SF_BYTES + h * 512) >> 4));
-            copy_scales(sfb + 8 * h + 4, desc_s0 + so + (uint32_t)((2 * SF_BYTES + h * 512) >> 4));
+            copy_scales<2>(sfa + 4 * h, desc_s0 + so + (uint32_t)((h * 512) >> 4));
+            copy_scales<2>(sfb + 8 * h, desc_s0 + so + (uint32_t)((SF_BYTES + h * 512) >> 4));
+            copy_scales<2>(sfb + 8 * h + 4, desc_s0 + so + (uint32_t)((2 * SF_BYTES + h * 512) >> 4));
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
               const uint32_t koff = (uint32_t)((2 * h + kk) * 32) >> 4;
-              mma_mxf4(d, desc_a0 + so + koff, desc_b0 + so + koff, idesc(2u * kk), sfa + 4 * h, sfb + 8 * h,
+              mma_mxf4<2>(d, desc_a0 + so + koff, desc_b0 + so + koff, idesc(MT, NT, 2u * kk), sfa + 4 * h, sfb + 8 * h,
                        (kb | h | kk) != 0 ? 1u : 0u);
             }
           }
@@ -443,36 +371,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-// 2D codes [rows, bytes per row], boxes of 128 bytes x box_rows rows, 128-byte swizzle.
-static bool codes_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {row_bytes, rows};
-  cuuint64_t strides[1] = {row_bytes};
-  cuuint32_t box[2] = {128, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Scales of [rows, K] (rows, K multiples of 128) as 32-bit words [rows / 128, K]: a box is the 1024 bytes of one stage.
-static bool scales_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t k) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {k, rows / 128};
-  cuuint64_t strides[1] = {k * 4};
-  cuuint32_t box[2] = {SF_BYTES / 4, 1};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct Maps {
-  CUtensorMap a, a32, b, sa, sb, c;
-};
-
 // The kernel's dynamic shared memory limit, raised once per device (the call costs a host microsecond).
 template <int K> static bool smem_allowed() {
   static std::atomic<uint64_t> done{0};
@@ -486,6 +384,8 @@ template <int K> static bool smem_allowed() {
   if (dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
   return true;
 }
+
+constexpr int kFewRows = 48;
 
 template <int K>
 static int launch(const Maps &m, const Params &p, cudaStream_t s) {
@@ -531,7 +431,13 @@ extern "C" int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales
   p.hdr = static_cast<WsHeader *>(ws);
   p.E = E;
   p.rows_max = rows_max;
+  p.d = d;
   p.f = f;
+  p.y = (__nv_bfloat16 *)y_perm;
+  // Which kernels: by the routed rows per expert, at most rows_max / E less the padding. From tokens to combined output
+  // at d = 2048, E = 64, k = 8, f = 1024, those for few rows against these: 0.1 rows per expert 24.3 and 26.2 us, 1 row
+  // 45.1 and 48.6, 8 rows 58.6 and 62.5, 42 rows 65.4 and 67.9, 64 rows 68.9 and 67.5, 128 rows 88 and 70.
+  const bool few = rows_max / E - (MOE_GROUP_ROWS - 1) <= kFewRows;
 
   if (!codes_map(&m.a, x_codes, rows_max, d / 2, MC) || !codes_map(&m.a32, x_codes, rows_max, d / 2, 32) ||
       !codes_map(&m.b, wgu_codes, (uint64_t)E * 2 * f, d / 2, 128) || !scales_map(&m.sa, x_scales, rows_max, d) ||
@@ -545,7 +451,7 @@ extern "C" int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales
   p.w_step = 128;
   p.h = (uint8_t *)h_codes;
   p.h_scales = (uint8_t *)h_scales;
-  int rc = launch<GATEUP>(m, p, s);
+  int rc = few ? few_gateup(m, p, s) : launch<GATEUP>(m, p, s);
   if (rc) return rc;
 
   if (!codes_map(&m.a, h_codes, rows_max, f / 2, MC) || !codes_map(&m.a32, h_codes, rows_max, f / 2, 32) ||
@@ -557,5 +463,5 @@ extern "C" int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales
   p.w_rows_e = d;
   p.w_second = 128;
   p.w_step = NT;
-  return launch<DOWN>(m, p, s);
+  return few ? few_down(m, p, s) : launch<DOWN>(m, p, s);
 }
