@@ -424,8 +424,6 @@ int moe_permute_fp4(const void *x, int dtype, int T, int d, int k, int E, const 
  *   y_perm                [rows_max, d] bf16: h Wd^T over the values that h_codes stand for
  * Products run on the block-scaled tensor cores with fp32 accumulation; h is quantised from fp32. Requires
  * d % 256 == 0 and f % 256 == 0. Padding rows come out as zeros. ws: as for moe_grouped_ffn_fwd with MOE_BF16.
- * The weights, offsets and tile_offsets may be read before the kernel launched just before this call has ended, if that
- * kernel allows programmatic dependents to start early (moe_permute_fp4's does): they must be older than that kernel.
  * A NaN or an infinity in a token makes that token's rows NaN; in the weights, the outputs that they enter.
  */
 int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales, const void *wgu_codes, const void *wgu_scales,

@@ -25,12 +25,12 @@
 // of the weights, which at such sizes are the traffic. Rows past the routed ones are not loaded where a box of
 // 32 rows can be spared; their lanes hold products of stale codes, which the epilogue replaces with zeros.
 //
-// Both kernels are launched as programmatic dependents, GATEUP of the permutation and DOWN of GATEUP (and the
-// combine after DOWN is one, too): a CTA sets up
-// and its producer brings the first tile's weights and their scales while the kernel before still runs, then
-// waits for that kernel before it touches the tokens or writes anything. The routing (offsets) and the weights
-// are older than the kernel before: of the kernels that let a successor start early, moe_permute_fp4's starts
-// after all that precedes it has ended, and GATEUP and DOWN end after what precedes them.
+// Both kernels are launched as programmatic dependents (and the combine after DOWN is one, too): they may start while the
+// kernel before them runs. What that one writes can be read only after the wait for it, and GATEUP may follow any
+// kernel, so until then it sets up and asks for its first tile's weights in L2, by offsets that may yet change: a hint
+// that stays within the weights whatever the offsets hold. After the wait it reads the offsets again, and lets DOWN start.
+// DOWN thus finds offsets and weights final and brings its first tile's weights at once; it waits for GATEUP before it
+// touches h or writes anything.
 //
 // Warp roles in both CTAs: warp 0 producer (TMA), warp 1 TMEM allocation and, in the leader, MMA issue,
 // warps 2..9 epilogue (two warps per 32-lane TMEM quarter). The grid is persistent, at most one CTA per SM; every
@@ -58,7 +58,7 @@ template <int K> struct Cfg {
   static constexpr int NBUF = K == GATEUP ? 0 : 1;           // per epilogue warp
   static constexpr int EPI_BYTES = EPI_WARPS * NBUF * BUF_BYTES;
   static constexpr int NBARS = 2 * STAGES + 3;
-  static constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 8 * NBARS + 16 + (MAX_E + 1) * 4;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 8 * NBARS + 16 + (int)sizeof(Plan);
   static_assert(SMEM <= 232448, "MXFP4 GEMM shared memory exceeds 227 KB");
 };
 static_assert(STAGE_BYTES % 1024 == 0, "ring stages keep the swizzle atoms' 1024-byte alignment");
@@ -66,30 +66,6 @@ static_assert(STAGE_BYTES % 1024 == 0, "ring stages keep the swizzle atoms' 1024
 constexpr uint32_t ACC1 = 208;                // first column of the second accumulator
 constexpr uint32_t SF_COL = 464;              // scales: two sets of 8 (tokens) + 16 (weights) columns
 constexpr uint32_t SF_SET = 24;
-
-struct Tile {
-  int e, ft, start, valid;   // expert, feature tile, first grouped row, routed rows (1..256)
-};
-
-// One pair's tiles in order: first, first + step, ...; tile = token tile gt * n_ft + feature tile.
-struct Walker {
-  int tile, step, num;
-  int e;
-  __device__ __forceinline__ Walker(int first, int step_, int n) : tile(first), step(step_), num(n), e(0) {}
-  __device__ __forceinline__ bool next(Tile &t, const Params &p, const int *ttoff) {
-    if (tile >= num) return false;
-    const int gt = tile / p.n_ft;
-    t.ft = tile - gt * p.n_ft;
-    while (e + 1 < p.E && ttoff[e + 1] <= gt) ++e;
-    const int i = gt - ttoff[e];
-    const int c = p.offsets[e + 1] - p.offsets[e];
-    t.e = e;
-    t.start = p.tile_offsets[e] * MC + i * MT;
-    t.valid = min(MT, c - i * MT);
-    tile += step;
-    return true;
-  }
-};
 
 // Arrival (without release) on a barrier that may lie in the peer CTA. Announces that TMEM columns have been read:
 // tcgen05.wait::ld has completed the reads and no memory is handed over. A releasing arrival would first
@@ -113,7 +89,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   // bars: full[STAGES], empty[STAGES], tfull, tdrain (the shared columns have been read), mma_done
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + C::NBARS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-  int *ttoff = reinterpret_cast<int *>(tmem_holder + 4);
+  Plan &plan = *reinterpret_cast<Plan *>(tmem_holder + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
@@ -124,7 +100,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   const uint32_t tfull_bar = bar0 + 8u * (2 * STAGES), tdrain_bar = tfull_bar + 8u, mma_done_bar = tfull_bar + 16u;
 
-  start_next();
+  if (K == DOWN) start_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);
@@ -138,7 +114,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmSB)) : "memory");
   }
-  if (warp == 0) scan_tiles(p, MT, lane, ttoff);
+  const int cluster_id = blockIdx.x >> 1, num_clusters = gridDim.x >> 1;
+  if (warp == 0) {
+    make_plan<MT>(p, lane, plan);
+    if (K == GATEUP) {
+      __syncwarp();
+      Walker<MT> walk(cluster_id, num_clusters, p, plan);
+      Tile t;
+      if (walk.next(t, p, plan) && elect_one()) {
+        const int w0 = t.e * p.w_rows_e + t.ft * p.w_step + (leader ? 0 : p.w_second);
+        for (int kb = 0; kb < min(p.num_kb, STAGES); ++kb) {
+          prefetch_2d(&tmB, kb * 128, w0);
+          prefetch_2d(&tmSB, kb * (SF_BYTES / 4), w0 / 128);
+        }
+      }
+      __syncwarp();
+      wait_previous();
+      make_plan<MT>(p, lane, plan);
+    }
+  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                  "r"(512u)
@@ -146,21 +140,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
-  cluster_sync();   // both CTAs: barriers initialised, ttoff written, TMEM allocated
+  cluster_sync();   // both CTAs: barriers initialised, plan made, TMEM allocated
+  if (K == GATEUP) start_next();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int num_tiles = ttoff[p.E] * p.n_ft;
-  const int cluster_id = blockIdx.x >> 1, num_clusters = gridDim.x >> 1;
   // routed rows of a tile among a CTA's 128, and the 32-row boxes that hold them (4: one box of 128)
   auto rows_of = [](const Tile &t, int r) { return min(MC, max(0, t.valid - MC * r)); };
   auto boxes_of = [](int rows) { return rows > MC / 2 ? 4 : (rows + 31) / 32; };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer (both CTAs)
-    int stage = 0, fills = 0, early = 0;
+    int stage = 0, fills = 0, early = -1;
     uint32_t phase = 0;
-    bool ok = true, waited = false;
-    // one stage's weights and scales; the tokens and theirs
+    bool ok = true;
+    // one stage's weights and scales
     auto load_weights = [&](const Tile &t, int kb, int st) {
       const uint32_t sB = sbase + st * STAGE_BYTES + A_BYTES, sS = sB + B_BYTES, fb = mapa_shared(full_bar(st), 0);
       const int w0 = t.e * p.w_rows_e + t.ft * p.w_step, w1 = w0 + p.w_second;
@@ -172,38 +165,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tma_load_2d_pair(sS + SF_BYTES, &tmSB, kb * (SF_BYTES / 4), w0 / 128, fb);
       tma_load_2d_pair(sS + 2 * SF_BYTES, &tmSB, kb * (SF_BYTES / 4), w1 / 128, fb);
     };
-    auto load_tokens = [&](const Tile &t, int kb, int st) {
-      const uint32_t sA = sbase + st * STAGE_BYTES, fb = mapa_shared(full_bar(st), 0);
-      const int arow = t.start + MC * rank, boxes = boxes_of(rows_of(t, rank));
-      if (boxes == 4) {
-        tma_load_2d_pair(sA, &tmA, kb * 128, arow, fb);
-      } else {
-        for (int b = 0; b < boxes; ++b) tma_load_2d_pair(sA + b * (A_BYTES / 4), &tmA32, kb * 128, arow + 32 * b, fb);
-      }
-      if (boxes) tma_load_2d_pair(sA + A_BYTES + B_BYTES, &tmSA, kb * (SF_BYTES / 4), arow / 128, fb);
-    };
-    Walker walk(cluster_id, num_clusters, num_tiles);
-    for (Tile t; ok && walk.next(t, p, ttoff);) {
-      if (!waited) {   // the first tile: its stages' weights first, then wait for the kernel before
+    Walker<MT> walk(cluster_id, num_clusters, p, plan);
+    for (Tile t; ok && walk.next(t, p, plan);) {
+      if (K == DOWN && early < 0) {   // the first tile: its stages' weights first, then wait for GATEUP
         early = min(p.num_kb, STAGES);
         if (elect_one())
           for (int kb = 0; kb < early; ++kb) load_weights(t, kb, kb);
         __syncwarp();
         wait_previous();
-        waited = true;
       }
+      const int arow = t.start + MC * rank, boxes = boxes_of(rows_of(t, rank));
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!mbar_spin_cluster(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 41)) { ok = false; break; }
         if (elect_one()) {
           if (fills >= early) load_weights(t, kb, stage);
-          load_tokens(t, kb, stage);
+          const uint32_t sA = sbase + stage * STAGE_BYTES, fb = mapa_shared(full_bar(stage), 0);
+          if (boxes == 4) {
+            tma_load_2d_pair(sA, &tmA, kb * 128, arow, fb);
+          } else {
+            for (int b = 0; b < boxes; ++b) tma_load_2d_pair(sA + b * (A_BYTES / 4), &tmA32, kb * 128, arow + 32 * b, fb);
+          }
+          if (boxes) tma_load_2d_pair(sA + A_BYTES + B_BYTES, &tmSA, kb * (SF_BYTES / 4), arow / 128, fb);
         }
         __syncwarp();
         ++fills;
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
     }
-    if (!waited) wait_previous();
+    if (K == DOWN && early < 0) wait_previous();
     if (leader && *abort_flag) {
       // leave no copy in flight: wait (bounded) for the last fill of every stage; the peer, whose bytes arrive on
       // the same barriers, stays until the cluster meets below
@@ -222,8 +211,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     bool issued = false, ok = true;
     const uint64_t desc_a0 = sdesc(sbase, 16, 1024), desc_b0 = sdesc(sbase + A_BYTES, 16, 1024);
     const uint64_t desc_s0 = sf_desc(sbase + A_BYTES + B_BYTES);
-    Walker walk(cluster_id, num_clusters, num_tiles);
-    for (Tile t; ok && walk.next(t, p, ttoff); ++n) {
+    Walker<MT> walk(cluster_id, num_clusters, p, plan);
+    for (Tile t; ok && walk.next(t, p, plan); ++n) {
       if (n > 0 && !mbar_spin_cluster(tdrain_bar, (uint32_t)(n - 1) & 1u, abort_flag, p.hdr, 42)) break;
       tc_fence_after();
       const uint32_t d = tmem_base + ((n & 1) ? ACC1 : 0u);
@@ -269,8 +258,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t buf = smem_u32(epi_smem) + (uint32_t)(warp - 2) * (C::NBUF * C::BUF_BYTES);
     int n = 0;
-    Walker walk(cluster_id, num_clusters, num_tiles);
-    for (Tile t; walk.next(t, p, ttoff); ++n) {
+    Walker<MT> walk(cluster_id, num_clusters, p, plan);
+    for (Tile t; walk.next(t, p, plan); ++n) {
       if (!mbar_spin_cluster(tfull_bar, (uint32_t)n & 1u, abort_flag, p.hdr, 44)) break;
       tc_fence_after();
       const bool second = n & 1;

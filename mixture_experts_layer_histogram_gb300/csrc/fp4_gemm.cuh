@@ -94,15 +94,31 @@ inline bool scales_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Exclusive scan of the token tiles per expert, ceil(rows / tile_rows), into shared memory: ttoff[0..E]. One warp.
-__device__ __forceinline__ void scan_tiles(const Params &p, int tile_rows, int lane, int *ttoff) {
-  int c[8], sum = 0;
+// Fetch a box into L2 (a hint: nothing depends on what it reads or when).
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *m, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
+// The experts' rows, as tiles of TR, in shared memory.
+struct Plan {
+  int tiles[MAX_E + 1];      // token tiles before expert e
+  int first[MAX_E];          // its first grouped row / 128
+  uint16_t last[MAX_E];      // routed rows in its last tile (1..TR)
+};
+// Filled by one warp. The offsets are read from L2: the kernel may have started, and read them, before the kernel
+// that writes them had ended.
+template <int TR> __device__ __forceinline__ void make_plan(const Params &p, int lane, Plan &plan) {
+  int c[8], at[8], sum = 0;
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     const int e = lane * 8 + q;
-    c[q] = e < p.E ? (p.offsets[e + 1] - p.offsets[e] + tile_rows - 1) / tile_rows : 0;
-    sum += c[q];
+    c[q] = e < p.E ? __ldcg(p.offsets + e + 1) - __ldcg(p.offsets + e) : 0;
+    at[q] = e < p.E ? __ldcg(p.tile_offsets + e) : 0;
   }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) sum += (c[q] + TR - 1) / TR;
   int incl = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -112,12 +128,41 @@ __device__ __forceinline__ void scan_tiles(const Params &p, int tile_rows, int l
   int run = incl - sum;
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const int e = lane * 8 + q;
-    if (e < p.E) ttoff[e] = run;
-    run += c[q];
+    const int e = lane * 8 + q, n = (c[q] + TR - 1) / TR;
+    if (e < p.E) {
+      plan.tiles[e] = run;
+      plan.first[e] = at[q];
+      plan.last[e] = (uint16_t)(c[q] - (n - 1) * TR);
+    }
+    run += n;
   }
-  if (lane == 31) ttoff[p.E] = incl;
+  if (lane == 31) plan.tiles[p.E] = incl;
 }
+
+struct Tile {
+  int e, ft, start, valid;   // expert, feature tile, first grouped row, routed rows (1..TR)
+  bool last;                 // the expert's last rows
+};
+// One CTA's (or pair's) tiles in order: first, first + step, ...; tile = token tile * n_ft + feature tile. Whatever the
+// plan holds, e < E and ft < n_ft.
+template <int TR> struct Walker {
+  int tile, step, num, e;
+  __device__ __forceinline__ Walker(int first, int step_, const Params &p, const Plan &plan)
+      : tile(first), step(step_), num(plan.tiles[p.E] * p.n_ft), e(0) {}
+  __device__ __forceinline__ bool next(Tile &t, const Params &p, const Plan &plan) {
+    if (tile >= num) return false;
+    const int gt = tile / p.n_ft;
+    t.ft = tile - gt * p.n_ft;
+    while (e + 1 < p.E && plan.tiles[e + 1] <= gt) ++e;
+    const int i = gt - plan.tiles[e];
+    t.e = e;
+    t.start = plan.first[e] * 128 + i * TR;
+    t.last = gt + 1 == plan.tiles[e + 1];
+    t.valid = t.last ? plan.last[e] : TR;
+    tile += step;
+    return true;
+  }
+};
 
 struct Maps {
   CUtensorMap a, a32, b, sa, sb, c;   // token codes in boxes of 128 and of 32 rows, weight codes, scales, y (DOWN)

@@ -33,30 +33,9 @@ constexpr uint32_t SET = 128;                          // columns of one set: tw
 constexpr uint32_t SF_COL = 2 * SET, SF_SET = 24;      // scales: two sets of 8 + 8 (weights) + 8 (tokens) columns
 static_assert(STAGE_BYTES % 1024 == 0, "ring stages keep the swizzle atoms' 1024-byte alignment");
 template <int K> constexpr int smem_bytes() {
-  return STAGES * STAGE_BYTES + (K == GATEUP ? EPI_WARPS * BUF_BYTES : 0) + 1024 + 8 * NBARS + 16 + (MAX_E + 1) * 4;
+  return STAGES * STAGE_BYTES + (K == GATEUP ? EPI_WARPS * BUF_BYTES : 0) + 1024 + 8 * NBARS + 16 + (int)sizeof(Plan);
 }
 static_assert(smem_bytes<GATEUP>() <= 232448, "MXFP4 GEMM shared memory exceeds 227 KB");
-
-struct Tile {
-  int e, ft, start, valid, end;   // expert, feature tile, first grouped row, routed rows (1..64), end of the rows to write
-};
-struct Walker {                   // one CTA's tiles: first, first + step, ...; tile = token tile * n_ft + feature tile
-  int tile, step, num, e;
-  __device__ __forceinline__ Walker(int first, int step_, int n) : tile(first), step(step_), num(n), e(0) {}
-  __device__ __forceinline__ bool next(Tile &t, const Params &p, const int *ttoff) {
-    if (tile >= num) return false;
-    const int gt = tile / p.n_ft;
-    t.ft = tile - gt * p.n_ft;
-    while (e + 1 < p.E && ttoff[e + 1] <= gt) ++e;
-    const int i = gt - ttoff[e], c = p.offsets[e + 1] - p.offsets[e], left = c - i * TT;
-    t.e = e;
-    t.start = p.tile_offsets[e] * 128 + i * TT;
-    t.valid = min(TT, left);
-    t.end = left <= TT ? p.tile_offsets[e + 1] * 128 : t.start + TT;   // the last tile writes the padding's zeros
-    tile += step;
-    return true;
-  }
-};
 
 __device__ __forceinline__ void arrive_here(uint32_t bar) {   // TMEM has been read (wait::ld); no memory is handed over
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -83,7 +62,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // bars: full[STAGES], empty[STAGES], tfull[2], tempty[2], mma_done
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + NBARS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-  int *ttoff = reinterpret_cast<int *>(tmem_holder + 4);
+  Plan &plan = *reinterpret_cast<Plan *>(tmem_holder + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
@@ -93,7 +72,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
   const uint32_t mma_done_bar = bar0 + 8u * (2 * STAGES + 4);
 
-  start_next();
+  if (K == DOWN) start_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);
@@ -109,7 +88,26 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmW)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmSW)) : "memory");
   }
-  if (warp == 0) scan_tiles(p, TT, lane, ttoff);
+  if (warp == 0) {   // see fp4_gemm.cu
+    make_plan<TT>(p, lane, plan);
+    if (K == GATEUP) {
+      __syncwarp();
+      Walker<TT> walk(blockIdx.x, gridDim.x, p, plan);
+      Tile t;
+      if (walk.next(t, p, plan) && elect_one()) {
+        const int w0 = t.e * p.w_rows_e + t.ft * p.w_step, w1 = w0 + p.w_second;
+        for (int kb = 0; kb < min(p.num_kb, STAGES); ++kb) {
+          prefetch_2d(&tmW, kb * 128, w0);
+          prefetch_2d(&tmW, kb * 128, w1);
+          prefetch_2d(&tmSW, kb * (SF_BYTES / 4), w0 / 128);
+          prefetch_2d(&tmSW, kb * (SF_BYTES / 4), w1 / 128);
+        }
+      }
+      __syncwarp();
+      wait_previous();
+      make_plan<TT>(p, lane, plan);
+    }
+  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                  "r"(512u)
@@ -118,52 +116,47 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (K == GATEUP) start_next();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int num_tiles = ttoff[p.E] * p.n_ft;
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
-    int stage = 0, fills = 0, early = 0;
+    int stage = 0, fills = 0, early = -1;
     uint32_t phase = 0;
-    bool ok = true, waited = false;
-    auto boxes_of = [](const Tile &t) { return (t.valid + 31) / 32; };
+    bool ok = true;
     auto load_weights = [&](const Tile &t, int kb, int st) {
       const uint32_t sA = sbase + st * STAGE_BYTES, sS = sA + 2 * A_BYTES + B_BYTES, fb = full_bar(st);
       const int w0 = t.e * p.w_rows_e + t.ft * p.w_step, w1 = w0 + p.w_second;
-      mbar_expect_tx(fb, 2 * A_BYTES + (uint32_t)boxes_of(t) * (B_BYTES / 2) + 3 * SF_BYTES);
+      mbar_expect_tx(fb, 2 * A_BYTES + (uint32_t)((t.valid + 31) / 32) * (B_BYTES / 2) + 3 * SF_BYTES);
       tma_load_2d(sA, &tmW, kb * 128, w0, fb);
       tma_load_2d(sA + A_BYTES, &tmW, kb * 128, w1, fb);
       tma_load_2d(sS, &tmSW, kb * (SF_BYTES / 4), w0 / 128, fb);
       tma_load_2d(sS + SF_BYTES, &tmSW, kb * (SF_BYTES / 4), w1 / 128, fb);
     };
-    auto load_tokens = [&](const Tile &t, int kb, int st) {
-      const uint32_t sB = sbase + st * STAGE_BYTES + 2 * A_BYTES, fb = full_bar(st);
-      for (int b = 0; b < boxes_of(t); ++b) tma_load_2d(sB + b * (B_BYTES / 2), &tmT32, kb * 128, t.start + 32 * b, fb);
-      tma_load_2d(sB + B_BYTES + 2 * SF_BYTES, &tmST, kb * (SF_BYTES / 4), t.start / 128, fb);
-    };
-    Walker walk(blockIdx.x, gridDim.x, num_tiles);
-    for (Tile t; ok && walk.next(t, p, ttoff);) {
-      if (!waited) {   // the first tile: its stages' weights first, then wait for the kernel before
+    Walker<TT> walk(blockIdx.x, gridDim.x, p, plan);
+    for (Tile t; ok && walk.next(t, p, plan);) {
+      if (K == DOWN && early < 0) {   // the first tile: its stages' weights first, then wait for GATEUP
         early = min(p.num_kb, STAGES);
         if (elect_one())
           for (int kb = 0; kb < early; ++kb) load_weights(t, kb, kb);
         __syncwarp();
         wait_previous();
-        waited = true;
       }
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!mbar_spin_cluster(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 51)) { ok = false; break; }
         if (elect_one()) {
           if (fills >= early) load_weights(t, kb, stage);
-          load_tokens(t, kb, stage);
+          const uint32_t sB = sbase + stage * STAGE_BYTES + 2 * A_BYTES, fb = full_bar(stage);
+          for (int b = 0; 32 * b < t.valid; ++b) tma_load_2d(sB + b * (B_BYTES / 2), &tmT32, kb * 128, t.start + 32 * b, fb);
+          tma_load_2d(sB + B_BYTES + 2 * SF_BYTES, &tmST, kb * (SF_BYTES / 4), t.start / 128, fb);
         }
         __syncwarp();
         ++fills;
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
     }
-    if (!waited) wait_previous();
+    if (K == DOWN && early < 0) wait_previous();
     if (*abort_flag) {   // leave no copy in flight: wait (bounded) for the last fill of every stage
       const uint64_t t0 = global_ns();
       fills = max(fills, early);   // stages whose weights were asked for early never complete if they were not reached
@@ -180,8 +173,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool issued = false, ok = true;
     const uint64_t desc_a0 = sdesc(sbase, 16, 1024), desc_b0 = sdesc(sbase + 2 * A_BYTES, 16, 1024);
     const uint64_t desc_s0 = sf_desc(sbase + 2 * A_BYTES + B_BYTES);
-    Walker walk(blockIdx.x, gridDim.x, num_tiles);
-    for (Tile t; ok && walk.next(t, p, ttoff);) {
+    Walker<TT> walk(blockIdx.x, gridDim.x, p, plan);
+    for (Tile t; ok && walk.next(t, p, plan);) {
       if (!mbar_spin_cluster(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.hdr, 52)) break;
       tc_fence_after();
       const uint32_t d0 = tmem_base + (uint32_t)acc * SET, d1 = d0 + TT;
@@ -233,8 +226,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t buf = smem_u32(epi_smem) + (uint32_t)(warp - 2) * BUF_BYTES;
     int acc = 0;
     uint32_t acc_phase = 0;
-    Walker walk(blockIdx.x, gridDim.x, num_tiles);
-    for (Tile t; walk.next(t, p, ttoff);) {
+    Walker<TT> walk(blockIdx.x, gridDim.x, p, plan);
+    for (Tile t; walk.next(t, p, plan);) {
       if (!mbar_spin_cluster(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 54)) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + lane_off + (uint32_t)acc * SET + 32u * hh;
@@ -251,6 +244,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
       const int64_t row0 = (int64_t)t.start + 32 * hh;
+      // the rows to write: the expert's last tile writes its padding's zeros
+      const int64_t pad = ((int64_t)t.start + t.valid + 127) / 128 * 128;
+      const int64_t end = !t.last ? (int64_t)t.start + TT : (pad < p.rows_max ? pad : p.rows_max);
       if (K == GATEUP) {
         uint32_t mine = 0;                    // lane c: scale byte of token c
 #pragma unroll
@@ -271,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           q = make_uint4(two(lo.x, lo.y), two(lo.z, lo.w), two(hi.x, hi.y), two(hi.z, hi.w));
         }
         __syncwarp();                         // the buffer is read before the next tile writes it
-        for (int64_t row = row0 + lane; row < t.end && row < p.rows_max; row += TT) {   // further rows: padding
+        for (int64_t row = row0 + lane; row < end; row += TT) {   // further rows: padding
           *reinterpret_cast<uint4 *>(p.h + row * (p.f / 2) + t.ft * 64 + 16 * quarter) = q;
           p.h_scales[fp4::scale_word(row, t.ft, p.f / 128) + quarter] = (uint8_t)mine;
           q = make_uint4(0, 0, 0, 0);
@@ -287,7 +283,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         // zeros in the rows past the routed ones: four lanes per 64 bytes of a row
-        const int64_t end = t.end < p.rows_max ? t.end : p.rows_max;
         for (int64_t base = row0; base < end; base += TT) {
           for (int i = base == row0 ? cnt : 0; i < 32; i += 8) {
             const int rr = i + (lane >> 2);
