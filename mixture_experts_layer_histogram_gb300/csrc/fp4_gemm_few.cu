@@ -40,6 +40,11 @@ static_assert(smem_bytes<GATEUP>() <= 232448, "MXFP4 GEMM shared memory exceeds 
 __device__ __forceinline__ void arrive_here(uint32_t bar) {   // TMEM has been read (wait::ld); no memory is handed over
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ uint32_t e2m1(float v) {           // one code, in the low four bits
   uint32_t r;
   asm("{\n\t.reg .b8 b;\n\t"
@@ -48,6 +53,22 @@ __device__ __forceinline__ uint32_t e2m1(float v) {           // one code, in th
       : "=r"(r)
       : "f"(v), "f"(0.0f));
   return r;
+}
+
+// f(c, this lane's value of token c in the first accumulator, in the second) for the `count` (warp-uniform) tokens from
+// TMEM column `col` on. Eight at a time in a loop: unrolled over 32 tokens the code of a tile with one token is mostly
+// jumped over, and fetching it cost 1 us per kernel.
+template <typename F> __device__ __forceinline__ void for_tokens(uint32_t col, int count, F f) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < count; c0 += 8) {
+    uint32_t r0[8], r1[8];
+    tmem_ld8(col + c0, r0);
+    tmem_ld8(col + TT + c0, r1);
+    tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c0 + c < count) f(c0 + c, __uint_as_float(r0[c]), __uint_as_float(r1[c]));
+  }
 }
 
 // tmT32: token codes, 32 rows per box; tmW: weight codes, 128 rows; tmST, tmSW: scales.
@@ -85,8 +106,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmW)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmSW)) : "memory");
+    for (const CUtensorMap *m : {&tmW, &tmSW, &tmT32, &tmST})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
   }
   if (warp == 0) {   // see fp4_gemm.cu
     make_plan<TT>(p, lane, plan);
@@ -232,34 +253,27 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
       const uint32_t tacc = tmem_base + lane_off + (uint32_t)acc * SET + 32u * hh;
       const int cnt = min(32, max(0, t.valid - 32 * hh));
-      uint32_t r0[32], r1[32];
-      if (cnt > 0) {
-        tmem_ld32(tacc, r0);
-        tmem_ld32(tacc + TT, r1);
-        tmem_ld_wait();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_here(tempty_bar(acc));
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
+      auto drained = [&] {   // this warp has read its part of the accumulators
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_here(tempty_bar(acc));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      };
       const int64_t row0 = (int64_t)t.start + 32 * hh;
       // the rows to write: the expert's last tile writes its padding's zeros
       const int64_t pad = ((int64_t)t.start + t.valid + 127) / 128 * 128;
       const int64_t end = !t.last ? (int64_t)t.start + TT : (pad < p.rows_max ? pad : p.rows_max);
       if (K == GATEUP) {
         uint32_t mine = 0;                    // lane c: scale byte of token c
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          if (c < cnt) {
-            const float a = __uint_as_float(r0[c]), h = a * __uint_as_float(r1[c]) * sigmoidf_(a);
-            const uint32_t byte = fp4::scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu));
-            const uint32_t code = byte == 255u ? 0u : e2m1(h * fp4::inv_scale(byte));
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(buf + 32u * c + lane), "r"(code) : "memory");
-            if (lane == c) mine = byte;
-          }
-        }
-        __syncwarp();
+        for_tokens(tacc, cnt, [&](int c, float a, float b) {
+          const float h = a * b * sigmoidf_(a);
+          const uint32_t byte = fp4::scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu));
+          const uint32_t code = byte == 255u ? 0u : e2m1(h * fp4::inv_scale(byte));
+          asm volatile("st.shared.u8 [%0], %1;" ::"r"(buf + 32u * c + lane), "r"(code) : "memory");
+          if (lane == c) mine = byte;
+        });
+        drained();
         uint4 q = make_uint4(0, 0, 0, 0);     // lane c: the 32 codes of token c
         if (lane < cnt) {
           const uint4 lo = ld_shared_v4(buf + 32u * lane), hi = ld_shared_v4(buf + 32u * lane + 16u);
@@ -275,13 +289,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       } else {
         __nv_bfloat16 *y = p.y + row0 * p.d + t.ft * 256 + 32 * quarter;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          if (c < cnt) {
-            y[(int64_t)c * p.d + lane] = __float2bfloat16_rn(__uint_as_float(r0[c]));
-            y[(int64_t)c * p.d + 128 + lane] = __float2bfloat16_rn(__uint_as_float(r1[c]));
-          }
-        }
+        for_tokens(tacc, cnt, [&](int c, float v0, float v1) {
+          y[(int64_t)c * p.d + lane] = __float2bfloat16_rn(v0);
+          y[(int64_t)c * p.d + 128 + lane] = __float2bfloat16_rn(v1);
+        });
+        drained();
         // zeros in the rows past the routed ones: four lanes per 64 bytes of a row
         for (int64_t base = row0; base < end; base += TT) {
           for (int i = base == row0 ? cnt : 0; i < 32; i += 8) {
