@@ -150,7 +150,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer (both CTAs)
-    int stage = 0, fills = 0, early = -1;
+    int stage = 0, fills = 0;
     uint32_t phase = 0;
     bool ok = true;
     // one stage's weights and scales
@@ -165,39 +165,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tma_load_2d_pair(sS + SF_BYTES, &tmSB, kb * (SF_BYTES / 4), w0 / 128, fb);
       tma_load_2d_pair(sS + 2 * SF_BYTES, &tmSB, kb * (SF_BYTES / 4), w1 / 128, fb);
     };
+    auto load_tokens = [&](const Tile &t, int kb, int st) {
+      const uint32_t sA = sbase + st * STAGE_BYTES, fb = mapa_shared(full_bar(st), 0);
+      const int arow = t.start + MC * rank, boxes = boxes_of(rows_of(t, rank));
+      if (boxes == 4) {
+        tma_load_2d_pair(sA, &tmA, kb * 128, arow, fb);
+      } else {
+        for (int b = 0; b < boxes; ++b) tma_load_2d_pair(sA + b * (A_BYTES / 4), &tmA32, kb * 128, arow + 32 * b, fb);
+      }
+      if (boxes) tma_load_2d_pair(sA + A_BYTES + B_BYTES, &tmSA, kb * (SF_BYTES / 4), arow / 128, fb);
+    };
     Walker<MT> walk(cluster_id, num_clusters, p, plan);
     for (Tile t; ok && walk.next(t, p, plan);) {
-      if (K == DOWN && early < 0) {   // the first tile: its stages' weights first, then wait for GATEUP
-        early = min(p.num_kb, STAGES);
-        if (elect_one())
-          for (int kb = 0; kb < early; ++kb) load_weights(t, kb, kb);
+      int kb = 0;
+      if (fills == 0) {   // the first tile: the ring is empty. DOWN: the weights, then wait for GATEUP
+        fills = kb = min(p.num_kb, STAGES);
+        if (elect_one()) {
+          for (int i = 0; i < kb; ++i) {
+            load_weights(t, i, i);
+            if (K == GATEUP) load_tokens(t, i, i);
+          }
+        }
         __syncwarp();
-        wait_previous();
+        if (K == DOWN) {
+          wait_previous();
+          if (elect_one())
+            for (int i = 0; i < kb; ++i) load_tokens(t, i, i);
+          __syncwarp();
+        }
+        if (kb < STAGES) {
+          stage = kb;
+        } else {
+          phase = 1;
+        }
       }
-      const int arow = t.start + MC * rank, boxes = boxes_of(rows_of(t, rank));
-      for (int kb = 0; kb < p.num_kb; ++kb) {
+      for (; kb < p.num_kb; ++kb) {
         if (!mbar_spin_cluster(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 41)) { ok = false; break; }
         if (elect_one()) {
-          if (fills >= early) load_weights(t, kb, stage);
-          const uint32_t sA = sbase + stage * STAGE_BYTES, fb = mapa_shared(full_bar(stage), 0);
-          if (boxes == 4) {
-            tma_load_2d_pair(sA, &tmA, kb * 128, arow, fb);
-          } else {
-            for (int b = 0; b < boxes; ++b) tma_load_2d_pair(sA + b * (A_BYTES / 4), &tmA32, kb * 128, arow + 32 * b, fb);
-          }
-          if (boxes) tma_load_2d_pair(sA + A_BYTES + B_BYTES, &tmSA, kb * (SF_BYTES / 4), arow / 128, fb);
+          load_weights(t, kb, stage);
+          load_tokens(t, kb, stage);
         }
         __syncwarp();
         ++fills;
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
     }
-    if (K == DOWN && early < 0) wait_previous();
+    if (K == DOWN && fills == 0) wait_previous();
     if (leader && *abort_flag) {
       // leave no copy in flight: wait (bounded) for the last fill of every stage; the peer, whose bytes arrive on
       // the same barriers, stays until the cluster meets below
       const uint64_t t0 = global_ns();
-      fills = max(fills, early);   // stages whose weights were asked for early never complete if they were not reached
       for (int i = 1; i <= STAGES && i <= fills; ++i) {
         const int f = fills - i;   // fill number f went to stage f % STAGES in ring round f / STAGES
         while (!mbar_try_wait(full_bar(f % STAGES), (uint32_t)(f / STAGES) & 1u) && global_ns() - t0 < kWaitLimitNs) {}

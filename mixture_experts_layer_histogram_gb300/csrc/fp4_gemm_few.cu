@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
-    int stage = 0, fills = 0, early = -1;
+    int stage = 0, fills = 0;
     uint32_t phase = 0;
     bool ok = true;
     auto load_weights = [&](const Tile &t, int kb, int st) {
@@ -155,32 +155,49 @@ __global__ void __launch_bounds__(THREADS, 1)
       tma_load_2d(sS, &tmSW, kb * (SF_BYTES / 4), w0 / 128, fb);
       tma_load_2d(sS + SF_BYTES, &tmSW, kb * (SF_BYTES / 4), w1 / 128, fb);
     };
+    auto load_tokens = [&](const Tile &t, int kb, int st) {
+      const uint32_t sB = sbase + st * STAGE_BYTES + 2 * A_BYTES, fb = full_bar(st);
+      for (int b = 0; 32 * b < t.valid; ++b) tma_load_2d(sB + b * (B_BYTES / 2), &tmT32, kb * 128, t.start + 32 * b, fb);
+      tma_load_2d(sB + B_BYTES + 2 * SF_BYTES, &tmST, kb * (SF_BYTES / 4), t.start / 128, fb);
+    };
     Walker<TT> walk(blockIdx.x, gridDim.x, p, plan);
     for (Tile t; ok && walk.next(t, p, plan);) {
-      if (K == DOWN && early < 0) {   // the first tile: its stages' weights first, then wait for GATEUP
-        early = min(p.num_kb, STAGES);
-        if (elect_one())
-          for (int kb = 0; kb < early; ++kb) load_weights(t, kb, kb);
+      int kb = 0;
+      if (fills == 0) {   // the first tile: the ring is empty. DOWN: the weights, then wait for GATEUP
+        fills = kb = min(p.num_kb, STAGES);
+        if (elect_one()) {
+          for (int i = 0; i < kb; ++i) {
+            load_weights(t, i, i);
+            if (K == GATEUP) load_tokens(t, i, i);
+          }
+        }
         __syncwarp();
-        wait_previous();
+        if (K == DOWN) {
+          wait_previous();
+          if (elect_one())
+            for (int i = 0; i < kb; ++i) load_tokens(t, i, i);
+          __syncwarp();
+        }
+        if (kb < STAGES) {
+          stage = kb;
+        } else {
+          phase = 1;
+        }
       }
-      for (int kb = 0; kb < p.num_kb; ++kb) {
+      for (; kb < p.num_kb; ++kb) {
         if (!mbar_spin_cluster(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 51)) { ok = false; break; }
         if (elect_one()) {
-          if (fills >= early) load_weights(t, kb, stage);
-          const uint32_t sB = sbase + stage * STAGE_BYTES + 2 * A_BYTES, fb = full_bar(stage);
-          for (int b = 0; 32 * b < t.valid; ++b) tma_load_2d(sB + b * (B_BYTES / 2), &tmT32, kb * 128, t.start + 32 * b, fb);
-          tma_load_2d(sB + B_BYTES + 2 * SF_BYTES, &tmST, kb * (SF_BYTES / 4), t.start / 128, fb);
+          load_weights(t, kb, stage);
+          load_tokens(t, kb, stage);
         }
         __syncwarp();
         ++fills;
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
     }
-    if (K == DOWN && early < 0) wait_previous();
+    if (K == DOWN && fills == 0) wait_previous();
     if (*abort_flag) {   // leave no copy in flight: wait (bounded) for the last fill of every stage
       const uint64_t t0 = global_ns();
-      fills = max(fills, early);   // stages whose weights were asked for early never complete if they were not reached
       for (int i = 1; i <= STAGES && i <= fills; ++i) {
         const int f = fills - i;   // fill number f went to stage f % STAGES in ring round f / STAGES
         while (!mbar_try_wait(full_bar(f % STAGES), (uint32_t)(f / STAGES) & 1u) && global_ns() - t0 < kWaitLimitNs) {}
