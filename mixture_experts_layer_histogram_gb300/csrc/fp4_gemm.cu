@@ -441,11 +441,12 @@ extern "C" int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales
   p.f = f;
   p.y = (__nv_bfloat16 *)y_perm;
   // Which kernels: by the routed rows per expert, at most rows_max / E less the padding. From tokens to combined output
-  // at d = 2048, E = 64, k = 8, f = 1024, those for few rows against these: 0.1 rows per expert 24.3 and 26.2 us, 1 row
-  // 45.1 and 48.6, 8 rows 58.6 and 62.5, 42 rows 65.4 and 67.9, 64 rows 68.9 and 67.5, 128 rows 88 and 70.
+  // at d = 2048, E = 64, k = 8, f = 1024, those for few rows against these: 0.1 rows per expert 20.7 and 24.8 us, 1 row
+  // 41.0 and 46.1, 8 rows 55.3 and 60.2, 42 rows 63.5 and 64.8, 64 rows 66.9 and 64.9, 128 rows 83.7 and 70.5.
   const bool few = rows_max / E - (MOE_GROUP_ROWS - 1) <= kFewRows;
 
-  if (!codes_map(&m.a, x_codes, rows_max, d / 2, MC) || !codes_map(&m.a32, x_codes, rows_max, d / 2, 32) ||
+  // (the kernels for few rows read tokens in boxes of 32 rows only and store y without a map)
+  if (!(few || codes_map(&m.a, x_codes, rows_max, d / 2, MC)) || !codes_map(&m.a32, x_codes, rows_max, d / 2, 32) ||
       !codes_map(&m.b, wgu_codes, (uint64_t)E * 2 * f, d / 2, 128) || !scales_map(&m.sa, x_scales, rows_max, d) ||
       !scales_map(&m.sb, wgu_scales, (uint64_t)E * 2 * f, d))
     return MOE_ERR_CUDA;
@@ -460,9 +461,9 @@ extern "C" int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales
   int rc = few ? few_gateup(m, p, s) : launch<GATEUP>(m, p, s);
   if (rc) return rc;
 
-  if (!codes_map(&m.a, h_codes, rows_max, f / 2, MC) || !codes_map(&m.a32, h_codes, rows_max, f / 2, 32) ||
+  if (!(few || codes_map(&m.a, h_codes, rows_max, f / 2, MC)) || !codes_map(&m.a32, h_codes, rows_max, f / 2, 32) ||
       !codes_map(&m.b, wd_codes, (uint64_t)E * d, f / 2, 128) || !scales_map(&m.sa, h_scales, rows_max, f) ||
-      !scales_map(&m.sb, wd_scales, (uint64_t)E * d, f) || !tc::make_map(&m.c, y_perm, rows_max, d, 32))
+      !scales_map(&m.sb, wd_scales, (uint64_t)E * d, f) || !(few || tc::make_map(&m.c, y_perm, rows_max, d, 32)))
     return MOE_ERR_CUDA;
   p.n_ft = d / NT;
   p.num_kb = f / KS;

@@ -259,3 +259,32 @@ def test_refusals():
     W = Fp4Weights.quantize(torch.randn(3, 512, 256, device="cuda"), torch.randn(2, 256, 256, device="cuda"))
     with pytest.raises(ValueError):                         # weights of unlike expert counts
         MoELayerFp4(4, 256, 2, 1, 256).forward(torch.randn(4, 256, device="cuda").bfloat16(), torch.randn(4, 2, device="cuda"), W)
+
+
+@pytest.mark.parametrize("T", [1, 96, 700])
+def test_ffn_right_after_what_writes_its_inputs(T):
+    """Offsets, weights and their scales written by the launches just before the call: the same result, bit for bit,
+    as with them in place long before. (Both sets of kernels: few rows per expert, and many.)"""
+    d, f, E, k = 512, 256, 4, 2
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, d, generator=g).to(torch.bfloat16).cuda()
+    logits = torch.randn(T, E, generator=g).cuda()
+    w = Fp4Weights.quantize((torch.randn(E, 2 * f, d, generator=g) * 0.05).cuda(), (torch.randn(E, d, f, generator=g) * 0.05).cuda())
+    layer = MoELayerFp4(T, d, E, k, f)
+    layer.forward(x, logits, w)
+    want = layer.y_perm.clone()
+    names = ("gate_up", "gate_up_scales", "down", "down_scales")
+    kept = [getattr(w, n).clone() for n in names] + [layer.offsets.clone(), layer.tile_offsets.clone()]
+    live = [getattr(w, n) for n in names] + [layer.offsets, layer.tile_offsets]
+    args = (layer.x_codes, layer.x_scales, *live[:4], layer.tile_offsets, layer.offsets, layer.h_codes, layer.h_scales,
+            layer.y_perm, layer.ws_ffn)
+    for last in range(len(live)):
+        for t in live:
+            t.zero_()
+        layer.y_perm.zero_()
+        L.moe_permute_fp4(x, k, E, layer.row_of_slot, layer.counts, kept[5], layer.x_codes, layer.x_scales)
+        for i in [j for j in range(len(live)) if j != last] + [last]:
+            live[i].copy_(kept[i])
+        L.moe_grouped_ffn_fwd_fp4(*args)
+        assert torch.equal(layer.y_perm, want), last
+    assert layer.status() == (0, 0)
