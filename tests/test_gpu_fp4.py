@@ -271,6 +271,7 @@ def test_ffn_right_after_what_writes_its_inputs(T):
     logits = torch.randn(T, E, generator=g).cuda()
     w = Fp4Weights.quantize((torch.randn(E, 2 * f, d, generator=g) * 0.05).cuda(), (torch.randn(E, d, f, generator=g) * 0.05).cuda())
     layer = MoELayerFp4(T, d, E, k, f)
+    layer.y_perm.zero_()        # rows past the experts' are not written
     layer.forward(x, logits, w)
     want = layer.y_perm.clone()
     names = ("gate_up", "gate_up_scales", "down", "down_scales")
