@@ -6,7 +6,7 @@
 // HBM-bound: every value is read and written once. The tensors are cut into chunks of 4096 (8-bit states: 8192)
 // values; a plan made on the host lists them, so a launch covers any number of tensors of any size and a block
 // finds its tensor with two dependent loads. The bias corrections come from the step count in device
-// memory, which the launch's last block advances: a captured step counts on when it is replayed.
+// memory, which the last block to have read it advances: a captured step counts on when it is replayed.
 //
 // 8-bit states: blocks of 256 consecutive values share one fp32 scale, max / 448; m is held as e4m3
 // codes of m / scale, v as e4m3 codes of sqrt(v) / scale (the root halves the range of exponents: e4m3
@@ -421,13 +421,15 @@ __global__ void __launch_bounds__(kThreads, per_sm_most(K)) adamw_kernel(const T
   constexpr bool kF8 = K >= F32_F8;
   constexpr int kChunk = chunk_of(K), kPasses = kChunk / (kThreads * kVec);
   const int lane = threadIdx.x & 31;
+  Chunk ahead = blockIdx.x < nchunks ? chunks[blockIdx.x] : Chunk{0, 0};
   const int64_t step = st->step + 1;
   Coef co;
   co.lr = st->lr;
   co.gs = st->grad_scale;
-  // Every thread of a block has read the state when the block arrives, so the block that arrives last may advance
-  // it at once. (Arriving at the kernel's end put a fence and an atomic behind the last stores.)
-  __syncthreads();
+  // Every thread of a block has read the step when the block arrives (the vote needs its value, so no load of it is
+  // still on its way), and the block that arrives last may advance it at once. (Arriving at the kernel's end put a fence
+  // and an atomic behind the last stores.)
+  __syncthreads_or(step <= 0);
   if (bump && threadIdx.x == 0 && atomicAdd(&st->arrived, 1u) == gridDim.x - 1) {
     st->arrived = 0;
     st->step = step;
@@ -437,7 +439,6 @@ __global__ void __launch_bounds__(kThreads, per_sm_most(K)) adamw_kernel(const T
   co.inv_root2 = 1.0f / sqrtf(bc2);
   co.t32 = (uint32_t)step;
 
-  Chunk ahead = blockIdx.x < nchunks ? chunks[blockIdx.x] : Chunk{0, 0};
   for (int64_t ci = blockIdx.x; ci < nchunks; ci += gridDim.x) {
     const Chunk ch = ahead;
     if (ci + gridDim.x < nchunks) ahead = chunks[ci + gridDim.x];
