@@ -349,13 +349,16 @@ int moe_norm_residual_bwd(const void *dout, const void *dn, const void *out, con
  * state type). With t the step count after this step and c = grad_scale, per value
  *   m = beta1 m + (1 - beta1) c g,  v = beta2 v + (1 - beta2) (c g)^2
  *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
- * computed in fp32 and written in place.
+ * computed in fp32 and written in place; 0 <= beta1, beta2 < 1, eps >= 2^-126.
  *   dtype   of p and g: MOE_F32 or MOE_BF16
  *   master  fp32 copy of a bf16 parameter, updated in its place (p is then its value rounded to nearest), or NULL
  *   state   MOE_ADAMW_F32: m, v fp32 [n].
  *           MOE_ADAMW_F8: m holds e4m3 codes of m / m_scale, v holds e4m3 codes of sqrt(v) / v_scale, one fp32
  *           scale (the block's largest magnitude / 448) per MOE_ADAMW_BLOCK consecutive values; m_scale, v_scale
  *           have ceil(n / MOE_ADAMW_BLOCK) entries. A block whose largest magnitude is below 1e-30 is held as zeros.
+ *           A root below 2^-18 of its block's largest may be held as zero while m is not (its next update is then
+ *           as large as lr m / eps), and a v below 2^-126 counts as zero: tensors whose blocks mix such
+ *           magnitudes belong in MOE_ADAMW_F32.
  * Values kept in few bits only (the e4m3 states, a bf16 parameter without a master) are rounded with a dither
  * that depends on the place in the tensor and on t: down after adding u / 2^b of a rounding step, where u is
  * the top b bits of (place * 2654435769 + t * 1640531535 + shift) mod 2^32 (b = 20 and shift 0 for m, shift

@@ -20,8 +20,9 @@ class AdamW:
                  masters=None, m=None, v=None, m_scale=None, v_scale=None, step=0):
         """params, grads: contiguous CUDA tensors, fp32 or bf16 (a gradient in its parameter's type).
         weight_decay: one value, or one per tensor. state: "f32", or "f8" (e4m3 codes with one fp32 scale per
-        256 values; v as the codes of its root). masters: True for fp32 copies of the bf16 parameters, or a list of
-        them (None for fp32 parameters). m, v, m_scale, v_scale, step: states to go on from (they are updated in place)."""
+        256 values; v as the codes of its root; not for tensors that mix gradients over 2^18 apart within 256
+        values). masters: True for fp32 copies of the bf16 parameters, or a list of them (None for fp32
+        parameters). m, v, m_scale, v_scale, step: states to go on from (they are updated in place)."""
         if state not in ("f32", "f8"):
             raise ValueError(f"state is 'f32' or 'f8', got {state!r}")
         params, grads = list(params), list(grads)
@@ -38,7 +39,9 @@ class AdamW:
         blocks = [-(-p.numel() // L.ADAMW_BLOCK) for p in params]
         if masters is True:
             masters = [p.float() if p.dtype == torch.bfloat16 else None for p in params]
-        self.masters = masters if masters is not None else [None] * len(params)
+        self.masters = list(masters) if masters is not None else [None] * len(params)
+        if len(self.masters) != len(params):
+            raise ValueError(f"{len(params)} parameters and {len(self.masters)} masters")
         self.m = self._states("m", m, held)
         self.v = self._states("v", v, held)
         self.m_scale = self._scales("m_scale", m_scale, blocks) if f8 else None

@@ -236,3 +236,25 @@ def test_refusals():
     with pytest.raises(L.MoeError):
         AdamW([p], [g], betas=(1.0, 0.9)).step()
     assert math.isfinite(p.sum().item())
+
+
+def test_subnormal_second_moment():
+    """Gradients of 1e-19 and an eps below them: v is about 1e-40, held in steps of 2^-149, so its root is off by at most
+    2^-150 / 1e-40 / 2 = 4e-6 and the update, lr in size, by that and a few 2^-22 (approximate root and
+    reciprocal): 1e-5."""
+    n = 5000
+    k = 1 + torch.arange(n, device="cuda") / n
+    p, g = torch.zeros(n, device="cuda"), 1e-19 * k
+    opt = AdamW([p], [g], lr=1e-3, betas=(0.9, 0.99), eps=1e-30, weight_decay=0.0)
+    opt.step()
+    m, v = 0.1 * g.double(), 0.01 * g.double() ** 2
+    exp = -1e-3 * (m / 0.1) / (torch.sqrt(v / 0.01) + 1e-30)
+    assert ((p.double() - exp).abs() <= 1e-5 * 1e-3).all()
+
+
+def test_refusals_of_masters_and_eps():
+    p = torch.zeros(64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        AdamW([p, p.clone()], [p.clone(), p.clone()], masters=[p.float()])
+    with pytest.raises(L.MoeError):
+        AdamW([p], [p.clone()], eps=1e-40).step()
