@@ -9,8 +9,9 @@
 // lane holds one output feature, a warp stores 64 consecutive bytes per token.
 //
 // With tokens as M (256 rows per pair, fp4_gemm.cu) a tile's MMAs take as long for one row as for 256. Measured (d = 2048,
-// E = 64, k = 8, f = 1024), GATEUP reads its 147 MB of weights in 33 us at 42 rows per expert (4.4 TB/s with launch and
-// last wave, about 6 TB/s while all CTAs run); the ring's depth and the L2 promotion do not matter there.
+// E = 64, k = 8, f = 1024), GATEUP reads its 147 MB of weights in 33-36 us at 42 rows per expert (4.1-4.4 TB/s with
+// launch and last wave, 5.4 TB/s while all CTAs run); the ring's depth, the L2 promotion, the order of K and smaller
+// tiles do not matter there.
 //
 // Two sets of accumulators (256 TMEM columns), scales behind them. A token tile that starts in the middle of a
 // 128-row scale tile finds its scales two TMEM columns further. Roles, waits and dependent launch as in fp4_gemm.cu.
