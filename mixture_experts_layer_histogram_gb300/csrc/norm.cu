@@ -824,7 +824,7 @@ extern "C" int moe_norm_bwd(const void *dn, const void *x, const void *w, const 
                             float eps, void *dx, void *dw, void *ws, size_t ws_bytes, moe_stream_t stream) {
   int rc = check_shape(T, d, dtype, eps);
   if (rc) return rc;
-  if (bad(dw) || (T > 0 && (bad(dn) || bad(x) || bad(w) || bad(dx) || (dx_in && bad(dx_in))))) return MOE_ERR_INVALID_ARG;
+  if (bad(dw) || bad(w) || (T > 0 && (bad(dn) || bad(x) || bad(dx) || (dx_in && bad(dx_in))))) return MOE_ERR_INVALID_ARG;
   BwdParams p{};
   p.dout = dx_in;
   p.dn = dn;

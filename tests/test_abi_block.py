@@ -103,3 +103,10 @@ def test_fp4_refusals(L):
     assert ffn(d=128) == -2 and ffn(f=384) == -2 and ffn(E=0) == -1 and ffn(E=300) == -1
     assert ffn(rows=rm + 1) == -1 and ffn(y=NULL) == -1 and ffn(w=NULL) == -1 and ffn(n=8) == -1 and ffn(w=ODD) == -1
     assert ffn(rows=0) == 0
+
+
+def test_norm_backward_without_rows_still_wants_its_weights(L):
+    """The kernel reads w before its first row, so a missing w is refused with T = 0 as well."""
+    ws = L.moe_norm_bwd_workspace_size(0, 64, 0)
+    assert L.moe_norm_bwd(NULL, NULL, NULL, NULL, 0, 64, 0, 1e-6, NULL, FAKE, FAKE, ws, NULL) == -1
+    assert L.moe_norm_bwd(NULL, NULL, ODD, NULL, 0, 64, 0, 1e-6, NULL, FAKE, FAKE, ws, NULL) == -1
