@@ -485,7 +485,7 @@ static int kind_of(const moe_adamw_tensor &t) {
 
 static int64_t chunks_of(const moe_adamw_tensor &t) {
   const int c = chunk_of(kind_of(t));
-  return t.n > 0 ? (t.n + c - 1) / c : 0;
+  return t.n > 0 ? (t.n - 1) / c + 1 : 0;
 }
 
 static int check(const moe_adamw_tensor &t) {

@@ -110,3 +110,11 @@ def test_norm_backward_without_rows_still_wants_its_weights(L):
     ws = L.moe_norm_bwd_workspace_size(0, 64, 0)
     assert L.moe_norm_bwd(NULL, NULL, NULL, NULL, 0, 64, 0, 1e-6, NULL, FAKE, FAKE, ws, NULL) == -1
     assert L.moe_norm_bwd(NULL, NULL, ODD, NULL, 0, 64, 0, 1e-6, NULL, FAKE, FAKE, ws, NULL) == -1
+
+
+def test_adamw_plan_of_too_many_values(L):
+    from mixture_experts_layer_histogram_gb300 import _lib
+    buf = (ctypes.c_int64 * 64)()
+    for n in ((1 << 63) - 1, 1 << 43):
+        a = _lib.AdamWTensor(p=4096, g=4096, m=4096, v=4096, n=n, dtype=0, state=0)
+        assert L.moe_adamw_plan(ctypes.byref(a), 1, buf, ctypes.sizeof(buf)) == -2
