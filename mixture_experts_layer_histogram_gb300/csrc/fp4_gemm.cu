@@ -450,7 +450,7 @@ extern "C" int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales
   p.y = (__nv_bfloat16 *)y_perm;
   // Which kernels: by the routed rows per expert, at most rows_max / E less the padding. From tokens to combined output
   // at d = 2048, E = 64, k = 8, f = 1024, those for few rows against these: 0.1 rows per expert 20.7 and 24.8 us, 1 row
-  // 41.0 and 46.1, 8 rows 55.3 and 60.2, 42 rows 63.5 and 64.8, 64 rows 66.9 and 64.9, 128 rows 83.7 and 70.5.
+  // 41.0 and 46.1, 8 rows 55.3 and 60.2, 42 rows 62.0 and 64.8, 64 rows 66.9 and 64.9, 128 rows 83.7 and 70.5.
   const bool few = rows_max / E - (MOE_GROUP_ROWS - 1) <= kFewRows;
 
   // (the kernels for few rows read tokens in boxes of 32 rows only and store y without a map)
