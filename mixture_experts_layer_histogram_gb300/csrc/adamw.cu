@@ -166,7 +166,7 @@ template <int K> struct Raw8 {
   static constexpr bool kF8 = K >= F32_F8, kF32 = K == F32_F32 || K == F32_F8;
   static constexpr bool kMaster = K == BF16_MASTER_F32 || K == BF16_MASTER_F8;
   uint4 g[kF32 ? 2 : 1], p[kF32 || kMaster ? 2 : 1], m[kF8 ? 1 : 2], v[kF8 ? 1 : 2];
-  float ms, vs;
+  float ms, vs;   // the block's scales (8-bit states)
   __device__ __forceinline__ void load(const Tensor &t, int64_t i0) {
     const int64_t es = kF32 ? 4 : 2;
     const uint8_t *gp = (const uint8_t *)t.g + i0 * es;
@@ -179,8 +179,6 @@ template <int K> struct Raw8 {
       const uint2 a = ld_once2((const uint8_t *)t.m + i0), b = ld_once2((const uint8_t *)t.v + i0);
       m[0] = make_uint4(a.x, a.y, 0, 0);
       v[0] = make_uint4(b.x, b.y, 0, 0);
-      ms = t.m_scale[i0 / kBlockQ];
-      vs = t.v_scale[i0 / kBlockQ];
     } else {
       const float *mp = (const float *)t.m + i0, *vp = (const float *)t.v + i0;
       m[0] = ld_once(mp);
@@ -197,9 +195,9 @@ __device__ __forceinline__ void unpack_f32x8(const uint4 &a, const uint4 &b, flo
 
 // Eight values of a tensor, the thread's own from i0 on. FULL: all eight are inside it, vector access is aligned and
 // `raw` holds them; otherwise the `live` ones inside are read one by one. All lanes of a warp take part (8-bit
-// states: its 256 values are one block).
+// states: its 256 values are one block, whose scales raw.ms and raw.vs are replaced by the new ones).
 template <int K, bool FULL>
-__device__ __forceinline__ void update8(const Tensor &t, const Raw8<K> &raw, int64_t i0, int live, const Hyper &hy,
+__device__ __forceinline__ void update8(const Tensor &t, Raw8<K> &raw, int64_t i0, int live, const Hyper &hy,
                                         const Coef &co, float decay) {
   constexpr bool kF8 = K >= F32_F8;
   constexpr bool kMaster = K == BF16_MASTER_F32 || K == BF16_MASTER_F8;
@@ -210,9 +208,7 @@ __device__ __forceinline__ void update8(const Tensor &t, const Raw8<K> &raw, int
   float *master = t.master + (kMaster ? i0 : 0);
   float *mf = (float *)t.m + (kF8 ? 0 : i0), *vf = (float *)t.v + (kF8 ? 0 : i0);
   uint8_t *m8 = (uint8_t *)t.m + (kF8 ? i0 : 0), *v8 = (uint8_t *)t.v + (kF8 ? i0 : 0);
-  const int64_t qb = i0 / kBlockQ;
   float g[kVec], p[kVec], m[kVec], v[kVec];
-  float ms = 0.0f, vs = 0.0f;
   if (FULL) {
     if (kF32) unpack_f32x8(raw.g[0], raw.g[kF32 ? 1 : 0], g);
     else unpack_bf16x8(raw.g[0], g);
@@ -221,17 +217,11 @@ __device__ __forceinline__ void update8(const Tensor &t, const Raw8<K> &raw, int
     if (kF8) {
       unpack_e4m3x8(make_uint2(raw.m[0].x, raw.m[0].y), m);
       unpack_e4m3x8(make_uint2(raw.v[0].x, raw.v[0].y), v);
-      ms = raw.ms;
-      vs = raw.vs;
     } else {
       unpack_f32x8(raw.m[0], raw.m[kF8 ? 0 : 1], m);
       unpack_f32x8(raw.v[0], raw.v[kF8 ? 0 : 1], v);
     }
   } else {
-    if (kF8) {
-      ms = t.m_scale[qb];
-      vs = t.v_scale[qb];
-    }
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       g[j] = p[j] = m[j] = v[j] = 0.0f;
@@ -271,7 +261,7 @@ __device__ __forceinline__ void update8(const Tensor &t, const Raw8<K> &raw, int
     // m and v are rounded at each operation (no fused multiply-add), and the largest root is the root of the
     // largest v, rounded to nearest: the scales then follow from the formulas alone, bit for bit, and a
     // block's largest value gets the code it should. The other roots may be approximate.
-    const F2 b1 = pair(hy.beta1, hy.beta1), b2 = pair(hy.beta2, hy.beta2), ms2 = pair(ms, ms), vs2 = pair(vs, vs);
+    const F2 b1 = pair(hy.beta1, hy.beta1), b2 = pair(hy.beta2, hy.beta2), ms2 = pair(raw.ms, raw.ms), vs2 = pair(raw.vs, raw.vs);
     const float kg1 = hy.omb1 * co.gs, kg2 = hy.omb2 * (co.gs * co.gs);
     const F2 c1 = pair(kg1, kg1), c2 = pair(kg2, kg2);
     F2 m2[kVec / 2];
@@ -362,10 +352,8 @@ __device__ __forceinline__ void update8(const Tensor &t, const Raw8<K> &raw, int
         }
       }
     }
-    if ((threadIdx.x & 31) == 0) {
-      t.m_scale[qb] = mk ? mx * (1.0f / 448.0f) : 0.0f;
-      t.v_scale[qb] = vk ? vx * (1.0f / 448.0f) : 0.0f;
-    }
+    raw.ms = mk ? mx * (1.0f / 448.0f) : 0.0f;
+    raw.vs = vk ? vx * (1.0f / 448.0f) : 0.0f;
     if (FULL) {
       *reinterpret_cast<uint2 *>(m8) = make_uint2(mc[0], mc[1]);
       *reinterpret_cast<uint2 *>(v8) = make_uint2(vc[0], vc[1]);
@@ -448,17 +436,32 @@ __global__ void __launch_bounds__(kThreads, per_sm_most(K)) adamw_kernel(const T
     const Tensor t = tensors[ch.tensor];
     const float decay = 1.0f - co.lr * t.weight_decay;
     const int64_t first = (int64_t)ch.index * kChunk + threadIdx.x * kVec;
-    Raw8<K> raw;
     if (t.aligned && (int64_t)(ch.index + 1) * kChunk <= t.n) {
-      constexpr int kAhead = kF8 ? kPasses : 1;   // passes whose loads are in flight together
+      if constexpr (kF8) {
+        // A warp takes kPasses blocks in a row, all their loads first. One lane each carries their scales, which are
+        // written together: single words, two for every 256 values, cost 37 us of 771 on 403M values.
+        const int64_t i0 = (int64_t)ch.index * kChunk + (threadIdx.x >> 5) * (kPasses * kBlockQ) + lane * kVec;
+        float *scales = (lane < kPasses ? t.m_scale : t.v_scale) + i0 / kBlockQ + (lane & (kPasses - 1));
+        float scale = lane < 2 * kPasses ? *scales : 0.0f;
+        Raw8<K> r[kPasses];
+#pragma unroll
+        for (int a = 0; a < kPasses; ++a) r[a].load(t, i0 + a * kBlockQ);
+#pragma unroll
+        for (int a = 0; a < kPasses; ++a) {
+          r[a].ms = __shfl_sync(0xffffffffu, scale, a);
+          r[a].vs = __shfl_sync(0xffffffffu, scale, kPasses + a);
+          update8<K, true>(t, r[a], i0 + a * kBlockQ, kVec, hy, co, decay);
+          if (lane == a) scale = r[a].ms;
+          if (lane == kPasses + a) scale = r[a].vs;
+        }
+        if (lane < 2 * kPasses) *scales = scale;
+      } else {
 #pragma unroll 1
-      for (int pass = 0; pass < kPasses; pass += kAhead) {
-        Raw8<K> r[kAhead];
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) r[a].load(t, first + (pass + a) * (kThreads * kVec));
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-          update8<K, true>(t, r[a], first + (pass + a) * (kThreads * kVec), kVec, hy, co, decay);
+        for (int pass = 0; pass < kPasses; ++pass) {
+          Raw8<K> raw;
+          raw.load(t, first + pass * (kThreads * kVec));
+          update8<K, true>(t, raw, first + pass * (kThreads * kVec), kVec, hy, co, decay);
+        }
       }
     } else {
 #pragma unroll 1
@@ -466,12 +469,21 @@ __global__ void __launch_bounds__(kThreads, per_sm_most(K)) adamw_kernel(const T
         const int64_t i0 = first + pass * (kThreads * kVec);
         const int64_t left = t.n - i0, warp_left = left + lane * kVec;
         if (warp_left <= 0) break;
+        Raw8<K> raw;
+        if (kF8) {
+          raw.ms = t.m_scale[i0 / kBlockQ];
+          raw.vs = t.v_scale[i0 / kBlockQ];
+        }
         // 8-bit states: the warp's 256 values are updated together
         if (t.aligned && (kF8 ? warp_left >= 32 * kVec : left >= kVec)) {
           raw.load(t, i0);
           update8<K, true>(t, raw, i0, kVec, hy, co, decay);
         } else {
           update8<K, false>(t, raw, i0, left >= kVec ? kVec : (left > 0 ? (int)left : 0), hy, co, decay);
+        }
+        if (kF8 && lane == 0) {
+          t.m_scale[i0 / kBlockQ] = raw.ms;
+          t.v_scale[i0 / kBlockQ] = raw.vs;
         }
       }
     }
