@@ -38,8 +38,8 @@ static_assert(kBlockQ == 32 * kVec, "a warp owns one block of an 8-bit state");
 // Kinds of tensors: parameter and gradient type, fp32 master copy, state.
 enum Kind { F32_F32 = 0, BF16_F32, BF16_MASTER_F32, F32_F8, BF16_F8, BF16_MASTER_F8, KINDS };
 
-// Values per chunk. fp32 states: two passes of 8 values per thread, one after the other. 8-bit states carry a
-// third of the bytes per value, so four passes' loads are issued before any of them is used.
+// Values per chunk. fp32 states: two passes of 8 values per thread. 8-bit states carry a third of the bytes per
+// value, so four passes' loads are issued before any of them is used.
 constexpr int chunk_of(int kind) { return kind >= F32_F8 ? 8192 : 4096; }
 
 struct Chunk {
@@ -146,14 +146,19 @@ template <typename T> __device__ __forceinline__ float load1(const T *p) {
   else return __bfloat162float(*p);
 }
 
-// Blocks per SM (they set the registers, and the grid of plans that fill the GPU). Measured on one layer's 403M
-// values (bf16): fp32 states with a master 1851 us at 2 blocks, 1922 at 3, 1956 at 4. 8-bit states, (values per
-// chunk, passes loaded ahead, blocks): (8192, 4, 2) 755 us, (8192, 4, 3) 795, (6144, 3, 3) 765, (4096, 2, 3) 800,
-// (4096, 1, 5) 903, (4096, 1, 3) 1063; one fp32 per instruction instead of two: (4096, 1, 5) 934. Sums that are
-// not paired (see update8) cost (8192, 4, 2) 18 us: 773.
-constexpr int per_sm(int) { return 2; }
 // Blocks per SM that the registers allow: a plan with at most that many chunks runs one chunk per block.
 constexpr int per_sm_most(int kind) { return kind >= F32_F8 ? 2 : 3; }
+// Blocks per SM on larger plans. Measured on one layer's 403M values (bf16): fp32 states with a master 1851 us at 2
+// blocks, 1922 at 3, 1956 at 4. 8-bit states, (values per chunk, passes loaded ahead, blocks): (8192, 4, 2) 755 us,
+// (8192, 4, 3) 795, (6144, 3, 3) 765, (4096, 2, 3) 800, (4096, 1, 5) 903, (4096, 1, 3) 1063; one fp32 per instruction
+// instead of two: (4096, 1, 5) 934. Since then sums that are not paired (see update8) cost 18 us and scales that
+// are written together took 37: 735.
+constexpr int per_sm(int) { return 2; }
+// 28 bytes per value (fp32 parameters, or bf16 ones with a master, and fp32 states): larger plans run one block per SM
+// that loads a whole chunk, then writes it. As many bytes are in flight as with two blocks and one pass each, but HBM
+// sees longer runs of reads and of writes. 201M values: 834 us against 905 with a master, 819 against 905 for fp32
+// (from 460 chunks of 4096 on; at 900 chunks 2-9% slower); the 22 bytes of bf16 parameters without a master are the other way round, 759 against 673.
+constexpr bool runs(int kind) { return kind == F32_F32 || kind == BF16_MASTER_F32; }
 
 // The step's constants.
 struct Coef {
@@ -405,10 +410,11 @@ __device__ __forceinline__ void update8(const Tensor &t, Raw8<K> &raw, int64_t i
   }
 }
 
-template <int K>
-__global__ void __launch_bounds__(kThreads, per_sm_most(K)) adamw_kernel(const Tensor *__restrict__ tensors,
-                                                                    const Chunk *__restrict__ chunks, int64_t nchunks,
-                                                                    const Hyper hy, moe_adamw_state *st, int bump) {
+// LARGE: the plan has more chunks than blocks run at once, and runs(K).
+template <int K, bool LARGE>
+__global__ void __launch_bounds__(kThreads, LARGE ? 1 : per_sm_most(K))
+    adamw_kernel(const Tensor *__restrict__ tensors, const Chunk *__restrict__ chunks, int64_t nchunks, const Hyper hy,
+                 moe_adamw_state *st, int bump) {
   constexpr bool kF8 = K >= F32_F8;
   constexpr int kChunk = chunk_of(K), kPasses = kChunk / (kThreads * kVec);
   const int lane = threadIdx.x & 31;
@@ -455,6 +461,12 @@ __global__ void __launch_bounds__(kThreads, per_sm_most(K)) adamw_kernel(const T
           if (lane == kPasses + a) scale = r[a].vs;
         }
         if (lane < 2 * kPasses) *scales = scale;
+      } else if constexpr (LARGE) {
+        Raw8<K> r[kPasses];
+#pragma unroll
+        for (int a = 0; a < kPasses; ++a) r[a].load(t, first + a * (kThreads * kVec));
+#pragma unroll
+        for (int a = 0; a < kPasses; ++a) update8<K, true>(t, r[a], first + a * (kThreads * kVec), kVec, hy, co, decay);
       } else {
 #pragma unroll 1
         for (int pass = 0; pass < kPasses; ++pass) {
@@ -519,11 +531,14 @@ template <int K>
 static int launch(const uint8_t *dev, const Header *h, int64_t first, int64_t n, const Hyper &hy, moe_adamw_state *st,
                   bool bump, cudaStream_t s) {
   const int sms = sm_count();
-  int64_t grid = n <= (int64_t)sms * per_sm_most(K) ? n : (int64_t)sms * per_sm(K);
-  if (grid > n) grid = n;
-  if (grid < 1) grid = 1;
-  adamw_kernel<K><<<(int)grid, kThreads, 0, s>>>((const Tensor *)(dev + sizeof(Header)),
-                                                 (const Chunk *)(dev + h->chunks_at) + first, n, hy, st, bump ? 1 : 0);
+  const bool small = n <= (int64_t)sms * per_sm_most(K);
+  const int64_t grid = small ? (n < 1 ? 1 : n) : (int64_t)sms * (runs(K) ? 1 : per_sm(K));
+  const Tensor *tensors = (const Tensor *)(dev + sizeof(Header));
+  const Chunk *chunks = (const Chunk *)(dev + h->chunks_at) + first;
+  if (runs(K) && !small)
+    adamw_kernel<K, runs(K)><<<(int)grid, kThreads, 0, s>>>(tensors, chunks, n, hy, st, bump ? 1 : 0);
+  else
+    adamw_kernel<K, false><<<(int)grid, kThreads, 0, s>>>(tensors, chunks, n, hy, st, bump ? 1 : 0);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
