@@ -156,8 +156,9 @@ constexpr int per_sm_most(int kind) { return kind >= F32_F8 ? 2 : 3; }
 constexpr int per_sm(int) { return 2; }
 // 28 bytes per value (fp32 parameters, or bf16 ones with a master, and fp32 states): larger plans run one block per SM
 // that loads a whole chunk, then writes it. As many bytes are in flight as with two blocks and one pass each, but HBM
-// sees longer runs of reads and of writes. 201M values: 834 us against 905 with a master, 819 against 905 for fp32
-// (from 460 chunks of 4096 on; at 900 chunks 2-9% slower); the 22 bytes of bf16 parameters without a master are the other way round, 759 against 673.
+// sees longer runs of reads and of writes. 201M values: 834 us against 905 with a master, 819 against 905 for fp32; from
+// 460 chunks on it is ahead but for 2-9% around 900. The 22 bytes of bf16 parameters without a master are the
+// other way round, 759 us against 673.
 constexpr bool runs(int kind) { return kind == F32_F32 || kind == BF16_MASTER_F32; }
 
 // The step's constants.
