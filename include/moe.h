@@ -357,8 +357,8 @@ int moe_norm_residual_bwd(const void *dout, const void *dn, const void *out, con
  *           scale (the block's largest magnitude / 448) per MOE_ADAMW_BLOCK consecutive values; m_scale, v_scale
  *           have ceil(n / MOE_ADAMW_BLOCK) entries. A block whose largest magnitude is below 1e-30 is held as zeros.
  *           A root below 2^-18 of its block's largest may be held as zero while m is not (its next update is then
- *           as large as lr m / eps), and a v below 2^-126 counts as zero: tensors whose blocks mix such
- *           magnitudes belong in MOE_ADAMW_F32.
+ *           as large as lr m / eps); for bf16 parameters without a master a v below 2^-126 counts as zero. Tensors
+ *           whose blocks mix such magnitudes belong in MOE_ADAMW_F32.
  * Values kept in few bits only (the e4m3 states, a bf16 parameter without a master) are rounded with a dither
  * that depends on the place in the tensor and on t: down after adding u / 2^b of a rounding step, where u is
  * the top b bits of (place * 2654435769 + t * 1640531535 + shift) mod 2^32 (b = 20 and shift 0 for m, shift

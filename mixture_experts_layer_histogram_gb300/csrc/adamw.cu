@@ -95,8 +95,8 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Approximate root: of subnormal numbers too, or (FTZ) taking them as zero. 8-bit states use the second: the other
-// costs them 5% (814 us against 771), and their v spans 2^36 within a block anyway.
+// Approximate root: of subnormal numbers too, or (FTZ) taking them as zero. bf16 parameters with 8-bit states and no
+// master use the second: the other costs them 5% (814 us against 771), and their v spans 2^36 within a block anyway.
 template <bool FTZ> __device__ __forceinline__ float sqrt_approx(float v) {
   float r;
   if (FTZ) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -208,6 +208,11 @@ __device__ __forceinline__ void update8(const Tensor &t, Raw8<K> &raw, int64_t i
   constexpr bool kF8 = K >= F32_F8;
   constexpr bool kMaster = K == BF16_MASTER_F32 || K == BF16_MASTER_F8;
   constexpr bool kF32 = K == F32_F32 || K == F32_F8;
+  // 8-bit states of an fp32 parameter (or master): every root is rounded to nearest and y before it is moved, so codes are
+  // those of the formulas bit for bit. A code on the other side of a rounding threshold (one in a million
+  // otherwise) changes the next update by a step of v; bf16 parameters hide that, fp32 ones show it. Here it costs
+  // nothing (HBM has 16 bytes to move per value); without a master it takes 735 us to 881.
+  constexpr bool kExact = K == F32_F8 || K == BF16_MASTER_F8;
   using T = typename std::conditional<kF32, float, __nv_bfloat16>::type;
   const T *gp = (const T *)t.g + i0;
   T *pp = (T *)t.p + i0;
@@ -266,7 +271,7 @@ __device__ __forceinline__ void update8(const Tensor &t, Raw8<K> &raw, int64_t i
   } else {
     // m and v are rounded at each operation (no fused multiply-add), and the largest root is the root of the
     // largest v, rounded to nearest: the scales then follow from the formulas alone, bit for bit, and a
-    // block's largest value gets the code it should. The other roots may be approximate.
+    // block's largest value gets the code it should. The other roots may be approximate (but for kExact).
     const F2 b1 = pair(hy.beta1, hy.beta1), b2 = pair(hy.beta2, hy.beta2), ms2 = pair(raw.ms, raw.ms), vs2 = pair(raw.vs, raw.vs);
     const float kg1 = hy.omb1 * co.gs, kg2 = hy.omb2 * (co.gs * co.gs);
     const F2 c1 = pair(kg1, kg1), c2 = pair(kg2, kg2);
@@ -297,8 +302,13 @@ __device__ __forceinline__ void update8(const Tensor &t, Raw8<K> &raw, int64_t i
     F2 sum2 = pair(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < kVec / 2; ++j) {
-      v[2 * j] = v[2 * j] == vtop ? vx : sqrt_approx<true>(v[2 * j]);
-      v[2 * j + 1] = v[2 * j + 1] == vtop ? vx : sqrt_approx<true>(v[2 * j + 1]);
+      if (kExact) {
+        v[2 * j] = sqrtf(v[2 * j]);
+        v[2 * j + 1] = sqrtf(v[2 * j + 1]);
+      } else {
+        v[2 * j] = v[2 * j] == vtop ? vx : sqrt_approx<true>(v[2 * j]);
+        v[2 * j + 1] = v[2 * j + 1] == vtop ? vx : sqrt_approx<true>(v[2 * j + 1]);
+      }
       float d0, d1;
       split(fma(pair(v[2 * j], v[2 * j + 1]), ir, eps), d0, d1);
       const F2 pp = fma(pair(p[2 * j], p[2 * j + 1]), dc, mul(mul(l1, m2[j]), pair(rcp_approx(d0), rcp_approx(d1))));
@@ -327,17 +337,19 @@ __device__ __forceinline__ void update8(const Tensor &t, Raw8<K> &raw, int64_t i
     const float mi = mk ? __frcp_rn(mx) * 448.0f : 0.0f, vi = vk ? __frcp_rn(vx) * 448.0f : 0.0f;
     uint32_t mc[2], vc[2];   // four codes each
     if (!odd) {
-      const float mz = mi * 0x1p-120f, vz = vi * 0x1p-120f;
-      const F2 mz2 = pair(mz, mz), vz2 = pair(vz, vz);
+      // kExact: y is rounded, and its move onto fp32's lowest exponents (see dither) then drops what lies below 2^-20 of
+      // a code's smallest step. Otherwise one product does both.
+      const F2 mi2 = pair(mi, mi), vi2 = pair(vi, vi), low = pair(0x1p-120f, 0x1p-120f);
+      const F2 mz2 = mul(mi2, low), vz2 = mul(vi2, low);
       uint32_t mw[kVec], vw[kVec];
 #pragma unroll
       for (int j = 0; j < kVec; j += 2) {
         const uint32_t h = h0 + (uint32_t)j * 2654435769u, h1 = h0 + (uint32_t)(j + 1) * 2654435769u;
         float x, y;
-        split(mul(m2[j / 2], mz2), x, y);
+        split(kExact ? mul_rz(mul(m2[j / 2], mi2), low) : mul(m2[j / 2], mz2), x, y);
         mw[j] = dither(x, h);
         mw[j + 1] = dither(y, h1);
-        split(mul(pair(v[j], v[j + 1]), vz2), x, y);
+        split(kExact ? mul_rz(mul(pair(v[j], v[j + 1]), vi2), low) : mul(pair(v[j], v[j + 1]), vz2), x, y);
         vw[j] = dither(x, h + 0x55555555u);
         vw[j + 1] = dither(y, h1 + 0x55555555u);
       }
