@@ -25,6 +25,8 @@
 // The weight gradients are summed over a block's rows in registers, written as one fp32 partial row per block and
 // added up by a second kernel in a fixed order, so they do not depend on timing. With a gate per
 // channel, dw_post and d_gate are both multiples of A = sum_t G y r, so one accumulator serves both.
+#include <atomic>
+
 #include "common.cuh"
 #include "f32x2.cuh"
 
@@ -34,7 +36,8 @@ namespace norm {
 constexpr int kMaxThreads = 512;
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kStages = 3;                    // at most; fewer where long rows leave no room
-constexpr size_t kRingMost = 200 * 1024;
+constexpr size_t kRingMost = 200 * 1024;      // bytes; one stage of five fp32 rows of MOE_NORM_MAX_D is 164 KB
+static_assert(5 * (MOE_NORM_MAX_D * 4 + 16) <= kRingMost, "every ring fits the limit that launches raise");
 
 // Arithmetic on one lane of values: two fp32 at a time (f32x2 instructions) for rows of 16-byte vectors, one fp32,
 // or one fp64. At bf16 the instructions, not HBM, bound these kernels when each value takes its own.
@@ -657,7 +660,7 @@ static Shape shape_of(int d, int dtype) {
 static int stages_of(const Shape &s, int tensors) {
   int n = kStages;
   while (n > 1 && (size_t)n * tensors * s.row_bytes > kRingMost) --n;
-  return n;   // one stage of five fp32 rows of MOE_NORM_MAX_D is 164 KB
+  return n;
 }
 static size_t ring_bytes(const Shape &s, int tensors) { return (size_t)stages_of(s, tensors) * tensors * s.row_bytes; }
 
@@ -677,13 +680,27 @@ static int bwd_blocks(int64_t T, const Shape &s, int tensors) {
   return b < 1 ? 1 : (int)b;
 }
 
-template <typename Params>
-static int launch(void (*kernel)(Params, Geometry), const Params &p, const Shape &sh, int tensors, int grid, cudaStream_t s) {
+// A kernel's dynamic shared memory limit is raised to the largest ring once per device, whatever this call needs: it is
+// the process's, and another thread may launch the same kernel on rows of another length at any time.
+template <auto KERNEL> static int raise_limit() {
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  MOE_TRY_CUDA(cudaGetDevice(&dev));
+  if (dev < 64 && (raised.load(std::memory_order_relaxed) >> dev & 1)) return MOE_OK;
+  MOE_TRY_CUDA(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingMost));
+  if (dev < 64) raised.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  return MOE_OK;
+}
+
+template <auto KERNEL, typename Params>
+static int launch(const Params &p, const Shape &sh, int tensors, int grid, cudaStream_t s) {
   const size_t smem = ring_bytes(sh, tensors);
   const Geometry ring{sh.row_bytes, tensors * sh.row_bytes, stages_of(sh, tensors)};
-  if (smem > 40 * 1024)   // with the sums' buffer past the 48 KB that every kernel may have
-    MOE_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  kernel<<<grid, sh.threads, smem, s>>>(p, ring);
+  if (smem > 40 * 1024) {   // with the sums' buffer past the 48 KB that every kernel may have
+    const int rc = raise_limit<KERNEL>();
+    if (rc) return rc;
+  }
+  KERNEL<<<grid, sh.threads, smem, s>>>(p, ring);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
@@ -692,15 +709,15 @@ static int launch_fwd(const FwdParams &p, bool block, bool next, const Shape &sh
   const int tensors = block ? (p.gate_kind == MOE_GATE_TOKEN ? 3 : 2) : 1;
   int64_t grid = (int64_t)sm_count() * per_sm(sh, tensors, sh.iter == 1 ? 2 * kMaxThreads : kMaxThreads);
   if (grid > p.T) grid = p.T;
-  if (!block) return launch(norm_fwd_kernel<T, VEC, ITER, false, true>, p, sh, tensors, (int)grid, s);
-  if (next) return launch(norm_fwd_kernel<T, VEC, ITER, true, true>, p, sh, tensors, (int)grid, s);
-  return launch(norm_fwd_kernel<T, VEC, ITER, true, false>, p, sh, tensors, (int)grid, s);
+  if (!block) return launch<norm_fwd_kernel<T, VEC, ITER, false, true>>(p, sh, tensors, (int)grid, s);
+  if (next) return launch<norm_fwd_kernel<T, VEC, ITER, true, true>>(p, sh, tensors, (int)grid, s);
+  return launch<norm_fwd_kernel<T, VEC, ITER, true, false>>(p, sh, tensors, (int)grid, s);
 }
 template <typename T, int VEC, int ITER, typename S = float>
 static int launch_bwd(const BwdParams &p, bool block, bool next, const Shape &sh, int tensors, int grid, cudaStream_t s) {
-  if (!block) return launch(norm_bwd_kernel<T, VEC, ITER, false, true, S>, p, sh, tensors, grid, s);
-  if (next) return launch(norm_bwd_kernel<T, VEC, ITER, true, true, S>, p, sh, tensors, grid, s);
-  return launch(norm_bwd_kernel<T, VEC, ITER, true, false, S>, p, sh, tensors, grid, s);
+  if (!block) return launch<norm_bwd_kernel<T, VEC, ITER, false, true, S>>(p, sh, tensors, grid, s);
+  if (next) return launch<norm_bwd_kernel<T, VEC, ITER, true, true, S>>(p, sh, tensors, grid, s);
+  return launch<norm_bwd_kernel<T, VEC, ITER, true, false, S>>(p, sh, tensors, grid, s);
 }
 
 #define MOE_NORM_DISPATCH(FN, ...)                                                   \
