@@ -74,6 +74,14 @@ __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {   // read-once data
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
 }
+// The same for a kernel launched with launch_after(): the kernel before it may be writing *p while this one already lives
+// (it reads after wait_previous()), and the non-coherent path is only for what nobody writes meanwhile.
+__device__ __forceinline__ uint4 ld_stream_coherent(const uint4 *p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
 
 // Logistic sigmoid for the bf16 tensor-core epilogues: __expf, then the approximate reciprocal
 // (one MUFU op, at most 1 ulp of fp32 error) instead of an IEEE-rounded divide, whose multi-
