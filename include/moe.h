@@ -64,12 +64,12 @@ enum moe_status {
   MOE_ERR_CUDA = -3,            /* a CUDA runtime call or launch failed */
   MOE_ERR_DEVICE_TIMEOUT = -4,  /* a bounded device-side wait ran out (device status word) */
   MOE_ERR_BAD_INDEX = -5,       /* an expert id outside [0, E) was seen (device status word) */
-  MOE_ERR_CHECK_FAILED = -6     /* a consistency check of the debug build failed (device status word):
-                                   see "Debug build" below */
+  MOE_ERR_CHECK_FAILED = -6     /* a consistency check failed (device status word): of the debug build (see
+                                   "Debug build" below), or of moe_grouped_ffn_fwd_fp4 */
 };
 
 /* Debug build. Compiled with -DMOE_CHECKS=1 (mixture_experts_layer_histogram_gb300/build.py:
- * build(checks=True) writes libmoe_checks.so), the grouped-GEMM kernels check on the device that
+ * build(checks=True) writes libmoe_checks.so), the bf16 grouped-GEMM kernels check on the device that
  * every tile's rows lie inside its expert's row group (offsets and tile_offsets agree: an expert's
  * routed rows fit its padded group) and inside rows_max, that every row a tile stores, zero-fills or
  * reads as a weight-gradient operand lies below rows_max, and that tile_offsets is non-decreasing.
@@ -427,6 +427,8 @@ int moe_permute_fp4(const void *x, int dtype, int T, int d, int k, int E, const 
  *   y_perm                [rows_max, d] bf16: h Wd^T over the values that h_codes stand for
  * Products run on the block-scaled tensor cores with fp32 accumulation; h is quantised from fp32. Requires
  * d % 256 == 0 and f % 256 == 0. Padding rows come out as zeros. ws: as for moe_grouped_ffn_fwd with MOE_BF16.
+ * In every build: an expert whose routed rows (offsets) do not fit its row group (tile_offsets), or whose group does not
+ * lie inside rows_max, is skipped (its rows are not written) and MOE_ERR_CHECK_FAILED recorded in ws.
  * A NaN or an infinity in a token makes that token's rows NaN; in the weights, the outputs that they enter.
  */
 int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales, const void *wgu_codes, const void *wgu_scales,

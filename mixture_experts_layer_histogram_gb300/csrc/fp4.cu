@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) permute_fp4_kernel(const T *__restri
     int64_t end = (int64_t)tile_offsets[e + 1] * kTileRows;
     if (end > rows_max) end = rows_max;
     if (end > start + kPadRows) end = start + kPadRows;
-    if (start >= end) return;
+    if (start < 0 || start >= end) return;
     uint4 *dst = reinterpret_cast<uint4 *>(codes + start * (K / 2));
     for (int64_t i = threadIdx.x; i < (end - start) * (K / 32); i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
     for (int i = threadIdx.x; i < (int)(end - start) * kgroups; i += kThreads) {

@@ -130,7 +130,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
       wait_previous();
-      make_plan<MT>(p, lane, plan);
+      make_plan<MT, true>(p, lane, plan);
     }
   }
   if (warp == 1) {

@@ -108,14 +108,34 @@ struct Plan {
   uint16_t last[MAX_E];      // routed rows in its last tile (1..TR)
 };
 // Filled by one warp. The offsets are read from L2: the kernel may have started, and read them, before the kernel
-// that writes them had ended.
-template <int TR> __device__ __forceinline__ void make_plan(const Params &p, int lane, Plan &plan) {
-  int c[8], at[8], sum = 0;
+// that writes them had ended. An expert whose rows do not lie inside its row group, or whose group does not lie inside
+// the buffers, counts as empty (REPORT: and MOE_ERR_CHECK_FAILED is recorded): every row that a tile touches is below rows_max.
+template <int TR, bool REPORT = false> __device__ __forceinline__ void make_plan(const Params &p, int lane, Plan &plan) {
+  int c[8], at[9], o[9], sum = 0;
+#pragma unroll
+  for (int q = 0; q < 9; ++q) {
+    const int e = min(lane * 8 + q, p.E);
+    o[q] = __ldcg(p.offsets + e);
+    at[q] = __ldcg(p.tile_offsets + e);
+  }
+  const uint32_t groups = (uint32_t)(p.rows_max / MOE_GROUP_ROWS);
+  auto fits = [&](int q) {   // unsigned: what is negative is too large
+    const uint32_t first = (uint32_t)at[q], next = (uint32_t)at[q + 1];
+    return first <= next && next <= groups && (uint32_t)c[q] <= (next - first) * MOE_GROUP_ROWS;
+  };
+  bool fit = true;
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const int e = lane * 8 + q;
-    c[q] = e < p.E ? __ldcg(p.offsets + e + 1) - __ldcg(p.offsets + e) : 0;
-    at[q] = e < p.E ? __ldcg(p.tile_offsets + e) : 0;
+    c[q] = o[q + 1] - o[q];
+    fit = fit && fits(q);
+  }
+  if (!fit) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (fits(q)) continue;
+      c[q] = 0;
+      if (REPORT) report(p.hdr, MOE_ERR_CHECK_FAILED, min(lane * 8 + q, p.E - 1));
+    }
   }
 #pragma unroll
   for (int q = 0; q < 8; ++q) sum += (c[q] + TR - 1) / TR;

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (walk.next(t, p, plan)) prefetch_weights(t, min(p.num_kb, STAGES));
       __syncwarp();
       wait_previous();
-      make_plan<TT>(p, lane, plan);
+      make_plan<TT, true>(p, lane, plan);
     }
   }
   if (warp == 1) {
