@@ -112,7 +112,7 @@ def exported_symbols():
     return list(_SIGS)
 
 
-_U8 = torch.uint8
+_U8, _I32 = torch.uint8, torch.int32
 _CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
@@ -170,6 +170,16 @@ def _bytes_at_least(name, t, n):
     if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{name}: a contiguous uint8 tensor of at least {n} bytes is needed, got {t.dtype} "
                          f"{tuple(t.shape)}")
+    return _p(t)
+
+
+def _ints(name, t, n):
+    """The address of an index tensor: at least n contiguous 32-bit integers. (None is the library's to refuse.)"""
+    if t is None:
+        return None
+    if t.dtype is not _I32 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 tensor of at least {n} entries is needed, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
     return _p(t)
 
 
@@ -455,7 +465,8 @@ def moe_permute_fp4(x, k, E, row_of_slot, counts, tile_offsets, codes, scales, s
     R = codes.shape[0]
     dt = x.dtype
     _ok("moe_permute_fp4", lib().moe_permute_fp4(
-        _ptr("x", x, dt, (T, d)), dtype_code(dt), T, d, k, E, _p(row_of_slot), _p(counts), _p(tile_offsets), R,
+        _ptr("x", x, dt, (T, d)), dtype_code(dt), T, d, k, E, _ints("row_of_slot", row_of_slot, T * k),
+        _ints("counts", counts, E), _ints("tile_offsets", tile_offsets, E + 1), R,
         _ptr("codes", codes, torch.uint8, (R, d // 2)), _bytes_at_least("scales", scales, _scale_bytes(R, d)),
         _s(stream)))
 
@@ -470,7 +481,8 @@ def moe_grouped_ffn_fwd_fp4(x_codes, x_scales, wgu_codes, wgu_scales, wd_codes, 
         _ptr("wgu_codes", wgu_codes, u8, (E, 2 * f, d // 2)),
         _bytes_at_least("wgu_scales", wgu_scales, _scale_bytes(E * 2 * f, d)),
         _ptr("wd_codes", wd_codes, u8, (E, d, f2)), _bytes_at_least("wd_scales", wd_scales, _scale_bytes(E * d, f)),
-        _p(tile_offsets), _p(offsets), E, d, f, R, _ptr("h_codes", h_codes, u8, (R, f2)),
+        _ints("tile_offsets", tile_offsets, E + 1), _ints("offsets", offsets, E + 1), E, d, f, R,
+        _ptr("h_codes", h_codes, u8, (R, f2)),
         _bytes_at_least("h_scales", h_scales, _scale_bytes(R, f)), _ptr("y_perm", y_perm, torch.bfloat16, (R, d)),
         _p(ws), ws.numel() * ws.element_size(), _s(stream)))
 

@@ -70,6 +70,8 @@ class MoELayerFp4:
 
     def forward(self, x, logits, weights, stream=None):
         """x [T, d] bf16 or fp32, logits [T, E] fp32 -> out [T, d] bf16."""
+        L._want("x", x, x.dtype, (self.T, self.d))
+        L._want("logits", logits, torch.float32, (self.T, self.E))
         L.moe_route_count_index(logits, self.k, self.topk_idx, self.topk_w, self.counts, self.offsets,
                                 self.tile_offsets, self.row_of_slot, self.token_of_row, self.ws_index, stream)
         L.moe_permute_fp4(x, self.k, self.E, self.row_of_slot, self.counts, self.tile_offsets, self.x_codes,
