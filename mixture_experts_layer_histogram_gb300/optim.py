@@ -18,7 +18,8 @@ from . import _lib as L
 class AdamW:
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state="f32",
                  masters=None, m=None, v=None, m_scale=None, v_scale=None, step=0):
-        """params, grads: contiguous CUDA tensors, fp32 or bf16 (a gradient in its parameter's type).
+        """params, grads: contiguous CUDA tensors, fp32 or bf16 (a gradient in its parameter's type). All tensors are on
+        one GPU, which is the current one when step is called.
         weight_decay: one value, or one per tensor. state: "f32", or "f8" (e4m3 codes with one fp32 scale per
         256 values; v as the codes of its root; not for tensors that mix gradients over 2^18 apart within 256
         values). masters: True for fp32 copies of the bf16 parameters, or a list of them (None for fp32
@@ -59,6 +60,8 @@ class AdamW:
                             ("m_scale", self.m_scale[i] if f8 else None), ("v_scale", self.v_scale[i] if f8 else None)):
                 if t is not None and not t.is_cuda:
                     raise ValueError("libmoe takes CUDA tensors only")
+                if t is not None and t.device != dev:
+                    raise ValueError(f"{name} of parameter {i} is on {t.device}, the first parameter on {dev}")
                 setattr(a, name, None if t is None else t.data_ptr())
             tensors.append(a)
         self._plan = L.moe_adamw_plan(tensors)
@@ -66,6 +69,7 @@ class AdamW:
         # moe_adamw_state: step, lr, grad_scale, arrived
         self._state = torch.zeros(3, dtype=torch.int64, device=dev)
         self._state[0] = step
+        self._index = self._state.device.index
         self._hyper = self._state[1:2].view(torch.float32)
         self._hyper.copy_(torch.tensor([lr, 1.0]))
 
@@ -88,6 +92,8 @@ class AdamW:
         return list(given)
 
     def step(self, stream=None):
+        if L._device() != self._index:
+            raise ValueError(f"the tensors are on cuda:{self._index}, the current device is cuda:{L._device()}")
         L.moe_adamw_step(self._plan, self._plan_device, self.betas[0], self.betas[1], self.eps, self._state, stream)
 
     def set_lr(self, lr):
