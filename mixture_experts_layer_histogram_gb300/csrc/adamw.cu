@@ -253,7 +253,7 @@ __device__ __forceinline__ void update8(const Tensor &t, Raw8<K> &raw, int64_t i
       m[j] = fmaf(hy.beta1, m[j], hy.omb1 * gj);
       v[j] = fmaf(hy.beta2, v[j], hy.omb2 * gj * gj);
       // approximate root and reciprocal: off by a few 2^-24, on a term that is a small part of p
-      p[j] = fmaf(p[j], decay, co.lr1 * m[j] * rcp_approx(fmaf(sqrt_approx<false>(v[j]), co.inv_root2, hy.eps)));
+      p[j] += fmaf(p[j], decay, co.lr1 * m[j] * rcp_approx(fmaf(sqrt_approx<false>(v[j]), co.inv_root2, hy.eps)));
       sum += p[j];
     }
     odd = sum != sum;
@@ -311,7 +311,8 @@ __device__ __forceinline__ void update8(const Tensor &t, Raw8<K> &raw, int64_t i
       }
       float d0, d1;
       split(fma(pair(v[2 * j], v[2 * j + 1]), ir, eps), d0, d1);
-      const F2 pp = fma(pair(p[2 * j], p[2 * j + 1]), dc, mul(mul(l1, m2[j]), pair(rcp_approx(d0), rcp_approx(d1))));
+      // the reciprocal is approximate, as above
+      const F2 p0 = pair(p[2 * j], p[2 * j + 1]), pp = add(p0, fma(p0, dc, mul(mul(l1, m2[j]), pair(rcp_approx(d0), rcp_approx(d1)))));
       sum2 = add(sum2, pp);
       split(pp, p[2 * j], p[2 * j + 1]);
     }
@@ -453,7 +454,9 @@ __global__ void __launch_bounds__(kThreads, LARGE ? 1 : per_sm_most(K))
     const Chunk ch = ahead;
     if (ci + gridDim.x < nchunks) ahead = chunks[ci + gridDim.x];
     const Tensor t = tensors[ch.tensor];
-    const float decay = 1.0f - co.lr * t.weight_decay;
+    // The change that decay makes, not the factor 1 - lr wd: fp32 numbers just below 1 are 6e-8 apart, so 1e-7
+    // would act as 1.2e-7 on every value alike, and half of that not at all.
+    const float decay = -co.lr * t.weight_decay;
     const int64_t first = (int64_t)ch.index * kChunk + threadIdx.x * kVec;
     if (t.aligned && (int64_t)(ch.index + 1) * kChunk <= t.n) {
       if constexpr (kF8) {
