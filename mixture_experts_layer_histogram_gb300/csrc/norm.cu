@@ -199,9 +199,10 @@ template <typename T, int VEC, int ITER> struct Ring {
 
 // Sums over the block, the same on every thread. `buf` alternates between two halves, so one barrier per
 // reduction is enough: a half is written again only after the next reduction's barrier.
-struct SumBuf {
+struct alignas(16) SumBuf {
   float v[2][8][kMaxWarps];
 };
+static_assert(alignof(SumBuf) >= alignof(float4) && kMaxWarps % 4 == 0, "the sums read it four values at a time");
 __device__ __forceinline__ void clear(SumBuf &buf) {   // the places of warps that the block does not have stay 0
   for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps; i += blockDim.x) (&buf.v[0][0][0])[i] = 0.0f;
   __syncthreads();
