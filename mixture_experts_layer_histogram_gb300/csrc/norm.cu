@@ -674,11 +674,22 @@ static int per_sm(const Shape &s, int tensors, int threads_max) {
 }
 
 // Blocks of the backward on rows of `tensors` inputs: each leaves a partial row, so there are no more than the GPU
-// holds at once. (More inputs, fewer blocks.)
+// holds at once. (The SMs of a GB300, not of the current device: the workspace's size follows from it, and may be asked
+// for anywhere.)
+constexpr int kSms = 152;
 static int bwd_blocks(int64_t T, const Shape &s, int tensors) {
-  int64_t b = 152 * per_sm(s, tensors, bwd_per_sm(s.vec, s.iter) * kMaxThreads);
+  int64_t b = kSms * per_sm(s, tensors, bwd_per_sm(s.vec, s.iter) * kMaxThreads);
   if (b > T) b = T;
   return b < 1 ? 1 : (int)b;
+}
+// The most partial rows that any form's inputs (two to five) lead to.
+static int bwd_blocks_most(int64_t T, const Shape &s) {
+  int most = 1;
+  for (int tensors = 2; tensors <= 5; ++tensors) {
+    const int b = bwd_blocks(T, s, tensors);
+    if (b > most) most = b;
+  }
+  return most;
 }
 
 // A kernel's dynamic shared memory limit is raised to the largest ring once per device, whatever this call needs: it is
@@ -792,7 +803,7 @@ using namespace moe::norm;
 
 extern "C" size_t moe_norm_bwd_workspace_size(int T, int d, int dtype) {
   if (T < 0 || d < 1) return 0;
-  return (size_t)2 * bwd_blocks(T, shape_of(d, dtype), 2) * d * sizeof(float) + 256;
+  return (size_t)2 * bwd_blocks_most(T, shape_of(d, dtype)) * d * sizeof(float) + 256;
 }
 
 extern "C" int moe_norm_fwd(const void *x, const void *w, int T, int d, int dtype, float eps, void *n,
