@@ -317,7 +317,8 @@ int moe_router_bwd(const void *x, const void *w_router, const float *d_logits, i
  *                           n   = out rms(out) w_next       (the next block's norm; w_next, n may be NULL)
  * w, w_post, w_next [d] and gate are in dtype; gate_kind says what gate is: none (NULL; 1), one value
  * per channel [d], or one per token and channel [T, d]. Sums and statistics are fp32; n is formed from
- * the unrounded out.
+ * the unrounded out. A row whose sum of squares passes fp32's range (magnitudes above about 1e19) counts as having
+ * rms 0: its norm is zeros, and so are the gradients through it (rows of more than 32 values).
  * Backward: for dout [T, d], the gradient that reaches out through the stream (NULL: zero, allowed only
  * with dn), and dn [T, d], the gradient of n (given exactly when w_next is),
  *   moe_norm_bwd            dx = dx_in + (norm backward of dn at x)  (dx_in NULL: zero; dx may be dx_in), dw [d]
