@@ -352,24 +352,26 @@ def moe_norm_fwd(x, w, n, eps=1e-6, stream=None):
     _ok("moe_norm_fwd", lib().moe_norm_fwd(_p(x), _p(w), T, d, dtype_code(dt), eps, _p(n), _s(stream)))
 
 
+def norm_residual_fwd_into(y, x, w_post, gate, kind, w_next, T, d, dt, out, n, res_scale, eps, stream):
+    """The call behind moe_norm_residual_fwd and BlockNorms.post: checks its inputs; out and n are the addresses of [T, d]
+    outputs of type dt (n None: no next norm)."""
+    rows, vec = (T, d), (d,)
+    _ok("moe_norm_residual_fwd", lib().moe_norm_residual_fwd(
+        _ptr("y", y, dt, rows), _ptr("x", x, dt, rows), _ptr("w_post", w_post, dt, vec),
+        _ptr("gate", gate, dt, vec if kind == GATE_CHANNEL else rows) if kind else None, kind,
+        None if n is None else _ptr("w_next", w_next, dt, vec), T, d, _CODES[dt], res_scale, eps, out, n, _s(stream)))
+
+
 def moe_norm_residual_fwd(y, x, w_post, gate, w_next, out, n, res_scale=1.0, eps=1e-6, stream=None):
     """out = res_scale x + gate * (y rms(y) w_post); n = out rms(out) w_next. gate: None, [d] or [T, d];
     w_next and n may be None (no next norm)."""
     T, d = x.shape
     dt = x.dtype
-    _want("x", x, dt, (T, d))
-    _want("y", y, dt, (T, d))
-    _want("out", out, dt, (T, d))
-    _want("w_post", w_post, dt, (d,))
+    dtype_code(dt)
     if (w_next is None) != (n is None):
         raise ValueError("w_next and n are given together")
-    if n is not None:
-        _want("w_next", w_next, dt, (d,))
-        _want("n", n, dt, (T, d))
-    kind = _gate_kind(gate, T, d, dt)
-    _ok("moe_norm_residual_fwd", lib().moe_norm_residual_fwd(
-        _p(y), _p(x), _p(w_post), _p(gate), kind, _p(w_next), T, d, dtype_code(dt), res_scale, eps, _p(out), _p(n),
-        _s(stream)))
+    norm_residual_fwd_into(y, x, w_post, gate, _gate_kind(gate, T, d, dt), w_next, T, d, dt, _ptr("out", out, dt, (T, d)),
+                           None if n is None else _ptr("n", n, dt, (T, d)), res_scale, eps, stream)
 
 
 def moe_norm_bwd_workspace_size(T, d, dtype):

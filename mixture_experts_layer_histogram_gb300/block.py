@@ -35,8 +35,8 @@ class BlockNorms:
         self.n = torch.empty((T, d), **act) if next_norm else None
         self.out = torch.empty((T, d), **act)
         self._kind = {None: L.GATE_NONE, "channel": L.GATE_CHANNEL, "token": L.GATE_TOKEN}[gate]
-        self._code = L.dtype_code(dtype)
         self._out_ptr, self._n_ptr = self.out.data_ptr(), self.n.data_ptr() if next_norm else None
+        code = L.dtype_code(dtype)
         self.backward_enabled = backward
         if backward:
             self.dx = torch.empty((T, d), **act)
@@ -45,8 +45,7 @@ class BlockNorms:
             self.dw_post = torch.empty(d, **act)
             self.dw_next = torch.empty(d, **act) if next_norm else None
             self.d_gate = None if gate is None else torch.empty((d,) if gate == "channel" else (T, d), **act)
-            self.ws = torch.empty(L.moe_norm_bwd_workspace_size(T, d, L.dtype_code(dtype)), dtype=torch.uint8,
-                                  device=self.device)
+            self.ws = torch.empty(L.moe_norm_bwd_workspace_size(T, d, code), dtype=torch.uint8, device=self.device)
 
     def _check_gate(self, gate):
         have = None if gate is None else ("channel" if gate.dim() == 1 else "token")
@@ -60,17 +59,12 @@ class BlockNorms:
 
     def post(self, y, x, w_post, gate=None, w_next=None, stream=None):
         """(out, n): the stream after the block and the next block's input (None without a next norm)."""
-        T, d, dt = self.T, self.d, self.dtype
         if (w_next is not None) != self.next_norm:
             raise ValueError("w_next is needed with a next norm, and only there")
         if self._kind or gate is not None:
             self._check_gate(gate)
-            gate = L._ptr("gate", gate, dt, (d,) if self._kind == L.GATE_CHANNEL else (T, d))
-        ptr = L._ptr
-        L._ok("moe_norm_residual_fwd", L.lib().moe_norm_residual_fwd(
-            ptr("y", y, dt, (T, d)), ptr("x", x, dt, (T, d)), ptr("w_post", w_post, dt, (d,)), gate, self._kind,
-            ptr("w_next", w_next, dt, (d,)) if self.next_norm else None, T, d, self._code, self.res_scale, self.eps,
-            self._out_ptr, self._n_ptr, L._s(stream)))
+        L.norm_residual_fwd_into(y, x, w_post, gate, self._kind, w_next, self.T, self.d, self.dtype, self._out_ptr,
+                                 self._n_ptr, self.res_scale, self.eps, stream)
         return self.out, self.n
 
     def post_backward(self, dout, dn, out, y, w_post, gate=None, w_next=None, stream=None):
