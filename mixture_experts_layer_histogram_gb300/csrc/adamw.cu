@@ -118,12 +118,6 @@ __device__ __forceinline__ void unpack_e4m3x8(const uint2 &q, float *v) {
     v[2 * i + 1] = f.y;
   }
 }
-// A bf16 value as the upper half of an fp32 word, rounded down in magnitude after adding u16 / 2^16 of a step.
-__device__ __forceinline__ uint32_t dither_bf16_bits(float p, uint32_t u16) {
-  const uint32_t b = __float_as_uint(p);
-  if ((b & 0x7f800000u) == 0x7f800000u) return p != p ? 0x7fff0000u : b;   // NaN, infinity
-  return (b + u16) & 0xffff0000u;
-}
 
 // Loads of values that are read once: they pass by the L1, which keeps the plan's entries.
 __device__ __forceinline__ uint4 ld_once(const void *p) {
