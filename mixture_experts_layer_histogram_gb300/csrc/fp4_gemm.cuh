@@ -118,6 +118,8 @@ template <int TR, bool REPORT = false> __device__ __forceinline__ void make_plan
     o[q] = __ldcg(p.offsets + e);
     at[q] = __ldcg(p.tile_offsets + e);
   }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) c[q] = o[q + 1] - o[q];
   const uint32_t groups = (uint32_t)(p.rows_max / MOE_GROUP_ROWS);
   auto fits = [&](int q) {   // unsigned: what is negative is too large
     const uint32_t first = (uint32_t)at[q], next = (uint32_t)at[q + 1];
@@ -125,10 +127,7 @@ template <int TR, bool REPORT = false> __device__ __forceinline__ void make_plan
   };
   bool fit = true;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    c[q] = o[q + 1] - o[q];
-    fit = fit && fits(q);
-  }
+  for (int q = 0; q < 8; ++q) fit = fit && fits(q);
   if (!fit) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
