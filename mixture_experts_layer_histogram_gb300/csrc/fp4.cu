@@ -6,6 +6,7 @@
 // Measured (bf16): quantising 16384 x 4096 takes 26.5 us (170 MB, 6.4 TB/s), permuting 8192 x 2048 to eight rows each
 // 18.4 us (105 MB, 5.7 TB/s). With eight values per thread, two exchanges and 4-byte words they took 44.5 and 34.5 us.
 #include "common.cuh"
+#include "dependent.cuh"
 #include "fp4.cuh"
 
 namespace moe {

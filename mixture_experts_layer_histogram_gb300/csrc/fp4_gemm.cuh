@@ -4,6 +4,7 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "fp4.cuh"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"

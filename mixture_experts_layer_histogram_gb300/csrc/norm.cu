@@ -28,6 +28,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "f32x2.cuh"
 
 namespace moe {

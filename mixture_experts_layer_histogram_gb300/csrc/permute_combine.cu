@@ -8,6 +8,7 @@
 // feed the grouped GEMM (permute) and the experts' outputs return to token order (combine); the
 // backward of both is part of the module's forward-backward pass (sections 为什么值得记录 / 关键结果).
 #include "common.cuh"
+#include "dependent.cuh"
 
 namespace moe {
 
