@@ -425,7 +425,8 @@ int moe_permute_fp4(const void *x, int dtype, int T, int d, int k, int E, const 
  *   wgu_codes, wgu_scales moe_fp4_quantize of w_gate_up viewed as [E * 2f, d]
  *   wd_codes, wd_scales   moe_fp4_quantize of w_down viewed as [E * d, f]
  *   h_codes, h_scales     scratch and output: MXFP4 of h = silu(x Wg^T) * (x Wu^T) [rows_max, f]
- *   y_perm                [rows_max, d] bf16: h Wd^T over the values that h_codes stand for
+ *   y_perm                [rows_max, d] bf16: h Wd^T over the values that h_codes stand for, each rounded once (the
+ *                         combine then adds a token's rows in fp32 and rounds their sum)
  * Products run on the block-scaled tensor cores with fp32 accumulation; h is quantised from fp32. Requires
  * d % 256 == 0 and f % 256 == 0. Padding rows come out as zeros. ws: as for moe_grouped_ffn_fwd with MOE_BF16.
  * In every build: an expert whose routed rows (offsets) do not fit its row group (tile_offsets), or whose group does not

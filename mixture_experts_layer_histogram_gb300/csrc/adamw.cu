@@ -96,7 +96,7 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   return r;
 }
 // Approximate root: of subnormal numbers too, or (FTZ) taking them as zero. bf16 parameters with 8-bit states and no
-// master use the second: the other costs them 5% (814 us against 771), and their v spans 2^36 within a block anyway.
+// master use the second: the other costs them 4% (771 us against 740), and their v spans 2^36 within a block anyway.
 template <bool FTZ> __device__ __forceinline__ float sqrt_approx(float v) {
   float r;
   if (FTZ) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -145,8 +145,8 @@ constexpr int per_sm_most(int kind) { return kind >= F32_F8 ? 2 : 3; }
 // Blocks per SM on larger plans. Measured on one layer's 403M values (bf16): fp32 states with a master 1851 us at 2
 // blocks, 1922 at 3, 1956 at 4. 8-bit states, (values per chunk, passes loaded ahead, blocks): (8192, 4, 2) 755 us,
 // (8192, 4, 3) 795, (6144, 3, 3) 765, (4096, 2, 3) 800, (4096, 1, 5) 903, (4096, 1, 3) 1063; one fp32 per instruction
-// instead of two: (4096, 1, 5) 934. Since then sums that are not paired (see update8) cost 18 us and scales that
-// are written together took 37: 735.
+// instead of two: (4096, 1, 5) 934. Since then sums that are not paired (see update8) cost 18 us, scales that are written
+// together took 37, and decay as a change of its own cost 7: 740.
 constexpr int per_sm(int) { return 2; }
 // 28 bytes per value (fp32 parameters, or bf16 ones with a master, and fp32 states): larger plans run one block per SM
 // that loads a whole chunk, then writes it. As many bytes are in flight as with two blocks and one pass each, but HBM
@@ -205,7 +205,7 @@ __device__ __forceinline__ void update8(const Tensor &t, Raw8<K> &raw, int64_t i
   // 8-bit states of an fp32 parameter (or master): every root is rounded to nearest and y before it is moved, so codes are
   // those of the formulas bit for bit. A code on the other side of a rounding threshold (one in a million
   // otherwise) changes the next update by a step of v; bf16 parameters hide that, fp32 ones show it. Here it costs
-  // nothing (HBM has 16 bytes to move per value); without a master it takes 735 us to 881.
+  // nothing (HBM has 16 bytes to move per value); without a master it takes 740 us to 897.
   constexpr bool kExact = K == F32_F8 || K == BF16_MASTER_F8;
   using T = typename std::conditional<kF32, float, __nv_bfloat16>::type;
   const T *gp = (const T *)t.g + i0;
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, LARGE ? 1 : per_sm_most(K))
     if (t.aligned && (int64_t)(ch.index + 1) * kChunk <= t.n) {
       if constexpr (kF8) {
         // A warp takes kPasses blocks in a row, all their loads first. One lane each carries their scales, which are
-        // written together: single words, two for every 256 values, cost 37 us of 771 on 403M values.
+        // written together: single words, two for every 256 values, cost 37 us on 403M values.
         const int64_t i0 = (int64_t)ch.index * kChunk + (threadIdx.x >> 5) * (kPasses * kBlockQ) + lane * kVec;
         float *scales = (lane < kPasses ? t.m_scale : t.v_scale) + i0 / kBlockQ + (lane & (kPasses - 1));
         float scale = lane < 2 * kPasses ? *scales : 0.0f;

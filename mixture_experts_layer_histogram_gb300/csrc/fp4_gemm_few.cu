@@ -6,10 +6,10 @@
 // rows rounded up to 16). GATEUP: the two are 128 gate rows and the same features' 128 up rows, so a lane of the
 // epilogue holds a and b of one feature, a warp the 32 features of one MXFP4 block: its largest magnitude is one
 // warp reduction per token, the codes go through shared memory to gather a token's 16 bytes in one lane. DOWN: a
-// lane holds one output feature, a warp stores 64 consecutive bytes per token.
+// lane holds one output feature, a warp stores 64 consecutive bytes per token, rounded to bf16 (why: fp4_gemm.cu).
 //
 // With tokens as M (256 rows per pair, fp4_gemm.cu) a tile's MMAs take as long for one row as for 256. Measured (d = 2048,
-// E = 64, k = 8, f = 1024), GATEUP reads its 147 MB of weights in 33-36 us at 42 rows per expert (4.1-4.4 TB/s with
+// E = 64, k = 8, f = 1024), GATEUP reads its 142.6 MB of weights in 33-36 us at 42 rows per expert (4.0-4.3 TB/s with
 // launch and last wave, 5.4 TB/s while all CTAs run); the ring's depth, the L2 promotion, the order of K and smaller
 // tiles do not matter there.
 //
