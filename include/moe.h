@@ -439,6 +439,44 @@ int moe_grouped_ffn_fwd_fp4(const void *x_codes, const void *x_scales, const voi
                             void *h_scales, void *y_perm, void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * Activations in 8 bits: what a forward keeps for its backward in half the bytes of bf16. Blocks of 32 values along a
+ * row (the last one of a row may be shorter) share a power of two; codes are e4m3 (largest 448).
+ *   codes   [R, K] bytes, e4m3 of x / scale, rounded to nearest even
+ *   scales  [R, ceil(K / 32)] bytes: b stands for 2^(b - 127), the least such power with max|x| <= 448 scale, not below
+ *           2^-127; a block that holds an infinity or a NaN gets 255 and zero codes, and stands for NaNs
+ * Requires K >= 1 and R K at most 2^39.
+ */
+size_t moe_act8_scale_bytes(int64_t R, int K);
+int moe_act8_quantize(const void *x, int dtype, int64_t R, int K, void *codes, void *scales, moe_stream_t stream);
+int moe_act8_dequantize(const void *codes, const void *scales, int64_t R, int K, int dtype, void *x,
+                        moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Layer norm. Per token (rows of x, n, dn, dx, dx_in: [T, d] in dtype; w, b [d] in dtype, b may be NULL: zero)
+ *   m = mean(x), r = 1 / sqrt(mean((x - m)^2) + eps), z = (x - m) r
+ *   moe_layer_norm_fwd      n = z w + b;  mean[T] = m, rstd[T] = r (fp32, either may be NULL);
+ *                           codes, scales (both or neither): z in 8 bits (moe_act8_quantize's format)
+ *   moe_layer_norm_restore  n = z w + b with the z that codes and scales stand for
+ *   moe_layer_norm_bwd      u = dn w;  dx = dx_in + r (u - mean(u) - z mean(u z)) (dx_in NULL: zero; dx may be dx_in),
+ *                           dw [d] = sum_t dn z, db [d] = sum_t dn (NULL: not wanted). z is formed from x, mean and
+ *                           rstd; with codes and scales (x NULL, mean unused) it is what they stand for.
+ * Sums and statistics are fp32. A row whose squared deviations pass fp32's range (magnitudes above about 1e19; up to
+ * 1e34 for its sum) counts as having r 0. Rows of at most 32 values are differentiated in 64 bits, with x's statistics
+ * formed again. Weight gradients are summed in fp32 in a fixed order, rounded once, and overwritten.
+ * Requires 1 <= d <= MOE_NORM_MAX_D, eps > 0, T >= 0 (T = 0: the weight gradients are zeros).
+ * ws: moe_layer_norm_bwd_workspace_size(T, d, dtype) bytes, 256-byte aligned, any content. Except dx == dx_in,
+ * outputs may not overlap inputs.
+ */
+int moe_layer_norm_fwd(const void *x, const void *w, const void *b, int T, int d, int dtype, float eps, void *n,
+                       float *mean, float *rstd, void *codes, void *scales, moe_stream_t stream);
+int moe_layer_norm_restore(const void *codes, const void *scales, const void *w, const void *b, int T, int d, int dtype,
+                           void *n, moe_stream_t stream);
+size_t moe_layer_norm_bwd_workspace_size(int T, int d, int dtype);
+int moe_layer_norm_bwd(const void *dn, const void *x, const void *codes, const void *scales, const float *mean,
+                       const float *rstd, const void *w, const void *dx_in, int T, int d, int dtype, float eps, void *dx,
+                       void *dw, void *db, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Synchronises `stream`, then returns the device status word at the start of a workspace used by
  * moe_count_index, moe_grouped_ffn_* or moe_router_*: MOE_OK or a negative moe_status. Not for
  * the hot path.

@@ -78,6 +78,13 @@ _SIGS = {
     "moe_fp4_dequantize": (_I, [_P, _P, _I64, _I, _I, _P, _P]),
     "moe_permute_fp4": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _I64, _P, _P, _P]),
     "moe_grouped_ffn_fwd_fp4": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "moe_act8_scale_bytes": (_SZ, [_I64, _I]),
+    "moe_act8_quantize": (_I, [_P, _I, _I64, _I, _P, _P, _P]),
+    "moe_act8_dequantize": (_I, [_P, _P, _I64, _I, _I, _P, _P]),
+    "moe_layer_norm_fwd": (_I, [_P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _P, _P, _P]),
+    "moe_layer_norm_restore": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P]),
+    "moe_layer_norm_bwd_workspace_size": (_SZ, [_I, _I, _I]),
+    "moe_layer_norm_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _P, _SZ, _P]),
     "moe_read_status": (_I, [_P, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_version": (_I, []),
@@ -487,6 +494,88 @@ def moe_grouped_ffn_fwd_fp4(x_codes, x_scales, wgu_codes, wgu_scales, wd_codes, 
         _ptr("h_codes", h_codes, u8, (R, f2)),
         _bytes_at_least("h_scales", h_scales, _scale_bytes(R, f)), _ptr("y_perm", y_perm, torch.bfloat16, (R, d)),
         _p(ws), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_act8_scale_bytes(R, K):
+    return int(lib().moe_act8_scale_bytes(R, K))
+
+
+def _scale_bytes8(rows, cols):
+    return rows * -(-cols // 32)
+
+
+def moe_act8_quantize(x, codes, scales, stream=None):
+    """x [..., K] (rows in order) -> codes [..., K] uint8, scales [moe_act8_scale_bytes(rows, K)] uint8."""
+    shape, dt = x.shape, x.dtype
+    R, K = _rows(shape)
+    _here(x, codes, scales)
+    _ok("moe_act8_quantize", lib().moe_act8_quantize(
+        _ptr("x", x, dt, shape), dtype_code(dt), R, K, _ptr("codes", codes, _U8, shape),
+        _bytes_at_least("scales", scales, _scale_bytes8(R, K)), _s(stream)))
+
+
+def moe_act8_dequantize(codes, scales, x, stream=None):
+    """The values that codes and scales stand for, into x [..., K]."""
+    shape, dt = x.shape, x.dtype
+    R, K = _rows(shape)
+    _here(codes, scales, x)
+    _ok("moe_act8_dequantize", lib().moe_act8_dequantize(
+        _ptr("codes", codes, _U8, shape), _bytes_at_least("scales", scales, _scale_bytes8(R, K)), R, K, dtype_code(dt),
+        _ptr("x", x, dt, shape), _s(stream)))
+
+
+def _here(*tensors):
+    """Refuses tensors of another GPU than the current one, on which the launch would go."""
+    dev = _device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _opt(name, t, dtype, shape):
+    return None if t is None else _ptr(name, t, dtype, shape)
+
+
+def moe_layer_norm_fwd(x, w, b, n, mean=None, rstd=None, codes=None, scales=None, eps=1e-5, stream=None):
+    """n = z w + b, z = (x - mean) rstd, x [T, d]; b may be None (zero). mean, rstd [T] fp32 and z in 8 bits (codes [T, d],
+    scales) are written where they are given."""
+    T, d = x.shape
+    dt, rows, vec = x.dtype, (T, d), (d,)
+    f32 = torch.float32
+    _here(x, w, b, n, mean, rstd, codes, scales)
+    _ok("moe_layer_norm_fwd", lib().moe_layer_norm_fwd(
+        _ptr("x", x, dt, rows), _ptr("w", w, dt, vec), _opt("b", b, dt, vec), T, d, dtype_code(dt), eps,
+        _ptr("n", n, dt, rows), _opt("mean", mean, f32, (T,)), _opt("rstd", rstd, f32, (T,)),
+        _opt("codes", codes, _U8, rows), None if scales is None else _bytes_at_least("scales", scales, _scale_bytes8(T, d)),
+        _s(stream)))
+
+
+def moe_layer_norm_restore(codes, scales, w, b, n, stream=None):
+    """n = z w + b with the z that codes and scales stand for; b may be None."""
+    T, d = n.shape
+    dt = n.dtype
+    _here(codes, scales, w, b, n)
+    _ok("moe_layer_norm_restore", lib().moe_layer_norm_restore(
+        _ptr("codes", codes, _U8, (T, d)), _bytes_at_least("scales", scales, _scale_bytes8(T, d)), _ptr("w", w, dt, (d,)),
+        _opt("b", b, dt, (d,)), T, d, dtype_code(dt), _ptr("n", n, dt, (T, d)), _s(stream)))
+
+
+def moe_layer_norm_bwd_workspace_size(T, d, dtype):
+    return int(lib().moe_layer_norm_bwd_workspace_size(T, d, dtype))
+
+
+def moe_layer_norm_bwd(dn, x, codes, scales, mean, rstd, w, dx_in, dx, dw, db, ws, eps=1e-5, stream=None):
+    """Backward of moe_layer_norm_fwd, from x and mean or from codes and scales (the others None); dx_in (may be None, may be
+    dx) is added to dx; db may be None (not wanted)."""
+    T, d = dn.shape
+    dt, rows, vec, f32 = dn.dtype, (T, d), (d,), torch.float32
+    _here(dn, x, codes, scales, mean, rstd, w, dx_in, dx, dw, db, ws)
+    _ok("moe_layer_norm_bwd", lib().moe_layer_norm_bwd(
+        _ptr("dn", dn, dt, rows), _opt("x", x, dt, rows), _opt("codes", codes, _U8, rows),
+        None if scales is None else _bytes_at_least("scales", scales, _scale_bytes8(T, d)), _opt("mean", mean, f32, (T,)),
+        _ptr("rstd", rstd, f32, (T,)), _ptr("w", w, dt, vec), _opt("dx_in", dx_in, dt, rows), T, d, dtype_code(dt), eps,
+        _ptr("dx", dx, dt, rows), _ptr("dw", dw, dt, vec), _opt("db", db, dt, vec), _p(ws),
+        ws.numel() * ws.element_size(), _s(stream)))
 
 
 def moe_read_status(ws, stream=None):

@@ -1,0 +1,636 @@
+// Layer norm, forward and backward, and the norm that keeps its rows in 8 bits for the backward.
+//
+//   m = mean(x), r = 1 / sqrt(mean((x - m)^2) + eps), z = (x - m) r, n = z w + b
+//   u = dn w,  dx = dx_in + r (u - mean(u) - z mean(u z)),  dw = sum_t dn z,  db = sum_t dn
+//
+// The forward leaves m and r (8 bytes a row) for the backward. m is the fp32 mean; what its rounding leaves,
+// mean(x - m), is formed with the deviations and taken off again, in both directions, so a row far from zero loses nothing.
+// Keeping: the forward also writes z as 8-bit codes with a power of two per 32 values (33 bytes per 32 values in the
+// place of the 64 that x takes in bf16); restore() gives z w + b again for the block's own backward, and
+// the backward reads z from the codes.
+//
+// HBM-bound, like the RMS norms (norm.cu): a thread block works on one row at a time, read once through the ring of rows and
+// written once; codes come through the ring as well, 8 (fp32: 4) bytes per thread beside its 16-byte vectors. Where the forward
+// needs two reductions per row (the deviations wait for the mean), the blocks that share an SM cover for one another.
+// The weight gradients are summed over a block's rows in registers and its partial rows added up in a fixed order.
+#include "act8.cuh"
+#include "row_ring.cuh"
+
+namespace moe {
+namespace norm {
+
+// N sums over the block (N at most 4), the same on every thread: the exchanges of block_sum6, for four values.
+template <int N> __device__ __forceinline__ void block_sums(float (&s)[N], SumBuf &buf, int &half) {
+  const int lane = threadIdx.x & 31;
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = i < N ? s[i < N ? i : 0] : 0.0f;
+#pragma unroll
+  for (int n = 2, off = 16; n >= 1; n >>= 1, off >>= 1) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+    }
+  }
+  float r = v[0];                                   // lanes 8 i .. 8 i + 7 carry value i
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
+  if (blockDim.x > 32) {
+    float(*b)[kMaxWarps] = buf.v[half];
+    half ^= 1;
+    if ((lane & 7) == 0) b[lane >> 3][threadIdx.x >> 5] = r;
+    __syncthreads();
+    const float2 q = *reinterpret_cast<const float2 *>(&b[lane >> 3][2 * (lane & 7)]);
+    r = q.x + q.y;
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = __shfl_sync(0xffffffffu, r, 8 * i);
+}
+template <int N> __device__ __forceinline__ void block_sums(double (&s)[N], SumBuf &, int &) {   // one warp
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
+  }
+}
+static_assert(kMaxWarps == 16, "eight lanes read the warps' sums two at a time");
+
+// Largest magnitude (fp32 bits) over a thread's VEC values and the other threads of its block of 32 values.
+template <int VEC> __device__ __forceinline__ uint32_t block_amax(uint32_t m) {
+#pragma unroll
+  for (int off = 1; off < act8::kBlock / VEC; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+  return m;
+}
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t magnitude(F2 v) {
+  float x, y;
+  split(v, x, y);
+  return max(magnitude(x), magnitude(y));
+}
+// The codes of N lanes of values times `inv`, written to p (VEC bytes)
+__device__ __forceinline__ void put_codes(uint8_t *p, const F2 (&v)[4], float inv) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split(mul(v[i], pair(inv, inv)), f[2 * i], f[2 * i + 1]);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(act8::pack4(f[0], f[1], f[2], f[3]), act8::pack4(f[4], f[5], f[6], f[7]));
+}
+__device__ __forceinline__ void put_codes(uint8_t *p, const F2 (&v)[2], float inv) {
+  float f[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) split(mul(v[i], pair(inv, inv)), f[2 * i], f[2 * i + 1]);
+  *reinterpret_cast<uint32_t *>(p) = act8::pack4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void put_codes(uint8_t *p, const float (&v)[1], float inv) { *p = act8::pack1(v[0] * inv); }
+// The values of codes in shared memory (at their scale)
+__device__ __forceinline__ void get_codes(uint32_t a, F2 (&v)[4], float scale) {
+  uint32_t q[2];
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q[0]), "=r"(q[1]) : "r"(a) : "memory");
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float f[4];
+    act8::unpack4(q[i], f);
+    v[2 * i] = mul(pair(f[0], f[1]), pair(scale, scale));
+    v[2 * i + 1] = mul(pair(f[2], f[3]), pair(scale, scale));
+  }
+}
+__device__ __forceinline__ void get_codes(uint32_t a, F2 (&v)[2], float scale) {
+  uint32_t q;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(q) : "r"(a) : "memory");
+  float f[4];
+  act8::unpack4(q, f);
+  v[0] = mul(pair(f[0], f[1]), pair(scale, scale));
+  v[1] = mul(pair(f[2], f[3]), pair(scale, scale));
+}
+
+struct LnFwdParams {
+  const void *x, *w, *b;       // b may be null
+  void *n;
+  float *mean, *rstd;          // may be null
+  uint8_t *codes, *scales;     // KEEP
+  int64_t T;
+  int d, nb;                   // nb: blocks of 32 per row
+  float eps;
+};
+
+template <typename T, int VEC, int ITER, bool KEEP>
+__global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(const LnFwdParams p, const Geometry geom) {
+  using V = Lanes<T, VEC, float>;
+  using L = typename V::L;
+  constexpr int N = V::N;
+  constexpr bool kHold = ITER * VEC <= 16 && ITER <= 4;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ SumBuf sums;
+  const Ring<T, VEC, ITER> ring(dyn, geom, p.T, p.d);
+  int half = 0;
+  const float inv_d = 1.0f / (float)p.d;
+  clear(sums);
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.T) ring.fetch(p.x, ring.offset(row), stage, 0);
+    ring.commit();
+  };
+  for (int s = 0; s < ring.stages - 1; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  auto weights = [&](int v, L *w, L *b) {
+    V::load((const T *)p.w + (int64_t)v * VEC, w);
+    if (p.b) {
+      V::load((const T *)p.b + (int64_t)v * VEC, b);
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; ++c) b[c] = splat<L>(0.0f);
+    }
+  };
+  L hold_w[kHold ? ITER : 1][N], hold_b[kHold ? ITER : 1][N];
+  if (kHold) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i)
+      if (ring.has(i)) weights(threadIdx.x + i * blockDim.x, hold_w[kHold ? i : 0], hold_b[kHold ? i : 0]);
+  }
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    if (ring.stages == 1) {
+      if (VEC == 1) __syncthreads();   // every thread has left the row before
+      fetch(row, 0);
+    }
+    ring.wait();
+    const int64_t off = ring.offset(row);
+    const uint32_t here = ring.at(stage, off);
+    L o[ITER][N], s = splat<L>(0.0f);
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      if (!ring.has(i)) continue;
+      V::load_shared(here + i * ring.step, o[i]);
+#pragma unroll
+      for (int c = 0; c < N; ++c) s = add(s, o[i][c]);
+    }
+    // the row is in registers: the stage of the row before it may be overwritten
+    if (ring.stages > 1) fetch(row + (int64_t)(ring.stages - 1) * gridDim.x, ring.freed(stage));
+    const float m = block_sum(total(s), sums, half) * inv_d;
+    L s1 = splat<L>(0.0f), s2 = splat<L>(0.0f);
+    const L minus = splat<L>(-m);
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      if (!ring.has(i)) continue;
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        o[i][c] = add(o[i][c], minus);
+        s1 = add(s1, o[i][c]);
+        s2 = fma(o[i][c], o[i][c], s2);
+      }
+    }
+    float t[2] = {total(s1), total(s2)};
+    block_sums(t, sums, half);
+    const float rest = t[0] * inv_d;                    // what the rounding of m left
+    const float var = fmaf(-rest, rest, t[1] * inv_d);
+    // squares past fp32's range: as if the variance were infinite
+    const float r = t[1] == __uint_as_float(0x7f800000u) ? 0.0f : rsqrtf(fmaxf(var, 0.0f) + p.eps);
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[row] = m + rest;
+      if (p.rstd) p.rstd[row] = var != var ? var : r;   // (fmaxf drops a NaN)
+    }
+    const L R = splat<L>(var != var ? var : r), shift = splat<L>(-rest);
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (ring.has(i)) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) o[i][c] = mul(add(o[i][c], shift), R);
+      }
+      if (KEEP) {
+        uint32_t top = 0;
+        if (ring.has(i)) {
+#pragma unroll
+          for (int c = 0; c < N; ++c) top = max(top, magnitude(o[i][c]));
+        }
+        const uint32_t byte = act8::scale_byte(block_amax<VEC>(top));
+        if (ring.has(i)) {
+          uint8_t *q = p.codes + row * p.d + (int64_t)v * VEC;
+          if (byte == 255u) {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) q[c] = 0;
+          } else {
+            put_codes(q, o[i], act8::inv_scale(byte));
+          }
+          if (v * VEC % act8::kBlock == 0) p.scales[row * p.nb + v * VEC / act8::kBlock] = (uint8_t)byte;
+        }
+      }
+      if (!ring.has(i)) continue;
+      L(&w)[N] = hold_w[kHold ? i : 0], (&b)[N] = hold_b[kHold ? i : 0];
+      if (!kHold) weights(v, w, b);
+#pragma unroll
+      for (int c = 0; c < N; ++c) o[i][c] = fma(o[i][c], w[c], b[c]);
+      V::store(reinterpret_cast<T *>((uint8_t *)p.n + off + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step),
+               o[i]);
+    }
+    if (++stage == ring.stages) stage = 0;
+  }
+}
+
+struct LnBwdParams {
+  const void *dn, *x, *dx_in, *w;     // dx_in may be null; x unless KEPT
+  const float *mean, *rstd;           // mean unless KEPT
+  const uint8_t *codes, *scales;      // KEPT
+  void *dx;
+  float *part;                        // [2][blocks][d]: dw, then db
+  int64_t T;
+  int d, nb;
+  float eps;
+};
+
+// S: float, or double for rows of at most 32 values, where u - mean(u) - z mean(u z) all but cancels (in a row of one or two
+// values what is left is of the order of eps): such rows are computed in 64 bits from x itself, its statistics too.
+template <typename T, int VEC, int ITER, bool KEPT, typename S>
+__global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln_bwd_kernel(const LnBwdParams p, const Geometry geom) {
+  using V = Lanes<T, VEC, S>;
+  using L = typename V::L;
+  constexpr int N = V::N;
+  constexpr bool kWide = sizeof(S) == 8;
+  constexpr bool kHold = ITER * VEC <= 16 && ITER <= 4;
+  constexpr int kDn = 0, kX = 1, kIn = 2;    // buffers of a stage; kX holds the codes where they are copied
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ SumBuf sums;
+  const Ring<T, VEC, ITER> ring(dyn, geom, p.T, p.d);
+  int half = 0;
+  const S inv_d = S(1) / (S)p.d;
+  const bool has_in = p.dx_in != nullptr;
+  const uint32_t codes_at = VEC > 1 ? (uint32_t)kX * ring.row_bytes - (16u - VEC) * threadIdx.x : 0u;   // from ring.mine
+  clear(sums);
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.T) {
+      const int64_t off = ring.offset(row);
+      ring.fetch(p.dn, off, stage, kDn);
+      if (!KEPT) {
+        ring.fetch(p.x, off, stage, kX);
+      } else if (VEC > 1) {   // VEC bytes per vector, copied by the thread that reads them
+        const uint32_t dst = ring.mine + (uint32_t)stage * ring.stage_bytes + codes_at;
+        const uint8_t *src = p.codes + row * p.d + VEC * threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+          if (ring.has(i))
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst + i * VEC * blockDim.x),
+                         "l"(src + i * VEC * blockDim.x), "n"(VEC > 1 ? VEC : 4)
+                         : "memory");
+        }
+      }
+      if (has_in) ring.fetch(p.dx_in, off, stage, kIn);
+    }
+    ring.commit();
+  };
+  L acc_w[ITER][N], acc_b[ITER][N];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) acc_w[i][c] = acc_b[i][c] = splat<L>(0.0f);
+  }
+  for (int s = 0; s < ring.stages - 1; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  L hold_w[kHold ? ITER : 1][N];
+  if (kHold) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i)
+      if (ring.has(i)) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, hold_w[kHold ? i : 0]);
+  }
+  // the row's statistics, and the scales of this thread's codes, are read one row ahead
+  float next_m = 0.0f, next_r = 0.0f;
+  uint8_t next_s[KEPT ? ITER : 1];
+  auto ahead = [&](int64_t row) {
+    if (row >= p.T) return;
+    if (!KEPT) next_m = p.mean[row];
+    next_r = p.rstd[row];
+    if (KEPT) {
+#pragma unroll
+      for (int i = 0; i < ITER; ++i)
+        if (ring.has(i)) next_s[KEPT ? i : 0] = p.scales[row * p.nb + (int)(threadIdx.x + i * blockDim.x) * VEC / act8::kBlock];
+    }
+  };
+  ahead(blockIdx.x);
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    if (ring.stages == 1) {
+      if (VEC == 1) __syncthreads();   // every thread has left the row before
+      fetch(row, 0);
+    }
+    S m = next_m, r = next_r;
+    float sc[KEPT ? ITER : 1];
+    if (KEPT) {
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) sc[KEPT ? i : 0] = act8::scale_value(next_s[KEPT ? i : 0]);
+    }
+    ahead(row + gridDim.x);
+    ring.wait();
+    // every thread has left the row before (its own vectors: the thread itself; windows: the barrier in wait())
+    if (ring.stages > 1) fetch(row + (int64_t)(ring.stages - 1) * gridDim.x, ring.freed(stage));
+    const int64_t off = ring.offset(row);
+    const uint32_t here = ring.at(stage, off);
+    const uint32_t codes_here = ring.mine + (uint32_t)stage * ring.stage_bytes + codes_at;
+    if constexpr (kWide && !KEPT) {   // one value per lane
+      S t[1] = {S(0)};
+      L x[N];
+      x[0] = S(0);
+      if (ring.has(0)) V::load_shared(here + kX * ring.row_bytes, x);
+      t[0] = x[0];
+      block_sums(t, sums, half);
+      m = t[0] * inv_d;
+      t[0] = ring.has(0) ? (x[0] - m) * (x[0] - m) : S(0);
+      block_sums(t, sums, half);
+      r = S(1) / sqrt(t[0] * inv_d + (S)p.eps);
+    }
+    // z (without KEPT: before the rest of the mean is taken off) of the i-th vector
+    auto normed = [&](int i, L (&z)[N]) {
+      if constexpr (KEPT) {
+        if constexpr (VEC > 1) {
+          get_codes(codes_here + i * VEC * blockDim.x, z, sc[i]);
+        } else {
+          z[0] = (S)(act8::unpack1(p.codes[row * p.d + threadIdx.x + (int64_t)i * blockDim.x]) * sc[i]);
+        }
+      } else {
+        V::load_shared(here + kX * ring.row_bytes + i * ring.step, z);
+#pragma unroll
+        for (int c = 0; c < N; ++c) z[c] = mul(add(z[c], all(-m, L())), all(r, L()));
+      }
+    };
+    // sums of u, u z, z
+    L t[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) t[i] = splat<L>(0.0f);
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      if (!ring.has(i)) continue;
+      L(&w)[N] = hold_w[kHold ? i : 0];
+      if (!kHold) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, w);
+      L u[N], z[N];
+      V::load_shared(here + kDn * ring.row_bytes + i * ring.step, u);
+      normed(i, z);
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        acc_b[i][c] = add(acc_b[i][c], u[c]);
+        u[c] = mul(u[c], w[c]);
+        t[0] = add(t[0], u[c]);
+        t[1] = fma(u[c], z[c], t[1]);
+        if (!KEPT) t[2] = add(t[2], z[c]);
+      }
+    }
+    S s[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) s[i] = total(t[i]);
+    block_sums(s, sums, half);
+    const S rest = KEPT ? S(0) : s[2] * inv_d;             // of z's mean, which is zero
+    const S mu = s[0] * inv_d, muz = (s[1] - rest * s[0]) * inv_d;
+    const L R = all(r, L()), Rest = all(-rest, L()), Mu = all(-mu, L()), Muz = all(-muz, L());
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      if (!ring.has(i)) continue;
+      L(&w)[N] = hold_w[kHold ? i : 0];
+      if (!kHold) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, w);
+      L u[N], z[N], g[N];
+      V::load_shared(here + kDn * ring.row_bytes + i * ring.step, u);
+      normed(i, z);
+      if (has_in) {
+        V::load_shared(here + kIn * ring.row_bytes + i * ring.step, g);
+      } else {
+#pragma unroll
+        for (int c = 0; c < N; ++c) g[c] = splat<L>(0.0f);
+      }
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        if (!KEPT) z[c] = add(z[c], Rest);
+        acc_w[i][c] = fma(u[c], z[c], acc_w[i][c]);
+        g[c] = fma(fma(z[c], Muz, fma(u[c], w[c], Mu)), R, g[c]);
+      }
+      V::store(reinterpret_cast<T *>((uint8_t *)p.dx + off + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step), g);
+    }
+    if (++stage == ring.stages) stage = 0;
+  }
+  start_next();   // the kernel that adds up the partial rows
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    if (!ring.has(i)) continue;
+    float *dst = p.part + (int64_t)blockIdx.x * p.d + (int64_t)(threadIdx.x + i * blockDim.x) * VEC;
+    put_part(dst, acc_w[i]);
+    put_part(dst + (int64_t)gridDim.x * p.d, acc_b[i]);
+  }
+}
+
+// n = z w + b of kept rows. A thread keeps its columns (VEC of them) and takes every `step`-th row.
+constexpr int kRestoreThreads = 256;
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kRestoreThreads) ln_restore_kernel(const uint8_t *__restrict__ codes,
+                                                                     const uint8_t *__restrict__ scales,
+                                                                     const T *__restrict__ w, const T *__restrict__ b, int64_t T_,
+                                                                     int d, int nb, int64_t step, T *__restrict__ n) {
+  using V = Lanes<T, VEC, float>;
+  using L = typename V::L;
+  constexpr int N = V::N;
+  const int cols = d / VEC;
+  const int64_t id = (int64_t)blockIdx.x * kRestoreThreads + threadIdx.x;
+  const int64_t row0 = id / cols;
+  const int col = (int)(id - row0 * cols) * VEC;
+  if (row0 >= step) return;
+  L W[N], B[N];
+  V::load(w + col, W);
+  if (b) {
+    V::load(b + col, B);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) B[c] = splat<L>(0.0f);
+  }
+  constexpr int kRows = 4;   // in flight
+  for (int64_t r0 = row0; r0 < T_; r0 += kRows * step) {
+    uint32_t q[kRows][VEC >= 4 ? VEC / 4 : 1];
+    float sc[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t r = r0 + k * step;
+      if (r >= T_) continue;
+      const uint8_t *src = codes + r * d + col;
+      if constexpr (VEC == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+        q[k][0] = v.x;
+        q[k][VEC >= 8 ? 1 : 0] = v.y;
+      } else if constexpr (VEC == 4) {
+        q[k][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+      } else {
+        q[k][0] = __ldg(src);
+      }
+      sc[k] = act8::scale_value(__ldg(scales + r * nb + col / act8::kBlock));
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t r = r0 + k * step;
+      if (r >= T_) continue;
+      L v[N];
+      if constexpr (VEC == 1) {
+        v[0] = act8::unpack1((uint8_t)q[k][0]) * sc[k];
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+          float f[4];
+          act8::unpack4(q[k][i], f);
+          v[2 * i] = mul(pair(f[0], f[1]), pair(sc[k], sc[k]));
+          v[2 * i + 1] = mul(pair(f[2], f[3]), pair(sc[k], sc[k]));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[c] = fma(v[c], W[c], B[c]);
+      V::store(n + r * d + col, v);
+    }
+  }
+}
+
+template <typename T, int VEC, int ITER> static int ln_launch_fwd(const LnFwdParams &p, const Shape &sh, cudaStream_t s) {
+  int64_t grid = (int64_t)sm_count() * per_sm(sh, 1, sh.iter == 1 ? 2 * kMaxThreads : kMaxThreads);
+  if (grid > p.T) grid = p.T;
+  if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true>>(p, sh, 1, (int)grid, s);
+  return launch<ln_fwd_kernel<T, VEC, ITER, false>>(p, sh, 1, (int)grid, s);
+}
+template <typename T, int VEC, int ITER, typename S = float>
+static int ln_launch_bwd(const LnBwdParams &p, const Shape &sh, int grid, cudaStream_t s) {
+  const int tensors = p.dx_in ? 3 : 2;
+  if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S>>(p, sh, tensors, grid, s);
+  return launch<ln_bwd_kernel<T, VEC, ITER, false, S>>(p, sh, tensors, grid, s);
+}
+template <typename T, int VEC>
+static int ln_launch_restore(const void *codes, const void *scales, const void *w, const void *b, int64_t T_, int d, void *n,
+                             cudaStream_t s) {
+  const int cols = d / VEC;
+  int64_t step = ((int64_t)sm_count() * 8 * kRestoreThreads + cols - 1) / cols;   // eight blocks per SM, about
+  if (step > T_) step = T_;
+  const int64_t grid = (step * cols + kRestoreThreads - 1) / kRestoreThreads;
+  ln_restore_kernel<T, VEC><<<(unsigned)grid, kRestoreThreads, 0, s>>>((const uint8_t *)codes, (const uint8_t *)scales,
+                                                                       (const T *)w, (const T *)b, T_, d,
+                                                                       (int)act8::blocks_of(d), step, (T *)n);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
+// Blocks of the backward: each leaves a partial row, so no more than the GPU holds at once (of a GB300's SMs, wherever the
+// workspace's size is asked for).
+static int ln_bwd_blocks(int64_t T, const Shape &s, int tensors) {
+  int64_t b = 152 * per_sm(s, tensors, s.vec == 1 && s.iter <= 4 ? 2 * kMaxThreads : kMaxThreads);
+  if (b > T) b = T;
+  return b < 1 ? 1 : (int)b;
+}
+
+#define MOE_LN_DISPATCH(FN, ...)                                                     \
+  do {                                                                               \
+    if (dtype == MOE_BF16) {                                                         \
+      if (sh.vec == 8 && sh.iter == 1) rc = FN<__nv_bfloat16, 8, 1>(__VA_ARGS__);    \
+      else if (sh.vec == 8) rc = FN<__nv_bfloat16, 8, 2>(__VA_ARGS__);               \
+      else if (sh.iter == 4) rc = FN<__nv_bfloat16, 1, 4>(__VA_ARGS__);              \
+      else rc = FN<__nv_bfloat16, 1, 16>(__VA_ARGS__);                               \
+    } else {                                                                         \
+      if (sh.vec == 4 && sh.iter == 1) rc = FN<float, 4, 1>(__VA_ARGS__);            \
+      else if (sh.vec == 4 && sh.iter == 2) rc = FN<float, 4, 2>(__VA_ARGS__);       \
+      else if (sh.vec == 4) rc = FN<float, 4, 4>(__VA_ARGS__);                       \
+      else if (sh.iter == 4) rc = FN<float, 1, 4>(__VA_ARGS__);                      \
+      else rc = FN<float, 1, 16>(__VA_ARGS__);                                       \
+    }                                                                                \
+  } while (0)
+
+}  // namespace norm
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::norm;
+
+extern "C" size_t moe_layer_norm_bwd_workspace_size(int T, int d, int dtype) {
+  if (T < 0 || d < 1 || d > MOE_NORM_MAX_D || (dtype != MOE_F32 && dtype != MOE_BF16)) return 0;
+  const Shape sh = shape_of(d, dtype);
+  const int two = ln_bwd_blocks(T, sh, 2), three = ln_bwd_blocks(T, sh, 3);
+  return (size_t)2 * (two > three ? two : three) * d * sizeof(float) + 256;
+}
+
+extern "C" int moe_layer_norm_fwd(const void *x, const void *w, const void *b, int T, int d, int dtype, float eps, void *n,
+                                  float *mean, float *rstd, void *codes, void *scales, moe_stream_t stream) {
+  int rc = check_shape(T, d, dtype, eps);
+  if (rc) return rc;
+  if ((codes == nullptr) != (scales == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (bad(x) || bad(w) || bad(n) || !aligned16(b) || !aligned16(mean) || !aligned16(rstd) || !aligned16(codes) || !aligned16(scales))
+    return MOE_ERR_INVALID_ARG;
+  LnFwdParams p{};
+  p.x = x;
+  p.w = w;
+  p.b = b;
+  p.n = n;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.codes = (uint8_t *)codes;
+  p.scales = (uint8_t *)scales;
+  p.T = T;
+  p.d = d;
+  p.nb = (int)act8::blocks_of(d);
+  p.eps = eps;
+  const Shape sh = shape_of(d, dtype);
+  MOE_LN_DISPATCH(ln_launch_fwd, p, sh, (cudaStream_t)stream);
+  return rc;
+}
+
+extern "C" int moe_layer_norm_restore(const void *codes, const void *scales, const void *w, const void *b, int T, int d,
+                                      int dtype, void *n, moe_stream_t stream) {
+  int rc = check_shape(T, d, dtype, 1.0f);
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  if (bad(codes) || bad(scales) || bad(w) || !aligned16(b) || bad(n)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == MOE_BF16)
+    return d % 8 == 0 ? ln_launch_restore<__nv_bfloat16, 8>(codes, scales, w, b, T, d, n, s)
+                      : ln_launch_restore<__nv_bfloat16, 1>(codes, scales, w, b, T, d, n, s);
+  return d % 4 == 0 ? ln_launch_restore<float, 4>(codes, scales, w, b, T, d, n, s)
+                    : ln_launch_restore<float, 1>(codes, scales, w, b, T, d, n, s);
+}
+
+extern "C" int moe_layer_norm_bwd(const void *dn, const void *x, const void *codes, const void *scales, const float *mean,
+                                  const float *rstd, const void *w, const void *dx_in, int T, int d, int dtype, float eps,
+                                  void *dx, void *dw, void *db, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_shape(T, d, dtype, eps);
+  if (rc) return rc;
+  if (bad(w) || bad(dw) || !aligned16(db) || bad(ws) || ((uintptr_t)ws & 255) ||
+      ws_bytes < moe_layer_norm_bwd_workspace_size(T, d, dtype))
+    return MOE_ERR_INVALID_ARG;
+  const bool kept = codes != nullptr;
+  if ((scales != nullptr) != kept || (kept && x)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (bad(dn) || bad(rstd) || bad(dx) || (dx_in && bad(dx_in)) ||
+                (kept ? bad(codes) || bad(scales) : bad(x) || bad(mean))))
+    return MOE_ERR_INVALID_ARG;
+  LnBwdParams p{};
+  p.dn = dn;
+  p.x = x;
+  p.dx_in = dx_in;
+  p.w = w;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.codes = (const uint8_t *)codes;
+  p.scales = (const uint8_t *)scales;
+  p.dx = dx;
+  p.part = static_cast<float *>(ws);
+  p.T = T;
+  p.d = d;
+  p.nb = (int)act8::blocks_of(d);
+  p.eps = eps;
+  cudaStream_t s = (cudaStream_t)stream;
+  Shape sh = shape_of(d, dtype);
+  const int grid = ln_bwd_blocks(T, sh, dx_in ? 3 : 2);
+  if (d <= 32) {   // one value per lane, in 64 bits
+    sh.vec = sh.iter = 1;
+    sh.threads = 32;
+    sh.row_bytes = ((uint32_t)d * (uint32_t)dtype_size(dtype) + 15) / 16 * 16 + 16;
+    if (dtype == MOE_BF16) rc = ln_launch_bwd<__nv_bfloat16, 1, 1, double>(p, sh, grid, s);
+    else rc = ln_launch_bwd<float, 1, 1, double>(p, sh, grid, s);
+  } else {
+    MOE_LN_DISPATCH(ln_launch_bwd, p, sh, grid, s);
+  }
+  if (rc) return rc;
+  const dim3 g((d + 31) / 32, db ? 2 : 1);
+  if (dtype == MOE_BF16) {
+    using B = __nv_bfloat16;
+    MOE_TRY_CUDA(launch_after(norm_bwd_sum_kernel<B>, g, dim3(1024), 0, s, (const float *)p.part, grid, d, (int)MOE_GATE_NONE,
+                              (const B *)nullptr, (const B *)nullptr, (B *)dw, (B *)db, (B *)nullptr));
+  } else {
+    MOE_TRY_CUDA(launch_after(norm_bwd_sum_kernel<float>, g, dim3(1024), 0, s, (const float *)p.part, grid, d,
+                              (int)MOE_GATE_NONE, (const float *)nullptr, (const float *)nullptr, (float *)dw, (float *)db,
+                              (float *)nullptr));
+  }
+  return MOE_OK;
+}
