@@ -477,8 +477,45 @@ int moe_layer_norm_bwd(const void *dn, const void *x, const void *codes, const v
                        void *dw, void *db, void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * Gated feed-forward block: the expert that every token takes, beside or in the place of the routed ones.
+ *   x          [T, d]
+ *   w_gate_up  [2f, d]  rows 0..f-1: gate projection Wg; rows f..2f-1: up projection Wu
+ *   w_down     [d, f]   Wd
+ *   a = x Wg^T, b = x Wu^T, h = act(a) b, y = y_in + h Wd^T            (y_in NULL: zero; y may be y_in)
+ *   act        MOE_ACT_SILU: a sigma(a); MOE_ACT_GELU: 0.5 a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3)))
+ *   keep       what the forward leaves for a backward: MOE_KEEP_NONE (ab, ab_scales NULL), MOE_KEEP_ALL (ab [T, 2f] in
+ *              dtype: a, then b; the backward also reads h), or MOE_KEEP_F8 (ab [T, 2f] codes, ab_scales
+ *              [moe_act8_scale_bytes(T, 2f)]: a, b in 8 bits, rounded once from fp32; h is scratch, and the backward writes
+ *              into its h, scratch as well, what the kept a, b make of it)
+ *   h          [T, f]
+ * Backward, with dy [T, d] and what the forward kept:
+ *   dh = dy Wd, da = dh b act'(a), db = dh act(a);  dab [T, 2f] (scratch and output) = da, db
+ *   dx = dx_in + [da | db] w_gate_up (dx_in NULL: zero; dx may be dx_in), dw_gate_up = [da | db]^T x, dw_down = dy^T h
+ * Weight gradients are overwritten; T = 0 makes them zeros.
+ * bf16: tensor cores, fp32 accumulation, every output rounded once; h and dab are rounded to bf16 between the products.
+ * Requires d % 8 == 0 and f % 8 == 0 (MOE_KEEP_F8: f % 32 == 0). Up to 64 tokens with MOE_KEEP_NONE take a path bound by
+ * reading the weights once. fp32: true fp32 FMA, any d, f >= 1; MOE_KEEP_F8 is for bf16 only.
+ * d, f at most MOE_FFN_MAX, T at most MOE_FFN_MAX_T. Results repeat bit for bit.
+ * ws: moe_ffn_workspace_size(...) bytes, 256-byte aligned; zeros before its first use (it holds arrival counts that every call
+ * leaves at zero, and the status word). Calls that may overlap on the GPU need one each; a call that reported an error
+ * leaves it to be zeroed again. Device errors: MOE_ERR_DEVICE_TIMEOUT (bf16: every wait is bounded to about 0.2 s).
+ * Except y == y_in and dx == dx_in, outputs may not overlap inputs.
+ */
+#define MOE_FFN_MAX (1 << 20)
+#define MOE_FFN_MAX_T (1 << 22)
+enum moe_act { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1 };
+enum moe_keep { MOE_KEEP_NONE = 0, MOE_KEEP_ALL = 1, MOE_KEEP_F8 = 2 };
+size_t moe_ffn_workspace_size(int T, int d, int f, int dtype, int backward);
+int moe_ffn_fwd(const void *x, const void *w_gate_up, const void *w_down, const void *y_in, int T, int d, int f, int dtype,
+                int act, int keep, void *ab, void *ab_scales, void *h, void *y, void *ws, size_t ws_bytes,
+                moe_stream_t stream);
+int moe_ffn_bwd(const void *dy, const void *x, const void *ab, const void *ab_scales, void *h, const void *w_gate_up,
+                const void *w_down, const void *dx_in, int T, int d, int f, int dtype, int act, int keep, void *dab,
+                void *dx, void *dw_gate_up, void *dw_down, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Synchronises `stream`, then returns the device status word at the start of a workspace used by
- * moe_count_index, moe_grouped_ffn_* or moe_router_*: MOE_OK or a negative moe_status. Not for
+ * moe_count_index, moe_grouped_ffn_*, moe_router_* or moe_ffn_*: MOE_OK or a negative moe_status. Not for
  * the hot path.
  */
 int moe_read_status(const void *ws, moe_stream_t stream);

@@ -4,12 +4,13 @@ GEMM on tcgen05 tensor cores, and the weighted combine, forward and backward, be
 include/moe.h. MoELayer holds one layer's buffers and call order (and can record a pass as a CUDA
 graph); HostPipeline runs passes from pinned host memory with the copies overlapped. Around the layer:
 BlockNorms (the norms before and after it, with the gate and the residual), AdamW (one step over many
-tensors, states in fp32 or 8 bits), MoELayerFp4 / Fp4Weights (serving with MXFP4 experts), LayerNorm, and
-act8_quantize / act8_dequantize (activations kept in 8 bits)."""
+tensors, states in fp32 or 8 bits), MoELayerFp4 / Fp4Weights (serving with MXFP4 experts), LayerNorm, GatedFFN
+(the dense gated feed-forward block, which every token takes), and act8_quantize / act8_dequantize (activations kept in 8 bits)."""
 from . import _lib
 from ._lib import MoeError
 from .act8 import act8_dequantize, act8_quantize
 from .block import BlockNorms
+from .ffn import GatedFFN
 from .fp4 import Fp4Weights, MoELayerFp4, fp4_dequantize, fp4_quantize
 from .layer import MoELayer
 from .layer_norm import LayerNorm
@@ -17,4 +18,4 @@ from .optim import AdamW
 from .pipeline import HostPipeline
 
 __all__ = ["MoELayer", "HostPipeline", "BlockNorms", "AdamW", "MoELayerFp4", "Fp4Weights", "fp4_quantize",
-           "fp4_dequantize", "LayerNorm", "act8_quantize", "act8_dequantize", "MoeError", "_lib"]
+           "fp4_dequantize", "LayerNorm", "GatedFFN", "act8_quantize", "act8_dequantize", "MoeError", "_lib"]

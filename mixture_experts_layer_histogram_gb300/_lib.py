@@ -22,6 +22,8 @@ MAX_TOPK = 16
 NORM_MAX_D = 8192
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 ADAMW_F32, ADAMW_F8 = 0, 1
+ACT_SILU, ACT_GELU = 0, 1
+KEEP_NONE, KEEP_ALL, KEEP_F8 = 0, 1, 2
 ADAMW_BLOCK = 256
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED", -3: "MOE_ERR_CUDA",
           -4: "MOE_ERR_DEVICE_TIMEOUT", -5: "MOE_ERR_BAD_INDEX", -6: "MOE_ERR_CHECK_FAILED"}
@@ -85,6 +87,9 @@ _SIGS = {
     "moe_layer_norm_restore": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P]),
     "moe_layer_norm_bwd_workspace_size": (_SZ, [_I, _I, _I]),
     "moe_layer_norm_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _P, _SZ, _P]),
+    "moe_ffn_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_ffn_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_ffn_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_read_status": (_I, [_P, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_version": (_I, []),
@@ -575,6 +580,49 @@ def moe_layer_norm_bwd(dn, x, codes, scales, mean, rstd, w, dx_in, dx, dw, db, w
         None if scales is None else _bytes_at_least("scales", scales, _scale_bytes8(T, d)), _opt("mean", mean, f32, (T,)),
         _ptr("rstd", rstd, f32, (T,)), _ptr("w", w, dt, vec), _opt("dx_in", dx_in, dt, rows), T, d, dtype_code(dt), eps,
         _ptr("dx", dx, dt, rows), _ptr("dw", dw, dt, vec), _opt("db", db, dt, vec), _p(ws),
+        ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_ffn_workspace_size(T, d, f, dtype, backward):
+    return int(lib().moe_ffn_workspace_size(T, d, f, dtype, int(bool(backward))))
+
+
+def _kept(ab, ab_scales, dt, T, f):
+    """What `keep` says, and the addresses of ab and ab_scales: nothing, ab in dt, or codes and scales."""
+    if ab is None:
+        if ab_scales is not None:
+            raise ValueError("ab_scales belong to an ab in 8 bits")
+        return KEEP_NONE, None, None
+    if ab_scales is None:
+        return KEEP_ALL, _ptr("ab", ab, dt, (T, 2 * f)), None
+    return KEEP_F8, _ptr("ab", ab, _U8, (T, 2 * f)), _bytes_at_least("ab_scales", ab_scales, _scale_bytes8(T, 2 * f))
+
+
+def moe_ffn_fwd(x, w_gate_up, w_down, y_in, ab, ab_scales, h, y, ws, act=ACT_SILU, stream=None):
+    """y = y_in + (act(x Wg^T) * (x Wu^T)) Wd^T, x [T, d], w_gate_up [2f, d], w_down [d, f]. y_in may be None, and may be y.
+    ab: None (nothing kept), [T, 2f] in x's type, or [T, 2f] uint8 codes with ab_scales. h [T, f] is written."""
+    T, d = x.shape
+    f, dt = w_down.shape[1], x.dtype
+    _here(x, w_gate_up, w_down, y_in, ab, ab_scales, h, y, ws)
+    keep, ab_p, sc_p = _kept(ab, ab_scales, dt, T, f)
+    _ok("moe_ffn_fwd", lib().moe_ffn_fwd(
+        _ptr("x", x, dt, (T, d)), _ptr("w_gate_up", w_gate_up, dt, (2 * f, d)), _ptr("w_down", w_down, dt, (d, f)),
+        _opt("y_in", y_in, dt, (T, d)), T, d, f, dtype_code(dt), act, keep, ab_p, sc_p, _ptr("h", h, dt, (T, f)),
+        _ptr("y", y, dt, (T, d)), _p(ws), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_ffn_bwd(dy, x, ab, ab_scales, h, w_gate_up, w_down, dx_in, dab, dx, dw_gate_up, dw_down, ws, act=ACT_SILU,
+                stream=None):
+    """Backward of moe_ffn_fwd from the ab (and h, or ab_scales) that it kept; dx_in (may be None, may be dx) is added to dx."""
+    T, d = dy.shape
+    f, dt = w_down.shape[1], dy.dtype
+    _here(dy, x, ab, ab_scales, h, w_gate_up, w_down, dx_in, dab, dx, dw_gate_up, dw_down, ws)
+    keep, ab_p, sc_p = _kept(ab, ab_scales, dt, T, f)
+    _ok("moe_ffn_bwd", lib().moe_ffn_bwd(
+        _ptr("dy", dy, dt, (T, d)), _ptr("x", x, dt, (T, d)), ab_p, sc_p, _ptr("h", h, dt, (T, f)),
+        _ptr("w_gate_up", w_gate_up, dt, (2 * f, d)), _ptr("w_down", w_down, dt, (d, f)), _opt("dx_in", dx_in, dt, (T, d)),
+        T, d, f, dtype_code(dt), act, keep, _ptr("dab", dab, dt, (T, 2 * f)), _ptr("dx", dx, dt, (T, d)),
+        _ptr("dw_gate_up", dw_gate_up, dt, (2 * f, d)), _ptr("dw_down", dw_down, dt, (d, f)), _p(ws),
         ws.numel() * ws.element_size(), _s(stream)))
 
 

@@ -18,7 +18,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 LIB_CHECKS = os.path.join(PKG, "libmoe_checks.so")
 SOURCES = ["route_index.cu", "permute_combine.cu", "gemm_simt.cu", "gemm_tc.cu", "gemm_rows.cu", "router.cu", "norm.cu",
-           "layer_norm.cu", "adamw.cu", "fp4.cu", "fp4_gemm.cu", "fp4_gemm_few.cu", "act8.cu", "api.cu"]
+           "layer_norm.cu", "adamw.cu", "fp4.cu", "fp4_gemm.cu", "fp4_gemm_few.cu", "act8.cu",
+           "ffn.cu", "ffn_gemm.cu", "ffn_few.cu", "ffn_f32.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

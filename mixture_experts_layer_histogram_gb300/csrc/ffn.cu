@@ -1,0 +1,99 @@
+// C-ABI entry points of the gated feed-forward block: checks, then the path for the type and size.
+#include "ffn.cuh"
+
+using namespace moe;
+using namespace moe::ffn;
+
+static bool bad(const void *p) { return !p || !aligned16(p); }
+constexpr size_t kHeader = 256;
+
+static int check(int T, int d, int f, int dtype, int act, int keep) {
+  if (T < 0 || d < 1 || f < 1 || (dtype != MOE_F32 && dtype != MOE_BF16) || (act != MOE_ACT_SILU && act != MOE_ACT_GELU) ||
+      keep < MOE_KEEP_NONE || keep > MOE_KEEP_F8)
+    return MOE_ERR_INVALID_ARG;
+  if (d > MOE_FFN_MAX || f > MOE_FFN_MAX || T > MOE_FFN_MAX_T) return MOE_ERR_UNSUPPORTED;
+  if (dtype == MOE_BF16 && (d % 8 || f % 8)) return MOE_ERR_UNSUPPORTED;
+  if (keep == MOE_KEEP_F8 && (dtype != MOE_BF16 || f % act8::kBlock)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+extern "C" size_t moe_ffn_workspace_size(int T, int d, int f, int dtype, int backward) {
+  if (check(T, d, f, dtype, MOE_ACT_SILU, MOE_KEEP_NONE)) return 0;
+  return kHeader + (dtype == MOE_BF16 ? gemm_workspace(T, d, f, backward != 0) : 0);
+}
+
+static int check_ws(const void *ws, size_t bytes, int T, int d, int f, int dtype, int backward) {
+  return !ws || ((uintptr_t)ws & 255) || bytes < moe_ffn_workspace_size(T, d, f, dtype, backward) ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+
+extern "C" int moe_ffn_fwd(const void *x, const void *w_gate_up, const void *w_down, const void *y_in, int T, int d, int f,
+                           int dtype, int act, int keep, void *ab, void *ab_scales, void *h, void *y, void *ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  int rc = check(T, d, f, dtype, act, keep);
+  if (rc) return rc;
+  if ((rc = check_ws(ws, ws_bytes, T, d, f, dtype, 0))) return rc;
+  if ((ab != nullptr) != (keep != MOE_KEEP_NONE) || (ab_scales != nullptr) != (keep == MOE_KEEP_F8)) {
+    if (T > 0) return MOE_ERR_INVALID_ARG;
+  }
+  if (T == 0) return MOE_OK;
+  if (bad(x) || bad(w_gate_up) || bad(w_down) || bad(h) || bad(y) || !aligned16(y_in) || !aligned16(ab) || !aligned16(ab_scales))
+    return MOE_ERR_INVALID_ARG;
+  Block b{};
+  b.T = T;
+  b.d = d;
+  b.f = f;
+  b.gate = gate_of(act);
+  b.x = x;
+  b.w_gate_up = w_gate_up;
+  b.w_down = w_down;
+  b.add = y_in;
+  b.ab = ab;
+  b.scales = (uint8_t *)ab_scales;
+  b.h = h;
+  b.y = y;
+  b.hdr = (WsHeader *)ws;
+  b.ws = (uint8_t *)ws + kHeader;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == MOE_F32) return f32_fwd(b, s);
+  return keep == MOE_KEEP_NONE && T <= kFewTokens ? few_fwd(b, s) : gemm_fwd(b, s);
+}
+
+extern "C" int moe_ffn_bwd(const void *dy, const void *x, const void *ab, const void *ab_scales, void *h, const void *w_gate_up,
+                           const void *w_down, const void *dx_in, int T, int d, int f, int dtype, int act, int keep, void *dab,
+                           void *dx, void *dw_gate_up, void *dw_down, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  int rc = check(T, d, f, dtype, act, keep);
+  if (rc) return rc;
+  if (keep == MOE_KEEP_NONE) return MOE_ERR_INVALID_ARG;
+  if ((rc = check_ws(ws, ws_bytes, T, d, f, dtype, 1))) return rc;
+  if (bad(dw_gate_up) || bad(dw_down)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (T == 0) {
+    const size_t n = (size_t)d * f * dtype_size(dtype);
+    MOE_TRY_CUDA(cudaMemsetAsync(dw_gate_up, 0, 2 * n, s));
+    MOE_TRY_CUDA(cudaMemsetAsync(dw_down, 0, n, s));
+    return MOE_OK;
+  }
+  if (bad(dy) || bad(x) || bad(ab) || bad(h) || bad(w_gate_up) || bad(w_down) || !aligned16(dx_in) || bad(dab) || bad(dx) ||
+      (ab_scales != nullptr) != (keep == MOE_KEEP_F8) || !aligned16(ab_scales))
+    return MOE_ERR_INVALID_ARG;
+  Block b{};
+  b.T = T;
+  b.d = d;
+  b.f = f;
+  b.gate = gate_of(act);
+  b.x = x;
+  b.w_gate_up = w_gate_up;
+  b.w_down = w_down;
+  b.add = dx_in;
+  b.ab = const_cast<void *>(ab);
+  b.scales = (uint8_t *)const_cast<void *>(ab_scales);
+  b.h = h;
+  b.dy = dy;
+  b.dab = dab;
+  b.dx = dx;
+  b.dw_gate_up = dw_gate_up;
+  b.dw_down = dw_down;
+  b.hdr = (WsHeader *)ws;
+  b.ws = (uint8_t *)ws + kHeader;
+  return dtype == MOE_F32 ? f32_bwd(b, s) : gemm_bwd(b, s);
+}

@@ -1,0 +1,67 @@
+// What the kernels of the gated feed-forward block share (ffn*.cu): the gate's arithmetic and the host entry points.
+//
+//   a = x Wg^T, b = x Wu^T, h = act(a) b, y = h Wd^T
+//
+// Both gates are act(a) = a s, s = sigma(g(a)) with a cubic g: silu g = a, gelu (its tanh form, 0.5 a (1 + tanh(c (a +
+// 0.044715 a^3))), c = sqrt(2 / pi)) g = 2 c (a + 0.044715 a^3), since 0.5 (1 + tanh(v)) = sigma(2 v). So one code
+// path serves both: g = a (k0 + k1 a^2), act' = s + a s (1 - s) (k0 + 3 k1 a^2).
+#pragma once
+
+#include "act8.cuh"
+#include "common.cuh"
+
+namespace moe {
+namespace ffn {
+
+struct Gate {
+  float k0, k1;
+};
+inline Gate gate_of(int act) {
+  const float c2 = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+  return act == MOE_ACT_GELU ? Gate{c2, c2 * 0.044715f} : Gate{1.0f, 0.0f};
+}
+
+// sigma(z) for the bf16 outputs (sigmoidf_), and with full fp32 accuracy for fp32 ones
+template <bool EXACT> __device__ __forceinline__ float sigma(float z) {
+  if (EXACT) return 1.0f / (1.0f + expf(-z));
+  return sigmoidf_(z);
+}
+// a^2, held below infinity: times k1 = 0 it has to stay 0, and at 1e30 the sigmoid has long been 0 or 1
+__device__ __forceinline__ float square_of(float a) { return fminf(a * a, 1e30f); }
+template <bool EXACT = false> __device__ __forceinline__ float gated(float a, const Gate &k) {
+  return a * sigma<EXACT>(a * fmaf(k.k1, square_of(a), k.k0));
+}
+// act(a) and act'(a)
+template <bool EXACT = false> __device__ __forceinline__ void gate_and_slope(float a, const Gate &k, float &act, float &slope) {
+  const float q = square_of(a), s = sigma<EXACT>(a * fmaf(k.k1, q, k.k0));
+  act = a * s;
+  slope = fmaf(act * (1.0f - s), fmaf(3.0f * k.k1, q, k.k0), s);
+}
+
+// One call's sizes and buffers (see moe.h). bf16 and fp32 share it.
+struct Block {
+  int T, d, f;
+  Gate gate;
+  const void *x, *w_gate_up, *w_down, *add;   // add: y_in, or dx_in
+  void *ab;                                   // [T, 2f] in dtype, or 8-bit codes with `scales`; null: not kept
+  uint8_t *scales;
+  void *h, *y;
+  const void *dy;
+  void *dab, *dx, *dw_gate_up, *dw_down;
+  WsHeader *hdr;
+  void *ws;                                   // past the header
+};
+
+// bf16, tensor cores (ffn_gemm.cu)
+size_t gemm_workspace(int T, int d, int f, bool backward);
+int gemm_fwd(const Block &b, cudaStream_t s);
+int gemm_bwd(const Block &b, cudaStream_t s);
+// bf16, few tokens: forward that keeps nothing (ffn_few.cu)
+constexpr int kFewTokens = 64;
+int few_fwd(const Block &b, cudaStream_t s);
+// fp32 (ffn_f32.cu)
+int f32_fwd(const Block &b, cudaStream_t s);
+int f32_bwd(const Block &b, cudaStream_t s);
+
+}  // namespace ffn
+}  // namespace moe

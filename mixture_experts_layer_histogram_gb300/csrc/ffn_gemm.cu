@@ -1,0 +1,687 @@
+// The gated feed-forward block's matrix products in bf16 on CTA pairs (sm_103a, tcgen05.mma.cta_group::2).
+//
+//   GATEUP  [a | b] = x [Wg | Wu]^T; the epilogue forms h = act(a) b from the fp32 accumulators, and keeps a, b (bf16, or
+//           8-bit codes with a power of two per 32 values) where a backward follows
+//   DOWN    y = h Wd^T (+ y_in)
+//   DH      dh = dy Wd; the epilogue reads the kept a, b and writes da = dh b act'(a), db = dh act(a) (from 8-bit codes also
+//           h again, which the weight gradient needs)
+//   DX      dx = [da | db] [Wg; Wu] (+ dx_in)
+//   WGRAD   dW = P^T Q over the tokens (dWd = dy^T h, dWgu = [da | db]^T x), both operands read MN-major
+//
+// A pair computes 256 x 256 outputs: each CTA holds 128 rows of A and half of B's 256 rows per 64-deep ring stage (32 KB for
+// 256 x 256 x 64 x 2 flops a pair, the ratio of bytes to flops at which the L2 just keeps up) and 128 x 256 accumulators
+// in its own TMEM, twice (512 columns), so the epilogue of one tile runs beside the products of the next.
+// GATEUP's B is 128 gate rows in one CTA and the same features' 128 up rows in the other: every thread of the epilogue
+// (a TMEM lane is a token) holds a and b of the same features, a whole block of 32 at a time for the 8-bit codes.
+//
+// Work is dealt to the C pairs in whole rounds of C tiles; the tiles of the last, incomplete round (all of them, for small
+// products) are cut along K into S parts, so that the pairs share what would leave most of them idle. A part leaves its
+// fp32 accumulators in the workspace, and the warp that brings the last part of its 32 x 128 outputs adds the
+// parts up in their order (so the result does not depend on which came last) and goes on as if it had read TMEM.
+// Nobody waits: an arrival count per slice, set back to zero by the warp that finds it complete, decides.
+//
+// Roles per CTA: warp 0 loads (TMA), warp 1 allocates TMEM and, in the leader, issues the products, warps 2..9 are the epilogue.
+// Every wait is bounded (0.2 s): on timeout the kernel records MOE_ERR_DEVICE_TIMEOUT, lets copies in flight
+// land, frees TMEM and leaves. Kernels of one call are launched as dependents of one another: set-up overlaps the tail of
+// the one before.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "dependent.cuh"
+#include "ffn.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+
+namespace moe {
+namespace tc {
+namespace ffng {
+
+using ffn::Gate;
+
+enum Kind { GATEUP = 0, DOWN = 1, DH = 2, DX = 3, WGRAD = 4 };
+
+constexpr int TILE = 256;                       // rows and columns of a pair's tile
+constexpr int HALF = TILE / 2;                  // a CTA's rows of A, and of B
+constexpr int BK = 64;
+constexpr int OPERAND = HALF * BK * 2;          // bytes of one operand per stage
+constexpr int STAGE = 2 * OPERAND;
+constexpr int STAGES = 6;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int BUF = 32 * 32 * 2;                // one 32 x 32 block of bf16
+constexpr int NBARS = 2 * STAGES + 5;
+constexpr int SMEM = STAGES * STAGE + EPI_WARPS * BUF + 1024 + 8 * NBARS + 16;
+static_assert(SMEM <= 232448, "shared memory exceeds 227 KB");
+constexpr int SLICES = 2 * EPI_WARPS;           // of a tile: one per epilogue warp of the pair, 32 rows x 128 columns
+constexpr int SLICE_FLOATS = 32 * HALF;
+constexpr int MAX_SPLIT = 8;
+
+struct Params {
+  WsHeader *hdr;
+  int M, N;                  // valid rows; valid columns (GATEUP, DH: f)
+  int m_tiles, n_tiles, num_kb;
+  bool more;                 // another kernel of the same call follows
+  int full, splits, units;   // tiles computed whole, parts of each of the others, units of work in all
+  float4 *part;              // [tile - full][part][slice][4][8][32] float4
+  int *arrived;              // [tile - full][slice]
+  Gate gate;
+  __nv_bfloat16 *out0;       // GATEUP: kept ab (null: not kept, or in 8 bits); DH: dab; else the result
+  __nv_bfloat16 *out1;       // GATEUP: h; DH from 8 bits: h
+  const __nv_bfloat16 *in0;  // DH: kept ab; DOWN, DX: what is added (null: nothing)
+  uint8_t *codes, *scales;   // GATEUP, DH: ab in 8 bits (null: bf16)
+};
+
+// One unit of work: a tile and its k-blocks.
+struct Unit {
+  int tile, m, n, kb0, kb1;
+  int part;                  // -1: the whole tile
+};
+
+// Tiles are numbered in bands of eight rows of tiles, column by column inside a band: the tiles that run at the same
+// time share few rows of A and few columns of B.
+constexpr int BAND = 8;
+__device__ __forceinline__ bool unit_of(int u, const Params &p, Unit &t) {
+  if (u >= p.units) return false;
+  t.part = -1;
+  t.tile = u;
+  t.kb0 = 0;
+  t.kb1 = p.num_kb;
+  if (u >= p.full && p.splits > 1) {
+    const int r = u - p.full, q = r / p.splits;
+    t.tile = p.full + q;
+    t.part = r - q * p.splits;
+    t.kb0 = (int)((int64_t)p.num_kb * t.part / p.splits);
+    t.kb1 = (int)((int64_t)p.num_kb * (t.part + 1) / p.splits);
+  }
+  const int per = BAND * p.n_tiles, band = t.tile / per, r = t.tile - band * per;
+  const int height = min(BAND, p.m_tiles - band * BAND);
+  t.n = r / height;
+  t.m = band * BAND + (r - t.n * height);
+  return true;
+}
+
+// kind::f16: D fp32, A and B bf16, M = 256, N = 256
+__host__ __device__ constexpr uint32_t idesc(bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+}
+
+// TMEM has been read (wait::ld): nothing in memory is handed over, so the arrival need not wait for this warp's stores
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
+}
+
+// A 32 x 32 block, a row per lane, to rows row0.. and columns col.. of a row-major output; rows from `rows` and columns from
+// `cols` on are left out. Through shared memory (64-byte swizzle), so that four lanes write 64 consecutive bytes of a row.
+__device__ __forceinline__ void put32(uint32_t buf, int lane, __nv_bfloat16 *out, int64_t ld, int row0, int rows, int col,
+                                      int cols, const float *v) {
+  const uint32_t row = buf + (uint32_t)lane * 64, sw = (uint32_t)(lane >> 1) & 3u;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint4 q = pack_bf16x8(v + 8 * c);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ sw) << 4)), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                 : "memory");
+  }
+  __syncwarp();
+  const int q = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int rr = (lane >> 2) + 8 * i;
+    const uint4 val = ld_shared_v4(buf + (uint32_t)rr * 64 + (((uint32_t)q ^ (((uint32_t)rr >> 1) & 3u)) << 4));
+    if (row0 + rr < rows && col + 8 * q < cols) *reinterpret_cast<uint4 *>(out + (int64_t)(row0 + rr) * ld + col + 8 * q) = val;
+  }
+  __syncwarp();
+}
+
+// This lane's 32 values of a row of a bf16 matrix; columns from `cols` on, and rows that do not exist, read as zero.
+__device__ __forceinline__ void get32(const __nv_bfloat16 *row, bool live, int col, int cols, uint4 (&q)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    q[c] = make_uint4(0, 0, 0, 0);
+    if (live && col + 8 * c < cols) q[c] = *reinterpret_cast<const uint4 *>(row + col + 8 * c);
+  }
+}
+__device__ __forceinline__ void unpack32(const uint4 (&q)[4], float *v) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) unpack_bf16x8(q[c], v + 8 * c);
+}
+
+// 32 values, one whole block, to their codes and scale
+__device__ __forceinline__ void put_block8(uint8_t *codes, uint8_t *scale, const float *v) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  const uint32_t byte = act8::scale_byte(top);
+  const float inv = act8::inv_scale(byte);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = act8::pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    if (byte == 255u) w[i] = 0;
+  }
+  reinterpret_cast<uint4 *>(codes)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4 *>(codes)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  *scale = (uint8_t)byte;
+}
+__device__ __forceinline__ void unpack_block8(const uint4 (&q)[2], float scale, float *v) {
+  const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    act8::unpack4(w[i], v + 4 * i);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[4 * i + c] *= scale;
+  }
+}
+
+// The warp's 32 x 128 outputs of a tile as accumulated: from TMEM, or (`part` not null) the sum of the parts in the workspace.
+// Block j holds columns 32 j .. of the slice.
+struct Slice {
+  uint32_t tmem;             // TMEM address of the first block
+  const float4 *part;
+  int splits;
+  template <int K> __device__ __forceinline__ void load(int j, int lane, float *v) const {
+    if (part == nullptr) {
+      uint32_t r[32];
+      tmem_ld32(tmem + (uint32_t)(K == GATEUP ? (j >> 1) * HALF + 32 * (j & 1) : 32 * j), r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+    const float4 *src = part + (int64_t)j * 8 * 32 + lane;
+    for (int s = 0; s < splits; ++s, src += (int64_t)SLICES * SLICE_FLOATS / 4) {
+      float4 q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = __ldcg(src + i * 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[4 * i] += q[i].x;
+        v[4 * i + 1] += q[i].y;
+        v[4 * i + 2] += q[i].z;
+        v[4 * i + 3] += q[i].w;
+      }
+    }
+  }
+};
+
+// What becomes of the warp's slice: rows row0 .. row0 + 31 (a lane each), columns from col0 on (GATEUP: 64 features from
+// col0 on, a in blocks 0 and 1, b in blocks 2 and 3).
+template <int K>
+__device__ __forceinline__ void finish(const Slice &acc, const Params &p, uint32_t buf, int lane, int row0, int col0) {
+  const int row = row0 + lane;
+  const bool live = row < p.M;
+  if (K == GATEUP) {
+#pragma unroll 1
+    for (int j = 0; j < 2; ++j) {
+      const int col = col0 + 32 * j;
+      float a[32], b[32];
+      acc.load<K>(j, lane, a);
+      acc.load<K>(2 + j, lane, b);
+      if (col >= p.N) continue;
+      const int64_t ld = 2 * (int64_t)p.N;
+      if (p.codes) {
+        if (live) {
+          uint8_t *c = p.codes + row * ld + col, *s = p.scales + (row * ld + col) / act8::kBlock;
+          put_block8(c, s, a);
+          put_block8(c + p.N, s + p.N / act8::kBlock, b);
+        }
+      } else if (p.out0) {
+        put32(buf, lane, p.out0, ld, row0, p.M, col, p.N, a);
+        put32(buf, lane, p.out0 + p.N, ld, row0, p.M, col, p.N, b);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) a[i] = ffn::gated(a[i], p.gate) * b[i];
+      put32(buf, lane, p.out1, p.N, row0, p.M, col, p.N, a);
+    }
+  } else if (K == DH) {
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      const int col = col0 + 32 * j;
+      if (col >= p.N) break;
+      const int64_t ld = 2 * (int64_t)p.N;
+      float a[32], b[32], v[32];
+      if (p.codes) {
+        uint4 qa[2] = {}, qb[2] = {};
+        uint32_t sa = 0, sb = 0;
+        if (live) {
+          const uint8_t *c = p.codes + row * ld + col, *s = p.scales + (row * ld + col) / act8::kBlock;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            qa[i] = reinterpret_cast<const uint4 *>(c)[i];
+            qb[i] = reinterpret_cast<const uint4 *>(c + p.N)[i];
+          }
+          sa = s[0];
+          sb = s[p.N / act8::kBlock];
+        }
+        acc.load<K>(j, lane, v);
+        unpack_block8(qa, act8::scale_value(sa), a);
+        unpack_block8(qb, act8::scale_value(sb), b);
+      } else {
+        uint4 qa[4], qb[4];
+        get32(p.in0 + row * ld, live, col, p.N, qa);
+        get32(p.in0 + row * ld + p.N, live, col, p.N, qb);
+        acc.load<K>(j, lane, v);
+        unpack32(qa, a);
+        unpack32(qb, b);
+      }
+      // a becomes da, v becomes db; with codes b becomes h
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float act, slope;
+        ffn::gate_and_slope(a[i], p.gate, act, slope);
+        a[i] = v[i] * b[i] * slope;
+        v[i] *= act;
+        b[i] *= act;
+      }
+      put32(buf, lane, p.out0, ld, row0, p.M, col, p.N, a);
+      put32(buf, lane, p.out0 + p.N, ld, row0, p.M, col, p.N, v);
+      if (p.codes) put32(buf, lane, p.out1, p.N, row0, p.M, col, p.N, b);
+    }
+  } else {
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      const int col = col0 + 32 * j;
+      if (col >= p.N) break;
+      float v[32];
+      if (K != WGRAD && p.in0) {
+        uint4 q[4];
+        get32(p.in0 + (int64_t)row * p.N, live, col, p.N, q);
+        acc.load<K>(j, lane, v);
+        float w[32];
+        unpack32(q, w);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += w[i];
+      } else {
+        acc.load<K>(j, lane, v);
+      }
+      put32(buf, lane, p.out0, p.N, row0, p.M, col, p.N, v);
+    }
+  }
+}
+
+template <int K>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+  constexpr bool A_MN = K == WGRAD, B_MN = K == DH || K == DX || K == WGRAD;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *epi_smem = smem + STAGES * STAGE;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + EPI_WARPS * BUF);
+  // bars: full[STAGES], empty[STAGES], tfull[2], tempty[2], mma_done
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + NBARS);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t mma_done_bar = bar0 + 8u * (2 * STAGES + 4);
+
+  if (p.more) start_next();   // it may set itself up on SMs that this one has left
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * EPI_WARPS);   // one arrival per epilogue warp of both CTAs
+    }
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+  }
+  if (warp == 1) {   // collective TMEM allocation by one warp of each CTA of the pair
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)), "r"(2 * TILE)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cluster_sync();   // both CTAs: barriers initialised, TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  wait_previous();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer (both CTAs)
+    // The whole warp runs the loop and waits, converged; one elected lane issues the copies.
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    Unit t;
+    for (int u = first; ok && unit_of(u, p, t); u += step) {
+      const int arow = t.m * TILE + (int)rank * HALF;
+      const int brow = K == GATEUP ? (int)rank * p.N + t.n * HALF : t.n * TILE + (int)rank * HALF;
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        if (!mbar_spin_cluster(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 41)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t sA = sbase + stage * STAGE, sB = sA + OPERAND;
+          const uint32_t fb = mapa_shared(full_bar(stage), 0);   // the leader's full barrier
+          if (leader) mbar_expect_tx(full_bar(stage), 2 * STAGE);
+          const int kx = kb * BK;
+          if (A_MN) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) tma_load_2d_pair(sA + q * (BK * 128), &tmA, arow + 64 * q, kx, fb);
+          } else {
+            tma_load_2d_pair(sA, &tmA, kx, arow, fb);
+          }
+          if (B_MN) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) tma_load_2d_pair(sB + q * (BK * 128), &tmB, brow + 64 * q, kx, fb);
+          } else {
+            tma_load_2d_pair(sB, &tmB, kx, brow, fb);
+          }
+        }
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1 && leader) {
+    // ------------------------------------------------------------------ MMA issuer (leader only)
+    // Descriptors are formed once: every shared address lies below 256 KB, so a stage's or a k step's offset adds to the
+    // start-address field without carry. K-major: 32 B per 16-deep step; MN-major: 2048 B per 16 k rows, the two
+    // 64-wide blocks BK * 128 B apart.
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true, issued = false;
+    const uint64_t desc_a = A_MN ? sdesc(sbase, BK * 128, 1024) : sdesc(sbase, 16, 1024);
+    const uint64_t desc_b = B_MN ? sdesc(sbase + OPERAND, BK * 128, 1024) : sdesc(sbase + OPERAND, 16, 1024);
+    Unit t;
+    for (int u = first; ok && unit_of(u, p, t); u += step) {
+      if (!mbar_ready_cluster(tempty_bar(acc), acc_phase ^ 1u) &&
+          !mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.hdr, 42))
+        break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * TILE);
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        if (!mbar_spin_cluster(full_bar(stage), phase, abort_flag, p.hdr, 43)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t so = (uint32_t)(stage * STAGE) >> 4;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_bf16_pair(d_tmem, desc_a + so + ((uint32_t)(kk * (A_MN ? 2048 : 32)) >> 4),
+                          desc_b + so + ((uint32_t)(kk * (B_MN ? 2048 : 32)) >> 4), idesc(A_MN, B_MN),
+                          kb > t.kb0 || kk > 0 ? 1u : 0u);
+          mma_commit_pair(empty_bar(stage), 0x3);   // frees this stage in both CTAs
+        }
+        __syncwarp();
+        issued = true;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) mma_commit_pair(tfull_bar(acc), 0x3);   // both CTAs' accumulators are ready
+      __syncwarp();
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (issued) {   // every MMA must have completed before TMEM is released
+      if (elect_one()) mma_commit_pair(mma_done_bar, 0x1);
+      __syncwarp();
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(mma_done_bar, 0) && global_ns() - t0 < kWaitLimitNs) {}
+    }
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------------ epilogue (both CTAs)
+    const int quarter = warp & 3;                 // TMEM lanes 32 quarter .. 32 quarter + 31
+    const int hh = (warp - 2) >> 2;               // which half of the columns
+    const uint32_t buf = smem_u32(epi_smem) + (uint32_t)(warp - 2) * BUF;
+    const int slice = (int)rank * EPI_WARPS + (warp - 2);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    Unit t;
+    for (int u = first; unit_of(u, p, t); u += step) {
+      if (!mbar_wait_cluster(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 44)) break;
+      tc_fence_after();
+      const uint32_t base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * TILE);
+      Slice s;
+      s.tmem = base + (uint32_t)((K == GATEUP ? 64 : HALF) * hh);
+      s.part = nullptr;
+      s.splits = p.splits;
+      const int row0 = t.m * TILE + (int)rank * HALF + quarter * 32;
+      const int col0 = K == GATEUP ? t.n * HALF + 64 * hh : t.n * TILE + HALF * hh;
+      if (t.part < 0) finish<K>(s, p, buf, lane, row0, col0);
+      else {
+        const int r = t.tile - p.full;
+        float4 *mine = p.part + (((int64_t)r * p.splits + t.part) * SLICES + slice) * (SLICE_FLOATS / 4);
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          float v[32];
+          s.load<K>(j, lane, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            __stcg(mine + (j * 8 + i) * 32 + lane, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader(tempty_bar(acc));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+      if (t.part >= 0) {
+        const int r = t.tile - p.full;
+        __threadfence();   // this lane's part is visible before the arrival
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(p.arrived + r * SLICES + slice, 1);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before == p.splits - 1) {
+          __threadfence();
+          if (lane == 0) p.arrived[r * SLICES + slice] = 0;
+          s.part = p.part + ((int64_t)r * p.splits * SLICES + slice) * (SLICE_FLOATS / 4);
+          finish<K>(s, p, buf, lane, row0, col0);
+        }
+      }
+    }
+  }
+
+  if (*abort_flag) {   // copies that were issued and never waited for land within microseconds
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 1000ull * 1000ull) {}
+  }
+  tc_fence_before();
+  cluster_sync();   // no CTA leaves while its peer may still signal its barriers or use its TMEM
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2 * TILE) : "memory");
+  }
+}
+
+// ----------------------------------------------------------------------------- host side -------
+// How a product's tiles are dealt out. One k-block of a tile takes about 0.29 us; a part that leaves and collects fp32
+// accumulators costs about as much as kPartCost of them.
+constexpr int kPartCost = 8;
+struct Deal {
+  int full, splits, units;
+  size_t bytes;   // of the parts
+};
+static Deal deal(int64_t M, int64_t tiles_n, int num_kb, int pairs) {
+  const int64_t tiles = (M + TILE - 1) / TILE * tiles_n;
+  Deal best{(int)tiles, 1, (int)tiles, 0};
+  const int rem = (int)(tiles % pairs);
+  if (rem == 0) return best;
+  int64_t cost = num_kb;   // of the last round
+  for (int s = 2; s <= MAX_SPLIT && s <= num_kb; ++s) {
+    if (rem * s > 2 * pairs) break;
+    const int64_t c = (int64_t)((rem * s + pairs - 1) / pairs) * ((num_kb + s - 1) / s + kPartCost);
+    if (c < cost) {
+      cost = c;
+      best = Deal{(int)(tiles - rem), s, (int)(tiles - rem) + rem * s, (size_t)rem * s * SLICES * SLICE_FLOATS * 4};
+    }
+  }
+  return best;
+}
+// The pairs that the plan counts on: those of a GB300, wherever it is asked for (the workspace's size follows from it).
+constexpr int kPairs = 76;
+constexpr size_t kArrivedBytes = (size_t)kPairs * SLICES * 4;   // fewer than kPairs tiles are cut
+
+static int64_t up(int64_t n, int64_t k) { return (n + k - 1) / k; }
+
+template <auto KERNEL> static int pairs_resident(int &pairs) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  MOE_TRY_CUDA(cudaGetDevice(&dev));
+  if (dev < 64 && (pairs = known[dev].load(std::memory_order_relaxed)) > 0) return MOE_OK;
+  MOE_TRY_CUDA(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM;
+  if (cudaOccupancyMaxActiveClusters(&pairs, KERNEL, &cfg) != cudaSuccess || pairs < 1) {
+    (void)cudaGetLastError();
+    pairs = sm_count() / 2;
+  }
+  if (dev < 64) known[dev].store(pairs, std::memory_order_relaxed);
+  return MOE_OK;
+}
+
+// M x (n_tiles of columns) outputs over num_kb k-blocks
+template <int K>
+static int launch(const CUtensorMap &a, const CUtensorMap &b, Params p, int64_t n_tiles, const ffn::Block &blk, bool first,
+                  bool last, cudaStream_t s) {
+  const Deal d = deal(p.M, n_tiles, p.num_kb, kPairs);
+  p.m_tiles = (int)up(p.M, TILE);
+  p.n_tiles = (int)n_tiles;
+  p.full = d.full;
+  p.splits = d.splits;
+  p.units = d.units;
+  p.more = !last;
+  p.hdr = blk.hdr;
+  p.gate = blk.gate;
+  p.arrived = (int *)blk.ws;
+  p.part = (float4 *)((uint8_t *)blk.ws + kArrivedBytes);
+  int pairs = 0;
+  const int rc = pairs_resident<ffn_gemm_kernel<K>>(pairs);
+  if (rc) return rc;
+  if (pairs > p.units) pairs = p.units;
+  if (!first) {
+    MOE_TRY_CUDA(launch_after(ffn_gemm_kernel<K>, dim3(2 * pairs), dim3(THREADS), (size_t)SMEM, s, a, b, p));
+  } else {
+    ffn_gemm_kernel<K><<<2 * pairs, THREADS, SMEM, s>>>(a, b, p);
+    MOE_CHECK_LAUNCH();
+  }
+  return MOE_OK;
+}
+
+}  // namespace ffng
+}  // namespace tc
+
+namespace ffn {
+
+using namespace tc;
+using namespace tc::ffng;
+typedef __nv_bfloat16 bf16;
+
+size_t gemm_workspace(int T, int d, int f, bool backward) {
+  size_t most = 0;
+  auto with = [&](int64_t M, int64_t n_tiles, int64_t k) {
+    const Deal dl = deal(M, n_tiles, (int)up(k, BK), kPairs);
+    if (dl.bytes > most) most = dl.bytes;
+  };
+  with(T, up(f, HALF), d);          // GATEUP
+  with(T, up(d, TILE), f);          // DOWN
+  if (backward) {
+    with(T, up(f, TILE), d);        // DH
+    with(T, up(d, TILE), 2 * f);    // DX
+    with(d, up(f, TILE), T);        // dWd
+    with(2 * f, up(d, TILE), T);    // dWgu
+  }
+  return kArrivedBytes + most;
+}
+
+int gemm_fwd(const Block &b, cudaStream_t s) {
+  CUtensorMap mx, mw;
+  if (!make_map(&mx, b.x, b.T, b.d, HALF) || !make_map(&mw, b.w_gate_up, 2 * (uint64_t)b.f, b.d, HALF)) return MOE_ERR_CUDA;
+  Params p{};
+  p.M = b.T;
+  p.N = b.f;
+  p.num_kb = (int)up(b.d, BK);
+  if (b.scales) {
+    p.codes = (uint8_t *)b.ab;
+    p.scales = b.scales;
+  } else {
+    p.out0 = (bf16 *)b.ab;
+  }
+  p.out1 = (bf16 *)b.h;
+  int rc = launch<GATEUP>(mx, mw, p, up(b.f, HALF), b, true, false, s);
+  if (rc) return rc;
+  CUtensorMap mh, md;
+  if (!make_map(&mh, b.h, b.T, b.f, HALF) || !make_map(&md, b.w_down, b.d, b.f, HALF)) return MOE_ERR_CUDA;
+  p = Params{};
+  p.M = b.T;
+  p.N = b.d;
+  p.num_kb = (int)up(b.f, BK);
+  p.in0 = (const bf16 *)b.add;
+  p.out0 = (bf16 *)b.y;
+  return launch<DOWN>(mh, md, p, up(b.d, TILE), b, false, true, s);
+}
+
+int gemm_bwd(const Block &b, cudaStream_t s) {
+  const uint64_t T = b.T, d = b.d, f = b.f;
+  CUtensorMap ma, mb;
+  // da, db (and h, from 8 bits)
+  if (!make_map(&ma, b.dy, T, d, HALF) || !make_map(&mb, b.w_down, d, f, BK)) return MOE_ERR_CUDA;
+  Params p{};
+  p.M = b.T;
+  p.N = b.f;
+  p.num_kb = (int)up(b.d, BK);
+  if (b.scales) {
+    p.codes = (uint8_t *)b.ab;
+    p.scales = b.scales;
+    p.out1 = (bf16 *)b.h;
+  } else {
+    p.in0 = (const bf16 *)b.ab;
+  }
+  p.out0 = (bf16 *)b.dab;
+  int rc = launch<DH>(ma, mb, p, up(b.f, TILE), b, true, false, s);
+  if (rc) return rc;
+  // dx
+  if (!make_map(&ma, b.dab, T, 2 * f, HALF) || !make_map(&mb, b.w_gate_up, 2 * f, d, BK)) return MOE_ERR_CUDA;
+  p = Params{};
+  p.M = b.T;
+  p.N = b.d;
+  p.num_kb = (int)up(2 * (int64_t)b.f, BK);
+  p.in0 = (const bf16 *)b.add;
+  p.out0 = (bf16 *)b.dx;
+  if ((rc = launch<DX>(ma, mb, p, up(b.d, TILE), b, false, false, s))) return rc;
+  // dWd [d, f] = dy^T h
+  if (!make_map(&ma, b.dy, T, d, BK) || !make_map(&mb, b.h, T, f, BK)) return MOE_ERR_CUDA;
+  p = Params{};
+  p.M = b.d;
+  p.N = b.f;
+  p.num_kb = (int)up(b.T, BK);
+  p.out0 = (bf16 *)b.dw_down;
+  if ((rc = launch<WGRAD>(ma, mb, p, up(b.f, TILE), b, false, false, s))) return rc;
+  // dWgu [2f, d] = dab^T x
+  if (!make_map(&ma, b.dab, T, 2 * f, BK) || !make_map(&mb, b.x, T, d, BK)) return MOE_ERR_CUDA;
+  p.M = 2 * b.f;
+  p.N = b.d;
+  p.out0 = (bf16 *)b.dw_gate_up;
+  return launch<WGRAD>(ma, mb, p, up(b.d, TILE), b, false, true, s);
+}
+
+}  // namespace ffn
+}  // namespace moe

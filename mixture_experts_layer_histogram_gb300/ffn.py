@@ -1,0 +1,78 @@
+"""The gated feed-forward block, y = (act(x Wg^T) * (x Wu^T)) Wd^T: the expert that every token takes. Beside a MoELayer it
+adds to the routed experts' output in its place, in a dense block it stands alone.
+
+    ffn = GatedFFN(T, d, f)                                     # training; backward=False: inference
+    y = ffn.forward(x, w_gate_up, w_down, add=layer_out)        # w_gate_up [2f, d]: gate rows first; w_down [d, f]
+    grads = ffn.backward(dy, x, w_gate_up, w_down, add=dx)      # dx, dw_gate_up, dw_down
+
+keep="f8" keeps the gate and up projections in 8 bits between forward and backward (33 bytes per 32 values, and no h)
+instead of in bf16.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib as L
+
+ACTS = {"silu": L.ACT_SILU, "gelu": L.ACT_GELU}
+
+
+class GatedFFN:
+    """Buffers of one block, allocated once and reused every step."""
+
+    def __init__(self, T, d, f, dtype=torch.bfloat16, act="silu", keep=None, backward=True, scratch=None, device="cuda"):
+        """act: "silu" or "gelu" (its tanh form). keep: None (everything the backward reads, in dtype) or "f8". scratch: a
+        dict with "h" [T, f] and "dab" [T, 2f] in dtype, shared with other blocks: dab always may be, h with keep="f8" or
+        without a backward."""
+        if act not in ACTS:
+            raise ValueError(f"act is one of {sorted(ACTS)}, got {act!r}")
+        if keep not in (None, "f8"):
+            raise ValueError(f"keep is None or 'f8', got {keep!r}")
+        if keep and not backward:
+            raise ValueError("keep needs a backward")
+        if not torch.cuda.is_available():
+            raise RuntimeError("GatedFFN needs a CUDA device")
+        self.T, self.d, self.f, self.dtype, self.act, self.keep = T, d, f, dtype, act, keep
+        self.device = torch.device(device)
+        self._act = ACTS[act]
+        scratch = scratch or {}
+        if "h" in scratch and backward and not keep:
+            raise ValueError("without keep the backward reads h: it cannot be shared")
+        act_ = dict(dtype=dtype, device=self.device)
+        u8 = dict(dtype=torch.uint8, device=self.device)
+        code = L.dtype_code(dtype)
+        self.h = scratch["h"] if "h" in scratch else torch.empty((T, f), **act_)
+        self.y = torch.empty((T, d), **act_)
+        self.ws = torch.zeros(L.moe_ffn_workspace_size(T, d, f, code, backward), **u8)
+        self.ab = self.ab_scales = None
+        self.backward_enabled = backward
+        if backward:
+            if keep:
+                self.ab = torch.empty((T, 2 * f), **u8)
+                self.ab_scales = torch.empty(L.moe_act8_scale_bytes(T, 2 * f), **u8)
+            else:
+                self.ab = torch.empty((T, 2 * f), **act_)
+            self.dab = scratch["dab"] if "dab" in scratch else torch.empty((T, 2 * f), **act_)
+            self.dx = torch.empty((T, d), **act_)
+            self.dw_gate_up = torch.empty((2 * f, d), **act_)
+            self.dw_down = torch.empty((d, f), **act_)
+
+    def forward(self, x, w_gate_up, w_down, add=None, out=None, stream=None):
+        """y [T, d] = add + FFN(x), into `out` (which may be add) where it is given."""
+        L._want("x", x, self.dtype, (self.T, self.d))
+        y = self.y if out is None else out
+        L.moe_ffn_fwd(x, w_gate_up, w_down, add, self.ab, self.ab_scales, self.h, y, self.ws, self._act, stream)
+        return y
+
+    def backward(self, dy, x, w_gate_up, w_down, add=None, stream=None):
+        """Gradients from what the last forward kept and its x: dx = add + the block's, dw_gate_up, dw_down."""
+        if not self.backward_enabled:
+            raise RuntimeError("the block was built without backward buffers")
+        L._want("dy", dy, self.dtype, (self.T, self.d))
+        L.moe_ffn_bwd(dy, x, self.ab, self.ab_scales, self.h, w_gate_up, w_down, add, self.dab, self.dx, self.dw_gate_up,
+                      self.dw_down, self.ws, self._act, stream)
+        return dict(dx=self.dx, dw_gate_up=self.dw_gate_up, dw_down=self.dw_down)
+
+    def status(self, stream=None):
+        """Device status word (synchronises)."""
+        return L.moe_read_status(self.ws, stream)
