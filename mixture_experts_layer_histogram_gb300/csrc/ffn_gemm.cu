@@ -15,10 +15,10 @@
 // (a TMEM lane is a token) holds a and b of the same features, a whole block of 32 at a time for the 8-bit codes.
 //
 // Work is dealt to the C pairs in whole rounds of C tiles; the tiles of the last, incomplete round (all of them, for small
-// products) are cut along K into S parts, so that the pairs share what would leave most of them idle. A part leaves its
-// fp32 accumulators in the workspace, and the warp that brings the last part of its 32 x 128 outputs adds the
-// parts up in their order (so the result does not depend on which came last) and goes on as if it had read TMEM.
-// Nobody waits: an arrival count per slice, set back to zero by the warp that finds it complete, decides.
+// products) are cut along K into S parts, so that the pairs share what would leave most of them idle. Of the warps that hold
+// the parts of the same 32 x 128 outputs the last one to claim them finishes them: the others leave their fp32 accumulators
+// in the workspace, it waits until they are there (those warps wait for nothing, so that ends), adds the parts up in
+// their order, its own from TMEM (so the result does not depend on which came last), and sets the counts back to zero.
 //
 // Roles per CTA: warp 0 loads (TMA), warp 1 allocates TMEM and, in the leader, issues the products, warps 2..9 are the epilogue.
 // Every wait is bounded (0.2 s): on timeout the kernel records MOE_ERR_DEVICE_TIMEOUT, lets copies in flight
@@ -49,7 +49,7 @@ constexpr int STAGE = 2 * OPERAND;
 constexpr int STAGES = 6;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int BUF = 32 * 32 * 2;                // one 32 x 32 block of bf16
+constexpr int BUF = 32 * 64 * 2;                // an epilogue warp's block of 32 rows x 64 columns
 constexpr int NBARS = 2 * STAGES + 5;
 constexpr int SMEM = STAGES * STAGE + EPI_WARPS * BUF + 1024 + 8 * NBARS + 16;
 static_assert(SMEM <= 232448, "shared memory exceeds 227 KB");
@@ -64,7 +64,7 @@ struct Params {
   bool more;                 // another kernel of the same call follows
   int full, splits, units;   // tiles computed whole, parts of each of the others, units of work in all
   float4 *part;              // [tile - full][part][slice][4][8][32] float4
-  int *arrived;              // [tile - full][slice]
+  int *arrived;              // [tile - full][slice][2]: parts claimed, parts written
   Gate gate;
   __nv_bfloat16 *out0;       // GATEUP: kept ab (null: not kept, or in 8 bits); DH: dab; else the result
   __nv_bfloat16 *out1;       // GATEUP: h; DH from 8 bits: h
@@ -112,39 +112,130 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
 }
 
-// A 32 x 32 block, a row per lane, to rows row0.. and columns col.. of a row-major output; rows from `rows` and columns from
-// `cols` on are left out. Through shared memory (64-byte swizzle), so that four lanes write 64 consecutive bytes of a row.
-__device__ __forceinline__ void put32(uint32_t buf, int lane, __nv_bfloat16 *out, int64_t ld, int row0, int rows, int col,
-                                      int cols, const float *v) {
-  const uint32_t row = buf + (uint32_t)lane * 64, sw = (uint32_t)(lane >> 1) & 3u;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint4 q = pack_bf16x8(v + 8 * c);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ sw) << 4)), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
-                 : "memory");
+// mbar_wait_cluster in place: across a call, what a warp has asked for ahead would be stored to the stack first, and so waited for
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int *abort_flag, WsHeader *hdr, int where) {
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((i & 15u) != 15u) continue;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      report(hdr, MOE_ERR_DEVICE_TIMEOUT, where);
+      *abort_flag = 1;
+      return false;
+    }
   }
-  __syncwarp();
-  const int q = lane & 3;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int rr = (lane >> 2) + 8 * i;
-    const uint4 val = ld_shared_v4(buf + (uint32_t)rr * 64 + (((uint32_t)q ^ (((uint32_t)rr >> 1) & 3u)) << 4));
-    if (row0 + rr < rows && col + 8 * q < cols) *reinterpret_cast<uint4 *>(out + (int64_t)(row0 + rr) * ld + col + 8 * q) = val;
-  }
-  __syncwarp();
 }
 
-// This lane's 32 values of a row of a bf16 matrix; columns from `cols` on, and rows that do not exist, read as zero.
-__device__ __forceinline__ void get32(const __nv_bfloat16 *row, bool live, int col, int cols, uint4 (&q)[4]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    q[c] = make_uint4(0, 0, 0, 0);
-    if (live && col + 8 * c < cols) q[c] = *reinterpret_cast<const uint4 *>(row + col + 8 * c);
+// Bounded wait of a whole warp until *count is n; what was written before the counts is then visible.
+__device__ __forceinline__ bool wait_count(const int *count, int n, volatile int *abort_flag, WsHeader *hdr) {
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+    if (__all_sync(0xffffffffu, v == n)) return true;
+    const bool late = global_ns() - t0 > kWaitLimitNs;
+    if (__any_sync(0xffffffffu, late || *abort_flag)) {
+      if (late) report(hdr, MOE_ERR_DEVICE_TIMEOUT, 45);
+      *abort_flag = 1;
+      return false;
+    }
   }
 }
-__device__ __forceinline__ void unpack32(const uint4 (&q)[4], float *v) {
+
+// Blocks on their way out and in. A warp holds 32 rows, one per lane; global memory wants consecutive bytes of a row from
+// neighbouring lanes. Blocks therefore pass through shared memory, W = 64 columns wide (128 bytes a row, eight lanes) or 32
+// (64 bytes, four lanes), 16-byte chunks XOR-swizzled so that neither side meets bank conflicts. (Straight from a row per lane,
+// 32 bytes each, needs no shared memory, but 32 lines per instruction slow the ring's own copies: 38 against 33 us for y at
+// 8192 x 2048 x 1024, 52 against 43 for da, db.) Rows from `rows` and columns from `cols` on are left out, and read as zero.
+template <int W> struct Chunk {
+  static constexpr int LANES = W / 8, STEP = 32 / LANES, N = W / 8;   // lanes per row, rows per instruction, instructions
+  static __device__ __forceinline__ uint32_t at(uint32_t buf, int row, int chunk) {
+    const uint32_t sw = W == 64 ? (uint32_t)row & 7u : ((uint32_t)row >> 1) & 3u;
+    return buf + (uint32_t)row * (2 * W) + (((uint32_t)chunk ^ sw) << 4);
+  }
+};
+__device__ __forceinline__ void st_shared_v4(uint32_t a, const uint4 &q) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
+}
+// This lane's row of 32 columns (from chunk c0 on) into the buffer
+template <int W> __device__ __forceinline__ void stage(uint32_t buf, int lane, int c0, const float *v) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) unpack_bf16x8(q[c], v + 8 * c);
+  for (int c = 0; c < 4; ++c) st_shared_v4(Chunk<W>::at(buf, lane, c0 + c), pack_bf16x8(v + 8 * c));
+}
+template <int W> __device__ __forceinline__ void stage(uint32_t buf, int lane, int c0, const uint4 (&q)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) st_shared_v4(Chunk<W>::at(buf, lane, c0 + c), q[c]);
+}
+// The buffer's block to rows row0.. and columns col.. of a row-major output
+template <int W>
+__device__ __forceinline__ void put(uint32_t buf, int lane, __nv_bfloat16 *out, int64_t ld, int row0, int rows, int col, int cols) {
+  using C = Chunk<W>;
+  __syncwarp();
+  const int c = lane % C::LANES, r0 = lane / C::LANES;
+  __nv_bfloat16 *dst = out + (int64_t)(row0 + r0) * ld + col + 8 * c;
+#pragma unroll
+  for (int i = 0; i < C::N; ++i) {
+    const int r = r0 + C::STEP * i;
+    const uint4 q = ld_shared_v4(C::at(buf, r, c));
+    if (row0 + r < rows && col + 8 * c < cols) *reinterpret_cast<uint4 *>(dst + (int64_t)(C::STEP * i) * ld) = q;
+  }
+  __syncwarp();
+}
+// A block of an input as neighbouring lanes load it, asked for long before it is needed, ...
+template <int W>
+__device__ __forceinline__ void fetch(const __nv_bfloat16 *in, int64_t ld, int row0, int rows, int col, int cols, int lane,
+                                      uint4 (&q)[Chunk<W>::N]) {
+  using C = Chunk<W>;
+  const int c = col + 8 * (lane % C::LANES), r0 = row0 + lane / C::LANES;
+  const __nv_bfloat16 *src = in + (int64_t)r0 * ld + c;
+#pragma unroll
+  for (int i = 0; i < C::N; ++i) {
+    q[i] = make_uint4(0, 0, 0, 0);
+    if (r0 + C::STEP * i < rows && c < cols) q[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(C::STEP * i) * ld);
+  }
+}
+// ... into the buffer, and from there as this lane's row: 32 columns from chunk c0 on
+template <int W> __device__ __forceinline__ void spread(uint32_t buf, int lane, const uint4 (&q)[Chunk<W>::N]) {
+  using C = Chunk<W>;
+#pragma unroll
+  for (int i = 0; i < C::N; ++i) st_shared_v4(C::at(buf, lane / C::LANES + C::STEP * i, lane % C::LANES), q[i]);
+  __syncwarp();
+}
+template <int W, bool ADD> __device__ __forceinline__ void take(uint32_t buf, int lane, int c0, float *v) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float w[8];
+    unpack_bf16x8(ld_shared_v4(Chunk<W>::at(buf, lane, c0 + c)), w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 * c + i] = ADD ? v[8 * c + i] + w[i] : w[i];
+  }
+}
+// The same for a 32 x 32 block of codes: two lanes per row (lane: 16-byte column lane % 2 of rows lane / 2 + 16 i).
+__device__ __forceinline__ void fetch_codes(const uint8_t *in, int64_t ld, int row0, int rows, int col, int cols, int lane, uint4 *q) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = row0 + (lane >> 1) + 16 * i;
+    q[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows && col < cols) q[i] = *reinterpret_cast<const uint4 *>(in + (int64_t)r * ld + col + 16 * (lane & 1));
+  }
+}
+__device__ __forceinline__ void take_codes(uint32_t buf, int lane, const uint4 *q, float scale, float *v) {
+  auto at = [&](uint32_t row, uint32_t half) { return buf + row * 32 + ((half ^ ((row >> 2) & 1u)) << 4); };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) st_shared_v4(at((lane >> 1) + 16 * i, lane & 1), q[i]);
+  __syncwarp();
+#pragma unroll
+  for (uint32_t i = 0; i < 2; ++i) {
+    const uint4 w = ld_shared_v4(at(lane, i));
+    act8::unpack4(w.x, v + 16 * i);
+    act8::unpack4(w.y, v + 16 * i + 4);
+    act8::unpack4(w.z, v + 16 * i + 8);
+    act8::unpack4(w.w, v + 16 * i + 12);
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] *= scale;
+  __syncwarp();
 }
 
 // 32 values, one whole block, to their codes and scale
@@ -164,44 +255,100 @@ __device__ __forceinline__ void put_block8(uint8_t *codes, uint8_t *scale, const
   reinterpret_cast<uint4 *>(codes)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   *scale = (uint8_t)byte;
 }
-__device__ __forceinline__ void unpack_block8(const uint4 (&q)[2], float scale, float *v) {
-  const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    act8::unpack4(w[i], v + 4 * i);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) v[4 * i + c] *= scale;
-  }
-}
-
-// The warp's 32 x 128 outputs of a tile as accumulated: from TMEM, or (`part` not null) the sum of the parts in the workspace.
-// Block j holds columns 32 j .. of the slice.
-struct Slice {
+// The warp's 32 x 128 outputs of a tile as accumulated: what TMEM holds, and for a cut tile (`splits` > 1) the sum of that and
+// the other parts in the workspace, always in the parts' order. Block j holds columns 32 j .. of the slice.
+template <int K> struct Slice {
+  static constexpr int64_t kNext = (int64_t)SLICES * SLICE_FLOATS / 4;   // from one part to the next
+  static constexpr bool kAsk = K == GATEUP || K == WGRAD;   // the first other part of the next block is asked for ahead (registers allowing)
   uint32_t tmem;             // TMEM address of the first block
-  const float4 *part;
-  int splits;
-  template <int K> __device__ __forceinline__ void load(int j, int lane, float *v) const {
-    if (part == nullptr) {
-      uint32_t r[32];
-      tmem_ld32(tmem + (uint32_t)(K == GATEUP ? (j >> 1) * HALF + 32 * (j & 1) : 32 * j), r);
-      tmem_ld_wait();
+  const float4 *part;        // part 0
+  int splits, mine;
+  float4 q[kAsk ? 8 : 1];
+  static __device__ __forceinline__ int after(int j) {   // the order in which finish() takes the blocks
+    return K == GATEUP ? (j == 0 ? 2 : (j == 2 ? 1 : 3)) : j + 1;
+  }
+  __device__ __forceinline__ void get(float4 (&to)[8], int j, int p, int lane) const {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 8; ++i) to[i] = __ldcg(part + p * kNext + (j * 8 + i) * 32 + lane);
+  }
+  __device__ __forceinline__ void ask(int j, int lane) {
+    if constexpr (kAsk) {
+      if (splits > 1) get(q, j, mine == 0 ? 1 : 0, lane);
+    }
+  }
+  __device__ __forceinline__ void held(int j, float *v, bool add) const {
+    uint32_t r[32];
+    tmem_ld32(tmem + (uint32_t)(K == GATEUP ? (j >> 1) * HALF + 32 * (j & 1) : 32 * j), r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = add ? v[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
+  }
+  __device__ __forceinline__ void load(int j, int lane, float *v) {
+    if (splits == 1) {
+      held(j, v, false);
       return;
     }
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-    const float4 *src = part + (int64_t)j * 8 * 32 + lane;
-    for (int s = 0; s < splits; ++s, src += (int64_t)SLICES * SLICE_FLOATS / 4) {
-      float4 q[8];
+#pragma unroll 1
+    for (int p = 0; p < splits; ++p) {
+      if (p == mine) {
+        held(j, v, true);
+        continue;
+      }
+      float4 w[8];
+      if (kAsk && p == (mine == 0 ? 1 : 0)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = __ldcg(src + i * 32);
+        for (int i = 0; i < 8; ++i) w[i] = q[kAsk ? i : 0];
+      } else {
+        get(w, j, p, lane);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[4 * i] += q[i].x;
-        v[4 * i + 1] += q[i].y;
-        v[4 * i + 2] += q[i].z;
-        v[4 * i + 3] += q[i].w;
+        v[4 * i] += w[i].x;
+        v[4 * i + 1] += w[i].y;
+        v[4 * i + 2] += w[i].z;
+        v[4 * i + 3] += w[i].w;
+      }
+    }
+    if (j != 3) ask(after(j), lane);
+  }
+};
+
+// What an epilogue warp reads besides the accumulators, asked for while the products still run: what is added (all of it), or
+// the kept a and b of its first block (the others are asked for a block ahead) and all of its scales.
+template <int K> struct Ahead {
+  static constexpr int ADDS = K == DOWN || K == DX ? 2 : 1;
+  uint4 add[ADDS][8];
+  uint4 a[4], b[4];
+  uint32_t sa, sb;           // a byte per block
+  __device__ __forceinline__ void block(const Params &p, int lane, int row0, int col) {   // DH: a, b at col
+    const int64_t ld = 2 * (int64_t)p.N;
+    if (p.codes) {
+      fetch_codes(p.codes, ld, row0, p.M, col, p.N, lane, a);
+      fetch_codes(p.codes + p.N, ld, row0, p.M, col, p.N, lane, b);
+    } else {
+      fetch<32>(p.in0, ld, row0, p.M, col, p.N, lane, a);
+      fetch<32>(p.in0 + p.N, ld, row0, p.M, col, p.N, lane, b);
+    }
+  }
+  __device__ __forceinline__ void start(const Params &p, int lane, int row0, int col0) {
+    if (K == DOWN || K == DX) {
+      if (p.in0) {
+#pragma unroll
+        for (int j = 0; j < ADDS; ++j) fetch<64>(p.in0, p.N, row0, p.M, col0 + 64 * j, p.N, lane, add[j]);
+      }
+    } else if (K == DH) {
+      block(p, lane, row0, col0);
+      sa = sb = 0;
+      if (p.codes) {
+        const uint8_t *s = p.scales + ((row0 + lane) * 2 * (int64_t)p.N + col0) / act8::kBlock;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool live = row0 + lane < p.M && col0 + 32 * j < p.N;
+          sa |= (live ? (uint32_t)s[j] : 0u) << (8 * j);
+          sb |= (live ? (uint32_t)s[j + p.N / act8::kBlock] : 0u) << (8 * j);
+        }
       }
     }
   }
@@ -210,32 +357,43 @@ struct Slice {
 // What becomes of the warp's slice: rows row0 .. row0 + 31 (a lane each), columns from col0 on (GATEUP: 64 features from
 // col0 on, a in blocks 0 and 1, b in blocks 2 and 3).
 template <int K>
-__device__ __forceinline__ void finish(const Slice &acc, const Params &p, uint32_t buf, int lane, int row0, int col0) {
-  const int row = row0 + lane;
-  const bool live = row < p.M;
+__device__ __forceinline__ void finish(Slice<K> &acc, Ahead<K> &ahead, const Params &p, uint32_t buf, int lane, int row0, int col0) {
   if (K == GATEUP) {
-#pragma unroll 1
+    if (col0 >= p.N) return;
+    const int row = row0 + lane;
+    const int64_t ld = 2 * (int64_t)p.N;
+    uint4 qb[2][4], qh[2][4];
+#pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int col = col0 + 32 * j;
       float a[32], b[32];
-      acc.load<K>(j, lane, a);
-      acc.load<K>(2 + j, lane, b);
-      if (col >= p.N) continue;
-      const int64_t ld = 2 * (int64_t)p.N;
+      acc.load(j, lane, a);
+      acc.load(2 + j, lane, b);
       if (p.codes) {
-        if (live) {
+        if (row < p.M && col < p.N) {
           uint8_t *c = p.codes + row * ld + col, *s = p.scales + (row * ld + col) / act8::kBlock;
           put_block8(c, s, a);
           put_block8(c + p.N, s + p.N / act8::kBlock, b);
         }
       } else if (p.out0) {
-        put32(buf, lane, p.out0, ld, row0, p.M, col, p.N, a);
-        put32(buf, lane, p.out0 + p.N, ld, row0, p.M, col, p.N, b);
+        stage<64>(buf, lane, 4 * j, a);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) qb[j][c] = pack_bf16x8(b + 8 * c);
       }
 #pragma unroll
       for (int i = 0; i < 32; ++i) a[i] = ffn::gated(a[i], p.gate) * b[i];
-      put32(buf, lane, p.out1, p.N, row0, p.M, col, p.N, a);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) qh[j][c] = pack_bf16x8(a + 8 * c);
     }
+    if (p.out0) {
+      put<64>(buf, lane, p.out0, ld, row0, p.M, col0, p.N);
+      stage<64>(buf, lane, 0, qb[0]);
+      stage<64>(buf, lane, 4, qb[1]);
+      put<64>(buf, lane, p.out0 + p.N, ld, row0, p.M, col0, p.N);
+    }
+    stage<64>(buf, lane, 0, qh[0]);
+    stage<64>(buf, lane, 4, qh[1]);
+    put<64>(buf, lane, p.out1, p.N, row0, p.M, col0, p.N);
   } else if (K == DH) {
 #pragma unroll 1
     for (int j = 0; j < 4; ++j) {
@@ -244,29 +402,17 @@ __device__ __forceinline__ void finish(const Slice &acc, const Params &p, uint32
       const int64_t ld = 2 * (int64_t)p.N;
       float a[32], b[32], v[32];
       if (p.codes) {
-        uint4 qa[2] = {}, qb[2] = {};
-        uint32_t sa = 0, sb = 0;
-        if (live) {
-          const uint8_t *c = p.codes + row * ld + col, *s = p.scales + (row * ld + col) / act8::kBlock;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            qa[i] = reinterpret_cast<const uint4 *>(c)[i];
-            qb[i] = reinterpret_cast<const uint4 *>(c + p.N)[i];
-          }
-          sa = s[0];
-          sb = s[p.N / act8::kBlock];
-        }
-        acc.load<K>(j, lane, v);
-        unpack_block8(qa, act8::scale_value(sa), a);
-        unpack_block8(qb, act8::scale_value(sb), b);
+        take_codes(buf, lane, ahead.a, act8::scale_value((ahead.sa >> (8 * j)) & 255u), a);
+        take_codes(buf, lane, ahead.b, act8::scale_value((ahead.sb >> (8 * j)) & 255u), b);
       } else {
-        uint4 qa[4], qb[4];
-        get32(p.in0 + row * ld, live, col, p.N, qa);
-        get32(p.in0 + row * ld + p.N, live, col, p.N, qb);
-        acc.load<K>(j, lane, v);
-        unpack32(qa, a);
-        unpack32(qb, b);
+        spread<32>(buf, lane, ahead.a);
+        spread<32>(buf + 2048, lane, ahead.b);
+        take<32, false>(buf, lane, 0, a);
+        take<32, false>(buf + 2048, lane, 0, b);
+        __syncwarp();
       }
+      if (j < 3) ahead.block(p, lane, row0, col + 32);
+      acc.load(j, lane, v);
       // a becomes da, v becomes db; with codes b becomes h
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -276,28 +422,30 @@ __device__ __forceinline__ void finish(const Slice &acc, const Params &p, uint32
         v[i] *= act;
         b[i] *= act;
       }
-      put32(buf, lane, p.out0, ld, row0, p.M, col, p.N, a);
-      put32(buf, lane, p.out0 + p.N, ld, row0, p.M, col, p.N, v);
-      if (p.codes) put32(buf, lane, p.out1, p.N, row0, p.M, col, p.N, b);
+      stage<32>(buf, lane, 0, a);
+      stage<32>(buf + 2048, lane, 0, v);
+      put<32>(buf, lane, p.out0, ld, row0, p.M, col, p.N);
+      put<32>(buf + 2048, lane, p.out0 + p.N, ld, row0, p.M, col, p.N);
+      if (p.codes) {
+        stage<32>(buf, lane, 0, b);
+        put<32>(buf, lane, p.out1, p.N, row0, p.M, col, p.N);
+      }
     }
   } else {
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-      const int col = col0 + 32 * j;
-      if (col >= p.N) break;
-      float v[32];
-      if (K != WGRAD && p.in0) {
-        uint4 q[4];
-        get32(p.in0 + (int64_t)row * p.N, live, col, p.N, q);
-        acc.load<K>(j, lane, v);
-        float w[32];
-        unpack32(q, w);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += w[i];
-      } else {
-        acc.load<K>(j, lane, v);
+    for (int j = 0; j < 2; ++j) {
+      const int col = col0 + 64 * j;
+      if (col >= p.N) break;
+      const bool add = K != WGRAD && p.in0;
+      if (add) spread<64>(buf, lane, ahead.add[j < Ahead<K>::ADDS ? j : 0]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {   // a lane's row of the buffer is its own: read, then overwritten
+        float v[32];
+        acc.load(2 * j + h, lane, v);
+        if (add) take<64, true>(buf, lane, 4 * h, v);
+        stage<64>(buf, lane, 4 * h, v);
       }
-      put32(buf, lane, p.out0, p.N, row0, p.M, col, p.N, v);
+      put<64>(buf, lane, p.out0, p.N, row0, p.M, col, p.N);
     }
   }
 }
@@ -453,47 +601,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint32_t acc_phase = 0;
     Unit t;
     for (int u = first; unit_of(u, p, t); u += step) {
-      if (!mbar_wait_cluster(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 44)) break;
-      tc_fence_after();
-      const uint32_t base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * TILE);
-      Slice s;
-      s.tmem = base + (uint32_t)((K == GATEUP ? 64 : HALF) * hh);
-      s.part = nullptr;
-      s.splits = p.splits;
       const int row0 = t.m * TILE + (int)rank * HALF + quarter * 32;
       const int col0 = K == GATEUP ? t.n * HALF + 64 * hh : t.n * TILE + HALF * hh;
-      if (t.part < 0) finish<K>(s, p, buf, lane, row0, col0);
-      else {
+      Ahead<K> ahead;
+      ahead.start(p, lane, row0, col0);
+      if (!wait_here(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 44)) break;
+      tc_fence_after();
+      Slice<K> s;
+      s.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * TILE + (K == GATEUP ? 64 : HALF) * hh);
+      s.splits = t.part < 0 ? 1 : p.splits;
+      s.mine = t.part;
+      bool here = true;   // the slice is finished by this warp
+      if (t.part >= 0) {
         const int r = t.tile - p.full;
-        float4 *mine = p.part + (((int64_t)r * p.splits + t.part) * SLICES + slice) * (SLICE_FLOATS / 4);
+        int *claimed = p.arrived + (r * SLICES + slice) * 2, *written = claimed + 1;
+        s.part = p.part + ((int64_t)r * p.splits * SLICES + slice) * (SLICE_FLOATS / 4);
+        int before = 0;
+        if (lane == 0) before = atomicAdd(claimed, 1);
+        here = __shfl_sync(0xffffffffu, before, 0) == p.splits - 1;
+        if (!here) {
+          float4 *out = const_cast<float4 *>(s.part) + t.part * Slice<K>::kNext + lane;
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          float v[32];
-          s.load<K>(j, lane, v);
+          for (int j = 0; j < 4; ++j) {
+            float v[32];
+            s.held(j, v, false);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            __stcg(mine + (j * 8 + i) * 32 + lane, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            for (int i = 0; i < 8; ++i) __stcg(out + (j * 8 + i) * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          }
+          __threadfence();   // this lane's part is visible before the count
+          __syncwarp();
+          if (lane == 0) atomicAdd(written, 1);
+        } else {
+          // the other parts' warps have all claimed before: they are writing, or have written, and wait for nothing
+          if (!wait_count(written, p.splits - 1, abort_flag, p.hdr)) break;
+          if (lane == 0) *claimed = *written = 0;
+          s.ask(0, lane);
         }
       }
+      if (here) finish<K>(s, ahead, p, buf, lane, row0, col0);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(tempty_bar(acc));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
-      if (t.part >= 0) {
-        const int r = t.tile - p.full;
-        __threadfence();   // this lane's part is visible before the arrival
-        __syncwarp();
-        int before = 0;
-        if (lane == 0) before = atomicAdd(p.arrived + r * SLICES + slice, 1);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before == p.splits - 1) {
-          __threadfence();
-          if (lane == 0) p.arrived[r * SLICES + slice] = 0;
-          s.part = p.part + ((int64_t)r * p.splits * SLICES + slice) * (SLICE_FLOATS / 4);
-          finish<K>(s, p, buf, lane, row0, col0);
-        }
-      }
     }
   }
 
@@ -512,8 +662,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 // ----------------------------------------------------------------------------- host side -------
 // How a product's tiles are dealt out. One k-block of a tile takes about 0.29 us; a part that leaves and collects fp32
-// accumulators costs about as much as kPartCost of them.
-constexpr int kPartCost = 8;
+// accumulators costs about as much as kPartCost of them (6.5 us: claim, store, fence, count, load).
+constexpr int kPartCost = 24;
 struct Deal {
   int full, splits, units;
   size_t bytes;   // of the parts
@@ -536,7 +686,7 @@ static Deal deal(int64_t M, int64_t tiles_n, int num_kb, int pairs) {
 }
 // The pairs that the plan counts on: those of a GB300, wherever it is asked for (the workspace's size follows from it).
 constexpr int kPairs = 76;
-constexpr size_t kArrivedBytes = (size_t)kPairs * SLICES * 4;   // fewer than kPairs tiles are cut
+constexpr size_t kArrivedBytes = (size_t)kPairs * SLICES * 8;   // fewer than kPairs tiles are cut
 
 static int64_t up(int64_t n, int64_t k) { return (n + k - 1) / k; }
 

@@ -74,7 +74,7 @@ def check_forward(ffn, s, act, add):
         within("ab", ffn.ab, ab, noise)
     product("y", y, ffn.h, s["wd"], dt, s["add"] if add else None)
     assert ffn.status() == 0
-    assert ffn.ws[:256 + 76 * 16 * 4].count_nonzero() == 0      # status, and the arrival counts of cut tiles
+    assert ffn.ws[:256 + 76 * 16 * 8].count_nonzero() == 0      # status, and the arrival counts of cut tiles
     return y
 
 
