@@ -5,8 +5,7 @@
 //   DOWN    y = h Wd^T (+ y_in)
 //   DH      dh = dy Wd; the epilogue reads the kept a, b and writes da = dh b act'(a), db = dh act(a) (from 8-bit codes also
 //           h again, which the weight gradient needs)
-//   DX      dx = [da | db] [Wg; Wu] (+ dx_in)
-//   WGRAD   dW = P^T Q over the tokens (dWd = dy^T h, dWgu = [da | db]^T x), both operands read MN-major
+//   BACK    dx = [da | db] [Wg; Wu] (+ dx_in), dWgu = [da | db]^T x and dWd = dy^T h (both operands read MN-major)
 //
 // A pair computes 256 x 256 outputs: each CTA holds 128 rows of A and half of B's 256 rows per 64-deep ring stage (32 KB for
 // 256 x 256 x 64 x 2 flops a pair, the ratio of bytes to flops at which the L2 just keeps up) and 128 x 256 accumulators
@@ -39,41 +38,51 @@ namespace ffng {
 
 using ffn::Gate;
 
-enum Kind { GATEUP = 0, DOWN = 1, DH = 2, DX = 3, WGRAD = 4 };
+enum Kind { GATEUP = 0, DOWN = 1, DH = 2, BACK = 3 };
 
 constexpr int TILE = 256;                       // rows and columns of a pair's tile
 constexpr int HALF = TILE / 2;                  // a CTA's rows of A, and of B
 constexpr int BK = 64;
 constexpr int OPERAND = HALF * BK * 2;          // bytes of one operand per stage
 constexpr int STAGE = 2 * OPERAND;
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int BUF = 32 * 64 * 2;                // an epilogue warp's block of 32 rows x 64 columns
+constexpr int BUF = 32 * 64 * 2;                // a block of 32 rows x 64 columns; every epilogue warp has two
 constexpr int NBARS = 2 * STAGES + 5;
-constexpr int SMEM = STAGES * STAGE + EPI_WARPS * BUF + 1024 + 8 * NBARS + 16;
+constexpr int SMEM = STAGES * STAGE + EPI_WARPS * 2 * BUF + 1024 + 8 * NBARS + 16;
 static_assert(SMEM <= 232448, "shared memory exceeds 227 KB");
 constexpr int SLICES = 2 * EPI_WARPS;           // of a tile: one per epilogue warp of the pair, 32 rows x 128 columns
 constexpr int SLICE_FLOATS = 32 * HALF;
 constexpr int MAX_SPLIT = 8;
 
-struct Params {
-  WsHeader *hdr;
+// One matrix product
+struct Product {
   int M, N;                  // valid rows; valid columns (GATEUP, DH: f)
   int m_tiles, n_tiles, num_kb;
+  __nv_bfloat16 *out0;       // GATEUP: kept ab (null: not kept, or in 8 bits); DH: dab; else the result
+  __nv_bfloat16 *out1;       // GATEUP: h; DH from 8 bits: h
+  const __nv_bfloat16 *in0;  // DH: kept ab; DOWN, DX: what is added (null: nothing)
+};
+template <int K> constexpr int products() { return K == BACK ? 3 : 1; }
+template <int K> struct Maps {
+  CUtensorMap a[products<K>()], b[products<K>()];
+};
+struct Params {
+  WsHeader *hdr;
+  Product prod[3];           // BACK: the longer products first
+  int dx;                    // BACK: which one is DX
   bool more;                 // another kernel of the same call follows
   int full, splits, units;   // tiles computed whole, parts of each of the others, units of work in all
   float4 *part;              // [tile - full][part][slice][4][8][32] float4
   int *arrived;              // [tile - full][slice][2]: parts claimed, parts written
   Gate gate;
-  __nv_bfloat16 *out0;       // GATEUP: kept ab (null: not kept, or in 8 bits); DH: dab; else the result
-  __nv_bfloat16 *out1;       // GATEUP: h; DH from 8 bits: h
-  const __nv_bfloat16 *in0;  // DH: kept ab; DOWN, DX: what is added (null: nothing)
   uint8_t *codes, *scales;   // GATEUP, DH: ab in 8 bits (null: bf16)
 };
 
 // One unit of work: a tile and its k-blocks.
 struct Unit {
+  int q;                     // product
   int tile, m, n, kb0, kb1;
   int part;                  // -1: the whole tile
 };
@@ -81,25 +90,89 @@ struct Unit {
 // Tiles are numbered in bands of eight rows of tiles, column by column inside a band: the tiles that run at the same
 // time share few rows of A and few columns of B.
 constexpr int BAND = 8;
-__device__ __forceinline__ bool unit_of(int u, const Params &p, Unit &t) {
-  if (u >= p.units) return false;
-  t.part = -1;
-  t.tile = u;
-  t.kb0 = 0;
-  t.kb1 = p.num_kb;
-  if (u >= p.full && p.splits > 1) {
-    const int r = u - p.full, q = r / p.splits;
-    t.tile = p.full + q;
-    t.part = r - q * p.splits;
-    t.kb0 = (int)((int64_t)p.num_kb * t.part / p.splits);
-    t.kb1 = (int)((int64_t)p.num_kb * (t.part + 1) / p.splits);
-  }
-  const int per = BAND * p.n_tiles, band = t.tile / per, r = t.tile - band * per;
-  const int height = min(BAND, p.m_tiles - band * BAND);
+__device__ __forceinline__ void place(Unit &t, const Product &o) {
+  const int per = BAND * o.n_tiles, band = t.tile / per, r = t.tile - band * per;
+  const int height = min(BAND, o.m_tiles - band * BAND);
   t.n = r / height;
   t.m = band * BAND + (r - t.n * height);
-  return true;
 }
+
+// The units of one pair, in order. One product: its tiles round by round, the last ones in parts.
+template <int K> struct Walk {
+  int u, step;
+  __device__ __forceinline__ Walk(int pair, int pairs, const Params &) : u(pair), step(pairs) {}
+  __device__ __forceinline__ bool next(Unit &t, const Params &p) {
+    if (u >= p.units) return false;
+    t.q = 0;
+    t.part = -1;
+    t.tile = u;
+    t.kb0 = 0;
+    t.kb1 = p.prod[0].num_kb;
+    if (u >= p.full && p.splits > 1) {
+      const int r = u - p.full, c = r / p.splits;
+      t.tile = p.full + c;
+      t.part = r - c * p.splits;
+      t.kb0 = (int)((int64_t)p.prod[0].num_kb * t.part / p.splits);
+      t.kb1 = (int)((int64_t)p.prod[0].num_kb * (t.part + 1) / p.splits);
+    }
+    place(t, p.prod[0]);
+    u += step;
+    return true;
+  }
+};
+// The three products of the backward that only need dy, x, h and dab, in one launch: their tiles last for two spans (K of the
+// weight gradients is T, of dx 2f). Every pair first takes its share of the longer tiles, r pairs one more than the others;
+// the others then take shorter ones for as long, and what is left goes round.
+template <> struct Walk<BACK> {
+  int pair, pairs, state, i, end, step;
+  int longs, shorts, swap, r, even;   // swap: DX alone is the longer class, else the two weight gradients are
+  __device__ __forceinline__ int tiles(const Params &p, int q) const { return p.prod[q].m_tiles * p.prod[q].n_tiles; }
+  __device__ __forceinline__ Walk(int pair_, int pairs_, const Params &p) : pair(pair_), pairs(pairs_), state(0) {
+    swap = p.dx == 0;
+    const int first = tiles(p, 0), last = tiles(p, 2), mid = tiles(p, 1);
+    longs = swap ? first : first + mid;
+    shorts = swap ? mid + last : last;
+    r = longs % pairs;
+    even = r == 0 ? 0 : min(shorts, p.prod[0].num_kb / p.prod[2].num_kb * (pairs - r));
+    i = pair;
+    end = longs;
+    step = pairs;
+  }
+  __device__ __forceinline__ bool next(Unit &t, const Params &p) {
+    while (i >= end) {
+      if (state == 0) {          // shorter tiles for the pairs that had one longer tile less
+        i = pair >= r ? pair - r : even;
+        end = even;
+        step = pairs - r;
+      } else if (state == 1) {   // the rest, those pairs first
+        i = even + (pair >= r ? pair - r : pair - r + pairs);
+        end = shorts;
+        step = pairs;
+      } else {
+        return false;
+      }
+      ++state;
+    }
+    const bool is_long = state == 0;
+    int tile = i;
+    t.q = is_long ? 0 : (swap ? 1 : 2);
+    const bool two = is_long != (bool)swap;    // the class of two products
+    if (two) {
+      const int n = tiles(p, t.q);
+      if (tile >= n) {
+        tile -= n;
+        ++t.q;
+      }
+    }
+    t.tile = tile;
+    t.part = -1;
+    t.kb0 = 0;
+    t.kb1 = p.prod[t.q].num_kb;
+    place(t, p.prod[t.q]);
+    i += step;
+    return true;
+  }
+};
 
 // kind::f16: D fp32, A and B bf16, M = 256, N = 256
 __host__ __device__ constexpr uint32_t idesc(bool a_mn, bool b_mn) {
@@ -182,26 +255,28 @@ __device__ __forceinline__ void put(uint32_t buf, int lane, __nv_bfloat16 *out, 
   }
   __syncwarp();
 }
-// A block of an input as neighbouring lanes load it, asked for long before it is needed, ...
-template <int W>
-__device__ __forceinline__ void fetch(const __nv_bfloat16 *in, int64_t ld, int row0, int rows, int col, int cols, int lane,
-                                      uint4 (&q)[Chunk<W>::N]) {
-  using C = Chunk<W>;
-  const int c = col + 8 * (lane % C::LANES), r0 = row0 + lane / C::LANES;
-  const __nv_bfloat16 *src = in + (int64_t)r0 * ld + c;
-#pragma unroll
-  for (int i = 0; i < C::N; ++i) {
-    q[i] = make_uint4(0, 0, 0, 0);
-    if (r0 + C::STEP * i < rows && c < cols) q[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(C::STEP * i) * ld);
-  }
+// A block of an input into the buffer, copied by neighbouring lanes (asynchronously; zeros for what lies outside)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-// ... into the buffer, and from there as this lane's row: 32 columns from chunk c0 on
-template <int W> __device__ __forceinline__ void spread(uint32_t buf, int lane, const uint4 (&q)[Chunk<W>::N]) {
-  using C = Chunk<W>;
-#pragma unroll
-  for (int i = 0; i < C::N; ++i) st_shared_v4(C::at(buf, lane / C::LANES + C::STEP * i, lane % C::LANES), q[i]);
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void landed() {   // all but the last N groups of every lane
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
   __syncwarp();
 }
+template <int W>
+__device__ __forceinline__ void fetch(uint32_t buf, const __nv_bfloat16 *in, int64_t ld, int row0, int rows, int col, int cols, int lane) {
+  using C = Chunk<W>;
+  const int c = lane % C::LANES, r0 = lane / C::LANES;
+  const __nv_bfloat16 *src = in + (int64_t)(row0 + r0) * ld + col + 8 * c;
+#pragma unroll
+  for (int i = 0; i < C::N; ++i) {
+    const int r = r0 + C::STEP * i;
+    const bool there = row0 + r < rows && col + 8 * c < cols;
+    copy16(C::at(buf, r, c), there ? src + (int64_t)(C::STEP * i) * ld : in, there);
+  }
+}
+// This lane's row of the buffer: 32 columns from chunk c0 on
 template <int W, bool ADD> __device__ __forceinline__ void take(uint32_t buf, int lane, int c0, float *v) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -211,23 +286,20 @@ template <int W, bool ADD> __device__ __forceinline__ void take(uint32_t buf, in
     for (int i = 0; i < 8; ++i) v[8 * c + i] = ADD ? v[8 * c + i] + w[i] : w[i];
   }
 }
-// The same for a 32 x 32 block of codes: two lanes per row (lane: 16-byte column lane % 2 of rows lane / 2 + 16 i).
-__device__ __forceinline__ void fetch_codes(const uint8_t *in, int64_t ld, int row0, int rows, int col, int cols, int lane, uint4 *q) {
+// The same for a 32 x 32 block of codes: two lanes per row.
+__device__ __forceinline__ uint32_t code_at(uint32_t buf, uint32_t row, uint32_t half) { return buf + row * 32 + ((half ^ ((row >> 2) & 1u)) << 4); }
+__device__ __forceinline__ void fetch_codes(uint32_t buf, const uint8_t *in, int64_t ld, int row0, int rows, int col, int cols, int lane) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = row0 + (lane >> 1) + 16 * i;
-    q[i] = make_uint4(0, 0, 0, 0);
-    if (r < rows && col < cols) q[i] = *reinterpret_cast<const uint4 *>(in + (int64_t)r * ld + col + 16 * (lane & 1));
+    const int r = (lane >> 1) + 16 * i;
+    const bool there = row0 + r < rows && col < cols;
+    copy16(code_at(buf, r, lane & 1), there ? in + (int64_t)(row0 + r) * ld + col + 16 * (lane & 1) : in, there);
   }
 }
-__device__ __forceinline__ void take_codes(uint32_t buf, int lane, const uint4 *q, float scale, float *v) {
-  auto at = [&](uint32_t row, uint32_t half) { return buf + row * 32 + ((half ^ ((row >> 2) & 1u)) << 4); };
-#pragma unroll
-  for (int i = 0; i < 2; ++i) st_shared_v4(at((lane >> 1) + 16 * i, lane & 1), q[i]);
-  __syncwarp();
+__device__ __forceinline__ void take_codes(uint32_t buf, int lane, float scale, float *v) {
 #pragma unroll
   for (uint32_t i = 0; i < 2; ++i) {
-    const uint4 w = ld_shared_v4(at(lane, i));
+    const uint4 w = ld_shared_v4(code_at(buf, lane, i));
     act8::unpack4(w.x, v + 16 * i);
     act8::unpack4(w.y, v + 16 * i + 4);
     act8::unpack4(w.z, v + 16 * i + 8);
@@ -235,7 +307,6 @@ __device__ __forceinline__ void take_codes(uint32_t buf, int lane, const uint4 *
   }
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] *= scale;
-  __syncwarp();
 }
 
 // 32 values, one whole block, to their codes and scale
@@ -259,7 +330,7 @@ __device__ __forceinline__ void put_block8(uint8_t *codes, uint8_t *scale, const
 // the other parts in the workspace, always in the parts' order. Block j holds columns 32 j .. of the slice.
 template <int K> struct Slice {
   static constexpr int64_t kNext = (int64_t)SLICES * SLICE_FLOATS / 4;   // from one part to the next
-  static constexpr bool kAsk = K == GATEUP || K == WGRAD;   // the first other part of the next block is asked for ahead (registers allowing)
+  static constexpr bool kAsk = K == GATEUP;   // the first other part of the next block is asked for ahead (registers allowing)
   uint32_t tmem;             // TMEM address of the first block
   const float4 *part;        // part 0
   int splits, mine;
@@ -315,39 +386,42 @@ template <int K> struct Slice {
   }
 };
 
-// What an epilogue warp reads besides the accumulators, asked for while the products still run: what is added (all of it), or
-// the kept a and b of its first block (the others are asked for a block ahead) and all of its scales.
+// What an epilogue warp reads besides the accumulators is on its way to shared memory while the products still run: what is added
+// (both its blocks), or the kept a and b of its first two blocks (the others follow as the buffers get free); scales in
+// registers. (Loads into registers instead: what did not fit there was waited for before it could be put on the stack.)
 template <int K> struct Ahead {
-  static constexpr int ADDS = K == DOWN || K == DX ? 2 : 1;
-  uint4 add[ADDS][8];
-  uint4 a[4], b[4];
-  uint32_t sa, sb;           // a byte per block
-  __device__ __forceinline__ void block(const Params &p, int lane, int row0, int col) {   // DH: a, b at col
-    const int64_t ld = 2 * (int64_t)p.N;
+  uint32_t sa, sb;           // DH from 8 bits: the blocks' scales, a byte each
+  static __device__ __forceinline__ void block(const Params &p, const Product &o, uint32_t buf, int lane, int row0, int col) {   // DH: a, b
+    const int64_t ld = 2 * (int64_t)o.N;
     if (p.codes) {
-      fetch_codes(p.codes, ld, row0, p.M, col, p.N, lane, a);
-      fetch_codes(p.codes + p.N, ld, row0, p.M, col, p.N, lane, b);
+      fetch_codes(buf, p.codes, ld, row0, o.M, col, o.N, lane);
+      fetch_codes(buf + 1024, p.codes + o.N, ld, row0, o.M, col, o.N, lane);
     } else {
-      fetch<32>(p.in0, ld, row0, p.M, col, p.N, lane, a);
-      fetch<32>(p.in0 + p.N, ld, row0, p.M, col, p.N, lane, b);
+      fetch<32>(buf, o.in0, ld, row0, o.M, col, o.N, lane);
+      fetch<32>(buf + 2048, o.in0 + o.N, ld, row0, o.M, col, o.N, lane);
     }
+    commit();
   }
-  __device__ __forceinline__ void start(const Params &p, int lane, int row0, int col0) {
-    if (K == DOWN || K == DX) {
-      if (p.in0) {
+  __device__ __forceinline__ void start(const Params &p, const Product &o, uint32_t buf, int lane, int row0, int col0) {
+    if (K == DOWN || K == BACK) {
+      if (o.in0) {
 #pragma unroll
-        for (int j = 0; j < ADDS; ++j) fetch<64>(p.in0, p.N, row0, p.M, col0 + 64 * j, p.N, lane, add[j]);
+        for (int j = 0; j < 2; ++j) {
+          fetch<64>(buf + j * BUF, o.in0, o.N, row0, o.M, col0 + 64 * j, o.N, lane);
+          commit();
+        }
       }
     } else if (K == DH) {
-      block(p, lane, row0, col0);
+      block(p, o, buf, lane, row0, col0);
+      block(p, o, buf + BUF, lane, row0, col0 + 32);
       sa = sb = 0;
       if (p.codes) {
-        const uint8_t *s = p.scales + ((row0 + lane) * 2 * (int64_t)p.N + col0) / act8::kBlock;
+        const uint8_t *s = p.scales + ((row0 + lane) * 2 * (int64_t)o.N + col0) / act8::kBlock;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bool live = row0 + lane < p.M && col0 + 32 * j < p.N;
+          const bool live = row0 + lane < o.M && col0 + 32 * j < o.N;
           sa |= (live ? (uint32_t)s[j] : 0u) << (8 * j);
-          sb |= (live ? (uint32_t)s[j + p.N / act8::kBlock] : 0u) << (8 * j);
+          sb |= (live ? (uint32_t)s[j + o.N / act8::kBlock] : 0u) << (8 * j);
         }
       }
     }
@@ -357,12 +431,12 @@ template <int K> struct Ahead {
 // What becomes of the warp's slice: rows row0 .. row0 + 31 (a lane each), columns from col0 on (GATEUP: 64 features from
 // col0 on, a in blocks 0 and 1, b in blocks 2 and 3).
 template <int K>
-__device__ __forceinline__ void finish(Slice<K> &acc, Ahead<K> &ahead, const Params &p, uint32_t buf, int lane, int row0, int col0) {
+__device__ __forceinline__ void finish(Slice<K> &acc, Ahead<K> &ahead, const Params &p, const Product &o, uint32_t buf, int lane, int row0, int col0) {
   if (K == GATEUP) {
-    if (col0 >= p.N) return;
+    if (col0 >= o.N) return;
     const int row = row0 + lane;
-    const int64_t ld = 2 * (int64_t)p.N;
-    uint4 qb[2][4], qh[2][4];
+    const int64_t ld = 2 * (int64_t)o.N;
+    uint4 qh[2][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int col = col0 + 32 * j;
@@ -370,94 +444,98 @@ __device__ __forceinline__ void finish(Slice<K> &acc, Ahead<K> &ahead, const Par
       acc.load(j, lane, a);
       acc.load(2 + j, lane, b);
       if (p.codes) {
-        if (row < p.M && col < p.N) {
+        if (row < o.M && col < o.N) {
           uint8_t *c = p.codes + row * ld + col, *s = p.scales + (row * ld + col) / act8::kBlock;
           put_block8(c, s, a);
-          put_block8(c + p.N, s + p.N / act8::kBlock, b);
+          put_block8(c + o.N, s + o.N / act8::kBlock, b);
         }
-      } else if (p.out0) {
+      } else if (o.out0) {
         stage<64>(buf, lane, 4 * j, a);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) qb[j][c] = pack_bf16x8(b + 8 * c);
+        stage<64>(buf + BUF, lane, 4 * j, b);
       }
 #pragma unroll
       for (int i = 0; i < 32; ++i) a[i] = ffn::gated(a[i], p.gate) * b[i];
 #pragma unroll
       for (int c = 0; c < 4; ++c) qh[j][c] = pack_bf16x8(a + 8 * c);
     }
-    if (p.out0) {
-      put<64>(buf, lane, p.out0, ld, row0, p.M, col0, p.N);
-      stage<64>(buf, lane, 0, qb[0]);
-      stage<64>(buf, lane, 4, qb[1]);
-      put<64>(buf, lane, p.out0 + p.N, ld, row0, p.M, col0, p.N);
+    if (o.out0) {
+      put<64>(buf, lane, o.out0, ld, row0, o.M, col0, o.N);
+      put<64>(buf + BUF, lane, o.out0 + o.N, ld, row0, o.M, col0, o.N);
     }
     stage<64>(buf, lane, 0, qh[0]);
     stage<64>(buf, lane, 4, qh[1]);
-    put<64>(buf, lane, p.out1, p.N, row0, p.M, col0, p.N);
+    put<64>(buf, lane, o.out1, o.N, row0, o.M, col0, o.N);
   } else if (K == DH) {
 #pragma unroll 1
     for (int j = 0; j < 4; ++j) {
       const int col = col0 + 32 * j;
-      if (col >= p.N) break;
-      const int64_t ld = 2 * (int64_t)p.N;
-      float a[32], b[32], v[32];
-      if (p.codes) {
-        take_codes(buf, lane, ahead.a, act8::scale_value((ahead.sa >> (8 * j)) & 255u), a);
-        take_codes(buf, lane, ahead.b, act8::scale_value((ahead.sb >> (8 * j)) & 255u), b);
-      } else {
-        spread<32>(buf, lane, ahead.a);
-        spread<32>(buf + 2048, lane, ahead.b);
-        take<32, false>(buf, lane, 0, a);
-        take<32, false>(buf + 2048, lane, 0, b);
-        __syncwarp();
-      }
-      if (j < 3) ahead.block(p, lane, row0, col + 32);
-      acc.load(j, lane, v);
-      // a becomes da, v becomes db; with codes b becomes h
+      const uint32_t here = buf + (j & 1) * BUF;
+      const int64_t ld = 2 * (int64_t)o.N;
+      landed<1>();                    // the next block may be on its way
+      if (col < o.N) {
+        float a[32], b[32], v[32];
+        if (p.codes) {
+          take_codes(here, lane, act8::scale_value((ahead.sa >> (8 * j)) & 255u), a);
+          take_codes(here + 1024, lane, act8::scale_value((ahead.sb >> (8 * j)) & 255u), b);
+        } else {
+          take<32, false>(here, lane, 0, a);
+          take<32, false>(here + 2048, lane, 0, b);
+        }
+        acc.load(j, lane, v);
+        // a becomes da, v becomes db; with codes b becomes h
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float act, slope;
-        ffn::gate_and_slope(a[i], p.gate, act, slope);
-        a[i] = v[i] * b[i] * slope;
-        v[i] *= act;
-        b[i] *= act;
+        for (int i = 0; i < 32; ++i) {
+          float act, slope;
+          ffn::gate_and_slope(a[i], p.gate, act, slope);
+          a[i] = v[i] * b[i] * slope;
+          v[i] *= act;
+          b[i] *= act;
+        }
+        __syncwarp();
+        stage<32>(here, lane, 0, a);
+        stage<32>(here + 2048, lane, 0, v);
+        put<32>(here, lane, o.out0, ld, row0, o.M, col, o.N);
+        put<32>(here + 2048, lane, o.out0 + o.N, ld, row0, o.M, col, o.N);
+        if (p.codes) {
+          stage<32>(here, lane, 0, b);
+          put<32>(here, lane, o.out1, o.N, row0, o.M, col, o.N);
+        }
       }
-      stage<32>(buf, lane, 0, a);
-      stage<32>(buf + 2048, lane, 0, v);
-      put<32>(buf, lane, p.out0, ld, row0, p.M, col, p.N);
-      put<32>(buf + 2048, lane, p.out0 + p.N, ld, row0, p.M, col, p.N);
-      if (p.codes) {
-        stage<32>(buf, lane, 0, b);
-        put<32>(buf, lane, p.out1, p.N, row0, p.M, col, p.N);
-      }
+      if (j < 2) Ahead<K>::block(p, o, here, lane, row0, col + 64);
+      else commit();                  // one group per block, for the count
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int col = col0 + 64 * j;
-      if (col >= p.N) break;
-      const bool add = K != WGRAD && p.in0;
-      if (add) spread<64>(buf, lane, ahead.add[j < Ahead<K>::ADDS ? j : 0]);
+      const uint32_t here = buf + j * BUF;
+      const bool add = o.in0 != nullptr;
+      if (add) {
+        if (j == 0) landed<1>();
+        else landed<0>();
+      }
+      if (col >= o.N) continue;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {   // a lane's row of the buffer is its own: read, then overwritten
         float v[32];
         acc.load(2 * j + h, lane, v);
-        if (add) take<64, true>(buf, lane, 4 * h, v);
-        stage<64>(buf, lane, 4 * h, v);
+        if (add) take<64, true>(here, lane, 4 * h, v);
+        stage<64>(here, lane, 4 * h, v);
       }
-      put<64>(buf, lane, p.out0, p.N, row0, p.M, col, p.N);
+      put<64>(here, lane, o.out0, o.N, row0, o.M, col, o.N);
     }
   }
 }
 
 template <int K>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
-  constexpr bool A_MN = K == WGRAD, B_MN = K == DH || K == DX || K == WGRAD;
+    ffn_gemm_kernel(const __grid_constant__ Maps<K> maps, const __grid_constant__ Params p) {
+  constexpr bool B_MN = K == DH || K == BACK;
+  auto a_mn = [&](const Unit &t) { return K == BACK && t.q != p.dx; };
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *epi_smem = smem + STAGES * STAGE;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + EPI_WARPS * BUF);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + EPI_WARPS * 2 * BUF);
   // bars: full[STAGES], empty[STAGES], tfull[2], tempty[2], mma_done
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + NBARS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -485,8 +563,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+    for (int q = 0; q < products<K>(); ++q) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.a[q])) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.b[q])) : "memory");
+    }
   }
   if (warp == 1) {   // collective TMEM allocation by one warp of each CTA of the pair
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)), "r"(2 * TILE)
@@ -497,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();   // both CTAs: barriers initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   wait_previous();
 
   if (warp == 0) {
@@ -506,10 +586,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    Unit t;
-    for (int u = first; ok && unit_of(u, p, t); u += step) {
+    Walk<K> walk(pair, pairs, p);
+    for (Unit t; ok && walk.next(t, p);) {
+      const CUtensorMap *tmA = &maps.a[t.q], *tmB = &maps.b[t.q];
       const int arow = t.m * TILE + (int)rank * HALF;
-      const int brow = K == GATEUP ? (int)rank * p.N + t.n * HALF : t.n * TILE + (int)rank * HALF;
+      const int brow = K == GATEUP ? (int)rank * p.prod[0].N + t.n * HALF : t.n * TILE + (int)rank * HALF;
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
         if (!mbar_spin_cluster(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 41)) {
           ok = false;
@@ -520,17 +601,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const uint32_t fb = mapa_shared(full_bar(stage), 0);   // the leader's full barrier
           if (leader) mbar_expect_tx(full_bar(stage), 2 * STAGE);
           const int kx = kb * BK;
-          if (A_MN) {
+          if (a_mn(t)) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) tma_load_2d_pair(sA + q * (BK * 128), &tmA, arow + 64 * q, kx, fb);
+            for (int q = 0; q < 2; ++q) tma_load_2d_pair(sA + q * (BK * 128), tmA, arow + 64 * q, kx, fb);
           } else {
-            tma_load_2d_pair(sA, &tmA, kx, arow, fb);
+            tma_load_2d_pair(sA, tmA, kx, arow, fb);
           }
           if (B_MN) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) tma_load_2d_pair(sB + q * (BK * 128), &tmB, brow + 64 * q, kx, fb);
+            for (int q = 0; q < 2; ++q) tma_load_2d_pair(sB + q * (BK * 128), tmB, brow + 64 * q, kx, fb);
           } else {
-            tma_load_2d_pair(sB, &tmB, kx, brow, fb);
+            tma_load_2d_pair(sB, tmB, kx, brow, fb);
           }
         }
         __syncwarp();
@@ -548,10 +629,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true, issued = false;
-    const uint64_t desc_a = A_MN ? sdesc(sbase, BK * 128, 1024) : sdesc(sbase, 16, 1024);
+    const uint64_t desc_a_mn = sdesc(sbase, BK * 128, 1024), desc_a_k = sdesc(sbase, 16, 1024);
     const uint64_t desc_b = B_MN ? sdesc(sbase + OPERAND, BK * 128, 1024) : sdesc(sbase + OPERAND, 16, 1024);
-    Unit t;
-    for (int u = first; ok && unit_of(u, p, t); u += step) {
+    Walk<K> walk(pair, pairs, p);
+    for (Unit t; ok && walk.next(t, p);) {
+      const uint64_t desc_a = a_mn(t) ? desc_a_mn : desc_a_k;
+      const uint32_t id = a_mn(t) ? idesc(true, B_MN) : idesc(false, B_MN), a_step = a_mn(t) ? 2048 >> 4 : 32 >> 4;
       if (!mbar_ready_cluster(tempty_bar(acc), acc_phase ^ 1u) &&
           !mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.hdr, 42))
         break;
@@ -567,8 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const uint32_t so = (uint32_t)(stage * STAGE) >> 4;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            mma_bf16_pair(d_tmem, desc_a + so + ((uint32_t)(kk * (A_MN ? 2048 : 32)) >> 4),
-                          desc_b + so + ((uint32_t)(kk * (B_MN ? 2048 : 32)) >> 4), idesc(A_MN, B_MN),
+            mma_bf16_pair(d_tmem, desc_a + so + (uint32_t)kk * a_step, desc_b + so + ((uint32_t)(kk * (B_MN ? 2048 : 32)) >> 4), id,
                           kb > t.kb0 || kk > 0 ? 1u : 0u);
           mma_commit_pair(empty_bar(stage), 0x3);   // frees this stage in both CTAs
         }
@@ -595,16 +677,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------------ epilogue (both CTAs)
     const int quarter = warp & 3;                 // TMEM lanes 32 quarter .. 32 quarter + 31
     const int hh = (warp - 2) >> 2;               // which half of the columns
-    const uint32_t buf = smem_u32(epi_smem) + (uint32_t)(warp - 2) * BUF;
+    const uint32_t buf = smem_u32(epi_smem) + (uint32_t)(warp - 2) * (2 * BUF);
     const int slice = (int)rank * EPI_WARPS + (warp - 2);
     int acc = 0;
     uint32_t acc_phase = 0;
-    Unit t;
-    for (int u = first; unit_of(u, p, t); u += step) {
+    Walk<K> walk(pair, pairs, p);
+    for (Unit t; walk.next(t, p);) {
+      const Product &o = p.prod[t.q];
       const int row0 = t.m * TILE + (int)rank * HALF + quarter * 32;
       const int col0 = K == GATEUP ? t.n * HALF + 64 * hh : t.n * TILE + HALF * hh;
       Ahead<K> ahead;
-      ahead.start(p, lane, row0, col0);
+      ahead.start(p, o, buf, lane, row0, col0);
       if (!wait_here(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 44)) break;
       tc_fence_after();
       Slice<K> s;
@@ -628,6 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) __stcg(out + (j * 8 + i) * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
           }
+          landed<0>();       // what was asked for to finish the slice is not needed: its place is free again
           __threadfence();   // this lane's part is visible before the count
           __syncwarp();
           if (lane == 0) atomicAdd(written, 1);
@@ -638,13 +722,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           s.ask(0, lane);
         }
       }
-      if (here) finish<K>(s, ahead, p, buf, lane, row0, col0);
+      if (here) finish<K>(s, ahead, p, o, buf, lane, row0, col0);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(tempty_bar(acc));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 
   if (*abort_flag) {   // copies that were issued and never waited for land within microseconds
@@ -668,8 +753,8 @@ struct Deal {
   int full, splits, units;
   size_t bytes;   // of the parts
 };
-static Deal deal(int64_t M, int64_t tiles_n, int num_kb, int pairs) {
-  const int64_t tiles = (M + TILE - 1) / TILE * tiles_n;
+static Deal deal(int64_t tiles_m, int64_t tiles_n, int num_kb, int pairs) {
+  const int64_t tiles = tiles_m * tiles_n;
   Deal best{(int)tiles, 1, (int)tiles, 0};
   const int rem = (int)(tiles % pairs);
   if (rem == 0) return best;
@@ -708,17 +793,9 @@ template <auto KERNEL> static int pairs_resident(int &pairs) {
   return MOE_OK;
 }
 
-// M x (n_tiles of columns) outputs over num_kb k-blocks
 template <int K>
-static int launch(const CUtensorMap &a, const CUtensorMap &b, Params p, int64_t n_tiles, const ffn::Block &blk, bool first,
-                  bool last, cudaStream_t s) {
-  const Deal d = deal(p.M, n_tiles, p.num_kb, kPairs);
-  p.m_tiles = (int)up(p.M, TILE);
-  p.n_tiles = (int)n_tiles;
-  p.full = d.full;
-  p.splits = d.splits;
-  p.units = d.units;
-  p.more = !last;
+static int start(const Maps<K> &maps, Params p, int units, const ffn::Block &blk, bool first, cudaStream_t s) {
+  p.more = first;            // a call makes two launches
   p.hdr = blk.hdr;
   p.gate = blk.gate;
   p.arrived = (int *)blk.ws;
@@ -726,14 +803,31 @@ static int launch(const CUtensorMap &a, const CUtensorMap &b, Params p, int64_t 
   int pairs = 0;
   const int rc = pairs_resident<ffn_gemm_kernel<K>>(pairs);
   if (rc) return rc;
-  if (pairs > p.units) pairs = p.units;
-  if (!first) {
-    MOE_TRY_CUDA(launch_after(ffn_gemm_kernel<K>, dim3(2 * pairs), dim3(THREADS), (size_t)SMEM, s, a, b, p));
-  } else {
-    ffn_gemm_kernel<K><<<2 * pairs, THREADS, SMEM, s>>>(a, b, p);
+  if (pairs > units) pairs = units;
+  if (first) {
+    ffn_gemm_kernel<K><<<2 * pairs, THREADS, SMEM, s>>>(maps, p);
     MOE_CHECK_LAUNCH();
+  } else {
+    MOE_TRY_CUDA(launch_after(ffn_gemm_kernel<K>, dim3(2 * pairs), dim3(THREADS), (size_t)SMEM, s, maps, p));
   }
   return MOE_OK;
+}
+static Product product(int64_t M, int64_t N, int64_t k, int64_t cols_per_tile) {
+  Product o{};
+  o.M = (int)M;
+  o.N = (int)N;
+  o.m_tiles = (int)up(M, TILE);
+  o.n_tiles = (int)up(N, cols_per_tile);
+  o.num_kb = (int)up(k, BK);
+  return o;
+}
+// One product
+template <int K> static int launch(const Maps<K> &maps, Params p, const ffn::Block &blk, bool first, cudaStream_t s) {
+  const Deal d = deal(p.prod[0].m_tiles, p.prod[0].n_tiles, p.prod[0].num_kb, kPairs);
+  p.full = d.full;
+  p.splits = d.splits;
+  p.units = d.units;
+  return start<K>(maps, p, d.units, blk, first, s);
 }
 
 }  // namespace ffng
@@ -747,90 +841,77 @@ typedef __nv_bfloat16 bf16;
 
 size_t gemm_workspace(int T, int d, int f, bool backward) {
   size_t most = 0;
-  auto with = [&](int64_t M, int64_t n_tiles, int64_t k) {
-    const Deal dl = deal(M, n_tiles, (int)up(k, BK), kPairs);
+  auto with = [&](const Product &o) {
+    const Deal dl = deal(o.m_tiles, o.n_tiles, o.num_kb, kPairs);
     if (dl.bytes > most) most = dl.bytes;
   };
-  with(T, up(f, HALF), d);          // GATEUP
-  with(T, up(d, TILE), f);          // DOWN
-  if (backward) {
-    with(T, up(f, TILE), d);        // DH
-    with(T, up(d, TILE), 2 * f);    // DX
-    with(d, up(f, TILE), T);        // dWd
-    with(2 * f, up(d, TILE), T);    // dWgu
-  }
+  with(product(T, f, d, HALF));                  // GATEUP
+  with(product(T, d, f, TILE));                  // DOWN
+  if (backward) with(product(T, f, d, TILE));    // DH
   return kArrivedBytes + most;
 }
 
 int gemm_fwd(const Block &b, cudaStream_t s) {
-  CUtensorMap mx, mw;
-  if (!make_map(&mx, b.x, b.T, b.d, HALF) || !make_map(&mw, b.w_gate_up, 2 * (uint64_t)b.f, b.d, HALF)) return MOE_ERR_CUDA;
+  Maps<GATEUP> m1;
+  if (!make_map(&m1.a[0], b.x, b.T, b.d, HALF) || !make_map(&m1.b[0], b.w_gate_up, 2 * (uint64_t)b.f, b.d, HALF)) return MOE_ERR_CUDA;
   Params p{};
-  p.M = b.T;
-  p.N = b.f;
-  p.num_kb = (int)up(b.d, BK);
+  p.prod[0] = product(b.T, b.f, b.d, HALF);
   if (b.scales) {
     p.codes = (uint8_t *)b.ab;
     p.scales = b.scales;
   } else {
-    p.out0 = (bf16 *)b.ab;
+    p.prod[0].out0 = (bf16 *)b.ab;
   }
-  p.out1 = (bf16 *)b.h;
-  int rc = launch<GATEUP>(mx, mw, p, up(b.f, HALF), b, true, false, s);
+  p.prod[0].out1 = (bf16 *)b.h;
+  int rc = launch<GATEUP>(m1, p, b, true, s);
   if (rc) return rc;
-  CUtensorMap mh, md;
-  if (!make_map(&mh, b.h, b.T, b.f, HALF) || !make_map(&md, b.w_down, b.d, b.f, HALF)) return MOE_ERR_CUDA;
+  Maps<DOWN> m2;
+  if (!make_map(&m2.a[0], b.h, b.T, b.f, HALF) || !make_map(&m2.b[0], b.w_down, b.d, b.f, HALF)) return MOE_ERR_CUDA;
   p = Params{};
-  p.M = b.T;
-  p.N = b.d;
-  p.num_kb = (int)up(b.f, BK);
-  p.in0 = (const bf16 *)b.add;
-  p.out0 = (bf16 *)b.y;
-  return launch<DOWN>(mh, md, p, up(b.d, TILE), b, false, true, s);
+  p.prod[0] = product(b.T, b.d, b.f, TILE);
+  p.prod[0].in0 = (const bf16 *)b.add;
+  p.prod[0].out0 = (bf16 *)b.y;
+  return launch<DOWN>(m2, p, b, false, s);
 }
 
 int gemm_bwd(const Block &b, cudaStream_t s) {
   const uint64_t T = b.T, d = b.d, f = b.f;
-  CUtensorMap ma, mb;
   // da, db (and h, from 8 bits)
-  if (!make_map(&ma, b.dy, T, d, HALF) || !make_map(&mb, b.w_down, d, f, BK)) return MOE_ERR_CUDA;
+  Maps<DH> m1;
+  if (!make_map(&m1.a[0], b.dy, T, d, HALF) || !make_map(&m1.b[0], b.w_down, d, f, BK)) return MOE_ERR_CUDA;
   Params p{};
-  p.M = b.T;
-  p.N = b.f;
-  p.num_kb = (int)up(b.d, BK);
+  p.prod[0] = product(b.T, b.f, b.d, TILE);
   if (b.scales) {
     p.codes = (uint8_t *)b.ab;
     p.scales = b.scales;
-    p.out1 = (bf16 *)b.h;
+    p.prod[0].out1 = (bf16 *)b.h;
   } else {
-    p.in0 = (const bf16 *)b.ab;
+    p.prod[0].in0 = (const bf16 *)b.ab;
   }
-  p.out0 = (bf16 *)b.dab;
-  int rc = launch<DH>(ma, mb, p, up(b.f, TILE), b, true, false, s);
+  p.prod[0].out0 = (bf16 *)b.dab;
+  int rc = launch<DH>(m1, p, b, true, s);
   if (rc) return rc;
-  // dx
-  if (!make_map(&ma, b.dab, T, 2 * f, HALF) || !make_map(&mb, b.w_gate_up, 2 * f, d, BK)) return MOE_ERR_CUDA;
+  // dWgu [2f, d] = dab^T x, dWd [d, f] = dy^T h, dx = dab Wgu (+ dx_in), the longer tiles first
   p = Params{};
-  p.M = b.T;
-  p.N = b.d;
-  p.num_kb = (int)up(2 * (int64_t)b.f, BK);
-  p.in0 = (const bf16 *)b.add;
-  p.out0 = (bf16 *)b.dx;
-  if ((rc = launch<DX>(ma, mb, p, up(b.d, TILE), b, false, false, s))) return rc;
-  // dWd [d, f] = dy^T h
-  if (!make_map(&ma, b.dy, T, d, BK) || !make_map(&mb, b.h, T, f, BK)) return MOE_ERR_CUDA;
-  p = Params{};
-  p.M = b.d;
-  p.N = b.f;
-  p.num_kb = (int)up(b.T, BK);
-  p.out0 = (bf16 *)b.dw_down;
-  if ((rc = launch<WGRAD>(ma, mb, p, up(b.f, TILE), b, false, false, s))) return rc;
-  // dWgu [2f, d] = dab^T x
-  if (!make_map(&ma, b.dab, T, 2 * f, BK) || !make_map(&mb, b.x, T, d, BK)) return MOE_ERR_CUDA;
-  p.M = 2 * b.f;
-  p.N = b.d;
-  p.out0 = (bf16 *)b.dw_gate_up;
-  return launch<WGRAD>(ma, mb, p, up(b.d, TILE), b, false, true, s);
+  Product gu = product(2 * (int64_t)b.f, b.d, b.T, TILE), down = product(b.d, b.f, b.T, TILE), dx = product(b.T, b.d, 2 * (int64_t)b.f, TILE);
+  gu.out0 = (bf16 *)b.dw_gate_up;
+  down.out0 = (bf16 *)b.dw_down;
+  dx.in0 = (const bf16 *)b.add;
+  dx.out0 = (bf16 *)b.dx;
+  const int w = dx.num_kb > gu.num_kb ? 1 : 0;
+  p.dx = w ? 0 : 2;
+  p.prod[w] = gu;
+  p.prod[w + 1] = down;
+  p.prod[p.dx] = dx;
+  Maps<BACK> m2;
+  if (!make_map(&m2.a[w], b.dab, T, 2 * f, BK) || !make_map(&m2.b[w], b.x, T, d, BK) || !make_map(&m2.a[w + 1], b.dy, T, d, BK) ||
+      !make_map(&m2.b[w + 1], b.h, T, f, BK) || !make_map(&m2.a[p.dx], b.dab, T, 2 * f, HALF) ||
+      !make_map(&m2.b[p.dx], b.w_gate_up, 2 * f, d, BK))
+    return MOE_ERR_CUDA;
+  p.splits = 1;
+  int64_t units = 0;
+  for (const Product &o : p.prod) units += (int64_t)o.m_tiles * o.n_tiles;
+  return start<BACK>(m2, p, (int)(units < kPairs ? units : kPairs), b, false, s);
 }
 
 }  // namespace ffn
