@@ -9,6 +9,7 @@
 
 #include "act8.cuh"
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace moe {
 namespace ffn {
@@ -36,6 +37,39 @@ template <bool EXACT = false> __device__ __forceinline__ void gate_and_slope(flo
   const float q = square_of(a), s = sigma<EXACT>(a * fmaf(k.k1, q, k.k0));
   act = a * s;
   slope = fmaf(act * (1.0f - s), fmaf(3.0f * k.k1, q, k.k0), s);
+}
+
+// The same for two values at a time, for the bf16 epilogues, whose instructions have to hide behind the products. The silu gate
+// leaves the cubic out (its k1 is 0): k.k1 is the same in all threads, so that is one branch.
+__device__ __forceinline__ F2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ F2 sigma2(F2 z) {   // 1 / (1 + 2^(-z log2 e)): ex2 and rcp, each good to an ulp or two
+  float x, y;
+  split(mul(z, both(-1.4426950408889634f)), x, y);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y));
+  split(add(pair(x, y), both(1.0f)), x, y);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y));
+  return pair(x, y);
+}
+__device__ __forceinline__ F2 square2(F2 a) {   // square_of
+  float x, y;
+  split(mul(a, a), x, y);
+  return pair(fminf(x, 1e30f), fminf(y, 1e30f));
+}
+template <bool CUBIC> __device__ __forceinline__ F2 gated2(F2 a, const Gate &k) {
+  return mul(a, sigma2(CUBIC ? mul(a, fma(both(k.k1), square2(a), both(k.k0))) : a));
+}
+template <bool CUBIC> __device__ __forceinline__ void gate_and_slope2(F2 a, const Gate &k, F2 &act, F2 &slope) {
+  if (CUBIC) {
+    const F2 q = square2(a), s = sigma2(mul(a, fma(both(k.k1), q, both(k.k0))));
+    act = mul(a, s);
+    slope = fma(mul(act, fma(s, both(-1.0f), both(1.0f))), fma(both(3.0f * k.k1), q, both(k.k0)), s);
+  } else {
+    const F2 s = sigma2(a);
+    act = mul(a, s);
+    slope = fma(act, fma(s, both(-1.0f), both(1.0f)), s);
+  }
 }
 
 // One call's sizes and buffers (see moe.h). bf16 and fp32 share it.

@@ -9,11 +9,16 @@
 // lane 4 g + q holds row (token) g, k = 8 q .. 8 q + 7 of each 32. GATEUP's 16 rows are 8 gate rows and the same features' 8 up rows,
 // so a lane's accumulators hold a and b of one feature. The warps' sums meet in shared memory, in a fixed order.
 //
-// Tokens are read through L2 by every block: with 32 weight rows per block half as often as with 16, which is worth it where
-// tokens outnumber rows and there are blocks enough (few_fwd). DOWN starts as a dependent of GATEUP and loads its
-// first weights while GATEUP runs.
+// DOWN starts as a dependent of GATEUP and loads its first weights while GATEUP runs.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+
 #include "dependent.cuh"
 #include "ffn.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
 
 namespace moe {
 namespace ffn {
@@ -38,6 +43,24 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A lane's four sums: a (v.x, v.y) and b (v.z, v.w) of feature n for tokens t and t + 1 ...
+__device__ __forceinline__ void put_up(const Params &p, int n, int t, const float4 &v) {
+  if (n >= p.N) return;
+  if (t < p.T) p.out[(int64_t)t * p.N + n] = __float2bfloat16_rn(gated(v.x, p.gate) * v.z);
+  if (t + 1 < p.T) p.out[(int64_t)(t + 1) * p.N + n] = __float2bfloat16_rn(gated(v.y, p.gate) * v.w);
+}
+// ... or y of columns n and n + apart for tokens t and t + 1
+__device__ __forceinline__ void put_down(const Params &p, int n, int apart, int t, const float4 &v) {
+  const float r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int nn = n + apart * (e >> 1), tt = t + (e & 1);
+    if (nn >= p.N || tt >= p.T) continue;
+    const int64_t at = (int64_t)tt * p.N + nn;
+    p.out[at] = __float2bfloat16_rn(r[e] + (p.add ? __bfloat162float(p.add[at]) : 0.0f));
+  }
 }
 
 // NT: groups of eight tokens. MT: groups of sixteen weight rows. CH: 32-deep steps whose loads are in flight together.
@@ -121,21 +144,8 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_few_kernel(const Params p) {
       v.w += o.w;
     }
     const int m = i / NT, t = 8 * (i - m * NT) + 2 * q;   // tokens t and t + 1
-    if (UP) {
-      const int n = (blockIdx.x * MT + m) * 8 + g;
-      if (n >= p.N) continue;
-      if (t < p.T) p.out[(int64_t)t * p.N + n] = __float2bfloat16_rn(gated(v.x, p.gate) * v.z);
-      if (t + 1 < p.T) p.out[(int64_t)(t + 1) * p.N + n] = __float2bfloat16_rn(gated(v.y, p.gate) * v.w);
-    } else {
-      const float r[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int n = (blockIdx.x * MT + m) * 16 + 8 * (e >> 1) + g, tt = t + (e & 1);
-        if (n >= p.N || tt >= p.T) continue;
-        const int64_t at = (int64_t)tt * p.N + n;
-        p.out[at] = __float2bfloat16_rn(r[e] + (p.add ? __bfloat162float(p.add[at]) : 0.0f));
-      }
-    }
+    if (UP) put_up(p, (blockIdx.x * MT + m) * 8 + g, t, v);
+    else put_down(p, (blockIdx.x * MT + m) * 16 + g, 8, t, v);
   }
 }
 
@@ -149,13 +159,226 @@ template <bool UP, int NT, int MT, int CH> static int launch(const Params &p, cu
   }
   return MOE_OK;
 }
-// 32 weight rows per block where more tokens than 16 read them and two blocks per SM remain.
-template <bool UP> static int run(const Params &p, cudaStream_t s) {
+
+// ---------------------------------------------------------------------------------------------
+// The same for weights that keep the GPU busy for longer than a kernel takes to start: one block per SM streams its row groups
+// through a ring in shared memory that TMA keeps full, 16 (or 32) weight rows and all tokens by 512 of K a stage, whatever the
+// registers hold; each of the eight warps takes 64 of the 512. The tensors are seen as [K / 64, rows, 64], so that one copy brings
+// eight 128-byte-swizzled boxes: 16-byte chunk c of row g lies at (c ^ g) * 16 (g its low three bits). A lane takes the chunks 2 q and
+// 2 q + 1, so that the eight lanes that read together, of two rows, meet all banks once (q and q + 4 met half of them twice).
+// With loads into registers (above) 134 MB of weights for 24 tokens took 33 us (4.0 TB/s).
+constexpr int KS = 512;                        // of K per stage
+struct Stream {
+  int groups, steps, stages;                   // row groups; stages per group; places of the ring
+};
+template <int NT, int MT> constexpr int weight_bytes() { return 16 * MT * KS * 2; }
+template <int NT> constexpr int token_bytes() { return 8 * NT * KS * 2; }
+template <int NT, int MT> constexpr int stage_bytes() { return weight_bytes<NT, MT>() + token_bytes<NT>(); }
+template <int NT, int MT> constexpr int sum_bytes() { return WARPS * MT * NT * 512; }
+constexpr int kSmemMost = 232448;
+template <int NT, int MT> constexpr int stages_with(int sums) {
+  const int n = (kSmemMost - 2048 - sums * sum_bytes<NT, MT>()) / stage_bytes<NT, MT>();
+  return n > 8 ? 8 : n;
+}
+template <int NT, int MT> constexpr int stages_of() { return stages_with<NT, MT>(1); }
+// The warps' sums in two buffers in turn, one barrier a group, where that costs no stage; else in one, with two barriers
+template <int NT, int MT> constexpr int sums_of() { return stages_with<NT, MT>(2) == stages_of<NT, MT>() ? 2 : 1; }
+template <int NT, int MT> constexpr int smem_of() {
+  return stages_of<NT, MT>() * stage_bytes<NT, MT>() + sums_of<NT, MT>() * sum_bytes<NT, MT>() + 1024 + 256;
+}
+
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// tmW: boxes of 8 MT weight rows, tmX: boxes of 8 NT tokens, each 64 x 8 of K
+template <bool UP, int NT, int MT>
+__global__ void __launch_bounds__(THREADS + 32, 1)
+    ffn_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p, const Stream st,
+                      WsHeader *hdr) {
+  constexpr int PS = stages_of<NT, MT>(), SB = stage_bytes<NT, MT>(), ROWS = 8 * MT, SUMS = sums_of<NT, MT>();
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  float4(*sums)[MT * NT][32] = reinterpret_cast<float4(*)[MT * NT][32]>(smem + PS * SB);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + PS * SB + SUMS * sum_bytes<NT, MT>());   // full[PS], empty[PS]
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 2 * PS);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const uint32_t base = tc::smem_u32(smem), bar0 = tc::smem_u32(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (PS + s); };
+  if (UP) start_next();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < PS; ++s) {
+      tc::mbar_init(full(s), 1);
+      tc::mbar_init(empty(s), WARPS);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  const int mine = (int)blockIdx.x < st.groups ? (st.groups - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+  const int total = mine * st.steps;           // stages that this block goes through
+  if (warp == WARPS) {
+    // ---- the ring's producer: one elected lane
+    if (tc::elect_one()) {
+      auto weights = [&](int i) {
+        const int gr = (int)blockIdx.x + i / st.steps * (int)gridDim.x, k = i % st.steps, s = i % PS;
+        const int row = gr * (UP ? ROWS : 2 * ROWS);
+        tc::mbar_expect_tx(full(s), SB);
+        load_3d(base + s * SB, &tmW, 0, row, k * (KS / 64), full(s));
+        load_3d(base + s * SB + weight_bytes<NT, MT>() / 2, &tmW, 0, UP ? p.N + row : row + ROWS, k * (KS / 64), full(s));
+      };
+      auto tokens = [&](int i) {
+        const int k = i % st.steps, s = i % PS;
+        load_3d(base + s * SB + weight_bytes<NT, MT>(), &tmX, 0, 0, k * (KS / 64), full(s));
+      };
+      const int head = total < PS ? total : PS;
+      for (int i = 0; i < head; ++i) weights(i);   // the weights do not wait for the kernel before
+      wait_previous();
+      for (int i = 0; i < head; ++i) tokens(i);
+      for (int i = head; i < total; ++i) {
+        if (!tc::mbar_wait(empty(i % PS), (uint32_t)(i / PS - 1) & 1u, abort_flag, hdr, 51)) break;
+        weights(i);
+        tokens(i);
+      }
+    }
+  } else {
+    wait_previous();
+    float acc[MT][NT][4] = {};
+    int k = 0, gr = blockIdx.x, at_sums = 0;
+    bool ok = true;
+    for (int i = 0; i < total; ++i) {
+      const int s = i % PS;
+      const uint32_t phase = (uint32_t)(i / PS) & 1u;
+      if (!tc::mbar_try_wait(full(s), phase) && !tc::mbar_wait(full(s), phase, abort_flag, hdr, 52)) {
+        ok = false;
+        break;
+      }
+      const uint32_t w0 = base + s * SB + (uint32_t)warp * (ROWS * 128), x0 = base + s * SB + weight_bytes<NT, MT>() + (uint32_t)warp * (NT * 1024);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = (uint32_t)g * 128 + (((uint32_t)(2 * q + h) ^ (uint32_t)g) << 4);
+        uint4 x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n] = tc::ld_shared_v4(x0 + n * 1024 + at);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint4 a = tc::ld_shared_v4(w0 + m * 1024 + at), b = tc::ld_shared_v4(w0 + weight_bytes<NT, MT>() / 2 + m * 1024 + at);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816(acc[m][n], a.x, b.x, a.y, b.y, x[n].x, x[n].y);
+            mma16816(acc[m][n], a.z, b.z, a.w, b.w, x[n].z, x[n].w);
+          }
+        }
+      }
+      // the reads above come before the TMA's next writes to this place: another proxy's, which the arrival alone does not order
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(empty(s));
+      if (++k < st.steps) continue;
+      // the group's sums over the warps, in their order
+      k = 0;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          sums[at_sums + warp][m * NT + n][lane] = make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+          acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+      for (int j = warp; j < MT * NT; j += WARPS) {
+        float4 v = sums[at_sums][j][lane];
+#pragma unroll
+        for (int u = 1; u < WARPS; ++u) {
+          const float4 o = sums[at_sums + u][j][lane];
+          v.x += o.x;
+          v.y += o.y;
+          v.z += o.z;
+          v.w += o.w;
+        }
+        const int m = j / NT, t = 8 * (j - m * NT) + 2 * q;   // tokens t and t + 1
+        if (UP) put_up(p, gr * ROWS + 8 * m + g, t, v);
+        else put_down(p, gr * 2 * ROWS + 8 * m + g, ROWS, t, v);
+      }
+      if (SUMS == 1) asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+      else at_sums ^= WARPS;
+      gr += gridDim.x;
+    }
+    if (!ok) {   // copies in flight land within microseconds
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < 1000ull * 1000ull) {}
+    }
+  }
+}
+
+// [rows, K] bf16 seen as [K / 64, rows, 64], boxes of 64 x box_rows x 8
+static bool stream_map(CUtensorMap *m, const void *p, uint64_t rows, uint64_t K, uint32_t box_rows) {
+  tc::EncodeTiledFn enc = tc::encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {64, rows, K / 64}, strides[2] = {K * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, KS / 64}, one[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+template <auto KERNEL, int SMEM> static int raise_limit() {
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  MOE_TRY_CUDA(cudaGetDevice(&dev));
+  if (dev < 64 && (raised.load(std::memory_order_relaxed) >> dev & 1)) return MOE_OK;
+  MOE_TRY_CUDA(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
+  if (dev < 64) raised.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  return MOE_OK;
+}
+template <bool UP, int NT, int MT> static int launch_stream(const Params &p, WsHeader *hdr, cudaStream_t s) {
+  constexpr int SMEM = smem_of<NT, MT>();
+  static_assert(SMEM <= kSmemMost && stages_of<NT, MT>() >= 2, "two stages at least");
+  CUtensorMap mw, mx;
+  if (!stream_map(&mw, p.w, UP ? 2 * (uint64_t)p.N : p.N, p.K, 8 * MT) || !stream_map(&mx, p.tok, p.T, p.K, 8 * NT)) return MOE_ERR_CUDA;
+  const int rc = raise_limit<ffn_stream_kernel<UP, NT, MT>, SMEM>();
+  if (rc) return rc;
+  const int per = UP ? 8 * MT : 16 * MT;
+  const Stream st{(p.N + per - 1) / per, (p.K + KS - 1) / KS, stages_of<NT, MT>()};
+  const int grid = std::min(st.groups, sm_count());
+  if (UP) {
+    ffn_stream_kernel<UP, NT, MT><<<grid, THREADS + 32, SMEM, s>>>(mw, mx, p, st, hdr);
+    MOE_CHECK_LAUNCH();
+  } else {
+    MOE_TRY_CUDA(launch_after(ffn_stream_kernel<UP, NT, MT>, dim3(grid), dim3(THREADS + 32), (size_t)SMEM, s, mw, mx, p, st, hdr));
+  }
+  return MOE_OK;
+}
+template <bool UP, int NT> static int stream(const Params &p, WsHeader *hdr, cudaStream_t s) {
+  // rounds of row groups over the SMs: 32 rows per group read the tokens half as often, 16 leave a shorter last round (and with
+  // more tokens than 32 more stages fit)
+  const int64_t sms = sm_count(), g16 = (p.N + (UP ? 7 : 15)) / (UP ? 8 : 16), g32 = (g16 + 1) / 2;
+  if constexpr (NT <= 4) {
+    if (2 * ((g32 + sms - 1) / sms) <= (g16 + sms - 1) / sms) return launch_stream<UP, NT, 2>(p, hdr, s);
+  }
+  return launch_stream<UP, NT, 1>(p, hdr, s);
+}
+
+// Small weights take the kernel that starts quickest, others (over 128 KB per SM, rows of whole 128 bytes) the ring.
+template <bool UP> static int run(const Params &p, WsHeader *hdr, cudaStream_t s) {
   const int nt = (p.T + 7) / 8;
-  const bool two = nt > 2 && (p.N + (UP ? 15 : 31)) / (UP ? 16 : 32) >= 2 * sm_count();
+  const int64_t bytes = (UP ? 4 : 2) * (int64_t)p.N * p.K;
+  if (p.K % 64 == 0 && bytes > (int64_t)sm_count() * 128 * 1024) {
+    switch (nt) {
+      case 1: return stream<UP, 1>(p, hdr, s);
+      case 2: return stream<UP, 2>(p, hdr, s);
+      case 3: return stream<UP, 3>(p, hdr, s);
+      case 4: return stream<UP, 4>(p, hdr, s);
+      case 5:
+      case 6: return stream<UP, 6>(p, hdr, s);
+      default: return stream<UP, 8>(p, hdr, s);
+    }
+  }
   if (nt == 1) return launch<UP, 1, 1, 8>(p, s);
   if (nt == 2) return launch<UP, 2, 1, 4>(p, s);
-  if (nt <= 4) return two ? launch<UP, 4, 2, 2>(p, s) : launch<UP, 4, 1, 4>(p, s);
+  if (nt <= 4) return launch<UP, 4, 1, 4>(p, s);
   return launch<UP, 8, 1, 2>(p, s);
 }
 
@@ -171,7 +394,7 @@ int few_fwd(const Block &b, cudaStream_t s) {
   p.K = b.d;
   p.N = b.f;
   p.gate = b.gate;
-  const int rc = few::run<true>(p, s);
+  const int rc = few::run<true>(p, b.hdr, s);
   if (rc) return rc;
   p.tok = (const bf16 *)b.h;
   p.w = (const bf16 *)b.w_down;
@@ -179,7 +402,7 @@ int few_fwd(const Block &b, cudaStream_t s) {
   p.out = (bf16 *)b.y;
   p.K = b.f;
   p.N = b.d;
-  return few::run<false>(p, s);
+  return few::run<false>(p, b.hdr, s);
 }
 
 }  // namespace ffn

@@ -13,21 +13,37 @@
 // GATEUP's B is 128 gate rows in one CTA and the same features' 128 up rows in the other: every thread of the epilogue
 // (a TMEM lane is a token) holds a and b of the same features, a whole block of 32 at a time for the 8-bit codes.
 //
-// Work is dealt to the C pairs in whole rounds of C tiles; the tiles of the last, incomplete round (all of them, for small
-// products) are cut along K into S parts, so that the pairs share what would leave most of them idle. Of the warps that hold
-// the parts of the same 32 x 128 outputs the last one to claim them finishes them: the others leave their fp32 accumulators
-// in the workspace, it waits until they are there (those warps wait for nothing, so that ends), adds the parts up in
-// their order, its own from TMEM (so the result does not depend on which came last), and sets the counts back to zero.
+// One launch runs all products of a call: y's tiles follow the ones of h in the same kernel, the last three products those of da, db.
+// A pair takes its tiles in the order of the products, as many of each as even out the pairs' work (deal_out); a unit that
+// reads what others of the launch write waits until the rows of tiles that it needs are complete (counts per row, in the
+// workspace; the pairs are all resident, a cooperative launch, and no pair waits before it has brought all its tiles of the
+// first product). In separate launches the incomplete last rounds, the set-up of each kernel and its last epilogues cost 45 of
+// 259 us of a step at 8192 x 2048 x 1024.
 //
-// Roles per CTA: warp 0 loads (TMA), warp 1 allocates TMEM and, in the leader, issues the products, warps 2..9 are the epilogue.
-// Every wait is bounded (0.2 s): on timeout the kernel records MOE_ERR_DEVICE_TIMEOUT, lets copies in flight
-// land, frees TMEM and leaves. Kernels of one call are launched as dependents of one another: set-up overlaps the tail of
-// the one before.
+// A first product of fewer tiles than pairs whose K is long is cut along K into S parts instead, in a launch of its own. Of the warps
+// that hold the parts of the same 32 x 128 outputs the last one to claim them finishes them: the others leave their fp32
+// accumulators in the workspace, it waits until they are there (those warps wait for nothing, so that ends), adds the parts
+// up in their order, its own from TMEM (so the result does not depend on which came last), and sets the counts back to zero.
+//
+// Roles per CTA: warp 0 loads (TMA), warp 1 allocates TMEM and, in the leader, issues the products, warps 2..9 are the epilogue
+// (sixteen warps of 96 registers were slower: 1474 against 1400 us for the three products at 8192 x 4096 x 8192).
+// Every wait is bounded (0.2 s): on timeout the kernel records MOE_ERR_DEVICE_TIMEOUT, lets copies in flight land, frees
+// TMEM and leaves.
+//
+// Measured (bf16, T x d x f): 8192 x 4096 x 8192 forward 0.86 ms, backward 1.73 ms each alone at full clocks (1.91 PFLOP/s), a step
+// under the power cap 2.73-2.8 ms; 8192 x 2048 x 1024 forward 72 us, backward 126 us, a step 202 us (1.53 PFLOP/s): per tile the
+// products take 8.6 us, but bursts of h, a, b and da, db from all pairs at once take 4-7 us of HBM's time each.
 #include <cuda.h>
 
+#include <string.h>
+
+#include <algorithm>
 #include <atomic>
+#include <type_traits>
+#include <utility>
 
 #include "dependent.cuh"
+#include "f32x2.cuh"
 #include "ffn.cuh"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
@@ -38,7 +54,8 @@ namespace ffng {
 
 using ffn::Gate;
 
-enum Kind { GATEUP = 0, DOWN = 1, DH = 2, BACK = 3 };
+enum Chain { FWD = 0, BWD = 1 };                     // the kernel's two instantiations, and
+enum Op { GATEUP = 0, DOWN = 1, DH = 2, DW = 3, DX = 4 };   // the products they run
 
 constexpr int TILE = 256;                       // rows and columns of a pair's tile
 constexpr int HALF = TILE / 2;                  // a CTA's rows of A, and of B
@@ -57,25 +74,36 @@ constexpr int SLICE_FLOATS = 32 * HALF;
 constexpr int MAX_SPLIT = 8;
 
 // One matrix product
+enum Needs { NOTHING = 0, ITS_ROWS = 1, ALL_ROWS = 2 };   // of what an earlier product of the same launch writes
 struct Product {
+  int op, needs;
   int M, N;                  // valid rows; valid columns (GATEUP, DH: f)
   int m_tiles, n_tiles, num_kb;
   __nv_bfloat16 *out0;       // GATEUP: kept ab (null: not kept, or in 8 bits); DH: dab; else the result
   __nv_bfloat16 *out1;       // GATEUP: h; DH from 8 bits: h
   const __nv_bfloat16 *in0;  // DH: kept ab; DOWN, DX: what is added (null: nothing)
 };
-template <int K> constexpr int products() { return K == BACK ? 3 : 1; }
-template <int K> struct Maps {
-  CUtensorMap a[products<K>()], b[products<K>()];
+constexpr int PRODUCTS = 4;
+template <int CH> constexpr int products() { return CH == FWD ? 2 : PRODUCTS; }
+template <int CH> struct Maps {
+  CUtensorMap a[products<CH>()], b[products<CH>()];
 };
+constexpr int MAX_PAIRS = 96;   // a warp holds the pairs' counts, three a lane
 struct Params {
   WsHeader *hdr;
-  Product prod[3];           // BACK: the longer products first
-  int dx;                    // BACK: which one is DX
+  // The products in the order in which every pair takes its tiles of them, and how many of each it gets; deal: the order in which
+  // the host deals them out
+  int products, deal[PRODUCTS];
+  Product prod[PRODUCTS];
+  uint16_t count[PRODUCTS][MAX_PAIRS];
   bool more;                 // another kernel of the same call follows
-  int full, splits, units;   // tiles computed whole, parts of each of the others, units of work in all
-  float4 *part;              // [tile - full][part][slice][4][8][32] float4
-  int *arrived;              // [tile - full][slice][2]: parts claimed, parts written
+  // One product with its tiles cut along K (else splits = 1): parts of a tile, and parts in all
+  int splits, units;
+  float4 *part;              // [tile][part][slice][4][8][32] float4
+  int *arrived;              // [tile][slice][2]: parts claimed, parts written
+  // Rows of tiles that the launch's first product has written: warps arrived per row, and what makes a row complete
+  int *ready, *left;         // left: pairs that are done (the last one sets ready back to zero)
+  int rows, row_need;        // rows: 0 where nobody waits
   Gate gate;
   uint8_t *codes, *scales;   // GATEUP, DH: ab in 8 bits (null: bf16)
 };
@@ -97,79 +125,55 @@ __device__ __forceinline__ void place(Unit &t, const Product &o) {
   t.m = band * BAND + (r - t.n * height);
 }
 
-// The units of one pair, in order. One product: its tiles round by round, the last ones in parts.
-template <int K> struct Walk {
-  int u, step;
-  __device__ __forceinline__ Walk(int pair, int pairs, const Params &) : u(pair), step(pairs) {}
-  __device__ __forceinline__ bool next(Unit &t, const Params &p) {
-    if (u >= p.units) return false;
-    t.q = 0;
-    t.part = -1;
-    t.tile = u;
-    t.kb0 = 0;
-    t.kb1 = p.prod[0].num_kb;
-    if (u >= p.full && p.splits > 1) {
-      const int r = u - p.full, c = r / p.splits;
-      t.tile = p.full + c;
-      t.part = r - c * p.splits;
-      t.kb0 = (int)((int64_t)p.prod[0].num_kb * t.part / p.splits);
-      t.kb1 = (int)((int64_t)p.prod[0].num_kb * (t.part + 1) / p.splits);
-    }
-    place(t, p.prod[0]);
-    u += step;
-    return true;
+// The units of one pair, in order; the whole warp walks. In round t of a product the pairs that have more than t of its tiles
+// take consecutive ones.
+struct Walk {
+  int pair, pairs, u, c, t, base;
+  int n0, n1, n2;            // this lane's share of the product's counts
+  __device__ __forceinline__ Walk(int pair_, int pairs_, const Params &p) : pair(pair_), pairs(pairs_), u(pair_), c(0) { open(p); }
+  // (Loads of the parameters through their generic address: one per 32 lanes, where the constant path takes them lane by lane.)
+  static __device__ __forceinline__ int count(const uint16_t *at) {
+    uint16_t v;
+    asm volatile("ld.u16 %0, [%1];" : "=h"(v) : "l"(at));
+    return v;
   }
-};
-// The three products of the backward that only need dy, x, h and dab, in one launch: their tiles last for two spans (K of the
-// weight gradients is T, of dx 2f). Every pair first takes its share of the longer tiles, r pairs one more than the others;
-// the others then take shorter ones for as long, and what is left goes round.
-template <> struct Walk<BACK> {
-  int pair, pairs, state, i, end, step;
-  int longs, shorts, swap, r, even;   // swap: DX alone is the longer class, else the two weight gradients are
-  __device__ __forceinline__ int tiles(const Params &p, int q) const { return p.prod[q].m_tiles * p.prod[q].n_tiles; }
-  __device__ __forceinline__ Walk(int pair_, int pairs_, const Params &p) : pair(pair_), pairs(pairs_), state(0) {
-    swap = p.dx == 0;
-    const int first = tiles(p, 0), last = tiles(p, 2), mid = tiles(p, 1);
-    longs = swap ? first : first + mid;
-    shorts = swap ? mid + last : last;
-    r = longs % pairs;
-    even = r == 0 ? 0 : min(shorts, p.prod[0].num_kb / p.prod[2].num_kb * (pairs - r));
-    i = pair;
-    end = longs;
-    step = pairs;
+  __device__ __forceinline__ void open(const Params &p) {
+    const uint16_t *row = p.count[c] + (threadIdx.x & 31);
+    t = base = 0;
+    n0 = count(row);
+    n1 = count(row + 32);
+    n2 = count(row + 64);
   }
-  __device__ __forceinline__ bool next(Unit &t, const Params &p) {
-    while (i >= end) {
-      if (state == 0) {          // shorter tiles for the pairs that had one longer tile less
-        i = pair >= r ? pair - r : even;
-        end = even;
-        step = pairs - r;
-      } else if (state == 1) {   // the rest, those pairs first
-        i = even + (pair >= r ? pair - r : pair - r + pairs);
-        end = shorts;
-        step = pairs;
-      } else {
-        return false;
-      }
-      ++state;
+  __device__ __forceinline__ bool next(Unit &w, const Params &p) {
+    w.q = 0;
+    w.part = -1;
+    if (p.splits > 1) {
+      if (u >= p.units) return false;
+      w.tile = u / p.splits;
+      w.part = u - w.tile * p.splits;
+      w.kb0 = (int)((int64_t)p.prod[0].num_kb * w.part / p.splits);
+      w.kb1 = (int)((int64_t)p.prod[0].num_kb * (w.part + 1) / p.splits);
+      u += pairs;
+      place(w, p.prod[0]);
+      return true;
     }
-    const bool is_long = state == 0;
-    int tile = i;
-    t.q = is_long ? 0 : (swap ? 1 : 2);
-    const bool two = is_long != (bool)swap;    // the class of two products
-    if (two) {
-      const int n = tiles(p, t.q);
-      if (tile >= n) {
-        tile -= n;
-        ++t.q;
+    for (;;) {
+      const uint32_t b0 = __ballot_sync(0xffffffffu, n0 > t), b1 = __ballot_sync(0xffffffffu, n1 > t),
+                     b2 = __ballot_sync(0xffffffffu, n2 > t);
+      const uint32_t mine = pair < 32 ? b0 : (pair < 64 ? b1 : b2), below = (1u << (pair & 31)) - 1;
+      if (mine >> (pair & 31) & 1) {
+        w.tile = base + __popc(mine & below) + (pair >= 32 ? __popc(b0) : 0) + (pair >= 64 ? __popc(b1) : 0);
+        base += __popc(b0) + __popc(b1) + __popc(b2);
+        ++t;
+        break;
       }
+      if (++c >= p.products) return false;
+      open(p);
     }
-    t.tile = tile;
-    t.part = -1;
-    t.kb0 = 0;
-    t.kb1 = p.prod[t.q].num_kb;
-    place(t, p.prod[t.q]);
-    i += step;
+    w.q = c;
+    w.kb0 = 0;
+    w.kb1 = p.prod[w.q].num_kb;
+    place(w, p.prod[w.q]);
     return true;
   }
 };
@@ -215,6 +219,45 @@ __device__ __forceinline__ bool wait_count(const int *count, int n, volatile int
     }
   }
 }
+
+// What the producer knows of the rows that its units read.
+struct Rows {
+  bool all = false;          // every row is written
+  // One look. What it finds written is ordered before the TMA's reads.
+  __device__ __forceinline__ bool look(const Params &p, const Product &o, int m) {
+    if (o.needs == NOTHING || all) return true;
+    bool there = true;
+    const int lane = threadIdx.x & 31;
+    if (o.needs == ITS_ROWS) {
+      there = arrived(p.ready + m) == p.row_need;
+    } else {
+      for (int r = lane; r < p.rows; r += 32) there = there && arrived(p.ready + r) == p.row_need;
+    }
+    there = __all_sync(0xffffffffu, there);
+    if (there) {
+      asm volatile("fence.proxy.async;" ::: "memory");
+      all = o.needs == ALL_ROWS;
+    }
+    return there;
+  }
+  static __device__ __forceinline__ int arrived(const int *at) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+    return v;
+  }
+  __device__ __forceinline__ bool wait(const Params &p, const Product &o, int m, volatile int *abort_flag) {   // bounded
+    const uint64_t t0 = global_ns();
+    while (!look(p, o, m)) {
+      const bool late = global_ns() - t0 > kWaitLimitNs;
+      if (__any_sync(0xffffffffu, late || *abort_flag)) {
+        if (late) report(p.hdr, MOE_ERR_DEVICE_TIMEOUT, 46);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+    return true;
+  }
+};
 
 // Blocks on their way out and in. A warp holds 32 rows, one per lane; global memory wants consecutive bytes of a row from
 // neighbouring lanes. Blocks therefore pass through shared memory, W = 64 columns wide (128 bytes a row, eight lanes) or 32
@@ -403,7 +446,7 @@ template <int K> struct Ahead {
     commit();
   }
   __device__ __forceinline__ void start(const Params &p, const Product &o, uint32_t buf, int lane, int row0, int col0) {
-    if (K == DOWN || K == BACK) {
+    if (K == DOWN || K == DX) {
       if (o.in0) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -427,6 +470,25 @@ template <int K> struct Ahead {
     }
   }
 };
+
+// a becomes act(a) b
+template <bool CUBIC> __device__ __forceinline__ void gate32(float *a, const float *b, const Gate &g) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2)
+    split(mul(ffn::gated2<CUBIC>(pair(a[i], a[i + 1]), g), pair(b[i], b[i + 1])), a[i], a[i + 1]);
+}
+// a becomes da = v b act'(a), v (dh) becomes db = v act(a), b becomes h = act(a) b
+template <bool CUBIC> __device__ __forceinline__ void back32(float *a, float *b, float *v, const Gate &g) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    F2 act, slope;
+    ffn::gate_and_slope2<CUBIC>(pair(a[i], a[i + 1]), g, act, slope);
+    const F2 B = pair(b[i], b[i + 1]), V = pair(v[i], v[i + 1]);
+    split(mul(mul(V, B), slope), a[i], a[i + 1]);
+    split(mul(V, act), v[i], v[i + 1]);
+    split(mul(B, act), b[i], b[i + 1]);
+  }
+}
 
 // What becomes of the warp's slice: rows row0 .. row0 + 31 (a lane each), columns from col0 on (GATEUP: 64 features from
 // col0 on, a in blocks 0 and 1, b in blocks 2 and 3).
@@ -453,8 +515,8 @@ __device__ __forceinline__ void finish(Slice<K> &acc, Ahead<K> &ahead, const Par
         stage<64>(buf, lane, 4 * j, a);
         stage<64>(buf + BUF, lane, 4 * j, b);
       }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) a[i] = ffn::gated(a[i], p.gate) * b[i];
+      if (p.gate.k1 == 0.0f) gate32<false>(a, b, p.gate);
+      else gate32<true>(a, b, p.gate);
 #pragma unroll
       for (int c = 0; c < 4; ++c) qh[j][c] = pack_bf16x8(a + 8 * c);
     }
@@ -482,15 +544,8 @@ __device__ __forceinline__ void finish(Slice<K> &acc, Ahead<K> &ahead, const Par
           take<32, false>(here + 2048, lane, 0, b);
         }
         acc.load(j, lane, v);
-        // a becomes da, v becomes db; with codes b becomes h
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float act, slope;
-          ffn::gate_and_slope(a[i], p.gate, act, slope);
-          a[i] = v[i] * b[i] * slope;
-          v[i] *= act;
-          b[i] *= act;
-        }
+        if (p.gate.k1 == 0.0f) back32<false>(a, b, v, p.gate);
+        else back32<true>(a, b, v, p.gate);
         __syncwarp();
         stage<32>(here, lane, 0, a);
         stage<32>(here + 2048, lane, 0, v);
@@ -527,11 +582,11 @@ __device__ __forceinline__ void finish(Slice<K> &acc, Ahead<K> &ahead, const Par
   }
 }
 
-template <int K>
+template <int CH>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    ffn_gemm_kernel(const __grid_constant__ Maps<K> maps, const __grid_constant__ Params p) {
-  constexpr bool B_MN = K == DH || K == BACK;
-  auto a_mn = [&](const Unit &t) { return K == BACK && t.q != p.dx; };
+    ffn_gemm_kernel(const __grid_constant__ Maps<CH> maps, const __grid_constant__ Params p) {
+  constexpr bool B_MN = CH == BWD;
+  auto a_mn = [&](const Unit &t) { return CH == BWD && p.prod[t.q].op == DW; };
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *epi_smem = smem + STAGES * STAGE;
@@ -550,6 +605,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
   const uint32_t mma_done_bar = bar0 + 8u * (2 * STAGES + 4);
 
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  Walk walk(pair, pairs, p);
+  Unit t{};
   if (p.more) start_next();   // it may set itself up on SMs that this one has left
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -563,7 +621,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    for (int q = 0; q < products<K>(); ++q) {
+    for (int q = 0; q < products<CH>(); ++q) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.a[q])) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.b[q])) : "memory");
     }
@@ -577,21 +635,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();   // both CTAs: barriers initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   wait_previous();
+  bool more = walk.next(t, p);
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer (both CTAs)
     // The whole warp runs the loop and waits, converged; one elected lane issues the copies.
     int stage = 0;
     uint32_t phase = 0;
-    bool ok = true;
-    Walk<K> walk(pair, pairs, p);
-    for (Unit t; ok && walk.next(t, p);) {
+    bool ok = true, seen = false;      // seen: what the unit reads is known to be written
+    Rows rows;
+    while (ok && more) {
       const CUtensorMap *tmA = &maps.a[t.q], *tmB = &maps.b[t.q];
+      const Product &o = p.prod[t.q];
+      const bool along_m = a_mn(t);
       const int arow = t.m * TILE + (int)rank * HALF;
-      const int brow = K == GATEUP ? (int)rank * p.prod[0].N + t.n * HALF : t.n * TILE + (int)rank * HALF;
+      const int brow = CH == FWD && o.op == GATEUP ? (int)rank * o.N + t.n * HALF : t.n * TILE + (int)rank * HALF;
+      if (!seen && !rows.wait(p, o, t.m, abort_flag)) break;
+      Unit nx{};
+      more = walk.next(nx, p);
+      seen = false;
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        // a look ahead for the next unit while this one's copies are still queued up
+        if (kb == max(t.kb0, t.kb1 - 3)) seen = more && rows.look(p, p.prod[nx.q], nx.m);
         if (!mbar_spin_cluster(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 41)) {
           ok = false;
           break;
@@ -601,7 +667,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const uint32_t fb = mapa_shared(full_bar(stage), 0);   // the leader's full barrier
           if (leader) mbar_expect_tx(full_bar(stage), 2 * STAGE);
           const int kx = kb * BK;
-          if (a_mn(t)) {
+          if (along_m) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) tma_load_2d_pair(sA + q * (BK * 128), tmA, arow + 64 * q, kx, fb);
           } else {
@@ -620,6 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           phase ^= 1u;
         }
       }
+      t = nx;
     }
   } else if (warp == 1 && leader) {
     // ------------------------------------------------------------------ MMA issuer (leader only)
@@ -631,8 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     bool ok = true, issued = false;
     const uint64_t desc_a_mn = sdesc(sbase, BK * 128, 1024), desc_a_k = sdesc(sbase, 16, 1024);
     const uint64_t desc_b = B_MN ? sdesc(sbase + OPERAND, BK * 128, 1024) : sdesc(sbase + OPERAND, 16, 1024);
-    Walk<K> walk(pair, pairs, p);
-    for (Unit t; ok && walk.next(t, p);) {
+    for (; ok && more; more = walk.next(t, p)) {
       const uint64_t desc_a = a_mn(t) ? desc_a_mn : desc_a_k;
       const uint32_t id = a_mn(t) ? idesc(true, B_MN) : idesc(false, B_MN), a_step = a_mn(t) ? 2048 >> 4 : 32 >> 4;
       if (!mbar_ready_cluster(tempty_bar(acc), acc_phase ^ 1u) &&
@@ -681,14 +747,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int slice = (int)rank * EPI_WARPS + (warp - 2);
     int acc = 0;
     uint32_t acc_phase = 0;
-    Walk<K> walk(pair, pairs, p);
-    for (Unit t; walk.next(t, p);) {
+    bool ok = true;
+    // One unit of product `op`
+    auto unit = [&](auto op) {
+      constexpr int K = decltype(op)::value;
       const Product &o = p.prod[t.q];
       const int row0 = t.m * TILE + (int)rank * HALF + quarter * 32;
       const int col0 = K == GATEUP ? t.n * HALF + 64 * hh : t.n * TILE + HALF * hh;
       Ahead<K> ahead;
       ahead.start(p, o, buf, lane, row0, col0);
-      if (!wait_here(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 44)) break;
+      if (!wait_here(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 44)) return false;
       tc_fence_after();
       Slice<K> s;
       s.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * TILE + (K == GATEUP ? 64 : HALF) * hh);
@@ -696,7 +764,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       s.mine = t.part;
       bool here = true;   // the slice is finished by this warp
       if (t.part >= 0) {
-        const int r = t.tile - p.full;
+        const int r = t.tile;
         int *claimed = p.arrived + (r * SLICES + slice) * 2, *written = claimed + 1;
         s.part = p.part + ((int64_t)r * p.splits * SLICES + slice) * (SLICE_FLOATS / 4);
         int before = 0;
@@ -717,7 +785,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (lane == 0) atomicAdd(written, 1);
         } else {
           // the other parts' warps have all claimed before: they are writing, or have written, and wait for nothing
-          if (!wait_count(written, p.splits - 1, abort_flag, p.hdr)) break;
+          if (!wait_count(written, p.splits - 1, abort_flag, p.hdr)) return false;
           if (lane == 0) *claimed = *written = 0;
           s.ask(0, lane);
         }
@@ -726,8 +794,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(tempty_bar(acc));
+      if ((K == GATEUP || K == DH) && p.rows > 0) {   // others in this launch read what this warp has written, by TMA
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) atomicAdd(p.ready + t.m, 1);
+      }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
+      return true;
+    };
+    for (; ok && more; more = walk.next(t, p)) {
+      const int op = p.prod[t.q].op;
+      if (CH == FWD) {
+        ok = op == GATEUP ? unit(std::integral_constant<int, GATEUP>()) : unit(std::integral_constant<int, DOWN>());
+      } else {
+        ok = op == DH ? unit(std::integral_constant<int, DH>()) : unit(std::integral_constant<int, DX>());
+      }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
@@ -738,6 +821,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   tc_fence_before();
   cluster_sync();   // no CTA leaves while its peer may still signal its barriers or use its TMEM
+  if (p.rows > 0 && leader && warp == 0) {   // nobody of this pair waits any more: the last pair clears up
+    int before = 0;
+    if (lane == 0) before = atomicAdd(p.left, 1);
+    if (__shfl_sync(0xffffffffu, before, 0) == pairs - 1) {
+      for (int r = lane; r < p.rows; r += 32) p.ready[r] = 0;
+      if (lane == 0) *p.left = 0;
+    }
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -750,21 +841,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 // accumulators costs about as much as kPartCost of them (6.5 us: claim, store, fence, count, load).
 constexpr int kPartCost = 24;
 struct Deal {
-  int full, splits, units;
+  int splits, units;
   size_t bytes;   // of the parts
 };
 static Deal deal(int64_t tiles_m, int64_t tiles_n, int num_kb, int pairs) {
   const int64_t tiles = tiles_m * tiles_n;
-  Deal best{(int)tiles, 1, (int)tiles, 0};
-  const int rem = (int)(tiles % pairs);
-  if (rem == 0) return best;
-  int64_t cost = num_kb;   // of the last round
+  Deal best{1, (int)tiles, 0};
+  if (tiles >= pairs) return best;   // one launch with the call's other products evens out an incomplete round
+  const int rem = (int)tiles;
+  int64_t cost = num_kb;
   for (int s = 2; s <= MAX_SPLIT && s <= num_kb; ++s) {
     if (rem * s > 2 * pairs) break;
     const int64_t c = (int64_t)((rem * s + pairs - 1) / pairs) * ((num_kb + s - 1) / s + kPartCost);
     if (c < cost) {
       cost = c;
-      best = Deal{(int)(tiles - rem), s, (int)(tiles - rem) + rem * s, (size_t)rem * s * SLICES * SLICE_FLOATS * 4};
+      best = Deal{s, rem * s, (size_t)rem * s * SLICES * SLICE_FLOATS * 4};
     }
   }
   return best;
@@ -793,41 +884,97 @@ template <auto KERNEL> static int pairs_resident(int &pairs) {
   return MOE_OK;
 }
 
-template <int K>
-static int start(const Maps<K> &maps, Params p, int units, const ffn::Block &blk, bool first, cudaStream_t s) {
-  p.more = first;            // a call makes two launches
+// The counters in front of the parts: for cut tiles, then pairs that are done (one line), then rows of tiles.
+static size_t counter_bytes(int64_t T) { return kArrivedBytes + 128 + (size_t)up(up(T, TILE), 32) * 128; }
+
+// How the products' tiles are dealt to the pairs: product after product (in p.deal's order), each tile to the pair with the least work so far (whole
+// rounds at once, but for the last two).
+static void deal_out(Params &p, int pairs) {
+  int64_t load[MAX_PAIRS] = {};
+  memset(p.count, 0, sizeof(p.count));
+  std::pair<int64_t, int> heap[MAX_PAIRS];
+  const auto later = [](const std::pair<int64_t, int> &x, const std::pair<int64_t, int> &y) { return x > y; };
+  for (int i = 0; i < p.products; ++i) {
+    const int c = p.deal[i];
+    int64_t n = (int64_t)p.prod[c].m_tiles * p.prod[c].n_tiles;
+    const int64_t cost = p.prod[c].num_kb + 2;
+    const int64_t even = n / pairs > 2 ? n / pairs - 2 : 0;
+    for (int k = 0; k < pairs; ++k) {
+      p.count[c][k] = (uint16_t)even;
+      load[k] += even * cost;
+      heap[k] = {load[k], k};
+    }
+    std::make_heap(heap, heap + pairs, later);
+    for (n -= even * pairs; n > 0; --n) {
+      std::pop_heap(heap, heap + pairs, later);
+      auto &least = heap[pairs - 1];
+      ++p.count[c][least.second];
+      least.first += cost;
+      std::push_heap(heap, heap + pairs, later);
+    }
+    for (int k = 0; k < pairs; ++k) load[heap[k].second] = heap[k].first;
+  }
+}
+
+// rows > 0: units wait for others of the same launch, so all its pairs have to be resident: a cooperative launch. `after`: launched
+// as a dependent of the kernel before it.
+template <int CH>
+static int start(const Maps<CH> &maps, Params &p, const ffn::Block &blk, bool after, cudaStream_t s) {
   p.hdr = blk.hdr;
   p.gate = blk.gate;
-  p.arrived = (int *)blk.ws;
-  p.part = (float4 *)((uint8_t *)blk.ws + kArrivedBytes);
+  uint8_t *ws = (uint8_t *)blk.ws;
+  p.arrived = (int *)ws;
+  p.left = (int *)(ws + kArrivedBytes);
+  p.ready = (int *)(ws + kArrivedBytes + 128);
+  p.part = (float4 *)(ws + counter_bytes(blk.T));
   int pairs = 0;
-  const int rc = pairs_resident<ffn_gemm_kernel<K>>(pairs);
+  const int rc = pairs_resident<ffn_gemm_kernel<CH>>(pairs);
   if (rc) return rc;
-  if (pairs > units) pairs = units;
-  if (first) {
-    ffn_gemm_kernel<K><<<2 * pairs, THREADS, SMEM, s>>>(maps, p);
-    MOE_CHECK_LAUNCH();
-  } else {
-    MOE_TRY_CUDA(launch_after(ffn_gemm_kernel<K>, dim3(2 * pairs), dim3(THREADS), (size_t)SMEM, s, maps, p));
+  if (pairs > MAX_PAIRS) pairs = MAX_PAIRS;
+  int64_t units = p.units;
+  if (p.splits == 1) {
+    units = 0;
+    for (int q = 0; q < p.products; ++q) units += (int64_t)p.prod[q].m_tiles * p.prod[q].n_tiles;
+    if (units > (int64_t)pairs * 60000) return MOE_ERR_UNSUPPORTED;   // counts have 16 bits
   }
+  if (pairs > units) pairs = (int)units;
+  if (p.splits == 1) deal_out(p, pairs);
+  if (after) {
+    MOE_TRY_CUDA(launch_after(ffn_gemm_kernel<CH>, dim3(2 * pairs), dim3(THREADS), (size_t)SMEM, s, maps, p));
+    return MOE_OK;
+  }
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.rows > 0 ? 1 : 0;
+  MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<CH>, maps, p));
   return MOE_OK;
 }
-static Product product(int64_t M, int64_t N, int64_t k, int64_t cols_per_tile) {
+
+static Product product(int op, int64_t M, int64_t N, int64_t k) {
   Product o{};
+  o.op = op;
   o.M = (int)M;
   o.N = (int)N;
   o.m_tiles = (int)up(M, TILE);
-  o.n_tiles = (int)up(N, cols_per_tile);
+  o.n_tiles = (int)up(N, op == GATEUP ? HALF : TILE);
   o.num_kb = (int)up(k, BK);
   return o;
 }
-// One product
-template <int K> static int launch(const Maps<K> &maps, Params p, const ffn::Block &blk, bool first, cudaStream_t s) {
-  const Deal d = deal(p.prod[0].m_tiles, p.prod[0].n_tiles, p.prod[0].num_kb, kPairs);
-  p.full = d.full;
+static Deal deal_of(const Product &o) { return deal(o.m_tiles, o.n_tiles, o.num_kb, kPairs); }
+
+// One launch of the first product alone
+static void alone(Params &p, const Deal &d) {
+  p.products = 1;
+  p.deal[0] = 0;
   p.splits = d.splits;
   p.units = d.units;
-  return start<K>(maps, p, d.units, blk, first, s);
 }
 
 }  // namespace ffng
@@ -840,78 +987,113 @@ using namespace tc::ffng;
 typedef __nv_bfloat16 bf16;
 
 size_t gemm_workspace(int T, int d, int f, bool backward) {
-  size_t most = 0;
-  auto with = [&](const Product &o) {
-    const Deal dl = deal(o.m_tiles, o.n_tiles, o.num_kb, kPairs);
-    if (dl.bytes > most) most = dl.bytes;
-  };
-  with(product(T, f, d, HALF));                  // GATEUP
-  with(product(T, d, f, TILE));                  // DOWN
-  if (backward) with(product(T, f, d, TILE));    // DH
-  return kArrivedBytes + most;
+  size_t most = deal_of(product(GATEUP, T, f, d)).bytes;
+  most = std::max(most, deal_of(product(DOWN, T, d, f)).bytes);
+  if (backward) most = std::max(most, deal_of(product(DH, T, f, d)).bytes);
+  return counter_bytes(T) + most;
 }
 
+// Forward: both products in one launch, y's tiles waiting for the rows of h that they read; where tiles are cut (few of them, many
+// idle pairs) two launches.
 int gemm_fwd(const Block &b, cudaStream_t s) {
-  Maps<GATEUP> m1;
-  if (!make_map(&m1.a[0], b.x, b.T, b.d, HALF) || !make_map(&m1.b[0], b.w_gate_up, 2 * (uint64_t)b.f, b.d, HALF)) return MOE_ERR_CUDA;
+  Maps<FWD> m;
+  if (!make_map(&m.a[0], b.x, b.T, b.d, HALF) || !make_map(&m.b[0], b.w_gate_up, 2 * (uint64_t)b.f, b.d, HALF) ||
+      !make_map(&m.a[1], b.h, b.T, b.f, HALF) || !make_map(&m.b[1], b.w_down, b.d, b.f, HALF))
+    return MOE_ERR_CUDA;
+  Product up_ = product(GATEUP, b.T, b.f, b.d), down = product(DOWN, b.T, b.d, b.f);
   Params p{};
-  p.prod[0] = product(b.T, b.f, b.d, HALF);
   if (b.scales) {
     p.codes = (uint8_t *)b.ab;
     p.scales = b.scales;
   } else {
-    p.prod[0].out0 = (bf16 *)b.ab;
+    up_.out0 = (bf16 *)b.ab;
   }
-  p.prod[0].out1 = (bf16 *)b.h;
-  int rc = launch<GATEUP>(m1, p, b, true, s);
+  up_.out1 = (bf16 *)b.h;
+  down.in0 = (const bf16 *)b.add;
+  down.out0 = (bf16 *)b.y;
+  const Deal d0 = deal_of(up_), d1 = deal_of(down);
+  p.prod[0] = up_;
+  p.splits = 1;
+  if (d0.splits == 1 && d1.splits == 1) {
+    down.needs = ITS_ROWS;
+    p.prod[1] = down;
+    p.products = 2;
+    p.deal[1] = 1;
+    p.rows = up_.m_tiles;
+    p.row_need = up_.n_tiles * SLICES;
+    return start<FWD>(m, p, b, false, s);
+  }
+  alone(p, d0);
+  p.more = true;
+  const int rc = start<FWD>(m, p, b, false, s);
   if (rc) return rc;
-  Maps<DOWN> m2;
-  if (!make_map(&m2.a[0], b.h, b.T, b.f, HALF) || !make_map(&m2.b[0], b.w_down, b.d, b.f, HALF)) return MOE_ERR_CUDA;
-  p = Params{};
-  p.prod[0] = product(b.T, b.d, b.f, TILE);
-  p.prod[0].in0 = (const bf16 *)b.add;
-  p.prod[0].out0 = (bf16 *)b.y;
-  return launch<DOWN>(m2, p, b, false, s);
+  p.prod[0] = down;
+  m.a[0] = m.a[1];
+  m.b[0] = m.b[1];
+  alone(p, d1);
+  p.more = false;
+  return start<FWD>(m, p, b, true, s);
 }
 
+// Backward: da, db (and h, from 8 bits), then dx = dab Wgu (+ dx_in), dWd = dy^T h and dWgu = dab^T x, in one launch. dx waits for
+// the rows of dab that it reads, which are there first, dWgu for all of them, dWd for nothing (for all rows of h where those
+// are written here): it is taken first then, by the pairs that the first product leaves with the least work. The longer
+// tiles are dealt out before the shorter ones, which even out what those leave.
 int gemm_bwd(const Block &b, cudaStream_t s) {
   const uint64_t T = b.T, d = b.d, f = b.f;
-  // da, db (and h, from 8 bits)
-  Maps<DH> m1;
-  if (!make_map(&m1.a[0], b.dy, T, d, HALF) || !make_map(&m1.b[0], b.w_down, d, f, BK)) return MOE_ERR_CUDA;
+  Product dh = product(DH, b.T, b.f, b.d), dx = product(DX, b.T, b.d, 2 * (int64_t)b.f), down = product(DW, b.d, b.f, b.T),
+          gu = product(DW, 2 * (int64_t)b.f, b.d, b.T);
   Params p{};
-  p.prod[0] = product(b.T, b.f, b.d, TILE);
   if (b.scales) {
     p.codes = (uint8_t *)b.ab;
     p.scales = b.scales;
-    p.prod[0].out1 = (bf16 *)b.h;
+    dh.out1 = (bf16 *)b.h;
   } else {
-    p.prod[0].in0 = (const bf16 *)b.ab;
+    dh.in0 = (const bf16 *)b.ab;
   }
-  p.prod[0].out0 = (bf16 *)b.dab;
-  int rc = launch<DH>(m1, p, b, true, s);
-  if (rc) return rc;
-  // dWgu [2f, d] = dab^T x, dWd [d, f] = dy^T h, dx = dab Wgu (+ dx_in), the longer tiles first
-  p = Params{};
-  Product gu = product(2 * (int64_t)b.f, b.d, b.T, TILE), down = product(b.d, b.f, b.T, TILE), dx = product(b.T, b.d, 2 * (int64_t)b.f, TILE);
-  gu.out0 = (bf16 *)b.dw_gate_up;
-  down.out0 = (bf16 *)b.dw_down;
+  dh.out0 = (bf16 *)b.dab;
   dx.in0 = (const bf16 *)b.add;
   dx.out0 = (bf16 *)b.dx;
-  const int w = dx.num_kb > gu.num_kb ? 1 : 0;
-  p.dx = w ? 0 : 2;
-  p.prod[w] = gu;
-  p.prod[w + 1] = down;
-  p.prod[p.dx] = dx;
-  Maps<BACK> m2;
-  if (!make_map(&m2.a[w], b.dab, T, 2 * f, BK) || !make_map(&m2.b[w], b.x, T, d, BK) || !make_map(&m2.a[w + 1], b.dy, T, d, BK) ||
-      !make_map(&m2.b[w + 1], b.h, T, f, BK) || !make_map(&m2.a[p.dx], b.dab, T, 2 * f, HALF) ||
-      !make_map(&m2.b[p.dx], b.w_gate_up, 2 * f, d, BK))
+  down.out0 = (bf16 *)b.dw_down;
+  gu.out0 = (bf16 *)b.dw_gate_up;
+  const Deal d0 = deal_of(dh);
+  const bool one = d0.splits == 1, dx_longer = dx.num_kb > gu.num_kb;
+  if (one) {
+    p.rows = dh.m_tiles;
+    p.row_need = dh.n_tiles * SLICES;
+    dx.needs = ITS_ROWS;
+    gu.needs = ALL_ROWS;
+    down.needs = b.scales ? ALL_ROWS : NOTHING;
+  }
+  const int ix = b.scales ? 1 : 2, iw = 3 - ix;   // dx and dWd
+  Maps<BWD> m;
+  p.prod[0] = dh;
+  p.prod[ix] = dx;
+  p.prod[iw] = down;
+  p.prod[3] = gu;
+  if (!make_map(&m.a[0], b.dy, T, d, HALF) || !make_map(&m.b[0], b.w_down, d, f, BK) || !make_map(&m.a[ix], b.dab, T, 2 * f, HALF) ||
+      !make_map(&m.b[ix], b.w_gate_up, 2 * f, d, BK) || !make_map(&m.a[iw], b.dy, T, d, BK) || !make_map(&m.b[iw], b.h, T, f, BK) ||
+      !make_map(&m.a[3], b.dab, T, 2 * f, BK) || !make_map(&m.b[3], b.x, T, d, BK))
     return MOE_ERR_CUDA;
   p.splits = 1;
-  int64_t units = 0;
-  for (const Product &o : p.prod) units += (int64_t)o.m_tiles * o.n_tiles;
-  return start<BACK>(m2, p, (int)(units < kPairs ? units : kPairs), b, false, s);
+  p.products = 4;
+  p.deal[1] = dx_longer ? ix : iw;
+  p.deal[2] = dx_longer ? iw : 3;
+  p.deal[3] = dx_longer ? 3 : ix;
+  if (one) return start<BWD>(m, p, b, false, s);
+  Params first = p;
+  alone(first, d0);
+  first.more = true;
+  const int rc = start<BWD>(m, first, b, false, s);
+  if (rc) return rc;
+  p.products = 3;
+  for (int q = 0; q < 3; ++q) {
+    p.prod[q] = p.prod[q + 1];
+    p.deal[q] = p.deal[q + 1] - 1;
+    m.a[q] = m.a[q + 1];
+    m.b[q] = m.b[q + 1];
+  }
+  return start<BWD>(m, p, b, true, s);
 }
 
 }  // namespace ffn
