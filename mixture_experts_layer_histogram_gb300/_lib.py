@@ -509,60 +509,74 @@ def _scale_bytes8(rows, cols):
     return rows * -(-cols // 32)
 
 
+def _at(name, t, dtype, shape, dev):
+    """The address of a tensor argument of this type and shape, contiguous, on the current GPU `dev`."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _want(name, t, dtype, shape)
+    return _on(name, t, dev)
+
+
+def _on(name, t, dev):
+    """The address of a tensor on the current GPU, on which the launch goes."""
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError("libmoe takes CUDA tensors only")
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _bytes_on(name, t, n, dev):
+    """The address of a tensor of at least n bytes on the current GPU."""
+    _bytes_at_least(name, t, n)
+    return _on(name, t, dev)
+
+
 def moe_act8_quantize(x, codes, scales, stream=None):
     """x [..., K] (rows in order) -> codes [..., K] uint8, scales [moe_act8_scale_bytes(rows, K)] uint8."""
-    shape, dt = x.shape, x.dtype
+    shape, dt, dev = x.shape, x.dtype, _device()
     R, K = _rows(shape)
-    _here(x, codes, scales)
     _ok("moe_act8_quantize", lib().moe_act8_quantize(
-        _ptr("x", x, dt, shape), dtype_code(dt), R, K, _ptr("codes", codes, _U8, shape),
-        _bytes_at_least("scales", scales, _scale_bytes8(R, K)), _s(stream)))
+        _at("x", x, dt, shape, dev), dtype_code(dt), R, K, _at("codes", codes, _U8, shape, dev),
+        _bytes_on("scales", scales, _scale_bytes8(R, K), dev), _s(stream)))
 
 
 def moe_act8_dequantize(codes, scales, x, stream=None):
     """The values that codes and scales stand for, into x [..., K]."""
-    shape, dt = x.shape, x.dtype
+    shape, dt, dev = x.shape, x.dtype, _device()
     R, K = _rows(shape)
-    _here(codes, scales, x)
     _ok("moe_act8_dequantize", lib().moe_act8_dequantize(
-        _ptr("codes", codes, _U8, shape), _bytes_at_least("scales", scales, _scale_bytes8(R, K)), R, K, dtype_code(dt),
-        _ptr("x", x, dt, shape), _s(stream)))
+        _at("codes", codes, _U8, shape, dev), _bytes_on("scales", scales, _scale_bytes8(R, K), dev), R, K, dtype_code(dt),
+        _at("x", x, dt, shape, dev), _s(stream)))
 
 
-def _here(*tensors):
-    """Refuses tensors of another GPU than the current one, on which the launch would go."""
-    dev = _device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-
-
-def _opt(name, t, dtype, shape):
-    return None if t is None else _ptr(name, t, dtype, shape)
+def layer_norm_fwd_into(x, w, b, T, d, dt, n, mean, rstd, codes, scales, eps, stream):
+    """The call behind moe_layer_norm_fwd and LayerNorm.forward: checks its inputs; n, mean, rstd, codes and scales are the
+    addresses of outputs of type dt and fitting size (all but n may be None)."""
+    dev, vec = _device(), (d,)
+    _ok("moe_layer_norm_fwd", lib().moe_layer_norm_fwd(
+        _at("x", x, dt, (T, d), dev), _at("w", w, dt, vec, dev), None if b is None else _at("b", b, dt, vec, dev), T, d,
+        dtype_code(dt), eps, n, mean, rstd, codes, scales, _s(stream)))
 
 
 def moe_layer_norm_fwd(x, w, b, n, mean=None, rstd=None, codes=None, scales=None, eps=1e-5, stream=None):
     """n = z w + b, z = (x - mean) rstd, x [T, d]; b may be None (zero). mean, rstd [T] fp32 and z in 8 bits (codes [T, d],
     scales) are written where they are given."""
     T, d = x.shape
-    dt, rows, vec = x.dtype, (T, d), (d,)
-    f32 = torch.float32
-    _here(x, w, b, n, mean, rstd, codes, scales)
-    _ok("moe_layer_norm_fwd", lib().moe_layer_norm_fwd(
-        _ptr("x", x, dt, rows), _ptr("w", w, dt, vec), _opt("b", b, dt, vec), T, d, dtype_code(dt), eps,
-        _ptr("n", n, dt, rows), _opt("mean", mean, f32, (T,)), _opt("rstd", rstd, f32, (T,)),
-        _opt("codes", codes, _U8, rows), None if scales is None else _bytes_at_least("scales", scales, _scale_bytes8(T, d)),
-        _s(stream)))
+    dt, dev, f32 = x.dtype, _device(), torch.float32
+    layer_norm_fwd_into(
+        x, w, b, T, d, dt, _at("n", n, dt, (T, d), dev), None if mean is None else _at("mean", mean, f32, (T,), dev),
+        None if rstd is None else _at("rstd", rstd, f32, (T,), dev), None if codes is None else _at("codes", codes, _U8, (T, d), dev),
+        None if scales is None else _bytes_on("scales", scales, _scale_bytes8(T, d), dev), eps, stream)
 
 
 def moe_layer_norm_restore(codes, scales, w, b, n, stream=None):
     """n = z w + b with the z that codes and scales stand for; b may be None."""
     T, d = n.shape
-    dt = n.dtype
-    _here(codes, scales, w, b, n)
+    dt, dev = n.dtype, _device()
     _ok("moe_layer_norm_restore", lib().moe_layer_norm_restore(
-        _ptr("codes", codes, _U8, (T, d)), _bytes_at_least("scales", scales, _scale_bytes8(T, d)), _ptr("w", w, dt, (d,)),
-        _opt("b", b, dt, (d,)), T, d, dtype_code(dt), _ptr("n", n, dt, (T, d)), _s(stream)))
+        _at("codes", codes, _U8, (T, d), dev), _bytes_on("scales", scales, _scale_bytes8(T, d), dev), _at("w", w, dt, (d,), dev),
+        None if b is None else _at("b", b, dt, (d,), dev), T, d, dtype_code(dt), _at("n", n, dt, (T, d), dev), _s(stream)))
 
 
 def moe_layer_norm_bwd_workspace_size(T, d, dtype):
@@ -573,13 +587,16 @@ def moe_layer_norm_bwd(dn, x, codes, scales, mean, rstd, w, dx_in, dx, dw, db, w
     """Backward of moe_layer_norm_fwd, from x and mean or from codes and scales (the others None); dx_in (may be None, may be
     dx) is added to dx; db may be None (not wanted)."""
     T, d = dn.shape
-    dt, rows, vec, f32 = dn.dtype, (T, d), (d,), torch.float32
-    _here(dn, x, codes, scales, mean, rstd, w, dx_in, dx, dw, db, ws)
+    dt, dev, rows, vec, f32 = dn.dtype, _device(), (T, d), (d,), torch.float32
+
+    def opt(name, t, dtype, shape):
+        return None if t is None else _at(name, t, dtype, shape, dev)
+
     _ok("moe_layer_norm_bwd", lib().moe_layer_norm_bwd(
-        _ptr("dn", dn, dt, rows), _opt("x", x, dt, rows), _opt("codes", codes, _U8, rows),
-        None if scales is None else _bytes_at_least("scales", scales, _scale_bytes8(T, d)), _opt("mean", mean, f32, (T,)),
-        _ptr("rstd", rstd, f32, (T,)), _ptr("w", w, dt, vec), _opt("dx_in", dx_in, dt, rows), T, d, dtype_code(dt), eps,
-        _ptr("dx", dx, dt, rows), _ptr("dw", dw, dt, vec), _opt("db", db, dt, vec), _p(ws),
+        _at("dn", dn, dt, rows, dev), opt("x", x, dt, rows), opt("codes", codes, _U8, rows),
+        None if scales is None else _bytes_on("scales", scales, _scale_bytes8(T, d), dev), opt("mean", mean, f32, (T,)),
+        _at("rstd", rstd, f32, (T,), dev), _at("w", w, dt, vec, dev), opt("dx_in", dx_in, dt, rows), T, d, dtype_code(dt), eps,
+        _at("dx", dx, dt, rows, dev), _at("dw", dw, dt, vec, dev), opt("db", db, dt, vec), _on("ws", ws, dev),
         ws.numel() * ws.element_size(), _s(stream)))
 
 
@@ -587,42 +604,49 @@ def moe_ffn_workspace_size(T, d, f, dtype, backward):
     return int(lib().moe_ffn_workspace_size(T, d, f, dtype, int(bool(backward))))
 
 
-def _kept(ab, ab_scales, dt, T, f):
+def kept(ab, ab_scales, dt, T, f):
     """What `keep` says, and the addresses of ab and ab_scales: nothing, ab in dt, or codes and scales."""
+    dev = _device()
     if ab is None:
         if ab_scales is not None:
             raise ValueError("ab_scales belong to an ab in 8 bits")
         return KEEP_NONE, None, None
     if ab_scales is None:
-        return KEEP_ALL, _ptr("ab", ab, dt, (T, 2 * f)), None
-    return KEEP_F8, _ptr("ab", ab, _U8, (T, 2 * f)), _bytes_at_least("ab_scales", ab_scales, _scale_bytes8(T, 2 * f))
+        return KEEP_ALL, _at("ab", ab, dt, (T, 2 * f), dev), None
+    return KEEP_F8, _at("ab", ab, _U8, (T, 2 * f), dev), _bytes_on("ab_scales", ab_scales, _scale_bytes8(T, 2 * f), dev)
+
+
+def ffn_fwd_into(x, w_gate_up, w_down, y_in, T, d, f, dt, act, keep, h, y, ws, ws_bytes, stream):
+    """The call behind moe_ffn_fwd and GatedFFN.forward: checks its inputs; keep is what kept() says of fitting buffers; h, y and ws
+    are the addresses of buffers of type dt and fitting size."""
+    dev = _device()
+    _ok("moe_ffn_fwd", lib().moe_ffn_fwd(
+        _at("x", x, dt, (T, d), dev), _at("w_gate_up", w_gate_up, dt, (2 * f, d), dev), _at("w_down", w_down, dt, (d, f), dev),
+        None if y_in is None else _at("y_in", y_in, dt, (T, d), dev), T, d, f, dtype_code(dt), act, keep[0], keep[1], keep[2], h, y,
+        ws, ws_bytes, _s(stream)))
 
 
 def moe_ffn_fwd(x, w_gate_up, w_down, y_in, ab, ab_scales, h, y, ws, act=ACT_SILU, stream=None):
     """y = y_in + (act(x Wg^T) * (x Wu^T)) Wd^T, x [T, d], w_gate_up [2f, d], w_down [d, f]. y_in may be None, and may be y.
     ab: None (nothing kept), [T, 2f] in x's type, or [T, 2f] uint8 codes with ab_scales. h [T, f] is written."""
     T, d = x.shape
-    f, dt = w_down.shape[1], x.dtype
-    _here(x, w_gate_up, w_down, y_in, ab, ab_scales, h, y, ws)
-    keep, ab_p, sc_p = _kept(ab, ab_scales, dt, T, f)
-    _ok("moe_ffn_fwd", lib().moe_ffn_fwd(
-        _ptr("x", x, dt, (T, d)), _ptr("w_gate_up", w_gate_up, dt, (2 * f, d)), _ptr("w_down", w_down, dt, (d, f)),
-        _opt("y_in", y_in, dt, (T, d)), T, d, f, dtype_code(dt), act, keep, ab_p, sc_p, _ptr("h", h, dt, (T, f)),
-        _ptr("y", y, dt, (T, d)), _p(ws), ws.numel() * ws.element_size(), _s(stream)))
+    f, dt, dev = w_down.shape[1], x.dtype, _device()
+    ffn_fwd_into(x, w_gate_up, w_down, y_in, T, d, f, dt, act, kept(ab, ab_scales, dt, T, f), _at("h", h, dt, (T, f), dev),
+                 _at("y", y, dt, (T, d), dev), _on("ws", ws, dev), ws.numel() * ws.element_size(), stream)
 
 
 def moe_ffn_bwd(dy, x, ab, ab_scales, h, w_gate_up, w_down, dx_in, dab, dx, dw_gate_up, dw_down, ws, act=ACT_SILU,
                 stream=None):
     """Backward of moe_ffn_fwd from the ab (and h, or ab_scales) that it kept; dx_in (may be None, may be dx) is added to dx."""
     T, d = dy.shape
-    f, dt = w_down.shape[1], dy.dtype
-    _here(dy, x, ab, ab_scales, h, w_gate_up, w_down, dx_in, dab, dx, dw_gate_up, dw_down, ws)
-    keep, ab_p, sc_p = _kept(ab, ab_scales, dt, T, f)
+    f, dt, dev = w_down.shape[1], dy.dtype, _device()
+    keep, ab_p, sc_p = kept(ab, ab_scales, dt, T, f)
     _ok("moe_ffn_bwd", lib().moe_ffn_bwd(
-        _ptr("dy", dy, dt, (T, d)), _ptr("x", x, dt, (T, d)), ab_p, sc_p, _ptr("h", h, dt, (T, f)),
-        _ptr("w_gate_up", w_gate_up, dt, (2 * f, d)), _ptr("w_down", w_down, dt, (d, f)), _opt("dx_in", dx_in, dt, (T, d)),
-        T, d, f, dtype_code(dt), act, keep, _ptr("dab", dab, dt, (T, 2 * f)), _ptr("dx", dx, dt, (T, d)),
-        _ptr("dw_gate_up", dw_gate_up, dt, (2 * f, d)), _ptr("dw_down", dw_down, dt, (d, f)), _p(ws),
+        _at("dy", dy, dt, (T, d), dev), _at("x", x, dt, (T, d), dev), ab_p, sc_p, _at("h", h, dt, (T, f), dev),
+        _at("w_gate_up", w_gate_up, dt, (2 * f, d), dev), _at("w_down", w_down, dt, (d, f), dev),
+        None if dx_in is None else _at("dx_in", dx_in, dt, (T, d), dev), T, d, f, dtype_code(dt), act, keep,
+        _at("dab", dab, dt, (T, 2 * f), dev), _at("dx", dx, dt, (T, d), dev),
+        _at("dw_gate_up", dw_gate_up, dt, (2 * f, d), dev), _at("dw_down", dw_down, dt, (d, f), dev), _on("ws", ws, dev),
         ws.numel() * ws.element_size(), _s(stream)))
 
 

@@ -9,8 +9,13 @@
 //
 // A product with few tiles and a long K is shared by a cluster of up to eight blocks, a part of K each: each block leaves its
 // tile in its shared memory and finishes a share of the rows, adding the parts up in the blocks' order.
-// Measured at 203 x 501 x 1337: forward and backward 409 us without the cluster and with one step in flight.
+// Measured at 203 x 501 x 1337 (2.4 GFLOP), forward and backward: 409 us without the cluster and with one step in flight, 155 with
+// both, 127 with addresses formed once and K cut by the work per SM. What bounds it then is FMA issue on SMs that get three
+// blocks where others get two, and rows and columns past the edge (203 rows are computed as 256). Launched as dependents of one
+// another the six kernels took 145 us.
 #include <cooperative_groups.h>
+
+#include <atomic>
 
 #include "f32x2.cuh"
 #include "ffn.cuh"
@@ -60,32 +65,46 @@ template <int KIND, int B> __global__ void __launch_bounds__(Tile<B>::THREADS) f
   const int all = (p.K + BK - 1) / BK;
   const int s0 = (int)((int64_t)all * part / splits), s1 = (int)((int64_t)all * (part + 1) / splits);
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
-  // Element i of this thread: consecutive threads along the axis whose stride is 1
+  // Element i of this thread: consecutive threads along the axis whose stride is 1. Its place and address are formed once; a
+  // step moves all of them by BK along k.
   const bool a_k = p.ak == 1, b_k = p.bk == 1;
+  const int ka0 = a_k ? threadIdx.x % BK : threadIdx.x / B, kb0 = b_k ? threadIdx.x % BK : threadIdx.x / B;
+  constexpr int RK = THREADS / BK, RM = THREADS / B > 0 ? THREADS / B : 1;   // rows (along k) or k (along rows) between elements
+  static_assert(THREADS % B == 0, "a thread keeps its row where threads run along rows");
+  const float *pa = p.A + (int64_t)(s0 * BK + ka0) * p.ak, *pb = p.B + (int64_t)(s0 * BK + kb0) * p.bk;
+  uint32_t a_rows = 0, b_rows = 0;   // which rows exist
+  int64_t a_off[PER], b_off[PER];
+  uint32_t a_dst[PER], b_dst[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int ra = a_k ? threadIdx.x / BK + i * RK : threadIdx.x % B, rb = b_k ? threadIdx.x / BK + i * RK : threadIdx.x % B;
+    int64_t row = n0 + rb;
+    bool ok = row < p.N;
+    if (KIND == GATEUP && rb >= HALF) {
+      ok = n0 + rb - HALF < p.N;
+      row = (int64_t)p.N + n0 + rb - HALF;
+    }
+    if (m0 + ra < p.M) a_rows |= 1u << i;
+    if (ok) b_rows |= 1u << i;
+    a_off[i] = (int64_t)(m0 + ra) * p.am + (a_k ? 0 : i * RM * p.ak);
+    b_off[i] = row * p.bn + (b_k ? 0 : i * RM * p.bk);
+    a_dst[i] = (uint32_t)((a_k ? ka0 : ka0 + i * RM) * LD + ra) * 4;
+    b_dst[i] = (uint32_t)((b_k ? kb0 : kb0 + i * RM) * LD + rb) * 4 + BK * LD * 4;
+  }
+  int left = p.K - s0 * BK;          // of K from the next step to fetch on
   auto fetch = [&](int s) {
     if (s < s1) {
-      const uint32_t as = base + (uint32_t)(s % STAGES) * (stage_floats<B>() * 4), bs = as + BK * LD * 4;
-      const int k0 = s * BK;
+      const uint32_t at = base + (uint32_t)(s % STAGES) * (stage_floats<B>() * 4);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int e = i * THREADS + threadIdx.x;
-        {
-          const int k = a_k ? e % BK : e / B, r = a_k ? e / BK : e % B;
-          const bool ok = m0 + r < p.M && k0 + k < p.K;
-          copy4(as + (uint32_t)(k * LD + r) * 4, ok ? p.A + (m0 + r) * p.am + (k0 + k) * p.ak : p.A, ok);
-        }
-        {
-          const int k = b_k ? e % BK : e / B, r = b_k ? e / BK : e % B;
-          int64_t row = n0 + r;
-          bool ok = row < p.N;
-          if (KIND == GATEUP && r >= HALF) {
-            ok = n0 + r - HALF < p.N;
-            row = (int64_t)p.N + n0 + r - HALF;
-          }
-          ok = ok && k0 + k < p.K;
-          copy4(bs + (uint32_t)(k * LD + r) * 4, ok ? p.B + row * p.bn + (k0 + k) * p.bk : p.B, ok);
-        }
+        const bool ok = (a_rows >> i & 1) && (a_k ? ka0 : ka0 + i * RM) < left;
+        copy4(at + a_dst[i], ok ? pa + a_off[i] : p.A, ok);
+        const bool okb = (b_rows >> i & 1) && (b_k ? kb0 : kb0 + i * RM) < left;
+        copy4(at + b_dst[i], okb ? pb + b_off[i] : p.B, okb);
       }
+      pa += BK * p.ak;
+      pb += BK * p.bk;
+      left -= BK;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -172,7 +191,13 @@ template <int KIND, int B> __global__ void __launch_bounds__(Tile<B>::THREADS) f
 
 template <int KIND, int B> static int launch_tile(const Args &a, int64_t cols, int64_t rows, int splits, cudaStream_t s) {
   if (rows > 65535 || cols * splits > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  MOE_TRY_CUDA(cudaFuncSetAttribute(ffn_f32_kernel<KIND, B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<B>()));
+  static std::atomic<uint64_t> raised{0};   // once per device: the limit is the process's
+  int dev = 0;
+  MOE_TRY_CUDA(cudaGetDevice(&dev));
+  if (dev >= 64 || !(raised.load(std::memory_order_relaxed) >> dev & 1)) {
+    MOE_TRY_CUDA(cudaFuncSetAttribute(ffn_f32_kernel<KIND, B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<B>()));
+    if (dev < 64) raised.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  }
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = (unsigned)splits;
@@ -188,15 +213,23 @@ template <int KIND, int B> static int launch_tile(const Args &a, int64_t cols, i
   return MOE_OK;
 }
 
-// Tiles of 128 where they fill the GPU twice over, else of 64; K cut until there are about two blocks of 64 per SM, each with at least
-// four steps.
+// Tiles of 128 where they fill the GPU twice over, else of 64, with K cut into the number of parts (powers of two) that gives the
+// shortest work per SM: the most blocks that one gets, times a part's steps and about four more for its start and end. Blocks
+// that have an SM to themselves (four warps) take about twice as long per step as those that share it.
 template <int KIND> static int launch(const Args &a, cudaStream_t s) {
   auto up = [](int64_t n, int64_t k) { return (n + k - 1) / k; };
   const int64_t sms = sm_count(), wide = KIND == GATEUP ? 2 : 1;
   if (up(a.M, 128) * up(wide * a.N, 128) >= 2 * sms) return launch_tile<KIND, 128>(a, up(wide * a.N, 128), up(a.M, 128), 1, s);
-  const int64_t cols = up(wide * a.N, 64), rows = up(a.M, 64);
+  const int64_t cols = up(wide * a.N, 64), rows = up(a.M, 64), steps = up(a.K, BK);
   int splits = 1;
-  while (splits < MAX_SPLIT && rows * cols * splits * 2 <= 3 * sms && a.K >= 2 * splits * 4 * BK) splits *= 2;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= MAX_SPLIT && n <= steps; n *= 2) {
+    const int64_t per_sm = up(rows * cols * n, sms), cost = (per_sm < 2 ? 2 : per_sm) * (up(steps, n) + 4);
+    if (cost < least) {
+      least = cost;
+      splits = n;
+    }
+  }
   return launch_tile<KIND, 64>(a, cols, rows, splits, s);
 }
 

@@ -41,6 +41,9 @@ class GatedFFN:
         act_ = dict(dtype=dtype, device=self.device)
         u8 = dict(dtype=torch.uint8, device=self.device)
         code = L.dtype_code(dtype)
+        for name, shape in (("h", (T, f)), ("dab", (T, 2 * f))):
+            if name in scratch:
+                L._want(f"scratch[{name!r}]", scratch[name], dtype, shape)
         self.h = scratch["h"] if "h" in scratch else torch.empty((T, f), **act_)
         self.y = torch.empty((T, d), **act_)
         self.ws = torch.zeros(L.moe_ffn_workspace_size(T, d, f, code, backward), **u8)
@@ -56,13 +59,23 @@ class GatedFFN:
             self.dx = torch.empty((T, d), **act_)
             self.dw_gate_up = torch.empty((2 * f, d), **act_)
             self.dw_down = torch.empty((d, f), **act_)
+        self._index = self.y.device.index
+        with torch.cuda.device(self._index):
+            self._kept = L.kept(self.ab, self.ab_scales, dtype, T, f)
+        self._h_ptr, self._y_ptr, self._ws_ptr, self._ws_bytes = (self.h.data_ptr(), self.y.data_ptr(), self.ws.data_ptr(),
+                                                                  self.ws.numel())
+
+    def _check_device(self):
+        if L._device() != self._index:
+            raise ValueError(f"the buffers are on cuda:{self._index}, the current device is cuda:{L._device()}")
 
     def forward(self, x, w_gate_up, w_down, add=None, out=None, stream=None):
         """y [T, d] = add + FFN(x), into `out` (which may be add) where it is given."""
-        L._want("x", x, self.dtype, (self.T, self.d))
-        y = self.y if out is None else out
-        L.moe_ffn_fwd(x, w_gate_up, w_down, add, self.ab, self.ab_scales, self.h, y, self.ws, self._act, stream)
-        return y
+        self._check_device()
+        y = self._y_ptr if out is None else L._at("out", out, self.dtype, (self.T, self.d), L._device())
+        L.ffn_fwd_into(x, w_gate_up, w_down, add, self.T, self.d, self.f, self.dtype, self._act, self._kept, self._h_ptr, y,
+                       self._ws_ptr, self._ws_bytes, stream)
+        return self.y if out is None else out
 
     def backward(self, dy, x, w_gate_up, w_down, add=None, stream=None):
         """Gradients from what the last forward kept and its x: dx = add + the block's, dw_gate_up, dw_down."""

@@ -44,6 +44,8 @@ class LayerNorm:
             self.dw = torch.empty(d, **act)
             self.db = torch.empty(d, **act) if bias else None
             self.ws = torch.empty(L.moe_layer_norm_bwd_workspace_size(T, d, code), dtype=torch.uint8, device=self.device)
+        self._index = self.n.device.index
+        self._out = [None if t is None else t.data_ptr() for t in (self.n, self.mean, self.rstd, self.codes, self.scales)]
 
     def _check(self, b):
         if (b is not None) != self.bias:
@@ -52,8 +54,9 @@ class LayerNorm:
     def forward(self, x, w, b=None, stream=None):
         """n [T, d]."""
         self._check(b)
-        L._want("x", x, self.dtype, (self.T, self.d))
-        L.moe_layer_norm_fwd(x, w, b, self.n, self.mean, self.rstd, self.codes, self.scales, self.eps, stream)
+        if L._device() != self._index:
+            raise ValueError(f"the buffers are on cuda:{self._index}, the current device is cuda:{L._device()}")
+        L.layer_norm_fwd_into(x, w, b, self.T, self.d, self.dtype, *self._out, self.eps, stream)
         return self.n
 
     def restore(self, w, b=None, out=None, stream=None):

@@ -108,3 +108,16 @@ def test_class_refusals():
     ffn.backward_enabled = False
     with pytest.raises(RuntimeError, match="backward"):
         ffn.backward(None, None, None, None)
+
+
+def test_another_current_gpu(monkeypatch):
+    from mixture_experts_layer_histogram_gb300 import GatedFFN, LayerNorm
+    from mixture_experts_layer_histogram_gb300 import _lib
+    monkeypatch.setattr(_lib, "_device", lambda: 1)
+    ffn, norm = GatedFFN.__new__(GatedFFN), LayerNorm.__new__(LayerNorm)
+    ffn._index = norm._index = 0
+    norm.bias = False
+    with pytest.raises(ValueError, match="cuda:0"):
+        ffn.forward(None, None, None)
+    with pytest.raises(ValueError, match="cuda:0"):
+        norm.forward(None, None)
