@@ -13,7 +13,13 @@
 // written once; codes come through the ring as well, 8 (fp32: 4) bytes per thread beside its 16-byte vectors. Where the forward
 // needs two reductions per row (the deviations wait for the mean), the blocks that share an SM cover for one another.
 // The weight gradients are summed over a block's rows in registers and its partial rows added up in a fixed order.
+// Measured (bf16): backward with dx_in at T = 16384, d = 4096 96.5 us (537 MB, 5.6 TB/s); at T = 8192, d = 2048 forward with codes
+// 22.5 us (84 MB), restore 11.4 us (51 MB), backward from codes 25 us (118 MB) and 4.8 us for the partial rows; fp32 T = 1023,
+// d = 1537 backward 9.7 and 4.8 us; four rows of 2048 3.5 us. Before dn and z stayed in registers between the backward's
+// two passes it took 100.5 us. The forward takes the same time with two vectors per thread and with a warp per row (fewer
+// instructions, no barriers): 84 MB are too few to fill and drain the memory system for.
 #include "act8.cuh"
+#include "raw16.cuh"
 #include "row_ring.cuh"
 
 namespace moe {
@@ -116,6 +122,39 @@ struct LnFwdParams {
   float eps;
 };
 
+// rstd of a row from its mean m, what the rounding of m left, and the sum of the squared deviations from m; `write`: this thread
+// writes the row's statistics.
+__device__ __forceinline__ void statistics(const LnFwdParams &p, int64_t row, float m, float rest, float squares, float inv_d,
+                                           bool write, float &r) {
+  const float var = fmaf(-rest, rest, squares * inv_d);
+  // squares past fp32's range: as if the variance were infinite
+  r = squares == __uint_as_float(0x7f800000u) ? 0.0f : rsqrtf(fmaxf(var, 0.0f) + p.eps);
+  if (var != var && squares != __uint_as_float(0x7f800000u)) r = var;   // (fmaxf drops a NaN)
+  if (write) {
+    if (p.mean) p.mean[row] = m + rest;
+    if (p.rstd) p.rstd[row] = r;
+  }
+}
+// Vector v of a row's normalised values to its codes (and, from the first thread of a block of 32 values, the scale)
+template <int VEC, typename L, int N>
+__device__ __forceinline__ void keep(const LnFwdParams &p, int64_t row, int v, bool has, const L (&z)[N]) {
+  uint32_t top = 0;
+  if (has) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) top = max(top, magnitude(z[c]));
+  }
+  const uint32_t byte = act8::scale_byte(block_amax<VEC>(top));
+  if (!has) return;
+  uint8_t *q = p.codes + row * p.d + (int64_t)v * VEC;
+  if (byte == 255u) {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) q[c] = 0;
+  } else {
+    put_codes(q, z, act8::inv_scale(byte));
+  }
+  if (v * VEC % act8::kBlock == 0) p.scales[row * p.nb + v * VEC / act8::kBlock] = (uint8_t)byte;
+}
+
 template <typename T, int VEC, int ITER, bool KEEP>
 __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(const LnFwdParams p, const Geometry geom) {
   using V = Lanes<T, VEC, float>;
@@ -183,14 +222,9 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
     float t[2] = {total(s1), total(s2)};
     block_sums(t, sums, half);
     const float rest = t[0] * inv_d;                    // what the rounding of m left
-    const float var = fmaf(-rest, rest, t[1] * inv_d);
-    // squares past fp32's range: as if the variance were infinite
-    const float r = t[1] == __uint_as_float(0x7f800000u) ? 0.0f : rsqrtf(fmaxf(var, 0.0f) + p.eps);
-    if (threadIdx.x == 0) {
-      if (p.mean) p.mean[row] = m + rest;
-      if (p.rstd) p.rstd[row] = var != var ? var : r;   // (fmaxf drops a NaN)
-    }
-    const L R = splat<L>(var != var ? var : r), shift = splat<L>(-rest);
+    float r;
+    statistics(p, row, m, rest, t[1], inv_d, threadIdx.x == 0, r);
+    const L R = splat<L>(r), shift = splat<L>(-rest);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
@@ -198,24 +232,7 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
 #pragma unroll
         for (int c = 0; c < N; ++c) o[i][c] = mul(add(o[i][c], shift), R);
       }
-      if (KEEP) {
-        uint32_t top = 0;
-        if (ring.has(i)) {
-#pragma unroll
-          for (int c = 0; c < N; ++c) top = max(top, magnitude(o[i][c]));
-        }
-        const uint32_t byte = act8::scale_byte(block_amax<VEC>(top));
-        if (ring.has(i)) {
-          uint8_t *q = p.codes + row * p.d + (int64_t)v * VEC;
-          if (byte == 255u) {
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) q[c] = 0;
-          } else {
-            put_codes(q, o[i], act8::inv_scale(byte));
-          }
-          if (v * VEC % act8::kBlock == 0) p.scales[row * p.nb + v * VEC / act8::kBlock] = (uint8_t)byte;
-        }
-      }
+      if (KEEP) keep<VEC>(p, row, v, ring.has(i), o[i]);
       if (!ring.has(i)) continue;
       L(&w)[N] = hold_w[kHold ? i : 0], (&b)[N] = hold_b[kHold ? i : 0];
       if (!kHold) weights(v, w, b);
@@ -350,7 +367,8 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
         for (int c = 0; c < N; ++c) z[c] = mul(add(z[c], all(-m, L())), all(r, L()));
       }
     };
-    // sums of u, u z, z
+    // sums of u, u z, z; with few vectors per thread dn and z stay in registers for the second pass
+    L hold_d[kHold ? ITER : 1][N], hold_z[kHold ? ITER : 1][N];
     L t[3];
 #pragma unroll
     for (int i = 0; i < 3; ++i) t[i] = splat<L>(0.0f);
@@ -359,15 +377,15 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
       if (!ring.has(i)) continue;
       L(&w)[N] = hold_w[kHold ? i : 0];
       if (!kHold) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, w);
-      L u[N], z[N];
+      L(&u)[N] = hold_d[kHold ? i : 0], (&z)[N] = hold_z[kHold ? i : 0];
       V::load_shared(here + kDn * ring.row_bytes + i * ring.step, u);
       normed(i, z);
 #pragma unroll
       for (int c = 0; c < N; ++c) {
         acc_b[i][c] = add(acc_b[i][c], u[c]);
-        u[c] = mul(u[c], w[c]);
-        t[0] = add(t[0], u[c]);
-        t[1] = fma(u[c], z[c], t[1]);
+        const L uw = mul(u[c], w[c]);
+        t[0] = add(t[0], uw);
+        t[1] = fma(uw, z[c], t[1]);
         if (!KEPT) t[2] = add(t[2], z[c]);
       }
     }
@@ -383,9 +401,12 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
       if (!ring.has(i)) continue;
       L(&w)[N] = hold_w[kHold ? i : 0];
       if (!kHold) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, w);
-      L u[N], z[N], g[N];
-      V::load_shared(here + kDn * ring.row_bytes + i * ring.step, u);
-      normed(i, z);
+      L(&u)[N] = hold_d[kHold ? i : 0], (&z)[N] = hold_z[kHold ? i : 0];
+      L g[N];
+      if (!kHold) {
+        V::load_shared(here + kDn * ring.row_bytes + i * ring.step, u);
+        normed(i, z);
+      }
       if (has_in) {
         V::load_shared(here + kIn * ring.row_bytes + i * ring.step, g);
       } else {
@@ -414,6 +435,52 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
 
 // n = z w + b of kept rows. A thread keeps its columns (VEC of them) and takes every `step`-th row.
 constexpr int kRestoreThreads = 256;
+// 16 values of bf16 rows of whole blocks: 16-byte loads, 32-byte stores
+__global__ void __launch_bounds__(kRestoreThreads) ln_restore16_kernel(const uint4 *__restrict__ codes,
+                                                                       const uint8_t *__restrict__ scales,
+                                                                       const __nv_bfloat16 *__restrict__ w,
+                                                                       const __nv_bfloat16 *__restrict__ b, int64_t T_, int d,
+                                                                       int64_t step, bool wide, __nv_bfloat16 *__restrict__ n) {
+  const int cols = d / 16;
+  const int64_t id = (int64_t)blockIdx.x * kRestoreThreads + threadIdx.x;
+  const int64_t row0 = id / cols;
+  const int col = (int)(id - row0 * cols);
+  if (row0 >= step) return;
+  Raw16<__nv_bfloat16> raw;
+  float W[16], B[16] = {};
+  raw.load(w + col * 16);
+  raw.unpack(W);
+  if (b) {
+    raw.load(b + col * 16);
+    raw.unpack(B);
+  }
+  constexpr int kRows = 4;   // in flight
+  for (int64_t r0 = row0; r0 < T_; r0 += kRows * step) {
+    uint4 q[kRows];
+    uint32_t sc[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t at = (r0 + k * step) * cols + col;
+      if (r0 + k * step >= T_) continue;
+      q[k] = __ldg(codes + at);
+      sc[k] = __ldg(scales + (at >> 1));
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (r0 + k * step >= T_) continue;
+      const float scale = act8::scale_value(sc[k]);
+      float v[16];
+      act8::unpack4(q[k].x, v);
+      act8::unpack4(q[k].y, v + 4);
+      act8::unpack4(q[k].z, v + 8);
+      act8::unpack4(q[k].w, v + 12);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i] * scale, W[i], B[i]);
+      Raw16<__nv_bfloat16>::store(n + (r0 + k * step) * d + col * 16, v, wide);
+    }
+  }
+}
+
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kRestoreThreads) ln_restore_kernel(const uint8_t *__restrict__ codes,
                                                                      const uint8_t *__restrict__ scales,
@@ -574,6 +641,17 @@ extern "C" int moe_layer_norm_restore(const void *codes, const void *scales, con
   if (T == 0) return MOE_OK;
   if (bad(codes) || bad(scales) || bad(w) || !aligned16(b) || bad(n)) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == MOE_BF16 && d % act8::kBlock == 0) {
+    const int cols = d / 16;
+    int64_t step = ((int64_t)sm_count() * 8 * kRestoreThreads + cols - 1) / cols;   // eight blocks per SM, about
+    if (step > T) step = T;
+    const unsigned grid = (unsigned)((step * cols + kRestoreThreads - 1) / kRestoreThreads);
+    ln_restore16_kernel<<<grid, kRestoreThreads, 0, s>>>((const uint4 *)codes, (const uint8_t *)scales, (const __nv_bfloat16 *)w,
+                                                        (const __nv_bfloat16 *)b, T, d, step, ((uintptr_t)n & 31) == 0,
+                                                        (__nv_bfloat16 *)n);
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+  }
   if (dtype == MOE_BF16)
     return d % 8 == 0 ? ln_launch_restore<__nv_bfloat16, 8>(codes, scales, w, b, T, d, n, s)
                       : ln_launch_restore<__nv_bfloat16, 1>(codes, scales, w, b, T, d, n, s);
