@@ -99,7 +99,7 @@ struct Params {
   bool more;                 // another kernel of the same call follows
   // One product with its tiles cut along K (else splits = 1): parts of a tile, and parts in all
   int splits, units;
-  float4 *part;              // [tile][part][slice][4][8][32] float4
+  float4 *part;              // [tile][part][slice][32][32] float4
   int *arrived;              // [tile][slice][2]: parts claimed, parts written
   // Rows of tiles that the launch's first product has written: warps arrived per row, and what makes a row complete
   int *ready, *left;         // left: pairs that are done (the last one sets ready back to zero)
@@ -274,14 +274,10 @@ template <int W> struct Chunk {
 __device__ __forceinline__ void st_shared_v4(uint32_t a, const uint4 &q) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
 }
-// This lane's row of 32 columns (from chunk c0 on) into the buffer
-template <int W> __device__ __forceinline__ void stage(uint32_t buf, int lane, int c0, const float *v) {
+// N chunks of 8 columns of this lane's row (from chunk c0 on) into the buffer
+template <int W, int N> __device__ __forceinline__ void stage(uint32_t buf, int lane, int c0, const float *v) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) st_shared_v4(Chunk<W>::at(buf, lane, c0 + c), pack_bf16x8(v + 8 * c));
-}
-template <int W> __device__ __forceinline__ void stage(uint32_t buf, int lane, int c0, const uint4 (&q)[4]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) st_shared_v4(Chunk<W>::at(buf, lane, c0 + c), q[c]);
+  for (int c = 0; c < N; ++c) st_shared_v4(Chunk<W>::at(buf, lane, c0 + c), pack_bf16x8(v + 8 * c));
 }
 // The buffer's block to rows row0.. and columns col.. of a row-major output
 template <int W>
@@ -319,10 +315,10 @@ __device__ __forceinline__ void fetch(uint32_t buf, const __nv_bfloat16 *in, int
     copy16(C::at(buf, r, c), there ? src + (int64_t)(C::STEP * i) * ld : in, there);
   }
 }
-// This lane's row of the buffer: 32 columns from chunk c0 on
-template <int W, bool ADD> __device__ __forceinline__ void take(uint32_t buf, int lane, int c0, float *v) {
+// This lane's row of the buffer: N chunks of 8 columns from chunk c0 on
+template <int W, int N, bool ADD> __device__ __forceinline__ void take(uint32_t buf, int lane, int c0, float *v) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < N; ++c) {
     float w[8];
     unpack_bf16x8(ld_shared_v4(Chunk<W>::at(buf, lane, c0 + c)), w);
 #pragma unroll
@@ -339,17 +335,13 @@ __device__ __forceinline__ void fetch_codes(uint32_t buf, const uint8_t *in, int
     copy16(code_at(buf, r, lane & 1), there ? in + (int64_t)(row0 + r) * ld + col + 16 * (lane & 1) : in, there);
   }
 }
-__device__ __forceinline__ void take_codes(uint32_t buf, int lane, float scale, float *v) {
+__device__ __forceinline__ void unpack_codes(const uint4 &w, float scale, float *v) {   // 16 of them
+  act8::unpack4(w.x, v);
+  act8::unpack4(w.y, v + 4);
+  act8::unpack4(w.z, v + 8);
+  act8::unpack4(w.w, v + 12);
 #pragma unroll
-  for (uint32_t i = 0; i < 2; ++i) {
-    const uint4 w = ld_shared_v4(code_at(buf, lane, i));
-    act8::unpack4(w.x, v + 16 * i);
-    act8::unpack4(w.y, v + 16 * i + 4);
-    act8::unpack4(w.z, v + 16 * i + 8);
-    act8::unpack4(w.w, v + 16 * i + 12);
-  }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] *= scale;
+  for (int i = 0; i < 16; ++i) v[i] *= scale;
 }
 
 // 32 values, one whole block, to their codes and scale
@@ -369,63 +361,53 @@ __device__ __forceinline__ void put_block8(uint8_t *codes, uint8_t *scale, const
   reinterpret_cast<uint4 *>(codes)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   *scale = (uint8_t)byte;
 }
-// The warp's 32 x 128 outputs of a tile as accumulated: what TMEM holds, and for a cut tile (`splits` > 1) the sum of that and
-// the other parts in the workspace, always in the parts' order. Block j holds columns 32 j .. of the slice.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// The warp's 32 x 128 outputs of a tile as accumulated (GATEUP: a of 64 features, then b of the same): what TMEM holds, and for a
+// cut tile (`splits` > 1) the sum of that and the other parts in the workspace, always in the parts' order.
 template <int K> struct Slice {
   static constexpr int64_t kNext = (int64_t)SLICES * SLICE_FLOATS / 4;   // from one part to the next
-  static constexpr bool kAsk = K == GATEUP;   // the first other part of the next block is asked for ahead (registers allowing)
-  uint32_t tmem;             // TMEM address of the first block
+  uint32_t tmem;             // TMEM address of the first column
   const float4 *part;        // part 0
   int splits, mine;
-  float4 q[kAsk ? 8 : 1];
-  static __device__ __forceinline__ int after(int j) {   // the order in which finish() takes the blocks
-    return K == GATEUP ? (j == 0 ? 2 : (j == 2 ? 1 : 3)) : j + 1;
-  }
-  __device__ __forceinline__ void get(float4 (&to)[8], int j, int p, int lane) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) to[i] = __ldcg(part + p * kNext + (j * 8 + i) * 32 + lane);
-  }
-  __device__ __forceinline__ void ask(int j, int lane) {
-    if constexpr (kAsk) {
-      if (splits > 1) get(q, j, mine == 0 ? 1 : 0, lane);
-    }
-  }
-  __device__ __forceinline__ void held(int j, float *v, bool add) const {
-    uint32_t r[32];
-    tmem_ld32(tmem + (uint32_t)(K == GATEUP ? (j >> 1) * HALF + 32 * (j & 1) : 32 * j), r);
+  // 16 columns from column c on
+  __device__ __forceinline__ void held(int c, float *v, bool add) const {
+    uint32_t r[16];
+    tmem_ld16(tmem + (uint32_t)(K == GATEUP && c >= 64 ? HALF - 64 + c : c), r);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = add ? v[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
+    for (int i = 0; i < 16; ++i) v[i] = add ? v[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
   }
-  __device__ __forceinline__ void load(int j, int lane, float *v) {
+  __device__ __forceinline__ void load(int c, int lane, float *v) const {
     if (splits == 1) {
-      held(j, v, false);
+      held(c, v, false);
       return;
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
 #pragma unroll 1
     for (int p = 0; p < splits; ++p) {
       if (p == mine) {
-        held(j, v, true);
+        held(c, v, true);
         continue;
       }
-      float4 w[8];
-      if (kAsk && p == (mine == 0 ? 1 : 0)) {
+      float4 w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = q[kAsk ? i : 0];
-      } else {
-        get(w, j, p, lane);
-      }
+      for (int i = 0; i < 4; ++i) w[i] = __ldcg(part + p * kNext + (c / 4 + i) * 32 + lane);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         v[4 * i] += w[i].x;
         v[4 * i + 1] += w[i].y;
         v[4 * i + 2] += w[i].z;
         v[4 * i + 3] += w[i].w;
       }
     }
-    if (j != 3) ask(after(j), lane);
   }
 };
 
@@ -472,15 +454,15 @@ template <int K> struct Ahead {
 };
 
 // a becomes act(a) b
-template <bool CUBIC> __device__ __forceinline__ void gate32(float *a, const float *b, const Gate &g) {
+template <bool CUBIC> __device__ __forceinline__ void gate16(float *a, const float *b, const Gate &g) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 2)
+  for (int i = 0; i < 16; i += 2)
     split(mul(ffn::gated2<CUBIC>(pair(a[i], a[i + 1]), g), pair(b[i], b[i + 1])), a[i], a[i + 1]);
 }
 // a becomes da = v b act'(a), v (dh) becomes db = v act(a), b becomes h = act(a) b
-template <bool CUBIC> __device__ __forceinline__ void back32(float *a, float *b, float *v, const Gate &g) {
+template <bool CUBIC> __device__ __forceinline__ void back16(float *a, float *b, float *v, const Gate &g) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
+  for (int i = 0; i < 16; i += 2) {
     F2 act, slope;
     ffn::gate_and_slope2<CUBIC>(pair(a[i], a[i + 1]), g, act, slope);
     const F2 B = pair(b[i], b[i + 1]), V = pair(v[i], v[i + 1]);
@@ -490,43 +472,68 @@ template <bool CUBIC> __device__ __forceinline__ void back32(float *a, float *b,
   }
 }
 
-// What becomes of the warp's slice: rows row0 .. row0 + 31 (a lane each), columns from col0 on (GATEUP: 64 features from
-// col0 on, a in blocks 0 and 1, b in blocks 2 and 3).
+// What becomes of the warp's slice: rows row0 .. row0 + 31 (a lane each), 128 columns from col0 on (GATEUP: 64 features). Sixteen
+// columns at a time in loops that stay loops: unrolled, most of the time of a first (or only) tile went into fetching the code.
 template <int K>
-__device__ __forceinline__ void finish(Slice<K> &acc, Ahead<K> &ahead, const Params &p, const Product &o, uint32_t buf, int lane, int row0, int col0) {
+__device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, const Params &p, const Product &o, uint32_t buf, int lane,
+                                       int row0, int col0) {
   if (K == GATEUP) {
-    if (col0 >= o.N) return;
     const int row = row0 + lane;
     const int64_t ld = 2 * (int64_t)o.N;
-    uint4 qh[2][4];
+    if (p.codes) {
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j) {
+        const int col = col0 + 32 * j;
+        if (col >= o.N) break;
+        float a[32], b[32];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int col = col0 + 32 * j;
-      float a[32], b[32];
-      acc.load(j, lane, a);
-      acc.load(2 + j, lane, b);
-      if (p.codes) {
-        if (row < o.M && col < o.N) {
+        for (int h = 0; h < 2; ++h) {
+          acc.load(32 * j + 16 * h, lane, a + 16 * h);
+          acc.load(64 + 32 * j + 16 * h, lane, b + 16 * h);
+        }
+        if (row < o.M) {
           uint8_t *c = p.codes + row * ld + col, *s = p.scales + (row * ld + col) / act8::kBlock;
           put_block8(c, s, a);
           put_block8(c + o.N, s + o.N / act8::kBlock, b);
         }
-      } else if (o.out0) {
-        stage<64>(buf, lane, 4 * j, a);
-        stage<64>(buf + BUF, lane, 4 * j, b);
-      }
-      if (p.gate.k1 == 0.0f) gate32<false>(a, b, p.gate);
-      else gate32<true>(a, b, p.gate);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) qh[j][c] = pack_bf16x8(a + 8 * c);
+        for (int h = 0; h < 2; ++h) {
+          if (p.gate.k1 == 0.0f) gate16<false>(a + 16 * h, b + 16 * h, p.gate);
+          else gate16<true>(a + 16 * h, b + 16 * h, p.gate);
+        }
+        stage<64, 4>(buf, lane, 4 * j, a);
+      }
+      if (col0 < o.N) put<64>(buf, lane, o.out1, o.N, row0, o.M, col0, o.N);
+      return;
     }
-    if (o.out0) {
-      put<64>(buf, lane, o.out0, ld, row0, o.M, col0, o.N);
-      put<64>(buf + BUF, lane, o.out0 + o.N, ld, row0, o.M, col0, o.N);
+    if (col0 >= o.N) return;
+    // a and b leave through the two halves of the buffers (32 features each), h through the place of a
+#pragma unroll 1
+    for (int j = 0; j < 2; ++j) {
+      const int col = col0 + 32 * j;
+      uint4 qh[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float a[16], b[16];
+        acc.load(32 * j + 16 * h, lane, a);
+        acc.load(64 + 32 * j + 16 * h, lane, b);
+        if (o.out0) {
+          stage<32, 2>(buf, lane, 2 * h, a);
+          stage<32, 2>(buf + 2048, lane, 2 * h, b);
+        }
+        if (p.gate.k1 == 0.0f) gate16<false>(a, b, p.gate);
+        else gate16<true>(a, b, p.gate);
+        qh[2 * h] = pack_bf16x8(a);
+        qh[2 * h + 1] = pack_bf16x8(a + 8);
+      }
+      if (o.out0) {
+        put<32>(buf, lane, o.out0, ld, row0, o.M, col, o.N);
+        put<32>(buf + 2048, lane, o.out0 + o.N, ld, row0, o.M, col, o.N);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) st_shared_v4(Chunk<64>::at(buf + BUF, lane, 4 * j + c), qh[c]);
     }
-    stage<64>(buf, lane, 0, qh[0]);
-    stage<64>(buf, lane, 4, qh[1]);
-    put<64>(buf, lane, o.out1, o.N, row0, o.M, col0, o.N);
+    put<64>(buf + BUF, lane, o.out1, o.N, row0, o.M, col0, o.N);
   } else if (K == DH) {
 #pragma unroll 1
     for (int j = 0; j < 4; ++j) {
@@ -535,24 +542,38 @@ __device__ __forceinline__ void finish(Slice<K> &acc, Ahead<K> &ahead, const Par
       const int64_t ld = 2 * (int64_t)o.N;
       landed<1>();                    // the next block may be on its way
       if (col < o.N) {
-        float a[32], b[32], v[32];
-        if (p.codes) {
-          take_codes(here, lane, act8::scale_value((ahead.sa >> (8 * j)) & 255u), a);
-          take_codes(here + 1024, lane, act8::scale_value((ahead.sb >> (8 * j)) & 255u), b);
-        } else {
-          take<32, false>(here, lane, 0, a);
-          take<32, false>(here + 2048, lane, 0, b);
+        uint4 ca[2], cb[2], qh[4];
+        if (p.codes) {   // before the buffer takes what is made of them
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ca[h] = ld_shared_v4(code_at(here, lane, h));
+            cb[h] = ld_shared_v4(code_at(here + 1024, lane, h));
+          }
+          __syncwarp();
         }
-        acc.load(j, lane, v);
-        if (p.gate.k1 == 0.0f) back32<false>(a, b, v, p.gate);
-        else back32<true>(a, b, v, p.gate);
-        __syncwarp();
-        stage<32>(here, lane, 0, a);
-        stage<32>(here + 2048, lane, 0, v);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float a[16], b[16], v[16];
+          acc.load(32 * j + 16 * h, lane, v);
+          if (p.codes) {
+            unpack_codes(ca[h], act8::scale_value((ahead.sa >> (8 * j)) & 255u), a);
+            unpack_codes(cb[h], act8::scale_value((ahead.sb >> (8 * j)) & 255u), b);
+          } else {       // a lane's row of the buffer is its own: read, then overwritten
+            take<32, 2, false>(here, lane, 2 * h, a);
+            take<32, 2, false>(here + 2048, lane, 2 * h, b);
+          }
+          if (p.gate.k1 == 0.0f) back16<false>(a, b, v, p.gate);
+          else back16<true>(a, b, v, p.gate);
+          stage<32, 2>(here, lane, 2 * h, a);
+          stage<32, 2>(here + 2048, lane, 2 * h, v);
+          qh[2 * h] = pack_bf16x8(b);
+          qh[2 * h + 1] = pack_bf16x8(b + 8);
+        }
         put<32>(here, lane, o.out0, ld, row0, o.M, col, o.N);
         put<32>(here + 2048, lane, o.out0 + o.N, ld, row0, o.M, col, o.N);
         if (p.codes) {
-          stage<32>(here, lane, 0, b);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) st_shared_v4(Chunk<32>::at(here, lane, c), qh[c]);
           put<32>(here, lane, o.out1, o.N, row0, o.M, col, o.N);
         }
       }
@@ -560,22 +581,25 @@ __device__ __forceinline__ void finish(Slice<K> &acc, Ahead<K> &ahead, const Par
       else commit();                  // one group per block, for the count
     }
   } else {
-#pragma unroll
+    const bool add = o.in0 != nullptr;
+#pragma unroll 1
     for (int j = 0; j < 2; ++j) {
       const int col = col0 + 64 * j;
       const uint32_t here = buf + j * BUF;
-      const bool add = o.in0 != nullptr;
       if (add) {
         if (j == 0) landed<1>();
         else landed<0>();
       }
       if (col >= o.N) continue;
+#pragma unroll 1
+      for (int h = 0; h < 4; h += 2) {   // a lane's row of the buffer is its own: read, then overwritten
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {   // a lane's row of the buffer is its own: read, then overwritten
-        float v[32];
-        acc.load(2 * j + h, lane, v);
-        if (add) take<64, true>(here, lane, 4 * h, v);
-        stage<64>(here, lane, 4 * h, v);
+        for (int g = 0; g < 2; ++g) {
+          float v[16];
+          acc.load(64 * j + 16 * (h + g), lane, v);
+          if (add) take<64, 2, true>(here, lane, 2 * (h + g), v);
+          stage<64, 2>(here, lane, 2 * (h + g), v);
+        }
       }
       put<64>(here, lane, o.out0, o.N, row0, o.M, col, o.N);
     }
@@ -773,11 +797,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!here) {
           float4 *out = const_cast<float4 *>(s.part) + t.part * Slice<K>::kNext + lane;
 #pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
-            float v[32];
-            s.held(j, v, false);
+          for (int c = 0; c < 128; c += 16) {
+            float v[16];
+            s.held(c, v, false);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) __stcg(out + (j * 8 + i) * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            for (int i = 0; i < 4; ++i) __stcg(out + (c / 4 + i) * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
           }
           landed<0>();       // what was asked for to finish the slice is not needed: its place is free again
           __threadfence();   // this lane's part is visible before the count
@@ -787,7 +811,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           // the other parts' warps have all claimed before: they are writing, or have written, and wait for nothing
           if (!wait_count(written, p.splits - 1, abort_flag, p.hdr)) return false;
           if (lane == 0) *claimed = *written = 0;
-          s.ask(0, lane);
         }
       }
       if (here) finish<K>(s, ahead, p, o, buf, lane, row0, col0);
