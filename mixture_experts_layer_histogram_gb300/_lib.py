@@ -528,6 +528,8 @@ def _on(name, t, dev):
 
 def _bytes_on(name, t, n, dev):
     """The address of a tensor of at least n bytes on the current GPU."""
+    if t.dtype is _U8 and t.numel() >= n and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     _bytes_at_least(name, t, n)
     return _on(name, t, dev)
 

@@ -17,6 +17,14 @@ static int check(int T, int d, int f, int dtype, int act, int keep) {
   return MOE_OK;
 }
 
+// Few tokens: the path that reads the weights once, whose blocks each read all tokens. With more of those than 32 and large weights
+// that reading costs more than the tiles of the other path: 57 and 60 us for 48 tokens of 4096 x 8192, 193 and 165 for 8192 x
+// 16384; for 64 tokens 39 and 41 us at 2048 x 8192, 76 and 61 at 4096 x 8192.
+static bool few(int T, int d, int f) {
+  const int64_t weights = (int64_t)6 * d * f;
+  return T <= 32 || (T <= 48 && weights <= (int64_t)512 << 20) || (T <= kFewTokens && weights <= (int64_t)128 << 20);
+}
+
 extern "C" size_t moe_ffn_workspace_size(int T, int d, int f, int dtype, int backward) {
   if (check(T, d, f, dtype, MOE_ACT_SILU, MOE_KEEP_NONE)) return 0;
   return kHeader + (dtype == MOE_BF16 ? gemm_workspace(T, d, f, backward != 0) : 0);
@@ -55,7 +63,7 @@ extern "C" int moe_ffn_fwd(const void *x, const void *w_gate_up, const void *w_d
   b.ws = (uint8_t *)ws + kHeader;
   cudaStream_t s = (cudaStream_t)stream;
   if (dtype == MOE_F32) return f32_fwd(b, s);
-  return keep == MOE_KEEP_NONE && T <= kFewTokens ? few_fwd(b, s) : gemm_fwd(b, s);
+  return keep == MOE_KEEP_NONE && few(T, d, f) ? few_fwd(b, s) : gemm_fwd(b, s);
 }
 
 extern "C" int moe_ffn_bwd(const void *dy, const void *x, const void *ab, const void *ab_scales, void *h, const void *w_gate_up,

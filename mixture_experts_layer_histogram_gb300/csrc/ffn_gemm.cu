@@ -20,10 +20,10 @@
 // first product). In separate launches the incomplete last rounds, the set-up of each kernel and its last epilogues cost 45 of
 // 259 us of a step at 8192 x 2048 x 1024.
 //
-// A first product of fewer tiles than pairs whose K is long is cut along K into S parts instead, in a launch of its own. Of the warps
-// that hold the parts of the same 32 x 128 outputs the last one to claim them finishes them: the others leave their fp32
-// accumulators in the workspace, it waits until they are there (those warps wait for nothing, so that ends), adds the parts
-// up in their order, its own from TMEM (so the result does not depend on which came last), and sets the counts back to zero.
+// A first product of fewer tiles than pairs whose K is long is cut along K into S parts instead, in a launch of its own. The warps that
+// hold the parts of the same 32 x 128 outputs leave their fp32 accumulators in the workspace, wait until all are there (every
+// pair is resident, and takes its units in the order of their tiles, so that ends) and finish a share of the outputs each, adding
+// the parts up in their order. (One warp finishing all of them took 22 us for eight parts.)
 //
 // Roles per CTA: warp 0 loads (TMA), warp 1 allocates TMEM and, in the leader, issues the products, warps 2..9 are the epilogue
 // (sixteen warps of 96 registers were slower: 1474 against 1400 us for the three products at 8192 x 4096 x 8192).
@@ -100,7 +100,7 @@ struct Params {
   // One product with its tiles cut along K (else splits = 1): parts of a tile, and parts in all
   int splits, units;
   float4 *part;              // [tile][part][slice][32][32] float4
-  int *arrived;              // [tile][slice][2]: parts claimed, parts written
+  int *arrived;              // [tile][slice][2]: parts written, warps done with them
   // Rows of tiles that the launch's first product has written: warps arrived per row, and what makes a row complete
   int *ready, *left;         // left: pairs that are done (the last one sets ready back to zero)
   int rows, row_need;        // rows: 0 where nobody waits
@@ -369,45 +369,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-// The warp's 32 x 128 outputs of a tile as accumulated (GATEUP: a of 64 features, then b of the same): what TMEM holds, and for a
-// cut tile (`splits` > 1) the sum of that and the other parts in the workspace, always in the parts' order.
+// The warp's 32 x 128 accumulated outputs of a tile (GATEUP: a of 64 features, then b of the same)
 template <int K> struct Slice {
-  static constexpr int64_t kNext = (int64_t)SLICES * SLICE_FLOATS / 4;   // from one part to the next
   uint32_t tmem;             // TMEM address of the first column
-  const float4 *part;        // part 0
-  int splits, mine;
-  // 16 columns from column c on
-  __device__ __forceinline__ void held(int c, float *v, bool add) const {
+  __device__ __forceinline__ void load(int c, float *v) const {   // 16 columns from column c on
     uint32_t r[16];
     tmem_ld16(tmem + (uint32_t)(K == GATEUP && c >= 64 ? HALF - 64 + c : c), r);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = add ? v[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
-  }
-  __device__ __forceinline__ void load(int c, int lane, float *v) const {
-    if (splits == 1) {
-      held(c, v, false);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-#pragma unroll 1
-    for (int p = 0; p < splits; ++p) {
-      if (p == mine) {
-        held(c, v, true);
-        continue;
-      }
-      float4 w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __ldcg(part + p * kNext + (c / 4 + i) * 32 + lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[4 * i] += w[i].x;
-        v[4 * i + 1] += w[i].y;
-        v[4 * i + 2] += w[i].z;
-        v[4 * i + 3] += w[i].w;
-      }
-    }
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
   }
 };
 
@@ -488,8 +458,8 @@ __device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, con
         float a[32], b[32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          acc.load(32 * j + 16 * h, lane, a + 16 * h);
-          acc.load(64 + 32 * j + 16 * h, lane, b + 16 * h);
+          acc.load(32 * j + 16 * h, a + 16 * h);
+          acc.load(64 + 32 * j + 16 * h, b + 16 * h);
         }
         if (row < o.M) {
           uint8_t *c = p.codes + row * ld + col, *s = p.scales + (row * ld + col) / act8::kBlock;
@@ -515,8 +485,8 @@ __device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, con
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float a[16], b[16];
-        acc.load(32 * j + 16 * h, lane, a);
-        acc.load(64 + 32 * j + 16 * h, lane, b);
+        acc.load(32 * j + 16 * h, a);
+        acc.load(64 + 32 * j + 16 * h, b);
         if (o.out0) {
           stage<32, 2>(buf, lane, 2 * h, a);
           stage<32, 2>(buf + 2048, lane, 2 * h, b);
@@ -554,7 +524,7 @@ __device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, con
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float a[16], b[16], v[16];
-          acc.load(32 * j + 16 * h, lane, v);
+          acc.load(32 * j + 16 * h, v);
           if (p.codes) {
             unpack_codes(ca[h], act8::scale_value((ahead.sa >> (8 * j)) & 255u), a);
             unpack_codes(cb[h], act8::scale_value((ahead.sb >> (8 * j)) & 255u), b);
@@ -596,12 +566,125 @@ __device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, con
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           float v[16];
-          acc.load(64 * j + 16 * (h + g), lane, v);
+          acc.load(64 * j + 16 * (h + g), v);
           if (add) take<64, 2, true>(here, lane, 2 * (h + g), v);
           stage<64, 2>(here, lane, 2 * (h + g), v);
         }
       }
       put<64>(here, lane, o.out0, o.N, row0, o.M, col, o.N);
+    }
+  }
+}
+
+// ---- tiles cut along K
+// A warp's 128 columns of its part, and what of the sum it finishes: the S warps that hold the parts of the same outputs share them
+// in granules of 16 columns (GATEUP: 16 features, 32 where whole blocks are kept in 8 bits; DH: 16 columns), granule g is
+// part g mod S's. All of it goes straight between registers and memory: it is little.
+__device__ __forceinline__ const float4 *part_of(const Params &p, int tile, int part, int slice, int c, int lane) {
+  return p.part + (((int64_t)tile * p.splits + part) * SLICES + slice) * (SLICE_FLOATS / 4) + (c / 4) * 32 + lane;
+}
+__device__ __forceinline__ void sum_parts(const Params &p, int tile, int slice, int c, int lane, float *v) {   // 16 columns from c on
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+  const float4 *src = part_of(p, tile, 0, slice, c, lane);
+  constexpr int64_t next = (int64_t)SLICES * SLICE_FLOATS / 4;
+#pragma unroll 1
+  for (int k = 0; k < p.splits; k += 4, src += 4 * next) {   // always in the parts' order, four parts' loads in flight
+    float4 w[4][4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[u][i] = k + u < p.splits ? __ldcg(src + u * next + i * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[4 * i] += w[u][i].x;
+        v[4 * i + 1] += w[u][i].y;
+        v[4 * i + 2] += w[u][i].z;
+        v[4 * i + 3] += w[u][i].w;
+      }
+    }
+  }
+}
+__device__ __forceinline__ void put16(__nv_bfloat16 *at, int col, int cols, const float *v) {
+  if (col < cols) *reinterpret_cast<uint4 *>(at) = pack_bf16x8(v);
+  if (col + 8 < cols) *reinterpret_cast<uint4 *>(at + 8) = pack_bf16x8(v + 8);
+}
+__device__ __forceinline__ void get16(const __nv_bfloat16 *at, int col, int cols, float *v) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+  if (col < cols) unpack_bf16x8(*reinterpret_cast<const uint4 *>(at), v);
+  if (col + 8 < cols) unpack_bf16x8(*reinterpret_cast<const uint4 *>(at + 8), v + 8);
+}
+template <int K>
+__device__ __forceinline__ void finish_part(const Params &p, const Product &o, const Unit &t, int slice, int lane, int row, int col0) {
+  const bool live = row < o.M;
+  const int64_t at1 = (int64_t)row * o.N, at2 = 2 * at1;   // the row in [., N] and in [., 2 N]
+  if (K == GATEUP && p.codes) {
+#pragma unroll 1
+    for (int g = t.part; g < 2; g += p.splits) {
+      const int col = col0 + 32 * g;
+      float a[32], b[32];
+      if (col >= o.N) break;
+#pragma unroll
+      for (int h = 0; h < 32; h += 16) {
+        sum_parts(p, t.tile, slice, 32 * g + h, lane, a + h);
+        sum_parts(p, t.tile, slice, 64 + 32 * g + h, lane, b + h);
+      }
+      if (!live) continue;
+      uint8_t *s = p.scales + (at2 + col) / act8::kBlock;
+      put_block8(p.codes + at2 + col, s, a);
+      put_block8(p.codes + at2 + o.N + col, s + o.N / act8::kBlock, b);
+#pragma unroll
+      for (int h = 0; h < 32; h += 16) {
+        gate16<true>(a + h, b + h, p.gate);
+        put16(o.out1 + at1 + col + h, col + h, o.N, a + h);
+      }
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int g = t.part; g < (K == GATEUP ? 4 : 8); g += p.splits) {
+    const int col = col0 + 16 * g;
+    if (col >= o.N) break;
+    float v[16];
+    sum_parts(p, t.tile, slice, 16 * g, lane, v);
+    if (K == GATEUP) {
+      float b[16];
+      sum_parts(p, t.tile, slice, 64 + 16 * g, lane, b);
+      if (!live) continue;
+      if (o.out0) {
+        put16(o.out0 + at2 + col, col, o.N, v);
+        put16(o.out0 + at2 + o.N + col, col, o.N, b);
+      }
+      gate16<true>(v, b, p.gate);
+      put16(o.out1 + at1 + col, col, o.N, v);
+    } else if (K == DH) {
+      if (!live) continue;
+      float a[16], b[16];
+      if (p.codes) {
+        const uint8_t *s = p.scales + (at2 + col) / act8::kBlock;
+        unpack_codes(*reinterpret_cast<const uint4 *>(p.codes + at2 + col), act8::scale_value(s[0]), a);
+        unpack_codes(*reinterpret_cast<const uint4 *>(p.codes + at2 + o.N + col), act8::scale_value(s[o.N / act8::kBlock]), b);
+      } else {
+        get16(o.in0 + at2 + col, col, o.N, a);
+        get16(o.in0 + at2 + o.N + col, col, o.N, b);
+      }
+      back16<true>(a, b, v, p.gate);
+      put16(o.out0 + at2 + col, col, o.N, a);
+      put16(o.out0 + at2 + o.N + col, col, o.N, v);
+      if (p.codes) put16(o.out1 + at1 + col, col, o.N, b);
+    } else {
+      if (!live) continue;
+      if (o.in0) {
+        float w[16];
+        get16(o.in0 + at1 + col, col, o.N, w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += w[i];
+      }
+      put16(o.out0 + at1 + col, col, o.N, v);
     }
   }
 }
@@ -778,45 +861,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const Product &o = p.prod[t.q];
       const int row0 = t.m * TILE + (int)rank * HALF + quarter * 32;
       const int col0 = K == GATEUP ? t.n * HALF + 64 * hh : t.n * TILE + HALF * hh;
+      const bool cut = t.part >= 0;
       Ahead<K> ahead;
-      ahead.start(p, o, buf, lane, row0, col0);
+      if (!cut) ahead.start(p, o, buf, lane, row0, col0);
       if (!wait_here(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 44)) return false;
       tc_fence_after();
       Slice<K> s;
       s.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * TILE + (K == GATEUP ? 64 : HALF) * hh);
-      s.splits = t.part < 0 ? 1 : p.splits;
-      s.mine = t.part;
-      bool here = true;   // the slice is finished by this warp
-      if (t.part >= 0) {
-        const int r = t.tile;
-        int *claimed = p.arrived + (r * SLICES + slice) * 2, *written = claimed + 1;
-        s.part = p.part + ((int64_t)r * p.splits * SLICES + slice) * (SLICE_FLOATS / 4);
-        int before = 0;
-        if (lane == 0) before = atomicAdd(claimed, 1);
-        here = __shfl_sync(0xffffffffu, before, 0) == p.splits - 1;
-        if (!here) {
-          float4 *out = const_cast<float4 *>(s.part) + t.part * Slice<K>::kNext + lane;
+      if (cut) {
+        float4 *out = const_cast<float4 *>(part_of(p, t.tile, t.part, slice, 0, lane));
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 16) {
-            float v[16];
-            s.held(c, v, false);
+        for (int c = 0; c < 128; c += 16) {
+          float v[16];
+          s.load(c, v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) __stcg(out + (c / 4 + i) * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-          }
-          landed<0>();       // what was asked for to finish the slice is not needed: its place is free again
-          __threadfence();   // this lane's part is visible before the count
-          __syncwarp();
-          if (lane == 0) atomicAdd(written, 1);
-        } else {
-          // the other parts' warps have all claimed before: they are writing, or have written, and wait for nothing
-          if (!wait_count(written, p.splits - 1, abort_flag, p.hdr)) return false;
-          if (lane == 0) *claimed = *written = 0;
+          for (int i = 0; i < 4; ++i) __stcg(out + (c / 4 + i) * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
         }
+      } else {
+        finish<K>(s, ahead, p, o, buf, lane, row0, col0);
       }
-      if (here) finish<K>(s, ahead, p, o, buf, lane, row0, col0);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(tempty_bar(acc));
+      if (cut) {
+        // the other parts' warps bring theirs without waiting for anything after this tile
+        int *written = p.arrived + (t.tile * SLICES + slice) * 2, *left = written + 1;
+        __threadfence();     // this lane's part is visible before the count
+        __syncwarp();
+        if (lane == 0) atomicAdd(written, 1);
+        if (!wait_count(written, p.splits, abort_flag, p.hdr)) return false;
+        finish_part<K>(p, o, t, slice, lane, row0 + lane, col0);
+        if (lane == 0 && atomicAdd(left, 1) == p.splits - 1) *written = *left = 0;
+      }
       if ((K == GATEUP || K == DH) && p.rows > 0) {   // others in this launch read what this warp has written, by TMA
         asm volatile("fence.proxy.async;" ::: "memory");
         __threadfence();
@@ -861,7 +937,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 // ----------------------------------------------------------------------------- host side -------
 // How a product's tiles are dealt out. One k-block of a tile takes about 0.29 us; a part that leaves and collects fp32
-// accumulators costs about as much as kPartCost of them (6.5 us: claim, store, fence, count, load).
+// accumulators costs about as much as kPartCost of them (6 us: store, fence, count, load; the second launch).
 constexpr int kPartCost = 24;
 struct Deal {
   int splits, units;
@@ -939,8 +1015,8 @@ static void deal_out(Params &p, int pairs) {
   }
 }
 
-// rows > 0: units wait for others of the same launch, so all its pairs have to be resident: a cooperative launch. `after`: launched
-// as a dependent of the kernel before it.
+// With rows > 0 or cut tiles units wait for others of the same launch, so all its pairs have to be resident: a cooperative launch.
+// `after`: launched as a dependent of the kernel before it where no unit waits.
 template <int CH>
 static int start(const Maps<CH> &maps, Params &p, const ffn::Block &blk, bool after, cudaStream_t s) {
   p.hdr = blk.hdr;
@@ -954,6 +1030,7 @@ static int start(const Maps<CH> &maps, Params &p, const ffn::Block &blk, bool af
   const int rc = pairs_resident<ffn_gemm_kernel<CH>>(pairs);
   if (rc) return rc;
   if (pairs > MAX_PAIRS) pairs = MAX_PAIRS;
+  if (p.splits > pairs) p.splits = 1;   // the parts of a tile wait for one another: on as many pairs
   int64_t units = p.units;
   if (p.splits == 1) {
     units = 0;
@@ -962,7 +1039,8 @@ static int start(const Maps<CH> &maps, Params &p, const ffn::Block &blk, bool af
   }
   if (pairs > units) pairs = (int)units;
   if (p.splits == 1) deal_out(p, pairs);
-  if (after) {
+  const bool waits = p.rows > 0 || p.splits > 1;
+  if (after && !waits) {
     MOE_TRY_CUDA(launch_after(ffn_gemm_kernel<CH>, dim3(2 * pairs), dim3(THREADS), (size_t)SMEM, s, maps, p));
     return MOE_OK;
   }
@@ -975,7 +1053,7 @@ static int start(const Maps<CH> &maps, Params &p, const ffn::Block &blk, bool af
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cfg.attrs = &attr;
-  cfg.numAttrs = p.rows > 0 ? 1 : 0;
+  cfg.numAttrs = waits ? 1 : 0;
   MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<CH>, maps, p));
   return MOE_OK;
 }
