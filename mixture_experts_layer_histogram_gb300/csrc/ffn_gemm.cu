@@ -42,7 +42,6 @@
 #include <type_traits>
 #include <utility>
 
-#include "dependent.cuh"
 #include "f32x2.cuh"
 #include "ffn.cuh"
 #include "tc_ptx.cuh"
@@ -78,7 +77,10 @@ enum Needs { NOTHING = 0, ITS_ROWS = 1, ALL_ROWS = 2 };   // of what an earlier 
 struct Product {
   int op, needs;
   int M, N;                  // valid rows; valid columns (GATEUP, DH: f)
+  int width;                 // columns of a tile: 256 or 128
   int m_tiles, n_tiles, num_kb;
+  int splits;                // its tiles are cut along K into this many parts (1: whole tiles)
+  int first, at;             // splits > 1: the pair that has the first part; the tiles' place in `part` and `arrived`
   __nv_bfloat16 *out0;       // GATEUP: kept ab (null: not kept, or in 8 bits); DH: dab; else the result
   __nv_bfloat16 *out1;       // GATEUP: h; DH from 8 bits: h
   const __nv_bfloat16 *in0;  // DH: kept ab; DOWN, DX: what is added (null: nothing)
@@ -96,14 +98,12 @@ struct Params {
   int products, deal[PRODUCTS];
   Product prod[PRODUCTS];
   uint16_t count[PRODUCTS][MAX_PAIRS];
-  bool more;                 // another kernel of the same call follows
-  // One product with its tiles cut along K (else splits = 1): parts of a tile, and parts in all
-  int splits, units;
-  float4 *part;              // [tile][part][slice][32][32] float4
-  int *arrived;              // [tile][slice][2]: parts written, warps done with them
+  // Tiles that are cut along K
+  float4 *part;              // [place + part][slice][32][32] float4
+  int *arrived;              // [place][slice][2]: parts written, warps done with them
   // Rows of tiles that the launch's first product has written: warps arrived per row, and what makes a row complete
   int *ready, *left;         // left: pairs that are done (the last one sets ready back to zero)
-  int rows, row_need;        // rows: 0 where nobody waits
+  int rows, row_need;
   Gate gate;
   uint8_t *codes, *scales;   // GATEUP, DH: ab in 8 bits (null: bf16)
 };
@@ -126,11 +126,11 @@ __device__ __forceinline__ void place(Unit &t, const Product &o) {
 }
 
 // The units of one pair, in order; the whole warp walks. In round t of a product the pairs that have more than t of its tiles
-// take consecutive ones.
+// take consecutive ones; parts of cut tiles go round all pairs.
 struct Walk {
-  int pair, pairs, u, c, t, base;
+  int pair, pairs, c, t, base;   // cut: t is the next part's number
   int n0, n1, n2;            // this lane's share of the product's counts
-  __device__ __forceinline__ Walk(int pair_, int pairs_, const Params &p) : pair(pair_), pairs(pairs_), u(pair_), c(0) { open(p); }
+  __device__ __forceinline__ Walk(int pair_, int pairs_, const Params &p) : pair(pair_), pairs(pairs_), c(0) { open(p); }
   // (Loads of the parameters through their generic address: one per 32 lanes, where the constant path takes them lane by lane.)
   static __device__ __forceinline__ int count(const uint16_t *at) {
     uint16_t v;
@@ -140,48 +140,51 @@ struct Walk {
   __device__ __forceinline__ void open(const Params &p) {
     const uint16_t *row = p.count[c] + (threadIdx.x & 31);
     t = base = 0;
+    if (p.prod[c].splits > 1) {
+      t = pair - p.prod[c].first;
+      if (t < 0) t += pairs;
+    }
     n0 = count(row);
     n1 = count(row + 32);
     n2 = count(row + 64);
   }
   __device__ __forceinline__ bool next(Unit &w, const Params &p) {
-    w.q = 0;
     w.part = -1;
-    if (p.splits > 1) {
-      if (u >= p.units) return false;
-      w.tile = u / p.splits;
-      w.part = u - w.tile * p.splits;
-      w.kb0 = (int)((int64_t)p.prod[0].num_kb * w.part / p.splits);
-      w.kb1 = (int)((int64_t)p.prod[0].num_kb * (w.part + 1) / p.splits);
-      u += pairs;
-      place(w, p.prod[0]);
-      return true;
-    }
     for (;;) {
-      const uint32_t b0 = __ballot_sync(0xffffffffu, n0 > t), b1 = __ballot_sync(0xffffffffu, n1 > t),
-                     b2 = __ballot_sync(0xffffffffu, n2 > t);
-      const uint32_t mine = pair < 32 ? b0 : (pair < 64 ? b1 : b2), below = (1u << (pair & 31)) - 1;
-      if (mine >> (pair & 31) & 1) {
-        w.tile = base + __popc(mine & below) + (pair >= 32 ? __popc(b0) : 0) + (pair >= 64 ? __popc(b1) : 0);
-        base += __popc(b0) + __popc(b1) + __popc(b2);
-        ++t;
-        break;
+      const Product &o = p.prod[c];
+      if (o.splits > 1) {
+        if (t < o.m_tiles * o.n_tiles * o.splits) {
+          w.tile = t / o.splits;
+          w.part = t - w.tile * o.splits;
+          t += pairs;
+          break;
+        }
+      } else {
+        const uint32_t b0 = __ballot_sync(0xffffffffu, n0 > t), b1 = __ballot_sync(0xffffffffu, n1 > t),
+                       b2 = __ballot_sync(0xffffffffu, n2 > t);
+        const uint32_t mine = pair < 32 ? b0 : (pair < 64 ? b1 : b2), below = (1u << (pair & 31)) - 1;
+        if (mine >> (pair & 31) & 1) {
+          w.tile = base + __popc(mine & below) + (pair >= 32 ? __popc(b0) : 0) + (pair >= 64 ? __popc(b1) : 0);
+          base += __popc(b0) + __popc(b1) + __popc(b2);
+          ++t;
+          break;
+        }
       }
       if (++c >= p.products) return false;
       open(p);
     }
-    w.q = c;
-    w.kb0 = 0;
-    w.kb1 = p.prod[w.q].num_kb;
-    place(w, p.prod[w.q]);
+    const Product &o = p.prod[w.q = c];
+    w.kb0 = w.part < 0 ? 0 : (int)((int64_t)o.num_kb * w.part / o.splits);
+    w.kb1 = w.part < 0 ? o.num_kb : (int)((int64_t)o.num_kb * (w.part + 1) / o.splits);
+    place(w, o);
     return true;
   }
 };
 
-// kind::f16: D fp32, A and B bf16, M = 256, N = 256
-__host__ __device__ constexpr uint32_t idesc(bool a_mn, bool b_mn) {
+// kind::f16: D fp32, A and B bf16, M = 256, N = width
+__device__ __forceinline__ uint32_t idesc(bool a_mn, bool b_mn, int width) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+         ((uint32_t)(width >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
 }
 
 // TMEM has been read (wait::ld): nothing in memory is handed over, so the arrival need not wait for this warp's stores
@@ -369,12 +372,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-// The warp's 32 x 128 accumulated outputs of a tile (GATEUP: a of 64 features, then b of the same)
+// The warp's 32 x width / 2 accumulated outputs of a tile (GATEUP: a of width / 4 features, and b of the same)
 template <int K> struct Slice {
   uint32_t tmem;             // TMEM address of the first column
+  int apart;                 // GATEUP: columns from a to b
   __device__ __forceinline__ void load(int c, float *v) const {   // 16 columns from column c on
     uint32_t r[16];
-    tmem_ld16(tmem + (uint32_t)(K == GATEUP && c >= 64 ? HALF - 64 + c : c), r);
+    tmem_ld16(tmem + (uint32_t)c, r);
     tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
@@ -402,7 +406,7 @@ template <int K> struct Ahead {
       if (o.in0) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          fetch<64>(buf + j * BUF, o.in0, o.N, row0, o.M, col0 + 64 * j, o.N, lane);
+          if (128 * j < o.width) fetch<64>(buf + j * BUF, o.in0, o.N, row0, o.M, col0 + 64 * j, o.N, lane);
           commit();
         }
       }
@@ -414,7 +418,7 @@ template <int K> struct Ahead {
         const uint8_t *s = p.scales + ((row0 + lane) * 2 * (int64_t)o.N + col0) / act8::kBlock;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bool live = row0 + lane < o.M && col0 + 32 * j < o.N;
+          const bool live = row0 + lane < o.M && 64 * j < o.width && col0 + 32 * j < o.N;
           sa |= (live ? (uint32_t)s[j] : 0u) << (8 * j);
           sb |= (live ? (uint32_t)s[j + o.N / act8::kBlock] : 0u) << (8 * j);
         }
@@ -442,24 +446,24 @@ template <bool CUBIC> __device__ __forceinline__ void back16(float *a, float *b,
   }
 }
 
-// What becomes of the warp's slice: rows row0 .. row0 + 31 (a lane each), 128 columns from col0 on (GATEUP: 64 features). Sixteen
+// What becomes of the warp's slice: rows row0 .. row0 + 31 (a lane each), width / 2 columns from col0 on (GATEUP: width / 4 features). Sixteen
 // columns at a time in loops that stay loops: unrolled, most of the time of a first (or only) tile went into fetching the code.
 template <int K>
 __device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, const Params &p, const Product &o, uint32_t buf, int lane,
                                        int row0, int col0) {
   if (K == GATEUP) {
-    const int row = row0 + lane;
+    const int row = row0 + lane, blocks = o.width / 128, end = min(o.N, col0 + 32 * blocks);
     const int64_t ld = 2 * (int64_t)o.N;
     if (p.codes) {
 #pragma unroll 1
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < blocks; ++j) {
         const int col = col0 + 32 * j;
         if (col >= o.N) break;
         float a[32], b[32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           acc.load(32 * j + 16 * h, a + 16 * h);
-          acc.load(64 + 32 * j + 16 * h, b + 16 * h);
+          acc.load(acc.apart + 32 * j + 16 * h, b + 16 * h);
         }
         if (row < o.M) {
           uint8_t *c = p.codes + row * ld + col, *s = p.scales + (row * ld + col) / act8::kBlock;
@@ -473,20 +477,20 @@ __device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, con
         }
         stage<64, 4>(buf, lane, 4 * j, a);
       }
-      if (col0 < o.N) put<64>(buf, lane, o.out1, o.N, row0, o.M, col0, o.N);
+      if (col0 < o.N) put<64>(buf, lane, o.out1, o.N, row0, o.M, col0, end);
       return;
     }
     if (col0 >= o.N) return;
     // a and b leave through the two halves of the buffers (32 features each), h through the place of a
 #pragma unroll 1
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < blocks; ++j) {
       const int col = col0 + 32 * j;
       uint4 qh[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float a[16], b[16];
         acc.load(32 * j + 16 * h, a);
-        acc.load(64 + 32 * j + 16 * h, b);
+        acc.load(acc.apart + 32 * j + 16 * h, b);
         if (o.out0) {
           stage<32, 2>(buf, lane, 2 * h, a);
           stage<32, 2>(buf + 2048, lane, 2 * h, b);
@@ -503,10 +507,11 @@ __device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, con
 #pragma unroll
       for (int c = 0; c < 4; ++c) st_shared_v4(Chunk<64>::at(buf + BUF, lane, 4 * j + c), qh[c]);
     }
-    put<64>(buf + BUF, lane, o.out1, o.N, row0, o.M, col0, o.N);
+    put<64>(buf + BUF, lane, o.out1, o.N, row0, o.M, col0, end);
   } else if (K == DH) {
+    const int blocks = o.width / 64;
 #pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < blocks; ++j) {
       const int col = col0 + 32 * j;
       const uint32_t here = buf + (j & 1) * BUF;
       const int64_t ld = 2 * (int64_t)o.N;
@@ -547,13 +552,13 @@ __device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, con
           put<32>(here, lane, o.out1, o.N, row0, o.M, col, o.N);
         }
       }
-      if (j < 2) Ahead<K>::block(p, o, here, lane, row0, col + 64);
+      if (j + 2 < blocks) Ahead<K>::block(p, o, here, lane, row0, col + 64);
       else commit();                  // one group per block, for the count
     }
   } else {
     const bool add = o.in0 != nullptr;
 #pragma unroll 1
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; 128 * j < o.width; ++j) {
       const int col = col0 + 64 * j;
       const uint32_t here = buf + j * BUF;
       if (add) {
@@ -577,24 +582,24 @@ __device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, con
 }
 
 // ---- tiles cut along K
-// A warp's 128 columns of its part, and what of the sum it finishes: the S warps that hold the parts of the same outputs share them
+// A warp's columns of its part, and what of the sum it finishes: the S warps that hold the parts of the same outputs share them
 // in granules of 16 columns (GATEUP: 16 features, 32 where whole blocks are kept in 8 bits; DH: 16 columns), granule g is
 // part g mod S's. All of it goes straight between registers and memory: it is little.
-__device__ __forceinline__ const float4 *part_of(const Params &p, int tile, int part, int slice, int c, int lane) {
-  return p.part + (((int64_t)tile * p.splits + part) * SLICES + slice) * (SLICE_FLOATS / 4) + (c / 4) * 32 + lane;
+__device__ __forceinline__ float4 *part_of(const Params &p, const Product &o, int tile, int part, int slice, int c, int lane) {
+  return p.part + ((int64_t)(o.at + tile * o.splits + part) * SLICES + slice) * (SLICE_FLOATS / 4) + (c / 4) * 32 + lane;
 }
-__device__ __forceinline__ void sum_parts(const Params &p, int tile, int slice, int c, int lane, float *v) {   // 16 columns from c on
+__device__ __forceinline__ void sum_parts(const Params &p, const Product &o, int tile, int slice, int c, int lane, float *v) {   // 16 columns from c on
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-  const float4 *src = part_of(p, tile, 0, slice, c, lane);
+  const float4 *src = part_of(p, o, tile, 0, slice, c, lane);
   constexpr int64_t next = (int64_t)SLICES * SLICE_FLOATS / 4;
 #pragma unroll 1
-  for (int k = 0; k < p.splits; k += 4, src += 4 * next) {   // always in the parts' order, four parts' loads in flight
+  for (int k = 0; k < o.splits; k += 4, src += 4 * next) {   // always in the parts' order, four parts' loads in flight
     float4 w[4][4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[u][i] = k + u < p.splits ? __ldcg(src + u * next + i * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int i = 0; i < 4; ++i) w[u][i] = k + u < o.splits ? __ldcg(src + u * next + i * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -624,14 +629,14 @@ __device__ __forceinline__ void finish_part(const Params &p, const Product &o, c
   const int64_t at1 = (int64_t)row * o.N, at2 = 2 * at1;   // the row in [., N] and in [., 2 N]
   if (K == GATEUP && p.codes) {
 #pragma unroll 1
-    for (int g = t.part; g < 2; g += p.splits) {
+    for (int g = t.part; g < o.width / 128; g += o.splits) {
       const int col = col0 + 32 * g;
       float a[32], b[32];
       if (col >= o.N) break;
 #pragma unroll
       for (int h = 0; h < 32; h += 16) {
-        sum_parts(p, t.tile, slice, 32 * g + h, lane, a + h);
-        sum_parts(p, t.tile, slice, 64 + 32 * g + h, lane, b + h);
+        sum_parts(p, o, t.tile, slice, 32 * g + h, lane, a + h);
+        sum_parts(p, o, t.tile, slice, 64 + 32 * g + h, lane, b + h);
       }
       if (!live) continue;
       uint8_t *s = p.scales + (at2 + col) / act8::kBlock;
@@ -646,14 +651,14 @@ __device__ __forceinline__ void finish_part(const Params &p, const Product &o, c
     return;
   }
 #pragma unroll 1
-  for (int g = t.part; g < (K == GATEUP ? 4 : 8); g += p.splits) {
+  for (int g = t.part; g < o.width / (K == GATEUP ? 64 : 32); g += o.splits) {
     const int col = col0 + 16 * g;
     if (col >= o.N) break;
     float v[16];
-    sum_parts(p, t.tile, slice, 16 * g, lane, v);
+    sum_parts(p, o, t.tile, slice, 16 * g, lane, v);
     if (K == GATEUP) {
       float b[16];
-      sum_parts(p, t.tile, slice, 64 + 16 * g, lane, b);
+      sum_parts(p, o, t.tile, slice, 64 + 16 * g, lane, b);
       if (!live) continue;
       if (o.out0) {
         put16(o.out0 + at2 + col, col, o.N, v);
@@ -715,7 +720,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   Walk walk(pair, pairs, p);
   Unit t{};
-  if (p.more) start_next();   // it may set itself up on SMs that this one has left
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);
@@ -742,7 +746,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();   // both CTAs: barriers initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  wait_previous();
   bool more = walk.next(t, p);
 
   if (warp == 0) {
@@ -757,7 +760,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const Product &o = p.prod[t.q];
       const bool along_m = a_mn(t);
       const int arow = t.m * TILE + (int)rank * HALF;
-      const int brow = CH == FWD && o.op == GATEUP ? (int)rank * o.N + t.n * HALF : t.n * TILE + (int)rank * HALF;
+      const int half = o.width / 2, b_bytes = half * (BK * 2);
+      const int brow = CH == FWD && o.op == GATEUP ? (int)rank * o.N + t.n * half : t.n * o.width + (int)rank * half;
       if (!seen && !rows.wait(p, o, t.m, abort_flag)) break;
       Unit nx{};
       more = walk.next(nx, p);
@@ -772,7 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (elect_one()) {
           const uint32_t sA = sbase + stage * STAGE, sB = sA + OPERAND;
           const uint32_t fb = mapa_shared(full_bar(stage), 0);   // the leader's full barrier
-          if (leader) mbar_expect_tx(full_bar(stage), 2 * STAGE);
+          if (leader) mbar_expect_tx(full_bar(stage), 2 * (OPERAND + b_bytes));
           const int kx = kb * BK;
           if (along_m) {
 #pragma unroll
@@ -781,8 +785,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             tma_load_2d_pair(sA, tmA, kx, arow, fb);
           }
           if (B_MN) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) tma_load_2d_pair(sB + q * (BK * 128), tmB, brow + 64 * q, kx, fb);
+            for (int q = 0; 64 * q < half; ++q) tma_load_2d_pair(sB + q * (BK * 128), tmB, brow + 64 * q, kx, fb);
           } else {
             tma_load_2d_pair(sB, tmB, kx, brow, fb);
           }
@@ -807,7 +810,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint64_t desc_b = B_MN ? sdesc(sbase + OPERAND, BK * 128, 1024) : sdesc(sbase + OPERAND, 16, 1024);
     for (; ok && more; more = walk.next(t, p)) {
       const uint64_t desc_a = a_mn(t) ? desc_a_mn : desc_a_k;
-      const uint32_t id = a_mn(t) ? idesc(true, B_MN) : idesc(false, B_MN), a_step = a_mn(t) ? 2048 >> 4 : 32 >> 4;
+      const uint32_t id = idesc(a_mn(t), B_MN, p.prod[t.q].width), a_step = a_mn(t) ? 2048 >> 4 : 32 >> 4;
       if (!mbar_ready_cluster(tempty_bar(acc), acc_phase ^ 1u) &&
           !mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.hdr, 42))
         break;
@@ -860,22 +863,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       constexpr int K = decltype(op)::value;
       const Product &o = p.prod[t.q];
       const int row0 = t.m * TILE + (int)rank * HALF + quarter * 32;
-      const int col0 = K == GATEUP ? t.n * HALF + 64 * hh : t.n * TILE + HALF * hh;
+      const int mine = o.width / (K == GATEUP ? 4 : 2);   // columns (GATEUP: features) of this warp
+      const int col0 = (2 * t.n + hh) * mine;
       const bool cut = t.part >= 0;
       Ahead<K> ahead;
       if (!cut) ahead.start(p, o, buf, lane, row0, col0);
       if (!wait_here(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 44)) return false;
       tc_fence_after();
       Slice<K> s;
-      s.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * TILE + (K == GATEUP ? 64 : HALF) * hh);
+      s.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * TILE + mine * hh);
+      s.apart = o.width / 2;
       if (cut) {
-        float4 *out = const_cast<float4 *>(part_of(p, t.tile, t.part, slice, 0, lane));
+        float4 *out = part_of(p, o, t.tile, t.part, slice, 0, lane);
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 16) {
+        for (int c = 0; c < o.width / 2; c += 16) {
           float v[16];
-          s.load(c, v);
+          s.load(K == GATEUP && c >= mine ? c - mine + s.apart : c, v);
+          const int to = K == GATEUP && c >= mine ? c - mine + 64 : c;   // b's columns from 64 on
 #pragma unroll
-          for (int i = 0; i < 4; ++i) __stcg(out + (c / 4 + i) * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          for (int i = 0; i < 4; ++i) __stcg(out + (to / 4 + i) * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
         }
       } else {
         finish<K>(s, ahead, p, o, buf, lane, row0, col0);
@@ -885,19 +891,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (lane == 0) arrive_leader(tempty_bar(acc));
       if (cut) {
         // the other parts' warps bring theirs without waiting for anything after this tile
-        int *written = p.arrived + (t.tile * SLICES + slice) * 2, *left = written + 1;
+        int *written = p.arrived + ((o.at + t.tile * o.splits) * SLICES + slice) * 2;
         __threadfence();     // this lane's part is visible before the count
         __syncwarp();
         if (lane == 0) atomicAdd(written, 1);
-        if (!wait_count(written, p.splits, abort_flag, p.hdr)) return false;
+        if (!wait_count(written, o.splits, abort_flag, p.hdr)) return false;
         finish_part<K>(p, o, t, slice, lane, row0 + lane, col0);
-        if (lane == 0 && atomicAdd(left, 1) == p.splits - 1) *written = *left = 0;
       }
-      if ((K == GATEUP || K == DH) && p.rows > 0) {   // others in this launch read what this warp has written, by TMA
+      if (K == GATEUP || K == DH) {   // others in this launch read what this warp has written, by TMA
         asm volatile("fence.proxy.async;" ::: "memory");
         __threadfence();
         __syncwarp();
         if (lane == 0) atomicAdd(p.ready + t.m, 1);
+      }
+      if (cut) {
+        int *written = p.arrived + ((o.at + t.tile * o.splits) * SLICES + slice) * 2, *left = written + 1;
+        if (lane == 0 && atomicAdd(left, 1) == o.splits - 1) *written = *left = 0;
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
@@ -920,7 +929,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   tc_fence_before();
   cluster_sync();   // no CTA leaves while its peer may still signal its barriers or use its TMEM
-  if (p.rows > 0 && leader && warp == 0) {   // nobody of this pair waits any more: the last pair clears up
+  if (leader && warp == 0) {   // nobody of this pair waits any more: the last pair clears up
     int before = 0;
     if (lane == 0) before = atomicAdd(p.left, 1);
     if (__shfl_sync(0xffffffffu, before, 0) == pairs - 1) {
@@ -936,34 +945,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 }
 
 // ----------------------------------------------------------------------------- host side -------
-// How a product's tiles are dealt out. One k-block of a tile takes about 0.29 us; a part that leaves and collects fp32
-// accumulators costs about as much as kPartCost of them (6 us: store, fence, count, load; the second launch).
-constexpr int kPartCost = 24;
-struct Deal {
-  int splits, units;
-  size_t bytes;   // of the parts
+// How a product is cut up: tiles of 256 or 128 columns, and along K. One k-block of a tile takes about 0.26 us at 256 columns,
+// three quarters of that at 128 (the copies bound it); a tile's start and epilogue 3 us or 2, a part's, which leaves and
+// collects fp32 accumulators, 3 or 2 more.
+struct Plan {
+  int width, splits;
 };
-static Deal deal(int64_t tiles_m, int64_t tiles_n, int num_kb, int pairs) {
-  const int64_t tiles = tiles_m * tiles_n;
-  Deal best{1, (int)tiles, 0};
-  if (tiles >= pairs) return best;   // one launch with the call's other products evens out an incomplete round
-  const int rem = (int)tiles;
-  int64_t cost = num_kb;
-  for (int s = 2; s <= MAX_SPLIT && s <= num_kb; ++s) {
-    if (rem * s > 2 * pairs) break;
-    const int64_t c = (int64_t)((rem * s + pairs - 1) / pairs) * ((num_kb + s - 1) / s + kPartCost);
-    if (c < cost) {
-      cost = c;
-      best = Deal{s, rem * s, (size_t)rem * s * SLICES * SLICE_FLOATS * 4};
+constexpr int kBlockCost[2] = {4, 3}, kTileCost[2] = {48, 32}, kPartCost[2] = {48, 32};   // of 256 columns, of 128
+static int64_t up(int64_t n, int64_t k) { return (n + k - 1) / k; }
+static Plan plan(int64_t m_tiles, int64_t columns, int num_kb, int pairs) {
+  Plan best{TILE, 1};
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t tiles = m_tiles * up(columns, TILE >> i);
+    const int64_t per = num_kb * kBlockCost[i];
+    // whole tiles: with more than one round the epilogues run beside the products
+    const int64_t cost = up(tiles, pairs) * per + kTileCost[i];
+    if (cost < least) {
+      least = cost;
+      best = {TILE >> i, 1};
+    }
+    if (tiles >= pairs) continue;   // with the call's other products in the same launch an incomplete round is evened out
+    for (int s = 2; s <= MAX_SPLIT && s <= num_kb && tiles * s <= 2 * pairs; ++s) {
+      const int64_t c = up(tiles * s, pairs) * (up(num_kb, s) * kBlockCost[i] + kTileCost[i] + kPartCost[i]);
+      if (c < least) {
+        least = c;
+        best = {TILE >> i, s};
+      }
     }
   }
   return best;
 }
 // The pairs that the plan counts on: those of a GB300, wherever it is asked for (the workspace's size follows from it).
 constexpr int kPairs = 76;
-constexpr size_t kArrivedBytes = (size_t)kPairs * SLICES * 8;   // fewer than kPairs tiles are cut
-
-static int64_t up(int64_t n, int64_t k) { return (n + k - 1) / k; }
+constexpr int kPlaces = 2 * 2 * kPairs;   // of parts: two products of a call may be cut, into 2 kPairs parts each at most
+constexpr size_t kArrivedBytes = (size_t)kPlaces * SLICES * 8;
+constexpr size_t kPartBytes = (size_t)SLICES * SLICE_FLOATS * 4;
 
 template <auto KERNEL> static int pairs_resident(int &pairs) {
   static std::atomic<int> known[64];
@@ -986,39 +1003,52 @@ template <auto KERNEL> static int pairs_resident(int &pairs) {
 // The counters in front of the parts: for cut tiles, then pairs that are done (one line), then rows of tiles.
 static size_t counter_bytes(int64_t T) { return kArrivedBytes + 128 + (size_t)up(up(T, TILE), 32) * 128; }
 
-// How the products' tiles are dealt to the pairs: product after product (in p.deal's order), each tile to the pair with the least work so far (whole
-// rounds at once, but for the last two).
+// How the products' tiles are dealt to the pairs, product after product (in p.deal's order): parts of cut tiles in turn, whole tiles each
+// to the pair with the least work so far (whole rounds at once, but for the last two). What waits for a first product of one
+// round waits for all of it.
 static void deal_out(Params &p, int pairs) {
   int64_t load[MAX_PAIRS] = {};
   memset(p.count, 0, sizeof(p.count));
   std::pair<int64_t, int> heap[MAX_PAIRS];
   const auto later = [](const std::pair<int64_t, int> &x, const std::pair<int64_t, int> &y) { return x > y; };
+  int next = 0, at = 0;
   for (int i = 0; i < p.products; ++i) {
-    const int c = p.deal[i];
-    int64_t n = (int64_t)p.prod[c].m_tiles * p.prod[c].n_tiles;
-    const int64_t cost = p.prod[c].num_kb + 2;
-    const int64_t even = n / pairs > 2 ? n / pairs - 2 : 0;
-    for (int k = 0; k < pairs; ++k) {
-      p.count[c][k] = (uint16_t)even;
-      load[k] += even * cost;
-      heap[k] = {load[k], k};
+    const int c = p.deal[i], wide = p.prod[c].width == TILE ? 0 : 1;
+    Product &o = p.prod[c];
+    int64_t n = (int64_t)o.m_tiles * o.n_tiles * o.splits;
+    const int64_t cost = o.num_kb * kBlockCost[wide] / o.splits + (o.splits > 1 ? kTileCost[wide] + kPartCost[wide] : 8);
+    if (o.splits > 1) {
+      o.first = next;
+      o.at = at;
+      for (int64_t u = 0; u < n; ++u) load[(next + u) % pairs] += cost;
+      next = (int)((next + n) % pairs);
+      at += (int)n;
+    } else {
+      const int64_t even = n / pairs > 2 ? n / pairs - 2 : 0;
+      for (int k = 0; k < pairs; ++k) {
+        p.count[c][k] = (uint16_t)even;
+        load[k] += even * cost;
+        heap[k] = {load[k], k};
+      }
+      std::make_heap(heap, heap + pairs, later);
+      for (n -= even * pairs; n > 0; --n) {
+        std::pop_heap(heap, heap + pairs, later);
+        auto &least = heap[pairs - 1];
+        ++p.count[c][least.second];
+        least.first += cost;
+        std::push_heap(heap, heap + pairs, later);
+      }
+      for (int k = 0; k < pairs; ++k) load[heap[k].second] = heap[k].first;
     }
-    std::make_heap(heap, heap + pairs, later);
-    for (n -= even * pairs; n > 0; --n) {
-      std::pop_heap(heap, heap + pairs, later);
-      auto &least = heap[pairs - 1];
-      ++p.count[c][least.second];
-      least.first += cost;
-      std::push_heap(heap, heap + pairs, later);
+    if (i == 0 && (int64_t)o.m_tiles * o.n_tiles * o.splits <= pairs) {
+      const int64_t most = *std::max_element(load, load + pairs);
+      for (int k = 0; k < pairs; ++k) load[k] = most;
     }
-    for (int k = 0; k < pairs; ++k) load[heap[k].second] = heap[k].first;
   }
 }
 
-// With rows > 0 or cut tiles units wait for others of the same launch, so all its pairs have to be resident: a cooperative launch.
-// `after`: launched as a dependent of the kernel before it where no unit waits.
-template <int CH>
-static int start(const Maps<CH> &maps, Params &p, const ffn::Block &blk, bool after, cudaStream_t s) {
+// Units wait for others of the same launch, so all its pairs have to be resident: a cooperative launch.
+template <int CH> static int start(const Maps<CH> &maps, Params &p, const ffn::Block &blk, cudaStream_t s) {
   p.hdr = blk.hdr;
   p.gate = blk.gate;
   uint8_t *ws = (uint8_t *)blk.ws;
@@ -1026,24 +1056,21 @@ static int start(const Maps<CH> &maps, Params &p, const ffn::Block &blk, bool af
   p.left = (int *)(ws + kArrivedBytes);
   p.ready = (int *)(ws + kArrivedBytes + 128);
   p.part = (float4 *)(ws + counter_bytes(blk.T));
+  p.rows = p.prod[0].m_tiles;
   int pairs = 0;
   const int rc = pairs_resident<ffn_gemm_kernel<CH>>(pairs);
   if (rc) return rc;
   if (pairs > MAX_PAIRS) pairs = MAX_PAIRS;
-  if (p.splits > pairs) p.splits = 1;   // the parts of a tile wait for one another: on as many pairs
-  int64_t units = p.units;
-  if (p.splits == 1) {
-    units = 0;
-    for (int q = 0; q < p.products; ++q) units += (int64_t)p.prod[q].m_tiles * p.prod[q].n_tiles;
-    if (units > (int64_t)pairs * 60000) return MOE_ERR_UNSUPPORTED;   // counts have 16 bits
+  int64_t units = 0;
+  for (int q = 0; q < p.products; ++q) {
+    Product &o = p.prod[q];
+    if (o.splits > pairs) o.splits = 1;   // the parts of a tile wait for one another: on as many pairs
+    units += (int64_t)o.m_tiles * o.n_tiles * o.splits;
   }
+  p.row_need = p.prod[0].n_tiles * SLICES * p.prod[0].splits;
+  if (units > (int64_t)pairs * 60000) return MOE_ERR_UNSUPPORTED;   // counts have 16 bits
   if (pairs > units) pairs = (int)units;
-  if (p.splits == 1) deal_out(p, pairs);
-  const bool waits = p.rows > 0 || p.splits > 1;
-  if (after && !waits) {
-    MOE_TRY_CUDA(launch_after(ffn_gemm_kernel<CH>, dim3(2 * pairs), dim3(THREADS), (size_t)SMEM, s, maps, p));
-    return MOE_OK;
-  }
+  deal_out(p, pairs);
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeCooperative;
   attr.val.cooperative = 1;
@@ -1053,31 +1080,27 @@ static int start(const Maps<CH> &maps, Params &p, const ffn::Block &blk, bool af
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cfg.attrs = &attr;
-  cfg.numAttrs = waits ? 1 : 0;
+  cfg.numAttrs = 1;
   MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<CH>, maps, p));
   return MOE_OK;
 }
 
-static Product product(int op, int64_t M, int64_t N, int64_t k) {
+// One product; width 0: planned by itself
+static Product product(int op, int64_t M, int64_t N, int64_t k, int width = 0) {
   Product o{};
   o.op = op;
   o.M = (int)M;
   o.N = (int)N;
   o.m_tiles = (int)up(M, TILE);
-  o.n_tiles = (int)up(N, op == GATEUP ? HALF : TILE);
   o.num_kb = (int)up(k, BK);
+  const int64_t columns = op == GATEUP ? 2 * N : N;
+  const Plan how = width ? Plan{width, 1} : plan(o.m_tiles, columns, o.num_kb, kPairs);
+  o.width = how.width;
+  o.splits = how.splits;
+  o.n_tiles = (int)up(columns, o.width);
   return o;
 }
-static Deal deal_of(const Product &o) { return deal(o.m_tiles, o.n_tiles, o.num_kb, kPairs); }
-
-// One launch of the first product alone
-static void alone(Params &p, const Deal &d) {
-  p.products = 1;
-  p.deal[0] = 0;
-  p.splits = d.splits;
-  p.units = d.units;
-}
-
+static size_t part_bytes(const Product &o) { return o.splits > 1 ? (size_t)o.m_tiles * o.n_tiles * o.splits * kPartBytes : 0; }
 }  // namespace ffng
 }  // namespace tc
 
@@ -1088,20 +1111,18 @@ using namespace tc::ffng;
 typedef __nv_bfloat16 bf16;
 
 size_t gemm_workspace(int T, int d, int f, bool backward) {
-  size_t most = deal_of(product(GATEUP, T, f, d)).bytes;
-  most = std::max(most, deal_of(product(DOWN, T, d, f)).bytes);
-  if (backward) most = std::max(most, deal_of(product(DH, T, f, d)).bytes);
+  size_t most = part_bytes(product(GATEUP, T, f, d)) + part_bytes(product(DOWN, T, d, f));
+  if (backward) most = std::max(most, part_bytes(product(DH, T, f, d)));
   return counter_bytes(T) + most;
 }
 
-// Forward: both products in one launch, y's tiles waiting for the rows of h that they read; where tiles are cut (few of them, many
-// idle pairs) two launches.
+// Forward: y's tiles wait for the rows of h that they read.
 int gemm_fwd(const Block &b, cudaStream_t s) {
-  Maps<FWD> m;
-  if (!make_map(&m.a[0], b.x, b.T, b.d, HALF) || !make_map(&m.b[0], b.w_gate_up, 2 * (uint64_t)b.f, b.d, HALF) ||
-      !make_map(&m.a[1], b.h, b.T, b.f, HALF) || !make_map(&m.b[1], b.w_down, b.d, b.f, HALF))
-    return MOE_ERR_CUDA;
   Product up_ = product(GATEUP, b.T, b.f, b.d), down = product(DOWN, b.T, b.d, b.f);
+  Maps<FWD> m;
+  if (!make_map(&m.a[0], b.x, b.T, b.d, HALF) || !make_map(&m.b[0], b.w_gate_up, 2 * (uint64_t)b.f, b.d, up_.width / 2) ||
+      !make_map(&m.a[1], b.h, b.T, b.f, HALF) || !make_map(&m.b[1], b.w_down, b.d, b.f, down.width / 2))
+    return MOE_ERR_CUDA;
   Params p{};
   if (b.scales) {
     p.codes = (uint8_t *)b.ab;
@@ -1112,28 +1133,12 @@ int gemm_fwd(const Block &b, cudaStream_t s) {
   up_.out1 = (bf16 *)b.h;
   down.in0 = (const bf16 *)b.add;
   down.out0 = (bf16 *)b.y;
-  const Deal d0 = deal_of(up_), d1 = deal_of(down);
+  down.needs = ITS_ROWS;
   p.prod[0] = up_;
-  p.splits = 1;
-  if (d0.splits == 1 && d1.splits == 1) {
-    down.needs = ITS_ROWS;
-    p.prod[1] = down;
-    p.products = 2;
-    p.deal[1] = 1;
-    p.rows = up_.m_tiles;
-    p.row_need = up_.n_tiles * SLICES;
-    return start<FWD>(m, p, b, false, s);
-  }
-  alone(p, d0);
-  p.more = true;
-  const int rc = start<FWD>(m, p, b, false, s);
-  if (rc) return rc;
-  p.prod[0] = down;
-  m.a[0] = m.a[1];
-  m.b[0] = m.b[1];
-  alone(p, d1);
-  p.more = false;
-  return start<FWD>(m, p, b, true, s);
+  p.prod[1] = down;
+  p.products = 2;
+  p.deal[1] = 1;
+  return start<FWD>(m, p, b, s);
 }
 
 // Backward: da, db (and h, from 8 bits), then dx = dab Wgu (+ dx_in), dWd = dy^T h and dWgu = dab^T x, in one launch. dx waits for
@@ -1142,8 +1147,11 @@ int gemm_fwd(const Block &b, cudaStream_t s) {
 // tiles are dealt out before the shorter ones, which even out what those leave.
 int gemm_bwd(const Block &b, cudaStream_t s) {
   const uint64_t T = b.T, d = b.d, f = b.f;
-  Product dh = product(DH, b.T, b.f, b.d), dx = product(DX, b.T, b.d, 2 * (int64_t)b.f), down = product(DW, b.d, b.f, b.T),
-          gu = product(DW, 2 * (int64_t)b.f, b.d, b.T);
+  // the last three run beside one another: narrow tiles where they give every pair one at most
+  const int64_t tiles = up(T, TILE) * up(d, HALF) + up(d, TILE) * up(f, HALF) + up(2 * f, TILE) * up(d, HALF);
+  const int width = tiles <= kPairs ? HALF : TILE;
+  Product dh = product(DH, b.T, b.f, b.d), dx = product(DX, b.T, b.d, 2 * (int64_t)b.f, width), down = product(DW, b.d, b.f, b.T, width),
+          gu = product(DW, 2 * (int64_t)b.f, b.d, b.T, width);
   Params p{};
   if (b.scales) {
     p.codes = (uint8_t *)b.ab;
@@ -1157,15 +1165,10 @@ int gemm_bwd(const Block &b, cudaStream_t s) {
   dx.out0 = (bf16 *)b.dx;
   down.out0 = (bf16 *)b.dw_down;
   gu.out0 = (bf16 *)b.dw_gate_up;
-  const Deal d0 = deal_of(dh);
-  const bool one = d0.splits == 1, dx_longer = dx.num_kb > gu.num_kb;
-  if (one) {
-    p.rows = dh.m_tiles;
-    p.row_need = dh.n_tiles * SLICES;
-    dx.needs = ITS_ROWS;
-    gu.needs = ALL_ROWS;
-    down.needs = b.scales ? ALL_ROWS : NOTHING;
-  }
+  const bool dx_longer = dx.num_kb > gu.num_kb;
+  dx.needs = ITS_ROWS;
+  gu.needs = ALL_ROWS;
+  down.needs = b.scales ? ALL_ROWS : NOTHING;
   const int ix = b.scales ? 1 : 2, iw = 3 - ix;   // dx and dWd
   Maps<BWD> m;
   p.prod[0] = dh;
@@ -1176,25 +1179,11 @@ int gemm_bwd(const Block &b, cudaStream_t s) {
       !make_map(&m.b[ix], b.w_gate_up, 2 * f, d, BK) || !make_map(&m.a[iw], b.dy, T, d, BK) || !make_map(&m.b[iw], b.h, T, f, BK) ||
       !make_map(&m.a[3], b.dab, T, 2 * f, BK) || !make_map(&m.b[3], b.x, T, d, BK))
     return MOE_ERR_CUDA;
-  p.splits = 1;
   p.products = 4;
   p.deal[1] = dx_longer ? ix : iw;
   p.deal[2] = dx_longer ? iw : 3;
   p.deal[3] = dx_longer ? 3 : ix;
-  if (one) return start<BWD>(m, p, b, false, s);
-  Params first = p;
-  alone(first, d0);
-  first.more = true;
-  const int rc = start<BWD>(m, first, b, false, s);
-  if (rc) return rc;
-  p.products = 3;
-  for (int q = 0; q < 3; ++q) {
-    p.prod[q] = p.prod[q + 1];
-    p.deal[q] = p.deal[q + 1] - 1;
-    m.a[q] = m.a[q + 1];
-    m.b[q] = m.b[q + 1];
-  }
-  return start<BWD>(m, p, b, true, s);
+  return start<BWD>(m, p, b, s);
 }
 
 }  // namespace ffn
