@@ -238,7 +238,7 @@ struct Rows {
     }
     there = __all_sync(0xffffffffu, there);
     if (there) {
-      asm volatile("fence.proxy.async;" ::: "memory");
+      asm volatile("fence.proxy.async.global;" ::: "memory");
       all = o.needs == ALL_ROWS;
     }
     return there;
@@ -892,17 +892,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (cut) {
         // the other parts' warps bring theirs without waiting for anything after this tile
         int *written = p.arrived + ((o.at + t.tile * o.splits) * SLICES + slice) * 2;
-        __threadfence();     // this lane's part is visible before the count
-        __syncwarp();
-        if (lane == 0) atomicAdd(written, 1);
+        __syncwarp();        // the other lanes' parts are visible before the count
+        if (lane == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(written) : "memory");
         if (!wait_count(written, o.splits, abort_flag, p.hdr)) return false;
         finish_part<K>(p, o, t, slice, lane, row0 + lane, col0);
       }
       if (K == GATEUP || K == DH) {   // others in this launch read what this warp has written, by TMA
-        asm volatile("fence.proxy.async;" ::: "memory");
-        __threadfence();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
         __syncwarp();
-        if (lane == 0) atomicAdd(p.ready + t.m, 1);
+        if (lane == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p.ready + t.m) : "memory");
       }
       if (cut) {
         int *written = p.arrived + ((o.at + t.tile * o.splits) * SLICES + slice) * 2, *left = written + 1;
@@ -945,13 +943,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 }
 
 // ----------------------------------------------------------------------------- host side -------
-// How a product is cut up: tiles of 256 or 128 columns, and along K. One k-block of a tile takes about 0.26 us at 256 columns,
-// three quarters of that at 128 (the copies bound it); a tile's start and epilogue 3 us or 2, a part's, which leaves and
-// collects fp32 accumulators, 3 or 2 more.
+// How a product is cut up: tiles of 256 or 128 columns, and along K. The costs are in units of 0.065 us, as measured at 389 x 2048 x
+// 1024 and 256 x 4096 x 2048: a k-block takes 0.26 us at 256 columns and 0.19 at 128 (the copies bound both), the last
+// epilogue 2-3 us or 1.2; a part, that leaves its fp32 accumulators, waits for the others' and adds up its share of them, 5.6
+// or 4.
 struct Plan {
   int width, splits;
 };
-constexpr int kBlockCost[2] = {4, 3}, kTileCost[2] = {48, 32}, kPartCost[2] = {48, 32};   // of 256 columns, of 128
+constexpr int kBlockCost[2] = {4, 3}, kTileCost[2] = {38, 18}, kPartCost[2] = {48, 44};   // of 256 columns, of 128
 static int64_t up(int64_t n, int64_t k) { return (n + k - 1) / k; }
 static Plan plan(int64_t m_tiles, int64_t columns, int num_kb, int pairs) {
   Plan best{TILE, 1};
@@ -966,7 +965,7 @@ static Plan plan(int64_t m_tiles, int64_t columns, int num_kb, int pairs) {
       best = {TILE >> i, 1};
     }
     if (tiles >= pairs) continue;   // with the call's other products in the same launch an incomplete round is evened out
-    for (int s = 2; s <= MAX_SPLIT && s <= num_kb && tiles * s <= 2 * pairs; ++s) {
+    for (int s = 2; s <= MAX_SPLIT && s <= num_kb && tiles * s <= pairs; ++s) {
       const int64_t c = up(tiles * s, pairs) * (up(num_kb, s) * kBlockCost[i] + kTileCost[i] + kPartCost[i]);
       if (c < least) {
         least = c;
