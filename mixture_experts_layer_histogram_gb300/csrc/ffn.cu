@@ -19,7 +19,8 @@ static int check(int T, int d, int f, int dtype, int act, int keep) {
 
 // Few tokens: the path that reads the weights once, whose blocks each read all tokens. With more of those than 32 and large weights
 // that reading costs more than the tiles of the other path. This one and the other, in us: 44 and 57 for 32 tokens of 4096 x
-// 8192 (201 MB), 57 and 57 for 48, 77 and 57 for 64; for 48 of 8192 x 16384 (805 MB) 193 and 164; for 64 of 4096 x 2048 28 and 30.
+// 8192 (201 MB), 57 and 57 for 48, 77 and 57 for 64; for 48 of 8192 x 16384 (805 MB) 193 and 164; for 64 of 4096 x 2048 23 and 30,
+// of 2048 x 8192 (101 MB) 39 and 39.
 static bool few(int T, int d, int f) {
   const int64_t weights = (int64_t)6 * d * f;
   return T <= 32 || (T <= 48 && weights <= (int64_t)512 << 20) || (T <= kFewTokens && weights <= (int64_t)128 << 20);

@@ -32,9 +32,9 @@ __device__ __forceinline__ float square_of(float a) { return fminf(a * a, 1e30f)
 template <bool EXACT = false> __device__ __forceinline__ float gated(float a, const Gate &k) {
   return a * sigma<EXACT>(a * fmaf(k.k1, square_of(a), k.k0));
 }
-// act(a) and act'(a)
-template <bool EXACT = false> __device__ __forceinline__ void gate_and_slope(float a, const Gate &k, float &act, float &slope) {
-  const float q = square_of(a), s = sigma<EXACT>(a * fmaf(k.k1, q, k.k0));
+// act(a) and act'(a), in full fp32
+__device__ __forceinline__ void gate_and_slope(float a, const Gate &k, float &act, float &slope) {
+  const float q = square_of(a), s = sigma<true>(a * fmaf(k.k1, q, k.k0));
   act = a * s;
   slope = fmaf(act * (1.0f - s), fmaf(3.0f * k.k1, q, k.k0), s);
 }

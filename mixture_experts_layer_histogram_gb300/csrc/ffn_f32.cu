@@ -179,7 +179,7 @@ template <int KIND, int B> __global__ void __launch_bounds__(Tile<B>::THREADS) f
     } else if (KIND == DH) {
       const float a = p.in[m * 2 * p.N + n], b = p.in[m * 2 * p.N + p.N + n];
       float act, slope;
-      gate_and_slope<true>(a, p.gate, act, slope);
+      gate_and_slope(a, p.gate, act, slope);
       p.C[m * 2 * p.N + n] = v * b * slope;
       p.C[m * 2 * p.N + p.N + n] = v * act;
     } else {

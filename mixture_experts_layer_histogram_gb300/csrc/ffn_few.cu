@@ -1,6 +1,6 @@
 // The gated feed-forward block's forward for few tokens (up to 64), bf16: one token is the case of serving.
 //
-// Bound: the weights' way from HBM, 6 d f bytes, once. A thread block therefore owns a few output features (16 or 32 weight
+// Bound: the weights' way from HBM, 6 d f bytes, once. A thread block therefore owns a few output features (16 weight
 // rows) over the whole of K, its eight warps an eighth of K each, and the weights go from memory to registers and from there into
 // the products, without a stop in shared memory: nothing in a block uses a weight twice. The products are mma.m16n8k16
 // (weights as the 16 rows, tokens as the 8 columns): at up to 64 tokens they take a fraction of the time of the loads,
@@ -10,6 +10,7 @@
 // so a lane's accumulators hold a and b of one feature. The warps' sums meet in shared memory, in a fixed order.
 //
 // DOWN starts as a dependent of GATEUP and loads its first weights while GATEUP runs.
+// Measured at 2048 x 1024 (12.6 MB of weights, in L2): 7.7 us for 1 to 16 tokens, most of it the two launches from the host, 10.2 for 32.
 #include <cuda.h>
 
 #include <algorithm>
@@ -63,44 +64,38 @@ __device__ __forceinline__ void put_down(const Params &p, int n, int apart, int 
   }
 }
 
-// NT: groups of eight tokens. MT: groups of sixteen weight rows. CH: 32-deep steps whose loads are in flight together.
-template <bool UP, int NT, int MT, int CH>
+// NT: groups of eight tokens. CH: 32-deep steps whose loads are in flight together.
+template <bool UP, int NT, int CH>
 __global__ void __launch_bounds__(THREADS, 2) ffn_few_kernel(const Params p) {
-  __shared__ float4 sums[WARPS][MT * NT][32];
+  __shared__ float4 sums[WARPS][NT][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int steps = (p.K + 31) / 32, each = (steps + WARPS - 1) / WARPS;
   const int s0 = warp * each, s1 = min(steps, s0 + each);
   if (UP) start_next();
-  // this lane's two weight rows of each group of sixteen
-  const __nv_bfloat16 *rows[MT][2];
-  bool have[MT][2];
+  // this lane's two weight rows
+  const __nv_bfloat16 *rows[2];
+  bool have[2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int n = UP ? (blockIdx.x * MT + m) * 8 + g : (blockIdx.x * MT + m) * 16 + 8 * u + g;
-      have[m][u] = n < p.N;
-      rows[m][u] = p.w + ((int64_t)(UP ? u * p.N : 0) + n) * p.K + 8 * q;
-    }
+  for (int u = 0; u < 2; ++u) {
+    const int n = UP ? blockIdx.x * 8 + g : blockIdx.x * 16 + 8 * u + g;
+    have[u] = n < p.N;
+    rows[u] = p.w + ((int64_t)(UP ? u * p.N : 0) + n) * p.K + 8 * q;
   }
-  uint4 w[CH][MT][2];
+  uint4 w[CH][2];
   auto load_weights = [&](int s) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int k = (s + c) * 32;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          w[c][m][u] = make_uint4(0, 0, 0, 0);
-          if (s + c < s1 && k + 8 * q < p.K && have[m][u]) w[c][m][u] = weight16(rows[m][u] + k);
-        }
+      for (int u = 0; u < 2; ++u) {
+        w[c][u] = make_uint4(0, 0, 0, 0);
+        if (s + c < s1 && k + 8 * q < p.K && have[u]) w[c][u] = weight16(rows[u] + k);
       }
     }
   };
   load_weights(s0);
   wait_previous();
-  float acc[MT][NT][4] = {};
+  float acc[NT][4] = {};
   for (int s = s0; s < s1; s += CH) {
     if (s > s0) load_weights(s);
     uint4 x[CH][NT];
@@ -116,24 +111,18 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_few_kernel(const Params p) {
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+      const uint4 a = w[c][0], b = w[c][1];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const uint4 a = w[c][m][0], b = w[c][m][1];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma16816(acc[m][n], a.x, b.x, a.y, b.y, x[c][n].x, x[c][n].y);
-          mma16816(acc[m][n], a.z, b.z, a.w, b.w, x[c][n].z, x[c][n].w);
-        }
+      for (int n = 0; n < NT; ++n) {
+        mma16816(acc[n], a.x, b.x, a.y, b.y, x[c][n].x, x[c][n].y);
+        mma16816(acc[n], a.z, b.z, a.w, b.w, x[c][n].z, x[c][n].w);
       }
     }
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) sums[warp][m * NT + n][lane] = make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
-  }
+  for (int n = 0; n < NT; ++n) sums[warp][n][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
   __syncthreads();
-  for (int i = warp; i < MT * NT; i += WARPS) {
+  for (int i = warp; i < NT; i += WARPS) {
     float4 v = sums[0][i][lane];
 #pragma unroll
     for (int s = 1; s < WARPS; ++s) {
@@ -143,19 +132,20 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_few_kernel(const Params p) {
       v.z += o.z;
       v.w += o.w;
     }
-    const int m = i / NT, t = 8 * (i - m * NT) + 2 * q;   // tokens t and t + 1
-    if (UP) put_up(p, (blockIdx.x * MT + m) * 8 + g, t, v);
-    else put_down(p, (blockIdx.x * MT + m) * 16 + g, 8, t, v);
+    const int t = 8 * i + 2 * q;   // tokens t and t + 1
+    if (UP) put_up(p, blockIdx.x * 8 + g, t, v);
+    else put_down(p, blockIdx.x * 16 + g, 8, t, v);
   }
 }
 
-template <bool UP, int NT, int MT, int CH> static int launch(const Params &p, cudaStream_t s) {
-  const int per = UP ? 8 * MT : 16 * MT, grid = (p.N + per - 1) / per;
+template <bool UP, int NT, int CH> static int launch(const Params &p, cudaStream_t s) {
+  constexpr int per = UP ? 8 : 16;
+  const int grid = (p.N + per - 1) / per;
   if (UP) {
-    ffn_few_kernel<UP, NT, MT, CH><<<grid, THREADS, 0, s>>>(p);
+    ffn_few_kernel<UP, NT, CH><<<grid, THREADS, 0, s>>>(p);
     MOE_CHECK_LAUNCH();
   } else {
-    MOE_TRY_CUDA(launch_after(ffn_few_kernel<UP, NT, MT, CH>, dim3(grid), dim3(THREADS), 0, s, p));
+    MOE_TRY_CUDA(launch_after(ffn_few_kernel<UP, NT, CH>, dim3(grid), dim3(THREADS), 0, s, p));
   }
   return MOE_OK;
 }
@@ -166,10 +156,11 @@ template <bool UP, int NT, int MT, int CH> static int launch(const Params &p, cu
 // registers hold; each of the eight warps takes 64 of the 512. The tensors are seen as [K / 64, rows, 64], so that one copy brings
 // eight 128-byte-swizzled boxes: 16-byte chunk c of row g lies at (c ^ g) * 16 (g its low three bits). A lane takes the chunks 2 q and
 // 2 q + 1, so that the eight lanes that read together, of two rows, meet all banks once (q and q + 4 met half of them twice).
-// With loads into registers (above) 134 MB of weights for 24 tokens took 33 us (4.0 TB/s).
+// Measured for 24 tokens of 4096 x 8192: 26.5 us for the 134 MB of Wg and Wu (5.1 TB/s) and 16 for the 67 MB of Wd, 41 together; with
+// loads into registers (above) the 134 MB took 33 us.
 constexpr int KS = 512;                        // of K per stage
 struct Stream {
-  int groups, steps, stages;                   // row groups; stages per group; places of the ring
+  int groups, steps;                           // row groups; stages per group
 };
 template <int NT, int MT> constexpr int weight_bytes() { return 16 * MT * KS * 2; }
 template <int NT> constexpr int token_bytes() { return 8 * NT * KS * 2; }
@@ -341,7 +332,7 @@ template <bool UP, int NT, int MT> static int launch_stream(const Params &p, WsH
   const int rc = raise_limit<ffn_stream_kernel<UP, NT, MT>, SMEM>();
   if (rc) return rc;
   const int per = UP ? 8 * MT : 16 * MT;
-  const Stream st{(p.N + per - 1) / per, (p.K + KS - 1) / KS, stages_of<NT, MT>()};
+  const Stream st{(p.N + per - 1) / per, (p.K + KS - 1) / KS};
   const int grid = std::min(st.groups, sm_count());
   if (UP) {
     ffn_stream_kernel<UP, NT, MT><<<grid, THREADS + 32, SMEM, s>>>(mw, mx, p, st, hdr);
@@ -361,11 +352,10 @@ template <bool UP, int NT> static int stream(const Params &p, WsHeader *hdr, cud
   return launch_stream<UP, NT, 1>(p, hdr, s);
 }
 
-// Small weights take the kernel that starts quickest, others (over 128 KB per SM, rows of whole 128 bytes) the ring.
-template <bool UP> static int run(const Params &p, WsHeader *hdr, cudaStream_t s) {
+// ring: through the ring, both products of a call
+template <bool UP> static int run(const Params &p, bool ring, WsHeader *hdr, cudaStream_t s) {
   const int nt = (p.T + 7) / 8;
-  const int64_t bytes = (UP ? 4 : 2) * (int64_t)p.N * p.K;
-  if (p.K % 64 == 0 && bytes > (int64_t)sm_count() * 128 * 1024) {
+  if (ring) {
     switch (nt) {
       case 1: return stream<UP, 1>(p, hdr, s);
       case 2: return stream<UP, 2>(p, hdr, s);
@@ -376,16 +366,21 @@ template <bool UP> static int run(const Params &p, WsHeader *hdr, cudaStream_t s
       default: return stream<UP, 8>(p, hdr, s);
     }
   }
-  if (nt == 1) return launch<UP, 1, 1, 8>(p, s);
-  if (nt == 2) return launch<UP, 2, 1, 4>(p, s);
-  if (nt <= 4) return launch<UP, 4, 1, 4>(p, s);
-  return launch<UP, 8, 1, 2>(p, s);
+  if (nt == 1) return launch<UP, 1, 8>(p, s);
+  if (nt == 2) return launch<UP, 2, 4>(p, s);
+  if (nt <= 4) return launch<UP, 4, 4>(p, s);
+  return launch<UP, 8, 2>(p, s);
 }
 
 }  // namespace few
 
 int few_fwd(const Block &b, cudaStream_t s) {
   typedef __nv_bfloat16 bf16;
+  // Small weights take the kernel that starts quickest, others the ring, whose rows are whole 128 bytes. In us, the ring and the other: 4
+  // tokens of 2048 x 1024 (12.6 MB) 8.9 and 8.0, of 2048 x 2048 10.1 and 8.2, of 4096 x 2048 (50 MB) 12.3 and 12.3, of 2048 x 8192 (101
+  // MB) 20 and 25; 24 tokens of 768 x 512 (2.4 MB) 8.7 and 7.9, of 2048 x 1024 8.9 and 9.0, of 2048 x 2048 10.3 and 12.3. (One product
+  // through the ring and the other not is slower than either: 14.1 for 4 tokens of 4096 x 2048.)
+  const bool ring = b.d % 64 == 0 && b.f % 64 == 0 && (int64_t)6 * b.d * b.f > (int64_t)(b.T <= 16 ? 48 : 8) << 20;
   few::Params p{};
   p.tok = (const bf16 *)b.x;
   p.w = (const bf16 *)b.w_gate_up;
@@ -394,7 +389,7 @@ int few_fwd(const Block &b, cudaStream_t s) {
   p.K = b.d;
   p.N = b.f;
   p.gate = b.gate;
-  const int rc = few::run<true>(p, b.hdr, s);
+  const int rc = few::run<true>(p, ring, b.hdr, s);
   if (rc) return rc;
   p.tok = (const bf16 *)b.h;
   p.w = (const bf16 *)b.w_down;
@@ -402,7 +397,7 @@ int few_fwd(const Block &b, cudaStream_t s) {
   p.out = (bf16 *)b.y;
   p.K = b.f;
   p.N = b.d;
-  return few::run<false>(p, b.hdr, s);
+  return few::run<false>(p, ring, b.hdr, s);
 }
 
 }  // namespace ffn

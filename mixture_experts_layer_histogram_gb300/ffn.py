@@ -44,6 +44,8 @@ class GatedFFN:
         for name, shape in (("h", (T, f)), ("dab", (T, 2 * f))):
             if name in scratch:
                 L._want(f"scratch[{name!r}]", scratch[name], dtype, shape)
+                if scratch[name].device != torch.empty(0, **act_).device:
+                    raise ValueError(f"scratch[{name!r}] is on {scratch[name].device}, the block is on {self.device}")
         self.h = scratch["h"] if "h" in scratch else torch.empty((T, f), **act_)
         self.y = torch.empty((T, d), **act_)
         self.ws = torch.zeros(L.moe_ffn_workspace_size(T, d, f, code, backward), **u8)

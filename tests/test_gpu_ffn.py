@@ -20,6 +20,7 @@ if torch.cuda.is_available():
 
 BF, F32 = torch.bfloat16, torch.float32
 C = math.sqrt(2 / math.pi)
+PARTS = 4 * 76 * 16 * 8     # bytes of the arrival counts of parts
 
 
 def gate(a, act):
@@ -74,7 +75,7 @@ def check_forward(ffn, s, act, add):
         within("ab", ffn.ab, ab, noise)
     product("y", y, ffn.h, s["wd"], dt, s["add"] if add else None)
     assert ffn.status() == 0
-    counters = 256 + 76 * 16 * 8 + 128 + -(-T // 8192) * 128     # status, parts of cut tiles, pairs done, rows of tiles written
+    counters = 256 + PARTS + 128 + -(-T // 8192) * 128            # status, parts of cut tiles, pairs done, rows of tiles written
     assert ffn.ws[:counters if dt == BF else 256].count_nonzero() == 0
     return y
 
@@ -95,15 +96,15 @@ def check_backward(ffn, s, act, add):
     product("dx", res["dx"], ffn.dab, s["wgu"].T, dt, s["dadd"] if add else None)
     product("dw_gate_up", res["dw_gate_up"], ffn.dab.T, s["x"].T, dt)
     product("dw_down", res["dw_down"], s["dy"].T, ffn.h.T, dt)
-    assert ffn.status() == 0 and ffn.ws[:256 + 76 * 16 * 8 + 128 if dt == BF else 256].count_nonzero() == 0
+    assert ffn.status() == 0 and ffn.ws[:256 + PARTS + 128 if dt == BF else 256].count_nonzero() == 0
     return res
 
 
 FEW = [(1, 64, 64), (1, 2048, 1024), (2, 8, 8), (3, 72, 40), (8, 520, 1000), (9, 256, 264), (17, 264, 136), (24, 256, 8192), (31, 1032, 4104),
        (33, 128, 72), (57, 2048, 512), (64, 512, 1000), (1, 4096, 8192), (9, 4096, 2744), (24, 4096, 8192), (26, 8192, 4104), (41, 2112, 9608),
-       (64, 4032, 5000)]
+       (64, 4032, 5000), (20, 1088, 1344), (33, 2048, 704), (64, 704, 2112)]
 MANY = [(65, 64, 64), (100, 8, 8), (127, 136, 72), (256, 256, 256), (257, 520, 264), (700, 1032, 328), (1000, 2048, 1024), (2500, 1024, 2048),
-        (3000, 64, 4096), (515, 4096, 96)]
+        (3000, 64, 4096), (515, 4096, 96), (256, 4096, 2048), (1300, 1024, 1088)]
 
 
 @pytest.mark.parametrize("act,add", [("silu", True), ("gelu", False)])
@@ -114,7 +115,7 @@ def test_forward(T, d, f, act, add):
 
 @pytest.mark.parametrize("keep", [None, "f8"])
 @pytest.mark.parametrize("act,add", [("silu", True), ("gelu", False)])
-@pytest.mark.parametrize("T,d,f", [(1, 64, 64), (5, 8, 32), (64, 200, 96)] + [m for m in MANY if m[2] % 32 == 0] + [(300, 72, 8192)])
+@pytest.mark.parametrize("T,d,f", [(1, 64, 64), (5, 8, 32), (64, 200, 96)] + [m for m in MANY if m[2] % 32 == 0] + [(300, 72, 8192), (130, 8192, 2048)])
 def test_step(T, d, f, act, add, keep):
     s = make(T, d, f, BF, T + d + f)
     ffn = GatedFFN(T, d, f, act=act, keep=keep)
@@ -273,3 +274,5 @@ def test_shared_scratch():
         assert all(torch.equal(p[k], q[k]) for k in p)
     with pytest.raises(ValueError, match="shared"):
         GatedFFN(T, d, f, scratch=scratch)
+    with pytest.raises(ValueError, match="scratch"):      # not where the block is
+        GatedFFN(T, d, f, keep="f8", scratch={k: v.cpu() for k, v in scratch.items()})
