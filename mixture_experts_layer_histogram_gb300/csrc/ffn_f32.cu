@@ -8,11 +8,13 @@
 // neighbouring columns.
 //
 // A product with few tiles and a long K is shared by a cluster of up to eight blocks, a part of K each: each block leaves its
-// tile in its shared memory and finishes a share of the rows, adding the parts up in the blocks' order.
-// Measured at 203 x 501 x 1337 (2.4 GFLOP), forward and backward: 409 us without the cluster and with one step in flight, 155 with
-// both, 127 with addresses formed once and K cut by the work per SM. What bounds it then is FMA issue on SMs that get three
-// blocks where others get two, and rows and columns past the edge (203 rows are computed as 256). Launched as dependents of one
-// another the six kernels took 145 us.
+// tile in its shared memory and finishes a share of the rows, adding the parts up in the blocks' order. Measured at 203 x 501 x
+// 1337 (2.4 GFLOP), forward and backward: 409 us without the cluster and with one step in flight, 155 with both, 130 in a
+// replayed graph (140 in a stream of calls) with addresses formed once and K cut by the work per SM; at 2000 x 1024 x 2048 (75
+// GFLOP) 1.81 ms, 42 TFLOP/s. There the FMA pipe is active 69% of the time and waits for its turn; the small case keeps it 44%
+// active: SMs that get three blocks where others get two, the ramp of six launches, and rows and columns past the edge (203 rows
+// are computed as 256). Launched as dependents of one another the six kernels took 145 us; 8 x 8 values per thread in the small
+// tile, two groups of threads sharing its K, took the same time.
 #include <cooperative_groups.h>
 
 #include <atomic>

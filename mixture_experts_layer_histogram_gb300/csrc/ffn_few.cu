@@ -1,18 +1,18 @@
 // The gated feed-forward block's forward for few tokens (up to 64), bf16: one token is the case of serving.
 //
-// Bound: the weights' way from HBM, 6 d f bytes, once. A thread block therefore owns a few output features (16 weight
-// rows) over the whole of K, its eight warps an eighth of K each, and the weights go from memory to registers and from there into
-// the products, without a stop in shared memory: nothing in a block uses a weight twice. The products are mma.m16n8k16
-// (weights as the 16 rows, tokens as the 8 columns): at up to 64 tokens they take a fraction of the time of the loads,
-// and unlike tcgen05 they read their operands from registers. K may be taken in any order as long as both operands take the
-// same, so a lane loads 16 consecutive bytes of a weight row and of a token and feeds them to two products:
-// lane 4 g + q holds row (token) g, k = 8 q .. 8 q + 7 of each 32. GATEUP's 16 rows are 8 gate rows and the same features' 8 up rows,
-// so a lane's accumulators hold a and b of one feature. The warps' sums meet in shared memory, in a fixed order.
+// Bound: the weights' way from HBM, 6 d f bytes, once. A thread block therefore owns a few output features (16 weight rows) over
+// the whole of K, its eight warps an eighth of K each, and the weights go from memory to registers and from there into the
+// products, without a stop in shared memory: nothing in a block uses a weight twice. The products are mma.m16n8k16 (weights as
+// the 16 rows, tokens as the 8 columns): at up to 64 tokens they take a fraction of the time of the loads, and unlike tcgen05
+// they read their operands from registers. K may be taken in any order as long as both operands take the same, so a lane loads
+// 16 consecutive bytes of a weight row and of a token and feeds them to two products: lane 4 g + q holds row (token) g, k = 8 q
+// .. 8 q + 7 of each 32. GATEUP's 16 rows are 8 gate rows and the same features' 8 up rows, so a lane's accumulators hold a and
+// b of one feature. The warps' sums meet in shared memory, in a fixed order.
 //
 // DOWN starts as a dependent of GATEUP and loads its first weights while GATEUP runs.
-// Measured at 2048 x 1024 (12.6 MB of weights, in L2): one token 4.3 us in a replayed graph, 8.1 us in a stream of calls (the host's
-// time); 16 tokens 5.8 us. Both products in one cooperative launch, with a count of finished blocks between them, took 5.3 and 7.3 us in
-// a graph and saved 1.6 us of host time.
+// Measured at 2048 x 1024 (12.6 MB of weights, in L2): one token 4.3 us in a replayed graph, 8.1 us in a stream of calls (the
+// host's time); 16 tokens 5.8 us. Both products in one cooperative launch, with a count of finished blocks between them, took
+// 5.3 and 7.3 us in a graph and saved 1.6 us of host time.
 #include <cuda.h>
 
 #include <algorithm>
@@ -155,11 +155,11 @@ template <bool UP, int NT, int CH> static int launch(const Params &p, cudaStream
 // ---------------------------------------------------------------------------------------------
 // The same for weights that keep the GPU busy for longer than a kernel takes to start: one block per SM streams its row groups
 // through a ring in shared memory that TMA keeps full, 16 (or 32) weight rows and all tokens by 512 of K a stage, whatever the
-// registers hold; each of the eight warps takes 64 of the 512. The tensors are seen as [K / 64, rows, 64], so that one copy brings
-// eight 128-byte-swizzled boxes: 16-byte chunk c of row g lies at (c ^ g) * 16 (g its low three bits). A lane takes the chunks 2 q and
-// 2 q + 1, so that the eight lanes that read together, of two rows, meet all banks once (q and q + 4 met half of them twice).
-// Measured for 24 tokens of 4096 x 8192: 26.5 us for the 134 MB of Wg and Wu (5.1 TB/s) and 16 for the 67 MB of Wd, 41 together; with
-// loads into registers (above) the 134 MB took 33 us.
+// registers hold; each of the eight warps takes 64 of the 512. The tensors are seen as [K / 64, rows, 64], so that one copy
+// brings eight 128-byte-swizzled boxes: 16-byte chunk c of row g lies at (c ^ g) * 16 (g its low three bits). A lane takes the
+// chunks 2 q and 2 q + 1, so that the eight lanes that read together, of two rows, meet all banks once (q and q + 4 met half of
+// them twice). Measured for 24 tokens of 4096 x 8192: 26.5 us for the 134 MB of Wg and Wu (5.1 TB/s) and 16 for the 67 MB of Wd,
+// 41 together; with loads into registers (above) the 134 MB took 33 us.
 constexpr int KS = 512;                        // of K per stage
 struct Stream {
   int groups, steps;                           // row groups; stages per group
@@ -378,10 +378,10 @@ template <bool UP> static int run(const Params &p, bool ring, WsHeader *hdr, cud
 
 int few_fwd(const Block &b, cudaStream_t s) {
   typedef __nv_bfloat16 bf16;
-  // Small weights take the kernel that starts quickest, others the ring, whose rows are whole 128 bytes. In us, the ring and the other: 4
-  // tokens of 2048 x 1024 (12.6 MB) 8.9 and 8.0, of 2048 x 2048 10.1 and 8.2, of 4096 x 2048 (50 MB) 12.3 and 12.3, of 2048 x 8192 (101
-  // MB) 20 and 25; 24 tokens of 768 x 512 (2.4 MB) 8.7 and 7.9, of 2048 x 1024 8.9 and 9.0, of 2048 x 2048 10.3 and 12.3. (One product
-  // through the ring and the other not is slower than either: 14.1 for 4 tokens of 4096 x 2048.)
+  // Small weights take the kernel that starts quickest, others the ring, whose rows are whole 128 bytes. In us, the ring and the
+  // other: 4 tokens of 2048 x 1024 (12.6 MB) 8.9 and 8.0, of 2048 x 2048 10.1 and 8.2, of 4096 x 2048 (50 MB) 12.3 and 12.3, of
+  // 2048 x 8192 (101 MB) 20 and 25; 24 tokens of 768 x 512 (2.4 MB) 8.7 and 7.9, of 2048 x 1024 8.9 and 9.0, of 2048 x 2048 10.3
+  // and 12.3. (One product through the ring and the other not is slower than either: 14.1 for 4 tokens of 4096 x 2048.)
   const bool ring = b.d % 64 == 0 && b.f % 64 == 0 && (int64_t)6 * b.d * b.f > (int64_t)(b.T <= 16 ? 48 : 8) << 20;
   few::Params p{};
   p.tok = (const bf16 *)b.x;

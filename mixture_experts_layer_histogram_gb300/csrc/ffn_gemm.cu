@@ -13,26 +13,31 @@
 // GATEUP's B is 128 gate rows in one CTA and the same features' 128 up rows in the other: every thread of the epilogue
 // (a TMEM lane is a token) holds a and b of the same features, a whole block of 32 at a time for the 8-bit codes.
 //
-// One launch runs all products of a call: y's tiles follow the ones of h in the same kernel, the last three products those of da, db.
-// A pair takes its tiles in the order of the products, as many of each as even out the pairs' work (deal_out); a unit that
-// reads what others of the launch write waits until the rows of tiles that it needs are complete (counts per row, in the
+// One launch runs all products of a call: y's tiles follow the ones of h in the same kernel, the last three products those of
+// da, db. A pair takes its tiles in the order of the products, as many of each as even out the pairs' work (deal_out); a unit
+// that reads what others of the launch write waits until the rows of tiles that it needs are complete (counts per row, in the
 // workspace; the pairs are all resident, a cooperative launch, and no pair waits before it has brought all its tiles of the
 // first product). In separate launches the incomplete last rounds, the set-up of each kernel and its last epilogues cost 45 of
 // 259 us of a step at 8192 x 2048 x 1024.
 //
-// A first product of fewer tiles than pairs whose K is long is cut along K into S parts instead, in a launch of its own. The warps that
-// hold the parts of the same 32 x 128 outputs leave their fp32 accumulators in the workspace, wait until all are there (every
-// pair is resident, and takes its units in the order of their tiles, so that ends) and finish a share of the outputs each, adding
-// the parts up in their order. (One warp finishing all of them took 22 us for eight parts.)
+// A product of fewer tiles than pairs gets more of them: tiles of 128 columns instead of 256, or its tiles cut along K into S
+// parts (plan). The warps that hold the parts of the same outputs leave their fp32 accumulators in the workspace, wait until all
+// are there (every pair is resident, and takes its parts in the order of their tiles, so that ends) and finish a share of the
+// outputs each, adding the parts up in their order. (One warp finishing all of them took 22 us for eight parts.) 389 x 2048 x
+// 1024 forward: 26.6 us in two launches of wide tiles, 22.5 in one with narrow ones. Of the 18.5 us inside the kernel, 2.7 pass
+// before the first product starts, 3 and 2.8 in the products, 3.8 in the exchange of parts, 2.4 between the last row of h and
+// the sight of it. There, proxy fences for all memory instead of global memory alone had cost 2 us more.
 //
 // Roles per CTA: warp 0 loads (TMA), warp 1 allocates TMEM and, in the leader, issues the products, warps 2..9 are the epilogue
 // (sixteen warps of 96 registers were slower: 1474 against 1400 us for the three products at 8192 x 4096 x 8192).
 // Every wait is bounded (0.2 s): on timeout the kernel records MOE_ERR_DEVICE_TIMEOUT, lets copies in flight land, frees
 // TMEM and leaves.
 //
-// Measured (bf16, T x d x f): 8192 x 4096 x 8192 forward 0.86 ms, backward 1.73 ms each alone at full clocks (1.91 PFLOP/s), a step
-// under the power cap 2.73-2.8 ms; 8192 x 2048 x 1024 forward 72 us, backward 126 us, a step 202 us (1.53 PFLOP/s): per tile the
-// products take 8.6 us, but bursts of h, a, b and da, db from all pairs at once take 4-7 us of HBM's time each.
+// Measured (bf16, T x d x f): 8192 x 4096 x 8192 with 8 bits kept, forward 0.87 ms, backward 1.73-1.78 ms each alone at full
+// clocks (1.91 PFLOP/s; the tensor pipe is busy 89% of the time), a step under the power cap 2.95-3.05 ms (1.65 PFLOP/s, of 1.75
+// that a long library product holds); 8192 x 2048 x 1024 forward 67 us, backward 126-130 us (tensor pipe 67% and 74%), a step
+// 196 us in short runs and 214 under the cap: per tile the products take 8.6 us, but bursts of h, a, b and da, db from all pairs
+// at once take 4-7 us of HBM's time each, and each launch 2.7 us to its first product and 3 us from its last.
 #include <cuda.h>
 
 #include <string.h>
@@ -192,7 +197,8 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
 }
 
-// mbar_wait_cluster in place: across a call, what a warp has asked for ahead would be stored to the stack first, and so waited for
+// mbar_wait_cluster in place: across a call, what a warp has asked for ahead would be stored to the stack first, and so waited
+// for
 __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int *abort_flag, WsHeader *hdr, int where) {
   const uint64_t t0 = global_ns();
   for (uint32_t i = 0;; ++i) {
@@ -263,10 +269,11 @@ struct Rows {
 };
 
 // Blocks on their way out and in. A warp holds 32 rows, one per lane; global memory wants consecutive bytes of a row from
-// neighbouring lanes. Blocks therefore pass through shared memory, W = 64 columns wide (128 bytes a row, eight lanes) or 32
-// (64 bytes, four lanes), 16-byte chunks XOR-swizzled so that neither side meets bank conflicts. (Straight from a row per lane,
-// 32 bytes each, needs no shared memory, but 32 lines per instruction slow the ring's own copies: 38 against 33 us for y at
-// 8192 x 2048 x 1024, 52 against 43 for da, db.) Rows from `rows` and columns from `cols` on are left out, and read as zero.
+// neighbouring lanes. Blocks therefore pass through shared memory, W = 64 columns wide (128 bytes a row, eight lanes) or 32 (64
+// bytes, four lanes), 16-byte chunks XOR-swizzled so that neither side meets bank conflicts. (Straight from a row per lane, 32
+// bytes each, needs no shared memory, but 32 lines per instruction slow the ring's own copies: in launches of their own 38
+// against 33 us for y at 8192 x 2048 x 1024, 52 against 43 for da, db.) Rows from `rows` and columns from `cols` on are left
+// out, and read as zero.
 template <int W> struct Chunk {
   static constexpr int LANES = W / 8, STEP = 32 / LANES, N = W / 8;   // lanes per row, rows per instruction, instructions
   static __device__ __forceinline__ uint32_t at(uint32_t buf, int row, int chunk) {
@@ -446,8 +453,9 @@ template <bool CUBIC> __device__ __forceinline__ void back16(float *a, float *b,
   }
 }
 
-// What becomes of the warp's slice: rows row0 .. row0 + 31 (a lane each), width / 2 columns from col0 on (GATEUP: width / 4 features). Sixteen
-// columns at a time in loops that stay loops: unrolled, most of the time of a first (or only) tile went into fetching the code.
+// What becomes of the warp's slice: rows row0 .. row0 + 31 (a lane each), width / 2 columns from col0 on (GATEUP: width / 4
+// features). Sixteen columns at a time in loops that stay loops: unrolled, most of the time of a first (or only) tile went into
+// fetching the code.
 template <int K>
 __device__ __forceinline__ void finish(const Slice<K> &acc, Ahead<K> &ahead, const Params &p, const Product &o, uint32_t buf, int lane,
                                        int row0, int col0) {
@@ -943,10 +951,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 }
 
 // ----------------------------------------------------------------------------- host side -------
-// How a product is cut up: tiles of 256 or 128 columns, and along K. The costs are in units of 0.065 us, as measured at 389 x 2048 x
-// 1024 and 256 x 4096 x 2048: a k-block takes 0.26 us at 256 columns and 0.19 at 128 (the copies bound both), the last
-// epilogue 2-3 us or 1.2; a part, that leaves its fp32 accumulators, waits for the others' and adds up its share of them, 5.6
-// or 4.
+// How a product is cut up: tiles of 256 or 128 columns, and along K. The costs are in units of 0.065 us, as measured at 389 x
+// 2048 x 1024 and 256 x 4096 x 2048: a k-block takes 0.26 us at 256 columns and 0.19 at 128 (the copies bound both), the last
+// epilogue 2-3 us or 1.2; a part, that leaves its fp32 accumulators, waits for the others' and adds up its share of them, 5.6 or
+// 4.
 struct Plan {
   int width, splits;
 };
@@ -1002,9 +1010,9 @@ template <auto KERNEL> static int pairs_resident(int &pairs) {
 // The counters in front of the parts: for cut tiles, then pairs that are done (one line), then rows of tiles.
 static size_t counter_bytes(int64_t T) { return kArrivedBytes + 128 + (size_t)up(up(T, TILE), 32) * 128; }
 
-// How the products' tiles are dealt to the pairs, product after product (in p.deal's order): parts of cut tiles in turn, whole tiles each
-// to the pair with the least work so far (whole rounds at once, but for the last two). What waits for a first product of one
-// round waits for all of it.
+// How the products' tiles are dealt to the pairs, product after product (in p.deal's order): parts of cut tiles in turn, whole
+// tiles each to the pair with the least work so far (whole rounds at once, but for the last two). What waits for a first product
+// of one round waits for all of it.
 static void deal_out(Params &p, int pairs) {
   int64_t load[MAX_PAIRS] = {};
   memset(p.count, 0, sizeof(p.count));
@@ -1140,10 +1148,10 @@ int gemm_fwd(const Block &b, cudaStream_t s) {
   return start<FWD>(m, p, b, s);
 }
 
-// Backward: da, db (and h, from 8 bits), then dx = dab Wgu (+ dx_in), dWd = dy^T h and dWgu = dab^T x, in one launch. dx waits for
-// the rows of dab that it reads, which are there first, dWgu for all of them, dWd for nothing (for all rows of h where those
-// are written here): it is taken first then, by the pairs that the first product leaves with the least work. The longer
-// tiles are dealt out before the shorter ones, which even out what those leave.
+// Backward: da, db (and h, from 8 bits), then dx = dab Wgu (+ dx_in), dWd = dy^T h and dWgu = dab^T x, in one launch. dx waits
+// for the rows of dab that it reads, which are there first, dWgu for all of them, dWd for nothing (for all rows of h where those
+// are written here): it is taken first then, by the pairs that the first product leaves with the least work. The longer tiles
+// are dealt out before the shorter ones, which even out what those leave.
 int gemm_bwd(const Block &b, cudaStream_t s) {
   const uint64_t T = b.T, d = b.d, f = b.f;
   // the last three run beside one another: narrow tiles where they give every pair one at most

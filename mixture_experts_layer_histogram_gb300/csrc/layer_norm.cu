@@ -11,13 +11,13 @@
 //
 // HBM-bound, like the RMS norms (norm.cu): a thread block works on one row at a time, read once through the ring of rows and
 // written once; codes come through the ring as well, 8 (fp32: 4) bytes per thread beside its 16-byte vectors. Where the forward
-// needs two reductions per row (the deviations wait for the mean), the blocks that share an SM cover for one another.
-// The weight gradients are summed over a block's rows in registers and its partial rows added up in a fixed order.
-// Measured (bf16): backward with dx_in at T = 16384, d = 4096 96.5 us (537 MB, 5.6 TB/s); at T = 8192, d = 2048 forward with codes
-// 22.5 us (84 MB), restore 11.4 us (51 MB), backward from codes 25 us (118 MB) and 4.8 us for the partial rows; fp32 T = 1023,
-// d = 1537 backward 9.7 and 4.8 us; four rows of 2048 3.5 us. Before dn and z stayed in registers between the backward's
-// two passes it took 100.5 us. The forward takes the same time with two vectors per thread and with a warp per row (fewer
-// instructions, no barriers): 84 MB are too few to fill and drain the memory system for.
+// needs two reductions per row (the deviations wait for the mean), the blocks that share an SM cover for one another. The weight
+// gradients are summed over a block's rows in registers and its partial rows added up in a fixed order. Measured (bf16):
+// backward with dx_in at T = 16384, d = 4096 96.5 us (537 MB, 5.6 TB/s); at T = 8192, d = 2048 forward with codes 22.5 us (84
+// MB), restore 11.4 us (51 MB), backward from codes 25 us (118 MB) and 4.8 us for the partial rows; fp32 T = 1023, d = 1537
+// backward 9.7 and 4.8 us; four rows of 2048 3.5 us. Before dn and z stayed in registers between the backward's two passes it
+// took 100.5 us. The forward takes the same time with two vectors per thread and with a warp per row (fewer instructions, no
+// barriers): 84 MB are too few to fill and drain the memory system for.
 #include "act8.cuh"
 #include "raw16.cuh"
 #include "row_ring.cuh"
