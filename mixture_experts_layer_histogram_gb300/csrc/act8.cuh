@@ -16,6 +16,12 @@ constexpr int kBlock = 32;   // values per scale
 
 __host__ __device__ __forceinline__ int64_t blocks_of(int64_t K) { return (K + kBlock - 1) / kBlock; }
 
+// The largest magnitude of three values; a NaN stays one
+__device__ __forceinline__ float larger(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Scale byte of a block whose largest magnitude has the fp32 bits `amax` (sign clear). NaN bits are the largest
 // integers, so an integer maximum carries a NaN through, and a block that is not finite gets 255.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {

@@ -356,10 +356,10 @@ __device__ __forceinline__ void unpack_codes(const uint4 &w, float scale, float 
 
 // 32 values, one whole block, to their codes and scale
 __device__ __forceinline__ void put_block8(uint8_t *codes, uint8_t *scale, const float *v) {
-  uint32_t top = 0;
+  float top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-  const uint32_t byte = act8::scale_byte(top);
+  for (int i = 0; i < 32; i += 2) top = act8::larger(top, v[i], v[i + 1]);
+  const uint32_t byte = act8::scale_byte(__float_as_uint(top));
   const float inv = act8::inv_scale(byte);
   uint32_t w[8];
 #pragma unroll

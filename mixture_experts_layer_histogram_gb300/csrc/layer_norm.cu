@@ -9,15 +9,16 @@
 // place of the 64 that x takes in bf16); restore() gives z w + b again for the block's own backward, and
 // the backward reads z from the codes.
 //
-// HBM-bound, like the RMS norms (norm.cu): a thread block works on one row at a time, read once through the ring of rows and
-// written once; codes come through the ring as well, 8 (fp32: 4) bytes per thread beside its 16-byte vectors. Where the forward
-// needs two reductions per row (the deviations wait for the mean), the blocks that share an SM cover for one another. The weight
-// gradients are summed over a block's rows in registers and its partial rows added up in a fixed order. Measured (bf16):
-// backward with dx_in at T = 16384, d = 4096 96.5 us (537 MB, 5.6 TB/s); at T = 8192, d = 2048 forward with codes 22.5 us (84
-// MB), restore 11.4 us (51 MB), backward from codes 25 us (118 MB) and 4.8 us for the partial rows; fp32 T = 1023, d = 1537
-// backward 9.7 and 4.8 us; four rows of 2048 3.5 us. Before dn and z stayed in registers between the backward's two passes it
-// took 100.5 us. The forward takes the same time with two vectors per thread and with a warp per row (fewer instructions, no
-// barriers): 84 MB are too few to fill and drain the memory system for.
+// HBM-bound, like the RMS norms (norm.cu): a thread block works on one row at a time (forward: on two, which share the two
+// reductions that a row needs, the deviations waiting for the mean), read once through the ring of rows and written once; codes
+// come through the ring as well, 8 (fp32: 4) bytes per thread beside its 16-byte vectors. The weight gradients are summed over a
+// block's rows in registers and its partial rows added up in a fixed order.
+// Measured (bf16, in replayed graphs): T = 8192, d = 2048 forward 16.1 us (67 MB), with codes 20.1 (84 MB, 75% of the issue
+// slots busy before the two rows shared their sums), restore 8.3 (51 MB), backward with dx_in 25.6 from x or codes (135 or 118
+// MB); T = 16384, d = 4096 forward 57.9, backward with dx_in 89 (537 MB, 6.0 TB/s; 96 in a stream of calls with other inputs
+// each time); fp32 T = 1023, d = 1537 backward 10.1 us; four rows of 2048 2.3 and 4.0 us. Before dn and z stayed in registers
+// between the backward's two passes it took 4% longer. One row at a time, two vectors per thread or a warp per row (fewer
+// instructions, no barriers) took the forward the same time as one another, 18.6 us.
 #include "act8.cuh"
 #include "raw16.cuh"
 #include "row_ring.cuh"
@@ -71,11 +72,11 @@ template <int VEC> __device__ __forceinline__ uint32_t block_amax(uint32_t m) {
   for (int off = 1; off < act8::kBlock / VEC; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
   return m;
 }
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-__device__ __forceinline__ uint32_t magnitude(F2 v) {
+__device__ __forceinline__ float larger(float top, float v) { return act8::larger(top, v, 0.0f); }
+__device__ __forceinline__ float larger(float top, F2 v) {
   float x, y;
   split(v, x, y);
-  return max(magnitude(x), magnitude(y));
+  return act8::larger(top, x, y);
 }
 // The codes of N lanes of values times `inv`, written to p (VEC bytes)
 __device__ __forceinline__ void put_codes(uint8_t *p, const F2 (&v)[4], float inv) {
@@ -138,12 +139,12 @@ __device__ __forceinline__ void statistics(const LnFwdParams &p, int64_t row, fl
 // Vector v of a row's normalised values to its codes (and, from the first thread of a block of 32 values, the scale)
 template <int VEC, typename L, int N>
 __device__ __forceinline__ void keep(const LnFwdParams &p, int64_t row, int v, bool has, const L (&z)[N]) {
-  uint32_t top = 0;
+  float top = 0.0f;
   if (has) {
 #pragma unroll
-    for (int c = 0; c < N; ++c) top = max(top, magnitude(z[c]));
+    for (int c = 0; c < N; ++c) top = larger(top, z[c]);
   }
-  const uint32_t byte = act8::scale_byte(block_amax<VEC>(top));
+  const uint32_t byte = act8::scale_byte(block_amax<VEC>(__float_as_uint(top)));
   if (!has) return;
   uint8_t *q = p.codes + row * p.d + (int64_t)v * VEC;
   if (byte == 255u) {
@@ -155,7 +156,8 @@ __device__ __forceinline__ void keep(const LnFwdParams &p, int64_t row, int v, b
   if (v * VEC % act8::kBlock == 0) p.scales[row * p.nb + v * VEC / act8::kBlock] = (uint8_t)byte;
 }
 
-template <typename T, int VEC, int ITER, bool KEEP>
+// ROWS: rows that a block takes at a time, which share the reductions' exchanges and barriers.
+template <typename T, int VEC, int ITER, bool KEEP, int ROWS>
 __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(const LnFwdParams p, const Geometry geom) {
   using V = Lanes<T, VEC, float>;
   using L = typename V::L;
@@ -167,11 +169,15 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
   int half = 0;
   const float inv_d = 1.0f / (float)p.d;
   clear(sums);
+  // The rows of one turn lie gridDim.x apart.
+  const int64_t turn = (int64_t)ROWS * gridDim.x;
   auto fetch = [&](int64_t row, int stage) {
-    if (row < p.T) ring.fetch(p.x, ring.offset(row), stage, 0);
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j, row += gridDim.x)
+      if (row < p.T) ring.fetch(p.x, ring.offset(row), stage, j);
     ring.commit();
   };
-  for (int s = 0; s < ring.stages - 1; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  for (int s = 0; s < ring.stages - 1; ++s) fetch(blockIdx.x + s * turn, s);
   auto weights = [&](int v, L *w, L *b) {
     V::load((const T *)p.w + (int64_t)v * VEC, w);
     if (p.b) {
@@ -188,58 +194,83 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
       if (ring.has(i)) weights(threadIdx.x + i * blockDim.x, hold_w[kHold ? i : 0], hold_b[kHold ? i : 0]);
   }
   int stage = 0;
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+  for (int64_t row = blockIdx.x; row < p.T; row += turn) {
     if (ring.stages == 1) {
-      if (VEC == 1) __syncthreads();   // every thread has left the row before
+      if (VEC == 1) __syncthreads();   // every thread has left the rows before
       fetch(row, 0);
     }
     ring.wait();
-    const int64_t off = ring.offset(row);
-    const uint32_t here = ring.at(stage, off);
-    L o[ITER][N], s = splat<L>(0.0f);
+    L o[ROWS][ITER][N];
+    float m[ROWS];
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      if (!ring.has(i)) continue;
-      V::load_shared(here + i * ring.step, o[i]);
+    for (int j = 0; j < ROWS; ++j) {
+      L s = splat<L>(0.0f);
+      if (j == 0 || row + j * gridDim.x < p.T) {
+        const uint32_t here = ring.at(stage, ring.offset(row + j * gridDim.x)) + j * ring.row_bytes;
 #pragma unroll
-      for (int c = 0; c < N; ++c) s = add(s, o[i][c]);
-    }
-    // the row is in registers: the stage of the row before it may be overwritten
-    if (ring.stages > 1) fetch(row + (int64_t)(ring.stages - 1) * gridDim.x, ring.freed(stage));
-    const float m = block_sum(total(s), sums, half) * inv_d;
-    L s1 = splat<L>(0.0f), s2 = splat<L>(0.0f);
-    const L minus = splat<L>(-m);
+        for (int i = 0; i < ITER; ++i) {
+          if (!ring.has(i)) continue;
+          V::load_shared(here + i * ring.step, o[j][i]);
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      if (!ring.has(i)) continue;
+          for (int c = 0; c < N; ++c) s = add(s, o[j][i][c]);
+        }
+      } else {
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        o[i][c] = add(o[i][c], minus);
-        s1 = add(s1, o[i][c]);
-        s2 = fma(o[i][c], o[i][c], s2);
+        for (int i = 0; i < ITER; ++i) {
+#pragma unroll
+          for (int c = 0; c < N; ++c) o[j][i][c] = splat<L>(0.0f);
+        }
       }
+      m[j] = total(s);
     }
-    float t[2] = {total(s1), total(s2)};
+    // the rows are in registers: the stage of those before them may be overwritten
+    if (ring.stages > 1) fetch(row + (ring.stages - 1) * turn, ring.freed(stage));
+    if constexpr (ROWS == 1) m[0] = block_sum(m[0], sums, half);
+    else block_sums(m, sums, half);
+    float t[2 * ROWS];   // sums of the deviations (what the rounding of m left), and of their squares
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      m[j] *= inv_d;
+      L s1 = splat<L>(0.0f), s2 = splat<L>(0.0f);
+      const L minus = splat<L>(-m[j]);
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        if (!ring.has(i)) continue;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          o[j][i][c] = add(o[j][i][c], minus);
+          s1 = add(s1, o[j][i][c]);
+          s2 = fma(o[j][i][c], o[j][i][c], s2);
+        }
+      }
+      t[2 * j] = total(s1);
+      t[2 * j + 1] = total(s2);
+    }
     block_sums(t, sums, half);
-    const float rest = t[0] * inv_d;                    // what the rounding of m left
-    float r;
-    statistics(p, row, m, rest, t[1], inv_d, threadIdx.x == 0, r);
-    const L R = splat<L>(r), shift = splat<L>(-rest);
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (ring.has(i)) {
+    for (int j = 0; j < ROWS; ++j) {
+      const int64_t r_ = row + j * gridDim.x;
+      if (j > 0 && r_ >= p.T) break;
+      const float rest = t[2 * j] * inv_d;
+      float r;
+      statistics(p, r_, m[j], rest, t[2 * j + 1], inv_d, threadIdx.x == 0, r);
+      const L R = splat<L>(r), shift = splat<L>(-rest * r);
 #pragma unroll
-        for (int c = 0; c < N; ++c) o[i][c] = mul(add(o[i][c], shift), R);
+      for (int i = 0; i < ITER; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (ring.has(i)) {
+#pragma unroll
+          for (int c = 0; c < N; ++c) o[j][i][c] = fma(o[j][i][c], R, shift);
+        }
+        if (KEEP) keep<VEC>(p, r_, v, ring.has(i), o[j][i]);
+        if (!ring.has(i)) continue;
+        L(&w)[N] = hold_w[kHold ? i : 0], (&b)[N] = hold_b[kHold ? i : 0];
+        if (!kHold) weights(v, w, b);
+#pragma unroll
+        for (int c = 0; c < N; ++c) o[j][i][c] = fma(o[j][i][c], w[c], b[c]);
+        V::store(reinterpret_cast<T *>((uint8_t *)p.n + ring.offset(r_) + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step),
+                 o[j][i]);
       }
-      if (KEEP) keep<VEC>(p, row, v, ring.has(i), o[i]);
-      if (!ring.has(i)) continue;
-      L(&w)[N] = hold_w[kHold ? i : 0], (&b)[N] = hold_b[kHold ? i : 0];
-      if (!kHold) weights(v, w, b);
-#pragma unroll
-      for (int c = 0; c < N; ++c) o[i][c] = fma(o[i][c], w[c], b[c]);
-      V::store(reinterpret_cast<T *>((uint8_t *)p.n + off + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step),
-               o[i]);
     }
     if (++stage == ring.stages) stage = 0;
   }
@@ -546,10 +577,21 @@ __global__ void __launch_bounds__(kRestoreThreads) ln_restore_kernel(const uint8
 }
 
 template <typename T, int VEC, int ITER> static int ln_launch_fwd(const LnFwdParams &p, const Shape &sh, cudaStream_t s) {
-  int64_t grid = (int64_t)sm_count() * per_sm(sh, 1, sh.iter == 1 ? 2 * kMaxThreads : kMaxThreads);
+  const int threads = sh.iter == 1 ? 2 * kMaxThreads : kMaxThreads;
+  int64_t grid = (int64_t)sm_count() * per_sm(sh, 1, threads);
+  // Two rows at a time where a thread has one vector of each and blocks have more rows than one: 16.4 against 18.6 us at T =
+  // 8192, d = 2048 bf16, 58.6 against 71.9 at 16384 x 4096; for four rows 2.5 against 2.3 (nothing is shared then).
+  if constexpr (VEC > 1 && ITER == 1) {
+    if (p.T > grid) {
+      grid = (int64_t)sm_count() * per_sm(sh, 2, threads);
+      if (grid > p.T) grid = p.T;
+      if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true, 2>>(p, sh, 2, (int)grid, s);
+      return launch<ln_fwd_kernel<T, VEC, ITER, false, 2>>(p, sh, 2, (int)grid, s);
+    }
+  }
   if (grid > p.T) grid = p.T;
-  if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true>>(p, sh, 1, (int)grid, s);
-  return launch<ln_fwd_kernel<T, VEC, ITER, false>>(p, sh, 1, (int)grid, s);
+  if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true, 1>>(p, sh, 1, (int)grid, s);
+  return launch<ln_fwd_kernel<T, VEC, ITER, false, 1>>(p, sh, 1, (int)grid, s);
 }
 template <typename T, int VEC, int ITER, typename S = float>
 static int ln_launch_bwd(const LnBwdParams &p, const Shape &sh, int grid, cudaStream_t s) {
