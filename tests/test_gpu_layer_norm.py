@@ -151,6 +151,25 @@ def test_rows_that_overflow_and_rows_that_are_not_finite(d, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,d", [(2431, 1024), (1300, 2048), (611, 4096)])
+def test_many_rows_some_not_finite(T, d, dtype):
+    """Rows that share a block's reductions: what stands in one changes no bit of the others, whatever their number."""
+    s = make(T, d, dtype, T)
+    x, bad = s["x"].clone(), torch.arange(5, T, 7, device="cuda")
+    x[bad] = float("nan")
+    ok = torch.ones(T, dtype=torch.bool, device="cuda")
+    ok[bad] = False
+    m, r = stats(s["x"])
+    for keep in (None, "f8"):
+        nm, ref = LayerNorm(T, d, dtype, eps=EPS, keep=keep), LayerNorm(T, d, dtype, eps=EPS, keep=keep)
+        n, want = nm.forward(x, s["w"], s["b"]), ref.forward(s["x"], s["w"], s["b"])
+        close(want, (s["x"].double() - m) * r * s["w"].double() + s["b"].double(), ("n", dtype))
+        assert torch.equal(n[ok], want[ok]) and n[bad].isnan().all() and torch.equal(nm.rstd[ok], ref.rstd[ok])
+        if keep:
+            assert torch.equal(nm.codes[ok], ref.codes[ok]) and nm.codes[bad].eq(0).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_no_tokens(dtype):
     for keep in (None, "f8"):
         nm = LayerNorm(0, 96, dtype, keep=keep)
