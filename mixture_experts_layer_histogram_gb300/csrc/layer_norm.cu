@@ -9,16 +9,15 @@
 // place of the 64 that x takes in bf16); restore() gives z w + b again for the block's own backward, and
 // the backward reads z from the codes.
 //
-// HBM-bound, like the RMS norms (norm.cu): a thread block works on one row at a time (forward: on two, which share the two
-// reductions that a row needs, the deviations waiting for the mean), read once through the ring of rows and written once; codes
+// HBM-bound, like the RMS norms (norm.cu): a thread block works on one row at a time, or on two, which share their reductions (the
+// forward needs two per row, the deviations waiting for the mean), read once through the ring of rows and written once; codes
 // come through the ring as well, 8 (fp32: 4) bytes per thread beside its 16-byte vectors. The weight gradients are summed over a
 // block's rows in registers and its partial rows added up in a fixed order.
-// Measured (bf16, in replayed graphs): T = 8192, d = 2048 forward 16.1 us (67 MB), with codes 20.1 (84 MB, 75% of the issue
-// slots busy before the two rows shared their sums), restore 8.3 (51 MB), backward with dx_in 25.6 from x or codes (135 or 118
-// MB); T = 16384, d = 4096 forward 57.9, backward with dx_in 89 (537 MB, 6.0 TB/s; 96 in a stream of calls with other inputs
-// each time); fp32 T = 1023, d = 1537 backward 10.1 us; four rows of 2048 2.3 and 4.0 us. Before dn and z stayed in registers
-// between the backward's two passes it took 4% longer. One row at a time, two vectors per thread or a warp per row (fewer
-// instructions, no barriers) took the forward the same time as one another, 18.6 us.
+// Measured (bf16, in replayed graphs): T = 8192, d = 2048 forward 16.1 us (67 MB), with codes 20.1 (84 MB), restore 8.3 (51 MB),
+// backward with dx_in 25.7 from x or codes (135 or 118 MB); T = 16384, d = 4096 forward 57.9, backward with dx_in 86.8 (537 MB,
+// 6.2 TB/s; 94 in a stream of calls with other inputs each time), from codes 84.8; fp32 T = 1023, d = 1537 backward 10.2 us; four
+// rows of 2048 2.3 and 4.0 us. Before dn and z stayed in registers between the backward's two passes it took 4% longer. Two
+// vectors per thread or a warp per row (fewer instructions, no barriers) took the forward as long as one row at a time, 18.6 us.
 #include "act8.cuh"
 #include "raw16.cuh"
 #include "row_ring.cuh"
@@ -289,30 +288,37 @@ struct LnBwdParams {
 
 // S: float, or double for rows of at most 32 values, where u - mean(u) - z mean(u z) all but cancels (in a row of one or two
 // values what is left is of the order of eps): such rows are computed in 64 bits from x itself, its statistics too.
-template <typename T, int VEC, int ITER, bool KEPT, typename S>
+// ROWS: rows that a block takes at a time, as in the forward.
+template <typename T, int VEC, int ITER, bool KEPT, typename S, int ROWS>
 __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln_bwd_kernel(const LnBwdParams p, const Geometry geom) {
   using V = Lanes<T, VEC, S>;
   using L = typename V::L;
   constexpr int N = V::N;
   constexpr bool kWide = sizeof(S) == 8;
   constexpr bool kHold = ITER * VEC <= 16 && ITER <= 4;
-  constexpr int kDn = 0, kX = 1, kIn = 2;    // buffers of a stage; kX holds the codes where they are copied
+  static_assert(ROWS == 1 || (VEC > 1 && kHold), "several rows at a time stay in registers");
+  constexpr int kDn = 0, kX = 1, kIn = 2;    // a row's buffers in a stage; kX holds the codes where they are copied
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ SumBuf sums;
   const Ring<T, VEC, ITER> ring(dyn, geom, p.T, p.d);
   int half = 0;
   const S inv_d = S(1) / (S)p.d;
   const bool has_in = p.dx_in != nullptr;
+  const int per_row = has_in ? 3 : 2;
   const uint32_t codes_at = VEC > 1 ? (uint32_t)kX * ring.row_bytes - (16u - VEC) * threadIdx.x : 0u;   // from ring.mine
   clear(sums);
+  const int64_t turn = (int64_t)ROWS * gridDim.x;   // the rows of one turn lie gridDim.x apart
   auto fetch = [&](int64_t row, int stage) {
-    if (row < p.T) {
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j, row += gridDim.x) {
+      if (row >= p.T) break;
       const int64_t off = ring.offset(row);
-      ring.fetch(p.dn, off, stage, kDn);
+      const int at = j * per_row;
+      ring.fetch(p.dn, off, stage, at + kDn);
       if (!KEPT) {
-        ring.fetch(p.x, off, stage, kX);
+        ring.fetch(p.x, off, stage, at + kX);
       } else if (VEC > 1) {   // VEC bytes per vector, copied by the thread that reads them
-        const uint32_t dst = ring.mine + (uint32_t)stage * ring.stage_bytes + codes_at;
+        const uint32_t dst = ring.mine + (uint32_t)stage * ring.stage_bytes + codes_at + at * ring.row_bytes;
         const uint8_t *src = p.codes + row * p.d + VEC * threadIdx.x;
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
                          : "memory");
         }
       }
-      if (has_in) ring.fetch(p.dx_in, off, stage, kIn);
+      if (has_in) ring.fetch(p.dx_in, off, stage, at + kIn);
     }
     ring.commit();
   };
@@ -332,45 +338,53 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
 #pragma unroll
     for (int c = 0; c < N; ++c) acc_w[i][c] = acc_b[i][c] = splat<L>(0.0f);
   }
-  for (int s = 0; s < ring.stages - 1; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  for (int s = 0; s < ring.stages - 1; ++s) fetch(blockIdx.x + s * turn, s);
   L hold_w[kHold ? ITER : 1][N];
   if (kHold) {
 #pragma unroll
     for (int i = 0; i < ITER; ++i)
       if (ring.has(i)) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, hold_w[kHold ? i : 0]);
   }
-  // the row's statistics, and the scales of this thread's codes, are read one row ahead
-  float next_m = 0.0f, next_r = 0.0f;
-  uint8_t next_s[KEPT ? ITER : 1];
+  // the rows' statistics, and the scales of this thread's codes, are read one turn ahead
+  float next_m[ROWS] = {}, next_r[ROWS] = {};
+  uint8_t next_s[ROWS][KEPT ? ITER : 1] = {};
   auto ahead = [&](int64_t row) {
-    if (row >= p.T) return;
-    if (!KEPT) next_m = p.mean[row];
-    next_r = p.rstd[row];
-    if (KEPT) {
 #pragma unroll
-      for (int i = 0; i < ITER; ++i)
-        if (ring.has(i)) next_s[KEPT ? i : 0] = p.scales[row * p.nb + (int)(threadIdx.x + i * blockDim.x) * VEC / act8::kBlock];
+    for (int j = 0; j < ROWS; ++j, row += gridDim.x) {
+      if (row >= p.T) break;
+      if (!KEPT) next_m[j] = p.mean[row];
+      next_r[j] = p.rstd[row];
+      if (KEPT) {
+#pragma unroll
+        for (int i = 0; i < ITER; ++i)
+          if (ring.has(i)) next_s[j][KEPT ? i : 0] = p.scales[row * p.nb + (int)(threadIdx.x + i * blockDim.x) * VEC / act8::kBlock];
+      }
     }
   };
   ahead(blockIdx.x);
   int stage = 0;
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+  for (int64_t row = blockIdx.x; row < p.T; row += turn) {
     if (ring.stages == 1) {
-      if (VEC == 1) __syncthreads();   // every thread has left the row before
+      if (VEC == 1) __syncthreads();   // every thread has left the rows before
       fetch(row, 0);
     }
-    S m = next_m, r = next_r;
-    float sc[KEPT ? ITER : 1];
-    if (KEPT) {
+    S m[ROWS], r[ROWS];
+    float sc[ROWS][KEPT ? ITER : 1];
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) sc[KEPT ? i : 0] = act8::scale_value(next_s[KEPT ? i : 0]);
+    for (int j = 0; j < ROWS; ++j) {
+      m[j] = next_m[j];
+      r[j] = next_r[j];
+      if (KEPT) {
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) sc[j][KEPT ? i : 0] = act8::scale_value(next_s[j][KEPT ? i : 0]);
+      }
     }
-    ahead(row + gridDim.x);
+    ahead(row + turn);
     ring.wait();
-    // every thread has left the row before (its own vectors: the thread itself; windows: the barrier in wait())
-    if (ring.stages > 1) fetch(row + (int64_t)(ring.stages - 1) * gridDim.x, ring.freed(stage));
-    const int64_t off = ring.offset(row);
-    const uint32_t here = ring.at(stage, off);
+    // every thread has left the rows before (its own vectors: the thread itself; windows: the barrier in wait())
+    if (ring.stages > 1) fetch(row + (ring.stages - 1) * turn, ring.freed(stage));
+    const int64_t off0 = ring.offset(row);
+    const uint32_t here = ring.at(stage, off0);
     const uint32_t codes_here = ring.mine + (uint32_t)stage * ring.stage_bytes + codes_at;
     if constexpr (kWide && !KEPT) {   // one value per lane
       S t[1] = {S(0)};
@@ -379,78 +393,90 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
       if (ring.has(0)) V::load_shared(here + kX * ring.row_bytes, x);
       t[0] = x[0];
       block_sums(t, sums, half);
-      m = t[0] * inv_d;
-      t[0] = ring.has(0) ? (x[0] - m) * (x[0] - m) : S(0);
+      m[0] = t[0] * inv_d;
+      t[0] = ring.has(0) ? (x[0] - m[0]) * (x[0] - m[0]) : S(0);
       block_sums(t, sums, half);
-      r = S(1) / sqrt(t[0] * inv_d + (S)p.eps);
+      r[0] = S(1) / sqrt(t[0] * inv_d + (S)p.eps);
     }
-    // z (without KEPT: before the rest of the mean is taken off) of the i-th vector
-    auto normed = [&](int i, L (&z)[N]) {
+    // z (without KEPT: before the rest of the mean is taken off) of the i-th vector of the j-th row
+    auto normed = [&](int j, int i, L (&z)[N]) {
       if constexpr (KEPT) {
         if constexpr (VEC > 1) {
-          get_codes(codes_here + i * VEC * blockDim.x, z, sc[i]);
+          get_codes(codes_here + j * per_row * ring.row_bytes + i * VEC * blockDim.x, z, sc[j][i]);
         } else {
-          z[0] = (S)(act8::unpack1(p.codes[row * p.d + threadIdx.x + (int64_t)i * blockDim.x]) * sc[i]);
+          z[0] = (S)(act8::unpack1(p.codes[row * p.d + threadIdx.x + (int64_t)i * blockDim.x]) * sc[j][i]);
         }
       } else {
-        V::load_shared(here + kX * ring.row_bytes + i * ring.step, z);
+        V::load_shared(here + (j * per_row + kX) * ring.row_bytes + i * ring.step, z);
 #pragma unroll
-        for (int c = 0; c < N; ++c) z[c] = mul(add(z[c], all(-m, L())), all(r, L()));
+        for (int c = 0; c < N; ++c) z[c] = mul(add(z[c], all(-m[j], L())), all(r[j], L()));
       }
     };
     // sums of u, u z, z; with few vectors per thread dn and z stay in registers for the second pass
-    L hold_d[kHold ? ITER : 1][N], hold_z[kHold ? ITER : 1][N];
-    L t[3];
+    constexpr int SUMS = KEPT ? 2 : 3;
+    L hold_d[ROWS][kHold ? ITER : 1][N], hold_z[ROWS][kHold ? ITER : 1][N];
+    S s[SUMS * ROWS];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) t[i] = splat<L>(0.0f);
+    for (int j = 0; j < ROWS; ++j) {
+      L t[3];
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      if (!ring.has(i)) continue;
-      L(&w)[N] = hold_w[kHold ? i : 0];
-      if (!kHold) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, w);
-      L(&u)[N] = hold_d[kHold ? i : 0], (&z)[N] = hold_z[kHold ? i : 0];
-      V::load_shared(here + kDn * ring.row_bytes + i * ring.step, u);
-      normed(i, z);
+      for (int i = 0; i < 3; ++i) t[i] = splat<L>(0.0f);
+      if (j == 0 || row + j * gridDim.x < p.T) {
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        acc_b[i][c] = add(acc_b[i][c], u[c]);
-        const L uw = mul(u[c], w[c]);
-        t[0] = add(t[0], uw);
-        t[1] = fma(uw, z[c], t[1]);
-        if (!KEPT) t[2] = add(t[2], z[c]);
+        for (int i = 0; i < ITER; ++i) {
+          if (!ring.has(i)) continue;
+          L(&w)[N] = hold_w[kHold ? i : 0];
+          if (!kHold) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, w);
+          L(&u)[N] = hold_d[j][kHold ? i : 0], (&z)[N] = hold_z[j][kHold ? i : 0];
+          V::load_shared(here + (j * per_row + kDn) * ring.row_bytes + i * ring.step, u);
+          normed(j, i, z);
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            acc_b[i][c] = add(acc_b[i][c], u[c]);
+            const L uw = mul(u[c], w[c]);
+            t[0] = add(t[0], uw);
+            t[1] = fma(uw, z[c], t[1]);
+            if (!KEPT) t[2] = add(t[2], z[c]);
+          }
+        }
       }
+#pragma unroll
+      for (int i = 0; i < SUMS; ++i) s[SUMS * j + i] = total(t[i]);
     }
-    S s[3];
+    if constexpr (SUMS * ROWS == 6) block_sum6(s, sums, half);
+    else block_sums(s, sums, half);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) s[i] = total(t[i]);
-    block_sums(s, sums, half);
-    const S rest = KEPT ? S(0) : s[2] * inv_d;             // of z's mean, which is zero
-    const S mu = s[0] * inv_d, muz = (s[1] - rest * s[0]) * inv_d;
-    const L R = all(r, L()), Rest = all(-rest, L()), Mu = all(-mu, L()), Muz = all(-muz, L());
+    for (int j = 0; j < ROWS; ++j) {
+      if (j > 0 && row + j * gridDim.x >= p.T) break;
+      const int64_t off = j == 0 ? off0 : ring.offset(row + j * gridDim.x);
+      const S rest = KEPT ? S(0) : s[SUMS * j + SUMS - 1] * inv_d;   // of z's mean, which is zero
+      const S mu = s[SUMS * j] * inv_d, muz = (s[SUMS * j + 1] - rest * s[SUMS * j]) * inv_d;
+      const L R = all(r[j], L()), Rest = all(-rest, L()), Mu = all(-mu, L()), Muz = all(-muz, L());
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      if (!ring.has(i)) continue;
-      L(&w)[N] = hold_w[kHold ? i : 0];
-      if (!kHold) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, w);
-      L(&u)[N] = hold_d[kHold ? i : 0], (&z)[N] = hold_z[kHold ? i : 0];
-      L g[N];
-      if (!kHold) {
-        V::load_shared(here + kDn * ring.row_bytes + i * ring.step, u);
-        normed(i, z);
+      for (int i = 0; i < ITER; ++i) {
+        if (!ring.has(i)) continue;
+        L(&w)[N] = hold_w[kHold ? i : 0];
+        if (!kHold) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, w);
+        L(&u)[N] = hold_d[j][kHold ? i : 0], (&z)[N] = hold_z[j][kHold ? i : 0];
+        L g[N];
+        if (!kHold) {
+          V::load_shared(here + kDn * ring.row_bytes + i * ring.step, u);
+          normed(j, i, z);
+        }
+        if (has_in) {
+          V::load_shared(here + (j * per_row + kIn) * ring.row_bytes + i * ring.step, g);
+        } else {
+#pragma unroll
+          for (int c = 0; c < N; ++c) g[c] = splat<L>(0.0f);
+        }
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          if (!KEPT) z[c] = add(z[c], Rest);
+          acc_w[i][c] = fma(u[c], z[c], acc_w[i][c]);
+          g[c] = fma(fma(z[c], Muz, fma(u[c], w[c], Mu)), R, g[c]);
+        }
+        V::store(reinterpret_cast<T *>((uint8_t *)p.dx + off + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step), g);
       }
-      if (has_in) {
-        V::load_shared(here + kIn * ring.row_bytes + i * ring.step, g);
-      } else {
-#pragma unroll
-        for (int c = 0; c < N; ++c) g[c] = splat<L>(0.0f);
-      }
-#pragma unroll
-      for (int c = 0; c < N; ++c) {
-        if (!KEPT) z[c] = add(z[c], Rest);
-        acc_w[i][c] = fma(u[c], z[c], acc_w[i][c]);
-        g[c] = fma(fma(z[c], Muz, fma(u[c], w[c], Mu)), R, g[c]);
-      }
-      V::store(reinterpret_cast<T *>((uint8_t *)p.dx + off + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step), g);
     }
     if (++stage == ring.stages) stage = 0;
   }
@@ -594,10 +620,16 @@ template <typename T, int VEC, int ITER> static int ln_launch_fwd(const LnFwdPar
   return launch<ln_fwd_kernel<T, VEC, ITER, false, 1>>(p, sh, 1, (int)grid, s);
 }
 template <typename T, int VEC, int ITER, typename S = float>
-static int ln_launch_bwd(const LnBwdParams &p, const Shape &sh, int grid, cudaStream_t s) {
-  const int tensors = p.dx_in ? 3 : 2;
-  if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S>>(p, sh, tensors, grid, s);
-  return launch<ln_bwd_kernel<T, VEC, ITER, false, S>>(p, sh, tensors, grid, s);
+static int ln_launch_bwd(const LnBwdParams &p, const Shape &sh, int rows, int grid, cudaStream_t s) {
+  const int tensors = rows * (p.dx_in ? 3 : 2);
+  if constexpr (VEC > 1 && ITER == 1) {
+    if (rows == 2) {
+      if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S, 2>>(p, sh, tensors, grid, s);
+      return launch<ln_bwd_kernel<T, VEC, ITER, false, S, 2>>(p, sh, tensors, grid, s);
+    }
+  }
+  if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S, 1>>(p, sh, tensors, grid, s);
+  return launch<ln_bwd_kernel<T, VEC, ITER, false, S, 1>>(p, sh, tensors, grid, s);
 }
 template <typename T, int VEC>
 static int ln_launch_restore(const void *codes, const void *scales, const void *w, const void *b, int64_t T_, int d, void *n,
@@ -731,15 +763,22 @@ extern "C" int moe_layer_norm_bwd(const void *dn, const void *x, const void *cod
   p.eps = eps;
   cudaStream_t s = (cudaStream_t)stream;
   Shape sh = shape_of(d, dtype);
-  const int grid = ln_bwd_blocks(T, sh, dx_in ? 3 : 2);
+  int rows = 1, grid = ln_bwd_blocks(T, sh, dx_in ? 3 : 2);
+  // Two rows at a time where blocks have more rows than one: at T = 16384, d = 4096 bf16 86.8 against 89.0 us (from codes 84.7 against
+  // 91.0), at 8192 x 1024 fp32 18.8 against 21.4; not where bf16 rows are short enough for two blocks per SM: 26.8 against 25.7 at 8192
+  // x 2048, 15.7 against 15.0 at 8192 x 1024.
+  if (sh.vec > 1 && sh.iter == 1 && T > grid && d > 32 && (dtype == MOE_F32 || sh.threads > kMaxThreads / 2)) {
+    rows = 2;
+    grid = ln_bwd_blocks(T, sh, dx_in ? 6 : 4);
+  }
   if (d <= 32) {   // one value per lane, in 64 bits
     sh.vec = sh.iter = 1;
     sh.threads = 32;
     sh.row_bytes = ((uint32_t)d * (uint32_t)dtype_size(dtype) + 15) / 16 * 16 + 16;
-    if (dtype == MOE_BF16) rc = ln_launch_bwd<__nv_bfloat16, 1, 1, double>(p, sh, grid, s);
-    else rc = ln_launch_bwd<float, 1, 1, double>(p, sh, grid, s);
+    if (dtype == MOE_BF16) rc = ln_launch_bwd<__nv_bfloat16, 1, 1, double>(p, sh, 1, grid, s);
+    else rc = ln_launch_bwd<float, 1, 1, double>(p, sh, 1, grid, s);
   } else {
-    MOE_LN_DISPATCH(ln_launch_bwd, p, sh, grid, s);
+    MOE_LN_DISPATCH(ln_launch_bwd, p, sh, rows, grid, s);
   }
   if (rc) return rc;
   const dim3 g((d + 31) / 32, db ? 2 : 1);
