@@ -156,6 +156,10 @@ def _s(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+def wrong_device(index, dev):
+    raise ValueError(f"the buffers are on cuda:{index}, the current device is cuda:{dev}")
+
+
 def _want(name, t, dtype, shape):
     """A tensor argument that a kernel reads as contiguous memory of this type and shape."""
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
@@ -552,10 +556,10 @@ def moe_act8_dequantize(codes, scales, x, stream=None):
         _at("x", x, dt, shape, dev), _s(stream)))
 
 
-def layer_norm_fwd_into(x, w, b, T, d, dt, n, mean, rstd, codes, scales, eps, stream):
-    """The call behind moe_layer_norm_fwd and LayerNorm.forward: checks its inputs; n, mean, rstd, codes and scales are the
-    addresses of outputs of type dt and fitting size (all but n may be None)."""
-    dev, vec = _device(), (d,)
+def layer_norm_fwd_into(dev, x, w, b, T, d, dt, n, mean, rstd, codes, scales, eps, stream):
+    """The call behind moe_layer_norm_fwd and LayerNorm.forward: checks its inputs (dev: the current device); n, mean, rstd, codes and
+    scales are the addresses of outputs of type dt and fitting size (all but n may be None)."""
+    vec = (d,)
     _ok("moe_layer_norm_fwd", lib().moe_layer_norm_fwd(
         _at("x", x, dt, (T, d), dev), _at("w", w, dt, vec, dev), None if b is None else _at("b", b, dt, vec, dev), T, d,
         dtype_code(dt), eps, n, mean, rstd, codes, scales, _s(stream)))
@@ -567,22 +571,40 @@ def moe_layer_norm_fwd(x, w, b, n, mean=None, rstd=None, codes=None, scales=None
     T, d = x.shape
     dt, dev, f32 = x.dtype, _device(), torch.float32
     layer_norm_fwd_into(
-        x, w, b, T, d, dt, _at("n", n, dt, (T, d), dev), None if mean is None else _at("mean", mean, f32, (T,), dev),
+        dev, x, w, b, T, d, dt, _at("n", n, dt, (T, d), dev), None if mean is None else _at("mean", mean, f32, (T,), dev),
         None if rstd is None else _at("rstd", rstd, f32, (T,), dev), None if codes is None else _at("codes", codes, _U8, (T, d), dev),
         None if scales is None else _bytes_on("scales", scales, _scale_bytes8(T, d), dev), eps, stream)
+
+
+def layer_norm_restore_into(dev, codes, scales, w, b, T, d, dt, n, stream):
+    """The call behind moe_layer_norm_restore and LayerNorm.restore: checks w and b; codes, scales and n are the addresses of buffers
+    of type dt and fitting size."""
+    vec = (d,)
+    _ok("moe_layer_norm_restore", lib().moe_layer_norm_restore(
+        codes, scales, _at("w", w, dt, vec, dev), None if b is None else _at("b", b, dt, vec, dev), T, d, dtype_code(dt), n,
+        _s(stream)))
 
 
 def moe_layer_norm_restore(codes, scales, w, b, n, stream=None):
     """n = z w + b with the z that codes and scales stand for; b may be None."""
     T, d = n.shape
     dt, dev = n.dtype, _device()
-    _ok("moe_layer_norm_restore", lib().moe_layer_norm_restore(
-        _at("codes", codes, _U8, (T, d), dev), _bytes_on("scales", scales, _scale_bytes8(T, d), dev), _at("w", w, dt, (d,), dev),
-        None if b is None else _at("b", b, dt, (d,), dev), T, d, dtype_code(dt), _at("n", n, dt, (T, d), dev), _s(stream)))
+    layer_norm_restore_into(dev, _at("codes", codes, _U8, (T, d), dev), _bytes_on("scales", scales, _scale_bytes8(T, d), dev), w, b, T, d,
+                            dt, _at("n", n, dt, (T, d), dev), stream)
 
 
 def moe_layer_norm_bwd_workspace_size(T, d, dtype):
     return int(lib().moe_layer_norm_bwd_workspace_size(T, d, dtype))
+
+
+def layer_norm_bwd_into(dev, dn, x, w, dx_in, T, d, dt, codes, scales, mean, rstd, dx, dw, db, ws, ws_bytes, eps, stream):
+    """The call behind moe_layer_norm_bwd and LayerNorm.backward: checks its inputs dn, x, w and dx_in; the others are the addresses of
+    buffers of type dt and fitting size."""
+    rows = (T, d)
+    _ok("moe_layer_norm_bwd", lib().moe_layer_norm_bwd(
+        _at("dn", dn, dt, rows, dev), None if x is None else _at("x", x, dt, rows, dev), codes, scales, mean, rstd,
+        _at("w", w, dt, (d,), dev), None if dx_in is None else _at("dx_in", dx_in, dt, rows, dev), T, d, dtype_code(dt), eps, dx, dw,
+        db, ws, ws_bytes, _s(stream)))
 
 
 def moe_layer_norm_bwd(dn, x, codes, scales, mean, rstd, w, dx_in, dx, dw, db, ws, eps=1e-5, stream=None):
@@ -594,12 +616,11 @@ def moe_layer_norm_bwd(dn, x, codes, scales, mean, rstd, w, dx_in, dx, dw, db, w
     def opt(name, t, dtype, shape):
         return None if t is None else _at(name, t, dtype, shape, dev)
 
-    _ok("moe_layer_norm_bwd", lib().moe_layer_norm_bwd(
-        _at("dn", dn, dt, rows, dev), opt("x", x, dt, rows), opt("codes", codes, _U8, rows),
+    layer_norm_bwd_into(
+        dev, dn, x, w, dx_in, T, d, dt, opt("codes", codes, _U8, rows),
         None if scales is None else _bytes_on("scales", scales, _scale_bytes8(T, d), dev), opt("mean", mean, f32, (T,)),
-        _at("rstd", rstd, f32, (T,), dev), _at("w", w, dt, vec, dev), opt("dx_in", dx_in, dt, rows), T, d, dtype_code(dt), eps,
-        _at("dx", dx, dt, rows, dev), _at("dw", dw, dt, vec, dev), opt("db", db, dt, vec), _on("ws", ws, dev),
-        ws.numel() * ws.element_size(), _s(stream)))
+        _at("rstd", rstd, f32, (T,), dev), _at("dx", dx, dt, rows, dev), _at("dw", dw, dt, vec, dev), opt("db", db, dt, vec),
+        _on("ws", ws, dev), ws.numel() * ws.element_size(), eps, stream)
 
 
 def moe_ffn_workspace_size(T, d, f, dtype, backward):
@@ -618,10 +639,9 @@ def kept(ab, ab_scales, dt, T, f):
     return KEEP_F8, _at("ab", ab, _U8, (T, 2 * f), dev), _bytes_on("ab_scales", ab_scales, _scale_bytes8(T, 2 * f), dev)
 
 
-def ffn_fwd_into(x, w_gate_up, w_down, y_in, T, d, f, dt, act, keep, h, y, ws, ws_bytes, stream):
+def ffn_fwd_into(dev, x, w_gate_up, w_down, y_in, T, d, f, dt, act, keep, h, y, ws, ws_bytes, stream):
     """The call behind moe_ffn_fwd and GatedFFN.forward: checks its inputs; keep is what kept() says of fitting buffers; h, y and ws
     are the addresses of buffers of type dt and fitting size."""
-    dev = _device()
     _ok("moe_ffn_fwd", lib().moe_ffn_fwd(
         _at("x", x, dt, (T, d), dev), _at("w_gate_up", w_gate_up, dt, (2 * f, d), dev), _at("w_down", w_down, dt, (d, f), dev),
         None if y_in is None else _at("y_in", y_in, dt, (T, d), dev), T, d, f, dtype_code(dt), act, keep[0], keep[1], keep[2], h, y,
@@ -633,8 +653,18 @@ def moe_ffn_fwd(x, w_gate_up, w_down, y_in, ab, ab_scales, h, y, ws, act=ACT_SIL
     ab: None (nothing kept), [T, 2f] in x's type, or [T, 2f] uint8 codes with ab_scales. h [T, f] is written."""
     T, d = x.shape
     f, dt, dev = w_down.shape[1], x.dtype, _device()
-    ffn_fwd_into(x, w_gate_up, w_down, y_in, T, d, f, dt, act, kept(ab, ab_scales, dt, T, f), _at("h", h, dt, (T, f), dev),
+    ffn_fwd_into(dev, x, w_gate_up, w_down, y_in, T, d, f, dt, act, kept(ab, ab_scales, dt, T, f), _at("h", h, dt, (T, f), dev),
                  _at("y", y, dt, (T, d), dev), _on("ws", ws, dev), ws.numel() * ws.element_size(), stream)
+
+
+def ffn_bwd_into(dev, dy, x, w_gate_up, w_down, dx_in, T, d, f, dt, act, keep, h, dab, dx, dw_gate_up, dw_down, ws, ws_bytes, stream):
+    """The call behind moe_ffn_bwd and GatedFFN.backward: checks its inputs; keep is what kept() says of fitting buffers, h and those
+    after it are the addresses of buffers of type dt and fitting size."""
+    _ok("moe_ffn_bwd", lib().moe_ffn_bwd(
+        _at("dy", dy, dt, (T, d), dev), _at("x", x, dt, (T, d), dev), keep[1], keep[2], h,
+        _at("w_gate_up", w_gate_up, dt, (2 * f, d), dev), _at("w_down", w_down, dt, (d, f), dev),
+        None if dx_in is None else _at("dx_in", dx_in, dt, (T, d), dev), T, d, f, dtype_code(dt), act, keep[0], dab, dx, dw_gate_up,
+        dw_down, ws, ws_bytes, _s(stream)))
 
 
 def moe_ffn_bwd(dy, x, ab, ab_scales, h, w_gate_up, w_down, dx_in, dab, dx, dw_gate_up, dw_down, ws, act=ACT_SILU,
@@ -642,14 +672,10 @@ def moe_ffn_bwd(dy, x, ab, ab_scales, h, w_gate_up, w_down, dx_in, dab, dx, dw_g
     """Backward of moe_ffn_fwd from the ab (and h, or ab_scales) that it kept; dx_in (may be None, may be dx) is added to dx."""
     T, d = dy.shape
     f, dt, dev = w_down.shape[1], dy.dtype, _device()
-    keep, ab_p, sc_p = kept(ab, ab_scales, dt, T, f)
-    _ok("moe_ffn_bwd", lib().moe_ffn_bwd(
-        _at("dy", dy, dt, (T, d), dev), _at("x", x, dt, (T, d), dev), ab_p, sc_p, _at("h", h, dt, (T, f), dev),
-        _at("w_gate_up", w_gate_up, dt, (2 * f, d), dev), _at("w_down", w_down, dt, (d, f), dev),
-        None if dx_in is None else _at("dx_in", dx_in, dt, (T, d), dev), T, d, f, dtype_code(dt), act, keep,
-        _at("dab", dab, dt, (T, 2 * f), dev), _at("dx", dx, dt, (T, d), dev),
-        _at("dw_gate_up", dw_gate_up, dt, (2 * f, d), dev), _at("dw_down", dw_down, dt, (d, f), dev), _on("ws", ws, dev),
-        ws.numel() * ws.element_size(), _s(stream)))
+    ffn_bwd_into(dev, dy, x, w_gate_up, w_down, dx_in, T, d, f, dt, act, kept(ab, ab_scales, dt, T, f), _at("h", h, dt, (T, f), dev),
+                 _at("dab", dab, dt, (T, 2 * f), dev), _at("dx", dx, dt, (T, d), dev),
+                 _at("dw_gate_up", dw_gate_up, dt, (2 * f, d), dev), _at("dw_down", dw_down, dt, (d, f), dev), _on("ws", ws, dev),
+                 ws.numel() * ws.element_size(), stream)
 
 
 def moe_read_status(ws, stream=None):

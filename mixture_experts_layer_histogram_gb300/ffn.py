@@ -64,18 +64,18 @@ class GatedFFN:
         self._index = self.y.device.index
         with torch.cuda.device(self._index):
             self._kept = L.kept(self.ab, self.ab_scales, dtype, T, f)
+        if backward:
+            self._grads = [t.data_ptr() for t in (self.dab, self.dx, self.dw_gate_up, self.dw_down)]
         self._h_ptr, self._y_ptr, self._ws_ptr, self._ws_bytes = (self.h.data_ptr(), self.y.data_ptr(), self.ws.data_ptr(),
                                                                   self.ws.numel())
 
-    def _check_device(self):
-        if L._device() != self._index:
-            raise ValueError(f"the buffers are on cuda:{self._index}, the current device is cuda:{L._device()}")
-
     def forward(self, x, w_gate_up, w_down, add=None, out=None, stream=None):
         """y [T, d] = add + FFN(x), into `out` (which may be add) where it is given."""
-        self._check_device()
-        y = self._y_ptr if out is None else L._at("out", out, self.dtype, (self.T, self.d), L._device())
-        L.ffn_fwd_into(x, w_gate_up, w_down, add, self.T, self.d, self.f, self.dtype, self._act, self._kept, self._h_ptr, y,
+        dev = L._device()
+        if dev != self._index:
+            L.wrong_device(self._index, dev)
+        y = self._y_ptr if out is None else L._at("out", out, self.dtype, (self.T, self.d), dev)
+        L.ffn_fwd_into(dev, x, w_gate_up, w_down, add, self.T, self.d, self.f, self.dtype, self._act, self._kept, self._h_ptr, y,
                        self._ws_ptr, self._ws_bytes, stream)
         return self.y if out is None else out
 
@@ -83,9 +83,11 @@ class GatedFFN:
         """Gradients from what the last forward kept and its x: dx = add + the block's, dw_gate_up, dw_down."""
         if not self.backward_enabled:
             raise RuntimeError("the block was built without backward buffers")
-        L._want("dy", dy, self.dtype, (self.T, self.d))
-        L.moe_ffn_bwd(dy, x, self.ab, self.ab_scales, self.h, w_gate_up, w_down, add, self.dab, self.dx, self.dw_gate_up,
-                      self.dw_down, self.ws, self._act, stream)
+        dev = L._device()
+        if dev != self._index:
+            L.wrong_device(self._index, dev)
+        L.ffn_bwd_into(dev, dy, x, w_gate_up, w_down, add, self.T, self.d, self.f, self.dtype, self._act, self._kept, self._h_ptr,
+                       *self._grads, self._ws_ptr, self._ws_bytes, stream)
         return dict(dx=self.dx, dw_gate_up=self.dw_gate_up, dw_down=self.dw_down)
 
     def status(self, stream=None):

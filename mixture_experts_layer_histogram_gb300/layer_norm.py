@@ -44,30 +44,38 @@ class LayerNorm:
             self.dw = torch.empty(d, **act)
             self.db = torch.empty(d, **act) if bias else None
             self.ws = torch.empty(L.moe_layer_norm_bwd_workspace_size(T, d, code), dtype=torch.uint8, device=self.device)
+            self._ws_bytes = self.ws.numel()
         self._index = self.n.device.index
-        self._out = [None if t is None else t.data_ptr() for t in (self.n, self.mean, self.rstd, self.codes, self.scales)]
+
+        def at(*tensors):
+            return [None if t is None else t.data_ptr() for t in tensors]
+
+        self._out, self._codes = at(self.n, self.mean, self.rstd, self.codes, self.scales), at(self.codes, self.scales)
+        if backward:
+            self._back = at(self.codes, self.scales, self.mean, self.rstd, self.dx, self.dw, self.db, self.ws)
 
     def _check(self, b):
+        """The current device, on which the buffers have to be."""
         if (b is not None) != self.bias:
             raise ValueError("b is needed with a bias, and only there")
+        dev = L._device()
+        if dev != self._index:
+            L.wrong_device(self._index, dev)
+        return dev
 
     def forward(self, x, w, b=None, stream=None):
         """n [T, d]."""
-        self._check(b)
-        if L._device() != self._index:
-            raise ValueError(f"the buffers are on cuda:{self._index}, the current device is cuda:{L._device()}")
-        L.layer_norm_fwd_into(x, w, b, self.T, self.d, self.dtype, *self._out, self.eps, stream)
+        L.layer_norm_fwd_into(self._check(b), x, w, b, self.T, self.d, self.dtype, *self._out, self.eps, stream)
         return self.n
 
     def restore(self, w, b=None, out=None, stream=None):
         """n again, from the kept rows, into `out` (or n's own buffer)."""
         if not self.keep:
             raise RuntimeError("the norm keeps nothing to restore n from")
-        self._check(b)
-        out = self.n if out is None else out
-        L._want("out", out, self.dtype, (self.T, self.d))
-        L.moe_layer_norm_restore(self.codes, self.scales, w, b, out, stream)
-        return out
+        dev = self._check(b)
+        n = self._out[0] if out is None else L._at("out", out, self.dtype, (self.T, self.d), dev)
+        L.layer_norm_restore_into(dev, *self._codes, w, b, self.T, self.d, self.dtype, n, stream)
+        return self.n if out is None else out
 
     def backward(self, dn, w, x=None, dx_in=None, stream=None):
         """dx (plus dx_in, the gradient that reaches x past the norm), dw, and db with a bias. x is what forward read;
@@ -76,9 +84,10 @@ class LayerNorm:
             raise RuntimeError("the norm was built without backward buffers")
         if (x is None) != bool(self.keep):
             raise ValueError("x is needed without keep, and only there")
-        L._want("dn", dn, self.dtype, (self.T, self.d))
-        L.moe_layer_norm_bwd(dn, x, self.codes, self.scales, self.mean, self.rstd, w, dx_in, self.dx, self.dw, self.db, self.ws,
-                             self.eps, stream)
+        dev = L._device()
+        if dev != self._index:
+            L.wrong_device(self._index, dev)
+        L.layer_norm_bwd_into(dev, dn, x, w, dx_in, self.T, self.d, self.dtype, *self._back, self._ws_bytes, self.eps, stream)
         res = dict(dx=self.dx, dw=self.dw)
         if self.bias:
             res["db"] = self.db
