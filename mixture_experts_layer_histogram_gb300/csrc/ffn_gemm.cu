@@ -1016,8 +1016,7 @@ static size_t counter_bytes(int64_t T) { return kArrivedBytes + 128 + (size_t)up
 static void deal_out(Params &p, int pairs) {
   int64_t load[MAX_PAIRS] = {};
   memset(p.count, 0, sizeof(p.count));
-  std::pair<int64_t, int> heap[MAX_PAIRS];
-  const auto later = [](const std::pair<int64_t, int> &x, const std::pair<int64_t, int> &y) { return x > y; };
+  typedef std::pair<int64_t, int> Pair;   // a pair's work, and its number
   int next = 0, at = 0;
   for (int i = 0; i < p.products; ++i) {
     const int c = p.deal[i], wide = p.prod[c].width == TILE ? 0 : 1;
@@ -1031,21 +1030,23 @@ static void deal_out(Params &p, int pairs) {
       next = (int)((next + n) % pairs);
       at += (int)n;
     } else {
+      // A tile's cost is the same for all, so the pairs that have just got one come back in the order in which they got it: the least
+      // work is at the front of the sorted pairs or of those.
       const int64_t even = n / pairs > 2 ? n / pairs - 2 : 0;
+      Pair sorted[MAX_PAIRS], again[3 * MAX_PAIRS];
       for (int k = 0; k < pairs; ++k) {
         p.count[c][k] = (uint16_t)even;
         load[k] += even * cost;
-        heap[k] = {load[k], k};
+        sorted[k] = {load[k], k};
       }
-      std::make_heap(heap, heap + pairs, later);
+      std::sort(sorted, sorted + pairs);
+      int front = 0, old = 0, last = 0;
       for (n -= even * pairs; n > 0; --n) {
-        std::pop_heap(heap, heap + pairs, later);
-        auto &least = heap[pairs - 1];
+        const Pair least = old < last && (front == pairs || again[old] < sorted[front]) ? again[old++] : sorted[front++];
         ++p.count[c][least.second];
-        least.first += cost;
-        std::push_heap(heap, heap + pairs, later);
+        load[least.second] += cost;
+        again[last++] = {load[least.second], least.second};
       }
-      for (int k = 0; k < pairs; ++k) load[heap[k].second] = heap[k].first;
     }
     if (i == 0 && (int64_t)o.m_tiles * o.n_tiles * o.splits <= pairs) {
       const int64_t most = *std::max_element(load, load + pairs);
