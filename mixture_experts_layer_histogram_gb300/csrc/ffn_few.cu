@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "dependent.cuh"
 #include "ffn.cuh"
@@ -161,11 +162,17 @@ template <bool UP, int NT, int CH> static int launch(const Params &p, cudaStream
 // them twice). Measured for 24 tokens of 4096 x 8192: 26.5 us for the 134 MB of Wg and Wu (5.1 TB/s) and 16 for the 67 MB of Wd,
 // 41 together; with loads into registers (above) the 134 MB took 33 us.
 constexpr int KS = 512;                        // of K per stage
+constexpr int BOX = 8 * KS * 2;                // bytes of 8 rows of a stage
 struct Stream {
-  int groups, steps;                           // row groups; stages per group
+  // Units of 16 weight rows (8 gate and the same features' 8 up rows, or 16 of Wd); a group takes MT of them, or (mixed) MT while
+  // groups are below `full`, then one
+  int full, groups, steps;                     // steps: stages per group
 };
-template <int NT, int MT> constexpr int weight_bytes() { return 16 * MT * KS * 2; }
-template <int NT> constexpr int token_bytes() { return 8 * NT * KS * 2; }
+// Groups of two kinds, for up to 16 tokens; their units come in boxes of 8 rows then, else in one box per half. (Small boxes
+// cost 3% with 24 tokens, where the shorter last round gains nothing.)
+template <int NT, int MT> constexpr bool mixed() { return NT <= 2 && MT == 2; }
+template <int NT, int MT> constexpr int weight_bytes() { return 2 * MT * BOX; }
+template <int NT> constexpr int token_bytes() { return NT * BOX; }
 template <int NT, int MT> constexpr int stage_bytes() { return weight_bytes<NT, MT>() + token_bytes<NT>(); }
 template <int NT, int MT> constexpr int sum_bytes() { return WARPS * MT * NT * 512; }
 constexpr int kSmemMost = 232448;
@@ -187,12 +194,14 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, in
       : "memory");
 }
 
-// tmW: boxes of 8 MT weight rows, tmX: boxes of 8 NT tokens, each 64 x 8 of K
+// tmW: boxes of 8 weight rows (8 MT unless mixed), tmX: boxes of 8 NT tokens, each 64 x 8 of K
 template <bool UP, int NT, int MT>
 __global__ void __launch_bounds__(THREADS + 32, 1)
     ffn_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p, const Stream st,
                       WsHeader *hdr) {
-  constexpr int PS = stages_of<NT, MT>(), SB = stage_bytes<NT, MT>(), ROWS = 8 * MT, SUMS = sums_of<NT, MT>();
+  constexpr int PS = stages_of<NT, MT>(), SB = stage_bytes<NT, MT>(), SUMS = sums_of<NT, MT>();
+  constexpr bool MIXED = mixed<NT, MT>();
+  constexpr int ROWS = MIXED ? 8 : 8 * MT;     // of a box
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   float4(*sums)[MT * NT][32] = reinterpret_cast<float4(*)[MT * NT][32]>(smem + PS * SB);
@@ -214,15 +223,20 @@ __global__ void __launch_bounds__(THREADS + 32, 1)
   __syncthreads();
   const int mine = (int)blockIdx.x < st.groups ? (st.groups - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
   const int total = mine * st.steps;           // stages that this block goes through
+  auto whole = [&](int gr) { return !MIXED || gr < st.full; };
+  auto first = [&](int gr) { return whole(gr) ? gr * MT : gr + st.full * (MT - 1); };   // the group's first unit
   if (warp == WARPS) {
     // ---- the ring's producer: one elected lane
     if (tc::elect_one()) {
       auto weights = [&](int i) {
         const int gr = (int)blockIdx.x + i / st.steps * (int)gridDim.x, k = i % st.steps, s = i % PS;
-        const int row = gr * (UP ? ROWS : 2 * ROWS);
-        tc::mbar_expect_tx(full(s), SB);
-        load_3d(base + s * SB, &tmW, 0, row, k * (KS / 64), full(s));
-        load_3d(base + s * SB + weight_bytes<NT, MT>() / 2, &tmW, 0, UP ? p.N + row : row + ROWS, k * (KS / 64), full(s));
+        const bool all = whole(gr);
+        tc::mbar_expect_tx(full(s), (all ? MT : 1) * 2 * BOX + token_bytes<NT>());
+        for (int m = 0; m < (MIXED && all ? MT : 1); ++m) {
+          const int row = (first(gr) + m) * (UP ? 8 : 16);
+          load_3d(base + s * SB + m * BOX, &tmW, 0, row, k * (KS / 64), full(s));
+          load_3d(base + s * SB + (MT + m) * BOX, &tmW, 0, UP ? p.N + row : row + ROWS, k * (KS / 64), full(s));
+        }
       };
       auto tokens = [&](int i) {
         const int k = i % st.steps, s = i % PS;
@@ -251,22 +265,28 @@ __global__ void __launch_bounds__(THREADS + 32, 1)
         break;
       }
       const uint32_t w0 = base + s * SB + (uint32_t)warp * (ROWS * 128), x0 = base + s * SB + weight_bytes<NT, MT>() + (uint32_t)warp * (NT * 1024);
+      const bool all = whole(gr);
+      auto products = [&](auto count) {   // of the group's units
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t at = (uint32_t)g * 128 + (((uint32_t)(2 * q + h) ^ (uint32_t)g) << 4);
-        uint4 x[NT];
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = (uint32_t)g * 128 + (((uint32_t)(2 * q + h) ^ (uint32_t)g) << 4);
+          uint4 x[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[n] = tc::ld_shared_v4(x0 + n * 1024 + at);
+          for (int n = 0; n < NT; ++n) x[n] = tc::ld_shared_v4(x0 + n * 1024 + at);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint4 a = tc::ld_shared_v4(w0 + m * 1024 + at), b = tc::ld_shared_v4(w0 + weight_bytes<NT, MT>() / 2 + m * 1024 + at);
+          for (int m = 0; m < decltype(count)::value; ++m) {
+            const uint32_t w = w0 + m * (MIXED ? BOX : 1024) + at;
+            const uint4 a = tc::ld_shared_v4(w), b = tc::ld_shared_v4(w + MT * BOX);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816(acc[m][n], a.x, b.x, a.y, b.y, x[n].x, x[n].y);
-            mma16816(acc[m][n], a.z, b.z, a.w, b.w, x[n].z, x[n].w);
+            for (int n = 0; n < NT; ++n) {
+              mma16816(acc[m][n], a.x, b.x, a.y, b.y, x[n].x, x[n].y);
+              mma16816(acc[m][n], a.z, b.z, a.w, b.w, x[n].z, x[n].w);
+            }
           }
         }
-      }
+      };
+      if (all) products(std::integral_constant<int, MT>());
+      else products(std::integral_constant<int, 1>());
       // the reads above come before the TMA's next writes to this place: another proxy's, which the arrival alone does not order
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -283,7 +303,7 @@ __global__ void __launch_bounds__(THREADS + 32, 1)
         }
       }
       asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
-      for (int j = warp; j < MT * NT; j += WARPS) {
+      for (int j = warp; j < (all ? MT : 1) * NT; j += WARPS) {
         float4 v = sums[at_sums][j][lane];
 #pragma unroll
         for (int u = 1; u < WARPS; ++u) {
@@ -294,8 +314,8 @@ __global__ void __launch_bounds__(THREADS + 32, 1)
           v.w += o.w;
         }
         const int m = j / NT, t = 8 * (j - m * NT) + 2 * q;   // tokens t and t + 1
-        if (UP) put_up(p, gr * ROWS + 8 * m + g, t, v);
-        else put_down(p, gr * 2 * ROWS + 8 * m + g, ROWS, t, v);
+        if (UP) put_up(p, 8 * (first(gr) + m) + g, t, v);
+        else put_down(p, 16 * first(gr) + (MIXED ? 16 : 8) * m + g, ROWS, t, v);
       }
       if (SUMS == 1) asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
       else at_sums ^= WARPS;
@@ -326,16 +346,15 @@ template <auto KERNEL, int SMEM> static int raise_limit() {
   if (dev < 64) raised.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
   return MOE_OK;
 }
-template <bool UP, int NT, int MT> static int launch_stream(const Params &p, WsHeader *hdr, cudaStream_t s) {
+template <bool UP, int NT, int MT> static int launch_stream(const Params &p, int full, int groups, WsHeader *hdr, cudaStream_t s) {
   constexpr int SMEM = smem_of<NT, MT>();
   static_assert(SMEM <= kSmemMost && stages_of<NT, MT>() >= 2, "two stages at least");
   CUtensorMap mw, mx;
-  if (!stream_map(&mw, p.w, UP ? 2 * (uint64_t)p.N : p.N, p.K, 8 * MT) || !stream_map(&mx, p.tok, p.T, p.K, 8 * NT)) return MOE_ERR_CUDA;
+  if (!stream_map(&mw, p.w, UP ? 2 * (uint64_t)p.N : p.N, p.K, mixed<NT, MT>() ? 8 : 8 * MT) || !stream_map(&mx, p.tok, p.T, p.K, 8 * NT)) return MOE_ERR_CUDA;
   const int rc = raise_limit<ffn_stream_kernel<UP, NT, MT>, SMEM>();
   if (rc) return rc;
-  const int per = UP ? 8 * MT : 16 * MT;
-  const Stream st{(p.N + per - 1) / per, (p.K + KS - 1) / KS};
-  const int grid = std::min(st.groups, sm_count());
+  const Stream st{full, groups, (p.K + KS - 1) / KS};
+  const int grid = std::min(groups, sm_count());
   if (UP) {
     ffn_stream_kernel<UP, NT, MT><<<grid, THREADS + 32, SMEM, s>>>(mw, mx, p, st, hdr);
     MOE_CHECK_LAUNCH();
@@ -345,13 +364,22 @@ template <bool UP, int NT, int MT> static int launch_stream(const Params &p, WsH
   return MOE_OK;
 }
 template <bool UP, int NT> static int stream(const Params &p, WsHeader *hdr, cudaStream_t s) {
-  // rounds of row groups over the SMs: 32 rows per group read the tokens half as often, 16 leave a shorter last round (and with
-  // more tokens than 32 more stages fit)
-  const int64_t sms = sm_count(), g16 = (p.N + (UP ? 7 : 15)) / (UP ? 8 : 16), g32 = (g16 + 1) / 2;
-  if constexpr (NT <= 4) {
-    if (2 * ((g32 + sms - 1) / sms) <= (g16 + sms - 1) / sms) return launch_stream<UP, NT, 2>(p, hdr, s);
+  const int units = (p.N + (UP ? 7 : 15)) / (UP ? 8 : 16), sms = sm_count();
+  if constexpr (NT <= 2) {
+    // Groups of two units, which read the tokens half as often, while they fill rounds over the SMs; what is left in single units
+    // where that is one round, half as long: 17.3 against 20.5 us for one token of 2048 x 8192.
+    int full = units / (2 * sms) * sms, rest = units - 2 * full;
+    if (rest > sms) {
+      full += rest / 2;
+      rest &= 1;
+    }
+    if (full > 0) return launch_stream<UP, NT, 2>(p, full, full + rest, hdr, s);
+  } else if constexpr (NT <= 4) {
+    // Groups of two where they take no longer in whole rounds than single units, of which more stages fit.
+    const int pairs = (units + 1) / 2;
+    if (2 * ((pairs + sms - 1) / sms) <= (units + sms - 1) / sms) return launch_stream<UP, NT, 2>(p, pairs, pairs, hdr, s);
   }
-  return launch_stream<UP, NT, 1>(p, hdr, s);
+  return launch_stream<UP, NT, 1>(p, 0, units, hdr, s);
 }
 
 // ring: through the ring, both products of a call

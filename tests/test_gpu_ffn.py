@@ -102,7 +102,8 @@ def check_backward(ffn, s, act, add):
 
 FEW = [(1, 64, 64), (1, 2048, 1024), (2, 8, 8), (3, 72, 40), (8, 520, 1000), (9, 256, 264), (17, 264, 136), (24, 256, 8192), (31, 1032, 4104),
        (33, 128, 72), (57, 2048, 512), (64, 512, 1000), (1, 4096, 8192), (9, 4096, 2744), (24, 4096, 8192), (26, 8192, 4104), (41, 2112, 9608),
-       (64, 4032, 5000), (20, 1088, 1344), (33, 2048, 704), (64, 704, 2112)]
+       (64, 4032, 5000), (20, 1088, 1344), (33, 2048, 704), (64, 704, 2112), (1, 4096, 2752),
+       (13, 4928, 2560), (16, 2048, 5120)]
 MANY = [(65, 64, 64), (100, 8, 8), (127, 136, 72), (256, 256, 256), (257, 520, 264), (700, 1032, 328), (1000, 2048, 1024), (2500, 1024, 2048),
         (3000, 64, 4096), (515, 4096, 96), (256, 4096, 2048), (1300, 1024, 1088)]
 
@@ -250,7 +251,8 @@ def test_stream_and_graph(T):
         assert all(torch.equal(a, b) for a, b in zip(now, step(ref, x)))
 
 
-@pytest.mark.parametrize("T,d,f", [(1, 4096, 2744), (16, 4096, 2744), (24, 4096, 2744), (24, 4096, 4864), (60, 2048, 5120)])
+@pytest.mark.parametrize("T,d,f", [(1, 4096, 2744), (16, 4096, 2744), (24, 4096, 2744), (24, 4096, 4864), (60, 2048, 5120),
+                                   (1, 4096, 2752), (16, 4096, 4864), (12, 4928, 2560)])
 def test_repeats_with_weights_in_the_cache(T, d, f):
     """The ring of streamed weights turns fastest when nothing comes from memory: every pass gives the first one's bits."""
     s = make(T, d, f, BF, 7)
