@@ -9,15 +9,19 @@
 // place of the 64 that x takes in bf16); restore() gives z w + b again for the block's own backward, and
 // the backward reads z from the codes.
 //
-// HBM-bound, like the RMS norms (norm.cu): a thread block works on one row at a time, or on two, which share their reductions (the
-// forward needs two per row, the deviations waiting for the mean), read once through the ring of rows and written once; codes
-// come through the ring as well, 8 (fp32: 4) bytes per thread beside its 16-byte vectors. The weight gradients are summed over a
-// block's rows in registers and its partial rows added up in a fixed order.
+// Rows whose length is no multiple of 16 bytes are read and written as the words that cover them (Windows), where that pays.
+// HBM-bound, like the RMS norms (norm.cu): a thread block works on one row at a time, or on two, which share their reductions
+// (the forward needs two per row, the deviations waiting for the mean), read once through the ring of rows and written once;
+// codes come through the ring as well, 8 (fp32: 4) bytes per thread beside its 16-byte vectors. The weight gradients are summed
+// over a block's rows in registers and its partial rows added up in a fixed order.
 // Measured (bf16, in replayed graphs): T = 8192, d = 2048 forward 16.1 us (67 MB), with codes 20.1 (84 MB), restore 8.3 (51 MB),
 // backward with dx_in 25.7 from x or codes (135 or 118 MB); T = 16384, d = 4096 forward 57.9, backward with dx_in 86.8 (537 MB,
 // 6.2 TB/s; 94 in a stream of calls with other inputs each time), from codes 84.8; fp32 T = 1023, d = 1537 backward 10.2 us; four
 // rows of 2048 2.3 and 4.0 us. Before dn and z stayed in registers between the backward's two passes it took 4% longer. Two
 // vectors per thread or a warp per row (fewer instructions, no barriers) took the forward as long as one row at a time, 18.6 us.
+#include <algorithm>
+#include <type_traits>
+
 #include "act8.cuh"
 #include "raw16.cuh"
 #include "row_ring.cuh"
@@ -112,6 +116,80 @@ __device__ __forceinline__ void get_codes(uint32_t a, F2 (&v)[2], float scale) {
   v[1] = mul(pair(f[2], f[3]), pair(scale, scale));
 }
 
+// Rows that start anywhere, as vectors all the same: a block's rows lie so far apart (a multiple of 16 / sizeof(T) rows, or it
+// has only one) that all of them start at the same place in a 16-byte word. Vectors are the words that cover a row, the ends of
+// the first and the last one belong to other rows: their values count as zero, and are not written. Same use as Ring.
+template <typename T, int VEC, int ITER> struct Windows {
+  uint32_t mine, row_bytes, stage_bytes, step;
+  int stages, d, nvec, lead;   // lead: values before the row in its first word
+  int64_t all;                 // bytes of one tensor
+  __device__ __forceinline__ Windows(const uint8_t *smem, const Geometry &g, int64_t rows, int d_)
+      : row_bytes(g.row_bytes), stage_bytes(g.stage_bytes), stages(g.stages), d(d_) {
+    lead = (int)((int64_t)blockIdx.x * d % VEC);
+    nvec = (lead + d + VEC - 1) / VEC;
+    mine = (uint32_t)__cvta_generic_to_shared(smem) + 16u * threadIdx.x;
+    step = 16u * blockDim.x;
+    all = rows * d * (int64_t)sizeof(T);
+  }
+  __device__ __forceinline__ bool has(int i) const { return (int)(threadIdx.x + i * blockDim.x) < nvec; }
+  __device__ __forceinline__ int64_t offset(int64_t row) const { return (row * d - lead) * (int64_t)sizeof(T) + 16u * threadIdx.x; }
+  // The column of the first value of this thread's i-th vector, and which of the vector's values are the row's
+  __device__ __forceinline__ int column(int i) const { return (int)(threadIdx.x + i * blockDim.x) * VEC - lead; }
+  __device__ __forceinline__ uint32_t valid(int i) const {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) bits |= (uint32_t)((unsigned)(column(i) + c) < (unsigned)d) << c;
+    return bits;
+  }
+  __device__ __forceinline__ void fetch(const void *base, int64_t off, int stage, int slot) const {
+    const uint32_t dst = mine + (uint32_t)stage * stage_bytes + (uint32_t)slot * row_bytes;
+    const uint8_t *src = (const uint8_t *)base + off;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      if (!has(i)) continue;
+      const int64_t left = all - off - i * step;   // up to the tensor's end: nothing past it is read
+      const int n = left < 16 ? (int)left : 16;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * step), "l"(src + i * step), "r"(n) : "memory");
+    }
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  __device__ __forceinline__ void wait() const {
+    if (stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  __device__ __forceinline__ uint32_t at(int stage, int64_t) const { return mine + (uint32_t)stage * stage_bytes; }
+  __device__ __forceinline__ int freed(int stage) const { return stage >= 1 ? stage - 1 : stages - 1; }
+};
+template <int VEC> constexpr uint32_t kWhole = (1u << VEC) - 1;   // valid()
+template <int N> __device__ __forceinline__ void only(F2 (&v)[N], uint32_t bits) {   // the values that are the row's, zeros for the others
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    float x, y;
+    split(v[c], x, y);
+    v[c] = pair(bits >> (2 * c) & 1 ? x : 0.0f, bits >> (2 * c + 1) & 1 ? y : 0.0f);
+  }
+}
+template <typename T> __device__ __forceinline__ float value_at(const T *p) { return (float)*p; }
+// A vector of w or b from any column on
+template <typename T, int N> __device__ __forceinline__ void gather(const T *p, int column, uint32_t bits, F2 (&v)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+    v[c] = pair(bits >> (2 * c) & 1 ? value_at(p + column + 2 * c) : 0.0f, bits >> (2 * c + 1) & 1 ? value_at(p + column + 2 * c + 1) : 0.0f);
+}
+__device__ __forceinline__ void put_value(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put_value(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+template <typename T, int N> __device__ __forceinline__ void scatter(T *p, uint32_t bits, const F2 (&v)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    float x, y;
+    split(v[c], x, y);
+    if (bits >> (2 * c) & 1) put_value(p + 2 * c, x);
+    if (bits >> (2 * c + 1) & 1) put_value(p + 2 * c + 1, y);
+  }
+}
+template <typename T, int VEC, int ITER, bool WIN>
+using RowsOf = typename std::conditional<WIN, Windows<T, VEC, ITER>, Ring<T, VEC, ITER>>::type;
+
 struct LnFwdParams {
   const void *x, *w, *b;       // b may be null
   void *n;
@@ -155,16 +233,22 @@ __device__ __forceinline__ void keep(const LnFwdParams &p, int64_t row, int v, b
   if (v * VEC % act8::kBlock == 0) p.scales[row * p.nb + v * VEC / act8::kBlock] = (uint8_t)byte;
 }
 
-// ROWS: rows that a block takes at a time, which share the reductions' exchanges and barriers.
-template <typename T, int VEC, int ITER, bool KEEP, int ROWS>
+// ROWS: rows that a block takes at a time, which share the reductions' exchanges and barriers. WIN: Windows.
+template <typename T, int VEC, int ITER, bool KEEP, int ROWS, bool WIN>
 __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(const LnFwdParams p, const Geometry geom) {
   using V = Lanes<T, VEC, float>;
   using L = typename V::L;
   constexpr int N = V::N;
   constexpr bool kHold = ITER * VEC <= 16 && ITER <= 4;
+  static_assert(!WIN || (kHold && !KEEP), "windows hold their weights, and keep nothing");
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ SumBuf sums;
-  const Ring<T, VEC, ITER> ring(dyn, geom, p.T, p.d);
+  const RowsOf<T, VEC, ITER, WIN> ring(dyn, geom, p.T, p.d);
+  uint32_t bits[WIN ? ITER : 1];
+  if constexpr (WIN) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) bits[i] = ring.valid(i);
+  }
   int half = 0;
   const float inv_d = 1.0f / (float)p.d;
   clear(sums);
@@ -187,7 +271,13 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
     }
   };
   L hold_w[kHold ? ITER : 1][N], hold_b[kHold ? ITER : 1][N];
-  if (kHold) {
+  if constexpr (WIN) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      gather((const T *)p.w, ring.column(i), bits[i], hold_w[i]);
+      gather((const T *)p.b, ring.column(i), p.b ? bits[i] : 0, hold_b[i]);
+    }
+  } else if (kHold) {
 #pragma unroll
     for (int i = 0; i < ITER; ++i)
       if (ring.has(i)) weights(threadIdx.x + i * blockDim.x, hold_w[kHold ? i : 0], hold_b[kHold ? i : 0]);
@@ -210,6 +300,9 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
         for (int i = 0; i < ITER; ++i) {
           if (!ring.has(i)) continue;
           V::load_shared(here + i * ring.step, o[j][i]);
+          if constexpr (WIN) {
+            if (bits[i] != kWhole<VEC>) only(o[j][i], bits[i]);
+          }
 #pragma unroll
           for (int c = 0; c < N; ++c) s = add(s, o[j][i][c]);
         }
@@ -236,8 +329,12 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
       for (int i = 0; i < ITER; ++i) {
         if (!ring.has(i)) continue;
 #pragma unroll
+        for (int c = 0; c < N; ++c) o[j][i][c] = add(o[j][i][c], minus);
+        if constexpr (WIN) {
+          if (bits[i] != kWhole<VEC>) only(o[j][i], bits[i]);
+        }
+#pragma unroll
         for (int c = 0; c < N; ++c) {
-          o[j][i][c] = add(o[j][i][c], minus);
           s1 = add(s1, o[j][i][c]);
           s2 = fma(o[j][i][c], o[j][i][c], s2);
         }
@@ -267,8 +364,14 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
         if (!kHold) weights(v, w, b);
 #pragma unroll
         for (int c = 0; c < N; ++c) o[j][i][c] = fma(o[j][i][c], w[c], b[c]);
-        V::store(reinterpret_cast<T *>((uint8_t *)p.n + ring.offset(r_) + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step),
-                 o[j][i]);
+        T *out = reinterpret_cast<T *>((uint8_t *)p.n + ring.offset(r_) + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step);
+        if constexpr (WIN) {
+          if (bits[i] != kWhole<VEC>) {
+            scatter(out, bits[i], o[j][i]);
+            continue;
+          }
+        }
+        V::store(out, o[j][i]);
       }
     }
     if (++stage == ring.stages) stage = 0;
@@ -288,8 +391,8 @@ struct LnBwdParams {
 
 // S: float, or double for rows of at most 32 values, where u - mean(u) - z mean(u z) all but cancels (in a row of one or two
 // values what is left is of the order of eps): such rows are computed in 64 bits from x itself, its statistics too.
-// ROWS: rows that a block takes at a time, as in the forward.
-template <typename T, int VEC, int ITER, bool KEPT, typename S, int ROWS>
+// ROWS, WIN: as in the forward.
+template <typename T, int VEC, int ITER, bool KEPT, typename S, int ROWS, bool WIN>
 __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln_bwd_kernel(const LnBwdParams p, const Geometry geom) {
   using V = Lanes<T, VEC, S>;
   using L = typename V::L;
@@ -297,10 +400,16 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
   constexpr bool kWide = sizeof(S) == 8;
   constexpr bool kHold = ITER * VEC <= 16 && ITER <= 4;
   static_assert(ROWS == 1 || (VEC > 1 && kHold), "several rows at a time stay in registers");
+  static_assert(!WIN || (kHold && !KEPT), "windows hold their weights, and read x");
   constexpr int kDn = 0, kX = 1, kIn = 2;    // a row's buffers in a stage; kX holds the codes where they are copied
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ SumBuf sums;
-  const Ring<T, VEC, ITER> ring(dyn, geom, p.T, p.d);
+  const RowsOf<T, VEC, ITER, WIN> ring(dyn, geom, p.T, p.d);
+  uint32_t bits[WIN ? ITER : 1];
+  if constexpr (WIN) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) bits[i] = ring.valid(i);
+  }
   int half = 0;
   const S inv_d = S(1) / (S)p.d;
   const bool has_in = p.dx_in != nullptr;
@@ -340,7 +449,10 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
   }
   for (int s = 0; s < ring.stages - 1; ++s) fetch(blockIdx.x + s * turn, s);
   L hold_w[kHold ? ITER : 1][N];
-  if (kHold) {
+  if constexpr (WIN) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) gather((const T *)p.w, ring.column(i), bits[i], hold_w[i]);
+  } else if (kHold) {
 #pragma unroll
     for (int i = 0; i < ITER; ++i)
       if (ring.has(i)) V::load((const T *)p.w + (int64_t)(threadIdx.x + i * blockDim.x) * VEC, hold_w[kHold ? i : 0]);
@@ -430,6 +542,12 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
           L(&u)[N] = hold_d[j][kHold ? i : 0], (&z)[N] = hold_z[j][kHold ? i : 0];
           V::load_shared(here + (j * per_row + kDn) * ring.row_bytes + i * ring.step, u);
           normed(j, i, z);
+          if constexpr (WIN) {
+            if (bits[i] != kWhole<VEC>) {
+              only(u, bits[i]);
+              only(z, bits[i]);
+            }
+          }
 #pragma unroll
           for (int c = 0; c < N; ++c) {
             acc_b[i][c] = add(acc_b[i][c], u[c]);
@@ -475,7 +593,14 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
           acc_w[i][c] = fma(u[c], z[c], acc_w[i][c]);
           g[c] = fma(fma(z[c], Muz, fma(u[c], w[c], Mu)), R, g[c]);
         }
-        V::store(reinterpret_cast<T *>((uint8_t *)p.dx + off + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step), g);
+        T *out = reinterpret_cast<T *>((uint8_t *)p.dx + off + (VEC > 1 ? 0u : (uint32_t)sizeof(T) * threadIdx.x) + i * ring.step);
+        if constexpr (WIN) {
+          if (bits[i] != kWhole<VEC>) {
+            scatter(out, bits[i], g);
+            continue;
+          }
+        }
+        V::store(out, g);
       }
     }
     if (++stage == ring.stages) stage = 0;
@@ -484,9 +609,15 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
     if (!ring.has(i)) continue;
-    float *dst = p.part + (int64_t)blockIdx.x * p.d + (int64_t)(threadIdx.x + i * blockDim.x) * VEC;
-    put_part(dst, acc_w[i]);
-    put_part(dst + (int64_t)gridDim.x * p.d, acc_b[i]);
+    if constexpr (WIN) {
+      float *dst = p.part + (int64_t)blockIdx.x * p.d + ring.column(i);
+      scatter(dst, bits[i], acc_w[i]);
+      scatter(dst + (int64_t)gridDim.x * p.d, bits[i], acc_b[i]);
+    } else {
+      float *dst = p.part + (int64_t)blockIdx.x * p.d + (int64_t)(threadIdx.x + i * blockDim.x) * VEC;
+      put_part(dst, acc_w[i]);
+      put_part(dst + (int64_t)gridDim.x * p.d, acc_b[i]);
+    }
   }
 }
 
@@ -602,34 +733,56 @@ __global__ void __launch_bounds__(kRestoreThreads) ln_restore_kernel(const uint8
   }
 }
 
-template <typename T, int VEC, int ITER> static int ln_launch_fwd(const LnFwdParams &p, const Shape &sh, cudaStream_t s) {
+// Rows of words for rows that start anywhere; vec 1 where a thread would have to hold too many values.
+static Shape windows_of(int d, int dtype) {
+  const int es = dtype == MOE_BF16 ? 2 : 4, vec = 16 / es, nvec = (d + 2 * vec - 2) / vec;   // words, wherever the row starts
+  Shape s;
+  s.vec = vec;
+  s.iter = 1;
+  while (s.iter * kMaxThreads < nvec) s.iter *= 2;
+  s.threads = ((nvec + s.iter - 1) / s.iter + 31) / 32 * 32;
+  s.row_bytes = (uint32_t)nvec * 16;
+  if (s.iter * vec > 16) s.vec = 1;
+  return s;
+}
+
+template <typename T, int VEC, int ITER, bool WIN> static int ln_launch_fwd(const LnFwdParams &p, const Shape &sh, cudaStream_t s) {
   const int threads = sh.iter == 1 ? 2 * kMaxThreads : kMaxThreads;
-  int64_t grid = (int64_t)sm_count() * per_sm(sh, 1, threads);
+  const int64_t sms = sm_count() / 8 * 8;   // (of windows all rows of a block have to start alike)
+  int64_t grid = sms * per_sm(sh, 1, threads);
   // Two rows at a time where a thread has one vector of each and blocks have more rows than one: 16.4 against 18.6 us at T =
   // 8192, d = 2048 bf16, 58.6 against 71.9 at 16384 x 4096; for four rows 2.5 against 2.3 (nothing is shared then).
   if constexpr (VEC > 1 && ITER == 1) {
     if (p.T > grid) {
-      grid = (int64_t)sm_count() * per_sm(sh, 2, threads);
+      grid = sms * per_sm(sh, 2, threads);
       if (grid > p.T) grid = p.T;
-      if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true, 2>>(p, sh, 2, (int)grid, s);
-      return launch<ln_fwd_kernel<T, VEC, ITER, false, 2>>(p, sh, 2, (int)grid, s);
+      if constexpr (!WIN) {
+        if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true, 2, false>>(p, sh, 2, (int)grid, s);
+      }
+      return launch<ln_fwd_kernel<T, VEC, ITER, false, 2, WIN>>(p, sh, 2, (int)grid, s);
     }
   }
   if (grid > p.T) grid = p.T;
-  if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true, 1>>(p, sh, 1, (int)grid, s);
-  return launch<ln_fwd_kernel<T, VEC, ITER, false, 1>>(p, sh, 1, (int)grid, s);
+  if constexpr (!WIN) {
+    if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true, 1, false>>(p, sh, 1, (int)grid, s);
+  }
+  return launch<ln_fwd_kernel<T, VEC, ITER, false, 1, WIN>>(p, sh, 1, (int)grid, s);
 }
-template <typename T, int VEC, int ITER, typename S = float>
+template <typename T, int VEC, int ITER, bool WIN, typename S = float>
 static int ln_launch_bwd(const LnBwdParams &p, const Shape &sh, int rows, int grid, cudaStream_t s) {
   const int tensors = rows * (p.dx_in ? 3 : 2);
   if constexpr (VEC > 1 && ITER == 1) {
     if (rows == 2) {
-      if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S, 2>>(p, sh, tensors, grid, s);
-      return launch<ln_bwd_kernel<T, VEC, ITER, false, S, 2>>(p, sh, tensors, grid, s);
+      if constexpr (!WIN) {
+        if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S, 2, false>>(p, sh, tensors, grid, s);
+      }
+      return launch<ln_bwd_kernel<T, VEC, ITER, false, S, 2, WIN>>(p, sh, tensors, grid, s);
     }
   }
-  if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S, 1>>(p, sh, tensors, grid, s);
-  return launch<ln_bwd_kernel<T, VEC, ITER, false, S, 1>>(p, sh, tensors, grid, s);
+  if constexpr (!WIN) {
+    if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S, 1, false>>(p, sh, tensors, grid, s);
+  }
+  return launch<ln_bwd_kernel<T, VEC, ITER, false, S, 1, WIN>>(p, sh, tensors, grid, s);
 }
 template <typename T, int VEC>
 static int ln_launch_restore(const void *codes, const void *scales, const void *w, const void *b, int64_t T_, int d, void *n,
@@ -653,21 +806,37 @@ static int ln_bwd_blocks(int64_t T, const Shape &s, int tensors) {
   return b < 1 ? 1 : (int)b;
 }
 
-#define MOE_LN_DISPATCH(FN, ...)                                                     \
-  do {                                                                               \
-    if (dtype == MOE_BF16) {                                                         \
-      if (sh.vec == 8 && sh.iter == 1) rc = FN<__nv_bfloat16, 8, 1>(__VA_ARGS__);    \
-      else if (sh.vec == 8) rc = FN<__nv_bfloat16, 8, 2>(__VA_ARGS__);               \
-      else if (sh.iter == 4) rc = FN<__nv_bfloat16, 1, 4>(__VA_ARGS__);              \
-      else rc = FN<__nv_bfloat16, 1, 16>(__VA_ARGS__);                               \
-    } else {                                                                         \
-      if (sh.vec == 4 && sh.iter == 1) rc = FN<float, 4, 1>(__VA_ARGS__);            \
-      else if (sh.vec == 4 && sh.iter == 2) rc = FN<float, 4, 2>(__VA_ARGS__);       \
-      else if (sh.vec == 4) rc = FN<float, 4, 4>(__VA_ARGS__);                       \
-      else if (sh.iter == 4) rc = FN<float, 1, 4>(__VA_ARGS__);                      \
-      else rc = FN<float, 1, 16>(__VA_ARGS__);                                       \
-    }                                                                                \
+#define MOE_LN_DISPATCH(FN, WIN, ...)                                                                 \
+  do {                                                                                                \
+    if (dtype == MOE_BF16) {                                                                          \
+      if (sh.vec == 8 && sh.iter == 1) rc = FN<__nv_bfloat16, 8, 1, WIN>(__VA_ARGS__);                \
+      else if (sh.vec == 8) rc = FN<__nv_bfloat16, 8, 2, WIN>(__VA_ARGS__);                           \
+      else if (sh.iter == 4) rc = FN<__nv_bfloat16, 1, 4, false>(__VA_ARGS__);                        \
+      else rc = FN<__nv_bfloat16, 1, 16, false>(__VA_ARGS__);                                         \
+    } else {                                                                                          \
+      if (sh.vec == 4 && sh.iter == 1) rc = FN<float, 4, 1, WIN>(__VA_ARGS__);                        \
+      else if (sh.vec == 4 && sh.iter == 2) rc = FN<float, 4, 2, WIN>(__VA_ARGS__);                   \
+      else if (sh.vec == 4) rc = FN<float, 4, 4, WIN>(__VA_ARGS__);                                   \
+      else if (sh.iter == 4) rc = FN<float, 1, 4, false>(__VA_ARGS__);                                \
+      else rc = FN<float, 1, 16, false>(__VA_ARGS__);                                                 \
+    }                                                                                                 \
   } while (0)
+
+// How a call's rows are read: as vectors, as windows of them (where rows start anywhere, nothing is kept in 8 bits, and there
+// are enough rows for what the windows' weights and partial rows cost once per block), or value by value. Windows and values, in
+// us: 8192 x 2047 bf16 forward 24.8 and 49.1, backward 51.9 and 54.9; 8192 x 1537 fp32 26.2 and 48.7, 42.6 and 52.4; 1023 x 1537
+// fp32 5.6 and 8.0, 10.6 and 10.3; 500 x 333 bf16 3.1 and 2.8, 6.9 and 6.5.
+constexpr int64_t kWindowsFwd = 4 * 152, kWindowsBwd = 8 * 152;   // rows, more than
+struct How {
+  Shape sh;
+  bool win;
+};
+static How how(int d, int dtype, bool may) {
+  const Shape sh = shape_of(d, dtype);
+  if (sh.vec > 1 || !may || d <= 32) return {sh, false};
+  const Shape w = windows_of(d, dtype);
+  return w.vec > 1 ? How{w, true} : How{sh, false};
+}
 
 }  // namespace norm
 }  // namespace moe
@@ -677,9 +846,10 @@ using namespace moe::norm;
 
 extern "C" size_t moe_layer_norm_bwd_workspace_size(int T, int d, int dtype) {
   if (T < 0 || d < 1 || d > MOE_NORM_MAX_D || (dtype != MOE_F32 && dtype != MOE_BF16)) return 0;
-  const Shape sh = shape_of(d, dtype);
-  const int two = ln_bwd_blocks(T, sh, 2), three = ln_bwd_blocks(T, sh, 3);
-  return (size_t)2 * (two > three ? two : three) * d * sizeof(float) + 256;
+  int most = 0;
+  for (int may = 0; may < 2; ++may)
+    for (int tensors = 2; tensors <= 3; ++tensors) most = std::max(most, ln_bwd_blocks(T, how(d, dtype, may).sh, tensors));
+  return (size_t)2 * most * d * sizeof(float) + 256;
 }
 
 extern "C" int moe_layer_norm_fwd(const void *x, const void *w, const void *b, int T, int d, int dtype, float eps, void *n,
@@ -703,8 +873,10 @@ extern "C" int moe_layer_norm_fwd(const void *x, const void *w, const void *b, i
   p.d = d;
   p.nb = (int)act8::blocks_of(d);
   p.eps = eps;
-  const Shape sh = shape_of(d, dtype);
-  MOE_LN_DISPATCH(ln_launch_fwd, p, sh, (cudaStream_t)stream);
+  const How h = how(d, dtype, !codes && T > kWindowsFwd);
+  const Shape &sh = h.sh;
+  if (h.win) MOE_LN_DISPATCH(ln_launch_fwd, true, p, sh, (cudaStream_t)stream);
+  else MOE_LN_DISPATCH(ln_launch_fwd, false, p, sh, (cudaStream_t)stream);
   return rc;
 }
 
@@ -762,11 +934,12 @@ extern "C" int moe_layer_norm_bwd(const void *dn, const void *x, const void *cod
   p.nb = (int)act8::blocks_of(d);
   p.eps = eps;
   cudaStream_t s = (cudaStream_t)stream;
-  Shape sh = shape_of(d, dtype);
+  const How h = how(d, dtype, !kept && T > kWindowsBwd);
+  Shape sh = h.sh;
   int rows = 1, grid = ln_bwd_blocks(T, sh, dx_in ? 3 : 2);
-  // Two rows at a time where blocks have more rows than one: at T = 16384, d = 4096 bf16 86.8 against 89.0 us (from codes 84.7 against
-  // 91.0), at 8192 x 1024 fp32 18.8 against 21.4; not where bf16 rows are short enough for two blocks per SM: 26.8 against 25.7 at 8192
-  // x 2048, 15.7 against 15.0 at 8192 x 1024.
+  // Two rows at a time where blocks have more rows than one: at T = 16384, d = 4096 bf16 86.8 against 89.0 us (from codes 84.7
+  // against 91.0), at 8192 x 1024 fp32 18.8 against 21.4; not where bf16 rows are short enough for two blocks per SM: 26.8
+  // against 25.7 at 8192 x 2048, 15.7 against 15.0 at 8192 x 1024.
   if (sh.vec > 1 && sh.iter == 1 && T > grid && d > 32 && (dtype == MOE_F32 || sh.threads > kMaxThreads / 2)) {
     rows = 2;
     grid = ln_bwd_blocks(T, sh, dx_in ? 6 : 4);
@@ -775,10 +948,12 @@ extern "C" int moe_layer_norm_bwd(const void *dn, const void *x, const void *cod
     sh.vec = sh.iter = 1;
     sh.threads = 32;
     sh.row_bytes = ((uint32_t)d * (uint32_t)dtype_size(dtype) + 15) / 16 * 16 + 16;
-    if (dtype == MOE_BF16) rc = ln_launch_bwd<__nv_bfloat16, 1, 1, double>(p, sh, 1, grid, s);
-    else rc = ln_launch_bwd<float, 1, 1, double>(p, sh, 1, grid, s);
+    if (dtype == MOE_BF16) rc = ln_launch_bwd<__nv_bfloat16, 1, 1, false, double>(p, sh, 1, grid, s);
+    else rc = ln_launch_bwd<float, 1, 1, false, double>(p, sh, 1, grid, s);
+  } else if (h.win) {
+    MOE_LN_DISPATCH(ln_launch_bwd, true, p, sh, rows, grid, s);
   } else {
-    MOE_LN_DISPATCH(ln_launch_bwd, p, sh, rows, grid, s);
+    MOE_LN_DISPATCH(ln_launch_bwd, false, p, sh, rows, grid, s);
   }
   if (rc) return rc;
   const dim3 g((d + 31) / 32, db ? 2 : 1);

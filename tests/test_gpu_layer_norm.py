@@ -80,7 +80,10 @@ def test_kept(T, d, dtype):
     m, r = stats(s["x"])
     z = (s["x"].double() - m) * r
     nm, plain = LayerNorm(T, d, dtype, eps=EPS, keep="f8"), LayerNorm(T, d, dtype, eps=EPS)
-    assert torch.equal(nm.forward(s["x"], s["w"], s["b"]), plain.forward(s["x"], s["w"], s["b"]))
+    n, other = nm.forward(s["x"], s["w"], s["b"]), plain.forward(s["x"], s["w"], s["b"])
+    close(n, z * s["w"].double() + s["b"].double(), ("n", dtype))
+    # the same kernel where rows are whole words (else the sums' order may differ: each is within the bound of the formula)
+    assert torch.equal(n, other) or d * s["x"].element_size() % 16
     zq = act8_dequantize(nm.codes, nm.scales, torch.float32).double()
     # half a step of the codes (2^-4 of the value, 2^-10 of a scale that is at most max / 224), and z's own rounding
     top = torch.nn.functional.pad(z.abs(), (0, -d % 32)).view(T, -1, 32).amax(2).repeat_interleave(32, 1)[:, :d]
@@ -148,6 +151,37 @@ def test_rows_that_overflow_and_rows_that_are_not_finite(d, dtype):
         b = ref.backward(s["dn"][rest].contiguous(), s["w"], x=None if keep else s["x"][rest], dx_in=s["dres"][rest].contiguous())
         assert torch.equal(a["dx"][rest], b["dx"]) and torch.equal(a["dx"][1], s["dres"][1]) and a["dx"][3].isnan().all()
         assert a["dw"].isnan().any() and torch.isfinite(a["db"]).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [33, 34, 61, 63, 1023, 1537, 2045, 4082, 4089, 4095, 8177, 8186, 8191])
+@pytest.mark.parametrize("T", [1, 9, 700, 2435])
+def test_rows_that_start_anywhere(T, d, dtype):
+    """Odd row lengths, one row per block and many, next to rows that are not finite: nothing of a neighbour's row is read into a row's
+    sums, and nothing is written outside the rows."""
+    s = make(T, d, dtype, T * d)
+    m, r = stats(s["x"])
+    z = (s["x"].double() - m) * r
+    nm = LayerNorm(T, d, dtype, eps=EPS)
+    room = torch.full((T * d + 64,), 7.0, dtype=dtype, device="cuda")
+    nm.n = room[32:32 + T * d].view(T, d)
+    nm._out[0] = nm.n.data_ptr()
+    n = nm.forward(s["x"], s["w"], s["b"])
+    close(n, z * s["w"].double() + s["b"].double(), ("n", dtype))
+    assert room[:32].eq(7).all() and room[32 + T * d:].eq(7).all()
+    res = nm.backward(s["dn"], s["w"], x=s["x"], dx_in=s["dres"])
+    dx, dw, db = grads(s["dn"], z, r, s["w"], s["dres"])
+    close(res["dx"], dx, ("dx", dtype))
+    close(res["dw"], dw, ("dw", dtype))
+    close(res["db"], db, ("db", dtype))
+    if T > 8:
+        want, dx = n.clone(), res["dx"].clone()
+        x, bad = s["x"].clone(), torch.arange(3, T, 5, device="cuda")
+        x[bad] = float("inf")
+        ok = torch.ones(T, dtype=torch.bool, device="cuda")
+        ok[bad] = False
+        n, res = nm.forward(x, s["w"], s["b"]), nm.backward(s["dn"], s["w"], x=x, dx_in=s["dres"])
+        assert torch.equal(n[ok], want[ok]) and n[bad].isnan().all() and torch.equal(res["dx"][ok], dx[ok])
 
 
 @pytest.mark.parametrize("dtype", TYPES)
