@@ -187,6 +187,35 @@ template <typename T, int N> __device__ __forceinline__ void scatter(T *p, uint3
     if (bits >> (2 * c + 1) & 1) put_value(p + 2 * c + 1, y);
   }
 }
+// A vector of a window lies in one block of 32 values or in two: `bound` of its values (those before the row's first counted) are the
+// first one's.
+struct Split {
+  int b0, b1, bound;
+  template <int VEC> static __device__ __forceinline__ Split of(int column, int d) {
+    Split x;
+    x.b0 = max(column, 0) / act8::kBlock;
+    x.b1 = max(min(column + VEC, d) - 1, 0) / act8::kBlock;
+    x.bound = min(max((x.b0 + 1) * act8::kBlock - column, 0), VEC);
+    return x;
+  }
+};
+// The values of a vector's codes, each at its block's scale
+template <int N> __device__ __forceinline__ void at_scales(const uint32_t *q, float s0, float s1, int bound, F2 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    float f[4];
+    act8::unpack4(q[i], f);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) f[c] *= 4 * i + c < bound ? s0 : s1;
+    v[2 * i] = pair(f[0], f[1]);
+    v[2 * i + 1] = pair(f[2], f[3]);
+  }
+}
+template <int VEC> __device__ __forceinline__ void copy_codes(uint32_t dst, const uint8_t *src, int64_t left) {   // VEC of them, none past the end
+  const int n = left < VEC ? (int)left : VEC;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(VEC > 1 ? VEC : 4), "r"(n) : "memory");
+}
+
 template <typename T, int VEC, int ITER, bool WIN>
 using RowsOf = typename std::conditional<WIN, Windows<T, VEC, ITER>, Ring<T, VEC, ITER>>::type;
 
@@ -234,15 +263,65 @@ __device__ __forceinline__ void keep(const LnFwdParams &p, int64_t row, int v, b
 }
 
 // ROWS: rows that a block takes at a time, which share the reductions' exchanges and barriers. WIN: Windows.
+// keep() for a window's vector. The largest magnitudes of the row's blocks meet in shared memory (`tops`, fp32 bits, zeros at first) ...
+template <int N> __device__ __forceinline__ void meet(uint32_t *tops, const Split &x, const F2 (&z)[N]) {
+  float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    float f[2];
+    split(z[c], f[0], f[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (2 * c + k < x.bound) m0 = act8::larger(m0, f[k], 0.0f);
+      else m1 = act8::larger(m1, f[k], 0.0f);
+    }
+  }
+  atomicMax(tops + x.b0, __float_as_uint(m0));
+  if (x.b1 != x.b0) atomicMax(tops + x.b1, __float_as_uint(m1));
+}
+// ... then codes, and the scales of the blocks that begin in this vector
+template <int VEC, int N>
+__device__ __forceinline__ void keep_window(const LnFwdParams &p, int64_t row, int column, uint32_t bits, const uint32_t *tops, const Split &x,
+                                            const F2 (&z)[N]) {
+  const uint32_t byte0 = act8::scale_byte(tops[x.b0]), byte1 = act8::scale_byte(tops[x.b1]);
+  const float i0 = act8::inv_scale(byte0), i1 = act8::inv_scale(byte1);
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    float f[4];
+    split(z[2 * i], f[0], f[1]);
+    split(z[2 * i + 1], f[2], f[3]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const bool nan = (4 * i + c < x.bound ? byte0 : byte1) == 255u;
+      f[c] = nan ? 0.0f : f[c] * (4 * i + c < x.bound ? i0 : i1);
+    }
+    w[i] = act8::pack4(f[0], f[1], f[2], f[3]);
+  }
+  uint8_t *q = p.codes + row * p.d + column;   // row * d - lead, and so this, is a multiple of VEC
+  if (bits == kWhole<VEC>) {
+    if constexpr (N == 4) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(q) = w[0];
+  } else {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c)
+      if (bits >> c & 1) q[c] = (uint8_t)(w[c / 4] >> (8 * (c & 3)));
+  }
+  if (x.b0 * act8::kBlock >= column) p.scales[row * p.nb + x.b0] = (uint8_t)byte0;
+  if (x.b1 != x.b0) p.scales[row * p.nb + x.b1] = (uint8_t)byte1;
+}
+
 template <typename T, int VEC, int ITER, bool KEEP, int ROWS, bool WIN>
 __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(const LnFwdParams p, const Geometry geom) {
   using V = Lanes<T, VEC, float>;
   using L = typename V::L;
   constexpr int N = V::N;
   constexpr bool kHold = ITER * VEC <= 16 && ITER <= 4;
-  static_assert(!WIN || (kHold && !KEEP), "windows hold their weights, and keep nothing");
+  static_assert(!WIN || kHold, "windows hold their weights");
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ SumBuf sums;
+  __shared__ uint32_t tops[WIN && KEEP ? 2 : 1][ROWS][WIN && KEEP ? MOE_NORM_MAX_D / act8::kBlock : 1];   // two turns' in turn
+  int tops_at = 0;
   const RowsOf<T, VEC, ITER, WIN> ring(dyn, geom, p.T, p.d);
   uint32_t bits[WIN ? ITER : 1];
   if constexpr (WIN) {
@@ -289,6 +368,10 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
       fetch(row, 0);
     }
     ring.wait();
+    if constexpr (WIN && KEEP) {   // (read last two turns ago; the sums' barriers come before this turn's writes)
+      for (int i = threadIdx.x; i < ROWS * p.nb; i += blockDim.x) tops[tops_at][i / p.nb][i % p.nb] = 0;
+      if (blockDim.x == 32) __syncwarp();
+    }
     L o[ROWS][ITER][N];
     float m[ROWS];
 #pragma unroll
@@ -353,13 +436,27 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
       const L R = splat<L>(r), shift = splat<L>(-rest * r);
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (ring.has(i)) {
-#pragma unroll
-          for (int c = 0; c < N; ++c) o[j][i][c] = fma(o[j][i][c], R, shift);
-        }
-        if (KEEP) keep<VEC>(p, r_, v, ring.has(i), o[j][i]);
         if (!ring.has(i)) continue;
+#pragma unroll
+        for (int c = 0; c < N; ++c) o[j][i][c] = fma(o[j][i][c], R, shift);
+        if constexpr (WIN && KEEP) {
+          if (bits[i] != kWhole<VEC>) only(o[j][i], bits[i]);
+          meet(tops[tops_at][j], Split::of<VEC>(ring.column(i), p.d), o[j][i]);
+        }
+      }
+    }
+    if constexpr (WIN && KEEP) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const int64_t r_ = row + j * gridDim.x;
+      if (j > 0 && r_ >= p.T) break;
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if constexpr (KEEP && !WIN) keep<VEC>(p, r_, v, ring.has(i), o[j][i]);
+        if (!ring.has(i)) continue;
+        if constexpr (KEEP && WIN)
+          keep_window<VEC>(p, r_, ring.column(i), bits[i], tops[tops_at][j], Split::of<VEC>(ring.column(i), p.d), o[j][i]);
         L(&w)[N] = hold_w[kHold ? i : 0], (&b)[N] = hold_b[kHold ? i : 0];
         if (!kHold) weights(v, w, b);
 #pragma unroll
@@ -374,6 +471,7 @@ __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(
         V::store(out, o[j][i]);
       }
     }
+    tops_at ^= 1;
     if (++stage == ring.stages) stage = 0;
   }
 }
@@ -400,7 +498,7 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
   constexpr bool kWide = sizeof(S) == 8;
   constexpr bool kHold = ITER * VEC <= 16 && ITER <= 4;
   static_assert(ROWS == 1 || (VEC > 1 && kHold), "several rows at a time stay in registers");
-  static_assert(!WIN || (kHold && !KEPT), "windows hold their weights, and read x");
+  static_assert(!WIN || kHold, "windows hold their weights");
   constexpr int kDn = 0, kX = 1, kIn = 2;    // a row's buffers in a stage; kX holds the codes where they are copied
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ SumBuf sums;
@@ -428,13 +526,13 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
         ring.fetch(p.x, off, stage, at + kX);
       } else if (VEC > 1) {   // VEC bytes per vector, copied by the thread that reads them
         const uint32_t dst = ring.mine + (uint32_t)stage * ring.stage_bytes + codes_at + at * ring.row_bytes;
-        const uint8_t *src = p.codes + row * p.d + VEC * threadIdx.x;
+        const int64_t first = row * p.d + VEC * threadIdx.x;
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-          if (ring.has(i))
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst + i * VEC * blockDim.x),
-                         "l"(src + i * VEC * blockDim.x), "n"(VEC > 1 ? VEC : 4)
-                         : "memory");
+          if (!ring.has(i)) continue;
+          const int64_t from = first + i * VEC * blockDim.x;
+          if constexpr (WIN) copy_codes<VEC>(dst + i * VEC * blockDim.x, p.codes + from - ring.lead, p.T * p.d - from + ring.lead);
+          else copy_codes<VEC>(dst + i * VEC * blockDim.x, p.codes + from, VEC);
         }
       }
       if (has_in) ring.fetch(p.dx_in, off, stage, at + kIn);
@@ -459,7 +557,7 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
   }
   // the rows' statistics, and the scales of this thread's codes, are read one turn ahead
   float next_m[ROWS] = {}, next_r[ROWS] = {};
-  uint8_t next_s[ROWS][KEPT ? ITER : 1] = {};
+  uint8_t next_s[ROWS][KEPT ? ITER : 1] = {}, next_s1[ROWS][KEPT && WIN ? ITER : 1] = {};   // next_s1: of the second block
   auto ahead = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < ROWS; ++j, row += gridDim.x) {
@@ -468,8 +566,16 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
       next_r[j] = p.rstd[row];
       if (KEPT) {
 #pragma unroll
-        for (int i = 0; i < ITER; ++i)
-          if (ring.has(i)) next_s[j][KEPT ? i : 0] = p.scales[row * p.nb + (int)(threadIdx.x + i * blockDim.x) * VEC / act8::kBlock];
+        for (int i = 0; i < ITER; ++i) {
+          if (!ring.has(i)) continue;
+          if constexpr (WIN) {
+            const Split x = Split::of<VEC>(ring.column(i), p.d);
+            next_s[j][KEPT ? i : 0] = p.scales[row * p.nb + x.b0];
+            next_s1[j][KEPT && WIN ? i : 0] = p.scales[row * p.nb + x.b1];
+          } else {
+            next_s[j][KEPT ? i : 0] = p.scales[row * p.nb + (int)(threadIdx.x + i * blockDim.x) * VEC / act8::kBlock];
+          }
+        }
       }
     }
   };
@@ -481,14 +587,17 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
       fetch(row, 0);
     }
     S m[ROWS], r[ROWS];
-    float sc[ROWS][KEPT ? ITER : 1];
+    float sc[ROWS][KEPT ? ITER : 1], sc1[ROWS][KEPT && WIN ? ITER : 1];
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
       m[j] = next_m[j];
       r[j] = next_r[j];
       if (KEPT) {
 #pragma unroll
-        for (int i = 0; i < ITER; ++i) sc[j][KEPT ? i : 0] = act8::scale_value(next_s[j][KEPT ? i : 0]);
+        for (int i = 0; i < ITER; ++i) {
+          sc[j][KEPT ? i : 0] = act8::scale_value(next_s[j][KEPT ? i : 0]);
+          if (WIN) sc1[j][KEPT && WIN ? i : 0] = act8::scale_value(next_s1[j][KEPT && WIN ? i : 0]);
+        }
       }
     }
     ahead(row + turn);
@@ -513,7 +622,13 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
     // z (without KEPT: before the rest of the mean is taken off) of the i-th vector of the j-th row
     auto normed = [&](int j, int i, L (&z)[N]) {
       if constexpr (KEPT) {
-        if constexpr (VEC > 1) {
+        if constexpr (WIN) {
+          uint32_t q[N / 2];
+          const uint32_t a = codes_here + j * per_row * ring.row_bytes + i * VEC * blockDim.x;
+#pragma unroll
+          for (int k = 0; k < N / 2; ++k) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(q[k]) : "r"(a + 4 * k) : "memory");
+          at_scales(q, sc[j][i], sc1[j][i], Split::of<VEC>(ring.column(i), p.d).bound, z);
+        } else if constexpr (VEC > 1) {
           get_codes(codes_here + j * per_row * ring.row_bytes + i * VEC * blockDim.x, z, sc[j][i]);
         } else {
           z[0] = (S)(act8::unpack1(p.codes[row * p.d + threadIdx.x + (int64_t)i * blockDim.x]) * sc[j][i]);
@@ -733,12 +848,75 @@ __global__ void __launch_bounds__(kRestoreThreads) ln_restore_kernel(const uint8
   }
 }
 
+// Rows that start anywhere: a thread's rows lie a multiple of VEC apart, so its words start at the same column in all of them.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kRestoreThreads) ln_restore_windows_kernel(const uint8_t *__restrict__ codes,
+                                                                             const uint8_t *__restrict__ scales,
+                                                                             const T *__restrict__ w, const T *__restrict__ b,
+                                                                             int64_t T_, int d, int nb, int words, int64_t step,
+                                                                             T *__restrict__ n) {
+  using V = Lanes<T, VEC, float>;
+  constexpr int N = V::N;
+  const int64_t id = (int64_t)blockIdx.x * kRestoreThreads + threadIdx.x, row0 = id / words;
+  if (row0 >= step) return;
+  const int column = (int)(id - row0 * words) * VEC - (int)(row0 * d % VEC);
+  uint32_t bits = 0;
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) bits |= (uint32_t)((unsigned)(column + c) < (unsigned)d) << c;
+  if (bits == 0) return;
+  F2 W[N], B[N];
+  gather(w, column, bits, W);
+  gather(b, column, b ? bits : 0, B);
+  const Split x = Split::of<VEC>(column, d);
+  constexpr int kRows = 4;   // in flight
+  for (int64_t r0 = row0; r0 < T_; r0 += kRows * step) {
+    uint32_t q[kRows][N / 2];
+    float s0[kRows], s1[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t r = r0 + k * step;
+      if (r >= T_) continue;
+      const uint8_t *src = codes + r * d + column;
+      if (bits == kWhole<VEC>) {
+        if constexpr (N == 4) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+          q[k][0] = v.x;
+          q[k][N / 2 - 1] = v.y;
+        } else {
+          q[k][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) q[k][i] = 0;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+          if (bits >> c & 1) q[k][c / 4] |= (uint32_t)__ldg(src + c) << (8 * (c & 3));
+      }
+      s0[k] = act8::scale_value(__ldg(scales + r * nb + x.b0));
+      s1[k] = act8::scale_value(__ldg(scales + r * nb + x.b1));
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t r = r0 + k * step;
+      if (r >= T_) continue;
+      F2 v[N];
+      at_scales(q[k], s0[k], s1[k], x.bound, v);
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[c] = fma(v[c], W[c], B[c]);
+      T *out = n + r * d + column;
+      if (bits == kWhole<VEC>) V::store(out, v);
+      else scatter(out, bits, v);
+    }
+  }
+}
+
 // Rows of words for rows that start anywhere; vec 1 where a thread would have to hold too many values.
 static Shape windows_of(int d, int dtype) {
   const int es = dtype == MOE_BF16 ? 2 : 4, vec = 16 / es, nvec = (d + 2 * vec - 2) / vec;   // words, wherever the row starts
   Shape s;
   s.vec = vec;
-  s.iter = 1;
+  // (fp32: two words per thread before more than 256 threads: 35 against 43 us for the backward at 8192 x 1537)
+  s.iter = dtype == MOE_F32 && nvec > kMaxThreads / 2 ? 2 : 1;
   while (s.iter * kMaxThreads < nvec) s.iter *= 2;
   s.threads = ((nvec + s.iter - 1) / s.iter + 31) / 32 * 32;
   s.row_bytes = (uint32_t)nvec * 16;
@@ -756,16 +934,12 @@ template <typename T, int VEC, int ITER, bool WIN> static int ln_launch_fwd(cons
     if (p.T > grid) {
       grid = sms * per_sm(sh, 2, threads);
       if (grid > p.T) grid = p.T;
-      if constexpr (!WIN) {
-        if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true, 2, false>>(p, sh, 2, (int)grid, s);
-      }
+      if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true, 2, WIN>>(p, sh, 2, (int)grid, s);
       return launch<ln_fwd_kernel<T, VEC, ITER, false, 2, WIN>>(p, sh, 2, (int)grid, s);
     }
   }
   if (grid > p.T) grid = p.T;
-  if constexpr (!WIN) {
-    if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true, 1, false>>(p, sh, 1, (int)grid, s);
-  }
+  if (p.codes) return launch<ln_fwd_kernel<T, VEC, ITER, true, 1, WIN>>(p, sh, 1, (int)grid, s);
   return launch<ln_fwd_kernel<T, VEC, ITER, false, 1, WIN>>(p, sh, 1, (int)grid, s);
 }
 template <typename T, int VEC, int ITER, bool WIN, typename S = float>
@@ -773,15 +947,11 @@ static int ln_launch_bwd(const LnBwdParams &p, const Shape &sh, int rows, int gr
   const int tensors = rows * (p.dx_in ? 3 : 2);
   if constexpr (VEC > 1 && ITER == 1) {
     if (rows == 2) {
-      if constexpr (!WIN) {
-        if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S, 2, false>>(p, sh, tensors, grid, s);
-      }
+      if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S, 2, WIN>>(p, sh, tensors, grid, s);
       return launch<ln_bwd_kernel<T, VEC, ITER, false, S, 2, WIN>>(p, sh, tensors, grid, s);
     }
   }
-  if constexpr (!WIN) {
-    if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S, 1, false>>(p, sh, tensors, grid, s);
-  }
+  if (p.codes) return launch<ln_bwd_kernel<T, VEC, ITER, true, S, 1, WIN>>(p, sh, tensors, grid, s);
   return launch<ln_bwd_kernel<T, VEC, ITER, false, S, 1, WIN>>(p, sh, tensors, grid, s);
 }
 template <typename T, int VEC>
@@ -794,6 +964,20 @@ static int ln_launch_restore(const void *codes, const void *scales, const void *
   ln_restore_kernel<T, VEC><<<(unsigned)grid, kRestoreThreads, 0, s>>>((const uint8_t *)codes, (const uint8_t *)scales,
                                                                        (const T *)w, (const T *)b, T_, d,
                                                                        (int)act8::blocks_of(d), step, (T *)n);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
+template <typename T, int VEC>
+static int ln_launch_restore_windows(const void *codes, const void *scales, const void *w, const void *b, int64_t T_, int d, void *n,
+                                     cudaStream_t s) {
+  const int words = (d + 2 * VEC - 2) / VEC;
+  int64_t step = ((int64_t)sm_count() * 8 * kRestoreThreads + words - 1) / words;   // eight blocks per SM, about
+  step = (step + VEC - 1) / VEC * VEC;
+  if (step > T_) step = T_;
+  const int64_t grid = (step * words + kRestoreThreads - 1) / kRestoreThreads;
+  ln_restore_windows_kernel<T, VEC><<<(unsigned)grid, kRestoreThreads, 0, s>>>(
+      (const uint8_t *)codes, (const uint8_t *)scales, (const T *)w, (const T *)b, T_, d, (int)act8::blocks_of(d), words, step, (T *)n);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
@@ -873,7 +1057,7 @@ extern "C" int moe_layer_norm_fwd(const void *x, const void *w, const void *b, i
   p.d = d;
   p.nb = (int)act8::blocks_of(d);
   p.eps = eps;
-  const How h = how(d, dtype, !codes && T > kWindowsFwd);
+  const How h = how(d, dtype, T > kWindowsFwd);
   const Shape &sh = h.sh;
   if (h.win) MOE_LN_DISPATCH(ln_launch_fwd, true, p, sh, (cudaStream_t)stream);
   else MOE_LN_DISPATCH(ln_launch_fwd, false, p, sh, (cudaStream_t)stream);
@@ -898,11 +1082,14 @@ extern "C" int moe_layer_norm_restore(const void *codes, const void *scales, con
     MOE_CHECK_LAUNCH();
     return MOE_OK;
   }
-  if (dtype == MOE_BF16)
-    return d % 8 == 0 ? ln_launch_restore<__nv_bfloat16, 8>(codes, scales, w, b, T, d, n, s)
-                      : ln_launch_restore<__nv_bfloat16, 1>(codes, scales, w, b, T, d, n, s);
-  return d % 4 == 0 ? ln_launch_restore<float, 4>(codes, scales, w, b, T, d, n, s)
-                    : ln_launch_restore<float, 1>(codes, scales, w, b, T, d, n, s);
+  if (dtype == MOE_BF16) {
+    if (d % 8 == 0) return ln_launch_restore<__nv_bfloat16, 8>(codes, scales, w, b, T, d, n, s);
+    return T > kWindowsFwd ? ln_launch_restore_windows<__nv_bfloat16, 8>(codes, scales, w, b, T, d, n, s)
+                           : ln_launch_restore<__nv_bfloat16, 1>(codes, scales, w, b, T, d, n, s);
+  }
+  if (d % 4 == 0) return ln_launch_restore<float, 4>(codes, scales, w, b, T, d, n, s);
+  return T > kWindowsFwd ? ln_launch_restore_windows<float, 4>(codes, scales, w, b, T, d, n, s)
+                         : ln_launch_restore<float, 1>(codes, scales, w, b, T, d, n, s);
 }
 
 extern "C" int moe_layer_norm_bwd(const void *dn, const void *x, const void *codes, const void *scales, const float *mean,
@@ -934,7 +1121,7 @@ extern "C" int moe_layer_norm_bwd(const void *dn, const void *x, const void *cod
   p.nb = (int)act8::blocks_of(d);
   p.eps = eps;
   cudaStream_t s = (cudaStream_t)stream;
-  const How h = how(d, dtype, !kept && T > kWindowsBwd);
+  const How h = how(d, dtype, T > kWindowsBwd);
   Shape sh = h.sh;
   int rows = 1, grid = ln_bwd_blocks(T, sh, dx_in ? 3 : 2);
   // Two rows at a time where blocks have more rows than one: at T = 16384, d = 4096 bf16 86.8 against 89.0 us (from codes 84.7

@@ -74,7 +74,7 @@ def test_forward_and_backward(T, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("T,d", SHAPES)
+@pytest.mark.parametrize("T,d", SHAPES + [(700, 33), (2435, 1023), (2435, 1537), (1300, 4089), (1300, 63), (1221, 8177), (611, 8191), (1300, 2046)])
 def test_kept(T, d, dtype):
     s = make(T, d, dtype, T + d)
     m, r = stats(s["x"])
@@ -185,7 +185,7 @@ def test_rows_that_start_anywhere(T, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("T,d", [(2431, 1024), (1300, 2048), (611, 4096)])
+@pytest.mark.parametrize("T,d", [(2431, 1024), (1300, 2048), (611, 4096), (1223, 1537), (1300, 2045), (2431, 97)])
 def test_many_rows_some_not_finite(T, d, dtype):
     """Rows that share a block's reductions: what stands in one changes no bit of the others, whatever their number."""
     s = make(T, d, dtype, T)
