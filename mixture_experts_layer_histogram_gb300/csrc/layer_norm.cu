@@ -9,16 +9,17 @@
 // place of the 64 that x takes in bf16); restore() gives z w + b again for the block's own backward, and
 // the backward reads z from the codes.
 //
-// Rows whose length is no multiple of 16 bytes are read and written as the words that cover them (Windows), where that pays.
 // HBM-bound, like the RMS norms (norm.cu): a thread block works on one row at a time, or on two, which share their reductions
 // (the forward needs two per row, the deviations waiting for the mean), read once through the ring of rows and written once;
-// codes come through the ring as well, 8 (fp32: 4) bytes per thread beside its 16-byte vectors. The weight gradients are summed
-// over a block's rows in registers and its partial rows added up in a fixed order.
-// Measured (bf16, in replayed graphs): T = 8192, d = 2048 forward 16.1 us (67 MB), with codes 20.1 (84 MB), restore 8.3 (51 MB),
-// backward with dx_in 25.7 from x or codes (135 or 118 MB); T = 16384, d = 4096 forward 57.9, backward with dx_in 86.8 (537 MB,
-// 6.2 TB/s; 94 in a stream of calls with other inputs each time), from codes 84.8; fp32 T = 1023, d = 1537 backward 10.2 us; four
-// rows of 2048 2.3 and 4.0 us. Before dn and z stayed in registers between the backward's two passes it took 4% longer. Two
-// vectors per thread or a warp per row (fewer instructions, no barriers) took the forward as long as one row at a time, 18.6 us.
+// codes come through the ring as well, 8 (fp32: 4) bytes per thread beside its 16-byte vectors. Rows whose length is no multiple
+// of 16 bytes are read and written as the words that cover them (Windows), where there are enough of them. The weight gradients
+// are summed over a block's rows in registers and its partial rows added up in a fixed order.
+// Measured (bf16, in replayed graphs): T = 8192, d = 2048 forward 15.3 us (67 MB), with codes 19.7 (84 MB), restore 8.2 (51 MB),
+// backward with dx_in 26 from x, 24.7 from codes (135 or 118 MB); T = 16384, d = 4096 forward 56, backward with dx_in 87 (537
+// MB, 6.2 TB/s; 90 in a stream of calls with other inputs each time), from codes 85; d = 2047 forward 24.9, backward 48.7,
+// keeping 8 bits 42.9, 15.0 and 58; fp32 T = 1023, d = 1537 forward 5.8, backward 8.8 us; four rows of 2048 2.3 and 4.0 us.
+// Before dn and z stayed in registers between the backward's two passes it took 4% longer. Two vectors per thread or a warp per
+// row (fewer instructions, no barriers) took the forward as long as one row at a time, 18.6 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -187,8 +188,8 @@ template <typename T, int N> __device__ __forceinline__ void scatter(T *p, uint3
     if (bits >> (2 * c + 1) & 1) put_value(p + 2 * c + 1, y);
   }
 }
-// A vector of a window lies in one block of 32 values or in two: `bound` of its values (those before the row's first counted) are the
-// first one's.
+// A vector of a window lies in one block of 32 values or in two: `bound` of its values (those before the row's first counted)
+// are the first one's.
 struct Split {
   int b0, b1, bound;
   template <int VEC> static __device__ __forceinline__ Split of(int column, int d) {
@@ -262,8 +263,8 @@ __device__ __forceinline__ void keep(const LnFwdParams &p, int64_t row, int v, b
   if (v * VEC % act8::kBlock == 0) p.scales[row * p.nb + v * VEC / act8::kBlock] = (uint8_t)byte;
 }
 
-// ROWS: rows that a block takes at a time, which share the reductions' exchanges and barriers. WIN: Windows.
-// keep() for a window's vector. The largest magnitudes of the row's blocks meet in shared memory (`tops`, fp32 bits, zeros at first) ...
+// ROWS: rows that a block takes at a time, which share the reductions' exchanges and barriers. WIN: Windows. keep() for a
+// window's vector. The largest magnitudes of the row's blocks meet in shared memory (`tops`, fp32 bits, zeros at first) ...
 template <int N> __device__ __forceinline__ void meet(uint32_t *tops, const Split &x, const F2 (&z)[N]) {
   float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
@@ -915,8 +916,10 @@ static Shape windows_of(int d, int dtype) {
   const int es = dtype == MOE_BF16 ? 2 : 4, vec = 16 / es, nvec = (d + 2 * vec - 2) / vec;   // words, wherever the row starts
   Shape s;
   s.vec = vec;
-  // (fp32: two words per thread before more than 256 threads: 35 against 43 us for the backward at 8192 x 1537)
-  s.iter = dtype == MOE_F32 && nvec > kMaxThreads / 2 ? 2 : 1;
+  // Two words per thread where a block of more than 256 threads would have an SM to itself: always for fp32 (35 against 43 us
+  // for the backward at 8192 x 1537), for bf16 while it would be few more (49 against 52 at 8192 x 2047; 67 against 57 at 8192 x
+  // 3001).
+  s.iter = nvec > kMaxThreads / 2 && (dtype == MOE_F32 || nvec <= 320) ? 2 : 1;
   while (s.iter * kMaxThreads < nvec) s.iter *= 2;
   s.threads = ((nvec + s.iter - 1) / s.iter + 31) / 32 * 32;
   s.row_bytes = (uint32_t)nvec * 16;
@@ -1006,11 +1009,12 @@ static int ln_bwd_blocks(int64_t T, const Shape &s, int tensors) {
     }                                                                                                 \
   } while (0)
 
-// How a call's rows are read: as vectors, as windows of them (where rows start anywhere, nothing is kept in 8 bits, and there
-// are enough rows for what the windows' weights and partial rows cost once per block), or value by value. Windows and values, in
-// us: 8192 x 2047 bf16 forward 24.8 and 49.1, backward 51.9 and 54.9; 8192 x 1537 fp32 26.2 and 48.7, 42.6 and 52.4; 1023 x 1537
-// fp32 5.6 and 8.0, 10.6 and 10.3; 500 x 333 bf16 3.1 and 2.8, 6.9 and 6.5.
-constexpr int64_t kWindowsFwd = 4 * 152, kWindowsBwd = 8 * 152;   // rows, more than
+// How a call's rows are read: as vectors, as windows of them (where rows start anywhere, and there are enough rows for what the
+// windows' weights and partial rows cost once per block), or value by value. Windows and values, in us: 8192 x 2047 bf16 forward
+// 24.8 and 49.1, keeping 8 bits 45 and 80; 8192 x 1537 fp32 26.2 and 48.7, backward 34.9 and 52.4; 1023 x 1537 fp32 5.6 and 8.0,
+// backward 10.6 and 10.3; 1300 x 501 bf16 backward (a row or two per block) 11.9 and 9.4; 500 x 333 bf16 forward 3.1 and 2.8.
+constexpr int64_t kWindowsFwd = 4 * 152;   // rows, more than
+constexpr int kWindowsBwd = 3;             // rows per block, more than
 struct How {
   Shape sh;
   bool win;
@@ -1121,7 +1125,8 @@ extern "C" int moe_layer_norm_bwd(const void *dn, const void *x, const void *cod
   p.nb = (int)act8::blocks_of(d);
   p.eps = eps;
   cudaStream_t s = (cudaStream_t)stream;
-  const How h = how(d, dtype, T > kWindowsBwd);
+  How h = how(d, dtype, true);
+  if (h.win && T <= (int64_t)kWindowsBwd * ln_bwd_blocks(T, h.sh, dx_in ? 3 : 2)) h = how(d, dtype, false);
   Shape sh = h.sh;
   int rows = 1, grid = ln_bwd_blocks(T, sh, dx_in ? 3 : 2);
   // Two rows at a time where blocks have more rows than one: at T = 16384, d = 4096 bf16 86.8 against 89.0 us (from codes 84.7
