@@ -74,7 +74,8 @@ def test_forward_and_backward(T, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("T,d", SHAPES + [(700, 33), (2435, 1023), (2435, 1537), (1300, 4089), (1300, 63), (1221, 8177), (611, 8191), (1300, 2046)])
+@pytest.mark.parametrize("T,d", SHAPES + [(700, 33), (2435, 1023), (2435, 1537), (1300, 4089), (1300, 63), (1221, 8177), (611, 8191), (1300, 2046), (700, 1),
+                                          (2000, 5), (3001, 31), (640, 3)])
 def test_kept(T, d, dtype):
     s = make(T, d, dtype, T + d)
     m, r = stats(s["x"])
