@@ -530,6 +530,15 @@ def _on(name, t, dev):
     return t.data_ptr()
 
 
+def _rows_on(name, t, dev):
+    """The address of a contiguous tensor [..., K] on the current GPU, its number of rows and K."""
+    if not t.is_contiguous():
+        _want(name, t, t.dtype, t.shape)
+    shape = t.shape
+    R, K = shape if len(shape) == 2 else _rows(shape)
+    return (t.data_ptr() if t.get_device() == dev else _on(name, t, dev)), R, K
+
+
 def _bytes_on(name, t, n, dev):
     """The address of a tensor of at least n bytes on the current GPU."""
     if t.dtype is _U8 and t.numel() >= n and t.is_contiguous() and t.get_device() == dev:
@@ -540,20 +549,20 @@ def _bytes_on(name, t, n, dev):
 
 def moe_act8_quantize(x, codes, scales, stream=None):
     """x [..., K] (rows in order) -> codes [..., K] uint8, scales [moe_act8_scale_bytes(rows, K)] uint8."""
-    shape, dt, dev = x.shape, x.dtype, _device()
-    R, K = _rows(shape)
+    dev = _device()
+    p, R, K = _rows_on("x", x, dev)
     _ok("moe_act8_quantize", lib().moe_act8_quantize(
-        _at("x", x, dt, shape, dev), dtype_code(dt), R, K, _at("codes", codes, _U8, shape, dev),
+        p, dtype_code(x.dtype), R, K, _at("codes", codes, _U8, x.shape, dev),
         _bytes_on("scales", scales, _scale_bytes8(R, K), dev), _s(stream)))
 
 
 def moe_act8_dequantize(codes, scales, x, stream=None):
     """The values that codes and scales stand for, into x [..., K]."""
-    shape, dt, dev = x.shape, x.dtype, _device()
-    R, K = _rows(shape)
+    dev = _device()
+    p, R, K = _rows_on("x", x, dev)
     _ok("moe_act8_dequantize", lib().moe_act8_dequantize(
-        _at("codes", codes, _U8, shape, dev), _bytes_on("scales", scales, _scale_bytes8(R, K), dev), R, K, dtype_code(dt),
-        _at("x", x, dt, shape, dev), _s(stream)))
+        _at("codes", codes, _U8, x.shape, dev), _bytes_on("scales", scales, _scale_bytes8(R, K), dev), R, K, dtype_code(x.dtype),
+        p, _s(stream)))
 
 
 def layer_norm_fwd_into(dev, x, w, b, T, d, dt, n, mean, rstd, codes, scales, eps, stream):
