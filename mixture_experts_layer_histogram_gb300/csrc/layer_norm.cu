@@ -1009,12 +1009,14 @@ static int ln_bwd_blocks(int64_t T, const Shape &s, int tensors) {
     }                                                                                                 \
   } while (0)
 
-// How a call's rows are read: as vectors, as windows of them (where rows start anywhere, and there are enough rows for what the
-// windows' weights and partial rows cost once per block), or value by value. Windows and values, in us: 8192 x 2047 bf16 forward
-// 24.8 and 49.1, keeping 8 bits 45 and 80; 8192 x 1537 fp32 26.2 and 48.7, backward 34.9 and 52.4; 1023 x 1537 fp32 5.6 and 8.0,
-// backward 10.6 and 10.3; 1300 x 501 bf16 backward (a row or two per block) 11.9 and 9.4; 500 x 333 bf16 forward 3.1 and 2.8.
-constexpr int64_t kWindowsFwd = 4 * 152;   // rows, more than
-constexpr int kWindowsBwd = 3;             // rows per block, more than
+// How a call's rows are read: as vectors, as windows of them (where rows start anywhere, and there is enough for what the
+// windows' weights and partial rows cost once per block), or value by value. Windows and values, in us: forward 500 x 333 bf16
+// 3.1 and 2.8, 600 x 501 3.2 and 3.0, 300 x 1537 fp32 3.0 and 3.6, 150 x 4001 bf16 3.7 and 7.0, 8192 x 2047 24.8 and 49.1;
+// restore 800 x 1537 fp32 4.3 and 4.2, 1023 x 1537 4.7 and 5.2, 8192 x 2047 bf16 15 and 35; backward 300 x 1537 fp32 (one row
+// per block) 6.1 and 6.0, 650 x 1537 7.6 and 8.4, 8192 x 1537 35 and 52; 1300 x 501 bf16 (one row per block) 12.0 and 9.1, 3700
+// x 501 (three) 12.9 and 12.9, 700 x 4001 (five) 15.9 and 14.5, 8192 x 2047 49 and 55.
+constexpr int64_t kWindowsFwd = 400000, kWindowsRestore = 1500000;                         // values, more than
+static int windows_bwd(int dtype) { return dtype == MOE_F32 ? 1 : 5; }                     // rows per block, more than
 struct How {
   Shape sh;
   bool win;
@@ -1061,7 +1063,7 @@ extern "C" int moe_layer_norm_fwd(const void *x, const void *w, const void *b, i
   p.d = d;
   p.nb = (int)act8::blocks_of(d);
   p.eps = eps;
-  const How h = how(d, dtype, T > kWindowsFwd);
+  const How h = how(d, dtype, (int64_t)T * d > kWindowsFwd);
   const Shape &sh = h.sh;
   if (h.win) MOE_LN_DISPATCH(ln_launch_fwd, true, p, sh, (cudaStream_t)stream);
   else MOE_LN_DISPATCH(ln_launch_fwd, false, p, sh, (cudaStream_t)stream);
@@ -1088,11 +1090,11 @@ extern "C" int moe_layer_norm_restore(const void *codes, const void *scales, con
   }
   if (dtype == MOE_BF16) {
     if (d % 8 == 0) return ln_launch_restore<__nv_bfloat16, 8>(codes, scales, w, b, T, d, n, s);
-    return T > kWindowsFwd ? ln_launch_restore_windows<__nv_bfloat16, 8>(codes, scales, w, b, T, d, n, s)
+    return (int64_t)T * d > kWindowsRestore ? ln_launch_restore_windows<__nv_bfloat16, 8>(codes, scales, w, b, T, d, n, s)
                            : ln_launch_restore<__nv_bfloat16, 1>(codes, scales, w, b, T, d, n, s);
   }
   if (d % 4 == 0) return ln_launch_restore<float, 4>(codes, scales, w, b, T, d, n, s);
-  return T > kWindowsFwd ? ln_launch_restore_windows<float, 4>(codes, scales, w, b, T, d, n, s)
+  return (int64_t)T * d > kWindowsRestore ? ln_launch_restore_windows<float, 4>(codes, scales, w, b, T, d, n, s)
                          : ln_launch_restore<float, 1>(codes, scales, w, b, T, d, n, s);
 }
 
@@ -1126,7 +1128,7 @@ extern "C" int moe_layer_norm_bwd(const void *dn, const void *x, const void *cod
   p.eps = eps;
   cudaStream_t s = (cudaStream_t)stream;
   How h = how(d, dtype, true);
-  if (h.win && T <= (int64_t)kWindowsBwd * ln_bwd_blocks(T, h.sh, dx_in ? 3 : 2)) h = how(d, dtype, false);
+  if (h.win && T <= (int64_t)windows_bwd(dtype) * ln_bwd_blocks(T, h.sh, dx_in ? 3 : 2)) h = how(d, dtype, false);
   Shape sh = h.sh;
   int rows = 1, grid = ln_bwd_blocks(T, sh, dx_in ? 3 : 2);
   // Two rows at a time where blocks have more rows than one: at T = 16384, d = 4096 bf16 86.8 against 89.0 us (from codes 84.7

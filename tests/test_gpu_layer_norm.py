@@ -75,7 +75,7 @@ def test_forward_and_backward(T, d, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,d", SHAPES + [(700, 33), (2435, 1023), (2435, 1537), (1300, 4089), (1300, 63), (1221, 8177), (611, 8191), (1300, 2046), (700, 1),
-                                          (2000, 5), (3001, 31), (640, 3)])
+                                          (2000, 5), (3001, 31), (640, 3), (80001, 5), (500000, 1), (50001, 31), (150, 4001)])
 def test_kept(T, d, dtype):
     s = make(T, d, dtype, T + d)
     m, r = stats(s["x"])
