@@ -958,6 +958,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 struct Plan {
   int width, splits;
 };
+constexpr int kPartBlocks = 24;   // k-blocks that take as long as a part's exchange, about
 constexpr int kBlockCost[2] = {4, 3}, kTileCost[2] = {38, 18}, kPartCost[2] = {48, 44};   // of 256 columns, of 128
 static int64_t up(int64_t n, int64_t k) { return (n + k - 1) / k; }
 static Plan plan(int64_t m_tiles, int64_t columns, int num_kb, int pairs) {
@@ -985,7 +986,7 @@ static Plan plan(int64_t m_tiles, int64_t columns, int num_kb, int pairs) {
 }
 // The pairs that the plan counts on: those of a GB300, wherever it is asked for (the workspace's size follows from it).
 constexpr int kPairs = 76;
-constexpr int kPlaces = 2 * 2 * kPairs;   // of parts: two products of a call may be cut, into 2 kPairs parts each at most
+constexpr int kPlaces = PRODUCTS * kPairs;   // of parts: every product may be cut, into kPairs parts at most
 constexpr size_t kArrivedBytes = (size_t)kPlaces * SLICES * 8;
 constexpr size_t kPartBytes = (size_t)SLICES * SLICE_FLOATS * 4;
 
@@ -1109,6 +1110,28 @@ static Product product(int op, int64_t M, int64_t N, int64_t k, int width = 0) {
   return o;
 }
 static size_t part_bytes(const Product &o) { return o.splits > 1 ? (size_t)o.m_tiles * o.n_tiles * o.splits * kPartBytes : 0; }
+
+// The backward's products. The last three run beside one another: narrow tiles where they give every pair one at most, and a product
+// whose K takes a tile much longer than a pair's share of all three (or, less than that, than a part costs) is cut along it:
+// 101 to 52 us for a step of 234 x 72 x 6768, whose dx is one tile of 212 k-blocks.
+struct Backward {
+  Product dh, dx, down, gu;
+};
+static Backward backward_of(int64_t T, int64_t d, int64_t f) {
+  const int64_t narrow = up(T, TILE) * up(d, HALF) + up(d, TILE) * up(f, HALF) + up(2 * f, TILE) * up(d, HALF);
+  const int width = narrow <= kPairs ? HALF : TILE;
+  Backward b{product(DH, T, f, d), product(DX, T, d, 2 * f, width), product(DW, d, f, T, width), product(DW, 2 * f, d, T, width)};
+  Product *const three[3] = {&b.dx, &b.down, &b.gu};
+  int64_t work = 0;
+  for (const Product *o : three) work += (int64_t)o->m_tiles * o->n_tiles * o->num_kb;
+  const int64_t share = std::max(work / kPairs, (int64_t)kPartBlocks);
+  for (Product *o : three) {
+    const int64_t tiles = (int64_t)o->m_tiles * o->n_tiles;
+    if (2 * o->num_kb <= 3 * share || tiles > kPairs) continue;
+    o->splits = (int)std::min({up(o->num_kb, share), (int64_t)MAX_SPLIT, kPairs / tiles});
+  }
+  return b;
+}
 }  // namespace ffng
 }  // namespace tc
 
@@ -1120,7 +1143,10 @@ typedef __nv_bfloat16 bf16;
 
 size_t gemm_workspace(int T, int d, int f, bool backward) {
   size_t most = part_bytes(product(GATEUP, T, f, d)) + part_bytes(product(DOWN, T, d, f));
-  if (backward) most = std::max(most, part_bytes(product(DH, T, f, d)));
+  if (backward) {
+    const Backward b = backward_of(T, d, f);
+    most = std::max(most, part_bytes(b.dh) + part_bytes(b.dx) + part_bytes(b.down) + part_bytes(b.gu));
+  }
   return counter_bytes(T) + most;
 }
 
@@ -1155,11 +1181,8 @@ int gemm_fwd(const Block &b, cudaStream_t s) {
 // are dealt out before the shorter ones, which even out what those leave.
 int gemm_bwd(const Block &b, cudaStream_t s) {
   const uint64_t T = b.T, d = b.d, f = b.f;
-  // the last three run beside one another: narrow tiles where they give every pair one at most
-  const int64_t tiles = up(T, TILE) * up(d, HALF) + up(d, TILE) * up(f, HALF) + up(2 * f, TILE) * up(d, HALF);
-  const int width = tiles <= kPairs ? HALF : TILE;
-  Product dh = product(DH, b.T, b.f, b.d), dx = product(DX, b.T, b.d, 2 * (int64_t)b.f, width), down = product(DW, b.d, b.f, b.T, width),
-          gu = product(DW, 2 * (int64_t)b.f, b.d, b.T, width);
+  Backward products = backward_of(b.T, b.d, b.f);
+  Product &dh = products.dh, &dx = products.dx, &down = products.down, &gu = products.gu;
   Params p{};
   if (b.scales) {
     p.codes = (uint8_t *)b.ab;

@@ -116,7 +116,8 @@ def test_forward(T, d, f, act, add):
 
 @pytest.mark.parametrize("keep", [None, "f8"])
 @pytest.mark.parametrize("act,add", [("silu", True), ("gelu", False)])
-@pytest.mark.parametrize("T,d,f", [(1, 64, 64), (5, 8, 32), (64, 200, 96)] + [m for m in MANY if m[2] % 32 == 0] + [(300, 72, 8192), (130, 8192, 2048)])
+@pytest.mark.parametrize("T,d,f", [(1, 64, 64), (5, 8, 32), (64, 200, 96)] + [m for m in MANY if m[2] % 32 == 0] + [(300, 72, 8192), (130, 8192, 2048), (234, 72, 6752), (2, 424, 3296),
+                                                                            (4178, 112, 2048), (3000, 264, 896)])
 def test_step(T, d, f, act, add, keep):
     s = make(T, d, f, BF, T + d + f)
     ffn = GatedFFN(T, d, f, act=act, keep=keep)
