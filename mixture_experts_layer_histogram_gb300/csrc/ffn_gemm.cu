@@ -1127,7 +1127,7 @@ static Backward backward_of(int64_t T, int64_t d, int64_t f) {
   const int64_t share = std::max(work / kPairs, (int64_t)kPartBlocks);
   for (Product *o : three) {
     const int64_t tiles = (int64_t)o->m_tiles * o->n_tiles;
-    if (2 * o->num_kb <= 3 * share || tiles > kPairs) continue;
+    if (tiles == 0 || 2 * o->num_kb <= 3 * share || tiles > kPairs) continue;   // (no tokens: dx has no tiles)
     o->splits = (int)std::min({up(o->num_kb, share), (int64_t)MAX_SPLIT, kPairs / tiles});
   }
   return b;
