@@ -497,8 +497,8 @@ int moe_layer_norm_bwd(const void *dn, const void *x, const void *codes, const v
  * MOE_KEEP_NONE take a path bound by reading the weights once. fp32: true fp32 FMA, any d, f >= 1; MOE_KEEP_F8 is for bf16 only.
  * d, f at most MOE_FFN_MAX, T at most MOE_FFN_MAX_T. Results repeat bit for bit.
  * ws: moe_ffn_workspace_size(...) bytes, 256-byte aligned; zeros before its first use (it holds arrival counts that every call
- * leaves at zero, and the status word). Calls that may overlap on the GPU need one each; a call that reported an error
- * leaves it to be zeroed again. Device errors: MOE_ERR_DEVICE_TIMEOUT (bf16: every wait is bounded to about 0.2 s).
+ * leaves at zero, and the status word). It may serve calls of different sizes, one after the other, each of which it is large
+ * enough for. Calls that may overlap on the GPU need one each; a call that reported an error leaves it to be zeroed again. Device errors: MOE_ERR_DEVICE_TIMEOUT (bf16: every wait is bounded to about 0.2 s).
  * Except y == y_in and dx == dx_in, outputs may not overlap inputs.
  */
 #define MOE_FFN_MAX (1 << 20)

@@ -1008,8 +1008,12 @@ template <auto KERNEL> static int pairs_resident(int &pairs) {
   return MOE_OK;
 }
 
-// The counters in front of the parts: for cut tiles, then pairs that are done (one line), then rows of tiles.
-static size_t counter_bytes(int64_t T) { return kArrivedBytes + 128 + (size_t)up(up(T, TILE), 32) * 128; }
+// The counters in front of the parts: for cut tiles, then pairs that are done (one line), then rows of tiles. As many of these
+// as the largest T has, whatever this call's is: a workspace may serve calls of any T, and parts never lie where another call
+// counts on zeros.
+constexpr size_t kReadyBytes = (MOE_FFN_MAX_T + TILE - 1) / TILE * sizeof(int);
+constexpr size_t kCounterBytes = kArrivedBytes + 128 + kReadyBytes;
+static_assert(kCounterBytes % 128 == 0, "parts start on a line");
 
 // How the products' tiles are dealt to the pairs, product after product (in p.deal's order): parts of cut tiles in turn, whole
 // tiles each to the pair with the least work so far (whole rounds at once, but for the last two). What waits for a first product
@@ -1064,7 +1068,7 @@ template <int CH> static int start(const Maps<CH> &maps, Params &p, const ffn::B
   p.arrived = (int *)ws;
   p.left = (int *)(ws + kArrivedBytes);
   p.ready = (int *)(ws + kArrivedBytes + 128);
-  p.part = (float4 *)(ws + counter_bytes(blk.T));
+  p.part = (float4 *)(ws + kCounterBytes);
   p.rows = p.prod[0].m_tiles;
   int pairs = 0;
   const int rc = pairs_resident<ffn_gemm_kernel<CH>>(pairs);
@@ -1147,7 +1151,7 @@ size_t gemm_workspace(int T, int d, int f, bool backward) {
     const Backward b = backward_of(T, d, f);
     most = std::max(most, part_bytes(b.dh) + part_bytes(b.dx) + part_bytes(b.down) + part_bytes(b.gu));
   }
-  return counter_bytes(T) + most;
+  return kCounterBytes + most;
 }
 
 // Forward: y's tiles wait for the rows of h that they read.
