@@ -461,8 +461,8 @@ int moe_act8_dequantize(const void *codes, const void *scales, int64_t R, int K,
  *                           dw [d] = sum_t dn z, db [d] = sum_t dn (NULL: not wanted). z is formed from x, mean and
  *                           rstd; with codes and scales (x NULL, mean unused) it is what they stand for.
  * Sums and statistics are fp32. A row whose squared deviations pass fp32's range (magnitudes above about 1e19; up to
- * 1e34 for its sum) counts as having r 0. Rows of at most 32 values are differentiated in 64 bits, with x's statistics
- * formed again. Weight gradients are summed in fp32 in a fixed order, rounded once, and overwritten.
+ * 1e34 for its sum) counts as having r 0, in both directions. Rows of at most 32 values are differentiated in 64 bits, with
+ * x's statistics formed again (but for a stored rstd of 0). Weight gradients are summed in fp32 in a fixed order, rounded once, and overwritten.
  * Requires 1 <= d <= MOE_NORM_MAX_D, eps > 0, T >= 0 (T = 0: the weight gradients are zeros).
  * ws: moe_layer_norm_bwd_workspace_size(T, d, dtype) bytes, 256-byte aligned, any content. Except dx == dx_in,
  * outputs may not overlap inputs.

@@ -618,7 +618,8 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
       m[0] = t[0] * inv_d;
       t[0] = ring.has(0) ? (x[0] - m[0]) * (x[0] - m[0]) : S(0);
       block_sums(t, sums, half);
-      r[0] = S(1) / sqrt(t[0] * inv_d + (S)p.eps);
+      // a stored 0: squares past fp32's range, whose row the forward took for one of infinite variance (z = 0)
+      if (r[0] != S(0)) r[0] = S(1) / sqrt(t[0] * inv_d + (S)p.eps);
     }
     // z (without KEPT: before the rest of the mean is taken off) of the i-th vector of the j-th row
     auto normed = [&](int j, int i, L (&z)[N]) {
