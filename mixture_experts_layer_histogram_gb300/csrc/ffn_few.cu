@@ -21,6 +21,7 @@
 
 #include "dependent.cuh"
 #include "ffn.cuh"
+#include "stages.h"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
 
@@ -255,17 +256,15 @@ __global__ void __launch_bounds__(THREADS + 32, 1)
   } else {
     wait_previous();
     float acc[MT][NT][4] = {};
-    int k = 0, gr = blockIdx.x, at_sums = 0;
-    bool ok = true;
-    for (int i = 0; i < total; ++i) {
-      const int s = i % PS;
+    int gr = blockIdx.x, at_sums = 0;
+    auto there = [&](int i) {   // lanes look one by one, but the warp goes on, or gives up, together
       const uint32_t phase = (uint32_t)(i / PS) & 1u;
-      if (!tc::mbar_try_wait(full(s), phase) && !tc::mbar_wait(full(s), phase, abort_flag, hdr, 52)) {
-        ok = false;
-        break;
-      }
+      const bool seen = tc::mbar_try_wait(full(i % PS), phase) || tc::mbar_wait(full(i % PS), phase, abort_flag, hdr, 52);
+      return __all_sync(0xffffffffu, seen) != 0;
+    };
+    auto use = [&](int i) {
+      const int s = i % PS;
       const uint32_t w0 = base + s * SB + (uint32_t)warp * (ROWS * 128), x0 = base + s * SB + weight_bytes<NT, MT>() + (uint32_t)warp * (NT * 1024);
-      const bool all = whole(gr);
       auto products = [&](auto count) {   // of the group's units
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -285,15 +284,15 @@ __global__ void __launch_bounds__(THREADS + 32, 1)
           }
         }
       };
-      if (all) products(std::integral_constant<int, MT>());
+      if (whole(gr)) products(std::integral_constant<int, MT>());
       else products(std::integral_constant<int, 1>());
       // the reads above come before the TMA's next writes to this place: another proxy's, which the arrival alone does not order
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(empty(s));
-      if (++k < st.steps) continue;
-      // the group's sums over the warps, in their order
-      k = 0;
+    };
+    // the group's sums over the warps, in their order (of an unfinished group nothing is written by a warp that knows)
+    auto meet = [&](bool ok) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -303,7 +302,7 @@ __global__ void __launch_bounds__(THREADS + 32, 1)
         }
       }
       asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
-      for (int j = warp; j < (all ? MT : 1) * NT; j += WARPS) {
+      for (int j = warp; ok && j < (whole(gr) ? MT : 1) * NT; j += WARPS) {
         float4 v = sums[at_sums][j][lane];
 #pragma unroll
         for (int u = 1; u < WARPS; ++u) {
@@ -320,7 +319,8 @@ __global__ void __launch_bounds__(THREADS + 32, 1)
       if (SUMS == 1) asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
       else at_sums ^= WARPS;
       gr += gridDim.x;
-    }
+    };
+    const bool ok = through_stages(total, st.steps, there, use, meet);
     if (!ok) {   // copies in flight land within microseconds
       const uint64_t t0 = global_ns();
       while (global_ns() - t0 < 1000ull * 1000ull) {}

@@ -197,19 +197,30 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
 }
 
-// mbar_wait_cluster in place: across a call, what a warp has asked for ahead would be stored to the stack first, and so waited
-// for
-__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int *abort_flag, WsHeader *hdr, int where) {
+// The waits below are made by whole warps. Lanes look for themselves, but go on, or give up, together: one that went on alone would
+// wait for the others at the warp's next barrier for good.
+__device__ __forceinline__ bool given_up(uint64_t t0, volatile int *abort_flag, WsHeader *hdr, int where) {
+  const bool late = global_ns() - t0 > kWaitLimitNs;
+  if (!__any_sync(0xffffffffu, late || *abort_flag)) return false;
+  if (late) report(hdr, MOE_ERR_DEVICE_TIMEOUT, where);
+  *abort_flag = 1;
+  return true;
+}
+// Polling, for the ring's producer and the MMA issuer (see mbar_spin_cluster) ...
+__device__ __forceinline__ bool spin_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag, WsHeader *hdr, int where) {
   const uint64_t t0 = global_ns();
   for (uint32_t i = 0;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 15u) != 15u) continue;
-    if (*abort_flag) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      report(hdr, MOE_ERR_DEVICE_TIMEOUT, where);
-      *abort_flag = 1;
-      return false;
-    }
+    if (__all_sync(0xffffffffu, mbar_ready_cluster(bar, parity))) return true;
+    if ((i & 255u) == 255u && given_up(t0, abort_flag, hdr, where)) return false;
+  }
+}
+// ... and for the others, in place: across a call, what a warp has asked for ahead would be stored to the stack first, and so waited
+// for.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag, WsHeader *hdr, int where) {
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 0;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
+    if ((i & 15u) == 15u && given_up(t0, abort_flag, hdr, where)) return false;
   }
 }
 
@@ -777,7 +788,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
         // a look ahead for the next unit while this one's copies are still queued up
         if (kb == max(t.kb0, t.kb1 - 3)) seen = more && rows.look(p, p.prod[nx.q], nx.m);
-        if (!mbar_spin_cluster(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 41)) {
+        if (!spin_warp(empty_bar(stage), phase ^ 1u, abort_flag, p.hdr, 41)) {
           ok = false;
           break;
         }
@@ -819,13 +830,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     for (; ok && more; more = walk.next(t, p)) {
       const uint64_t desc_a = a_mn(t) ? desc_a_mn : desc_a_k;
       const uint32_t id = idesc(a_mn(t), B_MN, p.prod[t.q].width), a_step = a_mn(t) ? 2048 >> 4 : 32 >> 4;
-      if (!mbar_ready_cluster(tempty_bar(acc), acc_phase ^ 1u) &&
-          !mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.hdr, 42))
-        break;
+      if (!wait_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.hdr, 42)) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + (uint32_t)(acc * TILE);
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        if (!mbar_spin_cluster(full_bar(stage), phase, abort_flag, p.hdr, 43)) {
+        if (!spin_warp(full_bar(stage), phase, abort_flag, p.hdr, 43)) {
           ok = false;
           break;
         }
@@ -876,7 +885,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const bool cut = t.part >= 0;
       Ahead<K> ahead;
       if (!cut) ahead.start(p, o, buf, lane, row0, col0);
-      if (!wait_here(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 44)) return false;
+      if (!wait_warp(tfull_bar(acc), acc_phase, abort_flag, p.hdr, 44)) return false;
       tc_fence_after();
       Slice<K> s;
       s.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * TILE + mine * hh);
