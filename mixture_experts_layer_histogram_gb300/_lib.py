@@ -505,6 +505,40 @@ def moe_grouped_ffn_fwd_fp4(x_codes, x_scales, wgu_codes, wgu_scales, wd_codes, 
         _p(ws), ws.numel() * ws.element_size(), _s(stream)))
 
 
+class OwnsBuffers:
+    """A class that allocates its buffers once and gives their addresses to every call. Another tensor may be set in the place of
+    one of them (a second set of what is kept, say): it has to be of the same type, shape and device, and the calls that follow use
+    it. (A captured graph goes on with the one that it was captured with.)"""
+
+    _buffers = ()          # their attributes' names
+
+    def _take(self):
+        """Notes the buffers' addresses: at the end of the construction, and whenever a buffer is set."""
+        raise NotImplementedError
+
+    def _built(self):
+        self._take()
+        self.__dict__["_buffers_taken"] = True
+
+    def __setattr__(self, name, t):
+        taken = name in self._buffers and "_buffers_taken" in self.__dict__
+        if taken:
+            old = self.__dict__.get(name)
+            if old is None or t is None:
+                raise ValueError(f"{name}: {type(self).__name__} was built {'without' if old is None else 'with'} this buffer")
+            _want(name, t, old.dtype, old.shape)
+            if t.device != old.device:
+                raise ValueError(f"{name}: the buffers are on {old.device}, got a tensor on {t.device}")
+        object.__setattr__(self, name, t)
+        if taken:
+            self._take()
+
+    def __delattr__(self, name):
+        if name in self._buffers:
+            raise AttributeError(f"{name}: the calls of {type(self).__name__} use this buffer")
+        object.__delattr__(self, name)
+
+
 def moe_act8_scale_bytes(R, K):
     return int(lib().moe_act8_scale_bytes(R, K))
 

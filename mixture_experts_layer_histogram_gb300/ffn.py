@@ -17,8 +17,11 @@ from . import _lib as L
 ACTS = {"silu": L.ACT_SILU, "gelu": L.ACT_GELU}
 
 
-class GatedFFN:
-    """Buffers of one block, allocated once and reused every step."""
+class GatedFFN(L.OwnsBuffers):
+    """Buffers of one block, allocated once and reused every step. Another tensor of the same type and shape may be set in the place
+    of any of them (y, h, ab, ab_scales, dab, dx, dw_gate_up, dw_down; ws: zeros)."""
+
+    _buffers = frozenset(("y", "h", "ab", "ab_scales", "dab", "dx", "dw_gate_up", "dw_down", "ws"))
 
     def __init__(self, T, d, f, dtype=torch.bfloat16, act="silu", keep=None, backward=True, scratch=None, device="cuda"):
         """act: "silu" or "gelu" (its tanh form). keep: None (everything the backward reads, in dtype) or "f8". scratch: a
@@ -62,9 +65,12 @@ class GatedFFN:
             self.dw_gate_up = torch.empty((2 * f, d), **act_)
             self.dw_down = torch.empty((d, f), **act_)
         self._index = self.y.device.index
+        self._built()
+
+    def _take(self):
         with torch.cuda.device(self._index):
-            self._kept = L.kept(self.ab, self.ab_scales, dtype, T, f)
-        if backward:
+            self._kept = L.kept(self.ab, self.ab_scales, self.dtype, self.T, self.f)
+        if self.backward_enabled:
             self._grads = [t.data_ptr() for t in (self.dab, self.dx, self.dw_gate_up, self.dw_down)]
         self._h_ptr, self._y_ptr, self._ws_ptr, self._ws_bytes = (self.h.data_ptr(), self.y.data_ptr(), self.ws.data_ptr(),
                                                                   self.ws.numel())

@@ -14,8 +14,11 @@ import torch
 from . import _lib as L
 
 
-class LayerNorm:
-    """Buffers of one norm, allocated once and reused every step."""
+class LayerNorm(L.OwnsBuffers):
+    """Buffers of one norm, allocated once and reused every step. Another tensor of the same type and shape may be set in the place
+    of any of them (n, mean, rstd, codes, scales, dx, dw, db, ws)."""
+
+    _buffers = frozenset(("n", "mean", "rstd", "codes", "scales", "dx", "dw", "db", "ws"))
 
     def __init__(self, T, d, dtype=torch.bfloat16, eps=1e-5, bias=True, keep=None, backward=True, device="cuda"):
         """bias: the norm has one (b is given to every call, and the backward returns db). keep: None, or "f8"."""
@@ -44,15 +47,17 @@ class LayerNorm:
             self.dw = torch.empty(d, **act)
             self.db = torch.empty(d, **act) if bias else None
             self.ws = torch.empty(L.moe_layer_norm_bwd_workspace_size(T, d, code), dtype=torch.uint8, device=self.device)
-            self._ws_bytes = self.ws.numel()
         self._index = self.n.device.index
+        self._built()
 
+    def _take(self):
         def at(*tensors):
             return [None if t is None else t.data_ptr() for t in tensors]
 
         self._out, self._codes = at(self.n, self.mean, self.rstd, self.codes, self.scales), at(self.codes, self.scales)
-        if backward:
+        if self.backward_enabled:
             self._back = at(self.codes, self.scales, self.mean, self.rstd, self.dx, self.dw, self.db, self.ws)
+            self._ws_bytes = self.ws.numel()
 
     def _check(self, b):
         """The current device, on which the buffers have to be."""
