@@ -511,6 +511,7 @@ class OwnsBuffers:
     it. (A captured graph goes on with the one that it was captured with.)"""
 
     _buffers = ()          # their attributes' names
+    _fixed = ()            # attributes that the buffers' sizes follow from, or that say what they are for
 
     def _take(self):
         """Notes the buffers' addresses: at the end of the construction, and whenever a buffer is set."""
@@ -521,7 +522,10 @@ class OwnsBuffers:
         self.__dict__["_buffers_taken"] = True
 
     def __setattr__(self, name, t):
-        taken = name in self._buffers and "_buffers_taken" in self.__dict__
+        built = "_buffers_taken" in self.__dict__
+        if built and name in self._fixed:
+            raise AttributeError(f"{name}: {type(self).__name__} was built for {self.__dict__[name]}")
+        taken = built and name in self._buffers
         if taken:
             old = self.__dict__.get(name)
             if old is None or t is None:

@@ -22,6 +22,7 @@ class GatedFFN(L.OwnsBuffers):
     of any of them (y, h, ab, ab_scales, dab, dx, dw_gate_up, dw_down; ws: zeros)."""
 
     _buffers = frozenset(("y", "h", "ab", "ab_scales", "dab", "dx", "dw_gate_up", "dw_down", "ws"))
+    _fixed = frozenset(("T", "d", "f", "dtype", "device", "act", "keep", "backward_enabled"))
 
     def __init__(self, T, d, f, dtype=torch.bfloat16, act="silu", keep=None, backward=True, scratch=None, device="cuda"):
         """act: "silu" or "gelu" (its tanh form). keep: None (everything the backward reads, in dtype) or "f8". scratch: a

@@ -19,6 +19,7 @@ class LayerNorm(L.OwnsBuffers):
     of any of them (n, mean, rstd, codes, scales, dx, dw, db, ws)."""
 
     _buffers = frozenset(("n", "mean", "rstd", "codes", "scales", "dx", "dw", "db", "ws"))
+    _fixed = frozenset(("T", "d", "dtype", "device", "bias", "keep", "backward_enabled"))
 
     def __init__(self, T, d, dtype=torch.bfloat16, eps=1e-5, bias=True, keep=None, backward=True, device="cuda"):
         """bias: the norm has one (b is given to every call, and the backward returns db). keep: None, or "f8"."""

@@ -45,3 +45,12 @@ def test_refusals(made):
     with pytest.raises(ValueError, match="without"):
         nm.dx = torch.empty(4, 64, dtype=torch.bfloat16)
     nm.eps = 1e-3                                           # (no buffer)
+
+
+@pytest.mark.parametrize("name,value", [("T", 5), ("T", 4), ("d", 32), ("dtype", torch.float32), ("bias", False), ("keep", "f8"),
+                                        ("backward_enabled", False), ("device", torch.device("cpu"))])
+def test_sizes_stay(made, name, value):
+    """Calls check their inputs against these, and the buffers are as large as they said at the construction."""
+    nm = made()
+    with pytest.raises(AttributeError, match=name):
+        setattr(nm, name, value)
