@@ -20,6 +20,7 @@ GROUP_ROWS = 128
 MAX_EXPERTS = 256
 MAX_TOPK = 16
 NORM_MAX_D = 8192
+FFN_MAX, FFN_MAX_T = 1 << 20, 1 << 22
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 ADAMW_F32, ADAMW_F8 = 0, 1
 ACT_SILU, ACT_GELU = 0, 1

@@ -34,6 +34,12 @@ class GatedFFN(L.OwnsBuffers):
             raise ValueError(f"keep is None or 'f8', got {keep!r}")
         if keep and not backward:
             raise ValueError("keep needs a backward")
+        ws_bytes = L.moe_ffn_workspace_size(T, d, f, L.dtype_code(dtype), backward)
+        if ws_bytes == 0:
+            raise ValueError(f"GatedFFN takes T from 0 to {L.FFN_MAX_T} and d, f from 1 to {L.FFN_MAX}, in bfloat16 multiples of 8, got "
+                             f"T = {T}, d = {d}, f = {f} in {dtype}")
+        if keep and (dtype != torch.bfloat16 or f % 32):
+            raise ValueError(f"keep='f8' is for bfloat16 and f a multiple of 32, got {dtype}, f = {f}")
         if not torch.cuda.is_available():
             raise RuntimeError("GatedFFN needs a CUDA device")
         self.T, self.d, self.f, self.dtype, self.act, self.keep = T, d, f, dtype, act, keep
@@ -44,7 +50,6 @@ class GatedFFN(L.OwnsBuffers):
             raise ValueError("without keep the backward reads h: it cannot be shared")
         act_ = dict(dtype=dtype, device=self.device)
         u8 = dict(dtype=torch.uint8, device=self.device)
-        code = L.dtype_code(dtype)
         for name, shape in (("h", (T, f)), ("dab", (T, 2 * f))):
             if name in scratch:
                 L._want(f"scratch[{name!r}]", scratch[name], dtype, shape)
@@ -52,7 +57,7 @@ class GatedFFN(L.OwnsBuffers):
                     raise ValueError(f"scratch[{name!r}] is on {scratch[name].device}, the block is on {self.device}")
         self.h = scratch["h"] if "h" in scratch else torch.empty((T, f), **act_)
         self.y = torch.empty((T, d), **act_)
-        self.ws = torch.zeros(L.moe_ffn_workspace_size(T, d, f, code, backward), **u8)
+        self.ws = torch.zeros(ws_bytes, **u8)
         self.ab = self.ab_scales = None
         self.backward_enabled = backward
         if backward:
@@ -98,5 +103,5 @@ class GatedFFN(L.OwnsBuffers):
         return dict(dx=self.dx, dw_gate_up=self.dw_gate_up, dw_down=self.dw_down)
 
     def status(self, stream=None):
-        """Device status word (synchronises)."""
+        """Device status word (synchronises). After an error the workspace has to be zeroed before the next call: ws.zero_()."""
         return L.moe_read_status(self.ws, stream)

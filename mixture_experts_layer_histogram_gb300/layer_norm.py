@@ -27,12 +27,17 @@ class LayerNorm(L.OwnsBuffers):
             raise ValueError(f"keep is None or 'f8', got {keep!r}")
         if keep and not backward:
             raise ValueError("keep needs a backward")
+        code = L.dtype_code(dtype)
+        ws_bytes = L.moe_layer_norm_bwd_workspace_size(T, d, code)
+        if ws_bytes == 0:
+            raise ValueError(f"LayerNorm takes T >= 0 rows of 1 to {L.NORM_MAX_D} values, got T = {T}, d = {d}")
+        if not eps > 0:
+            raise ValueError(f"eps is above 0, got {eps}")
         if not torch.cuda.is_available():
             raise RuntimeError("LayerNorm needs a CUDA device")
         self.T, self.d, self.dtype, self.eps, self.bias, self.keep = T, d, dtype, eps, bias, keep
         self.device = torch.device(device)
         act = dict(dtype=dtype, device=self.device)
-        code = L.dtype_code(dtype)
         self.n = torch.empty((T, d), **act)
         self.backward_enabled = backward
         self.mean = self.rstd = self.codes = self.scales = None
@@ -47,7 +52,7 @@ class LayerNorm(L.OwnsBuffers):
             self.dx = torch.empty((T, d), **act)
             self.dw = torch.empty(d, **act)
             self.db = torch.empty(d, **act) if bias else None
-            self.ws = torch.empty(L.moe_layer_norm_bwd_workspace_size(T, d, code), dtype=torch.uint8, device=self.device)
+            self.ws = torch.empty(ws_bytes, **u8)
         self._index = self.n.device.index
         self._built()
 
