@@ -544,7 +544,18 @@ class OwnsBuffers:
         object.__delattr__(self, name)
 
 
+_INT_MAX = 0x7fffffff
+
+
+def _ints_only(*sizes):
+    """Sizes that the library takes as 32-bit integers (ctypes would pass on their low bits)."""
+    for n in sizes:
+        if n > _INT_MAX:
+            raise ValueError(f"a size of {n} is past 2^31 - 1")
+
+
 def moe_act8_scale_bytes(R, K):
+    _ints_only(K)
     return int(lib().moe_act8_scale_bytes(R, K))
 
 
@@ -575,6 +586,8 @@ def _rows_on(name, t, dev):
         _want(name, t, t.dtype, t.shape)
     shape = t.shape
     R, K = shape if len(shape) == 2 else _rows(shape)
+    if K > _INT_MAX:
+        _ints_only(K)
     return (t.data_ptr() if t.get_device() == dev else _on(name, t, dev)), R, K
 
 
@@ -617,6 +630,7 @@ def moe_layer_norm_fwd(x, w, b, n, mean=None, rstd=None, codes=None, scales=None
     """n = z w + b, z = (x - mean) rstd, x [T, d]; b may be None (zero). mean, rstd [T] fp32 and z in 8 bits (codes [T, d],
     scales) are written where they are given."""
     T, d = x.shape
+    _ints_only(T, d)
     dt, dev, f32 = x.dtype, _device(), torch.float32
     layer_norm_fwd_into(
         dev, x, w, b, T, d, dt, _at("n", n, dt, (T, d), dev), None if mean is None else _at("mean", mean, f32, (T,), dev),
@@ -636,12 +650,14 @@ def layer_norm_restore_into(dev, codes, scales, w, b, T, d, dt, n, stream):
 def moe_layer_norm_restore(codes, scales, w, b, n, stream=None):
     """n = z w + b with the z that codes and scales stand for; b may be None."""
     T, d = n.shape
+    _ints_only(T, d)
     dt, dev = n.dtype, _device()
     layer_norm_restore_into(dev, _at("codes", codes, _U8, (T, d), dev), _bytes_on("scales", scales, _scale_bytes8(T, d), dev), w, b, T, d,
                             dt, _at("n", n, dt, (T, d), dev), stream)
 
 
 def moe_layer_norm_bwd_workspace_size(T, d, dtype):
+    _ints_only(T, d)
     return int(lib().moe_layer_norm_bwd_workspace_size(T, d, dtype))
 
 
@@ -659,6 +675,7 @@ def moe_layer_norm_bwd(dn, x, codes, scales, mean, rstd, w, dx_in, dx, dw, db, w
     """Backward of moe_layer_norm_fwd, from x and mean or from codes and scales (the others None); dx_in (may be None, may be
     dx) is added to dx; db may be None (not wanted)."""
     T, d = dn.shape
+    _ints_only(T, d)
     dt, dev, rows, vec, f32 = dn.dtype, _device(), (T, d), (d,), torch.float32
 
     def opt(name, t, dtype, shape):
@@ -672,6 +689,7 @@ def moe_layer_norm_bwd(dn, x, codes, scales, mean, rstd, w, dx_in, dx, dw, db, w
 
 
 def moe_ffn_workspace_size(T, d, f, dtype, backward):
+    _ints_only(T, d, f)
     return int(lib().moe_ffn_workspace_size(T, d, f, dtype, int(bool(backward))))
 
 
@@ -701,6 +719,7 @@ def moe_ffn_fwd(x, w_gate_up, w_down, y_in, ab, ab_scales, h, y, ws, act=ACT_SIL
     ab: None (nothing kept), [T, 2f] in x's type, or [T, 2f] uint8 codes with ab_scales. h [T, f] is written."""
     T, d = x.shape
     f, dt, dev = w_down.shape[1], x.dtype, _device()
+    _ints_only(T, d, f)
     ffn_fwd_into(dev, x, w_gate_up, w_down, y_in, T, d, f, dt, act, kept(ab, ab_scales, dt, T, f), _at("h", h, dt, (T, f), dev),
                  _at("y", y, dt, (T, d), dev), _on("ws", ws, dev), ws.numel() * ws.element_size(), stream)
 
@@ -720,6 +739,7 @@ def moe_ffn_bwd(dy, x, ab, ab_scales, h, w_gate_up, w_down, dx_in, dab, dx, dw_g
     """Backward of moe_ffn_fwd from the ab (and h, or ab_scales) that it kept; dx_in (may be None, may be dx) is added to dx."""
     T, d = dy.shape
     f, dt, dev = w_down.shape[1], dy.dtype, _device()
+    _ints_only(T, d, f)
     ffn_bwd_into(dev, dy, x, w_gate_up, w_down, dx_in, T, d, f, dt, act, kept(ab, ab_scales, dt, T, f), _at("h", h, dt, (T, f), dev),
                  _at("dab", dab, dt, (T, 2 * f), dev), _at("dx", dx, dt, (T, d), dev),
                  _at("dw_gate_up", dw_gate_up, dt, (2 * f, d), dev), _at("dw_down", dw_down, dt, (d, f), dev), _on("ws", ws, dev),
