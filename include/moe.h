@@ -493,7 +493,7 @@ int moe_layer_norm_bwd(const void *dn, const void *x, const void *codes, const v
  *   dx = dx_in + [da | db] w_gate_up (dx_in NULL: zero; dx may be dx_in), dw_gate_up = [da | db]^T x, dw_down = dy^T h
  * Weight gradients are overwritten; T = 0 makes them zeros.
  * bf16: tensor cores, fp32 accumulation, every output rounded once; h and dab are rounded to bf16 between the products.
- * Requires d % 8 == 0 and f % 8 == 0 (MOE_KEEP_F8: f % 32 == 0). Few tokens (up to 32, with smaller weights up to 64) with
+ * Requires d % 8 == 0 and f % 8 == 0 (MOE_KEEP_F8: f % 32 == 0). Few tokens (up to 64, of large weights fewer) with
  * MOE_KEEP_NONE take a path bound by reading the weights once. fp32: true fp32 FMA, any d, f >= 1; MOE_KEEP_F8 is for bf16 only.
  * d, f at most MOE_FFN_MAX, T at most MOE_FFN_MAX_T. Results repeat bit for bit.
  * ws: moe_ffn_workspace_size(...) bytes, 256-byte aligned; zeros before its first use (it holds arrival counts that every call

@@ -20,10 +20,14 @@ static int check(int T, int d, int f, int dtype, int act, int keep) {
 // Few tokens: the path that reads the weights once, whose blocks each read all tokens. With more of those than 32 and large weights
 // that reading costs more than the tiles of the other path. This one and the other, in us: 44 and 57 for 32 tokens of 4096 x
 // 8192 (201 MB), 57 and 57 for 48, 77 and 57 for 64; for 48 of 8192 x 16384 (805 MB) 193 and 164; for 64 of 4096 x 2048 23 and 30,
-// of 2048 x 8192 (101 MB) 39 and 39.
+// of 2048 x 8192 (101 MB) 39 and 39. Without its ring (few_ring), in replayed graphs: 16 tokens of 8200 x 16392 148 and 160, of 4104 x
+// 8200 47 and 57; 32 of that 67 and 57, of 2056 x 8200 49 and 38, of 4104 x 4104 36 and 43, of 1000 x 10248 (61 MB) 36 and 38, of 2056
+// x 5128 (63 MB) 35 and 31, of 4104 x 2056 (51 MB) 20 and 30; 48 of that 27 and 31, of 2056 x 4104 (51 MB) 35 and 28, of 8200 x 1032 36 and
+// 33; 64 of 2056 x 2056 (25 MB) 21 and 24, of 1000 x 4104 29 and 24, of 1000 x 2056 16 and 19.
 static bool few(int T, int d, int f) {
-  const int64_t weights = (int64_t)6 * d * f;
-  return T <= 32 || (T <= 48 && weights <= (int64_t)512 << 20) || (T <= kFewTokens && weights <= (int64_t)128 << 20);
+  const int64_t weights = (int64_t)6 * d * f, MiB = 1 << 20;
+  if (few_ring(T, d, f)) return T <= 32 || (T <= 48 && weights <= 512 * MiB) || (T <= kFewTokens && weights <= 128 * MiB);
+  return T <= 16 || (T <= 32 && weights <= 64 * MiB) || (T <= kFewTokens && weights <= 25 * MiB);
 }
 
 extern "C" size_t moe_ffn_workspace_size(int T, int d, int f, int dtype, int backward) {

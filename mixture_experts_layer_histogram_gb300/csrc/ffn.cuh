@@ -92,6 +92,7 @@ int gemm_fwd(const Block &b, cudaStream_t s);
 int gemm_bwd(const Block &b, cudaStream_t s);
 // bf16, few tokens: forward that keeps nothing (ffn_few.cu)
 constexpr int kFewTokens = 64;
+bool few_ring(int T, int d, int f);   // whether it streams the weights through its ring
 int few_fwd(const Block &b, cudaStream_t s);
 // fp32 (ffn_f32.cu)
 int f32_fwd(const Block &b, cudaStream_t s);

@@ -404,13 +404,17 @@ template <bool UP> static int run(const Params &p, bool ring, WsHeader *hdr, cud
 
 }  // namespace few
 
+// Small weights take the kernel that starts quickest, others the ring, whose rows are whole 128 bytes. In us, the ring and the
+// other: 4 tokens of 2048 x 1024 (12.6 MB) 8.9 and 8.0, of 2048 x 2048 10.1 and 8.2, of 4096 x 2048 (50 MB) 12.3 and 12.3, of
+// 2048 x 8192 (101 MB) 20 and 25; 24 tokens of 768 x 512 (2.4 MB) 8.7 and 7.9, of 2048 x 1024 8.9 and 9.0, of 2048 x 2048 10.3
+// and 12.3. (One product through the ring and the other not is slower than either: 14.1 for 4 tokens of 4096 x 2048.)
+bool few_ring(int T, int d, int f) {
+  return d % 64 == 0 && f % 64 == 0 && (int64_t)6 * d * f > (int64_t)(T <= 16 ? 48 : 8) << 20;
+}
+
 int few_fwd(const Block &b, cudaStream_t s) {
   typedef __nv_bfloat16 bf16;
-  // Small weights take the kernel that starts quickest, others the ring, whose rows are whole 128 bytes. In us, the ring and the
-  // other: 4 tokens of 2048 x 1024 (12.6 MB) 8.9 and 8.0, of 2048 x 2048 10.1 and 8.2, of 4096 x 2048 (50 MB) 12.3 and 12.3, of
-  // 2048 x 8192 (101 MB) 20 and 25; 24 tokens of 768 x 512 (2.4 MB) 8.7 and 7.9, of 2048 x 1024 8.9 and 9.0, of 2048 x 2048 10.3
-  // and 12.3. (One product through the ring and the other not is slower than either: 14.1 for 4 tokens of 4096 x 2048.)
-  const bool ring = b.d % 64 == 0 && b.f % 64 == 0 && (int64_t)6 * b.d * b.f > (int64_t)(b.T <= 16 ? 48 : 8) << 20;
+  const bool ring = few_ring(b.T, b.d, b.f);
   few::Params p{};
   p.tok = (const bf16 *)b.x;
   p.w = (const bf16 *)b.w_gate_up;
