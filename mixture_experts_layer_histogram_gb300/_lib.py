@@ -538,6 +538,10 @@ class OwnsBuffers:
         if taken:
             self._take()
 
+    def __setstate__(self, state):   # a deep copy has buffers of its own, or was read back onto another GPU
+        self.__dict__.update(state)
+        self._take()
+
     def __delattr__(self, name):
         if name in self._buffers:
             raise AttributeError(f"{name}: the calls of {type(self).__name__} use this buffer")

@@ -70,10 +70,10 @@ class GatedFFN(L.OwnsBuffers):
             self.dx = torch.empty((T, d), **act_)
             self.dw_gate_up = torch.empty((2 * f, d), **act_)
             self.dw_down = torch.empty((d, f), **act_)
-        self._index = self.y.device.index
         self._built()
 
     def _take(self):
+        self._index = self.y.device.index
         with torch.cuda.device(self._index):
             self._kept = L.kept(self.ab, self.ab_scales, self.dtype, self.T, self.f)
         if self.backward_enabled:

@@ -53,10 +53,11 @@ class LayerNorm(L.OwnsBuffers):
             self.dw = torch.empty(d, **act)
             self.db = torch.empty(d, **act) if bias else None
             self.ws = torch.empty(ws_bytes, **u8)
-        self._index = self.n.device.index
         self._built()
 
     def _take(self):
+        self._index = self.n.device.index
+
         def at(*tensors):
             return [None if t is None else t.data_ptr() for t in tensors]
 

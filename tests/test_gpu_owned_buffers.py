@@ -1,4 +1,6 @@
 """Two sets of buffers in turn on one object: what each micro-batch keeps is what its backward reads."""
+import copy
+
 import pytest
 import torch
 
@@ -62,3 +64,23 @@ def test_gated_ffn(keep):
     for name, bad in (("ab", torch.empty(T, f, dtype=BF, device="cuda")), ("y", ffn.y.cpu()), ("h", ffn.h.T)):
         with pytest.raises(ValueError, match=name):
             setattr(ffn, name, bad)
+
+
+@pytest.mark.parametrize("keep", [None, "f8"])
+def test_deep_copies(keep):
+    """A copy writes into buffers of its own, and leaves the original's alone."""
+    T, d, f = 70, 128, 64
+    w, b, wgu, wd, x, z, dy = randn(0, d, d, (2 * f, d), (d, f), (T, d), (T, d), (T, d))
+    nm, ffn = LayerNorm(T, d, keep=keep), GatedFFN(T, d, f, keep=keep)
+
+    def step(norm, block, x):
+        n = norm.forward(x, w, b)
+        y = block.forward(n, wgu, wd)
+        g = block.backward(dy, n, wgu, wd)
+        return [n, y, *g.values(), *norm.backward(g["dx"], w, x=None if keep else x).values()]
+
+    first = step(nm, ffn, x)
+    kept = [t.clone() for t in first]
+    other = [t.clone() for t in step(copy.deepcopy(nm), copy.deepcopy(ffn), z)]
+    assert all(torch.equal(a, k) for a, k in zip(first, kept))
+    assert all(torch.equal(a, k) for a, k in zip(step(nm, ffn, z), other))

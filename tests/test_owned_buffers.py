@@ -1,5 +1,7 @@
 """Buffers that are set in the place of a class's own: taken where they fit, refused where they do not (no GPU needed: the layer norm's
 buffers are put on the CPU, and only addresses are looked at)."""
+import copy
+import io
 import os
 
 import pytest
@@ -54,3 +56,15 @@ def test_sizes_stay(made, name, value):
     nm = made()
     with pytest.raises(AttributeError, match=name):
         setattr(nm, name, value)
+
+
+def test_copies_use_their_own_buffers(made):
+    nm = made(keep="f8")
+    stream = io.BytesIO()
+    torch.save(nm, stream)
+    stream.seek(0)
+    for other in (copy.deepcopy(nm), torch.load(stream, weights_only=False)):
+        for mine, own in ((other._out, nm._out), (other._codes, nm._codes), (other._back, nm._back)):
+            assert [p is None for p in mine] == [p is None for p in own] and not {p for p in mine if p} & {p for p in own if p}
+        assert other._out[0] == other.n.data_ptr() and other._back[-1] == other.ws.data_ptr() and other._ws_bytes == nm._ws_bytes
+    assert copy.copy(nm)._out == nm._out                    # a shallow copy shares them
