@@ -263,8 +263,8 @@ __device__ __forceinline__ void keep(const LnFwdParams &p, int64_t row, int v, b
   if (v * VEC % act8::kBlock == 0) p.scales[row * p.nb + v * VEC / act8::kBlock] = (uint8_t)byte;
 }
 
-// ROWS: rows that a block takes at a time, which share the reductions' exchanges and barriers. WIN: Windows. keep() for a
-// window's vector. The largest magnitudes of the row's blocks meet in shared memory (`tops`, fp32 bits, zeros at first) ...
+// keep() for a window's vector. The largest magnitudes of the row's blocks meet in shared memory (`tops`, fp32 bits, zeros at
+// first) ...
 template <int N> __device__ __forceinline__ void meet(uint32_t *tops, const Split &x, const F2 (&z)[N]) {
   float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
@@ -312,6 +312,7 @@ __device__ __forceinline__ void keep_window(const LnFwdParams &p, int64_t row, i
   if (x.b1 != x.b0) p.scales[row * p.nb + x.b1] = (uint8_t)byte1;
 }
 
+// ROWS: rows that a block takes at a time, which share the reductions' exchanges and barriers. WIN: Windows.
 template <typename T, int VEC, int ITER, bool KEEP, int ROWS, bool WIN>
 __global__ void __launch_bounds__(kMaxThreads, ITER == 1 ? 2 : 1) ln_fwd_kernel(const LnFwdParams p, const Geometry geom) {
   using V = Lanes<T, VEC, float>;
@@ -603,7 +604,7 @@ __global__ void __launch_bounds__(kMaxThreads, VEC == 1 && ITER <= 4 ? 2 : 1) ln
     }
     ahead(row + turn);
     ring.wait();
-    // every thread has left the rows before (its own vectors: the thread itself; windows: the barrier in wait())
+    // every thread has left the rows before (words: it reads what it has copied itself; single values: the barrier in wait())
     if (ring.stages > 1) fetch(row + (ring.stages - 1) * turn, ring.freed(stage));
     const int64_t off0 = ring.offset(row);
     const uint32_t here = ring.at(stage, off0);
@@ -912,7 +913,8 @@ __global__ void __launch_bounds__(kRestoreThreads) ln_restore_windows_kernel(con
   }
 }
 
-// Rows of words for rows that start anywhere; vec 1 where a thread would have to hold too many values.
+// Rows of words for rows that start anywhere; vec 1 where a thread would have to hold too many values (bf16 from 8186 values on, fp32
+// from 8190).
 static Shape windows_of(int d, int dtype) {
   const int es = dtype == MOE_BF16 ? 2 : 4, vec = 16 / es, nvec = (d + 2 * vec - 2) / vec;   // words, wherever the row starts
   Shape s;
